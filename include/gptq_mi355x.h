@@ -319,6 +319,122 @@ gptq_status gptq_w4a16_matmul_noalloc(const void* X, int64_t tokens, int64_t ldx
                                       void* stream);
 
 /* ------------------------------------------------------------------------
+ * Layers on the packed weights
+ *
+ * Three layers of a model whose weights are the quantizer's 2/3/4-bit codes,
+ * with Ŵ[r][c] = (q[r][c] - z[r][g_idx[c]])·s[r][g_idx[c]] as in
+ * gptq_w4a16_matmul.  Shared rules: X is bf16 with unit column stride; Y is
+ * GPTQ_BF16 or GPTQ_FP32; biases, residuals and router weights are either
+ * type.  A code enters its bf16 product exactly (as 16 + q), every sum and
+ * the epilogue are fp32, and the result is rounded once, to Y's type.  X must
+ * be finite (an Inf or NaN makes its own token's outputs NaN).  The summation
+ * order is fixed: the same call gives the same bits.  Stream-ordered, no
+ * synchronisation, nothing allocated; calls may be captured into a graph.
+ * `packed` is read only and may be shared by any number of concurrent calls;
+ * `workspace` (256-byte aligned, contents not kept) belongs to one call at a
+ * time.  tokens == 0 is a no-op.  Y may be the residual itself (the same
+ * pointer, type and row stride); otherwise no output may overlap an input.
+ *
+ * gptq_w4a16_linear: Y[t][r] = act(Σ_c X[t][c]·Ŵ[r][c] + bias[r]) +
+ * residual[t][r], with gptq_w4a16_pack's packed weight; bias [m] and residual
+ * [tokens][ldr] may be NULL.  `packed_bytes` is the size of the packed buffer
+ * (at least gptq_w4a16_packed_bytes(m, n, group_size)).  epilogue NULL: no
+ * bias, activation or residual.
+ *
+ * gptq_w4a16_glu: Y[t][r] = act(Σ_c X[t][c]·Ŵg[r][c] + gate_bias[r]) ·
+ * (Σ_c X[t][c]·Ŵu[r][c] + up_bias[r]); each bias [m] may be NULL.  The packed
+ * weight is gptq_w4a16_glu_pack's: gate and up read one input, so they have
+ * one column order (one g_idx).  gptq_w4a16_glu_pack synchronises `stream`
+ * once and checks g_idx as gptq_w4a16_pack does.
+ * ---------------------------------------------------------------------- */
+typedef enum {
+  GPTQ_ACT_NONE = 0,
+  GPTQ_ACT_RELU = 1,
+  GPTQ_ACT_SILU = 2,      /* x·sigmoid(x)                                  */
+  GPTQ_ACT_GELU = 3,      /* x·Φ(x), with erf                              */
+  GPTQ_ACT_GELU_TANH = 4  /* ½x(1 + tanh(√(2/π)(x + 0.044715 x³)))         */
+} gptq_activation;
+
+typedef struct {
+  int32_t activation;     /* gptq_activation                               */
+  int32_t bias_dtype;
+  const void* bias;       /* [m], or NULL                                  */
+  int32_t residual_dtype;
+  const void* residual;   /* [tokens][ldr], or NULL                        */
+  int64_t ldr;
+} gptq_epilogue;
+
+size_t gptq_w4a16_linear_workspace_bytes(int64_t tokens, int64_t m, int64_t n, int32_t group_size);
+gptq_status gptq_w4a16_linear(const void* X, int64_t tokens, int64_t ldx, const void* packed,
+                              size_t packed_bytes, int64_t m, int64_t n, int32_t group_size,
+                              const gptq_epilogue* epilogue, void* Y, int32_t y_dtype, int64_t ldy,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+size_t gptq_w4a16_glu_packed_bytes(int64_t m, int64_t n, int32_t group_size);
+gptq_status gptq_w4a16_glu_pack(const uint32_t* gate_qweight, const float* gate_scales,
+                                const int32_t* gate_zeros, const uint32_t* up_qweight,
+                                const float* up_scales, const int32_t* up_zeros, const int32_t* g_idx,
+                                int64_t m, int64_t n, int32_t bits, int32_t group_size, void* packed,
+                                size_t packed_bytes, void* stream);
+size_t gptq_w4a16_glu_workspace_bytes(int64_t tokens, int64_t m, int64_t n, int32_t group_size);
+gptq_status gptq_w4a16_glu(const void* X, int64_t tokens, int64_t ldx, const void* packed,
+                           size_t packed_bytes, int64_t m, int64_t n, int32_t group_size,
+                           int32_t activation, const void* gate_bias, const void* up_bias,
+                           int32_t bias_dtype, void* Y, int32_t y_dtype, int64_t ldy, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A mixture-of-experts layer on the packed weights, for a few tokens
+ *
+ *   logits = X·routerᵀ (summed in fp64), p = softmax(logits),
+ *   ids    = the top_k largest of p, largest first, ties to the lower expert
+ *            (a NaN logit counts as the largest),
+ *   w      = p[ids], divided by its sum over the top_k if renormalize,
+ *   Y      = Σ_j w_j·Ŵdown(act(Ŵgate·x) ⊙ (Ŵup·x)) of expert ids_j + residual.
+ * The hidden activation act(gate)·up goes from one product to the next as two
+ * bf16 parts (16 significant bits) for a bf16 Y, three (24) for an fp32 Y.
+ *
+ * gptq_w4a16_moe_pack packs one expert (0 <= expert < experts) into its place
+ * in `packed` (gptq_w4a16_moe_packed_bytes(cfg) bytes for all experts): gate
+ * and up [inter x hidden] with one g_idx [hidden], down [hidden x inter] with
+ * its own g_idx [inter].  Synchronises `stream`; g_idx are checked as in
+ * gptq_w4a16_pack.  Every expert must be packed before the layer runs.
+ *
+ * gptq_w4a16_moe runs the layer on X [tokens][ldx].  router [experts][hidden]
+ * contiguous; residual [tokens][ldr] may be NULL; topk_ids and topk_weights
+ * [tokens][top_k] receive ids and w and may be NULL.  Tokens are processed 64
+ * per launch sequence; the rules of the layers above hold.
+ * Limits (GPTQ_ERR_UNSUPPORTED beyond them): experts <= 1024, top_k <= 64 and
+ * <= experts, hidden and inter <= 32768, bits 2, 3 or 4, group_size 32, 64,
+ * 128 or -1.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int64_t hidden;
+  int64_t inter;
+  int32_t experts;
+  int32_t top_k;
+  int32_t bits;
+  int32_t group_size;
+  int32_t activation;     /* gptq_activation, of the gate                  */
+  int32_t renormalize;    /* 0 or 1                                        */
+} gptq_moe_config;
+
+size_t gptq_w4a16_moe_packed_bytes(const gptq_moe_config* cfg);
+gptq_status gptq_w4a16_moe_pack(const gptq_moe_config* cfg, int32_t expert,
+                                const uint32_t* gate_qweight, const float* gate_scales,
+                                const int32_t* gate_zeros, const uint32_t* up_qweight,
+                                const float* up_scales, const int32_t* up_zeros, const int32_t* g_idx,
+                                const uint32_t* down_qweight, const float* down_scales,
+                                const int32_t* down_zeros, const int32_t* down_g_idx, void* packed,
+                                size_t packed_bytes, void* stream);
+size_t gptq_w4a16_moe_workspace_bytes(const gptq_moe_config* cfg, int64_t tokens);
+gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const void* router,
+                           int32_t router_dtype, const gptq_moe_config* cfg, const void* packed,
+                           size_t packed_bytes, const void* residual, int32_t residual_dtype,
+                           int64_t ldr, void* Y, int32_t y_dtype, int64_t ldy, int32_t* topk_ids,
+                           float* topk_weights, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Export of a quantized layer to the tensor layout of GPTQ checkpoints.
  * Page "模型量化实战：从 INT8 PTQ 到 GPTQ…" §3.3 saves the quantized model as
  * a GPTQ checkpoint (about 4.1 GB for 7B) but does not define its tensors;

@@ -41,6 +41,13 @@ from .quantized_matmul import (  # noqa: F401,E402
     dequant_matmul,
     dequantized_weight,
 )
+from .quantized_layers import (  # noqa: F401,E402
+    activate,
+    glu,
+    linear,
+    moe,
+    route,
+)
 from .awq import (  # noqa: F401,E402
     awq_quantize,
     channel_abs_sum,

@@ -37,6 +37,20 @@ class GptqRtnConfig(ctypes.Structure):
                 ("clip_ratio", ctypes.c_float)]
 
 
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+class GptqEpilogue(ctypes.Structure):
+    _fields_ = [("activation", ctypes.c_int32), ("bias_dtype", ctypes.c_int32), ("bias", ctypes.c_void_p),
+                ("residual_dtype", ctypes.c_int32), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64)]
+
+
+class GptqMoeConfig(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int64), ("inter", ctypes.c_int64), ("experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("bits", ctypes.c_int32), ("group_size", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("renormalize", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -66,6 +80,20 @@ SIGNATURES = {
     "gptq_w4a16_matmul": (_ST, [_P, _I64, _I64, _P, _I64, _I64, _I32, _P, _I64, _P, _SZ, _P]),
     "gptq_w4a16_noalloc_scratch_bytes": (_SZ, []),
     "gptq_w4a16_matmul_noalloc": (_ST, [_P, _I64, _I64, _P, _I64, _I64, _I32, _P, _I64, _P]),
+    "gptq_w4a16_linear_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),
+    "gptq_w4a16_linear": (_ST, [_P, _I64, _I64, _P, _SZ, _I64, _I64, _I32, ctypes.POINTER(GptqEpilogue), _P, _I32,
+                                _I64, _P, _SZ, _P]),
+    "gptq_w4a16_glu_packed_bytes": (_SZ, [_I64, _I64, _I32]),
+    "gptq_w4a16_glu_pack": (_ST, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _P, _SZ, _P]),
+    "gptq_w4a16_glu_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),
+    "gptq_w4a16_glu": (_ST, [_P, _I64, _I64, _P, _SZ, _I64, _I64, _I32, _I32, _P, _P, _I32, _P, _I32, _I64, _P, _SZ,
+                             _P]),
+    "gptq_w4a16_moe_packed_bytes": (_SZ, [ctypes.POINTER(GptqMoeConfig)]),
+    "gptq_w4a16_moe_pack": (_ST, [ctypes.POINTER(GptqMoeConfig), _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                  _SZ, _P]),
+    "gptq_w4a16_moe_workspace_bytes": (_SZ, [ctypes.POINTER(GptqMoeConfig), _I64]),
+    "gptq_w4a16_moe": (_ST, [_P, _I64, _I64, _P, _I32, ctypes.POINTER(GptqMoeConfig), _P, _SZ, _P, _I32, _I64, _P,
+                             _I32, _I64, _P, _P, _P, _SZ, _P]),
     "gptq_checkpoint_qweight_rows": (_I64, [_I64, _I32]),
     "gptq_checkpoint_qzeros_words": (_I64, [_I64, _I32]),
     "gptq_export_checkpoint": (_ST, [_P, _P, _P, _I64, _I64, _I32, _I32, _I32, _P, _P, _P, _P]),

@@ -20,7 +20,7 @@ SRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libgptq_mi355x.so")
-SOURCES = ("abi.hip", "gemm_f32.hip", "hessian.hip", "prepare.hip", "quantize.hip", "rtn.hip", "w4a16.hip", "awq.hip", "gemm_x6.hip", "checkpoint.hip",
+SOURCES = ("abi.hip", "gemm_f32.hip", "hessian.hip", "prepare.hip", "quantize.hip", "rtn.hip", "w4a16.hip", "w4a16_linear.hip", "w4a16_moe.hip", "awq.hip", "gemm_x6.hip", "checkpoint.hip",
            *(f"block_quant_g{g}.hip" for g in (0, 8, 16, 32, 64, 128)))
 
 HIPCC = os.environ.get("HIPCC") or shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
@@ -31,10 +31,10 @@ CFLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", INCLUDE, "-I", SRC,
 ]
-# per-source additions: the W4A16 product keeps its MFMA accumulators in
+# per-source additions: the W4A16 products keep their MFMA accumulators in
 # ordinary VGPRs (they are read by VALU code after every group; in AGPRs each
 # read is a v_accvgpr_read first)
-EXTRA = {"w4a16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for src in ("w4a16.hip", "w4a16_linear.hip", "w4a16_moe.hip")}
 
 
 def _compile(src: str, verbose: bool) -> str:

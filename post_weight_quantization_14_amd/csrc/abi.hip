@@ -414,4 +414,218 @@ gptq_status gptq_w4a16_matmul_noalloc(const void* X, int64_t tokens, int64_t ldx
                                   plan_w4a16(m, n, group_size), Y, ldy, static_cast<hipStream_t>(stream));
 }
 
+// ---------------------------------------------------------------- layers on packed weights
+static bool float_dtype(int32_t d) { return d == GPTQ_BF16 || d == GPTQ_FP32; }
+static size_t dtype_bytes(int32_t d) { return d == GPTQ_FP32 ? 4 : 2; }
+constexpr int64_t kL4MaxDim = (int64_t)1 << 24;
+constexpr int64_t kL4MaxTokens = (int64_t)1 << 30;
+
+// the checks that the linear and the glu share; *done: nothing to compute
+static gptq_status check_l4(const void* X, int64_t tokens, int64_t ldx, const void* packed, int64_t m, int64_t n,
+                            int32_t group_size, int32_t activation, const void* Y, int32_t y_dtype, int64_t ldy,
+                            bool* done) {
+  *done = false;
+  if (tokens < 0 || m < 0 || n <= 0)
+    return fail(GPTQ_ERR_INVALID_ARG, "tokens=%lld m=%lld n=%lld", (long long)tokens, (long long)m, (long long)n);
+  if (!w4_group_ok(group_size)) return fail(GPTQ_ERR_UNSUPPORTED, "group_size=%d (32, 64, 128 or -1)", group_size);
+  if (activation < GPTQ_ACT_NONE || activation > GPTQ_ACT_GELU_TANH)
+    return fail(GPTQ_ERR_UNSUPPORTED, "activation=%d", activation);
+  if (!float_dtype(y_dtype)) return fail(GPTQ_ERR_UNSUPPORTED, "y_dtype=%d", y_dtype);
+  if (m > kL4MaxDim || n > kL4MaxDim || tokens > kL4MaxTokens)
+    return fail(GPTQ_ERR_UNSUPPORTED, "tokens=%lld m=%lld n=%lld too large", (long long)tokens, (long long)m,
+                (long long)n);
+  if (tokens == 0 || m == 0) {
+    *done = true;
+    return GPTQ_OK;
+  }
+  if (ldx < n || ldy < m)
+    return fail(GPTQ_ERR_INVALID_ARG, "ldx=%lld < n or ldy=%lld < m", (long long)ldx, (long long)ldy);
+  if (bad_ptr(X, 2) || bad_ptr(Y, dtype_bytes(y_dtype)))
+    return fail(GPTQ_ERR_INVALID_ARG, "X or Y is NULL or misaligned");
+  if (bad_ptr(packed, 256)) return fail(GPTQ_ERR_INVALID_ARG, "packed is NULL or not 256-byte aligned");
+  return GPTQ_OK;
+}
+
+static gptq_status check_l4_buffers(size_t packed_bytes, size_t need_packed, const void* workspace, size_t ws_bytes,
+                                    size_t need) {
+  if (packed_bytes < need_packed)
+    return fail(GPTQ_ERR_INVALID_ARG, "packed buffer %zu bytes, this weight takes %zu", packed_bytes, need_packed);
+  if (workspace == nullptr || ws_bytes < need || bad_ptr(workspace, 256))
+    return fail(GPTQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu (256-byte aligned)", ws_bytes, need);
+  return GPTQ_OK;
+}
+
+static gptq_status check_l4_tensor(const char* name, const void* p, int32_t dtype) {
+  if (p == nullptr) return GPTQ_OK;
+  if (!float_dtype(dtype)) return fail(GPTQ_ERR_UNSUPPORTED, "%s dtype=%d", name, dtype);
+  if (bad_ptr(p, dtype_bytes(dtype))) return fail(GPTQ_ERR_INVALID_ARG, "%s is misaligned", name);
+  return GPTQ_OK;
+}
+
+size_t gptq_w4a16_linear_workspace_bytes(int64_t tokens, int64_t m, int64_t n, int32_t group_size) {
+  if (tokens < 0 || tokens > kL4MaxTokens || m < 0 || m > kL4MaxDim || n <= 0 || n > kL4MaxDim ||
+      !w4_group_ok(group_size))
+    return 0;
+  return plan_w4a16_linear(tokens, n).total;
+}
+
+gptq_status gptq_w4a16_linear(const void* X, int64_t tokens, int64_t ldx, const void* packed, size_t packed_bytes,
+                              int64_t m, int64_t n, int32_t group_size, const gptq_epilogue* epilogue, void* Y,
+                              int32_t y_dtype, int64_t ldy, void* workspace, size_t ws_bytes, void* stream) {
+  clear_error();
+  const gptq_epilogue e = epilogue ? *epilogue : gptq_epilogue{GPTQ_ACT_NONE, 0, nullptr, 0, nullptr, 0};
+  bool done = false;
+  GPTQ_TRY(check_l4(X, tokens, ldx, packed, m, n, group_size, e.activation, Y, y_dtype, ldy, &done));
+  if (done) return GPTQ_OK;
+  GPTQ_TRY(check_l4_tensor("bias", e.bias, e.bias_dtype));
+  GPTQ_TRY(check_l4_tensor("residual", e.residual, e.residual_dtype));
+  if (e.residual && e.ldr < m) return fail(GPTQ_ERR_INVALID_ARG, "ldr=%lld < m", (long long)e.ldr);
+  if (e.residual == Y && (e.residual_dtype != y_dtype || e.ldr != ldy))
+    return fail(GPTQ_ERR_INVALID_ARG, "Y is the residual, with another type or row stride");
+  const W4Layout L = plan_w4a16(m, n, group_size);
+  const L4LinearPlan p = plan_w4a16_linear(tokens, n);
+  GPTQ_TRY(check_l4_buffers(packed_bytes, L.total, workspace, ws_bytes, p.total));
+  const L4Call c{static_cast<const uint16_t*>(X), tokens, ldx, m, packed, e.activation, e.bias_dtype,
+                 e.residual_dtype, y_dtype, e.bias, nullptr, e.residual, e.ldr, Y, ldy};
+  return run_w4a16_linear(c, L, false, workspace, p, static_cast<hipStream_t>(stream));
+}
+
+size_t gptq_w4a16_glu_packed_bytes(int64_t m, int64_t n, int32_t group_size) {
+  if (m < 0 || n < 0 || m > kL4MaxDim || n > kL4MaxDim || !w4_group_ok(group_size)) return 0;
+  return plan_w4a16_pair(m, n, group_size).total;
+}
+
+static gptq_status check_l4_pack(int64_t m, int64_t n, int32_t bits, int32_t group_size) {
+  if (m <= 0 || n <= 0) return fail(GPTQ_ERR_INVALID_ARG, "m=%lld n=%lld", (long long)m, (long long)n);
+  if (bits != 2 && bits != 3 && bits != 4)
+    return fail(GPTQ_ERR_UNSUPPORTED, "bits=%d (the W4A16 layers take 2-, 3- and 4-bit codes)", bits);
+  if (!w4_group_ok(group_size)) return fail(GPTQ_ERR_UNSUPPORTED, "group_size=%d (32, 64, 128 or -1)", group_size);
+  if (m > kL4MaxDim || n > kL4MaxDim)
+    return fail(GPTQ_ERR_UNSUPPORTED, "m=%lld n=%lld too large", (long long)m, (long long)n);
+  return GPTQ_OK;
+}
+
+gptq_status gptq_w4a16_glu_pack(const uint32_t* gate_qweight, const float* gate_scales, const int32_t* gate_zeros,
+                                const uint32_t* up_qweight, const float* up_scales, const int32_t* up_zeros,
+                                const int32_t* g_idx, int64_t m, int64_t n, int32_t bits, int32_t group_size,
+                                void* packed, size_t packed_bytes, void* stream) {
+  clear_error();
+  GPTQ_TRY(check_l4_pack(m, n, bits, group_size));
+  const void* in[] = {gate_qweight, gate_scales, gate_zeros, up_qweight, up_scales, up_zeros, g_idx};
+  for (const void* p : in)
+    if (bad_ptr(p, 4)) return fail(GPTQ_ERR_INVALID_ARG, "an input pointer is NULL or misaligned");
+  const W4Layout L = plan_w4a16_pair(m, n, group_size);
+  if (packed == nullptr || packed_bytes < L.total || bad_ptr(packed, 256))
+    return fail(GPTQ_ERR_WORKSPACE, "packed buffer %zu bytes, need %zu (256-byte aligned)", packed_bytes, L.total);
+  const L4PairSource src{gate_qweight, up_qweight, gate_scales, up_scales, gate_zeros, up_zeros, m, nullptr};
+  return run_w4a16_glu_pack(src, g_idx, L, packed, static_cast<hipStream_t>(stream));
+}
+
+size_t gptq_w4a16_glu_workspace_bytes(int64_t tokens, int64_t m, int64_t n, int32_t group_size) {
+  return gptq_w4a16_linear_workspace_bytes(tokens, m, n, group_size);
+}
+
+gptq_status gptq_w4a16_glu(const void* X, int64_t tokens, int64_t ldx, const void* packed, size_t packed_bytes,
+                           int64_t m, int64_t n, int32_t group_size, int32_t activation, const void* gate_bias,
+                           const void* up_bias, int32_t bias_dtype, void* Y, int32_t y_dtype, int64_t ldy,
+                           void* workspace, size_t ws_bytes, void* stream) {
+  clear_error();
+  bool done = false;
+  GPTQ_TRY(check_l4(X, tokens, ldx, packed, m, n, group_size, activation, Y, y_dtype, ldy, &done));
+  if (done) return GPTQ_OK;
+  GPTQ_TRY(check_l4_tensor("gate_bias", gate_bias, bias_dtype));
+  GPTQ_TRY(check_l4_tensor("up_bias", up_bias, bias_dtype));
+  const W4Layout L = plan_w4a16_pair(m, n, group_size);
+  const L4LinearPlan p = plan_w4a16_linear(tokens, n);
+  GPTQ_TRY(check_l4_buffers(packed_bytes, L.total, workspace, ws_bytes, p.total));
+  const L4Call c{static_cast<const uint16_t*>(X), tokens, ldx, m, packed, activation, bias_dtype, 0, y_dtype,
+                 gate_bias, up_bias, nullptr, 0, Y, ldy};
+  return run_w4a16_linear(c, L, true, workspace, p, static_cast<hipStream_t>(stream));
+}
+
+// ---------------------------------------------------------------- mixture of experts
+static gptq_status check_moe(const gptq_moe_config* c) {
+  if (c == nullptr) return fail(GPTQ_ERR_INVALID_ARG, "cfg is NULL");
+  if (c->hidden <= 0 || c->inter <= 0 || c->experts <= 0 || c->top_k <= 0 || c->top_k > c->experts)
+    return fail(GPTQ_ERR_INVALID_ARG, "hidden=%lld inter=%lld experts=%d top_k=%d", (long long)c->hidden,
+                (long long)c->inter, c->experts, c->top_k);
+  if (c->renormalize != 0 && c->renormalize != 1) return fail(GPTQ_ERR_INVALID_ARG, "renormalize=%d", c->renormalize);
+  if (c->hidden > 32768 || c->inter > 32768 || c->experts > 1024 || c->top_k > 64)
+    return fail(GPTQ_ERR_UNSUPPORTED, "hidden=%lld inter=%lld experts=%d top_k=%d (up to 32768, 32768, 1024, 64)",
+                (long long)c->hidden, (long long)c->inter, c->experts, c->top_k);
+  if (c->bits != 2 && c->bits != 3 && c->bits != 4)
+    return fail(GPTQ_ERR_UNSUPPORTED, "bits=%d (the W4A16 layers take 2-, 3- and 4-bit codes)", c->bits);
+  if (!w4_group_ok(c->group_size))
+    return fail(GPTQ_ERR_UNSUPPORTED, "group_size=%d (32, 64, 128 or -1)", c->group_size);
+  if (c->activation < GPTQ_ACT_NONE || c->activation > GPTQ_ACT_GELU_TANH)
+    return fail(GPTQ_ERR_UNSUPPORTED, "activation=%d", c->activation);
+  return GPTQ_OK;
+}
+
+size_t gptq_w4a16_moe_packed_bytes(const gptq_moe_config* cfg) {
+  if (check_moe(cfg) != GPTQ_OK) {
+    clear_error();
+    return 0;
+  }
+  return plan_moe(*cfg).stride * (size_t)cfg->experts;
+}
+
+gptq_status gptq_w4a16_moe_pack(const gptq_moe_config* cfg, int32_t expert, const uint32_t* gate_qweight,
+                                const float* gate_scales, const int32_t* gate_zeros, const uint32_t* up_qweight,
+                                const float* up_scales, const int32_t* up_zeros, const int32_t* g_idx,
+                                const uint32_t* down_qweight, const float* down_scales, const int32_t* down_zeros,
+                                const int32_t* down_g_idx, void* packed, size_t packed_bytes, void* stream) {
+  clear_error();
+  GPTQ_TRY(check_moe(cfg));
+  if (expert < 0 || expert >= cfg->experts) return fail(GPTQ_ERR_INVALID_ARG, "expert=%d of %d", expert, cfg->experts);
+  const void* in[] = {gate_qweight, gate_scales,  gate_zeros,  up_qweight, up_scales, up_zeros,
+                      g_idx,        down_qweight, down_scales, down_zeros, down_g_idx};
+  for (const void* p : in)
+    if (bad_ptr(p, 4)) return fail(GPTQ_ERR_INVALID_ARG, "an input pointer is NULL or misaligned");
+  const size_t need = plan_moe(*cfg).stride * (size_t)cfg->experts;
+  if (packed == nullptr || packed_bytes < need || bad_ptr(packed, 256))
+    return fail(GPTQ_ERR_WORKSPACE, "packed buffer %zu bytes, need %zu (256-byte aligned)", packed_bytes, need);
+  const L4PairSource src{gate_qweight, up_qweight, gate_scales, up_scales, gate_zeros, up_zeros, cfg->inter, nullptr};
+  return run_moe_pack(*cfg, expert, src, g_idx, down_qweight, down_scales, down_zeros, down_g_idx, packed,
+                      static_cast<hipStream_t>(stream));
+}
+
+size_t gptq_w4a16_moe_workspace_bytes(const gptq_moe_config* cfg, int64_t tokens) {
+  if (check_moe(cfg) != GPTQ_OK || tokens < 0 || tokens > kL4MaxTokens) {
+    clear_error();
+    return 0;
+  }
+  return plan_moe_work(*cfg, tokens).total;
+}
+
+gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const void* router, int32_t router_dtype,
+                           const gptq_moe_config* cfg, const void* packed, size_t packed_bytes,
+                           const void* residual, int32_t residual_dtype, int64_t ldr, void* Y, int32_t y_dtype,
+                           int64_t ldy, int32_t* topk_ids, float* topk_weights, void* workspace, size_t ws_bytes,
+                           void* stream) {
+  clear_error();
+  GPTQ_TRY(check_moe(cfg));
+  if (tokens < 0) return fail(GPTQ_ERR_INVALID_ARG, "tokens=%lld", (long long)tokens);
+  if (tokens > kL4MaxTokens) return fail(GPTQ_ERR_UNSUPPORTED, "tokens=%lld too large", (long long)tokens);
+  if (!float_dtype(y_dtype)) return fail(GPTQ_ERR_UNSUPPORTED, "y_dtype=%d", y_dtype);
+  if (!float_dtype(router_dtype)) return fail(GPTQ_ERR_UNSUPPORTED, "router dtype=%d", router_dtype);
+  if (tokens == 0) return GPTQ_OK;
+  if (ldx < cfg->hidden || ldy < cfg->hidden)
+    return fail(GPTQ_ERR_INVALID_ARG, "ldx=%lld or ldy=%lld < hidden", (long long)ldx, (long long)ldy);
+  if (bad_ptr(X, 2) || bad_ptr(Y, dtype_bytes(y_dtype)) || bad_ptr(router, dtype_bytes(router_dtype)))
+    return fail(GPTQ_ERR_INVALID_ARG, "X, Y or router is NULL or misaligned");
+  if (bad_ptr(packed, 256)) return fail(GPTQ_ERR_INVALID_ARG, "packed is NULL or not 256-byte aligned");
+  GPTQ_TRY(check_l4_tensor("residual", residual, residual_dtype));
+  if (residual && ldr < cfg->hidden) return fail(GPTQ_ERR_INVALID_ARG, "ldr=%lld < hidden", (long long)ldr);
+  if (residual == Y && (residual_dtype != y_dtype || ldr != ldy))
+    return fail(GPTQ_ERR_INVALID_ARG, "Y is the residual, with another type or row stride");
+  if ((topk_ids && bad_ptr(topk_ids, 4)) || (topk_weights && bad_ptr(topk_weights, 4)))
+    return fail(GPTQ_ERR_INVALID_ARG, "topk_ids or topk_weights is misaligned");
+  const MoeWork w = plan_moe_work(*cfg, tokens);
+  GPTQ_TRY(check_l4_buffers(packed_bytes, plan_moe(*cfg).stride * (size_t)cfg->experts, workspace, ws_bytes, w.total));
+  const MoeCall c{static_cast<const uint16_t*>(X), tokens, ldx, router, router_dtype, packed, residual,
+                  residual_dtype, ldr, Y, y_dtype, ldy, topk_ids, topk_weights};
+  return run_moe(c, *cfg, workspace, w, static_cast<hipStream_t>(stream));
+}
+
 }  // extern "C"

@@ -201,6 +201,84 @@ W4GemmPlan plan_w4a16_noalloc(int64_t tokens, int64_t m, int64_t n);
 gptq_status run_w4a16_matmul_noalloc(const uint16_t* X, int64_t tokens, int64_t ldx, const void* packed,
                                      const W4Layout& L, float* Y, int64_t ldy, hipStream_t stream);
 
+// Pieces of the pack and the gather that the layers below share: order[p] =
+// the column processed at position p (-1: padding) from g_idx, *flag != 0 if
+// g_idx does not split the columns; the host check of that flag (synchronises);
+// X' = X[:, order] with its 32- and 128-position sums.
+gptq_status launch_w4_order(const int32_t* g_idx, const W4Layout& L, int32_t* order, int* flag,
+                            hipStream_t stream);
+gptq_status check_w4_order(const int* flag, const char* where, hipStream_t stream);
+gptq_status launch_w4_gather(const uint16_t* X, int64_t ldx, const int32_t* order, int64_t n128, uint16_t* Xp,
+                             float* xs, float* xs4, int64_t tokens, hipStream_t stream);
+
+// ---------------------------------------------------------------- layers on packed weights
+// Two m x n weights of one input (gate and up), rows taken in row_order
+// (position -> row, -1: a zero row) or as they are.
+struct L4PairSource {
+  const uint32_t *qweight0, *qweight1;
+  const float *scales0, *scales1;
+  const int32_t *zeros0, *zeros1;
+  int64_t m;
+  const int32_t* row_order;
+};
+// gate tile i at packed tile 2i, up tile i at 2i + 1
+W4Layout plan_w4a16_pair(int64_t m, int64_t n, int32_t group_size);
+gptq_status launch_l4_pair(const L4PairSource& src, int64_t rows, const W4Layout& L, const int32_t* order,
+                           char* base, hipStream_t stream);
+gptq_status run_w4a16_glu_pack(const L4PairSource& src, const int32_t* g_idx, const W4Layout& L, void* packed,
+                               hipStream_t stream);
+
+constexpr int64_t kL4BlockTokens = 4096;   // tokens per launch sequence
+struct L4LinearPlan {
+  int64_t block = 0;
+  size_t xs_off = 0, total = 0;
+};
+L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n);
+struct L4Call {
+  const uint16_t* X;
+  int64_t tokens, ldx, m;
+  const void* packed;
+  int act, bias_dtype, res_dtype, y_dtype;
+  const void *bias, *bias2, *res;
+  int64_t ldr;
+  void* Y;
+  int64_t ldy;
+};
+gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, void* ws, const L4LinearPlan& p,
+                             hipStream_t stream);
+
+// ---------------------------------------------------------------- mixture of experts
+struct MoeLayout {
+  W4Layout gu, down;      // gate/up pair of f128 rows x hidden; hidden rows x inter
+  int64_t f128 = 0;
+  size_t down_off = 0, stride = 0;   // within an expert's blob; bytes per expert
+};
+MoeLayout plan_moe(const gptq_moe_config& c);
+struct MoeWork {
+  int64_t block = 0;
+  size_t wts_off = 0, mid_off = 0, out_off = 0, total = 0;
+};
+MoeWork plan_moe_work(const gptq_moe_config& c, int64_t tokens);
+struct MoeCall {
+  const uint16_t* X;
+  int64_t tokens, ldx;
+  const void* router;
+  int router_dtype;
+  const void* packed;
+  const void* res;
+  int res_dtype;
+  int64_t ldr;
+  void* Y;
+  int y_dtype;
+  int64_t ldy;
+  int32_t* topk_ids;
+  float* topk_weights;
+};
+gptq_status run_moe_pack(const gptq_moe_config& c, int expert, const L4PairSource& gate_up, const int32_t* g_idx,
+                         const uint32_t* down_qweight, const float* down_scales, const int32_t* down_zeros,
+                         const int32_t* down_g_idx, void* packed, hipStream_t stream);
+gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, const MoeWork& w, hipStream_t stream);
+
 // ---------------------------------------------------------------- fp32-accurate GEMM on bf16 MFMA
 // Operands as three exact bf16 planes, each stored k-step-major: element
 // (r, k) of plane q at p + q·pstride + (k / 16)·sst + 16·r + k % 16, so the 16

@@ -734,6 +734,27 @@ W4GemmPlan plan_w4a16_gemm(int64_t tokens, int64_t m, int64_t n, int64_t max_chu
   return p;
 }
 
+gptq_status launch_w4_order(const int32_t* g_idx, const W4Layout& L, int32_t* order, int* flag,
+                            hipStream_t stream) {
+  GPTQ_HIP_CHECK(hipMemsetAsync(flag, 0, sizeof(int), stream));
+  hipLaunchKernelGGL(w4_order_kernel, dim3((unsigned)L.Gp), dim3(256), 0, stream, g_idx, L.n, L.g,
+                     L.G, L.n128, order, flag);
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+gptq_status check_w4_order(const int* flag, const char* where, hipStream_t stream) {
+  int hflag = 0;
+  GPTQ_HIP_CHECK(hipMemcpyAsync(&hflag, flag, sizeof(int), hipMemcpyDeviceToHost, stream));
+  GPTQ_HIP_CHECK(hipStreamSynchronize(stream));
+  if (hflag) {
+    set_error("%s: g_idx does not split the columns into groups of the group size "
+              "(group p must hold min(g, n - p·g) columns)", where);
+    return GPTQ_ERR_INVALID_ARG;
+  }
+  return GPTQ_OK;
+}
+
 gptq_status run_w4a16_pack(const uint32_t* qweight, const float* scales, const int32_t* zeros,
                            const int32_t* g_idx, int bits, const W4Layout& L, void* packed,
                            hipStream_t stream) {
@@ -741,10 +762,7 @@ gptq_status run_w4a16_pack(const uint32_t* qweight, const float* scales, const i
   char* base = static_cast<char*>(packed);
   int* flag = reinterpret_cast<int*>(base + L.flag_off);
   int32_t* order = reinterpret_cast<int32_t*>(base + L.order_off);
-  GPTQ_HIP_CHECK(hipMemsetAsync(flag, 0, sizeof(int), stream));
-  hipLaunchKernelGGL(w4_order_kernel, dim3((unsigned)L.Gp), dim3(256), 0, stream, g_idx, L.n, L.g,
-                     L.G, L.n128, order, flag);
-  GPTQ_LAUNCH_CHECK();
+  GPTQ_TRY(launch_w4_order(g_idx, L, order, flag, stream));
   const int64_t np = L.mt * L.Gp * kW4Rows;
   hipLaunchKernelGGL(w4_params_kernel, dim3((unsigned)ceil_div(np, 256)), dim3(256), 0, stream,
                      scales, zeros, L.m, L.G, L.mt, L.Gp,
@@ -755,15 +773,7 @@ gptq_status run_w4a16_pack(const uint32_t* qweight, const float* scales, const i
                      qweight, ceil_div(L.n, 8), L.m, L.n, L.kc, nw, (const int32_t*)order,
                      reinterpret_cast<uint32_t*>(base + L.code_off));
   GPTQ_LAUNCH_CHECK();
-  int hflag = 0;
-  GPTQ_HIP_CHECK(hipMemcpyAsync(&hflag, flag, sizeof(int), hipMemcpyDeviceToHost, stream));
-  GPTQ_HIP_CHECK(hipStreamSynchronize(stream));
-  if (hflag) {
-    set_error("gptq_w4a16_pack: g_idx does not split the columns into groups of the group size "
-              "(group p must hold min(g, n - p·g) columns)");
-    return GPTQ_ERR_INVALID_ARG;
-  }
-  return GPTQ_OK;
+  return check_w4_order(flag, "gptq_w4a16_pack", stream);
 }
 
 gptq_status launch_w4_gather(const uint16_t* X, int64_t ldx, const int32_t* order, int64_t n128, uint16_t* Xp,

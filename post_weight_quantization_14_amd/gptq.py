@@ -392,6 +392,320 @@ def gptq_w4a16_matmul_noalloc(X: torch.Tensor, packed: torch.Tensor, m: int, n: 
     return Y
 
 
+# ---------------------------------------------------------------- layers on packed weights
+def _activation_code(name: str) -> int:
+    try:
+        return _lib.ACTIVATIONS[name]
+    except KeyError:
+        raise ValueError(f"activation {name!r}: one of {', '.join(_lib.ACTIVATIONS)}") from None
+
+
+def _on(X: torch.Tensor, **tensors: Optional[torch.Tensor]) -> None:
+    """Every tensor of a call lives on X's GPU (a pointer of another device,
+    or of the host, would be read by the kernels as it is)."""
+    if not X.is_cuda:
+        raise ValueError("X must be on the GPU")
+    dev = X.device
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, X on {dev}")
+
+
+def _rows(name: str, t: torch.Tensor, rows: int, cols: int) -> int:
+    """The row stride of a [rows, cols] tensor with contiguous rows."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (cols > 1 and rows > 0 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{rows}, {cols}] with contiguous rows")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _vector(name: str, t: Optional[torch.Tensor], m: int) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != m or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{m}]")
+    return t.data_ptr()
+
+
+def _bf16_rows(X: torch.Tensor, n: int) -> int:
+    if X.dim() != 2 or X.shape[1] != n or (X.shape[0] > 0 and n > 1 and X.stride(1) != 1):
+        raise ValueError(f"X must be [tokens, {n}] with contiguous rows")
+    if X.dtype != torch.bfloat16:
+        raise TypeError(f"X must be bfloat16, not {X.dtype}")
+    return X.stride(0) if X.shape[0] > 1 else n
+
+
+def _uint8(name: str, t: torch.Tensor) -> int:
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.numel() * t.element_size()
+
+
+def _scratch(nbytes: int, X: torch.Tensor, workspace: Optional[torch.Tensor]) -> torch.Tensor:
+    """The caller's workspace if it is large enough (it then belongs to this
+    call until its work is done), else a new one."""
+    if workspace is not None and _uint8("workspace", workspace) >= nbytes:
+        return workspace
+    return torch.empty(nbytes, dtype=torch.uint8, device=X.device)
+
+
+class _Device:
+    """The tensors' GPU is the current device during a call."""
+
+    __slots__ = ("index", "was")
+
+    def __init__(self, X: torch.Tensor):
+        self.index = X.device.index
+
+    def __enter__(self):
+        self.was = torch.cuda.current_device()
+        if self.was != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.was != self.index:
+            torch.cuda.set_device(self.was)
+
+
+def _int32(**tensors: torch.Tensor) -> None:
+    for name, t in tensors.items():
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous int32")
+
+
+def _quantized(name: str, qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, m: int, n: int,
+               group_size: int) -> None:
+    """The quantizer's tensors of an m x n weight (codes of 4-bit fields)."""
+    G = gptq_num_groups(n, group_size)
+    words = gptq_qweight_words(n, 4)
+    _int32(**{f"{name} qweight": qweight, f"{name} zeros": zeros})
+    if scales.dtype != torch.float32 or not scales.is_contiguous():
+        raise ValueError(f"{name} scales must be contiguous float32")
+    if tuple(qweight.shape) != (m, words) or (G >= 0 and not tuple(scales.shape) == tuple(zeros.shape) == (m, G)):
+        raise ValueError(f"{name}: qweight must be [{m}, {words}], scales and zeros [{m}, {G}]")
+
+
+def gptq_w4a16_linear_workspace_bytes(tokens: int, m: int, n: int, group_size: int) -> int:
+    return int(lib().gptq_w4a16_linear_workspace_bytes(tokens, m, n, group_size))
+
+
+def gptq_w4a16_linear(X: torch.Tensor, packed: torch.Tensor, m: int, n: int, group_size: int,
+                      bias: Optional[torch.Tensor] = None, activation: str = "none",
+                      residual: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
+                      out_dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """Y [tokens, m] = act(X·Ŵᵀ + bias) + residual for X [tokens, n] bf16 and
+    gptq_w4a16_pack's packed weight.  bias [m] and residual [tokens, m] are
+    bf16 or fp32; activation is none, relu, silu, gelu or gelu_tanh.  Y (bf16
+    or fp32; out_dtype if it is allocated here) may be the residual itself."""
+    ldx = _bf16_rows(X, n)
+    tokens = X.shape[0]
+    _on(X, packed=packed, bias=bias, residual=residual, Y=Y, workspace=workspace)
+    if Y is None:
+        Y = torch.empty(tokens, m, dtype=out_dtype, device=X.device)
+    e = _lib.GptqEpilogue(activation=_activation_code(activation))
+    if bias is not None:
+        e.bias, e.bias_dtype = _vector("bias", bias, m), _dtype_code(bias)
+    if residual is not None:
+        e.ldr = _rows("residual", residual, tokens, m)
+        e.residual, e.residual_dtype = residual.data_ptr(), _dtype_code(residual)
+    ws = _scratch(gptq_w4a16_linear_workspace_bytes(tokens, m, n, group_size), X, workspace)
+    with _Device(X):
+        st = lib().gptq_w4a16_linear(X.data_ptr(), tokens, ldx, packed.data_ptr(), _uint8("packed", packed), m, n,
+                                     group_size, ctypes.byref(e), Y.data_ptr(), _dtype_code(Y),
+                                     _rows("Y", Y, tokens, m), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                     _stream(stream))
+    _check(st, "gptq_w4a16_linear")
+    return Y
+
+
+def gptq_w4a16_glu_packed_bytes(m: int, n: int, group_size: int) -> int:
+    return int(lib().gptq_w4a16_glu_packed_bytes(m, n, group_size))
+
+
+def gptq_w4a16_glu_pack(gate_qweight: torch.Tensor, gate_scales: torch.Tensor, gate_zeros: torch.Tensor,
+                        up_qweight: torch.Tensor, up_scales: torch.Tensor, up_zeros: torch.Tensor,
+                        g_idx: torch.Tensor, n: int, bits: int, group_size: int,
+                        packed: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The quantizer's output of gate and up (both m x n, one g_idx: they read
+    one input) -> the glu's layout (uint8 tensor)."""
+    m = gate_qweight.shape[0]
+    if bits in (2, 3, 4):
+        _quantized("gate", gate_qweight, gate_scales, gate_zeros, m, n, group_size)
+        _quantized("up", up_qweight, up_scales, up_zeros, m, n, group_size)
+    _int32(g_idx=g_idx)
+    if g_idx.numel() != n:
+        raise ValueError(f"g_idx must be [{n}]")
+    _on(gate_qweight, gate_scales=gate_scales, gate_zeros=gate_zeros, up_qweight=up_qweight, up_scales=up_scales,
+        up_zeros=up_zeros, g_idx=g_idx, packed=packed)
+    if packed is None:
+        packed = torch.empty(max(gptq_w4a16_glu_packed_bytes(m, n, group_size), 1), dtype=torch.uint8,
+                             device=gate_qweight.device)
+    with _Device(gate_qweight):
+        st = lib().gptq_w4a16_glu_pack(_ptr(gate_qweight), _ptr(gate_scales), _ptr(gate_zeros), _ptr(up_qweight),
+                                       _ptr(up_scales), _ptr(up_zeros), _ptr(g_idx), m, n, bits, group_size,
+                                       _ptr(packed), _uint8("packed", packed), _stream(stream))
+    _check(st, "gptq_w4a16_glu_pack")
+    return packed
+
+
+def gptq_w4a16_glu_workspace_bytes(tokens: int, m: int, n: int, group_size: int) -> int:
+    return int(lib().gptq_w4a16_glu_workspace_bytes(tokens, m, n, group_size))
+
+
+def gptq_w4a16_glu(X: torch.Tensor, packed: torch.Tensor, m: int, n: int, group_size: int, activation: str = "silu",
+                   gate_bias: Optional[torch.Tensor] = None, up_bias: Optional[torch.Tensor] = None,
+                   Y: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y [tokens, m] = act(X·Ŵgᵀ + gate_bias) ⊙ (X·Ŵuᵀ + up_bias) for X
+    [tokens, n] bf16 and gptq_w4a16_glu_pack's packed weight."""
+    ldx = _bf16_rows(X, n)
+    tokens = X.shape[0]
+    _on(X, packed=packed, gate_bias=gate_bias, up_bias=up_bias, Y=Y, workspace=workspace)
+    if Y is None:
+        Y = torch.empty(tokens, m, dtype=out_dtype, device=X.device)
+    some = gate_bias if gate_bias is not None else up_bias
+    if gate_bias is not None and up_bias is not None and gate_bias.dtype != up_bias.dtype:
+        raise TypeError("gate_bias and up_bias must have one dtype")
+    ws = _scratch(gptq_w4a16_glu_workspace_bytes(tokens, m, n, group_size), X, workspace)
+    with _Device(X):
+        st = lib().gptq_w4a16_glu(X.data_ptr(), tokens, ldx, packed.data_ptr(), _uint8("packed", packed), m, n,
+                                  group_size, _activation_code(activation), _vector("gate_bias", gate_bias, m),
+                                  _vector("up_bias", up_bias, m), 0 if some is None else _dtype_code(some),
+                                  Y.data_ptr(), _dtype_code(Y), _rows("Y", Y, tokens, m), ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), _stream(stream))
+    _check(st, "gptq_w4a16_glu")
+    return Y
+
+
+# ---------------------------------------------------------------- mixture of experts
+@dataclass
+class MoeConfig:
+    """Sizes and settings of gptq_w4a16_moe: hidden (the layer's width), inter
+    (an expert's), experts, top_k, the experts' bits and group_size, the
+    gate's activation, and whether the top_k router weights are divided by
+    their sum."""
+    hidden: int
+    inter: int
+    experts: int
+    top_k: int
+    bits: int = 4
+    group_size: int = 64
+    activation: str = "silu"
+    renormalize: bool = True
+
+    def c(self) -> "_lib.GptqMoeConfig":
+        return _lib.GptqMoeConfig(self.hidden, self.inter, self.experts, self.top_k, self.bits, self.group_size,
+                                  _activation_code(self.activation), int(bool(self.renormalize)))
+
+
+def gptq_w4a16_moe_packed_bytes(cfg: MoeConfig) -> int:
+    c = cfg.c()
+    return int(lib().gptq_w4a16_moe_packed_bytes(ctypes.byref(c)))
+
+
+def gptq_w4a16_moe_workspace_bytes(cfg: MoeConfig, tokens: int) -> int:
+    c = cfg.c()
+    return int(lib().gptq_w4a16_moe_workspace_bytes(ctypes.byref(c), tokens))
+
+
+def gptq_w4a16_moe_pack(cfg: MoeConfig, expert: int, gate_qweight: torch.Tensor, gate_scales: torch.Tensor,
+                        gate_zeros: torch.Tensor, up_qweight: torch.Tensor, up_scales: torch.Tensor,
+                        up_zeros: torch.Tensor, g_idx: torch.Tensor, down_qweight: torch.Tensor,
+                        down_scales: torch.Tensor, down_zeros: torch.Tensor, down_g_idx: torch.Tensor,
+                        packed: torch.Tensor, stream=None) -> torch.Tensor:
+    """One expert's quantized weights into its place in `packed`
+    (gptq_w4a16_moe_packed_bytes(cfg) bytes for all experts): gate and up
+    [inter x hidden] share g_idx, down [hidden x inter] has its own."""
+    if cfg.bits in (2, 3, 4):
+        _quantized("gate", gate_qweight, gate_scales, gate_zeros, cfg.inter, cfg.hidden, cfg.group_size)
+        _quantized("up", up_qweight, up_scales, up_zeros, cfg.inter, cfg.hidden, cfg.group_size)
+        _quantized("down", down_qweight, down_scales, down_zeros, cfg.hidden, cfg.inter, cfg.group_size)
+    _int32(g_idx=g_idx, down_g_idx=down_g_idx)
+    if g_idx.numel() != cfg.hidden or down_g_idx.numel() != cfg.inter:
+        raise ValueError(f"g_idx must be [{cfg.hidden}] and down_g_idx [{cfg.inter}]")
+    _on(gate_qweight, gate_scales=gate_scales, gate_zeros=gate_zeros, up_qweight=up_qweight, up_scales=up_scales,
+        up_zeros=up_zeros, g_idx=g_idx, down_qweight=down_qweight, down_scales=down_scales, down_zeros=down_zeros,
+        down_g_idx=down_g_idx, packed=packed)
+    c = cfg.c()
+    with _Device(gate_qweight):
+        st = lib().gptq_w4a16_moe_pack(ctypes.byref(c), expert, _ptr(gate_qweight), _ptr(gate_scales),
+                                       _ptr(gate_zeros), _ptr(up_qweight), _ptr(up_scales), _ptr(up_zeros),
+                                       _ptr(g_idx), _ptr(down_qweight), _ptr(down_scales), _ptr(down_zeros),
+                                       _ptr(down_g_idx), _ptr(packed), _uint8("packed", packed), _stream(stream))
+    _check(st, "gptq_w4a16_moe_pack")
+    return packed
+
+
+def moe_pack_experts(cfg: MoeConfig, experts) -> torch.Tensor:
+    """Allocate the packed buffer and pack every expert: `experts` yields
+    (gate, up, down) output dicts of quantize_layer, quantize_shared_input
+    (gate and up of one expert in one call) or rtn_quantize (which has no
+    g_idx: groups of consecutive columns)."""
+    packed = None
+    count = 0
+
+    def g_idx(o, n):
+        if "g_idx" in o:
+            return o["g_idx"]
+        g = n if cfg.group_size == -1 else cfg.group_size
+        return (torch.arange(n, device=o["qweight"].device) // g).to(torch.int32)
+
+    for expert, (gate, up, down) in enumerate(experts):
+        gi = g_idx(gate, cfg.hidden)
+        if not torch.equal(gi, g_idx(up, cfg.hidden)):
+            raise ValueError(f"expert {expert}: gate and up have different g_idx (quantize them on one input)")
+        if packed is None:
+            packed = torch.empty(max(gptq_w4a16_moe_packed_bytes(cfg), 1), dtype=torch.uint8,
+                                 device=gate["qweight"].device)
+        gptq_w4a16_moe_pack(cfg, expert, gate["qweight"], gate["scales"], gate["zeros"], up["qweight"], up["scales"],
+                            up["zeros"], gi, down["qweight"], down["scales"], down["zeros"],
+                            g_idx(down, cfg.inter), packed)
+        count += 1
+    if count != cfg.experts:
+        raise ValueError(f"{count} experts given, the config has {cfg.experts}")
+    return packed
+
+
+def gptq_w4a16_moe(X: torch.Tensor, router: torch.Tensor, packed: torch.Tensor, cfg: MoeConfig,
+                   residual: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
+                   out_dtype: torch.dtype = torch.bfloat16, topk_ids: Optional[torch.Tensor] = None,
+                   topk_weights: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> tuple:
+    """The whole layer for X [tokens, hidden] bf16: softmax router (weights
+    [experts, hidden], bf16 or fp32), the top_k experts' gated MLPs, their
+    weighted sum plus the residual.  Returns (Y [tokens, hidden], topk_ids
+    int32 [tokens, top_k], topk_weights fp32 [tokens, top_k])."""
+    ldx = _bf16_rows(X, cfg.hidden)
+    tokens = X.shape[0]
+    dev = X.device
+    _on(X, router=router, packed=packed, residual=residual, Y=Y, topk_ids=topk_ids, topk_weights=topk_weights,
+        workspace=workspace)
+    if tuple(router.shape) != (cfg.experts, cfg.hidden) or not router.is_contiguous():
+        raise ValueError(f"router must be a contiguous [{cfg.experts}, {cfg.hidden}]")
+    if Y is None:
+        Y = torch.empty(tokens, cfg.hidden, dtype=out_dtype, device=dev)
+    if topk_ids is None:
+        topk_ids = torch.empty(tokens, cfg.top_k, dtype=torch.int32, device=dev)
+    if topk_weights is None:
+        topk_weights = torch.empty(tokens, cfg.top_k, dtype=torch.float32, device=dev)
+    _int32(topk_ids=topk_ids)
+    if topk_weights.dtype != torch.float32 or not topk_weights.is_contiguous():
+        raise ValueError("topk_weights must be contiguous float32")
+    if not tuple(topk_ids.shape) == tuple(topk_weights.shape) == (tokens, cfg.top_k):
+        raise ValueError(f"topk_ids and topk_weights must be [{tokens}, {cfg.top_k}]")
+    ldr = cfg.hidden if residual is None else _rows("residual", residual, tokens, cfg.hidden)
+    c = cfg.c()
+    ws = _scratch(int(lib().gptq_w4a16_moe_workspace_bytes(ctypes.byref(c), tokens)), X, workspace)
+    with _Device(X):
+        st = lib().gptq_w4a16_moe(X.data_ptr(), tokens, ldx, router.data_ptr(), _dtype_code(router), ctypes.byref(c),
+                                  packed.data_ptr(), _uint8("packed", packed), _ptr(residual),
+                                  0 if residual is None else _dtype_code(residual), ldr, Y.data_ptr(), _dtype_code(Y),
+                                  _rows("Y", Y, tokens, cfg.hidden), topk_ids.data_ptr(), topk_weights.data_ptr(),
+                                  ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
+    _check(st, "gptq_w4a16_moe")
+    return Y, topk_ids, topk_weights
+
+
 # ---------------------------------------------------------------- whole layer
 def alloc_outputs(m: int, n: int, cfg: QuantConfig, device) -> dict:
     words = gptq_qweight_words(n, cfg.bits)
