@@ -417,7 +417,8 @@ gptq_status gptq_w4a16_matmul_noalloc(const void* X, int64_t tokens, int64_t ldx
 // ---------------------------------------------------------------- layers on packed weights
 static bool float_dtype(int32_t d) { return d == GPTQ_BF16 || d == GPTQ_FP32; }
 static size_t dtype_bytes(int32_t d) { return d == GPTQ_FP32 ? 4 : 2; }
-constexpr int64_t kL4MaxDim = (int64_t)1 << 24;
+constexpr int64_t kL4MaxRows = (int64_t)1 << 23;
+constexpr int64_t kL4MaxCols = (int64_t)1 << 20;   // 256 rows of X' stay within 32-bit offsets
 constexpr int64_t kL4MaxTokens = (int64_t)1 << 30;
 
 // the checks that the linear and the glu share; *done: nothing to compute
@@ -431,7 +432,7 @@ static gptq_status check_l4(const void* X, int64_t tokens, int64_t ldx, const vo
   if (activation < GPTQ_ACT_NONE || activation > GPTQ_ACT_GELU_TANH)
     return fail(GPTQ_ERR_UNSUPPORTED, "activation=%d", activation);
   if (!float_dtype(y_dtype)) return fail(GPTQ_ERR_UNSUPPORTED, "y_dtype=%d", y_dtype);
-  if (m > kL4MaxDim || n > kL4MaxDim || tokens > kL4MaxTokens)
+  if (m > kL4MaxRows || n > kL4MaxCols || tokens > kL4MaxTokens)
     return fail(GPTQ_ERR_UNSUPPORTED, "tokens=%lld m=%lld n=%lld too large", (long long)tokens, (long long)m,
                 (long long)n);
   if (tokens == 0 || m == 0) {
@@ -463,10 +464,10 @@ static gptq_status check_l4_tensor(const char* name, const void* p, int32_t dtyp
 }
 
 size_t gptq_w4a16_linear_workspace_bytes(int64_t tokens, int64_t m, int64_t n, int32_t group_size) {
-  if (tokens < 0 || tokens > kL4MaxTokens || m < 0 || m > kL4MaxDim || n <= 0 || n > kL4MaxDim ||
+  if (tokens < 0 || tokens > kL4MaxTokens || m < 0 || m > kL4MaxRows || n <= 0 || n > kL4MaxCols ||
       !w4_group_ok(group_size))
     return 0;
-  return plan_w4a16_linear(tokens, n).total;
+  return plan_w4a16_linear(tokens, n, plan_w4a16(m, n, group_size).mt * 16).total;
 }
 
 gptq_status gptq_w4a16_linear(const void* X, int64_t tokens, int64_t ldx, const void* packed, size_t packed_bytes,
@@ -483,7 +484,7 @@ gptq_status gptq_w4a16_linear(const void* X, int64_t tokens, int64_t ldx, const 
   if (e.residual == Y && (e.residual_dtype != y_dtype || e.ldr != ldy))
     return fail(GPTQ_ERR_INVALID_ARG, "Y is the residual, with another type or row stride");
   const W4Layout L = plan_w4a16(m, n, group_size);
-  const L4LinearPlan p = plan_w4a16_linear(tokens, n);
+  const L4LinearPlan p = plan_w4a16_linear(tokens, n, L.mt * 16);
   GPTQ_TRY(check_l4_buffers(packed_bytes, L.total, workspace, ws_bytes, p.total));
   const L4Call c{static_cast<const uint16_t*>(X), tokens, ldx, m, packed, e.activation, e.bias_dtype,
                  e.residual_dtype, y_dtype, e.bias, nullptr, e.residual, e.ldr, Y, ldy};
@@ -491,7 +492,7 @@ gptq_status gptq_w4a16_linear(const void* X, int64_t tokens, int64_t ldx, const 
 }
 
 size_t gptq_w4a16_glu_packed_bytes(int64_t m, int64_t n, int32_t group_size) {
-  if (m < 0 || n < 0 || m > kL4MaxDim || n > kL4MaxDim || !w4_group_ok(group_size)) return 0;
+  if (m < 0 || n < 0 || m > kL4MaxRows || n > kL4MaxCols || !w4_group_ok(group_size)) return 0;
   return plan_w4a16_pair(m, n, group_size).total;
 }
 
@@ -500,7 +501,7 @@ static gptq_status check_l4_pack(int64_t m, int64_t n, int32_t bits, int32_t gro
   if (bits != 2 && bits != 3 && bits != 4)
     return fail(GPTQ_ERR_UNSUPPORTED, "bits=%d (the W4A16 layers take 2-, 3- and 4-bit codes)", bits);
   if (!w4_group_ok(group_size)) return fail(GPTQ_ERR_UNSUPPORTED, "group_size=%d (32, 64, 128 or -1)", group_size);
-  if (m > kL4MaxDim || n > kL4MaxDim)
+  if (m > kL4MaxRows || n > kL4MaxCols)
     return fail(GPTQ_ERR_UNSUPPORTED, "m=%lld n=%lld too large", (long long)m, (long long)n);
   return GPTQ_OK;
 }
@@ -522,7 +523,10 @@ gptq_status gptq_w4a16_glu_pack(const uint32_t* gate_qweight, const float* gate_
 }
 
 size_t gptq_w4a16_glu_workspace_bytes(int64_t tokens, int64_t m, int64_t n, int32_t group_size) {
-  return gptq_w4a16_linear_workspace_bytes(tokens, m, n, group_size);
+  if (tokens < 0 || tokens > kL4MaxTokens || m < 0 || m > kL4MaxRows || n <= 0 || n > kL4MaxCols ||
+      !w4_group_ok(group_size))
+    return 0;
+  return plan_w4a16_linear(tokens, n, plan_w4a16_pair(m, n, group_size).mt * 16).total;
 }
 
 gptq_status gptq_w4a16_glu(const void* X, int64_t tokens, int64_t ldx, const void* packed, size_t packed_bytes,
@@ -536,7 +540,7 @@ gptq_status gptq_w4a16_glu(const void* X, int64_t tokens, int64_t ldx, const voi
   GPTQ_TRY(check_l4_tensor("gate_bias", gate_bias, bias_dtype));
   GPTQ_TRY(check_l4_tensor("up_bias", up_bias, bias_dtype));
   const W4Layout L = plan_w4a16_pair(m, n, group_size);
-  const L4LinearPlan p = plan_w4a16_linear(tokens, n);
+  const L4LinearPlan p = plan_w4a16_linear(tokens, n, L.mt * 16);
   GPTQ_TRY(check_l4_buffers(packed_bytes, L.total, workspace, ws_bytes, p.total));
   const L4Call c{static_cast<const uint16_t*>(X), tokens, ldx, m, packed, activation, bias_dtype, 0, y_dtype,
                  gate_bias, up_bias, nullptr, 0, Y, ldy};

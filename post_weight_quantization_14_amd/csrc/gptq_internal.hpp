@@ -230,10 +230,11 @@ gptq_status run_w4a16_glu_pack(const L4PairSource& src, const int32_t* g_idx, co
 
 constexpr int64_t kL4BlockTokens = 4096;   // tokens per launch sequence
 struct L4LinearPlan {
-  int64_t block = 0;
-  size_t xs_off = 0, total = 0;
+  int64_t block = 0, tpad = 0;
+  size_t xs_off = 0, part_off = 0, total = 0;
 };
-L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n);
+// packed_rows: 16 x the packed tiles (gate and up together)
+L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n, int64_t packed_rows);
 struct L4Call {
   const uint16_t* X;
   int64_t tokens, ldx, m;

@@ -36,6 +36,18 @@ struct L4Consts {
     r[3] = ((w >> 9) & m) | c;
     return __builtin_bit_cast(bf16x8_t, r);
   }
+  // q - zc for an integer 0 <= zc <= 15 (off = 16 + zc): exact in bf16, so the
+  // upper halves of the fp32 differences are the operand itself
+  __device__ __forceinline__ bf16x8_t unpack_centred(uint32_t w, float off) const {
+    const u32x4_t r = __builtin_bit_cast(u32x4_t, unpack(w));
+    u32x4_t o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float lo = __uint_as_float(r[i] << 16) - off, hi = __uint_as_float(r[i] & 0xffff0000u) - off;
+      o[i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302);
+    }
+    return __builtin_bit_cast(bf16x8_t, o);
+  }
   __device__ __forceinline__ bf16x8_t ones() const {
     return __builtin_bit_cast(bf16x8_t, u32x4_t{one, one, one, one});
   }
@@ -43,6 +55,7 @@ struct L4Consts {
 
 // packed group parameters hold (s, 128 + z)
 __device__ __forceinline__ float l4_zero(float y) { return y - 112.f; }
+__device__ __forceinline__ float l4_centre(float y) { return fminf(fmaxf(y - 128.f, 0.f), 15.f); }
 
 // ---------------------------------------------------------------- the K loop
 // y[r] += the product of one 16-token tile with RT row tiles over chunks
@@ -58,7 +71,12 @@ __device__ __forceinline__ float l4_zero(float y) { return y - 112.f; }
 // in D's layout it already sits where the fold needs it, and the matrix cores
 // are idle in a product that is bound by the code stream.
 // Loads run one batch ahead of the products in registers.
-template <int GS, int RT, int NP, int B, class AF>
+// CENTRED: the operand is q - zc with zc the zero point clamped to 0..15, and
+// only z - zc (0 for a zero point in the code range) is taken off the group
+// sum.  Activations of 24 bits fill the fp32 sums, whose rounding the offset
+// would then magnify (2-bit codes: 1.8e-6 against 4e-7 for the result); it
+// takes 28 VALU instructions per operand instead of 8, so only they use it.
+template <int GS, int RT, int NP, int B, bool CENTRED, class AF>
 __device__ __forceinline__ void l4_stream(const AF& af, const u32x4_t* const (&cp)[RT],
                                           const float2* const (&pp)[RT], int pmul, int c0, int c1,
                                           const L4Consts& kc, f32x4_t (&y)[RT]) {
@@ -108,14 +126,16 @@ __device__ __forceinline__ void l4_stream(const AF& af, const u32x4_t* const (&c
           for (int p = 0; p < NP; ++p) sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], kc.ones(), sx, 0, 0, 0);
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
-            const bf16x8_t w = kc.unpack(b.cw[i][r][j]);
+            const bf16x8_t w = CENTRED ? kc.unpack_centred(b.cw[i][r][j], 16.f + l4_centre(b.p[i][r][g].y))
+                                       : kc.unpack(b.cw[i][r][j]);
 #pragma unroll
             for (int p = 0; p < NP; ++p) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], w, acc[r], 0, 0, 0);
           }
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          const float s = b.p[i][r][g].x, z = l4_zero(b.p[i][r][g].y);
+          const float s = b.p[i][r][g].x, y0 = b.p[i][r][g].y;
+          const float z = CENTRED ? y0 - 128.f - l4_centre(y0) : l4_zero(y0);
 #pragma unroll
           for (int v = 0; v < 4; ++v) y[r][v] = fmaf(s, fmaf(-z, sx[v], acc[r][v]), y[r][v]);
         }

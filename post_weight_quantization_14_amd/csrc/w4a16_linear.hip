@@ -113,7 +113,7 @@ __global__ __launch_bounds__(512) void l4_stream_kernel(L4StreamArgs a) {
   f32x4_t y[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) y[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  l4_stream<GS, RT, 1, (GATED ? 2 : 4)>(af, cp, pp, a.pmul, c0, c1, kc, y);
+  l4_stream<GS, RT, 1, (GATED ? 2 : 4), false>(af, cp, pp, a.pmul, c0, c1, kc, y);
 #pragma unroll
   for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4_t*>(&red[wave][r][lane * 4]) = y[r];
   __syncthreads();
@@ -133,6 +133,300 @@ __global__ __launch_bounds__(512) void l4_stream_kernel(L4StreamArgs a) {
       a.ep.gated(t0 + tl, r, v[0], v[RT - 1]);
     else
       a.ep.linear(t0 + tl, r, v[0]);
+  }
+}
+
+// ---------------------------------------------------------------- many tokens
+// X' = X[:, order] and its group sums, groups-major: sums[c·NG + g][t] for the
+// tile kernel's contiguous copies.  Thread: 8 positions of one token; GS·4
+// threads make one group's sum.  The workgroups of one token run on one XCD
+// (dispatch deals them to the XCDs round-robin), whose L2 then holds its row.
+template <int GS>
+__global__ __launch_bounds__(256) void l4_gather_kernel(const uint16_t* __restrict__ X, int64_t ldx,
+                                                        const int32_t* __restrict__ order, int64_t n128,
+                                                        uint16_t* __restrict__ Xp, float* __restrict__ sums,
+                                                        int64_t tokens, int64_t tpad, int wpt) {
+  const int64_t L = blockIdx.x, q = L >> 3;
+  const int64_t t = (L & 7) + 8 * (q / wpt);
+  if (t >= tokens) return;
+  const int64_t p0 = (q % wpt) * 2048 + 8 * threadIdx.x;
+  if (p0 >= n128) return;   // n128 is a multiple of 128: whole 16-thread groups leave together
+  const int4 o0 = *reinterpret_cast<const int4*>(order + p0), o1 = *reinterpret_cast<const int4*>(order + p0 + 4);
+  const int oi[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+  uint32_t v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {   // unconditional loads, all in flight together
+    const uint16_t x = X[t * ldx + (oi[e] >= 0 ? oi[e] : 0)];
+    v[e] = oi[e] >= 0 ? x : 0u;
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s += __uint_as_float(v[e] << 16);
+  *reinterpret_cast<u32x4_t*>(Xp + t * n128 + p0) =
+      u32x4_t{v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
+#pragma unroll
+  for (int d = 1; d < 4 * GS; d <<= 1) s += __shfl_xor(s, d);
+  if ((threadIdx.x & (4 * GS - 1)) == 0) sums[(p0 / (32 * GS)) * tpad + t] = s;
+}
+
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+struct L4GemmArgs {
+  const uint16_t* Xp;     // [tokens][n128]
+  const float* sums;      // [kc·NG][tpad]
+  const float2* params;
+  const u32x4_t* codes;
+  float* part;            // split K: [splits][token blocks][row blocks][fragments]
+  int64_t n128, kc, Gp, mt, m, tokens, tpad;
+  int64_t tblocks, rblocks;
+  int pmul, splits, chunks;   // K slices, chunks per slice
+  L4Epilogue ep;
+};
+
+// Tile: 64·TG tokens x 64·RG rows, TG·RG waves of (32·MT = 64·..) tokens x 64
+// rows on v_mfma_f32_32x32x16_bf16.
+template <int GS, int MT, int TG, int RG>
+struct L4Tile {
+  static constexpr int kTokens = 32 * MT * TG, kRows = 64 * RG, kWaves = TG * RG;
+  static constexpr int kNG = 4 / GS;
+  static constexpr int kX = kTokens * 256;                 // X' of one chunk
+  static constexpr int kBytes = kX + kNG * kTokens * 4;    // and its group sums
+  static constexpr int kXCopies = kX / 1024 / kWaves;      // 1 KB copies per wave
+  static_assert(kX % (1024 * kWaves) == 0, "copies split evenly over the waves");
+  static_assert(kTokens % 64 == 0, "sums are copied 64 floats at a time");
+};
+
+template <int GS, int MT, int TG, int RG, bool GATED>
+__device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __restrict__ s0, uint8_t* __restrict__ s1) {
+  using Tl = L4Tile<GS, MT, TG, RG>;
+  constexpr int NG = Tl::kNG, U = Tl::kXCopies;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int rg = wave % RG, tg = wave / RG;
+  // slices outermost, then row blocks in bands of token blocks
+  int64_t i = blockIdx.x;
+  const int64_t per = a.tblocks * a.rblocks;
+  const int sl = (int)(i / per);
+  i %= per;
+  const int64_t tb = i % a.tblocks, rb = i / a.tblocks;
+  const int64_t t0 = tb * Tl::kTokens;
+  const int c0 = sl * a.chunks, nch = (int)std::min<int64_t>(a.chunks, a.kc - c0);
+
+  // X' rows past the last token lie outside the descriptor and read as zero
+  const int64_t trows = std::min<int64_t>(Tl::kTokens, a.tokens - t0);
+  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint16_t*>(a.Xp + t0 * a.n128), 0, (int32_t)(trows * a.n128 * 2), 0x00020000);
+  int32_t xoff[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    // 1 KB = 4 token rows of 16 pieces; row t keeps piece p in slot p ^ (t mod 16)
+    const int q = (wave * U + u) * 64 + lane, t = q >> 4, pc = (q & 15) ^ (t & 15);
+    xoff[u] = (int32_t)(t * a.n128 * 2 + pc * 16);
+  }
+  // 64-lane copies of the sums, 4 bytes each, spread over the waves
+  constexpr int SC = NG * Tl::kTokens / 64;
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(a.sums + t0), 0, (int32_t)std::min<int64_t>((a.kc * NG * a.tpad - t0) * 4, 0x7fffffff),
+      0x00020000);
+  auto issue = [&](int c, uint8_t* slot) {
+    const int cc = c0 + std::min(c, nch - 1);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)(slot + (wave * U + u) * 1024), 16, xoff[u], cc * 256, 0, 0);
+#pragma unroll
+    for (int k = 0; k < (SC + Tl::kWaves - 1) / Tl::kWaves; ++k) {
+      const int s = k * Tl::kWaves + wave;
+      if (SC % Tl::kWaves == 0 || s < SC) {
+        const int g = s / (Tl::kTokens / 64), part = s % (Tl::kTokens / 64);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(slot + Tl::kX + s * 256), 4, (part * 64 + lane) * 4,
+                                                (int32_t)((cc * NG + g) * a.tpad * 4), 0, 0);
+      }
+    }
+  };
+
+  // operand b of a wave's 64 rows: lane l feeds row l % 32 of 32, which is row
+  // l % 16 of packed tile 2b + (l / 16) % 2; for a gate/up pair, whose tiles
+  // alternate, tile b + 2·((l / 16) % 2): b = 0 all gate, b = 1 all up.
+  // Positions 32j + 16h + 8(l / 32).. of a chunk are word j of the packed lane
+  // 16·(2h + l / 32) + l % 16.
+  const int half = (lane >> 4) & 1;
+  const u32x4_t* cp[2][2];
+  const float2* pp[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int64_t tile =
+        std::min<int64_t>((rb * RG + rg) * 4 + (GATED ? b + 2 * half : 2 * b + half), a.mt - 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      cp[b][h] = a.codes + (tile * a.kc + c0) * 64 + 16 * (2 * h + (lane >> 5)) + (lane & 15);
+    pp[b] = a.params + tile * a.Gp * kL4Rows + (lane & 15) + (int64_t)c0 * NG * a.pmul;
+  }
+  struct Codes {
+    u32x4_t w[2][2];
+    float2 p[2][NG];
+  };
+  auto fetch = [&](int c, Codes& k) {
+    const int cc = std::min(c, nch - 1);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) k.w[b][h] = cp[b][h][(int64_t)cc * 64];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) k.p[b][g] = pp[b][(int64_t)(cc * NG + g) * a.pmul];
+    }
+  };
+
+  const L4Consts kc;
+  f32x16_t y[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) y[mt][b][v] = 0.f;
+
+  const int trow = lane & 31;   // + 32·(MT·tg + mt): (t mod 16) is lane mod 16
+  // One chunk: per group the operands of its 2·GS steps are unpacked once,
+  // then each 32-token tile runs its chain and is folded while the next
+  // tile's chain runs.
+  auto compute = [&](const uint8_t* cur, const Codes& k) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      bf16x8_t w[2][2 * GS];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int q = 0; q < 2 * GS; ++q) {
+          const int st = g * 2 * GS + q;
+          w[b][q] = kc.unpack(k.w[b][st & 1][st >> 1]);
+        }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int t = 32 * (MT * tg + mt) + trow;
+        f32x16_t acc[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[b][v] = 0.f;
+#pragma unroll
+        for (int q = 0; q < 2 * GS; ++q) {
+          const int st = g * 2 * GS + q;
+          const bf16x8_t av = __builtin_bit_cast(
+              bf16x8_t, *reinterpret_cast<const uint4*>(cur + t * 256 + (((2 * st + (lane >> 5)) ^ (t & 15)) * 16)));
+#pragma unroll
+          for (int b = 0; b < 2; ++b) acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av, w[b][q], acc[b], 0, 0, 0);
+        }
+        // D: lane l, v: token 8·(v / 4) + 4·(l / 32) + v % 4, row l % 32
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4_t sx = *reinterpret_cast<const f32x4_t*>(
+              cur + Tl::kX + (g * Tl::kTokens + 32 * (MT * tg + mt) + 8 * q + 4 * (lane >> 5)) * 4);
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              y[mt][b][4 * q + v] = fmaf(k.p[b][g].x, fmaf(-l4_zero(k.p[b][g].y), sx[v], acc[b][4 * q + v]), y[mt][b][4 * q + v]);
+        }
+      }
+    }
+  };
+
+  Codes k0, k1;
+  issue(0, s0);
+  fetch(0, k0);
+  // one step: every copy of this chunk has landed (all waves', after the
+  // barrier) and every wave is done with the other slot, which the next refills
+#define L4_STEP(c, cur, kcur, nxt, knxt)                                          \
+  {                                                                               \
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");      \
+    issue((c) + 1, nxt);                                                          \
+    fetch((c) + 1, knxt);                                                         \
+    if ((c) < nch) compute(cur, kcur);                                            \
+  }
+  for (int c = 0; c < nch; c += 2) {
+    L4_STEP(c, s0, k0, s1, k1)
+    L4_STEP(c + 1, s1, k1, s0, k0)
+  }
+#undef L4_STEP
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy may land after the workgroup ends
+
+  if (a.splits > 1) {
+    // fragments as they lie: [slice][tile][wave][mt][b][q][lane] float4
+    f32x4_t* out = reinterpret_cast<f32x4_t*>(a.part) +
+                   (((int64_t)sl * per + i) * Tl::kWaves + wave) * (MT * 2 * 4 * 64) + lane;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          out[((mt * 2 + b) * 4 + q) * 64] =
+              f32x4_t{y[mt][b][4 * q], y[mt][b][4 * q + 1], y[mt][b][4 * q + 2], y[mt][b][4 * q + 3]};
+    return;
+  }
+  const int64_t rbase = (rb * RG + rg) * (GATED ? 32 : 64) + (lane & 31);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int64_t t = t0 + 32 * (MT * tg + mt) + 8 * (v / 4) + 4 * (lane >> 5) + (v & 3);
+      if (t >= a.tokens) continue;
+      if (GATED) {
+        if (rbase < a.m) a.ep.gated(t, rbase, y[mt][0][v], y[mt][1][v]);
+      } else {
+        if (rbase < a.m) a.ep.linear(t, rbase, y[mt][0][v]);
+        if (rbase + 32 < a.m) a.ep.linear(t, rbase + 32, y[mt][1][v]);
+      }
+    }
+}
+
+template <int GS, int MT, int TG, int RG, bool GATED>
+__global__ __launch_bounds__(64 * TG * RG, TG * RG == 8 ? 1 : 2) void l4_gemm_kernel(L4GemmArgs a) {
+  using Tl = L4Tile<GS, MT, TG, RG>;
+  // two arrays, not one indexed at run time: a read of one is then known not
+  // to alias the copies in flight into the other
+  __shared__ __attribute__((aligned(16))) uint8_t s0[Tl::kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s1[Tl::kBytes];
+  l4_gemm_tile<GS, MT, TG, RG, GATED>(a, s0, s1);
+}
+
+// Sums the K slices in slice order and finishes.  Thread: one float4 fragment
+// (4 tokens of one row; gate and up together for a pair).
+template <int MT, int TG, int RG, bool GATED>
+__global__ __launch_bounds__(256) void l4_reduce_kernel(L4GemmArgs a) {
+  constexpr int FR = TG * RG * MT * 2 * 4 * 64;   // fragments of one tile
+  const int64_t per = a.tblocks * a.rblocks;
+  int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  constexpr int PER = GATED ? FR / 2 : FR;
+  if (f >= per * PER) return;
+  const int64_t i = f / PER;
+  int k = (int)(f % PER);
+  const int lane = k & 63, q = (k >> 6) & 3;
+  k >>= 8;
+  int b = 0;
+  if (!GATED) {
+    b = k & 1;
+    k >>= 1;
+  }
+  const int mt = k % MT, wave = k / MT, rg = wave % RG, tg = wave / RG;
+  const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.part) + i * FR + ((wave * MT + mt) * 2 + b) * 256 + q * 64 + lane;
+  f32x4_t v0 = p[0], v1 = {0.f, 0.f, 0.f, 0.f};
+  if (GATED) v1 = p[256];
+  for (int s = 1; s < a.splits; ++s) {
+    v0 += p[(int64_t)s * per * FR];
+    if (GATED) v1 += p[(int64_t)s * per * FR + 256];
+  }
+  const int64_t tb = i % a.tblocks, rb = i / a.tblocks;
+  const int64_t t = tb * (32 * MT * TG) + 32 * (MT * tg + mt) + 8 * q + 4 * (lane >> 5);
+  const int64_t r = (rb * RG + rg) * (GATED ? 32 : 64) + 32 * b + (lane & 31);
+  if (r >= a.m) return;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (t + v >= a.tokens) break;
+    if (GATED)
+      a.ep.gated(t + v, r, v0[v], v1[v]);
+    else
+      a.ep.linear(t + v, r, v0[v]);
   }
 }
 
@@ -164,12 +458,76 @@ gptq_status run_w4a16_glu_pack(const L4PairSource& src, const int32_t* g_idx, co
   return check_w4_order(flag, "gptq_w4a16_glu_pack", stream);
 }
 
-L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n) {
+namespace {
+// the tile of `tokens` tokens: its extents, and the K slices that fill the GPU
+struct L4Shape {
+  int mt = 2, tg = 1, rg = 2;
+  int64_t tblocks = 0, rblocks = 0;
+  int splits = 1, chunks = 0;
+  int64_t tile_tokens() const { return 32 * mt * tg; }
+};
+L4Shape l4_shape(int64_t tokens, int64_t packed_rows, int64_t kc) {
+  L4Shape s;
+  s.tg = tokens > 128 ? 4 : tokens > 64 ? 2 : 1;
+  s.rg = s.tg == 1 ? 4 : 2;
+  s.tblocks = ceil_div(tokens, s.tile_tokens());
+  s.rblocks = ceil_div(packed_rows, 64 * s.rg);
+  const int64_t tiles = s.tblocks * s.rblocks;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kc / 4, 256 / tiles));
+  s.chunks = (int)ceil_div(kc, want);
+  s.splits = (int)ceil_div(kc, s.chunks);
+  return s;
+}
+constexpr int64_t kL4StreamTokens = 16;   // up to here the stream kernel
+
+template <int GS, int MT, int TG, int RG, bool GATED>
+gptq_status launch_l4_tile(const L4GemmArgs& g, hipStream_t stream) {
+  const int64_t tiles = g.tblocks * g.rblocks;
+  hipLaunchKernelGGL((l4_gemm_kernel<GS, MT, TG, RG, GATED>), dim3((unsigned)(tiles * g.splits)), dim3(64 * TG * RG), 0,
+                     stream, g);
+  GPTQ_LAUNCH_CHECK();
+  if (g.splits > 1) {
+    const int64_t frags = tiles * TG * RG * MT * 8 * 64 / (GATED ? 2 : 1);
+    hipLaunchKernelGGL((l4_reduce_kernel<MT, TG, RG, GATED>), dim3((unsigned)ceil_div(frags, 256)), dim3(256), 0, stream, g);
+    GPTQ_LAUNCH_CHECK();
+  }
+  return GPTQ_OK;
+}
+
+template <int GS, bool GATED>
+gptq_status launch_l4_shape(const L4GemmArgs& g, const L4Shape& s, hipStream_t stream) {
+  switch (s.tg) {
+    case 1: return launch_l4_tile<GS, 2, 1, 4, GATED>(g, stream);
+    case 2: return launch_l4_tile<GS, 2, 2, 2, GATED>(g, stream);
+    default: return launch_l4_tile<GS, 2, 4, 2, GATED>(g, stream);
+  }
+}
+
+gptq_status launch_l4_gemm(const L4GemmArgs& g, const L4Shape& s, int gs, bool gated, hipStream_t stream) {
+  switch (gs) {
+    case 1: return gated ? launch_l4_shape<1, true>(g, s, stream) : launch_l4_shape<1, false>(g, s, stream);
+    case 2: return gated ? launch_l4_shape<2, true>(g, s, stream) : launch_l4_shape<2, false>(g, s, stream);
+    default: return gated ? launch_l4_shape<4, true>(g, s, stream) : launch_l4_shape<4, false>(g, s, stream);
+  }
+}
+}  // namespace
+
+L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n, int64_t packed_rows) {
   L4LinearPlan p;
-  const int64_t n128 = ceil_div(n, kL4Chunk) * kL4Chunk;
+  const int64_t kc = ceil_div(n, kL4Chunk), n128 = kc * kL4Chunk;
   p.block = std::min<int64_t>(std::max<int64_t>(tokens, 1), kL4BlockTokens);
+  p.tpad = round_up(p.block, 256);
   p.xs_off = align256((size_t)(p.block * n128) * sizeof(uint16_t));
-  p.total = p.xs_off + align256((size_t)(p.block * (n128 / 32 + n128 / 128)) * sizeof(float));
+  p.part_off = p.xs_off + align256((size_t)(p.tpad * (n128 / 32)) * sizeof(float));
+  p.total = p.part_off;
+  // the last, shorter block of a long call may take more slices than the others
+  for (int64_t tk : {p.block, tokens % p.block}) {
+    if (tk <= kL4StreamTokens) continue;
+    const L4Shape s = l4_shape(tk, packed_rows, kc);
+    if (s.splits > 1)
+      p.total = std::max(p.total, p.part_off + align256((size_t)(s.splits * s.tblocks * s.rblocks) *
+                                                        (size_t)(s.tile_tokens() * 64 * s.rg) * sizeof(float)));
+  }
   return p;
 }
 
@@ -196,11 +554,46 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
   const size_t ysz = c.y_dtype == GPTQ_FP32 ? 4 : 2, rsz = c.res_dtype == GPTQ_FP32 ? 4 : 2;
   for (int64_t t0 = 0; t0 < c.tokens; t0 += p.block) {
     const int64_t tk = std::min<int64_t>(p.block, c.tokens - t0);
-    GPTQ_TRY(launch_w4_gather(c.X + t0 * c.ldx, c.ldx, order, L.n128, Xp, xs, xs + tk * (L.n128 / 32), tk, stream));
+    const int wpt = (int)ceil_div(L.n128, 2048);
+    const dim3 ggrid((unsigned)(8 * ceil_div(tk, 8) * wpt));
+#define L4_GATHER(GS)                                                                                     \
+  hipLaunchKernelGGL(l4_gather_kernel<GS>, ggrid, dim3(256), 0, stream, c.X + t0 * c.ldx, c.ldx, order, \
+                     L.n128, Xp, xs, tk, p.tpad, wpt)
+    switch (gs) {
+      case 1: L4_GATHER(1); break;
+      case 2: L4_GATHER(2); break;
+      default: L4_GATHER(4); break;
+    }
+#undef L4_GATHER
+    GPTQ_LAUNCH_CHECK();
     a.tokens = tk;
     a.ep = L4Epilogue{c.act, c.bias_dtype, c.res_dtype, c.y_dtype, c.bias, c.bias2,
                       c.res ? static_cast<const char*>(c.res) + (size_t)(t0 * c.ldr) * rsz : nullptr,
                       static_cast<char*>(c.Y) + (size_t)(t0 * c.ldy) * ysz, c.ldr, c.ldy};
+    if (tk > kL4StreamTokens) {
+      L4GemmArgs g;
+      const L4Shape sh = l4_shape(tk, L.mt * kL4Rows, L.kc);
+      g.Xp = Xp;
+      g.sums = xs;
+      g.params = a.params;
+      g.codes = a.codes;
+      g.part = reinterpret_cast<float*>(w + p.part_off);
+      g.n128 = L.n128;
+      g.kc = L.kc;
+      g.Gp = L.Gp;
+      g.mt = L.mt;
+      g.m = c.m;
+      g.tokens = tk;
+      g.tpad = p.tpad;
+      g.tblocks = sh.tblocks;
+      g.rblocks = sh.rblocks;
+      g.pmul = a.pmul;
+      g.splits = sh.splits;
+      g.chunks = sh.chunks;
+      g.ep = a.ep;
+      GPTQ_TRY(launch_l4_gemm(g, sh, gs, gated, stream));
+      continue;
+    }
     const dim3 grid((unsigned)ceil_div(a.units, 8 >> a.kslog), (unsigned)ceil_div(tk, 16));
 #define L4_STREAM(GS)                                                                            \
   if (gated)                                                                                     \

@@ -227,7 +227,7 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(MoeGateUpArgs a) {
     __syncthreads();
     const L4LdsA af{xsh + std::min(lane & 15, np - 1) * xrow + 8 * (lane >> 4)};
     f32x4_t y[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    l4_stream<GS, 2, 1, 2>(af, cp, pp, a.pmul, c0, c1, kc, y);
+    l4_stream<GS, 2, 1, 2, false>(af, cp, pp, a.pmul, c0, c1, kc, y);
 #pragma unroll
     for (int r = 0; r < 2; ++r) *reinterpret_cast<f32x4_t*>(&red[wave][r][lane * 4]) = y[r];
     __syncthreads();
@@ -289,7 +289,7 @@ __global__ __launch_bounds__(512) void moe_down_kernel(MoeDownArgs a) {
     const L4GlobalA af{a.mid + (int64_t)list.pair[p0 + std::min(lane & 15, np - 1)] * NP * a.f128 + 8 * (lane >> 4),
                        a.f128};
     f32x4_t y[1] = {{0.f, 0.f, 0.f, 0.f}};
-    l4_stream<GS, 1, NP, 2>(af, cp, pp, a.pmul, c0, c1, kc, y);
+    l4_stream<GS, 1, NP, 2, NP == 3>(af, cp, pp, a.pmul, c0, c1, kc, y);
     *reinterpret_cast<f32x4_t*>(&red[wave][lane * 4]) = y[0];
     __syncthreads();
     for (int i = tid; i < upw * 256; i += 512) {
