@@ -162,6 +162,19 @@ struct L4GlobalA {
   }
 };
 
+// one row of n bf16 into LDS (16-byte pieces when the row is 16-byte aligned)
+__device__ __forceinline__ void l4_row_to_lds(const uint16_t* __restrict__ x, int64_t n, int vec, uint8_t* lds, int tid,
+                                              int threads) {
+  int64_t done = 0;
+  if (vec) {
+    const int pieces = (int)(n / 8);
+    for (int i = tid; i < pieces; i += threads)
+      reinterpret_cast<uint4*>(lds)[i] = reinterpret_cast<const uint4*>(x)[i];
+    done = (int64_t)pieces * 8;
+  }
+  for (int64_t i = done + tid; i < n; i += threads) reinterpret_cast<uint16_t*>(lds)[i] = x[i];
+}
+
 // ---------------------------------------------------------------- values
 __device__ __forceinline__ float l4_load(const void* p, int dtype, int64_t i) {
   if (dtype == GPTQ_FP32) return static_cast<const float*>(p)[i];

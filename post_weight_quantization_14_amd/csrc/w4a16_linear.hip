@@ -62,6 +62,50 @@ struct L4Epilogue {
   const void *bias, *bias2, *res;
   void* Y;
   int64_t ldr, ldy;
+  // N tokens (runs of 4, 8 apart, from t) of one row: every residual load is
+  // in flight before the first is used.  Under the type's branch and a range
+  // check each, they would be one memory latency apart.
+  template <int N, bool GATED>
+  __device__ __forceinline__ void block(int64_t t, int64_t tokens, int64_t r, int64_t m, const float (&v)[N],
+                                        const float (&u)[N]) const {
+    if (r >= m || t >= tokens) return;
+    const float b0 = bias ? l4_load(bias, bias_dt, r) : 0.f;
+    float z[N];
+    if (GATED) {
+      const float b1 = bias2 ? l4_load(bias2, bias_dt, r) : 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = l4_activate(v[i] + b0, act) * (u[i] + b1);
+    } else {
+      float rv[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) rv[i] = 0.f;
+      if (res) {
+        int64_t at[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) at[i] = std::min<int64_t>(t + 8 * (i / 4) + (i & 3), tokens - 1) * ldr + r;
+        if (res_dt == GPTQ_FP32) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) rv[i] = static_cast<const float*>(res)[at[i]];
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            rv[i] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(res)[at[i]] << 16);
+        }
+      }
+      if (act == GPTQ_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = v[i] + b0 + rv[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = l4_activate(v[i] + b0, act) + rv[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t ti = t + 8 * (i / 4) + (i & 3);
+      if (ti < tokens) l4_store(Y, y_dt, ti * ldy + r, z[i]);
+    }
+  }
   __device__ __forceinline__ void linear(int64_t t, int64_t r, float v) const {
     if (bias) v += l4_load(bias, bias_dt, r);
     v = l4_activate(v, act);
@@ -137,36 +181,55 @@ __global__ __launch_bounds__(512) void l4_stream_kernel(L4StreamArgs a) {
 }
 
 // ---------------------------------------------------------------- many tokens
-// X' = X[:, order] and its group sums, groups-major: sums[c·NG + g][t] for the
-// tile kernel's contiguous copies.  Thread: 8 positions of one token; GS·4
-// threads make one group's sum.  The workgroups of one token run on one XCD
-// (dispatch deals them to the XCDs round-robin), whose L2 then holds its row.
-template <int GS>
-__global__ __launch_bounds__(256) void l4_gather_kernel(const uint16_t* __restrict__ X, int64_t ldx,
-                                                        const int32_t* __restrict__ order, int64_t n128,
+// X' = X[:, order] and its group sums, groups-major (sums[c·NG + g][t], for the
+// tile kernel's contiguous copies).  A row of X is read once, 16 bytes a
+// thread, into LDS and gathered from there: 2-byte loads at scattered columns
+// cost the memory pipe a cycle or more a lane (2048 x 4096: 13 us, through
+// LDS 4), LDS serves 64 of them in a few cycles.  Thread: 8 positions; GS·4
+// threads make one group's sum; a workgroup covers 4096 positions of `per`
+// tokens one after the other, keeping its part of the order in registers.
+template <int GS, bool LDS>
+__global__ __launch_bounds__(512) void l4_gather_kernel(const uint16_t* __restrict__ X, int64_t ldx,
+                                                        const int32_t* __restrict__ order, int64_t n, int64_t n128,
                                                         uint16_t* __restrict__ Xp, float* __restrict__ sums,
-                                                        int64_t tokens, int64_t tpad, int wpt) {
-  const int64_t L = blockIdx.x, q = L >> 3;
-  const int64_t t = (L & 7) + 8 * (q / wpt);
-  if (t >= tokens) return;
-  const int64_t p0 = (q % wpt) * 2048 + 8 * threadIdx.x;
-  if (p0 >= n128) return;   // n128 is a multiple of 128: whole 16-thread groups leave together
-  const int4 o0 = *reinterpret_cast<const int4*>(order + p0), o1 = *reinterpret_cast<const int4*>(order + p0 + 4);
-  const int oi[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-  uint32_t v[8];
+                                                        int64_t tokens, int64_t tpad, int per, int vec) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tid = threadIdx.x;
+  const int64_t p0 = (int64_t)blockIdx.y * 4096 + 8 * tid;
+  const bool live = p0 < n128;   // n128 is a multiple of 128: whole 16-thread groups agree
+  int oi[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {   // unconditional loads, all in flight together
-    const uint16_t x = X[t * ldx + (oi[e] >= 0 ? oi[e] : 0)];
-    v[e] = oi[e] >= 0 ? x : 0u;
+  for (int e = 0; e < 8; ++e) oi[e] = -1;
+  if (live) {
+    const int4 o0 = *reinterpret_cast<const int4*>(order + p0), o1 = *reinterpret_cast<const int4*>(order + p0 + 4);
+    oi[0] = o0.x, oi[1] = o0.y, oi[2] = o0.z, oi[3] = o0.w;
+    oi[4] = o1.x, oi[5] = o1.y, oi[6] = o1.z, oi[7] = o1.w;
   }
-  float s = 0.f;
+  const int64_t ta = (int64_t)blockIdx.x * per, te = std::min<int64_t>(tokens, ta + per);
+  for (int64_t t = ta; t < te; ++t) {
+    const uint16_t* x = X + t * ldx;
+    if (LDS) {
+      if (t != ta) __syncthreads();   // the row before has been gathered
+      l4_row_to_lds(x, n, vec, lds, tid, 512);
+      __syncthreads();
+      x = reinterpret_cast<const uint16_t*>(lds);
+    }
+    if (!live) continue;
+    uint32_t v[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s += __uint_as_float(v[e] << 16);
-  *reinterpret_cast<u32x4_t*>(Xp + t * n128 + p0) =
-      u32x4_t{v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
+    for (int e = 0; e < 8; ++e) {   // unconditional reads, all in flight together
+      const uint16_t xe = x[oi[e] >= 0 ? oi[e] : 0];
+      v[e] = oi[e] >= 0 ? xe : 0u;
+    }
+    float s = 0.f;
 #pragma unroll
-  for (int d = 1; d < 4 * GS; d <<= 1) s += __shfl_xor(s, d);
-  if ((threadIdx.x & (4 * GS - 1)) == 0) sums[(p0 / (32 * GS)) * tpad + t] = s;
+    for (int e = 0; e < 8; ++e) s += __uint_as_float(v[e] << 16);
+    *reinterpret_cast<u32x4_t*>(Xp + t * n128 + p0) =
+        u32x4_t{v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
+#pragma unroll
+    for (int d = 1; d < 4 * GS; d <<= 1) s += __shfl_xor(s, d);
+    if ((tid & (4 * GS - 1)) == 0) sums[(p0 / (32 * GS)) * tpad + t] = s;
+  }
 }
 
 typedef __attribute__((address_space(3))) void lds_void_t;
@@ -286,37 +349,54 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
       for (int v = 0; v < 16; ++v) y[mt][b][v] = 0.f;
 
   const int trow = lane & 31;   // + 32·(MT·tg + mt): (t mod 16) is lane mod 16
-  // One chunk: per group the operands of its 2·GS steps are unpacked once,
-  // then each 32-token tile runs its chain and is folded while the next
-  // tile's chain runs.
+  // One chunk.  Per 16-position step: the next step's A fragments are read
+  // from LDS, this step's two operands are unpacked and MT·2 products issued;
+  // the scheduling barriers spread the VALU work between the matrix
+  // instructions (left alone the compiler unpacks a whole group first, and
+  // reads each fragment right before its use).
   auto compute = [&](const uint8_t* cur, const Codes& k) {
+    auto frag = [&](int st, int mt) {
+      const int t = 32 * (MT * tg + mt) + trow;
+      return *reinterpret_cast<const u32x4_t*>(cur + t * 256 + (((2 * st + (lane >> 5)) ^ (t & 15)) * 16));
+    };
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      bf16x8_t w[2][2 * GS];
+      f32x16_t acc[MT][2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int q = 0; q < 2 * GS; ++q) {
-          const int st = g * 2 * GS + q;
-          w[b][q] = kc.unpack(k.w[b][st & 1][st >> 1]);
-        }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int t = 32 * (MT * tg + mt) + trow;
-        f32x16_t acc[2];
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int v = 0; v < 16; ++v) acc[b][v] = 0.f;
+          for (int v = 0; v < 16; ++v) acc[mt][b][v] = 0.f;
+      u32x4_t av[2][MT];
 #pragma unroll
-        for (int q = 0; q < 2 * GS; ++q) {
-          const int st = g * 2 * GS + q;
-          const bf16x8_t av = __builtin_bit_cast(
-              bf16x8_t, *reinterpret_cast<const uint4*>(cur + t * 256 + (((2 * st + (lane >> 5)) ^ (t & 15)) * 16)));
+      for (int mt = 0; mt < MT; ++mt) av[0][mt] = frag(g * 2 * GS, mt);
 #pragma unroll
-          for (int b = 0; b < 2; ++b) acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av, w[b][q], acc[b], 0, 0, 0);
+      for (int q = 0; q < 2 * GS; ++q) {
+        const int st = g * 2 * GS + q;
+        if (q + 1 < 2 * GS) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) av[(q + 1) & 1][mt] = frag(st + 1, mt);
         }
-        // D: lane l, v: token 8·(v / 4) + 4·(l / 32) + v % 4, row l % 32
+        bf16x8_t w[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) w[b] = kc.unpack(k.w[b][st & 1][st >> 1]);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            acc[mt][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, av[q & 1][mt]), w[b],
+                                                                 acc[mt][b], 0, 0, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, MT, 0);   // LDS reads
+#pragma unroll
+        for (int u = 0; u < 2 * MT; ++u) {
+          __builtin_amdgcn_sched_group_barrier(0x002, 16 / (2 * MT), 0);   // VALU
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);               // MFMA
+        }
+      }
+      // D: lane l, v: token 8·(v / 4) + 4·(l / 32) + v % 4, row l % 32
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const f32x4_t sx = *reinterpret_cast<const f32x4_t*>(
@@ -325,9 +405,9 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
           for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-              y[mt][b][4 * q + v] = fmaf(k.p[b][g].x, fmaf(-l4_zero(k.p[b][g].y), sx[v], acc[b][4 * q + v]), y[mt][b][4 * q + v]);
+              y[mt][b][4 * q + v] =
+                  fmaf(k.p[b][g].x, fmaf(-l4_zero(k.p[b][g].y), sx[v], acc[mt][b][4 * q + v]), y[mt][b][4 * q + v]);
         }
-      }
     }
   };
 
@@ -366,18 +446,20 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
   }
   const int64_t rbase = (rb * RG + rg) * (GATED ? 32 : 64) + (lane & 31);
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int mt = 0; mt < MT; ++mt) {
+    const int64_t t = t0 + 32 * (MT * tg + mt) + 4 * (lane >> 5);
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int64_t t = t0 + 32 * (MT * tg + mt) + 8 * (v / 4) + 4 * (lane >> 5) + (v & 3);
-      if (t >= a.tokens) continue;
-      if (GATED) {
-        if (rbase < a.m) a.ep.gated(t, rbase, y[mt][0][v], y[mt][1][v]);
-      } else {
-        if (rbase < a.m) a.ep.linear(t, rbase, y[mt][0][v]);
-        if (rbase + 32 < a.m) a.ep.linear(t, rbase + 32, y[mt][1][v]);
+    for (int q = 0; q < 4; q += 2) {   // 8 tokens at a time: tokens t + 8q + {0..3, 8..11}
+      float v0[8], v1[8];
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        v0[v] = y[mt][0][4 * q + v];
+        v1[v] = y[mt][1][4 * q + v];
       }
+      a.ep.template block<8, GATED>(t + 8 * q, a.tokens, rbase, a.m, v0, v1);
+      if (!GATED) a.ep.template block<8, false>(t + 8 * q, a.tokens, rbase + 32, a.m, v1, v1);
     }
+  }
 }
 
 template <int GS, int MT, int TG, int RG, bool GATED>
@@ -419,15 +501,8 @@ __global__ __launch_bounds__(256) void l4_reduce_kernel(L4GemmArgs a) {
   const int64_t tb = i % a.tblocks, rb = i / a.tblocks;
   const int64_t t = tb * (32 * MT * TG) + 32 * (MT * tg + mt) + 8 * q + 4 * (lane >> 5);
   const int64_t r = (rb * RG + rg) * (GATED ? 32 : 64) + 32 * b + (lane & 31);
-  if (r >= a.m) return;
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    if (t + v >= a.tokens) break;
-    if (GATED)
-      a.ep.gated(t + v, r, v0[v], v1[v]);
-    else
-      a.ep.linear(t + v, r, v0[v]);
-  }
+  const float g4[4] = {v0[0], v0[1], v0[2], v0[3]}, u4[4] = {v1[0], v1[1], v1[2], v1[3]};
+  a.ep.template block<4, GATED>(t, a.tokens, r, a.m, g4, u4);
 }
 
 }  // namespace
@@ -468,7 +543,7 @@ struct L4Shape {
 };
 L4Shape l4_shape(int64_t tokens, int64_t packed_rows, int64_t kc) {
   L4Shape s;
-  s.tg = tokens > 128 ? 4 : tokens > 64 ? 2 : 1;
+  s.tg = tokens > 64 ? 2 : 1;
   s.rg = s.tg == 1 ? 4 : 2;
   s.tblocks = ceil_div(tokens, s.tile_tokens());
   s.rblocks = ceil_div(packed_rows, 64 * s.rg);
@@ -478,6 +553,7 @@ L4Shape l4_shape(int64_t tokens, int64_t packed_rows, int64_t kc) {
   s.splits = (int)ceil_div(kc, s.chunks);
   return s;
 }
+constexpr size_t kL4GatherLds = 65536;    // rows up to 32768 columns are gathered through LDS
 constexpr int64_t kL4StreamTokens = 16;   // up to here the stream kernel
 
 template <int GS, int MT, int TG, int RG, bool GATED>
@@ -554,11 +630,18 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
   const size_t ysz = c.y_dtype == GPTQ_FP32 ? 4 : 2, rsz = c.res_dtype == GPTQ_FP32 ? 4 : 2;
   for (int64_t t0 = 0; t0 < c.tokens; t0 += p.block) {
     const int64_t tk = std::min<int64_t>(p.block, c.tokens - t0);
-    const int wpt = (int)ceil_div(L.n128, 2048);
-    const dim3 ggrid((unsigned)(8 * ceil_div(tk, 8) * wpt));
-#define L4_GATHER(GS)                                                                                     \
-  hipLaunchKernelGGL(l4_gather_kernel<GS>, ggrid, dim3(256), 0, stream, c.X + t0 * c.ldx, c.ldx, order, \
-                     L.n128, Xp, xs, tk, p.tpad, wpt)
+    // a row of X in LDS, rounded up to whole 16-byte pieces of 512 threads
+    const size_t glds = (size_t)L.n * 2 <= kL4GatherLds ? (size_t)round_up(L.n * 2, 16) : 0;
+    const int vec = (reinterpret_cast<uintptr_t>(c.X) & 15) == 0 && c.ldx % 8 == 0;
+    const int per = 1;
+    const dim3 ggrid((unsigned)ceil_div(tk, per), (unsigned)ceil_div(L.n128, 4096));
+#define L4_GATHER(GS)                                                                                          \
+  if (glds)                                                                                                    \
+    hipLaunchKernelGGL((l4_gather_kernel<GS, true>), ggrid, dim3(512), glds, stream, c.X + t0 * c.ldx, c.ldx, order, \
+                       L.n, L.n128, Xp, xs, tk, p.tpad, per, vec);                                             \
+  else                                                                                                         \
+    hipLaunchKernelGGL((l4_gather_kernel<GS, false>), ggrid, dim3(512), 0, stream, c.X + t0 * c.ldx, c.ldx, order, \
+                       L.n, L.n128, Xp, xs, tk, p.tpad, per, vec)
     switch (gs) {
       case 1: L4_GATHER(1); break;
       case 2: L4_GATHER(2); break;

@@ -426,6 +426,19 @@ def _vector(name: str, t: Optional[torch.Tensor], m: int) -> Optional[int]:
     return t.data_ptr()
 
 
+# the handle of a device's current stream, without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(X: torch.Tensor, stream) -> Optional[int]:
+    """The given stream, or the current stream of X's device."""
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(X.device.index)
+        stream = torch.cuda.current_stream(X.device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _bf16_rows(X: torch.Tensor, n: int) -> int:
     if X.dim() != 2 or X.shape[1] != n or (X.shape[0] > 0 and n > 1 and X.stride(1) != 1):
         raise ValueError(f"X must be [tokens, {n}] with contiguous rows")
@@ -437,7 +450,7 @@ def _bf16_rows(X: torch.Tensor, n: int) -> int:
 def _uint8(name: str, t: torch.Tensor) -> int:
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 def _scratch(nbytes: int, X: torch.Tensor, workspace: Optional[torch.Tensor]) -> torch.Tensor:
@@ -512,8 +525,7 @@ def gptq_w4a16_linear(X: torch.Tensor, packed: torch.Tensor, m: int, n: int, gro
     with _Device(X):
         st = lib().gptq_w4a16_linear(X.data_ptr(), tokens, ldx, packed.data_ptr(), _uint8("packed", packed), m, n,
                                      group_size, ctypes.byref(e), Y.data_ptr(), _dtype_code(Y),
-                                     _rows("Y", Y, tokens, m), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                     _stream(stream))
+                                     _rows("Y", Y, tokens, m), ws.data_ptr(), ws.nbytes, _stream_on(X, stream))
     _check(st, "gptq_w4a16_linear")
     return Y
 
@@ -543,7 +555,7 @@ def gptq_w4a16_glu_pack(gate_qweight: torch.Tensor, gate_scales: torch.Tensor, g
     with _Device(gate_qweight):
         st = lib().gptq_w4a16_glu_pack(_ptr(gate_qweight), _ptr(gate_scales), _ptr(gate_zeros), _ptr(up_qweight),
                                        _ptr(up_scales), _ptr(up_zeros), _ptr(g_idx), m, n, bits, group_size,
-                                       _ptr(packed), _uint8("packed", packed), _stream(stream))
+                                       _ptr(packed), _uint8("packed", packed), _stream_on(gate_qweight, stream))
     _check(st, "gptq_w4a16_glu_pack")
     return packed
 
@@ -571,8 +583,8 @@ def gptq_w4a16_glu(X: torch.Tensor, packed: torch.Tensor, m: int, n: int, group_
         st = lib().gptq_w4a16_glu(X.data_ptr(), tokens, ldx, packed.data_ptr(), _uint8("packed", packed), m, n,
                                   group_size, _activation_code(activation), _vector("gate_bias", gate_bias, m),
                                   _vector("up_bias", up_bias, m), 0 if some is None else _dtype_code(some),
-                                  Y.data_ptr(), _dtype_code(Y), _rows("Y", Y, tokens, m), ws.data_ptr(),
-                                  ws.numel() * ws.element_size(), _stream(stream))
+                                  Y.data_ptr(), _dtype_code(Y), _rows("Y", Y, tokens, m), ws.data_ptr(), ws.nbytes,
+                                  _stream_on(X, stream))
     _check(st, "gptq_w4a16_glu")
     return Y
 
@@ -631,7 +643,7 @@ def gptq_w4a16_moe_pack(cfg: MoeConfig, expert: int, gate_qweight: torch.Tensor,
         st = lib().gptq_w4a16_moe_pack(ctypes.byref(c), expert, _ptr(gate_qweight), _ptr(gate_scales),
                                        _ptr(gate_zeros), _ptr(up_qweight), _ptr(up_scales), _ptr(up_zeros),
                                        _ptr(g_idx), _ptr(down_qweight), _ptr(down_scales), _ptr(down_zeros),
-                                       _ptr(down_g_idx), _ptr(packed), _uint8("packed", packed), _stream(stream))
+                                       _ptr(down_g_idx), _ptr(packed), _uint8("packed", packed), _stream_on(gate_qweight, stream))
     _check(st, "gptq_w4a16_moe_pack")
     return packed
 
@@ -701,7 +713,7 @@ def gptq_w4a16_moe(X: torch.Tensor, router: torch.Tensor, packed: torch.Tensor, 
                                   packed.data_ptr(), _uint8("packed", packed), _ptr(residual),
                                   0 if residual is None else _dtype_code(residual), ldr, Y.data_ptr(), _dtype_code(Y),
                                   _rows("Y", Y, tokens, cfg.hidden), topk_ids.data_ptr(), topk_weights.data_ptr(),
-                                  ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
+                                  ws.data_ptr(), ws.nbytes, _stream_on(X, stream))
     _check(st, "gptq_w4a16_moe")
     return Y, topk_ids, topk_weights
 
