@@ -3,6 +3,8 @@
 // 16-row tile, activations and typed loads and stores.
 #pragma once
 
+#include <algorithm>
+
 #include "gptq_internal.hpp"
 
 namespace gptq {
@@ -57,54 +59,81 @@ struct L4Consts {
 __device__ __forceinline__ float l4_zero(float y) { return y - 112.f; }
 __device__ __forceinline__ float l4_centre(float y) { return fminf(fmaxf(y - 128.f, 0.f), 15.f); }
 
-// ---------------------------------------------------------------- the K loop
-// y[r] += the product of one 16-token tile with RT row tiles over chunks
-// [c0, c1), NP planes of A summed (x = plane 0 + plane 1).  GS = 32-position
-// steps per group (1, 2, 4); one group per row is passed as GS = 4 with
-// pmul = 0, which folds the group's scale in after every chunk (the formula is
-// linear in the chunk) and keeps the offset sums short.
-//   cp[r]  codes of row tile r, this lane's u32x4 of chunk 0
-//   pp[r]  (s, 128 + z) of this lane's row, group 0; groups are pmul (16) apart
-//   af     A fragments: load(c, j, p) = 8 positions 128c + 32j + 8·(lane/16)
-//          of this lane's token row (lane % 16), plane p
+// ---------------------------------------------------------------- few tokens
+// The kernels of up to 16 tokens are bound by the code stream from HBM.  A
+// workgroup of 16 waves takes `rounds` rounds of units (a unit is RT row tiles
+// of 16 weight rows), 16 / ks units a round with ks waves splitting the K
+// range of each, and every wave keeps B·RT KB of codes in flight through all
+// of its rounds: the next batch, of the same unit or the next one, is loaded
+// before the current one is multiplied.
+constexpr int kL4Waves = 16;
+constexpr int kL4Threads = 64 * kL4Waves;
+
+struct L4Stream {
+  const u32x4_t* codes;    // [units·RT][kc][64]
+  const float2* params;    // [units·RT][Gp][16]: (s, 128 + z)
+  int64_t kc, Gp, units;
+  int pmul;                // distance of groups in params: 16, or 0 for one group per row
+  int kslog, rounds;
+};
+
+// Runs a wave's share.  GS = 32-position steps per group (1, 2, 4); one group
+// per row is GS = 4 with pmul = 0: its scale is folded in after every chunk
+// (the formula is linear in the chunk), which keeps the offset sums short.
+// NP: planes of A that are summed (x = plane 0 + plane 1 + ..).
+//   fill()            puts A where `af` reads it; called by every wave once,
+//                     after the first batch of codes has been requested
+//   af.load(c, j, p)  8 positions 128c + 32j + 8·(lane/16) of token lane % 16
+//   end(unit, y)      the wave's sums of its K share of a unit, every round
 // The group sum Σx comes from the matrix cores too (A times a tile of ones):
 // in D's layout it already sits where the fold needs it, and the matrix cores
-// are idle in a product that is bound by the code stream.
-// Loads run one batch ahead of the products in registers.
+// are idle in a product that is bound by its codes.
 // CENTRED: the operand is q - zc with zc the zero point clamped to 0..15, and
 // only z - zc (0 for a zero point in the code range) is taken off the group
 // sum.  Activations of 24 bits fill the fp32 sums, whose rounding the offset
 // would then magnify (2-bit codes: 1.8e-6 against 4e-7 for the result); it
 // takes 28 VALU instructions per operand instead of 8, so only they use it.
-template <int GS, int RT, int NP, int B, bool CENTRED, class AF>
-__device__ __forceinline__ void l4_stream(const AF& af, const u32x4_t* const (&cp)[RT],
-                                          const float2* const (&pp)[RT], int pmul, int c0, int c1,
-                                          const L4Consts& kc, f32x4_t (&y)[RT]) {
+template <int GS, int RT, int NP, int B, bool CENTRED, class AF, class FF, class EF>
+__device__ __forceinline__ void l4_units(const L4Stream& st, int64_t first, int64_t step, const AF& af, const FF& fill,
+                                         const EF& end) {
   constexpr int NG = 4 / GS;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int ks = 1 << st.kslog, sl = wave & (ks - 1);
+  const int cps = (int)((st.kc + ks - 1) >> st.kslog);
+  const int c0 = sl * cps, c1 = (int)std::min<int64_t>(st.kc, c0 + cps);
+  const int64_t u0 = first + (wave >> st.kslog);
+  const L4Consts kc;
   struct Batch {
     u32x4_t cw[B][RT];
     float2 p[B][RT][NG];
-    uint4 a[B][AF::kPrefetch ? 4 : 1][NP];
+    uint4 a[AF::kPrefetch ? B : 1][AF::kPrefetch ? 4 : 1][NP];
   };
-  const int last = c1 - 1;
-  auto load = [&](int c, Batch& b) {
+  auto load = [&](int r, int c, Batch& b) {
+    const int64_t unit = std::min<int64_t>(u0 + r * step, st.units - 1);   // past the last: computed, not stored
 #pragma unroll
-    for (int i = 0; i < B; ++i) {
-      const int cc = c + i < last ? c + i : last;   // past the end: the last chunk again, not used
+    for (int t = 0; t < RT; ++t) {
+      const u32x4_t* cp = st.codes + (unit * RT + t) * st.kc * 64 + lane;
+      const float2* pp = st.params + (unit * RT + t) * st.Gp * kL4Rows + (lane & 15);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) b.cw[i][r] = cp[r][(int64_t)cc * 64];
+      for (int i = 0; i < B; ++i) {
+        const int cc = std::max(0, std::min(c + i, c1 - 1));   // past the end: the last chunk again, not used
+        b.cw[i][t] = cp[(int64_t)cc * 64];
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+        for (int g = 0; g < NG; ++g) b.p[i][t][g] = pp[(int64_t)(cc * NG + g) * st.pmul];
+      }
+    }
+    if (AF::kPrefetch) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g) b.p[i][r][g] = pp[r][(int64_t)(cc * NG + g) * pmul];
-      if (AF::kPrefetch) {
+      for (int i = 0; i < B; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int p = 0; p < NP; ++p) b.a[i][AF::kPrefetch ? j : 0][p] = af.load(cc, j, p);
-      }
+          for (int p = 0; p < NP; ++p)
+            b.a[AF::kPrefetch ? i : 0][AF::kPrefetch ? j : 0][p] = af.load(std::max(0, std::min(c + i, c1 - 1)), j, p);
     }
   };
+  f32x4_t y[RT];
   auto compute = [&](int c, const Batch& b) {
 #pragma unroll
     for (int i = 0; i < B; ++i) {
@@ -114,42 +143,90 @@ __device__ __forceinline__ void l4_stream(const AF& af, const u32x4_t* const (&c
         f32x4_t sx = {0.f, 0.f, 0.f, 0.f};
         f32x4_t acc[RT];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) acc[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < RT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int q = 0; q < GS; ++q) {
           const int j = g * GS + q;
           bf16x8_t a[NP];
 #pragma unroll
           for (int p = 0; p < NP; ++p)
-            a[p] = __builtin_bit_cast(bf16x8_t, AF::kPrefetch ? b.a[i][AF::kPrefetch ? j : 0][p] : af.load(c + i, j, p));
+            a[p] = __builtin_bit_cast(
+                bf16x8_t, AF::kPrefetch ? b.a[AF::kPrefetch ? i : 0][AF::kPrefetch ? j : 0][p] : af.load(c + i, j, p));
 #pragma unroll
           for (int p = 0; p < NP; ++p) sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], kc.ones(), sx, 0, 0, 0);
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const bf16x8_t w = CENTRED ? kc.unpack_centred(b.cw[i][r][j], 16.f + l4_centre(b.p[i][r][g].y))
-                                       : kc.unpack(b.cw[i][r][j]);
+          for (int t = 0; t < RT; ++t) {
+            const bf16x8_t w = CENTRED ? kc.unpack_centred(b.cw[i][t][j], 16.f + l4_centre(b.p[i][t][g].y))
+                                       : kc.unpack(b.cw[i][t][j]);
 #pragma unroll
-            for (int p = 0; p < NP; ++p) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], w, acc[r], 0, 0, 0);
+            for (int p = 0; p < NP; ++p) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], w, acc[t], 0, 0, 0);
           }
         }
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const float s = b.p[i][r][g].x, y0 = b.p[i][r][g].y;
+        for (int t = 0; t < RT; ++t) {
+          const float s = b.p[i][t][g].x, y0 = b.p[i][t][g].y;
           const float z = CENTRED ? y0 - 128.f - l4_centre(y0) : l4_zero(y0);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) y[r][v] = fmaf(s, fmaf(-z, sx[v], acc[r][v]), y[r][v]);
+          for (int v = 0; v < 4; ++v) y[t][v] = fmaf(s, fmaf(-z, sx[v], acc[t][v]), y[t][v]);
         }
       }
     }
   };
-  if (c0 >= c1) return;
   Batch cur, nxt;
-  load(c0, cur);
-  for (int c = c0; c < c1; c += B) {
-    load(c + B, nxt);
-    compute(c, cur);
-    cur = nxt;
+  load(0, c0, cur);
+  fill();
+  for (int r = 0; r < st.rounds; ++r) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) y[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int c = c0; c < c1; c += B) {
+      const bool more = c + B < c1;
+      load(more ? r : std::min(r + 1, st.rounds - 1), more ? c + B : c0, nxt);
+      compute(c, cur);
+      cur = nxt;
+    }
+    end(u0 + r * step, y);
   }
+}
+
+// Sums of the ks waves of each unit, in wave order, through LDS.  red: [16
+// waves][RT][quads][64] floats, quads = 4-token groups that hold tokens.  Calls
+// out(unit, token, row, value[RT]) once per result; every wave calls it.
+template <int RT, class OF>
+__device__ __forceinline__ void l4_finish(float* red, int quads, int tokens, int kslog, int64_t unit,
+                                          const f32x4_t (&y)[RT], const OF& out) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (kslog == 0) {   // every wave holds its whole unit: D[4·(lane/16) + v][lane % 16]
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      if (4 * (lane >> 4) + v >= tokens) break;
+      float z[RT];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) z[t] = y[t][v];
+      out(unit, 4 * (lane >> 4) + v, lane & 15, z);
+    }
+    return;
+  }
+  const int ks = 1 << kslog, upw = kL4Waves >> kslog;
+  if ((lane >> 4) < quads) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+      *reinterpret_cast<f32x4_t*>(red + ((wave * RT + t) * quads + (lane >> 4)) * 64 + (lane & 15) * 4) = y[t];
+  }
+  __syncthreads();
+  const int64_t base = unit - (wave >> kslog);   // the round's first unit
+  for (int i = tid; i < upw * quads * 64; i += kL4Threads) {
+    const int ul = i / (quads * 64), tok = (i >> 4) % (quads * 4), row = i & 15;
+    if (tok >= tokens) continue;
+    float z[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const float* p = red + (((ul << kslog) * RT + t) * quads + (tok >> 2)) * 64 + row * 4 + (tok & 3);
+      z[t] = p[0];
+      for (int s = 1; s < ks; ++s) z[t] += p[s * RT * quads * 64];
+    }
+    out(base + ul, tok, row, z);
+  }
+  __syncthreads();
 }
 
 // A fragments from memory: rows in processing order, planes `plane` elements apart
@@ -162,6 +239,39 @@ struct L4GlobalA {
   }
 };
 
+// A fragments from LDS: rows 16 bytes apart in the banks
+constexpr int kL4Pad = 8;
+struct L4LdsA {
+  static constexpr bool kPrefetch = false;
+  const uint16_t* row;
+  int plane;
+  __device__ __forceinline__ uint4 load(int c, int j, int p) const {
+    return *reinterpret_cast<const uint4*>(row + p * plane + c * kL4Chunk + 32 * j);
+  }
+};
+
+// Host: the split of `units` units over `wgs` workgroups.  ks waves share a
+// unit; the choice with the fullest rounds wins, the smaller ks on a tie (no
+// sums through LDS, fewer barriers).
+struct L4Split {
+  int kslog, rounds;
+};
+inline L4Split l4_split(int64_t units, int64_t wgs, int64_t kc) {
+  L4Split best{0, 1};
+  double eff = 0.0;
+  for (int lg = 0; lg <= 4; ++lg) {
+    if (lg > 0 && (int64_t(1) << lg) > kc) break;
+    const int64_t per = wgs * (kL4Waves >> lg), rounds = ceil_div(units, per);
+    const int64_t cps = (kc + (1 << lg) - 1) >> lg;
+    const double e = (double)units * (double)kc / ((double)(rounds * per * cps) * (1 << lg));
+    if (e > eff * 1.05) {
+      eff = e;
+      best = L4Split{lg, (int)rounds};
+    }
+  }
+  return best;
+}
+
 // one row of n bf16 into LDS (16-byte pieces when the row is 16-byte aligned)
 __device__ __forceinline__ void l4_row_to_lds(const uint16_t* __restrict__ x, int64_t n, int vec, uint8_t* lds, int tid,
                                               int threads) {
@@ -173,6 +283,30 @@ __device__ __forceinline__ void l4_row_to_lds(const uint16_t* __restrict__ x, in
     done = (int64_t)pieces * 8;
   }
   for (int64_t i = done + tid; i < n; i += threads) reinterpret_cast<uint16_t*>(lds)[i] = x[i];
+}
+
+// X' = X[:, order] of `tokens` rows into LDS (rows n128 + 8 apart), through a
+// raw copy of one row at a time: LDS serves scattered 2-byte reads in a few
+// cycles where the memory pipe takes one or more per lane.
+__device__ __forceinline__ void l4_gather_lds(const uint16_t* __restrict__ X, int64_t ldx, int64_t n, int vec,
+                                              const int32_t* __restrict__ order, int n128, int tokens, uint16_t* xsh,
+                                              uint8_t* raw) {
+  const int tid = threadIdx.x;
+  const uint16_t* x = reinterpret_cast<const uint16_t*>(raw);
+  for (int t = 0; t < tokens; ++t) {
+    if (t) __syncthreads();
+    l4_row_to_lds(X + t * ldx, n, vec, raw, tid, kL4Threads);
+    __syncthreads();
+    for (int p = 4 * tid; p < n128; p += 4 * kL4Threads) {
+      const int4 o = *reinterpret_cast<const int4*>(order + p);
+      const uint32_t a = x[std::max(o.x, 0)], b = x[std::max(o.y, 0)], c = x[std::max(o.z, 0)], d = x[std::max(o.w, 0)];
+      uint2 v;
+      v.x = (o.x >= 0 ? a : 0u) | (o.y >= 0 ? b : 0u) << 16;
+      v.y = (o.z >= 0 ? c : 0u) | (o.w >= 0 ? d : 0u) << 16;
+      *reinterpret_cast<uint2*>(xsh + t * (n128 + kL4Pad) + p) = v;
+    }
+  }
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------- values

@@ -119,64 +119,65 @@ struct L4Epilogue {
   }
 };
 
-struct L4StreamArgs {
-  const uint16_t* Xp;     // [tokens][n128] bf16, processing order
-  const float2* params;   // [tiles][Gp][16]
-  const u32x4_t* codes;   // [tiles][kc][64]
-  int64_t n128, kc, Gp, units, m, tokens;
-  int pmul, kslog;        // waves that split K: 1 << kslog
+struct L4DecodeArgs {
+  L4Stream st;
+  const uint16_t* X;      // in-kernel gather: the activations and the order
+  const int32_t* order;
+  int64_t ldx, n;
+  const uint16_t* Xp;     // else X' [tokens][n128]
+  int64_t n128, m;
+  int tokens, quads, vec;
   L4Epilogue ep;
 };
 
-// Unit = one row tile (linear) or one gate/up pair of tiles (glu).  A
-// workgroup of 8 waves holds 8 >> kslog units x 16 tokens, 1 << kslog waves
-// splitting the K range of each; their sums meet in LDS in wave order.
-template <int GS, bool GATED>
-__global__ __launch_bounds__(512) void l4_stream_kernel(L4StreamArgs a) {
+enum L4Source { kL4Gather = 0, kL4Copy = 1, kL4Global = 2 };
+
+// Up to 16 tokens.  Unit = one row tile (linear) or one gate/up pair of tiles
+// (glu).  X' sits in LDS, gathered here (kL4Gather) or copied from X' in
+// memory (kL4Copy), or is read from memory fragment by fragment (kL4Global)
+// where it does not fit.
+template <int GS, bool GATED, int SRC>
+__global__ __launch_bounds__(kL4Threads) void l4_decode_kernel(L4DecodeArgs a) {
   constexpr int RT = GATED ? 2 : 1;
-  __shared__ float red[8][RT][256];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int ks = 1 << a.kslog, upw = 8 >> a.kslog;
-  const int64_t u0 = (int64_t)blockIdx.x * upw;
-  const int64_t unit = std::min<int64_t>(u0 + (wave >> a.kslog), a.units - 1);
-  const int sl = wave & (ks - 1);
-  const int cps = (int)((a.kc + ks - 1) >> a.kslog);
-  const int c0 = sl * cps, c1 = (int)std::min<int64_t>(a.kc, c0 + cps);
-  const int64_t t0 = (int64_t)blockIdx.y * 16;
-  const int64_t t = std::min<int64_t>(t0 + (lane & 15), a.tokens - 1);   // rows past the last: computed, not stored
-  const L4GlobalA af{a.Xp + t * a.n128 + 8 * (lane >> 4), 0};
-  const u32x4_t* cp[RT];
-  const float2* pp[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    cp[r] = a.codes + (unit * RT + r) * a.kc * 64 + lane;
-    pp[r] = a.params + (unit * RT + r) * a.Gp * kL4Rows + (lane & 15);
-  }
-  const L4Consts kc;
-  f32x4_t y[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) y[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  l4_stream<GS, RT, 1, (GATED ? 2 : 4), false>(af, cp, pp, a.pmul, c0, c1, kc, y);
-#pragma unroll
-  for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4_t*>(&red[wave][r][lane * 4]) = y[r];
-  __syncthreads();
-  // D[4·(lane/16) + v][lane % 16]: token 4·quad + v of weight row lane % 16
-  for (int i = tid; i < upw * 256; i += 512) {
-    const int ul = i >> 8, tl = (i >> 4) & 15, row = i & 15;
-    const int at = ((tl >> 2) * 16 + row) * 4 + (tl & 3);
-    const int64_t r = (u0 + ul) * kL4Rows + row;
-    if (t0 + tl >= a.tokens || u0 + ul >= a.units || r >= a.m) continue;
-    float v[RT];
-#pragma unroll
-    for (int q = 0; q < RT; ++q) {
-      v[q] = red[ul << a.kslog][q][at];
-      for (int s = 1; s < ks; ++s) v[q] += red[(ul << a.kslog) + s][q][at];
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int lane = threadIdx.x & 63;
+  const int xrow = (int)a.n128 + kL4Pad;
+  uint16_t* xsh = reinterpret_cast<uint16_t*>(lds);
+  uint8_t* rest = lds + (SRC == kL4Global ? 0 : (size_t)a.tokens * xrow * 2);
+  float* red = reinterpret_cast<float*>(rest);   // after the gather, over its raw row
+  auto fill = [&] {
+    if (SRC == kL4Gather) {
+      l4_gather_lds(a.X, a.ldx, a.n, a.vec, a.order, (int)a.n128, a.tokens, xsh, rest);
+    } else if (SRC == kL4Copy) {
+      const int pieces = (int)(a.n128 / 8);
+      for (int i = threadIdx.x; i < a.tokens * pieces; i += kL4Threads)
+        *reinterpret_cast<uint4*>(xsh + (i / pieces) * xrow + 8 * (i % pieces)) =
+            *reinterpret_cast<const uint4*>(a.Xp + (int64_t)(i / pieces) * a.n128 + 8 * (i % pieces));
+      __syncthreads();
     }
-    if (GATED)
-      a.ep.gated(t0 + tl, r, v[0], v[RT - 1]);
-    else
-      a.ep.linear(t0 + tl, r, v[0]);
+  };
+  const int upw = kL4Waves >> a.st.kslog;
+  auto end = [&](int64_t unit, const f32x4_t (&y)[RT]) {
+    l4_finish<RT>(red, a.quads, a.tokens, a.st.kslog, unit, y, [&](int64_t u, int t, int row, const float (&z)[RT]) {
+      const int64_t r = u * kL4Rows + row;
+      if (u >= a.st.units || r >= a.m) return;
+      if (GATED)
+        a.ep.gated(t, r, z[0], z[RT - 1]);
+      else
+        a.ep.linear(t, r, z[0]);
+    });
+  };
+  const int t = std::min(lane & 15, a.tokens - 1);   // rows past the last: computed, not stored
+  const int64_t first = (int64_t)blockIdx.x * upw, step = (int64_t)gridDim.x * upw;
+  // batches that leave the wave within 128 registers (16 waves on a CU)
+  constexpr int BL = GATED ? (GS == 1 ? 1 : 2) : (GS == 4 ? 4 : GS == 2 ? 3 : 2);
+  constexpr int BG = GATED ? 1 : (GS == 4 ? 2 : 1);
+  if (SRC == kL4Global) {
+    const L4GlobalA af{a.Xp + t * a.n128 + 8 * (lane >> 4), 0};
+    l4_units<GS, RT, 1, BG, false>(a.st, first, step, af, fill, end);
+  } else {
+    const L4LdsA af{xsh + t * xrow + 8 * (lane >> 4), 0};
+    l4_units<GS, RT, 1, BL, false>(a.st, first, step, af, fill, end);
   }
 }
 
@@ -185,14 +186,14 @@ __global__ __launch_bounds__(512) void l4_stream_kernel(L4StreamArgs a) {
 // tile kernel's contiguous copies).  A row of X is read once, 16 bytes a
 // thread, into LDS and gathered from there: 2-byte loads at scattered columns
 // cost the memory pipe a cycle or more a lane (2048 x 4096: 13 us, through
-// LDS 4), LDS serves 64 of them in a few cycles.  Thread: 8 positions; GS·4
-// threads make one group's sum; a workgroup covers 4096 positions of `per`
-// tokens one after the other, keeping its part of the order in registers.
+// LDS 8.5), LDS serves 64 of them in a few cycles.  Thread: 8 positions; GS·4
+// threads make one group's sum; a workgroup covers 4096 positions of a token.
+// One token per workgroup: eight in a row, each behind a barrier, took 12 us.
 template <int GS, bool LDS>
 __global__ __launch_bounds__(512) void l4_gather_kernel(const uint16_t* __restrict__ X, int64_t ldx,
                                                         const int32_t* __restrict__ order, int64_t n, int64_t n128,
                                                         uint16_t* __restrict__ Xp, float* __restrict__ sums,
-                                                        int64_t tokens, int64_t tpad, int per, int vec) {
+                                                        int64_t tokens, int64_t tpad, int vec) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x;
   const int64_t p0 = (int64_t)blockIdx.y * 4096 + 8 * tid;
@@ -205,31 +206,28 @@ __global__ __launch_bounds__(512) void l4_gather_kernel(const uint16_t* __restri
     oi[0] = o0.x, oi[1] = o0.y, oi[2] = o0.z, oi[3] = o0.w;
     oi[4] = o1.x, oi[5] = o1.y, oi[6] = o1.z, oi[7] = o1.w;
   }
-  const int64_t ta = (int64_t)blockIdx.x * per, te = std::min<int64_t>(tokens, ta + per);
-  for (int64_t t = ta; t < te; ++t) {
-    const uint16_t* x = X + t * ldx;
-    if (LDS) {
-      if (t != ta) __syncthreads();   // the row before has been gathered
-      l4_row_to_lds(x, n, vec, lds, tid, 512);
-      __syncthreads();
-      x = reinterpret_cast<const uint16_t*>(lds);
-    }
-    if (!live) continue;
-    uint32_t v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {   // unconditional reads, all in flight together
-      const uint16_t xe = x[oi[e] >= 0 ? oi[e] : 0];
-      v[e] = oi[e] >= 0 ? xe : 0u;
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s += __uint_as_float(v[e] << 16);
-    *reinterpret_cast<u32x4_t*>(Xp + t * n128 + p0) =
-        u32x4_t{v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
-#pragma unroll
-    for (int d = 1; d < 4 * GS; d <<= 1) s += __shfl_xor(s, d);
-    if ((tid & (4 * GS - 1)) == 0) sums[(p0 / (32 * GS)) * tpad + t] = s;
+  const int64_t t = blockIdx.x;
+  const uint16_t* x = X + t * ldx;
+  if (LDS) {
+    l4_row_to_lds(x, n, vec, lds, tid, 512);
+    __syncthreads();
+    x = reinterpret_cast<const uint16_t*>(lds);
   }
+  if (!live) return;
+  uint32_t v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {   // unconditional reads, all in flight together
+    const uint16_t xe = x[oi[e] >= 0 ? oi[e] : 0];
+    v[e] = oi[e] >= 0 ? xe : 0u;
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s += __uint_as_float(v[e] << 16);
+  *reinterpret_cast<u32x4_t*>(Xp + t * n128 + p0) =
+      u32x4_t{v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
+#pragma unroll
+  for (int d = 1; d < 4 * GS; d <<= 1) s += __shfl_xor(s, d);
+  if ((tid & (4 * GS - 1)) == 0) sums[(p0 / (32 * GS)) * tpad + t] = s;
 }
 
 typedef __attribute__((address_space(3))) void lds_void_t;
@@ -554,7 +552,31 @@ L4Shape l4_shape(int64_t tokens, int64_t packed_rows, int64_t kc) {
   return s;
 }
 constexpr size_t kL4GatherLds = 65536;    // rows up to 32768 columns are gathered through LDS
-constexpr int64_t kL4StreamTokens = 16;   // up to here the stream kernel
+constexpr int64_t kL4DecodeTokens = 16;   // up to here the few-token kernel
+constexpr int64_t kL4GatherTokens = 4;    // up to here it gathers X' itself
+constexpr size_t kL4MaxLds = 158 * 1024;
+constexpr int64_t kL4Cus = 256;
+
+template <int GS, bool GATED>
+gptq_status launch_l4_source(const L4DecodeArgs& d, int src, unsigned grid, size_t lds, hipStream_t stream) {
+  const void* fn = src == kL4Gather ? (const void*)l4_decode_kernel<GS, GATED, kL4Gather>
+                   : src == kL4Copy ? (const void*)l4_decode_kernel<GS, GATED, kL4Copy>
+                                    : (const void*)l4_decode_kernel<GS, GATED, kL4Global>;
+  if (lds > 65536) GPTQ_HIP_CHECK(hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
+  L4DecodeArgs args = d;
+  void* argv[] = {&args};
+  GPTQ_HIP_CHECK(hipLaunchKernel(fn, dim3(grid), dim3(kL4Threads), argv, lds, stream));
+  return GPTQ_OK;
+}
+
+gptq_status launch_l4_decode(const L4DecodeArgs& d, int gs, bool gated, int src, unsigned grid, size_t lds,
+                             hipStream_t stream) {
+  switch (gs) {
+    case 1: return gated ? launch_l4_source<1, true>(d, src, grid, lds, stream) : launch_l4_source<1, false>(d, src, grid, lds, stream);
+    case 2: return gated ? launch_l4_source<2, true>(d, src, grid, lds, stream) : launch_l4_source<2, false>(d, src, grid, lds, stream);
+    default: return gated ? launch_l4_source<4, true>(d, src, grid, lds, stream) : launch_l4_source<4, false>(d, src, grid, lds, stream);
+  }
+}
 
 template <int GS, int MT, int TG, int RG, bool GATED>
 gptq_status launch_l4_tile(const L4GemmArgs& g, hipStream_t stream) {
@@ -598,7 +620,7 @@ L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n, int64_t packed_rows) {
   p.total = p.part_off;
   // the last, shorter block of a long call may take more slices than the others
   for (int64_t tk : {p.block, tokens % p.block}) {
-    if (tk <= kL4StreamTokens) continue;
+    if (tk <= kL4DecodeTokens) continue;
     const L4Shape s = l4_shape(tk, packed_rows, kc);
     if (s.splits > 1)
       p.total = std::max(p.total, p.part_off + align256((size_t)(s.splits * s.tblocks * s.rblocks) *
@@ -614,82 +636,102 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
   uint16_t* Xp = reinterpret_cast<uint16_t*>(w);
   float* xs = reinterpret_cast<float*>(w + p.xs_off);
   const int32_t* order = reinterpret_cast<const int32_t*>(base + L.order_off);
-  L4StreamArgs a;
-  a.Xp = Xp;
-  a.params = reinterpret_cast<const float2*>(base + L.param_off);
-  a.codes = reinterpret_cast<const u32x4_t*>(base + L.code_off);
-  a.n128 = L.n128;
-  a.kc = L.kc;
-  a.Gp = L.Gp;
-  a.units = gated ? L.mt / 2 : L.mt;
-  a.m = c.m;
+  L4Stream st;
+  st.params = reinterpret_cast<const float2*>(base + L.param_off);
+  st.codes = reinterpret_cast<const u32x4_t*>(base + L.code_off);
+  st.kc = L.kc;
+  st.Gp = L.Gp;
+  st.units = gated ? L.mt / 2 : L.mt;
   const bool one_group = L.g >= L.n128;
-  a.pmul = one_group ? 0 : kL4Rows;
+  st.pmul = one_group ? 0 : kL4Rows;
   const int gs = one_group ? 4 : (int)(L.g / 32);
-  a.kslog = L.kc >= 32 ? 3 : L.kc >= 16 ? 2 : L.kc >= 4 ? 1 : 0;
   const size_t ysz = c.y_dtype == GPTQ_FP32 ? 4 : 2, rsz = c.res_dtype == GPTQ_FP32 ? 4 : 2;
+  const int vec = (reinterpret_cast<uintptr_t>(c.X) & 15) == 0 && c.ldx % 8 == 0;
   for (int64_t t0 = 0; t0 < c.tokens; t0 += p.block) {
     const int64_t tk = std::min<int64_t>(p.block, c.tokens - t0);
-    // a row of X in LDS, rounded up to whole 16-byte pieces of 512 threads
-    const size_t glds = (size_t)L.n * 2 <= kL4GatherLds ? (size_t)round_up(L.n * 2, 16) : 0;
-    const int vec = (reinterpret_cast<uintptr_t>(c.X) & 15) == 0 && c.ldx % 8 == 0;
-    const int per = 1;
-    const dim3 ggrid((unsigned)ceil_div(tk, per), (unsigned)ceil_div(L.n128, 4096));
-#define L4_GATHER(GS)                                                                                          \
-  if (glds)                                                                                                    \
-    hipLaunchKernelGGL((l4_gather_kernel<GS, true>), ggrid, dim3(512), glds, stream, c.X + t0 * c.ldx, c.ldx, order, \
-                       L.n, L.n128, Xp, xs, tk, p.tpad, per, vec);                                             \
-  else                                                                                                         \
-    hipLaunchKernelGGL((l4_gather_kernel<GS, false>), ggrid, dim3(512), 0, stream, c.X + t0 * c.ldx, c.ldx, order, \
-                       L.n, L.n128, Xp, xs, tk, p.tpad, per, vec)
-    switch (gs) {
-      case 1: L4_GATHER(1); break;
-      case 2: L4_GATHER(2); break;
-      default: L4_GATHER(4); break;
+    const uint16_t* X = c.X + t0 * c.ldx;
+    const L4Epilogue ep{c.act, c.bias_dtype, c.res_dtype, c.y_dtype, c.bias, c.bias2,
+                        c.res ? static_cast<const char*>(c.res) + (size_t)(t0 * c.ldr) * rsz : nullptr,
+                        static_cast<char*>(c.Y) + (size_t)(t0 * c.ldy) * ysz, c.ldr, c.ldy};
+    const bool decode = tk <= kL4DecodeTokens;
+    int src = kL4Copy;
+    L4DecodeArgs d;
+    size_t dlds = 0;
+    if (decode) {
+      d.quads = (int)ceil_div(tk, 4);
+      const size_t rows = (size_t)tk * (size_t)(L.n128 + kL4Pad) * 2;
+      const size_t red = (size_t)kL4Waves * (gated ? 2 : 1) * d.quads * 64 * sizeof(float);
+      const size_t raw = (size_t)round_up(L.n * 2, 16);
+      if (tk <= kL4GatherTokens && rows + std::max(red, raw) <= kL4MaxLds) {
+        src = kL4Gather;
+        dlds = rows + std::max(red, raw);
+      } else if (rows + red <= kL4MaxLds) {
+        dlds = rows + red;
+      } else {
+        src = kL4Global;
+        dlds = red;
+      }
     }
+    if (src != kL4Gather) {
+      const size_t glds = (size_t)L.n * 2 <= kL4GatherLds ? (size_t)round_up(L.n * 2, 16) : 0;
+      const dim3 ggrid((unsigned)tk, (unsigned)ceil_div(L.n128, 4096));
+#define L4_GATHER(GS)                                                                                             \
+  if (glds)                                                                                                       \
+    hipLaunchKernelGGL((l4_gather_kernel<GS, true>), ggrid, dim3(512), glds, stream, X, c.ldx, order, L.n, L.n128, \
+                       Xp, xs, tk, p.tpad, vec);                                                                  \
+  else                                                                                                            \
+    hipLaunchKernelGGL((l4_gather_kernel<GS, false>), ggrid, dim3(512), 0, stream, X, c.ldx, order, L.n, L.n128,  \
+                       Xp, xs, tk, p.tpad, vec)
+      switch (gs) {
+        case 1: L4_GATHER(1); break;
+        case 2: L4_GATHER(2); break;
+        default: L4_GATHER(4); break;
+      }
 #undef L4_GATHER
-    GPTQ_LAUNCH_CHECK();
-    a.tokens = tk;
-    a.ep = L4Epilogue{c.act, c.bias_dtype, c.res_dtype, c.y_dtype, c.bias, c.bias2,
-                      c.res ? static_cast<const char*>(c.res) + (size_t)(t0 * c.ldr) * rsz : nullptr,
-                      static_cast<char*>(c.Y) + (size_t)(t0 * c.ldy) * ysz, c.ldr, c.ldy};
-    if (tk > kL4StreamTokens) {
-      L4GemmArgs g;
-      const L4Shape sh = l4_shape(tk, L.mt * kL4Rows, L.kc);
-      g.Xp = Xp;
-      g.sums = xs;
-      g.params = a.params;
-      g.codes = a.codes;
-      g.part = reinterpret_cast<float*>(w + p.part_off);
-      g.n128 = L.n128;
-      g.kc = L.kc;
-      g.Gp = L.Gp;
-      g.mt = L.mt;
-      g.m = c.m;
-      g.tokens = tk;
-      g.tpad = p.tpad;
-      g.tblocks = sh.tblocks;
-      g.rblocks = sh.rblocks;
-      g.pmul = a.pmul;
-      g.splits = sh.splits;
-      g.chunks = sh.chunks;
-      g.ep = a.ep;
-      GPTQ_TRY(launch_l4_gemm(g, sh, gs, gated, stream));
+      GPTQ_LAUNCH_CHECK();
+    }
+    if (decode) {
+      d.X = X;
+      d.order = order;
+      d.ldx = c.ldx;
+      d.n = L.n;
+      d.Xp = Xp;
+      d.n128 = L.n128;
+      d.m = c.m;
+      d.tokens = (int)tk;
+      d.vec = vec;
+      d.ep = ep;
+      const int64_t wgs = std::min<int64_t>(st.units, kL4Cus);
+      const L4Split sp = l4_split(st.units, wgs, L.kc);
+      st.kslog = sp.kslog;
+      st.rounds = sp.rounds;
+      d.st = st;
+      // workgroups that the split leaves without units are not launched
+      const unsigned grid = (unsigned)std::min<int64_t>(wgs, ceil_div(st.units, kL4Waves >> sp.kslog));
+      GPTQ_TRY(launch_l4_decode(d, gs, gated, src, grid, dlds, stream));
       continue;
     }
-    const dim3 grid((unsigned)ceil_div(a.units, 8 >> a.kslog), (unsigned)ceil_div(tk, 16));
-#define L4_STREAM(GS)                                                                            \
-  if (gated)                                                                                     \
-    hipLaunchKernelGGL((l4_stream_kernel<GS, true>), grid, dim3(512), 0, stream, a);             \
-  else                                                                                           \
-    hipLaunchKernelGGL((l4_stream_kernel<GS, false>), grid, dim3(512), 0, stream, a)
-    switch (gs) {
-      case 1: L4_STREAM(1); break;
-      case 2: L4_STREAM(2); break;
-      default: L4_STREAM(4); break;
-    }
-#undef L4_STREAM
-    GPTQ_LAUNCH_CHECK();
+    const L4Shape sh = l4_shape(tk, L.mt * kL4Rows, L.kc);
+    L4GemmArgs g;
+    g.Xp = Xp;
+    g.sums = xs;
+    g.params = st.params;
+    g.codes = st.codes;
+    g.part = reinterpret_cast<float*>(w + p.part_off);
+    g.n128 = L.n128;
+    g.kc = L.kc;
+    g.Gp = L.Gp;
+    g.mt = L.mt;
+    g.m = c.m;
+    g.tokens = tk;
+    g.tpad = p.tpad;
+    g.tblocks = sh.tblocks;
+    g.rblocks = sh.rblocks;
+    g.pmul = st.pmul;
+    g.splits = sh.splits;
+    g.chunks = sh.chunks;
+    g.ep = ep;
+    GPTQ_TRY(launch_l4_gemm(g, sh, gs, gated, stream));
   }
   return GPTQ_OK;
 }

@@ -10,8 +10,9 @@
 // the gate/up kernel writes is the down kernel's operand as it lies, with no
 // gather between them.
 //
-// Launches for up to 64 tokens: router (a workgroup per token), gate/up (a
-// workgroup per active expert and row tiles), down (the same), combine.
+// Launches for up to 64 tokens: router (a workgroup per token; it also gathers
+// the token into each chosen expert's column order), gate/up and down (some
+// workgroups per active expert, each a share of its row tiles), combine.
 #include <algorithm>
 
 #include "w4a16_device.hpp"
@@ -30,11 +31,14 @@ struct MoeRouterArgs {
   const uint16_t* X;
   int64_t ldx, hidden;
   const void* R;          // [experts][hidden]
-  int r_dt, experts, top_k, renorm, vec;
+  int r_dt, experts, top_k, renorm, vec, xvec, parts;
   int32_t* ids;           // [tokens][top_k]
   float* wts;
   int32_t* ids_out;       // the caller's copies, may be null
   float* wts_out;
+  const char* packed;     // expert e's column order at e·stride + order_off
+  int64_t stride, order_off, n128;
+  uint16_t* Xp;           // [pairs][n128]
 };
 
 // a before b: larger, NaN above every number, ties to the lower index
@@ -45,40 +49,9 @@ __device__ __forceinline__ bool moe_before(double a, int ia, double b, int ib) {
   return ia < ib;
 }
 
-// One workgroup per token.  The logits are summed in 64 bits: which experts
-// are chosen hangs on the last bits of the k-th and the next, and a choice
-// that falls the other way is no rounding error in the result.
-__global__ __launch_bounds__(1024) void moe_router_kernel(MoeRouterArgs a) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const int64_t t = blockIdx.x, h = a.hidden;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
-  double* logit = reinterpret_cast<double*>(lds);
-  float* x = reinterpret_cast<float*>(lds + (size_t)a.experts * sizeof(double) + (a.experts & 1) * sizeof(double));
-  for (int64_t i = tid; i < h; i += blockDim.x) x[i] = __uint_as_float((uint32_t)a.X[t * a.ldx + i] << 16);
-  __syncthreads();
-  for (int e = wave; e < a.experts; e += waves) {
-    double s0 = 0.0, s1 = 0.0;
-    if (a.vec && a.r_dt == GPTQ_BF16) {
-      const uint16_t* r = static_cast<const uint16_t*>(a.R) + (int64_t)e * h;
-      for (int64_t i = 8 * lane; i < h; i += 512) {
-        const uint4 w = *reinterpret_cast<const uint4*>(r + i);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          s0 += (double)(x[i + 2 * q] * __uint_as_float(ww[q] << 16));   // bf16·bf16: exact in fp32
-          s1 += (double)(x[i + 2 * q + 1] * __uint_as_float(ww[q] & 0xffff0000u));
-        }
-      }
-    } else {
-      for (int64_t i = lane; i < h; i += 64) s0 = fma((double)x[i], (double)l4_load(a.R, a.r_dt, (int64_t)e * h + i), s0);
-    }
-    s0 += s1;
-#pragma unroll
-    for (int d = 32; d; d >>= 1) s0 += __shfl_xor(s0, d);
-    if (lane == 0) logit[e] = s0;
-  }
-  __syncthreads();
-  if (wave != 0) return;
+// The top_k experts of one token, largest first, and their weights (one wave).
+__device__ __forceinline__ void moe_choose(const MoeRouterArgs& a, const double* logit, int64_t t, int* chosen_ids) {
+  const int lane = threadIdx.x & 63;
   // lane l holds experts l, l + 64, ...; taken = those already chosen
   uint32_t taken = 0;
   double top = 0.0, chosen = 0.0, mine = 0.0;
@@ -117,10 +90,79 @@ __global__ __launch_bounds__(1024) void moe_router_kernel(MoeRouterArgs a) {
   }
   if (lane < a.top_k) {
     const float w = (float)(mine / chosen);
+    chosen_ids[lane] = my_id;
     a.ids[t * a.top_k + lane] = my_id;
     a.wts[t * a.top_k + lane] = w;
     if (a.ids_out) a.ids_out[t * a.top_k + lane] = my_id;
     if (a.wts_out) a.wts_out[t * a.top_k + lane] = w;
+  }
+}
+
+// One workgroup per token.  The logits are summed in 64 bits: which experts
+// are chosen hangs on the last bits of the k-th and the next, and a choice
+// that falls the other way is no rounding error in the result.  `parts` waves
+// share an expert's row when there are fewer experts than waves; four
+// 512-element pieces are in flight per wave.
+__global__ __launch_bounds__(1024) void moe_router_kernel(MoeRouterArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ int chosen_ids[kMoeMaxTopK];
+  const int64_t t = blockIdx.x;
+  const int h = (int)a.hidden;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  double* logit = reinterpret_cast<double*>(lds);                      // [parts][experts]
+  uint16_t* x = reinterpret_cast<uint16_t*>(lds + (((size_t)a.parts * a.experts + 1) & ~(size_t)1) * sizeof(double));
+  l4_row_to_lds(a.X + t * a.ldx, h, a.xvec, reinterpret_cast<uint8_t*>(x), tid, 1024);
+  __syncthreads();
+  const int part = wave % a.parts, wpe = 16 / a.parts;
+  for (int e = wave / a.parts; e < a.experts; e += wpe) {
+    double s[2] = {0.0, 0.0};
+    if (a.vec && a.r_dt == GPTQ_BF16) {
+      const uint16_t* r = static_cast<const uint16_t*>(a.R) + (int64_t)e * h;
+      for (int i = 8 * lane + 512 * part; i < h; i += 2048 * a.parts) {
+        u32x4_t w[4], xv[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int k = i + 512 * a.parts * u;
+          const bool in = k < h;   // past the end: the row's start again, times zero
+          w[u] = *reinterpret_cast<const u32x4_t*>(r + (in ? k : 8 * lane % h));
+          xv[u] = in ? *reinterpret_cast<const u32x4_t*>(x + k) : u32x4_t{0u, 0u, 0u, 0u};
+          if (!in) w[u] = u32x4_t{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {   // bf16·bf16: exact in fp32
+            s[0] += (double)(__uint_as_float(xv[u][q] << 16) * __uint_as_float(w[u][q] << 16));
+            s[1] += (double)(__uint_as_float(xv[u][q] & 0xffff0000u) * __uint_as_float(w[u][q] & 0xffff0000u));
+          }
+      }
+    } else {
+      for (int i = lane + 64 * part; i < h; i += 64 * a.parts)
+        s[0] = fma((double)__uint_as_float((uint32_t)x[i] << 16), (double)l4_load(a.R, a.r_dt, (int64_t)e * h + i), s[0]);
+    }
+    s[0] += s[1];
+#pragma unroll
+    for (int d = 32; d; d >>= 1) s[0] += __shfl_xor(s[0], d);
+    if (lane == 0) logit[part * a.experts + e] = s[0];
+  }
+  if (a.parts > 1) {
+    __syncthreads();
+    if (tid < a.experts)
+      for (int p = 1; p < a.parts; ++p) logit[tid] += logit[p * a.experts + tid];
+  }
+  __syncthreads();
+  if (wave == 0) moe_choose(a, logit, t, chosen_ids);
+  __syncthreads();
+  // the token in the column order of each of its experts
+  const int quarter = (int)(a.n128 / 4);
+  for (int i = tid; i < a.top_k * quarter; i += 1024) {
+    const int j = i / quarter, p = 4 * (i % quarter);
+    const int4 o = *reinterpret_cast<const int4*>(a.packed + chosen_ids[j] * a.stride + a.order_off + (int64_t)p * 4);
+    const uint32_t v0 = x[std::max(o.x, 0)], v1 = x[std::max(o.y, 0)], v2 = x[std::max(o.z, 0)], v3 = x[std::max(o.w, 0)];
+    uint2 v;
+    v.x = (o.x >= 0 ? v0 : 0u) | (o.y >= 0 ? v1 : 0u) << 16;
+    v.y = (o.z >= 0 ? v2 : 0u) | (o.w >= 0 ? v3 : 0u) << 16;
+    *reinterpret_cast<uint2*>(a.Xp + (t * a.top_k + j) * a.n128 + p) = v;
   }
 }
 
@@ -164,145 +206,97 @@ __device__ __forceinline__ int moe_expert(const int32_t* __restrict__ ids, int t
   return e;
 }
 
-struct L4LdsA {
-  static constexpr bool kPrefetch = false;
-  const uint16_t* row;   // this lane's token row + 8·(lane/16)
-  __device__ __forceinline__ uint4 load(int c, int j, int) const {
-    return *reinterpret_cast<const uint4*>(row + c * kL4Chunk + 32 * j);
-  }
-};
-
-struct MoeGateUpArgs {
-  const uint16_t* X;
-  int64_t ldx;
-  const char* packed;         // expert e's blob at e·stride
-  int64_t stride;
-  int64_t order_off, param_off, code_off;
-  int64_t n128, kc, Gp, units, f128;
+struct MoeExpertArgs {
+  const char* packed;         // expert e's weight at e·stride
+  int64_t stride, param_off, code_off;
+  L4Stream st;
+  const uint16_t* A;          // [pairs][planes][k128], processing order
+  int64_t k128;               // positions of the product's input
   const int32_t* ids;
-  uint16_t* mid;              // [pairs][planes][f128]: bf16 parts, largest first
-  int tokens, top_k, experts, pmul, kslog, act, pass, planes;
+  int tokens, top_k, experts, pass, quads, act, planes;
+  int64_t rows;               // gate/up: f128 (positions); down: hidden
+  uint16_t* mid;              // gate/up's result [pairs][planes][rows]: bf16 parts, largest first
+  float* out;                 // down's result [pairs][rows]
 };
 
-// act(gate)·up of one expert's tokens for 8 >> kslog tile pairs.  X' =
-// X[:, order] of up to `pass` tokens sits in LDS in processing order.
-template <int GS>
-__global__ __launch_bounds__(512) void moe_gate_up_kernel(MoeGateUpArgs a) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ MoeList list;
-  __shared__ float red[8][2][256];
-  uint16_t* xsh = reinterpret_cast<uint16_t*>(lds);
-  const int xrow = (int)a.n128 + 8;   // rows 16 bytes apart in the banks
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+// A workgroup's share of one expert's units, NP planes of A per token.  LDS:
+// the rows of a pass are copied into LDS, else every fragment is read from
+// memory.  GATE_UP: RT = 2, act(gate)·up to `mid`; else to `out`.
+template <int GS, bool GATE_UP, int NP, bool LDS>
+__device__ __forceinline__ void moe_expert_units(const MoeExpertArgs& a, MoeList& list, uint8_t* lds) {
+  constexpr int RT = GATE_UP ? 2 : 1;
+  // batches that leave the wave within 128 registers
+  constexpr int B = LDS ? (GATE_UP ? (GS == 1 ? 1 : 2) : (GS == 4 ? 4 : 2)) : 1;
   const int e = __builtin_amdgcn_readfirstlane(moe_expert(a.ids, a.tokens, a.top_k, a.experts, blockIdx.y, list));
   if (e < 0) return;
   const char* blob = a.packed + e * a.stride;
-  const int32_t* order = reinterpret_cast<const int32_t*>(blob + a.order_off);
-  const int ks = 1 << a.kslog, upw = 8 >> a.kslog;
-  const int64_t u0 = (int64_t)blockIdx.x * upw;
-  const int64_t unit = std::min<int64_t>(u0 + (wave >> a.kslog), a.units - 1);
-  const int sl = wave & (ks - 1);
-  const int cps = (int)((a.kc + ks - 1) >> a.kslog);
-  const int c0 = sl * cps, c1 = (int)std::min<int64_t>(a.kc, c0 + cps);
-  const u32x4_t* cp[2];
-  const float2* pp[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    cp[r] = reinterpret_cast<const u32x4_t*>(blob + a.code_off) + (unit * 2 + r) * a.kc * 64 + lane;
-    pp[r] = reinterpret_cast<const float2*>(blob + a.param_off) + (unit * 2 + r) * a.Gp * kL4Rows + (lane & 15);
-  }
-  const L4Consts kc;
+  L4Stream st = a.st;
+  st.codes = reinterpret_cast<const u32x4_t*>(blob + a.code_off);
+  st.params = reinterpret_cast<const float2*>(blob + a.param_off);
+  const int lane = threadIdx.x & 63, tid = threadIdx.x;
+  const int upw = kL4Waves >> st.kslog;
+  const int64_t first = (int64_t)blockIdx.x * upw, step = (int64_t)gridDim.x * upw;
+  const int xrow = (int)a.k128 + kL4Pad;
+  uint16_t* xsh = reinterpret_cast<uint16_t*>(lds);
+  float* red = reinterpret_cast<float*>(lds + (LDS ? (size_t)a.pass * NP * xrow * 2 : 0));
   for (int p0 = 0; p0 < list.count; p0 += a.pass) {
     const int np = std::min(a.pass, list.count - p0);
-    for (int i = tid; i < np * (int)(a.n128 / 4); i += 512) {
-      const int q = i / (int)(a.n128 / 4), p = 4 * (i % (int)(a.n128 / 4));
-      const uint16_t* x = a.X + (int64_t)(list.pair[p0 + q] / a.top_k) * a.ldx;
-      const int4 o = *reinterpret_cast<const int4*>(order + p);
-      uint2 v;
-      v.x = (o.x >= 0 ? (uint32_t)x[o.x] : 0u) | ((o.y >= 0 ? (uint32_t)x[o.y] : 0u) << 16);
-      v.y = (o.z >= 0 ? (uint32_t)x[o.z] : 0u) | ((o.w >= 0 ? (uint32_t)x[o.w] : 0u) << 16);
-      *reinterpret_cast<uint2*>(xsh + q * xrow + p) = v;
-    }
-    __syncthreads();
-    const L4LdsA af{xsh + std::min(lane & 15, np - 1) * xrow + 8 * (lane >> 4)};
-    f32x4_t y[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    l4_stream<GS, 2, 1, 2, false>(af, cp, pp, a.pmul, c0, c1, kc, y);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) *reinterpret_cast<f32x4_t*>(&red[wave][r][lane * 4]) = y[r];
-    __syncthreads();
-    for (int i = tid; i < upw * 256; i += 512) {
-      const int ul = i >> 8, q = (i >> 4) & 15, row = i & 15;
-      const int at = ((q >> 2) * 16 + row) * 4 + (q & 3);
-      if (q >= np || u0 + ul >= a.units) continue;
-      float g = red[ul << a.kslog][0][at], u = red[ul << a.kslog][1][at];
-      for (int s = 1; s < ks; ++s) {
-        g += red[(ul << a.kslog) + s][0][at];
-        u += red[(ul << a.kslog) + s][1][at];
+    auto fill = [&] {
+      if (!LDS) return;
+      if (p0) __syncthreads();   // the pass before has been read
+      const int pieces = (int)(a.k128 / 8);
+      for (int i = tid; i < np * NP * pieces; i += kL4Threads) {
+        const int q = i / pieces, k = 8 * (i % pieces);   // row q = token q / NP, plane q % NP
+        *reinterpret_cast<uint4*>(xsh + q * xrow + k) =
+            *reinterpret_cast<const uint4*>(a.A + ((int64_t)list.pair[p0 + q / NP] * NP + q % NP) * a.k128 + k);
       }
-      // The hidden activation leaves as 2 or 3 bf16 parts (16 or 24 significant
-      // bits, for a bf16 or an fp32 result), so it adds no rounding of its own;
-      // a single bf16 would add as much error as the result's rounding.
-      float v = l4_activate(g, a.act) * u;
-      uint16_t* o = a.mid + (int64_t)list.pair[p0 + q] * a.planes * a.f128 + (u0 + ul) * kL4Rows + row;
-      for (int p = 0; p < a.planes; ++p) {
-        const uint16_t part = l4_bf16(v);
-        const float f = __uint_as_float((uint32_t)part << 16);
-        o[p * a.f128] = part;
-        v = isfinite(f) ? v - f : 0.f;
-      }
+      __syncthreads();
+    };
+    auto end = [&](int64_t unit, const f32x4_t (&y)[RT]) {
+      l4_finish<RT>(red, a.quads, np, st.kslog, unit, y, [&](int64_t u, int q, int row, const float (&z)[RT]) {
+        const int64_t r = u * kL4Rows + row, pair = list.pair[p0 + q];
+        if (u >= st.units || r >= a.rows) return;
+        if (GATE_UP) {
+          // The hidden activation leaves as 2 or 3 bf16 parts (16 or 24
+          // significant bits, for a bf16 or an fp32 result), so it adds no
+          // rounding of its own; a single bf16 would add as much error as the
+          // result's rounding.
+          float v = l4_activate(z[0], a.act) * z[RT - 1];
+          uint16_t* o = a.mid + pair * a.planes * a.rows + r;
+          for (int p = 0; p < a.planes; ++p) {
+            const uint16_t part = l4_bf16(v);
+            const float f = __uint_as_float((uint32_t)part << 16);
+            o[p * a.rows] = part;
+            v = isfinite(f) ? v - f : 0.f;
+          }
+        } else {
+          a.out[pair * a.rows + r] = z[0];
+        }
+      });
+    };
+    const int q = std::min(lane & 15, np - 1);   // rows past the last: computed, not stored
+    if (LDS) {
+      const L4LdsA af{xsh + q * NP * xrow + 8 * (lane >> 4), xrow};
+      l4_units<GS, RT, NP, B, NP == 3>(st, first, step, af, fill, end);
+    } else {
+      const L4GlobalA af{a.A + (int64_t)list.pair[p0 + q] * NP * a.k128 + 8 * (lane >> 4), a.k128};
+      l4_units<GS, RT, NP, B, NP == 3>(st, first, step, af, fill, end);
     }
-    __syncthreads();
   }
 }
 
-struct MoeDownArgs {
-  const uint16_t* mid;
-  const char* packed;
-  int64_t stride, param_off, code_off;
-  int64_t f128, kc, Gp, units, hidden;
-  const int32_t* ids;
-  float* out;                 // [pairs][hidden]
-  int tokens, top_k, experts, pmul, kslog;
-};
-
-template <int GS, int NP>
-__global__ __launch_bounds__(512) void moe_down_kernel(MoeDownArgs a) {
+template <int GS, bool LDS>
+__global__ __launch_bounds__(kL4Threads) void moe_gate_up_kernel(MoeExpertArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ MoeList list;
-  __shared__ float red[8][256];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int e = __builtin_amdgcn_readfirstlane(moe_expert(a.ids, a.tokens, a.top_k, a.experts, blockIdx.y, list));
-  if (e < 0) return;
-  const char* blob = a.packed + e * a.stride;
-  const int ks = 1 << a.kslog, upw = 8 >> a.kslog;
-  const int64_t u0 = (int64_t)blockIdx.x * upw;
-  const int64_t unit = std::min<int64_t>(u0 + (wave >> a.kslog), a.units - 1);
-  const int sl = wave & (ks - 1);
-  const int cps = (int)((a.kc + ks - 1) >> a.kslog);
-  const int c0 = sl * cps, c1 = (int)std::min<int64_t>(a.kc, c0 + cps);
-  const u32x4_t* cp[1] = {reinterpret_cast<const u32x4_t*>(blob + a.code_off) + unit * a.kc * 64 + lane};
-  const float2* pp[1] = {reinterpret_cast<const float2*>(blob + a.param_off) + unit * a.Gp * kL4Rows + (lane & 15)};
-  const L4Consts kc;
-  for (int p0 = 0; p0 < list.count; p0 += kMoePass) {
-    const int np = std::min(kMoePass, list.count - p0);
-    const L4GlobalA af{a.mid + (int64_t)list.pair[p0 + std::min(lane & 15, np - 1)] * NP * a.f128 + 8 * (lane >> 4),
-                       a.f128};
-    f32x4_t y[1] = {{0.f, 0.f, 0.f, 0.f}};
-    l4_stream<GS, 1, NP, 2, NP == 3>(af, cp, pp, a.pmul, c0, c1, kc, y);
-    *reinterpret_cast<f32x4_t*>(&red[wave][lane * 4]) = y[0];
-    __syncthreads();
-    for (int i = tid; i < upw * 256; i += 512) {
-      const int ul = i >> 8, q = (i >> 4) & 15, row = i & 15;
-      const int at = ((q >> 2) * 16 + row) * 4 + (q & 3);
-      const int64_t r = (u0 + ul) * kL4Rows + row;
-      if (q >= np || u0 + ul >= a.units || r >= a.hidden) continue;
-      float v = red[ul << a.kslog][at];
-      for (int s = 1; s < ks; ++s) v += red[(ul << a.kslog) + s][at];
-      a.out[(int64_t)list.pair[p0 + q] * a.hidden + r] = v;
-    }
-    __syncthreads();
-  }
+  moe_expert_units<GS, true, 1, LDS>(a, list, lds);
+}
+
+template <int GS, int NP, bool LDS>
+__global__ __launch_bounds__(kL4Threads) void moe_down_kernel(MoeExpertArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ MoeList list;
+  moe_expert_units<GS, false, NP, LDS>(a, list, lds);
 }
 
 __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restrict__ pairs, const float* __restrict__ wts,
@@ -316,7 +310,45 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
   l4_store(Y, y_dt, t * ldy + r, v);
 }
 
-int ks_log(int64_t kc) { return kc >= 32 ? 3 : kc >= 16 ? 2 : kc >= 4 ? 1 : 0; }
+constexpr size_t kMoeMaxLds = 120 * 1024;   // beyond: fragments from memory
+
+// fills the launch-dependent fields; returns the dynamic LDS bytes, 0 < lds
+// with *in_lds when the rows of a pass fit
+size_t moe_plan(MoeExpertArgs& a, int tokens, int planes, int rt, int64_t wgs, bool* in_lds) {
+  a.pass = std::min(kMoePass, tokens);
+  a.quads = (int)ceil_div(a.pass, 4);
+  const L4Split sp = l4_split(a.st.units, wgs, a.st.kc);
+  a.st.kslog = sp.kslog;
+  a.st.rounds = sp.rounds;
+  const size_t red = sp.kslog ? (size_t)kL4Waves * rt * a.quads * 64 * sizeof(float) : 0;
+  const size_t rows = (size_t)a.pass * planes * (size_t)(a.k128 + kL4Pad) * 2;
+  *in_lds = rows + red <= kMoeMaxLds;
+  return *in_lds ? rows + red : red;
+}
+
+template <class K>
+gptq_status moe_launch(K kernel, dim3 grid, size_t lds, const MoeExpertArgs& a, hipStream_t stream) {
+  if (lds > 65536)
+    GPTQ_HIP_CHECK(hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
+  hipLaunchKernelGGL(kernel, grid, dim3(kL4Threads), lds, stream, a);
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+template <int GS>
+gptq_status launch_gate_up(dim3 grid, size_t lds, bool in_lds, const MoeExpertArgs& a, hipStream_t stream) {
+  return in_lds ? moe_launch(moe_gate_up_kernel<GS, true>, grid, lds, a, stream)
+                : moe_launch(moe_gate_up_kernel<GS, false>, grid, lds, a, stream);
+}
+
+template <int GS>
+gptq_status launch_down(dim3 grid, size_t lds, bool in_lds, const MoeExpertArgs& a, hipStream_t stream) {
+  if (a.planes == 3)
+    return in_lds ? moe_launch(moe_down_kernel<GS, 3, true>, grid, lds, a, stream)
+                  : moe_launch(moe_down_kernel<GS, 3, false>, grid, lds, a, stream);
+  return in_lds ? moe_launch(moe_down_kernel<GS, 2, true>, grid, lds, a, stream)
+                : moe_launch(moe_down_kernel<GS, 2, false>, grid, lds, a, stream);
+}
 
 }  // namespace
 
@@ -336,7 +368,9 @@ MoeWork plan_moe_work(const gptq_moe_config& c, int64_t tokens) {
   const size_t pairs = (size_t)(w.block * c.top_k);
   const size_t f128 = (size_t)(ceil_div(c.inter, kL4Chunk) * kL4Chunk);
   w.wts_off = align256(pairs * sizeof(int32_t));
-  w.mid_off = w.wts_off + align256(pairs * sizeof(float));
+  const size_t h128 = (size_t)(ceil_div(c.hidden, kL4Chunk) * kL4Chunk);
+  w.xp_off = w.wts_off + align256(pairs * sizeof(float));
+  w.mid_off = w.xp_off + align256(pairs * h128 * sizeof(uint16_t));
   w.out_off = w.mid_off + align256(pairs * kMoeMaxPlanes * f128 * sizeof(uint16_t));
   w.total = w.out_off + align256(pairs * (size_t)c.hidden * sizeof(float));
   return w;
@@ -368,46 +402,31 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
   const char* packed = static_cast<const char*>(c.packed);
   const int h = (int)cfg.hidden;
 
-  MoeGateUpArgs g;
-  g.ldx = c.ldx;
-  g.packed = packed;
-  g.stride = (int64_t)L.stride;
-  g.order_off = (int64_t)L.gu.order_off;
-  g.param_off = (int64_t)L.gu.param_off;
-  g.code_off = (int64_t)L.gu.code_off;
-  g.n128 = L.gu.n128;
-  g.kc = L.gu.kc;
-  g.Gp = L.gu.Gp;
-  g.units = L.gu.mt / 2;
-  g.f128 = L.f128;
-  g.ids = ids;
-  g.mid = mid;
-  g.top_k = cfg.top_k;
-  g.experts = cfg.experts;
-  g.pmul = L.gu.g >= L.gu.n128 ? 0 : kL4Rows;
-  g.kslog = ks_log(L.gu.kc);
-  g.act = cfg.activation;
-  g.planes = c.y_dtype == GPTQ_FP32 ? 3 : 2;
-  MoeDownArgs d;
-  d.mid = mid;
-  d.packed = packed + L.down_off;
-  d.stride = (int64_t)L.stride;
-  d.param_off = (int64_t)L.down.param_off;
-  d.code_off = (int64_t)L.down.code_off;
-  d.f128 = L.f128;
-  d.kc = L.down.kc;
-  d.Gp = L.down.Gp;
-  d.units = L.down.mt;
-  d.hidden = cfg.hidden;
-  d.ids = ids;
-  d.out = out;
-  d.top_k = cfg.top_k;
-  d.experts = cfg.experts;
-  d.pmul = L.down.g >= L.down.n128 ? 0 : kL4Rows;
-  d.kslog = ks_log(L.down.kc);
-  const size_t row = (size_t)(g.n128 + 8) * sizeof(uint16_t);
+  uint16_t* Xp = reinterpret_cast<uint16_t*>(wb + w.xp_off);
   // one group per row folds as groups of 128 (pmul = 0 repeats its parameters)
+  auto weight = [&](MoeExpertArgs& a, const W4Layout& l, const char* base, int64_t units) {
+    a.packed = base;
+    a.stride = (int64_t)L.stride;
+    a.param_off = (int64_t)l.param_off;
+    a.code_off = (int64_t)l.code_off;
+    a.st = L4Stream{nullptr, nullptr, l.kc, l.Gp, units, l.g >= l.n128 ? 0 : kL4Rows, 0, 1};
+    a.k128 = l.n128;
+    a.ids = ids;
+    a.top_k = cfg.top_k;
+    a.experts = cfg.experts;
+    a.act = cfg.activation;
+    a.planes = c.y_dtype == GPTQ_FP32 ? 3 : 2;
+    a.mid = mid;
+    a.out = out;
+  };
   auto steps = [&](const W4Layout& l) { return l.g >= l.n128 ? 4 : (int)(l.g / 32); };
+  MoeExpertArgs g, d;
+  weight(g, L.gu, packed, L.gu.mt / 2);
+  weight(d, L.down, packed + L.down_off, L.down.mt);
+  g.A = Xp;
+  g.rows = L.f128;
+  d.A = mid;
+  d.rows = cfg.hidden;
 
   for (int64_t t0 = 0; t0 < c.tokens; t0 += w.block) {
     const int tk = (int)std::min<int64_t>(w.block, c.tokens - t0);
@@ -421,49 +440,43 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
     r.top_k = cfg.top_k;
     r.renorm = cfg.renormalize;
     r.vec = h % 8 == 0 && (reinterpret_cast<uintptr_t>(c.router) & 15) == 0;
+    r.xvec = (reinterpret_cast<uintptr_t>(c.X) & 15) == 0 && c.ldx % 8 == 0;
+    r.parts = cfg.experts > 8 ? 1 : cfg.experts > 4 ? 2 : cfg.experts > 2 ? 4 : 8;
     r.ids = ids;
     r.wts = wts;
     r.ids_out = c.topk_ids ? c.topk_ids + t0 * cfg.top_k : nullptr;
     r.wts_out = c.topk_weights ? c.topk_weights + t0 * cfg.top_k : nullptr;
-    const size_t rlds = (size_t)round_up(cfg.experts, 2) * sizeof(double) + (size_t)h * sizeof(float);
+    r.packed = packed;
+    r.stride = (int64_t)L.stride;
+    r.order_off = (int64_t)L.gu.order_off;
+    r.n128 = L.gu.n128;
+    r.Xp = Xp;
+    const size_t rlds = (size_t)round_up((int64_t)r.parts * cfg.experts, 2) * sizeof(double) + (size_t)round_up(h, 8) * 2;
     if (rlds > 65536)
       GPTQ_HIP_CHECK(hipFuncSetAttribute((const void*)moe_router_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)rlds));
     hipLaunchKernelGGL(moe_router_kernel, dim3((unsigned)tk), dim3(1024), rlds, stream, r);
     GPTQ_LAUNCH_CHECK();
 
-    const unsigned slots = (unsigned)std::min<int64_t>(cfg.experts, (int64_t)tk * cfg.top_k);
-    g.X = r.X;
+    // the workgroups of the GPU dealt over the experts that can be active
+    const int64_t slots = std::min<int64_t>(cfg.experts, (int64_t)tk * cfg.top_k);
+    const int64_t share = std::max<int64_t>(1, 256 / slots);
     g.tokens = d.tokens = tk;
-    g.pass = (int)std::min<size_t>({(size_t)kMoePass, (size_t)tk, (size_t)(128 * 1024) / row});
-    const size_t glds = row * (size_t)g.pass;
-    const dim3 ggrid((unsigned)ceil_div(g.units, 8 >> g.kslog), slots);
-    const dim3 dgrid((unsigned)ceil_div(d.units, 8 >> d.kslog), slots);
-#define MOE_GATE_UP(GS)                                                                                          \
-  do {                                                                                                           \
-    if (glds > 32768)                                                                                            \
-      GPTQ_HIP_CHECK(hipFuncSetAttribute((const void*)moe_gate_up_kernel<GS>,                                    \
-                                         hipFuncAttributeMaxDynamicSharedMemorySize, (int)glds));                \
-    hipLaunchKernelGGL(moe_gate_up_kernel<GS>, ggrid, dim3(512), glds, stream, g);                               \
-  } while (0)
+    bool in_lds = false;
+    const int64_t gw = std::min<int64_t>(share, g.st.units), dw = std::min<int64_t>(share, d.st.units);
+    size_t lds = moe_plan(g, tk, 1, 2, gw, &in_lds);
+    const dim3 ggrid((unsigned)std::min<int64_t>(gw, ceil_div(g.st.units, kL4Waves >> g.st.kslog)), (unsigned)slots);
     switch (steps(L.gu)) {
-      case 1: MOE_GATE_UP(1); break;
-      case 2: MOE_GATE_UP(2); break;
-      default: MOE_GATE_UP(4); break;
+      case 1: GPTQ_TRY(launch_gate_up<1>(ggrid, lds, in_lds, g, stream)); break;
+      case 2: GPTQ_TRY(launch_gate_up<2>(ggrid, lds, in_lds, g, stream)); break;
+      default: GPTQ_TRY(launch_gate_up<4>(ggrid, lds, in_lds, g, stream)); break;
     }
-#undef MOE_GATE_UP
-    GPTQ_LAUNCH_CHECK();
-#define MOE_DOWN(GS)                                                                                             \
-  if (g.planes == 3)                                                                                             \
-    hipLaunchKernelGGL((moe_down_kernel<GS, 3>), dgrid, dim3(512), 0, stream, d);                                \
-  else                                                                                                           \
-    hipLaunchKernelGGL((moe_down_kernel<GS, 2>), dgrid, dim3(512), 0, stream, d)
+    lds = moe_plan(d, tk, d.planes, 1, dw, &in_lds);
+    const dim3 dgrid((unsigned)std::min<int64_t>(dw, ceil_div(d.st.units, kL4Waves >> d.st.kslog)), (unsigned)slots);
     switch (steps(L.down)) {
-      case 1: MOE_DOWN(1); break;
-      case 2: MOE_DOWN(2); break;
-      default: MOE_DOWN(4); break;
+      case 1: GPTQ_TRY(launch_down<1>(dgrid, lds, in_lds, d, stream)); break;
+      case 2: GPTQ_TRY(launch_down<2>(dgrid, lds, in_lds, d, stream)); break;
+      default: GPTQ_TRY(launch_down<4>(dgrid, lds, in_lds, d, stream)); break;
     }
-#undef MOE_DOWN
-    GPTQ_LAUNCH_CHECK();
     hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)ceil_div(cfg.hidden, 256), (unsigned)tk), dim3(256), 0, stream,
                        (const float*)out, (const float*)wts, (int)cfg.top_k, cfg.hidden,
                        c.res ? (const void*)(static_cast<const char*>(c.res) + (size_t)(t0 * c.ldr) * rsz) : nullptr,
