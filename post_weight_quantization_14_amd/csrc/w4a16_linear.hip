@@ -244,26 +244,28 @@ struct L4GemmArgs {
   L4Epilogue ep;
 };
 
-// Tile: 64·TG tokens x 64·RG rows, TG·RG waves of (32·MT = 64·..) tokens x 64
-// rows on v_mfma_f32_32x32x16_bf16.
-template <int GS, int MT, int TG, int RG>
+// Tile: 32·MT·TG tokens x 64·RG rows; TG·RG waves of 32·MT tokens x 64 rows on
+// v_mfma_f32_32x32x16_bf16, and KG such groups of waves that take every KG-th
+// chunk of the slice (few tokens: the chain of chunks is latency, and a
+// workgroup's groups run KG of them side by side).
+template <int GS, int MT, int TG, int RG, int KG>
 struct L4Tile {
-  static constexpr int kTokens = 32 * MT * TG, kRows = 64 * RG, kWaves = TG * RG;
+  static constexpr int kTokens = 32 * MT * TG, kRows = 64 * RG, kGroup = TG * RG, kThreads = 64 * kGroup * KG;
   static constexpr int kNG = 4 / GS;
-  static constexpr int kX = kTokens * 256;                 // X' of one chunk
-  static constexpr int kBytes = kX + kNG * kTokens * 4;    // and its group sums
-  static constexpr int kXCopies = kX / 1024 / kWaves;      // 1 KB copies per wave
-  static_assert(kX % (1024 * kWaves) == 0, "copies split evenly over the waves");
-  static_assert(kTokens % 64 == 0, "sums are copied 64 floats at a time");
+  static constexpr int kX = kTokens * 256;                                         // X' of one chunk
+  static constexpr int kBytes = kX + ((kNG * kTokens * 4 + 255) & ~255);           // and its group sums
+  static constexpr int kXCopies = kX / 1024 / kGroup;                              // 1 KB copies per wave
+  static_assert(kX % (1024 * kGroup) == 0, "copies split evenly over the waves");
+  static_assert(kTokens % 32 == 0, "sums are copied 32 or 64 floats at a time");
 };
 
-template <int GS, int MT, int TG, int RG, bool GATED>
+template <int GS, int MT, int TG, int RG, int KG, bool GATED>
 __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __restrict__ s0, uint8_t* __restrict__ s1) {
-  using Tl = L4Tile<GS, MT, TG, RG>;
+  using Tl = L4Tile<GS, MT, TG, RG, KG>;
   constexpr int NG = Tl::kNG, U = Tl::kXCopies;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int rg = wave % RG, tg = wave / RG;
+  const int kg = wave / Tl::kGroup, gw = wave % Tl::kGroup, rg = gw % RG, tg = gw / RG;
   // slices outermost, then row blocks in bands of token blocks
   int64_t i = blockIdx.x;
   const int64_t per = a.tblocks * a.rblocks;
@@ -272,6 +274,7 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
   const int64_t tb = i % a.tblocks, rb = i / a.tblocks;
   const int64_t t0 = tb * Tl::kTokens;
   const int c0 = sl * a.chunks, nch = (int)std::min<int64_t>(a.chunks, a.kc - c0);
+  const int steps = (nch + KG - 1) / KG;   // this wave's chunk of step s: s·KG + kg
 
   // X' rows past the last token lie outside the descriptor and read as zero
   const int64_t trows = std::min<int64_t>(Tl::kTokens, a.tokens - t0);
@@ -281,26 +284,30 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     // 1 KB = 4 token rows of 16 pieces; row t keeps piece p in slot p ^ (t mod 16)
-    const int q = (wave * U + u) * 64 + lane, t = q >> 4, pc = (q & 15) ^ (t & 15);
+    const int q = (gw * U + u) * 64 + lane, t = q >> 4, pc = (q & 15) ^ (t & 15);
     xoff[u] = (int32_t)(t * a.n128 * 2 + pc * 16);
   }
-  // 64-lane copies of the sums, 4 bytes each, spread over the waves
-  constexpr int SC = NG * Tl::kTokens / 64;
+  // copies of the sums, 4 bytes a lane, 64 (or 32) tokens each, spread over
+  // the group's waves
+  constexpr int SW = Tl::kTokens >= 64 ? 64 : 32;          // tokens per copy
+  constexpr int SC = NG * Tl::kTokens / SW;
   const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<float*>(a.sums + t0), 0, (int32_t)std::min<int64_t>((a.kc * NG * a.tpad - t0) * 4, 0x7fffffff),
       0x00020000);
-  auto issue = [&](int c, uint8_t* slot) {
-    const int cc = c0 + std::min(c, nch - 1);
+  auto issue = [&](int s, uint8_t* slots) {
+    uint8_t* slot = slots + kg * Tl::kBytes;
+    const int cc = c0 + std::min(s * KG + kg, nch - 1);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)(slot + (wave * U + u) * 1024), 16, xoff[u], cc * 256, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)(slot + (gw * U + u) * 1024), 16, xoff[u], cc * 256, 0, 0);
 #pragma unroll
-    for (int k = 0; k < (SC + Tl::kWaves - 1) / Tl::kWaves; ++k) {
-      const int s = k * Tl::kWaves + wave;
-      if (SC % Tl::kWaves == 0 || s < SC) {
-        const int g = s / (Tl::kTokens / 64), part = s % (Tl::kTokens / 64);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(slot + Tl::kX + s * 256), 4, (part * 64 + lane) * 4,
-                                                (int32_t)((cc * NG + g) * a.tpad * 4), 0, 0);
+    for (int k = 0; k < (SC + Tl::kGroup - 1) / Tl::kGroup; ++k) {
+      const int c = k * Tl::kGroup + gw;
+      if (SC % Tl::kGroup == 0 || c < SC) {
+        const int g = c / (Tl::kTokens / SW), part = c % (Tl::kTokens / SW);
+        if (SW == 64 || lane < 32)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(slot + Tl::kX + c * SW * 4), 4, (part * SW + lane) * 4,
+                                                  (int32_t)((cc * NG + g) * a.tpad * 4), 0, 0);
       }
     }
   };
@@ -327,7 +334,7 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
     float2 p[2][NG];
   };
   auto fetch = [&](int c, Codes& k) {
-    const int cc = std::min(c, nch - 1);
+    const int cc = std::min(c * KG + kg, nch - 1);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
 #pragma unroll
@@ -412,26 +419,51 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
   Codes k0, k1;
   issue(0, s0);
   fetch(0, k0);
-  // one step: every copy of this chunk has landed (all waves', after the
+  // one step: every copy of this step has landed (all waves', after the
   // barrier) and every wave is done with the other slot, which the next refills
-#define L4_STEP(c, cur, kcur, nxt, knxt)                                          \
+#define L4_STEP(s, cur, kcur, nxt, knxt)                                          \
   {                                                                               \
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");      \
-    issue((c) + 1, nxt);                                                          \
-    fetch((c) + 1, knxt);                                                         \
-    if ((c) < nch) compute(cur, kcur);                                            \
+    issue((s) + 1, nxt);                                                          \
+    fetch((s) + 1, knxt);                                                         \
+    if ((s) * KG + kg < nch) compute(cur + kg * Tl::kBytes, kcur);                \
   }
-  for (int c = 0; c < nch; c += 2) {
-    L4_STEP(c, s0, k0, s1, k1)
-    L4_STEP(c + 1, s1, k1, s0, k0)
+  for (int s = 0; s < steps; s += 2) {
+    L4_STEP(s, s0, k0, s1, k1)
+    L4_STEP(s + 1, s1, k1, s0, k0)
   }
 #undef L4_STEP
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy may land after the workgroup ends
 
+  // the groups' sums through LDS, halving: group kg takes over kg + KG/2, ..
+#pragma unroll
+  for (int half = KG / 2; half > 0; half /= 2) {
+    static_assert(KG == 1 || (KG / 2) * Tl::kGroup * MT * 2 * 16 * 256 <= KG * Tl::kBytes, "half of the groups fit");
+    __syncthreads();   // the copies and reads of s0, and the round before, are done
+    f32x4_t* at = reinterpret_cast<f32x4_t*>(s0) + (((kg & (half - 1)) * Tl::kGroup + gw) * MT * 8) * 64 + lane;
+    if (kg >= half && kg < 2 * half) {
+#pragma unroll
+      for (int f = 0; f < MT * 8; ++f) {
+        const f32x16_t& v = y[f >> 3][(f >> 2) & 1];
+        at[f * 64] = f32x4_t{v[4 * (f & 3)], v[4 * (f & 3) + 1], v[4 * (f & 3) + 2], v[4 * (f & 3) + 3]};
+      }
+    }
+    __syncthreads();
+    if (kg < half) {
+#pragma unroll
+      for (int f = 0; f < MT * 8; ++f) {
+        const f32x4_t o = at[f * 64];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) y[f >> 3][(f >> 2) & 1][4 * (f & 3) + v] += o[v];
+      }
+    }
+  }
+  if (kg > 0) return;
+
   if (a.splits > 1) {
     // fragments as they lie: [slice][tile][wave][mt][b][q][lane] float4
     f32x4_t* out = reinterpret_cast<f32x4_t*>(a.part) +
-                   (((int64_t)sl * per + i) * Tl::kWaves + wave) * (MT * 2 * 4 * 64) + lane;
+                   (((int64_t)sl * per + i) * Tl::kGroup + gw) * (MT * 2 * 4 * 64) + lane;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -460,14 +492,14 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
   }
 }
 
-template <int GS, int MT, int TG, int RG, bool GATED>
-__global__ __launch_bounds__(64 * TG * RG, TG * RG == 8 ? 1 : 2) void l4_gemm_kernel(L4GemmArgs a) {
-  using Tl = L4Tile<GS, MT, TG, RG>;
+template <int GS, int MT, int TG, int RG, int KG, bool GATED>
+__global__ __launch_bounds__(64 * TG * RG * KG, 2) void l4_gemm_kernel(L4GemmArgs a) {
+  using Tl = L4Tile<GS, MT, TG, RG, KG>;
   // two arrays, not one indexed at run time: a read of one is then known not
   // to alias the copies in flight into the other
-  __shared__ __attribute__((aligned(16))) uint8_t s0[Tl::kBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t s1[Tl::kBytes];
-  l4_gemm_tile<GS, MT, TG, RG, GATED>(a, s0, s1);
+  __shared__ __attribute__((aligned(16))) uint8_t s0[KG * Tl::kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s1[KG * Tl::kBytes];
+  l4_gemm_tile<GS, MT, TG, RG, KG, GATED>(a, s0, s1);
 }
 
 // Sums the K slices in slice order and finishes.  Thread: one float4 fragment
@@ -532,20 +564,19 @@ gptq_status run_w4a16_glu_pack(const L4PairSource& src, const int32_t* g_idx, co
 }
 
 namespace {
-// the tile of `tokens` tokens: its extents, and the K slices that fill the GPU
+// the tile for a number of tokens, and the K slices that fill the GPU
 struct L4Shape {
-  int mt = 2, tg = 1, rg = 2;
+  int tokens = 128;                 // 32, 64 or 128, x 128 packed rows
   int64_t tblocks = 0, rblocks = 0;
   int splits = 1, chunks = 0;
-  int64_t tile_tokens() const { return 32 * mt * tg; }
 };
 L4Shape l4_shape(int64_t tokens, int64_t packed_rows, int64_t kc) {
   L4Shape s;
-  s.tg = tokens > 64 ? 2 : 1;
-  s.rg = s.tg == 1 ? 4 : 2;
-  s.tblocks = ceil_div(tokens, s.tile_tokens());
-  s.rblocks = ceil_div(packed_rows, 64 * s.rg);
+  s.tokens = tokens > 64 ? 128 : tokens > 32 ? 64 : 32;
+  s.tblocks = ceil_div(tokens, s.tokens);
+  s.rblocks = ceil_div(packed_rows, 128);
   const int64_t tiles = s.tblocks * s.rblocks;
+  // four chunks at least in a slice: one step of the 4 groups, or 4 steps
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kc / 4, 256 / tiles));
   s.chunks = (int)ceil_div(kc, want);
   s.splits = (int)ceil_div(kc, s.chunks);
@@ -578,11 +609,11 @@ gptq_status launch_l4_decode(const L4DecodeArgs& d, int gs, bool gated, int src,
   }
 }
 
-template <int GS, int MT, int TG, int RG, bool GATED>
+template <int GS, int MT, int TG, int RG, int KG, bool GATED>
 gptq_status launch_l4_tile(const L4GemmArgs& g, hipStream_t stream) {
   const int64_t tiles = g.tblocks * g.rblocks;
-  hipLaunchKernelGGL((l4_gemm_kernel<GS, MT, TG, RG, GATED>), dim3((unsigned)(tiles * g.splits)), dim3(64 * TG * RG), 0,
-                     stream, g);
+  hipLaunchKernelGGL((l4_gemm_kernel<GS, MT, TG, RG, KG, GATED>), dim3((unsigned)(tiles * g.splits)),
+                     dim3(64 * TG * RG * KG), 0, stream, g);
   GPTQ_LAUNCH_CHECK();
   if (g.splits > 1) {
     const int64_t frags = tiles * TG * RG * MT * 8 * 64 / (GATED ? 2 : 1);
@@ -594,11 +625,9 @@ gptq_status launch_l4_tile(const L4GemmArgs& g, hipStream_t stream) {
 
 template <int GS, bool GATED>
 gptq_status launch_l4_shape(const L4GemmArgs& g, const L4Shape& s, hipStream_t stream) {
-  switch (s.tg) {
-    case 1: return launch_l4_tile<GS, 2, 1, 4, GATED>(g, stream);
-    case 2: return launch_l4_tile<GS, 2, 2, 2, GATED>(g, stream);
-    default: return launch_l4_tile<GS, 2, 4, 2, GATED>(g, stream);
-  }
+  if (s.tokens == 32) return launch_l4_tile<GS, 1, 1, 2, 4, GATED>(g, stream);
+  if (s.tokens == 64) return launch_l4_tile<GS, 2, 1, 2, 4, GATED>(g, stream);
+  return launch_l4_tile<GS, 2, 2, 2, 1, GATED>(g, stream);
 }
 
 gptq_status launch_l4_gemm(const L4GemmArgs& g, const L4Shape& s, int gs, bool gated, hipStream_t stream) {
@@ -624,7 +653,7 @@ L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n, int64_t packed_rows) {
     const L4Shape s = l4_shape(tk, packed_rows, kc);
     if (s.splits > 1)
       p.total = std::max(p.total, p.part_off + align256((size_t)(s.splits * s.tblocks * s.rblocks) *
-                                                        (size_t)(s.tile_tokens() * 64 * s.rg) * sizeof(float)));
+                                                        (size_t)(s.tokens * 128) * sizeof(float)));
   }
   return p;
 }
