@@ -285,25 +285,30 @@ __device__ __forceinline__ void l4_row_to_lds(const uint16_t* __restrict__ x, in
   for (int64_t i = done + tid; i < n; i += threads) reinterpret_cast<uint16_t*>(lds)[i] = x[i];
 }
 
-// X' = X[:, order] of `tokens` rows into LDS (rows n128 + 8 apart), through a
-// raw copy of one row at a time: LDS serves scattered 2-byte reads in a few
+// X' = X[:, order] of `tokens` rows into LDS (rows n128 + 8 apart), through raw
+// copies of `batch` rows at a time: LDS serves scattered 2-byte reads in a few
 // cycles where the memory pipe takes one or more per lane.
-__device__ __forceinline__ void l4_gather_lds(const uint16_t* __restrict__ X, int64_t ldx, int64_t n, int vec,
-                                              const int32_t* __restrict__ order, int n128, int tokens, uint16_t* xsh,
-                                              uint8_t* raw) {
-  const int tid = threadIdx.x;
-  const uint16_t* x = reinterpret_cast<const uint16_t*>(raw);
-  for (int t = 0; t < tokens; ++t) {
-    if (t) __syncthreads();
-    l4_row_to_lds(X + t * ldx, n, vec, raw, tid, kL4Threads);
+__device__ __forceinline__ void l4_gather_lds(const uint16_t* __restrict__ X, int64_t ldx, int n, int vec,
+                                              const int32_t* __restrict__ order, int n128, int tokens, int batch,
+                                              uint16_t* xsh, uint8_t* raw) {
+  const int tid = threadIdx.x, rrow = (n + 7) & ~7;   // raw rows start 16-byte aligned
+  for (int t0 = 0; t0 < tokens; t0 += batch) {
+    const int nt = std::min(batch, tokens - t0);
+    if (t0) __syncthreads();   // the batch before has been gathered
+    for (int t = 0; t < nt; ++t)
+      l4_row_to_lds(X + (t0 + t) * ldx, n, vec, raw + (size_t)t * rrow * 2, tid, kL4Threads);
     __syncthreads();
     for (int p = 4 * tid; p < n128; p += 4 * kL4Threads) {
       const int4 o = *reinterpret_cast<const int4*>(order + p);
-      const uint32_t a = x[std::max(o.x, 0)], b = x[std::max(o.y, 0)], c = x[std::max(o.z, 0)], d = x[std::max(o.w, 0)];
-      uint2 v;
-      v.x = (o.x >= 0 ? a : 0u) | (o.y >= 0 ? b : 0u) << 16;
-      v.y = (o.z >= 0 ? c : 0u) | (o.w >= 0 ? d : 0u) << 16;
-      *reinterpret_cast<uint2*>(xsh + t * (n128 + kL4Pad) + p) = v;
+      const int a = std::max(o.x, 0), b = std::max(o.y, 0), c = std::max(o.z, 0), d = std::max(o.w, 0);
+      for (int t = 0; t < nt; ++t) {
+        const uint16_t* x = reinterpret_cast<const uint16_t*>(raw) + (size_t)t * rrow;
+        const uint32_t xa = x[a], xb = x[b], xc = x[c], xd = x[d];
+        uint2 v;
+        v.x = (o.x >= 0 ? xa : 0u) | (o.y >= 0 ? xb : 0u) << 16;
+        v.y = (o.z >= 0 ? xc : 0u) | (o.w >= 0 ? xd : 0u) << 16;
+        *reinterpret_cast<uint2*>(xsh + (t0 + t) * (n128 + kL4Pad) + p) = v;
+      }
     }
   }
   __syncthreads();

@@ -126,29 +126,26 @@ struct L4DecodeArgs {
   int64_t ldx, n;
   const uint16_t* Xp;     // else X' [tokens][n128]
   int64_t n128, m;
-  int tokens, quads, vec;
+  int tokens, quads, vec, batch;   // batch: raw rows gathered at a time
   L4Epilogue ep;
 };
 
-enum L4Source { kL4Gather = 0, kL4Copy = 1, kL4Global = 2 };
-
-// Up to 16 tokens.  Unit = one row tile (linear) or one gate/up pair of tiles
-// (glu).  X' sits in LDS, gathered here (kL4Gather) or copied from X' in
-// memory (kL4Copy), or is read from memory fragment by fragment (kL4Global)
-// where it does not fit.
-template <int GS, bool GATED, int SRC>
+// Few tokens whose X' fits in LDS.  Unit = one row tile (linear) or one
+// gate/up pair of tiles (glu).  X' is gathered here (GATHER) or copied from X'
+// in memory.
+template <int GS, bool GATED, bool GATHER>
 __global__ __launch_bounds__(kL4Threads) void l4_decode_kernel(L4DecodeArgs a) {
   constexpr int RT = GATED ? 2 : 1;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63;
   const int xrow = (int)a.n128 + kL4Pad;
   uint16_t* xsh = reinterpret_cast<uint16_t*>(lds);
-  uint8_t* rest = lds + (SRC == kL4Global ? 0 : (size_t)a.tokens * xrow * 2);
-  float* red = reinterpret_cast<float*>(rest);   // after the gather, over its raw row
+  uint8_t* rest = lds + (size_t)a.tokens * xrow * 2;
+  float* red = reinterpret_cast<float*>(rest);   // after the gather, over its raw rows
   auto fill = [&] {
-    if (SRC == kL4Gather) {
-      l4_gather_lds(a.X, a.ldx, a.n, a.vec, a.order, (int)a.n128, a.tokens, xsh, rest);
-    } else if (SRC == kL4Copy) {
+    if (GATHER) {
+      l4_gather_lds(a.X, a.ldx, (int)a.n, a.vec, a.order, (int)a.n128, a.tokens, a.batch, xsh, rest);
+    } else {
       const int pieces = (int)(a.n128 / 8);
       for (int i = threadIdx.x; i < a.tokens * pieces; i += kL4Threads)
         *reinterpret_cast<uint4*>(xsh + (i / pieces) * xrow + 8 * (i % pieces)) =
@@ -168,17 +165,10 @@ __global__ __launch_bounds__(kL4Threads) void l4_decode_kernel(L4DecodeArgs a) {
     });
   };
   const int t = std::min(lane & 15, a.tokens - 1);   // rows past the last: computed, not stored
-  const int64_t first = (int64_t)blockIdx.x * upw, step = (int64_t)gridDim.x * upw;
   // batches that leave the wave within 128 registers (16 waves on a CU)
-  constexpr int BL = GATED ? (GS == 1 ? 1 : 2) : (GS == 4 ? 4 : GS == 2 ? 3 : 2);
-  constexpr int BG = GATED ? 1 : (GS == 4 ? 2 : 1);
-  if (SRC == kL4Global) {
-    const L4GlobalA af{a.Xp + t * a.n128 + 8 * (lane >> 4), 0};
-    l4_units<GS, RT, 1, BG, false>(a.st, first, step, af, fill, end);
-  } else {
-    const L4LdsA af{xsh + t * xrow + 8 * (lane >> 4), 0};
-    l4_units<GS, RT, 1, BL, false>(a.st, first, step, af, fill, end);
-  }
+  constexpr int B = GATED ? (GS == 1 ? 1 : 2) : (GS == 4 ? 4 : GS == 2 ? 3 : 2);
+  const L4LdsA af{xsh + t * xrow + 8 * (lane >> 4), 0};
+  l4_units<GS, RT, 1, B, false>(a.st, (int64_t)blockIdx.x * upw, (int64_t)gridDim.x * upw, af, fill, end);
 }
 
 // ---------------------------------------------------------------- many tokens
@@ -435,30 +425,48 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
 #undef L4_STEP
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy may land after the workgroup ends
 
-  // the groups' sums through LDS, halving: group kg takes over kg + KG/2, ..
+  if (KG > 1) {
+    // The groups' sums through LDS: every wave leaves its fragments, then each
+    // group adds and finishes its share of them (4 tokens of a row, gate and
+    // up together), so the epilogue runs on all waves.
+    constexpr int F = MT * 8, SHARE = MT * 4 / KG;
+    static_assert(KG == 1 || (MT * 4) % KG == 0, "the fragments split evenly over the groups");
+    static_assert(KG == 1 || (KG / 2) * Tl::kGroup * F * 1024 <= KG * Tl::kBytes, "half of the groups fit in each array");
+    __syncthreads();   // every copy into the slots and every read of them is done
+    auto at = [&](int k, int f) {
+      return reinterpret_cast<f32x4_t*>(k < KG / 2 ? s0 : s1) + (((k % (KG / 2)) * Tl::kGroup + gw) * F + f) * 64 + lane;
+    };
 #pragma unroll
-  for (int half = KG / 2; half > 0; half /= 2) {
-    static_assert(KG == 1 || (KG / 2) * Tl::kGroup * MT * 2 * 16 * 256 <= KG * Tl::kBytes, "half of the groups fit");
-    __syncthreads();   // the copies and reads of s0, and the round before, are done
-    f32x4_t* at = reinterpret_cast<f32x4_t*>(s0) + (((kg & (half - 1)) * Tl::kGroup + gw) * MT * 8) * 64 + lane;
-    if (kg >= half && kg < 2 * half) {
-#pragma unroll
-      for (int f = 0; f < MT * 8; ++f) {
-        const f32x16_t& v = y[f >> 3][(f >> 2) & 1];
-        at[f * 64] = f32x4_t{v[4 * (f & 3)], v[4 * (f & 3) + 1], v[4 * (f & 3) + 2], v[4 * (f & 3) + 3]};
-      }
+    for (int f = 0; f < F; ++f) {
+      const f32x16_t& v = y[f >> 3][(f >> 2) & 1];
+      *at(kg, f) = f32x4_t{v[4 * (f & 3)], v[4 * (f & 3) + 1], v[4 * (f & 3) + 2], v[4 * (f & 3) + 3]};
     }
     __syncthreads();
-    if (kg < half) {
 #pragma unroll
-      for (int f = 0; f < MT * 8; ++f) {
-        const f32x4_t o = at[f * 64];
+    for (int j = 0; j < SHARE; ++j) {
+      const int c = kg * SHARE + j, mt = c >> 2, q = c & 3;
+      f32x4_t z[2];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) y[f >> 3][(f >> 2) & 1][4 * (f & 3) + v] += o[v];
+      for (int b = 0; b < 2; ++b) {
+        z[b] = *at(0, mt * 8 + b * 4 + q);
+#pragma unroll
+        for (int k = 1; k < KG; ++k) z[b] += *at(k, mt * 8 + b * 4 + q);
       }
+      if (a.splits > 1) {
+        f32x4_t* out = reinterpret_cast<f32x4_t*>(a.part) +
+                       ((((int64_t)sl * per + i) * Tl::kGroup + gw) * F + mt * 8 + q) * 64 + lane;
+        out[0] = z[0];
+        out[256] = z[1];
+        continue;
+      }
+      const int64_t t = t0 + 32 * (MT * tg + mt) + 8 * q + 4 * (lane >> 5);
+      const int64_t r = (rb * RG + rg) * (GATED ? 32 : 64) + (lane & 31);
+      const float g4[4] = {z[0][0], z[0][1], z[0][2], z[0][3]}, u4[4] = {z[1][0], z[1][1], z[1][2], z[1][3]};
+      a.ep.template block<4, GATED>(t, a.tokens, r, a.m, g4, u4);
+      if (!GATED) a.ep.template block<4, false>(t, a.tokens, r + 32, a.m, u4, u4);
     }
+    return;
   }
-  if (kg > 0) return;
 
   if (a.splits > 1) {
     // fragments as they lie: [slice][tile][wave][mt][b][q][lane] float4
@@ -577,22 +585,22 @@ L4Shape l4_shape(int64_t tokens, int64_t packed_rows, int64_t kc) {
   s.rblocks = ceil_div(packed_rows, 128);
   const int64_t tiles = s.tblocks * s.rblocks;
   // four chunks at least in a slice: one step of the 4 groups, or 4 steps
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kc / 4, 256 / tiles));
+  // (up to 12 chunks are not split at all: three steps of the 4 groups cost
+  // less than the launch that adds the slices)
+  const int64_t want = kc <= 12 && s.tokens <= 64 ? 1 : std::max<int64_t>(1, std::min<int64_t>(kc / 4, 256 / tiles));
   s.chunks = (int)ceil_div(kc, want);
   s.splits = (int)ceil_div(kc, s.chunks);
   return s;
 }
 constexpr size_t kL4GatherLds = 65536;    // rows up to 32768 columns are gathered through LDS
-constexpr int64_t kL4DecodeTokens = 16;   // up to here the few-token kernel
-constexpr int64_t kL4GatherTokens = 4;    // up to here it gathers X' itself
+constexpr int64_t kL4DecodeTokens = 16;   // up to here the decode kernel, if X' fits in LDS
+constexpr int64_t kL4GatherMax = 65536;   // up to this many elements of X' it gathers them itself
 constexpr size_t kL4MaxLds = 158 * 1024;
 constexpr int64_t kL4Cus = 256;
 
 template <int GS, bool GATED>
-gptq_status launch_l4_source(const L4DecodeArgs& d, int src, unsigned grid, size_t lds, hipStream_t stream) {
-  const void* fn = src == kL4Gather ? (const void*)l4_decode_kernel<GS, GATED, kL4Gather>
-                   : src == kL4Copy ? (const void*)l4_decode_kernel<GS, GATED, kL4Copy>
-                                    : (const void*)l4_decode_kernel<GS, GATED, kL4Global>;
+gptq_status launch_l4_source(const L4DecodeArgs& d, bool gather, unsigned grid, size_t lds, hipStream_t stream) {
+  const void* fn = gather ? (const void*)l4_decode_kernel<GS, GATED, true> : (const void*)l4_decode_kernel<GS, GATED, false>;
   if (lds > 65536) GPTQ_HIP_CHECK(hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
   L4DecodeArgs args = d;
   void* argv[] = {&args};
@@ -600,12 +608,12 @@ gptq_status launch_l4_source(const L4DecodeArgs& d, int src, unsigned grid, size
   return GPTQ_OK;
 }
 
-gptq_status launch_l4_decode(const L4DecodeArgs& d, int gs, bool gated, int src, unsigned grid, size_t lds,
+gptq_status launch_l4_decode(const L4DecodeArgs& d, int gs, bool gated, bool gather, unsigned grid, size_t lds,
                              hipStream_t stream) {
   switch (gs) {
-    case 1: return gated ? launch_l4_source<1, true>(d, src, grid, lds, stream) : launch_l4_source<1, false>(d, src, grid, lds, stream);
-    case 2: return gated ? launch_l4_source<2, true>(d, src, grid, lds, stream) : launch_l4_source<2, false>(d, src, grid, lds, stream);
-    default: return gated ? launch_l4_source<4, true>(d, src, grid, lds, stream) : launch_l4_source<4, false>(d, src, grid, lds, stream);
+    case 1: return gated ? launch_l4_source<1, true>(d, gather, grid, lds, stream) : launch_l4_source<1, false>(d, gather, grid, lds, stream);
+    case 2: return gated ? launch_l4_source<2, true>(d, gather, grid, lds, stream) : launch_l4_source<2, false>(d, gather, grid, lds, stream);
+    default: return gated ? launch_l4_source<4, true>(d, gather, grid, lds, stream) : launch_l4_source<4, false>(d, gather, grid, lds, stream);
   }
 }
 
@@ -649,7 +657,7 @@ L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n, int64_t packed_rows) {
   p.total = p.part_off;
   // the last, shorter block of a long call may take more slices than the others
   for (int64_t tk : {p.block, tokens % p.block}) {
-    if (tk <= kL4DecodeTokens) continue;
+    if (tk == 0) continue;
     const L4Shape s = l4_shape(tk, packed_rows, kc);
     if (s.splits > 1)
       p.total = std::max(p.total, p.part_off + align256((size_t)(s.splits * s.tblocks * s.rblocks) *
@@ -682,26 +690,24 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
     const L4Epilogue ep{c.act, c.bias_dtype, c.res_dtype, c.y_dtype, c.bias, c.bias2,
                         c.res ? static_cast<const char*>(c.res) + (size_t)(t0 * c.ldr) * rsz : nullptr,
                         static_cast<char*>(c.Y) + (size_t)(t0 * c.ldy) * ysz, c.ldr, c.ldy};
-    const bool decode = tk <= kL4DecodeTokens;
-    int src = kL4Copy;
+    // Few tokens whose X' and sums fit in LDS take the decode kernel, which
+    // gathers X' itself where that is a barrier or two of work.
     L4DecodeArgs d;
+    bool decode = false, gather = false;
     size_t dlds = 0;
-    if (decode) {
+    if (tk <= kL4DecodeTokens) {
       d.quads = (int)ceil_div(tk, 4);
       const size_t rows = (size_t)tk * (size_t)(L.n128 + kL4Pad) * 2;
       const size_t red = (size_t)kL4Waves * (gated ? 2 : 1) * d.quads * 64 * sizeof(float);
       const size_t raw = (size_t)round_up(L.n * 2, 16);
-      if (tk <= kL4GatherTokens && rows + std::max(red, raw) <= kL4MaxLds) {
-        src = kL4Gather;
-        dlds = rows + std::max(red, raw);
-      } else if (rows + red <= kL4MaxLds) {
-        dlds = rows + red;
-      } else {
-        src = kL4Global;
-        dlds = red;
+      decode = rows + red <= kL4MaxLds;
+      if (decode) {
+        d.batch = (int)std::min<int64_t>(tk, (int64_t)((kL4MaxLds - rows) / raw));
+        gather = 2 * d.batch >= tk && tk * L.n128 <= kL4GatherMax;
+        dlds = rows + std::max(red, gather ? raw * (size_t)d.batch : 0);
       }
     }
-    if (src != kL4Gather) {
+    if (!gather) {
       const size_t glds = (size_t)L.n * 2 <= kL4GatherLds ? (size_t)round_up(L.n * 2, 16) : 0;
       const dim3 ggrid((unsigned)tk, (unsigned)ceil_div(L.n128, 4096));
 #define L4_GATHER(GS)                                                                                             \
@@ -737,7 +743,7 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
       d.st = st;
       // workgroups that the split leaves without units are not launched
       const unsigned grid = (unsigned)std::min<int64_t>(wgs, ceil_div(st.units, kL4Waves >> sp.kslog));
-      GPTQ_TRY(launch_l4_decode(d, gs, gated, src, grid, dlds, stream));
+      GPTQ_TRY(launch_l4_decode(d, gs, gated, gather, grid, dlds, stream));
       continue;
     }
     const L4Shape sh = l4_shape(tk, L.mt * kL4Rows, L.kc);

@@ -49,115 +49,124 @@ __device__ __forceinline__ bool moe_before(double a, int ia, double b, int ib) {
   return ia < ib;
 }
 
-// The top_k experts of one token, largest first, and their weights (one wave).
-__device__ __forceinline__ void moe_choose(const MoeRouterArgs& a, const double* logit, int64_t t, int* chosen_ids) {
-  const int lane = threadIdx.x & 63;
-  // lane l holds experts l, l + 64, ...; taken = those already chosen
-  uint32_t taken = 0;
-  double top = 0.0, chosen = 0.0, mine = 0.0;
-  int my_id = 0;
-  for (int j = 0; j < a.top_k; ++j) {
-    double bv = 0.0;
-    int bi = kMoeMaxExperts;   // none
-    for (int e = lane, q = 0; e < a.experts; e += 64, ++q)
-      if (!(taken >> q & 1) && (bi == kMoeMaxExperts || moe_before(logit[e], e, bv, bi))) {
-        bv = logit[e];
-        bi = e;
-      }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-      const double ov = __shfl_xor(bv, d);
-      const int oi = __shfl_xor(bi, d);
-      if (oi != kMoeMaxExperts && (bi == kMoeMaxExperts || moe_before(ov, oi, bv, bi))) {
-        bv = ov;
-        bi = oi;
-      }
-    }
-    if ((bi & 63) == lane) taken |= 1u << (bi >> 6);
-    if (j == 0) top = bv;
-    const double p = exp(bv - top);
-    chosen += p;
-    if (lane == j) {
-      mine = p;
-      my_id = bi;
-    }
-  }
-  if (!a.renorm) {
-    chosen = 0.0;
-    for (int e = lane; e < a.experts; e += 64) chosen += exp(logit[e] - top);
-#pragma unroll
-    for (int d = 32; d; d >>= 1) chosen += __shfl_xor(chosen, d);
-  }
-  if (lane < a.top_k) {
-    const float w = (float)(mine / chosen);
-    chosen_ids[lane] = my_id;
-    a.ids[t * a.top_k + lane] = my_id;
-    a.wts[t * a.top_k + lane] = w;
-    if (a.ids_out) a.ids_out[t * a.top_k + lane] = my_id;
-    if (a.wts_out) a.wts_out[t * a.top_k + lane] = w;
-  }
-}
-
 // One workgroup per token.  The logits are summed in 64 bits: which experts
 // are chosen hangs on the last bits of the k-th and the next, and a choice
 // that falls the other way is no rounding error in the result.  `parts` waves
-// share an expert's row when there are fewer experts than waves; four
-// 512-element pieces are in flight per wave.
+// share an expert's row when there are fewer experts than waves.
+//
+// Then every expert's rank is the number of experts before it, counted by all
+// threads together (a chain of top_k wave-wide maxima took three times as
+// long), and the token is gathered into the column order of each chosen one.
 __global__ __launch_bounds__(1024) void moe_router_kernel(MoeRouterArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ int chosen_ids[kMoeMaxTopK];
+  __shared__ int chosen[kMoeMaxTopK];
+  __shared__ double total[16];
   const int64_t t = blockIdx.x;
-  const int h = (int)a.hidden;
+  const int h = (int)a.hidden, E = a.experts;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   double* logit = reinterpret_cast<double*>(lds);                      // [parts][experts]
-  uint16_t* x = reinterpret_cast<uint16_t*>(lds + (((size_t)a.parts * a.experts + 1) & ~(size_t)1) * sizeof(double));
+  int* rank = reinterpret_cast<int*>(logit + (((size_t)a.parts * E + 1) & ~(size_t)1));
+  uint16_t* x = reinterpret_cast<uint16_t*>(rank + ((E + 3) & ~3));
+  const int part = wave % a.parts, wpe = 16 / a.parts, e0 = wave / a.parts;
+  const bool fast = a.vec && a.r_dt == GPTQ_BF16;
+  const uint16_t* R = static_cast<const uint16_t*>(a.R);
+  // four 512-element pieces of a row; past its end zeros
+  auto fetch = [&](int e, int i, u32x4_t (&w)[4]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = i + 512 * a.parts * u;
+      const bool in = k < h && e < E;
+      w[u] = *reinterpret_cast<const u32x4_t*>(R + (in ? (int64_t)e * h + k : 0));
+      if (!in) w[u] = u32x4_t{0u, 0u, 0u, 0u};
+    }
+  };
+  const int i0 = 8 * lane + 512 * part, istep = 2048 * a.parts;
+  u32x4_t w[4], nx[4];
+  if (fast) fetch(e0, i0, w);   // in flight while the token is copied
   l4_row_to_lds(a.X + t * a.ldx, h, a.xvec, reinterpret_cast<uint8_t*>(x), tid, 1024);
+  for (int e = tid; e < E; e += 1024) rank[e] = 0;
   __syncthreads();
-  const int part = wave % a.parts, wpe = 16 / a.parts;
-  for (int e = wave / a.parts; e < a.experts; e += wpe) {
-    double s[2] = {0.0, 0.0};
-    if (a.vec && a.r_dt == GPTQ_BF16) {
-      const uint16_t* r = static_cast<const uint16_t*>(a.R) + (int64_t)e * h;
-      for (int i = 8 * lane + 512 * part; i < h; i += 2048 * a.parts) {
-        u32x4_t w[4], xv[4];
+  for (int e = e0; e < E; e += wpe) {
+    double s0 = 0.0, s1 = 0.0;
+    if (fast) {
+      for (int i = i0; i - 8 * lane < h; i += istep) {
+        const bool more = i + istep - 8 * lane < h;
+        fetch(more ? e : e + wpe, more ? i + istep : i0, nx);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int k = i + 512 * a.parts * u;
-          const bool in = k < h;   // past the end: the row's start again, times zero
-          w[u] = *reinterpret_cast<const u32x4_t*>(r + (in ? k : 8 * lane % h));
-          xv[u] = in ? *reinterpret_cast<const u32x4_t*>(x + k) : u32x4_t{0u, 0u, 0u, 0u};
-          if (!in) w[u] = u32x4_t{0u, 0u, 0u, 0u};
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
+          const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(x + (k < h ? k : 0));
 #pragma unroll
           for (int q = 0; q < 4; ++q) {   // bf16·bf16: exact in fp32
-            s[0] += (double)(__uint_as_float(xv[u][q] << 16) * __uint_as_float(w[u][q] << 16));
-            s[1] += (double)(__uint_as_float(xv[u][q] & 0xffff0000u) * __uint_as_float(w[u][q] & 0xffff0000u));
+            s0 += (double)(__uint_as_float(xv[q] << 16) * __uint_as_float(w[u][q] << 16));
+            s1 += (double)(__uint_as_float(xv[q] & 0xffff0000u) * __uint_as_float(w[u][q] & 0xffff0000u));
           }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = nx[u];
       }
     } else {
       for (int i = lane + 64 * part; i < h; i += 64 * a.parts)
-        s[0] = fma((double)__uint_as_float((uint32_t)x[i] << 16), (double)l4_load(a.R, a.r_dt, (int64_t)e * h + i), s[0]);
+        s0 = fma((double)__uint_as_float((uint32_t)x[i] << 16), (double)l4_load(a.R, a.r_dt, (int64_t)e * h + i), s0);
     }
-    s[0] += s[1];
+    s0 += s1;
 #pragma unroll
-    for (int d = 32; d; d >>= 1) s[0] += __shfl_xor(s[0], d);
-    if (lane == 0) logit[part * a.experts + e] = s[0];
+    for (int d = 32; d; d >>= 1) s0 += __shfl_xor(s0, d);
+    if (lane == 0) logit[part * E + e] = s0;
   }
+  __syncthreads();
   if (a.parts > 1) {
+    if (tid < E)
+      for (int p = 1; p < a.parts; ++p) logit[tid] += logit[p * E + tid];
     __syncthreads();
-    if (tid < a.experts)
-      for (int p = 1; p < a.parts; ++p) logit[tid] += logit[p * a.experts + tid];
+  }
+  // segs threads per expert, each comparing it with every segs-th other
+  int slog = 0;
+  while ((E << (slog + 1)) <= 1024) ++slog;
+  for (int i = tid; i < E << slog; i += 1024) {
+    const int e = i >> slog;
+    const double mine = logit[e];
+    int before = 0;
+    for (int o = i & ((1 << slog) - 1); o < E; o += 1 << slog) before += o != e && moe_before(logit[o], o, mine, e);
+    if (before) atomicAdd(&rank[e], before);
   }
   __syncthreads();
-  if (wave == 0) moe_choose(a, logit, t, chosen_ids);
+  for (int e = tid; e < E; e += 1024)
+    if (rank[e] < a.top_k) chosen[rank[e]] = e;
   __syncthreads();
+  const double top = logit[chosen[0]];
+  if (!a.renorm) {   // the sum over all experts, wave by wave
+    double s = 0.0;
+    for (int e = tid; e < E; e += 1024) s += exp(logit[e] - top);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+    if (lane == 0) total[wave] = s;
+    __syncthreads();
+  }
+  if (wave == 0) {
+    const double mine = lane < a.top_k ? exp(logit[chosen[lane]] - top) : 0.0;
+    double sum = 0.0;
+    if (a.renorm) {
+      sum = mine;
+#pragma unroll
+      for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    } else {
+      for (int v = 0; v < 16; ++v) sum += total[v];
+    }
+    if (lane < a.top_k) {
+      const float wt = (float)(mine / sum);
+      const int64_t at = t * a.top_k + lane;
+      a.ids[at] = chosen[lane];
+      a.wts[at] = wt;
+      if (a.ids_out) a.ids_out[at] = chosen[lane];
+      if (a.wts_out) a.wts_out[at] = wt;
+    }
+  }
   // the token in the column order of each of its experts
   const int quarter = (int)(a.n128 / 4);
   for (int i = tid; i < a.top_k * quarter; i += 1024) {
     const int j = i / quarter, p = 4 * (i % quarter);
-    const int4 o = *reinterpret_cast<const int4*>(a.packed + chosen_ids[j] * a.stride + a.order_off + (int64_t)p * 4);
+    const int4 o = *reinterpret_cast<const int4*>(a.packed + chosen[j] * a.stride + a.order_off + (int64_t)p * 4);
     const uint32_t v0 = x[std::max(o.x, 0)], v1 = x[std::max(o.y, 0)], v2 = x[std::max(o.z, 0)], v3 = x[std::max(o.w, 0)];
     uint2 v;
     v.x = (o.x >= 0 ? v0 : 0u) | (o.y >= 0 ? v1 : 0u) << 16;
@@ -451,7 +460,8 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
     r.order_off = (int64_t)L.gu.order_off;
     r.n128 = L.gu.n128;
     r.Xp = Xp;
-    const size_t rlds = (size_t)round_up((int64_t)r.parts * cfg.experts, 2) * sizeof(double) + (size_t)round_up(h, 8) * 2;
+    const size_t rlds = (size_t)round_up((int64_t)r.parts * cfg.experts, 2) * sizeof(double) +
+                        (size_t)round_up(cfg.experts, 4) * sizeof(int) + (size_t)round_up(h, 8) * 2;
     if (rlds > 65536)
       GPTQ_HIP_CHECK(hipFuncSetAttribute((const void*)moe_router_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)rlds));
     hipLaunchKernelGGL(moe_router_kernel, dim3((unsigned)tk), dim3(1024), rlds, stream, r);

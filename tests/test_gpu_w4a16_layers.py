@@ -56,6 +56,11 @@ LINEAR = [
     (513, 513, 257, 4, 64, False, "relu", "", "bf16", "bf16"),
     (1024, 256, 1024, 4, 128, True, "none", "", "", "fp32"),
     (4103, 20, 96, 4, 32, True, "none", "bf16", "", "fp32"),     # more than one launch sequence
+    (1, 17, 90001, 4, 128, True, "none", "", "bf16", "fp32"),    # one token's row beyond LDS
+    (3, 40, 33000, 4, 64, True, "none", "", "", "fp32"),
+    (7, 64, 11008, 4, 128, True, "silu", "", "", "fp32"),
+    (14, 33, 4096, 4, 32, True, "none", "bf16", "", "bf16"),
+    (100, 16, 40000, 4, -1, True, "none", "", "", "fp32"),
 ]
 
 
@@ -239,6 +244,9 @@ MOE = [
     (64, 2, 1, 515, 200, 4, 64, True, "silu", True, "bf16", "bf16", "bf16"),
     (70, 12, 4, 256, 140, 4, 32, True, "silu", True, "", "fp32", "bf16"),        # more than one launch sequence
     (7, 200, 3, 64, 32, 4, 32, True, "silu", True, "", "fp32", "bf16"),          # several words of expert bits
+    (2, 1024, 64, 40, 16, 4, 32, False, "relu", False, "", "fp32", "bf16"),      # the largest counts
+    (3, 4, 1, 8200, 48, 4, 128, True, "silu", True, "", "fp32", "bf16"),
+    (20, 3, 2, 4104, 1500, 4, 64, True, "silu", True, "bf16", "bf16", "bf16"),   # a pass that LDS does not hold
 ]
 
 
