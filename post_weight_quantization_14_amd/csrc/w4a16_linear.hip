@@ -130,7 +130,7 @@ struct L4DecodeArgs {
   L4Epilogue ep;
 };
 
-// Few tokens whose X' fits in LDS.  Unit = one row tile (linear) or one
+// Few tokens: 16 (grid y) whose X' fits in LDS.  Unit = one row tile (linear) or one
 // gate/up pair of tiles (glu).  X' is gathered here (GATHER) or copied from X'
 // in memory.
 template <int GS, bool GATED, bool GATHER>
@@ -139,32 +139,34 @@ __global__ __launch_bounds__(kL4Threads) void l4_decode_kernel(L4DecodeArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63;
   const int xrow = (int)a.n128 + kL4Pad;
+  const int t0 = blockIdx.y * 16, tokens = std::min(16, a.tokens - t0);
   uint16_t* xsh = reinterpret_cast<uint16_t*>(lds);
-  uint8_t* rest = lds + (size_t)a.tokens * xrow * 2;
+  uint8_t* rest = lds + (size_t)std::min(16, a.tokens) * xrow * 2;
   float* red = reinterpret_cast<float*>(rest);   // after the gather, over its raw rows
   auto fill = [&] {
     if (GATHER) {
-      l4_gather_lds(a.X, a.ldx, (int)a.n, a.vec, a.order, (int)a.n128, a.tokens, a.batch, xsh, rest);
+      l4_gather_lds(a.X + t0 * a.ldx, a.ldx, (int)a.n, a.vec, a.order, (int)a.n128, tokens, a.batch, xsh, rest);
     } else {
       const int pieces = (int)(a.n128 / 8);
-      for (int i = threadIdx.x; i < a.tokens * pieces; i += kL4Threads)
+      const uint16_t* xp = a.Xp + t0 * a.n128;
+      for (int i = threadIdx.x; i < tokens * pieces; i += kL4Threads)
         *reinterpret_cast<uint4*>(xsh + (i / pieces) * xrow + 8 * (i % pieces)) =
-            *reinterpret_cast<const uint4*>(a.Xp + (int64_t)(i / pieces) * a.n128 + 8 * (i % pieces));
+            *reinterpret_cast<const uint4*>(xp + (int64_t)(i / pieces) * a.n128 + 8 * (i % pieces));
       __syncthreads();
     }
   };
   const int upw = kL4Waves >> a.st.kslog;
   auto end = [&](int64_t unit, const f32x4_t (&y)[RT]) {
-    l4_finish<RT>(red, a.quads, a.tokens, a.st.kslog, unit, y, [&](int64_t u, int t, int row, const float (&z)[RT]) {
+    l4_finish<RT>(red, a.quads, tokens, a.st.kslog, unit, y, [&](int64_t u, int t, int row, const float (&z)[RT]) {
       const int64_t r = u * kL4Rows + row;
       if (u >= a.st.units || r >= a.m) return;
       if (GATED)
-        a.ep.gated(t, r, z[0], z[RT - 1]);
+        a.ep.gated(t0 + t, r, z[0], z[RT - 1]);
       else
-        a.ep.linear(t, r, z[0]);
+        a.ep.linear(t0 + t, r, z[0]);
     });
   };
-  const int t = std::min(lane & 15, a.tokens - 1);   // rows past the last: computed, not stored
+  const int t = std::min(lane & 15, tokens - 1);   // rows past the last: computed, not stored
   // batches that leave the wave within 128 registers (16 waves on a CU)
   constexpr int B = GATED ? (GS == 1 ? 1 : 2) : (GS == 4 ? 4 : GS == 2 ? 3 : 2);
   const L4LdsA af{xsh + t * xrow + 8 * (lane >> 4), 0};
@@ -593,22 +595,25 @@ L4Shape l4_shape(int64_t tokens, int64_t packed_rows, int64_t kc) {
   return s;
 }
 constexpr size_t kL4GatherLds = 65536;    // rows up to 32768 columns are gathered through LDS
-constexpr int64_t kL4DecodeTokens = 16;   // up to here the decode kernel, if X' fits in LDS
+// the decode kernel's tiles of 16 tokens, for more than one of them only while
+// tokens x weight is two rounds of workgroups (1024 x 1024, 64 tokens: 13.3 us
+// by the tiled product and its launches, 10 us here)
+constexpr int64_t kL4DecodeWgs = 512;
 constexpr int64_t kL4GatherMax = 65536;   // up to this many elements of X' it gathers them itself
 constexpr size_t kL4MaxLds = 158 * 1024;
 constexpr int64_t kL4Cus = 256;
 
 template <int GS, bool GATED>
-gptq_status launch_l4_source(const L4DecodeArgs& d, bool gather, unsigned grid, size_t lds, hipStream_t stream) {
+gptq_status launch_l4_source(const L4DecodeArgs& d, bool gather, dim3 grid, size_t lds, hipStream_t stream) {
   const void* fn = gather ? (const void*)l4_decode_kernel<GS, GATED, true> : (const void*)l4_decode_kernel<GS, GATED, false>;
   if (lds > 65536) GPTQ_HIP_CHECK(hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
   L4DecodeArgs args = d;
   void* argv[] = {&args};
-  GPTQ_HIP_CHECK(hipLaunchKernel(fn, dim3(grid), dim3(kL4Threads), argv, lds, stream));
+  GPTQ_HIP_CHECK(hipLaunchKernel(fn, grid, dim3(kL4Threads), argv, lds, stream));
   return GPTQ_OK;
 }
 
-gptq_status launch_l4_decode(const L4DecodeArgs& d, int gs, bool gated, bool gather, unsigned grid, size_t lds,
+gptq_status launch_l4_decode(const L4DecodeArgs& d, int gs, bool gated, bool gather, dim3 grid, size_t lds,
                              hipStream_t stream) {
   switch (gs) {
     case 1: return gated ? launch_l4_source<1, true>(d, gather, grid, lds, stream) : launch_l4_source<1, false>(d, gather, grid, lds, stream);
@@ -695,15 +700,17 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
     L4DecodeArgs d;
     bool decode = false, gather = false;
     size_t dlds = 0;
-    if (tk <= kL4DecodeTokens) {
-      d.quads = (int)ceil_div(tk, 4);
-      const size_t rows = (size_t)tk * (size_t)(L.n128 + kL4Pad) * 2;
+    const int64_t ttiles = ceil_div(tk, 16);
+    if (ttiles == 1 || ttiles * st.units <= kL4DecodeWgs) {
+      const int64_t tt = std::min<int64_t>(tk, 16);   // tokens of a tile
+      d.quads = (int)ceil_div(tt, 4);
+      const size_t rows = (size_t)tt * (size_t)(L.n128 + kL4Pad) * 2;
       const size_t red = (size_t)kL4Waves * (gated ? 2 : 1) * d.quads * 64 * sizeof(float);
       const size_t raw = (size_t)round_up(L.n * 2, 16);
       decode = rows + red <= kL4MaxLds;
       if (decode) {
-        d.batch = (int)std::min<int64_t>(tk, (int64_t)((kL4MaxLds - rows) / raw));
-        gather = 2 * d.batch >= tk && tk * L.n128 <= kL4GatherMax;
+        d.batch = (int)std::min<int64_t>(tt, (int64_t)((kL4MaxLds - rows) / raw));
+        gather = 2 * d.batch >= tt && tt * L.n128 <= kL4GatherMax;
         dlds = rows + std::max(red, gather ? raw * (size_t)d.batch : 0);
       }
     }
@@ -736,14 +743,14 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
       d.tokens = (int)tk;
       d.vec = vec;
       d.ep = ep;
-      const int64_t wgs = std::min<int64_t>(st.units, kL4Cus);
+      const int64_t wgs = std::min<int64_t>(st.units, std::max<int64_t>(1, kL4Cus / ttiles));
       const L4Split sp = l4_split(st.units, wgs, L.kc);
       st.kslog = sp.kslog;
       st.rounds = sp.rounds;
       d.st = st;
       // workgroups that the split leaves without units are not launched
       const unsigned grid = (unsigned)std::min<int64_t>(wgs, ceil_div(st.units, kL4Waves >> sp.kslog));
-      GPTQ_TRY(launch_l4_decode(d, gs, gated, gather, grid, dlds, stream));
+      GPTQ_TRY(launch_l4_decode(d, gs, gated, gather, dim3(grid, (unsigned)ttiles), dlds, stream));
       continue;
     }
     const L4Shape sh = l4_shape(tk, L.mt * kL4Rows, L.kc);

@@ -49,6 +49,79 @@ __device__ __forceinline__ bool moe_before(double a, int ia, double b, int ib) {
   return ia < ib;
 }
 
+// One logit in 64 bits by one wave: `part` of `parts` interleaved 512-element
+// pieces, four pieces in flight.
+__device__ __forceinline__ double moe_logit(const uint16_t* x, const void* R, int r_dt, int vec, int64_t e, int h,
+                                            int part, int parts) {
+  const int lane = threadIdx.x & 63;
+  double s0 = 0.0, s1 = 0.0;
+  if (vec && r_dt == GPTQ_BF16) {
+    const uint16_t* r = static_cast<const uint16_t*>(R) + e * h;
+    for (int b = 512 * part; b < h; b += 2048 * parts) {
+      u32x4_t w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = b + 512 * parts * u + 8 * lane;
+        w[u] = *reinterpret_cast<const u32x4_t*>(r + (k < h ? k : 0));
+        if (k >= h) w[u] = u32x4_t{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = b + 512 * parts * u + 8 * lane;
+        const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(x + (k < h ? k : 0));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {   // bf16·bf16: exact in fp32
+          s0 += (double)(__uint_as_float(xv[q] << 16) * __uint_as_float(w[u][q] << 16));
+          s1 += (double)(__uint_as_float(xv[q] & 0xffff0000u) * __uint_as_float(w[u][q] & 0xffff0000u));
+        }
+      }
+    }
+  } else if (vec) {
+    const float* r = static_cast<const float*>(R) + e * h;
+    for (int b = 512 * part; b < h; b += 1024 * parts) {
+      f32x4_t w[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int k = b + 512 * parts * u + 8 * lane;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          w[u][q] = *reinterpret_cast<const f32x4_t*>(r + (k < h ? k : 0) + 4 * q);
+          if (k >= h) w[u][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int k = b + 512 * parts * u + 8 * lane;
+        const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(x + (k < h ? k : 0));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          s0 = fma((double)__uint_as_float(xv[q] << 16), (double)w[u][q >> 1][2 * (q & 1)], s0);
+          s1 = fma((double)__uint_as_float(xv[q] & 0xffff0000u), (double)w[u][q >> 1][2 * (q & 1) + 1], s1);
+        }
+      }
+    }
+  } else {
+    for (int b = 64 * part; b < h; b += 256 * parts) {
+      float w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = b + 64 * parts * u + lane;
+        w[u] = l4_load(R, r_dt, e * h + (i < h ? i : 0));
+        if (i >= h) w[u] = 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = b + 64 * parts * u + lane;
+        s0 = fma((double)__uint_as_float((uint32_t)x[i < h ? i : 0] << 16), (double)w[u], s0);
+      }
+    }
+  }
+  s0 += s1;
+#pragma unroll
+  for (int d = 32; d; d >>= 1) s0 += __shfl_xor(s0, d);
+  return s0;
+}
+
 // One workgroup per token.  The logits are summed in 64 bits: which experts
 // are chosen hangs on the last bits of the k-th and the next, and a choice
 // that falls the other way is no rounding error in the result.  `parts` waves
@@ -105,13 +178,12 @@ __global__ __launch_bounds__(1024) void moe_router_kernel(MoeRouterArgs a) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) w[u] = nx[u];
       }
-    } else {
-      for (int i = lane + 64 * part; i < h; i += 64 * a.parts)
-        s0 = fma((double)__uint_as_float((uint32_t)x[i] << 16), (double)l4_load(a.R, a.r_dt, (int64_t)e * h + i), s0);
-    }
-    s0 += s1;
+      s0 += s1;
 #pragma unroll
-    for (int d = 32; d; d >>= 1) s0 += __shfl_xor(s0, d);
+      for (int d = 32; d; d >>= 1) s0 += __shfl_xor(s0, d);
+    } else {
+      s0 = moe_logit(x, a.R, a.r_dt, a.vec, e, h, part, a.parts);
+    }
     if (lane == 0) logit[part * E + e] = s0;
   }
   __syncthreads();
@@ -228,6 +300,21 @@ struct MoeExpertArgs {
   float* out;                 // down's result [pairs][rows]
 };
 
+// act(gate)·up of one pair and row.  It leaves as 2 or 3 bf16 parts (16 or 24
+// significant bits, for a bf16 or an fp32 result), so it adds no rounding of
+// its own; a single bf16 would add as much error as the result's rounding.
+template <int RT>
+__device__ __forceinline__ void moe_hidden(const MoeExpertArgs& a, int64_t pair, int64_t r, const float (&z)[RT]) {
+  float v = l4_activate(z[0], a.act) * z[RT - 1];
+  uint16_t* o = a.mid + pair * a.planes * a.rows + r;
+  for (int p = 0; p < a.planes; ++p) {
+    const uint16_t part = l4_bf16(v);
+    const float f = __uint_as_float((uint32_t)part << 16);
+    o[p * a.rows] = part;
+    v = isfinite(f) ? v - f : 0.f;
+  }
+}
+
 // A workgroup's share of one expert's units, NP planes of A per token.  LDS:
 // the rows of a pass are copied into LDS, else every fragment is read from
 // memory.  GATE_UP: RT = 2, act(gate)·up to `mid`; else to `out`.
@@ -266,18 +353,7 @@ __device__ __forceinline__ void moe_expert_units(const MoeExpertArgs& a, MoeList
         const int64_t r = u * kL4Rows + row, pair = list.pair[p0 + q];
         if (u >= st.units || r >= a.rows) return;
         if (GATE_UP) {
-          // The hidden activation leaves as 2 or 3 bf16 parts (16 or 24
-          // significant bits, for a bf16 or an fp32 result), so it adds no
-          // rounding of its own; a single bf16 would add as much error as the
-          // result's rounding.
-          float v = l4_activate(z[0], a.act) * z[RT - 1];
-          uint16_t* o = a.mid + pair * a.planes * a.rows + r;
-          for (int p = 0; p < a.planes; ++p) {
-            const uint16_t part = l4_bf16(v);
-            const float f = __uint_as_float((uint32_t)part << 16);
-            o[p * a.rows] = part;
-            v = isfinite(f) ? v - f : 0.f;
-          }
+          moe_hidden(a, pair, r, z);
         } else {
           a.out[pair * a.rows + r] = z[0];
         }
@@ -308,6 +384,267 @@ __global__ __launch_bounds__(kL4Threads) void moe_down_kernel(MoeExpertArgs a) {
   moe_expert_units<GS, false, NP, LDS>(a, list, lds);
 }
 
+// ---------------------------------------------------------------- a token or a few: two launches
+// While the router's work is small (tokens x experts x hidden), every
+// gate/up workgroup does all of it for itself and gathers its expert's tokens,
+// and the down kernel adds all experts of a row tile: two launches instead of
+// four, with no pass of ids, X' or pair results through memory between them.
+constexpr int kSmallTokens = 16;
+constexpr int kSmallPairs = 64;
+constexpr int kSmallLogits = 512;
+
+struct MoeSmallArgs {
+  MoeExpertArgs x;        // gate/up: A unused; down: the combine's part below
+  const uint16_t* X;
+  int64_t ldx, order_off;
+  int hidden, renorm, vec, xvec, r_dt;
+  const void* R;
+  int32_t *ids, *ids_out;
+  float *wts, *wts_out;
+};
+
+template <int GS>
+__global__ __launch_bounds__(kL4Threads) void moe_small_gate_up_kernel(MoeSmallArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ MoeList list;
+  __shared__ double logit[kSmallLogits];
+  __shared__ double part_sum[16];
+  __shared__ int rank[kSmallLogits];
+  __shared__ int32_t ids[kSmallPairs];
+  const MoeExpertArgs& g = a.x;
+  const int T = g.tokens, E = g.experts, K = g.top_k, h = a.hidden, hrow = (h + 7) & ~7;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int xrow = (int)g.k128 + kL4Pad;
+  uint16_t* xsh = reinterpret_cast<uint16_t*>(lds);                    // X' [pass][xrow]
+  uint16_t* raw = xsh + (size_t)g.pass * xrow;                         // X [T][hrow]
+  float* red = reinterpret_cast<float*>(raw);                          // after the gather
+  for (int t = 0; t < T; ++t)
+    l4_row_to_lds(a.X + t * a.ldx, h, a.xvec, reinterpret_cast<uint8_t*>(raw + t * hrow), tid, kL4Threads);
+  const int pairs = T * E;
+  for (int i = tid; i < pairs; i += kL4Threads) rank[i] = 0;
+  __syncthreads();
+  int parts = 1;
+  while (parts < 16 && pairs * parts * 2 <= 16) parts *= 2;
+  for (int i = wave / parts; i < pairs; i += 16 / parts) {
+    const int t = i / E, e = i - t * E, part = wave % parts;
+    const double s = moe_logit(raw + t * hrow, a.R, a.r_dt, a.vec, e, h, part, parts);
+    if (lane == 0) {
+      if (parts == 1)
+        logit[i] = s;
+      else
+        part_sum[wave] = s;   // pairs * parts <= 16: each wave has one
+    }
+  }
+  __syncthreads();
+  if (parts > 1) {
+    if (tid < pairs) {
+      double s = part_sum[tid * parts];
+      for (int p = 1; p < parts; ++p) s += part_sum[tid * parts + p];
+      logit[tid] = s;
+    }
+    __syncthreads();
+  }
+  int slog = 0;
+  while ((pairs << (slog + 1)) <= kL4Threads && (1 << slog) < E) ++slog;
+  for (int i = tid; i < pairs << slog; i += kL4Threads) {
+    const int at = i >> slog, t = at / E, e = at - t * E;
+    const double mine = logit[at];
+    int before = 0;
+    for (int o = i & ((1 << slog) - 1); o < E; o += 1 << slog)
+      before += o != e && moe_before(logit[t * E + o], o, mine, e);
+    if (before) atomicAdd(&rank[at], before);
+  }
+  __syncthreads();
+  if (tid < pairs && rank[tid] < K) ids[(tid / E) * K + rank[tid]] = tid % E;
+  __syncthreads();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && wave < T) {   // one workgroup leaves them for the down kernel
+    const double* lg = logit + wave * E;
+    const double top = lg[ids[wave * K]];
+    const double mine = lane < K ? exp(lg[ids[wave * K + lane]] - top) : 0.0;
+    double sum = mine;
+    if (!a.renorm) {
+      sum = 0.0;
+      for (int e = lane; e < E; e += 64) sum += exp(lg[e] - top);
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    if (lane < K) {
+      const int at = wave * K + lane;
+      const float wt = (float)(mine / sum);
+      a.ids[at] = ids[at];
+      a.wts[at] = wt;
+      if (a.ids_out) a.ids_out[at] = ids[at];
+      if (a.wts_out) a.wts_out[at] = wt;
+    }
+  }
+  const int e = __builtin_amdgcn_readfirstlane(moe_expert(ids, T, K, E, blockIdx.y, list));
+  if (e < 0) return;
+  const char* blob = g.packed + e * g.stride;
+  L4Stream st = g.st;
+  st.codes = reinterpret_cast<const u32x4_t*>(blob + g.code_off);
+  st.params = reinterpret_cast<const float2*>(blob + g.param_off);
+  const int np = list.count;   // at most the pass: one pass
+  auto fill = [&] {
+    const int32_t* order = reinterpret_cast<const int32_t*>(blob + a.order_off);
+    for (int p = 4 * tid; p < (int)g.k128; p += 4 * kL4Threads) {
+      const int4 o = *reinterpret_cast<const int4*>(order + p);
+      for (int q = 0; q < np; ++q) {
+        const uint16_t* x = raw + (list.pair[q] / K) * hrow;
+        const uint32_t v0 = x[std::max(o.x, 0)], v1 = x[std::max(o.y, 0)], v2 = x[std::max(o.z, 0)], v3 = x[std::max(o.w, 0)];
+        uint2 v;
+        v.x = (o.x >= 0 ? v0 : 0u) | (o.y >= 0 ? v1 : 0u) << 16;
+        v.y = (o.z >= 0 ? v2 : 0u) | (o.w >= 0 ? v3 : 0u) << 16;
+        *reinterpret_cast<uint2*>(xsh + q * xrow + p) = v;
+      }
+    }
+    __syncthreads();
+  };
+  auto end = [&](int64_t unit, const f32x4_t (&y)[2]) {
+    l4_finish<2>(red, g.quads, np, st.kslog, unit, y, [&](int64_t u, int q, int row, const float (&z)[2]) {
+      if (u < st.units) moe_hidden(g, list.pair[q], u * kL4Rows + row, z);
+    });
+  };
+  const int upw = kL4Waves >> st.kslog, q = std::min(lane & 15, np - 1);
+  const L4LdsA af{xsh + q * xrow + 8 * (lane >> 4), 0};
+  l4_units<GS, 2, 1, (GS == 1 ? 1 : 2), false>(st, (int64_t)blockIdx.x * upw, (int64_t)gridDim.x * upw, af, fill, end);
+}
+
+struct MoeSmallDownArgs {
+  MoeExpertArgs x;
+  const float* wts;
+  const void* res;
+  int res_dt, y_dt;
+  int64_t ldr, ldy;
+  void* Y;
+};
+
+// Y = Σ over the active experts, in ascending order, of w·(down product) +
+// residual.  A workgroup takes row tiles; its 16 waves share the chunks of all
+// active experts, laid end to end, in equal runs; where a run passes from one
+// expert to the next the sums so far are weighted and put by.
+template <int GS, int NP>
+__global__ __launch_bounds__(kL4Threads) void moe_small_down_kernel(MoeSmallDownArgs a) {
+  constexpr int NG = 4 / GS, B = GS == 4 ? 4 : 2;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ uint32_t used[kMoeMaxExperts / 32];
+  __shared__ int expert[kSmallPairs];
+  __shared__ int active;
+  __shared__ __attribute__((aligned(16))) float weight[kSmallPairs][16];    // [slot][token]
+  __shared__ __attribute__((aligned(16))) int pair_of[kSmallPairs][16];     // the token's pair, -1: it did not choose the expert
+  const MoeExpertArgs& g = a.x;
+  const int T = g.tokens, K = g.top_k;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int xrow = (int)g.k128 + kL4Pad;
+  uint16_t* xsh = reinterpret_cast<uint16_t*>(lds);                                    // [pairs][NP][xrow]
+  float* red = reinterpret_cast<float*>(xsh + (size_t)T * K * NP * xrow);
+  if (tid < kMoeMaxExperts / 32) used[tid] = 0;
+  for (int i = tid; i < kSmallPairs * 16; i += kL4Threads) {
+    (&weight[0][0])[i] = 0.f;
+    (&pair_of[0][0])[i] = -1;
+  }
+  __syncthreads();
+  const int my = tid < T * K ? g.ids[tid] : 0;
+  if (tid < T * K) atomicOr(&used[my >> 5], 1u << (my & 31));
+  const int pieces = (int)(g.k128 / 8);
+  for (int i = tid; i < T * K * NP * pieces; i += kL4Threads)
+    *reinterpret_cast<uint4*>(xsh + (i / pieces) * xrow + 8 * (i % pieces)) =
+        *reinterpret_cast<const uint4*>(g.A + (int64_t)(i / pieces) * g.k128 + 8 * (i % pieces));
+  __syncthreads();
+  if (tid < T * K) {
+    int slot = __popc(used[my >> 5] & ((1u << (my & 31)) - 1u));
+    for (int w = 0; w < (my >> 5); ++w) slot += __popc(used[w]);
+    expert[slot] = my;
+    weight[slot][tid / K] = a.wts[tid];
+    pair_of[slot][tid / K] = tid;
+  }
+  if (tid == 0) {
+    int n = 0;
+    for (int w = 0; w < (g.experts + 31) / 32; ++w) n += __popc(used[w]);
+    active = n;
+  }
+  __syncthreads();
+  const int kc = (int)g.st.kc, total = active * kc, per = (total + 15) / 16;
+  const int i0 = std::min(total, wave * per), i1 = std::min(total, i0 + per);
+  const L4Consts k;
+  struct Batch {
+    u32x4_t cw[B];
+    float2 p[B][NG];
+  };
+  auto load = [&](int64_t unit, int i, int n, Batch& b) {   // n >= 1 chunks from item i of one slot
+    const int slot = i / kc, c = i - slot * kc;
+    const char* blob = g.packed + (int64_t)__builtin_amdgcn_readfirstlane(expert[slot]) * g.stride;
+    const u32x4_t* cp = reinterpret_cast<const u32x4_t*>(blob + g.code_off) + unit * kc * 64 + lane;
+    const float2* pp = reinterpret_cast<const float2*>(blob + g.param_off) + unit * g.st.Gp * kL4Rows + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      const int cc = c + std::min(j, n - 1);
+      b.cw[j] = cp[(int64_t)cc * 64];
+#pragma unroll
+      for (int q = 0; q < NG; ++q) b.p[j][q] = pp[(int64_t)(cc * NG + q) * g.st.pmul];
+    }
+  };
+  // chunks of a batch from item i: up to B, within the slot and the run
+  auto count = [&](int i) { return std::min(std::min(B, i1 - i), kc - i % kc); };
+  f32x4_t y[1];
+  const int64_t first = blockIdx.x, step = gridDim.x;
+  Batch cur, nxt;
+  if (i0 < i1) load(std::min<int64_t>(first, g.st.units - 1), i0, count(i0), cur);
+  for (int r = 0; r < g.st.rounds; ++r) {
+    const int64_t unit = first + r * step;
+    y[0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    f32x4_t z = {0.f, 0.f, 0.f, 0.f};
+    for (int i = i0; i < i1;) {
+      const int n = count(i), slot = i / kc, c = i - slot * kc;
+      const bool more = i + n < i1;
+      const int ni = more ? i + n : i0;
+      load(std::min<int64_t>(more ? unit : unit + step, g.st.units - 1), ni, count(ni), nxt);
+      const uint16_t* row = xsh + (size_t)std::max(pair_of[slot][lane & 15], 0) * NP * xrow + 8 * (lane >> 4);
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        if (j >= n) break;
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+          f32x4_t sx = {0.f, 0.f, 0.f, 0.f}, acc = {0.f, 0.f, 0.f, 0.f};
+          const float s = cur.p[j][q].x, y0 = cur.p[j][q].y;
+#pragma unroll
+          for (int st = q * GS; st < q * GS + GS; ++st) {
+            const bf16x8_t w = NP == 3 ? k.unpack_centred(cur.cw[j][st], 16.f + l4_centre(y0)) : k.unpack(cur.cw[j][st]);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+              const bf16x8_t av = __builtin_bit_cast(
+                  bf16x8_t, *reinterpret_cast<const uint4*>(row + p * xrow + (c + j) * kL4Chunk + 32 * st));
+              sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, k.ones(), sx, 0, 0, 0);
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, w, acc, 0, 0, 0);
+            }
+          }
+          const float zp = NP == 3 ? y0 - 128.f - l4_centre(y0) : l4_zero(y0);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) z[v] = fmaf(s, fmaf(-zp, sx[v], acc[v]), z[v]);
+        }
+      }
+      i += n;
+      if (i >= i1 || i % kc == 0) {   // the run leaves this expert
+        const f32x4_t wt = *reinterpret_cast<const f32x4_t*>(&weight[slot][4 * (lane >> 4)]);
+        const int4 po = *reinterpret_cast<const int4*>(&pair_of[slot][4 * (lane >> 4)]);
+        const int chose[4] = {po.x, po.y, po.z, po.w};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) y[0][v] = chose[v] >= 0 ? fmaf(wt[v], z[v], y[0][v]) : y[0][v];
+        z = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+      cur = nxt;
+    }
+    l4_finish<1>(red, g.quads, T, 4, unit + wave / 16, y, [&](int64_t u, int t, int row, const float (&v)[1]) {
+      const int64_t c = u * kL4Rows + row;
+      if (u >= g.st.units || c >= g.rows) return;
+      float o = v[0];
+      if (a.res) o += l4_load(a.res, a.res_dt, t * a.ldr + c);
+      l4_store(a.Y, a.y_dt, t * a.ldy + c, o);
+    });
+  }
+}
+
 __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restrict__ pairs, const float* __restrict__ wts,
                                                           int top_k, int64_t hidden, const void* res, int res_dt,
                                                           int64_t ldr, void* Y, int y_dt, int64_t ldy) {
@@ -319,6 +656,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
   l4_store(Y, y_dt, t * ldy + r, v);
 }
 
+constexpr int64_t kSmallRouter = 65536;       // logit products that every workgroup repeats
 constexpr size_t kMoeMaxLds = 120 * 1024;   // beyond: fragments from memory
 
 // fills the launch-dependent fields; returns the dynamic LDS bytes, 0 < lds
@@ -333,6 +671,23 @@ size_t moe_plan(MoeExpertArgs& a, int tokens, int planes, int rt, int64_t wgs, b
   const size_t rows = (size_t)a.pass * planes * (size_t)(a.k128 + kL4Pad) * 2;
   *in_lds = rows + red <= kMoeMaxLds;
   return *in_lds ? rows + red : red;
+}
+
+// Whether a call of `tokens` tokens takes the two-launch form.
+bool moe_is_small(const gptq_moe_config& c, int64_t tokens, int planes, const MoeLayout& L) {
+  const size_t x = (size_t)tokens * (size_t)(L.gu.n128 + kL4Pad) * 2 + (size_t)tokens * (size_t)round_up(c.hidden, 8) * 2;
+  const size_t mid = (size_t)(tokens * c.top_k * planes) * (size_t)(L.f128 + kL4Pad) * 2;
+  return tokens <= kSmallTokens && tokens * c.top_k <= kSmallPairs && tokens * c.experts <= kSmallLogits &&
+         tokens * c.experts * c.hidden <= kSmallRouter && x <= 64 * 1024 && mid <= 100 * 1024;
+}
+
+template <class A, class K>
+gptq_status moe_launch_any(K kernel, dim3 grid, size_t lds, const A& a, hipStream_t stream) {
+  if (lds > 32768)
+    GPTQ_HIP_CHECK(hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
+  hipLaunchKernelGGL(kernel, grid, dim3(kL4Threads), lds, stream, a);
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
 }
 
 template <class K>
@@ -460,6 +815,66 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
     r.order_off = (int64_t)L.gu.order_off;
     r.n128 = L.gu.n128;
     r.Xp = Xp;
+    const void* res = c.res ? (const void*)(static_cast<const char*>(c.res) + (size_t)(t0 * c.ldr) * rsz) : nullptr;
+    void* Y = static_cast<char*>(c.Y) + (size_t)(t0 * c.ldy) * ysz;
+    // the workgroups of the GPU dealt over the experts that can be active
+    const int64_t slots = std::min<int64_t>(cfg.experts, (int64_t)tk * cfg.top_k);
+    const int64_t share = std::max<int64_t>(1, 256 / slots);
+    const int64_t gw = std::min<int64_t>(share, g.st.units), dw = std::min<int64_t>(share, d.st.units);
+    g.tokens = d.tokens = tk;
+    bool in_lds = false;
+    size_t lds = moe_plan(g, tk, 1, 2, gw, &in_lds);
+    const dim3 ggrid((unsigned)std::min<int64_t>(gw, ceil_div(g.st.units, kL4Waves >> g.st.kslog)), (unsigned)slots);
+    if (moe_is_small(cfg, tk, g.planes, L)) {
+      MoeSmallArgs sa;
+      sa.x = g;
+      sa.X = r.X;
+      sa.ldx = c.ldx;
+      sa.order_off = r.order_off;
+      sa.hidden = h;
+      sa.renorm = cfg.renormalize;
+      sa.vec = r.vec;
+      sa.xvec = r.xvec;
+      sa.r_dt = c.router_dtype;
+      sa.R = c.router;
+      sa.ids = ids;
+      sa.wts = wts;
+      sa.ids_out = r.ids_out;
+      sa.wts_out = r.wts_out;
+      const size_t rows = (size_t)g.pass * (size_t)(g.k128 + kL4Pad) * 2;
+      const size_t raw = (size_t)tk * (size_t)round_up(h, 8) * 2, red = (size_t)kL4Waves * 2 * g.quads * 64 * sizeof(float);
+      lds = rows + std::max(raw, red);
+      switch (steps(L.gu)) {
+        case 1: GPTQ_TRY(moe_launch_any(moe_small_gate_up_kernel<1>, ggrid, lds, sa, stream)); break;
+        case 2: GPTQ_TRY(moe_launch_any(moe_small_gate_up_kernel<2>, ggrid, lds, sa, stream)); break;
+        default: GPTQ_TRY(moe_launch_any(moe_small_gate_up_kernel<4>, ggrid, lds, sa, stream)); break;
+      }
+      MoeSmallDownArgs sd;
+      sd.x = d;
+      sd.wts = wts;
+      sd.res = res;
+      sd.res_dt = c.res_dtype;
+      sd.y_dt = c.y_dtype;
+      sd.ldr = c.ldr;
+      sd.ldy = c.ldy;
+      sd.Y = Y;
+      const int64_t wgs = std::min<int64_t>(d.st.units, 256);
+      sd.x.quads = g.quads;
+      sd.x.st.rounds = (int)ceil_div(d.st.units, wgs);
+      lds = (size_t)(tk * cfg.top_k * d.planes) * (size_t)(d.k128 + kL4Pad) * 2 +
+            (size_t)kL4Waves * sd.x.quads * 64 * sizeof(float);
+      const dim3 sgrid((unsigned)wgs);
+#define MOE_SMALL_DOWN(GS)                                                                                       \
+  GPTQ_TRY(d.planes == 3 ? moe_launch_any(moe_small_down_kernel<GS, 3>, sgrid, lds, sd, stream)                  \
+                         : moe_launch_any(moe_small_down_kernel<GS, 2>, sgrid, lds, sd, stream))
+      switch (steps(L.down)) {
+        case 1: MOE_SMALL_DOWN(1); break;
+        case 2: MOE_SMALL_DOWN(2); break;
+        default: MOE_SMALL_DOWN(4); break;
+      }
+#undef MOE_SMALL_DOWN
+      continue;
+    }
     const size_t rlds = (size_t)round_up((int64_t)r.parts * cfg.experts, 2) * sizeof(double) +
                         (size_t)round_up(cfg.experts, 4) * sizeof(int) + (size_t)round_up(h, 8) * 2;
     if (rlds > 65536)
@@ -467,14 +882,6 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
     hipLaunchKernelGGL(moe_router_kernel, dim3((unsigned)tk), dim3(1024), rlds, stream, r);
     GPTQ_LAUNCH_CHECK();
 
-    // the workgroups of the GPU dealt over the experts that can be active
-    const int64_t slots = std::min<int64_t>(cfg.experts, (int64_t)tk * cfg.top_k);
-    const int64_t share = std::max<int64_t>(1, 256 / slots);
-    g.tokens = d.tokens = tk;
-    bool in_lds = false;
-    const int64_t gw = std::min<int64_t>(share, g.st.units), dw = std::min<int64_t>(share, d.st.units);
-    size_t lds = moe_plan(g, tk, 1, 2, gw, &in_lds);
-    const dim3 ggrid((unsigned)std::min<int64_t>(gw, ceil_div(g.st.units, kL4Waves >> g.st.kslog)), (unsigned)slots);
     switch (steps(L.gu)) {
       case 1: GPTQ_TRY(launch_gate_up<1>(ggrid, lds, in_lds, g, stream)); break;
       case 2: GPTQ_TRY(launch_gate_up<2>(ggrid, lds, in_lds, g, stream)); break;
@@ -488,9 +895,8 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
       default: GPTQ_TRY(launch_down<4>(dgrid, lds, in_lds, d, stream)); break;
     }
     hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)ceil_div(cfg.hidden, 256), (unsigned)tk), dim3(256), 0, stream,
-                       (const float*)out, (const float*)wts, (int)cfg.top_k, cfg.hidden,
-                       c.res ? (const void*)(static_cast<const char*>(c.res) + (size_t)(t0 * c.ldr) * rsz) : nullptr,
-                       c.res_dtype, c.ldr, (void*)(static_cast<char*>(c.Y) + (size_t)(t0 * c.ldy) * ysz), c.y_dtype, c.ldy);
+                       (const float*)out, (const float*)wts, (int)cfg.top_k, cfg.hidden, res, c.res_dtype, c.ldr, Y,
+                       c.y_dtype, c.ldy);
     GPTQ_LAUNCH_CHECK();
   }
   return GPTQ_OK;

@@ -7,6 +7,7 @@ GptqError carrying the library's message.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 from typing import Optional
@@ -405,10 +406,10 @@ def _on(X: torch.Tensor, **tensors: Optional[torch.Tensor]) -> None:
     or of the host, would be read by the kernels as it is)."""
     if not X.is_cuda:
         raise ValueError("X must be on the GPU")
-    dev = X.device
+    dev = X.get_device()
     for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, X on {dev}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, X on {X.device}")
 
 
 def _rows(name: str, t: torch.Tensor, rows: int, cols: int) -> int:
@@ -453,12 +454,16 @@ def _uint8(name: str, t: torch.Tensor) -> int:
     return t.nbytes
 
 
-def _scratch(nbytes: int, X: torch.Tensor, workspace: Optional[torch.Tensor]) -> torch.Tensor:
-    """The caller's workspace if it is large enough (it then belongs to this
-    call until its work is done), else a new one."""
-    if workspace is not None and _uint8("workspace", workspace) >= nbytes:
-        return workspace
-    return torch.empty(nbytes, dtype=torch.uint8, device=X.device)
+def _with_workspace(call, nbytes, X: torch.Tensor, workspace: Optional[torch.Tensor], where: str) -> None:
+    """call(pointer, bytes) -> status on the caller's workspace (it then belongs
+    to this call until its work is done), or on a new one of nbytes() bytes if
+    there is none or the library finds it too small."""
+    if workspace is not None:
+        st = call(workspace.data_ptr(), _uint8("workspace", workspace))
+        if st != _lib.GPTQ_ERR_WORKSPACE:
+            return _check(st, where)
+    ws = torch.empty(nbytes(), dtype=torch.uint8, device=X.device)
+    _check(call(ws.data_ptr(), ws.nbytes), where)
 
 
 class _Device:
@@ -471,12 +476,18 @@ class _Device:
 
     def __enter__(self):
         self.was = torch.cuda.current_device()
-        if self.was != self.index:
-            torch.cuda.set_device(self.index)
+        torch.cuda.set_device(self.index)
 
     def __exit__(self, *exc):
-        if self.was != self.index:
-            torch.cuda.set_device(self.was)
+        torch.cuda.set_device(self.was)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _device(X: torch.Tensor):
+    """X's GPU as the current device (nothing to do where it already is)."""
+    return _SAME_DEVICE if X.device.index == torch.cuda.current_device() else _Device(X)
 
 
 def _int32(**tensors: torch.Tensor) -> None:
@@ -521,12 +532,14 @@ def gptq_w4a16_linear(X: torch.Tensor, packed: torch.Tensor, m: int, n: int, gro
     if residual is not None:
         e.ldr = _rows("residual", residual, tokens, m)
         e.residual, e.residual_dtype = residual.data_ptr(), _dtype_code(residual)
-    ws = _scratch(gptq_w4a16_linear_workspace_bytes(tokens, m, n, group_size), X, workspace)
-    with _Device(X):
-        st = lib().gptq_w4a16_linear(X.data_ptr(), tokens, ldx, packed.data_ptr(), _uint8("packed", packed), m, n,
-                                     group_size, ctypes.byref(e), Y.data_ptr(), _dtype_code(Y),
-                                     _rows("Y", Y, tokens, m), ws.data_ptr(), ws.nbytes, _stream_on(X, stream))
-    _check(st, "gptq_w4a16_linear")
+    fn = lib().gptq_w4a16_linear
+    args = (X.data_ptr(), tokens, ldx, packed.data_ptr(), _uint8("packed", packed), m, n, group_size, ctypes.byref(e),
+            Y.data_ptr(), _dtype_code(Y), _rows("Y", Y, tokens, m))
+    s = _stream_on(X, stream)
+    with _device(X):
+        _with_workspace(lambda ws, nbytes: fn(*args, ws, nbytes, s),
+                        lambda: gptq_w4a16_linear_workspace_bytes(tokens, m, n, group_size), X, workspace,
+                        "gptq_w4a16_linear")
     return Y
 
 
@@ -552,7 +565,7 @@ def gptq_w4a16_glu_pack(gate_qweight: torch.Tensor, gate_scales: torch.Tensor, g
     if packed is None:
         packed = torch.empty(max(gptq_w4a16_glu_packed_bytes(m, n, group_size), 1), dtype=torch.uint8,
                              device=gate_qweight.device)
-    with _Device(gate_qweight):
+    with _device(gate_qweight):
         st = lib().gptq_w4a16_glu_pack(_ptr(gate_qweight), _ptr(gate_scales), _ptr(gate_zeros), _ptr(up_qweight),
                                        _ptr(up_scales), _ptr(up_zeros), _ptr(g_idx), m, n, bits, group_size,
                                        _ptr(packed), _uint8("packed", packed), _stream_on(gate_qweight, stream))
@@ -578,14 +591,15 @@ def gptq_w4a16_glu(X: torch.Tensor, packed: torch.Tensor, m: int, n: int, group_
     some = gate_bias if gate_bias is not None else up_bias
     if gate_bias is not None and up_bias is not None and gate_bias.dtype != up_bias.dtype:
         raise TypeError("gate_bias and up_bias must have one dtype")
-    ws = _scratch(gptq_w4a16_glu_workspace_bytes(tokens, m, n, group_size), X, workspace)
-    with _Device(X):
-        st = lib().gptq_w4a16_glu(X.data_ptr(), tokens, ldx, packed.data_ptr(), _uint8("packed", packed), m, n,
-                                  group_size, _activation_code(activation), _vector("gate_bias", gate_bias, m),
-                                  _vector("up_bias", up_bias, m), 0 if some is None else _dtype_code(some),
-                                  Y.data_ptr(), _dtype_code(Y), _rows("Y", Y, tokens, m), ws.data_ptr(), ws.nbytes,
-                                  _stream_on(X, stream))
-    _check(st, "gptq_w4a16_glu")
+    fn = lib().gptq_w4a16_glu
+    args = (X.data_ptr(), tokens, ldx, packed.data_ptr(), _uint8("packed", packed), m, n, group_size,
+            _activation_code(activation), _vector("gate_bias", gate_bias, m), _vector("up_bias", up_bias, m),
+            0 if some is None else _dtype_code(some), Y.data_ptr(), _dtype_code(Y), _rows("Y", Y, tokens, m))
+    s = _stream_on(X, stream)
+    with _device(X):
+        _with_workspace(lambda ws, nbytes: fn(*args, ws, nbytes, s),
+                        lambda: gptq_w4a16_glu_workspace_bytes(tokens, m, n, group_size), X, workspace,
+                        "gptq_w4a16_glu")
     return Y
 
 
@@ -639,7 +653,7 @@ def gptq_w4a16_moe_pack(cfg: MoeConfig, expert: int, gate_qweight: torch.Tensor,
         up_zeros=up_zeros, g_idx=g_idx, down_qweight=down_qweight, down_scales=down_scales, down_zeros=down_zeros,
         down_g_idx=down_g_idx, packed=packed)
     c = cfg.c()
-    with _Device(gate_qweight):
+    with _device(gate_qweight):
         st = lib().gptq_w4a16_moe_pack(ctypes.byref(c), expert, _ptr(gate_qweight), _ptr(gate_scales),
                                        _ptr(gate_zeros), _ptr(up_qweight), _ptr(up_scales), _ptr(up_zeros),
                                        _ptr(g_idx), _ptr(down_qweight), _ptr(down_scales), _ptr(down_zeros),
@@ -707,14 +721,16 @@ def gptq_w4a16_moe(X: torch.Tensor, router: torch.Tensor, packed: torch.Tensor, 
         raise ValueError(f"topk_ids and topk_weights must be [{tokens}, {cfg.top_k}]")
     ldr = cfg.hidden if residual is None else _rows("residual", residual, tokens, cfg.hidden)
     c = cfg.c()
-    ws = _scratch(int(lib().gptq_w4a16_moe_workspace_bytes(ctypes.byref(c), tokens)), X, workspace)
-    with _Device(X):
-        st = lib().gptq_w4a16_moe(X.data_ptr(), tokens, ldx, router.data_ptr(), _dtype_code(router), ctypes.byref(c),
-                                  packed.data_ptr(), _uint8("packed", packed), _ptr(residual),
-                                  0 if residual is None else _dtype_code(residual), ldr, Y.data_ptr(), _dtype_code(Y),
-                                  _rows("Y", Y, tokens, cfg.hidden), topk_ids.data_ptr(), topk_weights.data_ptr(),
-                                  ws.data_ptr(), ws.nbytes, _stream_on(X, stream))
-    _check(st, "gptq_w4a16_moe")
+    fn = lib().gptq_w4a16_moe
+    args = (X.data_ptr(), tokens, ldx, router.data_ptr(), _dtype_code(router), ctypes.byref(c), packed.data_ptr(),
+            _uint8("packed", packed), _ptr(residual), 0 if residual is None else _dtype_code(residual), ldr,
+            Y.data_ptr(), _dtype_code(Y), _rows("Y", Y, tokens, cfg.hidden), topk_ids.data_ptr(),
+            topk_weights.data_ptr())
+    s = _stream_on(X, stream)
+    with _device(X):
+        _with_workspace(lambda ws, nbytes: fn(*args, ws, nbytes, s),
+                        lambda: int(lib().gptq_w4a16_moe_workspace_bytes(ctypes.byref(c), tokens)), X, workspace,
+                        "gptq_w4a16_moe")
     return Y, topk_ids, topk_weights
 
 

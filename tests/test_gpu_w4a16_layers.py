@@ -246,6 +246,10 @@ MOE = [
     (7, 200, 3, 64, 32, 4, 32, True, "silu", True, "", "fp32", "bf16"),          # several words of expert bits
     (2, 1024, 64, 40, 16, 4, 32, False, "relu", False, "", "fp32", "bf16"),      # the largest counts
     (3, 4, 1, 8200, 48, 4, 128, True, "silu", True, "", "fp32", "bf16"),
+    (1, 3, 2, 515, 2000, 2, 128, True, "silu", False, "fp32", "fp32", "fp32"),
+    (16, 4, 4, 256, 128, 4, 64, True, "silu", True, "bf16", "bf16", "bf16"),     # the most pairs of two launches
+    (1, 16, 8, 4096, 256, 4, 64, True, "silu", True, "", "bf16", "bf16"),
+    (1, 20, 8, 4096, 256, 4, 64, True, "silu", True, "", "bf16", "bf16"),
     (20, 3, 2, 4104, 1500, 4, 64, True, "silu", True, "bf16", "bf16", "bf16"),   # a pass that LDS does not hold
 ]
 
@@ -267,13 +271,14 @@ def test_moe_matches_oracle(pq, case):
     H.check(Y, ref, bound, f"moe {case}", out)
 
 
-def test_moe_ties_go_to_the_lower_expert(pq):
+@pytest.mark.parametrize("tokens", [5, 40])
+def test_moe_ties_go_to_the_lower_expert(pq, tokens):
     E, k, hidden, inter = 9, 4, 64, 32
     rng = np.random.default_rng(1)
     experts = _experts(E, hidden, inter, 4, 32, rng, True)
     cfg = pq.MoeConfig(hidden, inter, E, k, 4, 32, "silu", True)
     packed = _pack(pq, cfg, experts)
-    X = H.activations(5, hidden, seed=2)
+    X = H.activations(tokens, hidden, seed=2)
     R = H.vector((E, hidden), "bf16", 3)
     R[4] = R[7]
     R[2] = R[7]
@@ -284,16 +289,17 @@ def test_moe_ties_go_to_the_lower_expert(pq):
     H.check(Y, ref, bound, "tied logits")
     same = torch.zeros_like(R)
     _, ids, wts = pq.gptq_w4a16_moe(X.cuda(), same.cuda(), packed, cfg)
-    assert torch.equal(ids.cpu(), torch.arange(k, dtype=torch.int32).expand(5, k))
+    assert torch.equal(ids.cpu(), torch.arange(k, dtype=torch.int32).expand(tokens, k))
     assert torch.all(wts == 0.25)
 
 
-def test_moe_token_of_nan_spoils_its_own_row(pq):
+@pytest.mark.parametrize("tokens", [6, 20])
+def test_moe_token_of_nan_spoils_its_own_row(pq, tokens):
     E, k, hidden, inter = 8, 2, 128, 96
     rng = np.random.default_rng(5)
     cfg = pq.MoeConfig(hidden, inter, E, k, 4, 32, "silu", True)
     packed = _pack(pq, cfg, _experts(E, hidden, inter, 4, 32, rng, True))
-    X = H.activations(20, hidden, seed=6).cuda()
+    X = H.activations(tokens, hidden, seed=6).cuda()
     R = H.vector((E, hidden), "bf16", 7).cuda()
     Y, ids, _ = pq.gptq_w4a16_moe(X, R, packed, cfg)
     B = X.clone()
@@ -301,17 +307,17 @@ def test_moe_token_of_nan_spoils_its_own_row(pq):
     Z, zids, _ = pq.gptq_w4a16_moe(B, R, packed, cfg)
     assert torch.equal(zids[3].cpu(), torch.arange(k, dtype=torch.int32))   # all logits NaN: the lowest experts
     assert not torch.isfinite(Z[3]).any()
-    keep = [t for t in range(20) if t != 3]
+    keep = [t for t in range(tokens) if t != 3]
     assert torch.equal(Y[keep], Z[keep]) and torch.equal(ids[keep], zids[keep])
 
 
-def test_moe_strided_rows_and_in_place_residual(pq):
+@pytest.mark.parametrize("tokens", [4, 11, 90])
+def test_moe_strided_rows_and_in_place_residual(pq, tokens):
     E, k, hidden, inter = 6, 2, 203, 77
     rng = np.random.default_rng(8)
     experts = _experts(E, hidden, inter, 4, 64, rng, True)
     cfg = pq.MoeConfig(hidden, inter, E, k, 4, 64, "silu", True)
     packed = _pack(pq, cfg, experts)
-    tokens = 11
     X = H.activations(tokens, hidden, seed=9)
     big = torch.full((tokens, hidden + 6), float("nan"), dtype=torch.bfloat16, device="cuda")
     big[:, 3:3 + hidden] = X.cuda()
