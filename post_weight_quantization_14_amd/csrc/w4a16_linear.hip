@@ -236,13 +236,13 @@ struct L4GemmArgs {
   L4Epilogue ep;
 };
 
-// Tile: 32·MT·TG tokens x 64·RG rows; TG·RG waves of 32·MT tokens x 64 rows on
+// Tile: 32·MT·TG tokens x 32·NB·RG rows; TG·RG waves of 32·MT tokens x 32·NB rows on
 // v_mfma_f32_32x32x16_bf16, and KG such groups of waves that take every KG-th
 // chunk of the slice (few tokens: the chain of chunks is latency, and a
 // workgroup's groups run KG of them side by side).
-template <int GS, int MT, int TG, int RG, int KG>
+template <int GS, int MT, int NB, int TG, int RG, int KG>
 struct L4Tile {
-  static constexpr int kTokens = 32 * MT * TG, kRows = 64 * RG, kGroup = TG * RG, kThreads = 64 * kGroup * KG;
+  static constexpr int kTokens = 32 * MT * TG, kRows = 32 * NB * RG, kGroup = TG * RG, kThreads = 64 * kGroup * KG;
   static constexpr int kNG = 4 / GS;
   static constexpr int kX = kTokens * 256;                                         // X' of one chunk
   static constexpr int kBytes = kX + ((kNG * kTokens * 4 + 255) & ~255);           // and its group sums
@@ -251,9 +251,9 @@ struct L4Tile {
   static_assert(kTokens % 32 == 0, "sums are copied 32 or 64 floats at a time");
 };
 
-template <int GS, int MT, int TG, int RG, int KG, bool GATED>
+template <int GS, int MT, int NB, int TG, int RG, int KG, bool GATED>
 __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __restrict__ s0, uint8_t* __restrict__ s1) {
-  using Tl = L4Tile<GS, MT, TG, RG, KG>;
+  using Tl = L4Tile<GS, MT, NB, TG, RG, KG>;
   constexpr int NG = Tl::kNG, U = Tl::kXCopies;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -310,25 +310,25 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
   // Positions 32j + 16h + 8(l / 32).. of a chunk are word j of the packed lane
   // 16·(2h + l / 32) + l % 16.
   const int half = (lane >> 4) & 1;
-  const u32x4_t* cp[2][2];
-  const float2* pp[2];
+  const u32x4_t* cp[NB][2];
+  const float2* pp[NB];
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
+  for (int b = 0; b < NB; ++b) {
     const int64_t tile =
-        std::min<int64_t>((rb * RG + rg) * 4 + (GATED ? b + 2 * half : 2 * b + half), a.mt - 1);
+        std::min<int64_t>((rb * RG + rg) * 2 * NB + (GATED && NB == 2 ? b + 2 * half : 2 * b + half), a.mt - 1);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       cp[b][h] = a.codes + (tile * a.kc + c0) * 64 + 16 * (2 * h + (lane >> 5)) + (lane & 15);
     pp[b] = a.params + tile * a.Gp * kL4Rows + (lane & 15) + (int64_t)c0 * NG * a.pmul;
   }
   struct Codes {
-    u32x4_t w[2][2];
-    float2 p[2][NG];
+    u32x4_t w[NB][2];
+    float2 p[NB][NG];
   };
   auto fetch = [&](int c, Codes& k) {
     const int cc = std::min(c * KG + kg, nch - 1);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < NB; ++b) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) k.w[b][h] = cp[b][h][(int64_t)cc * 64];
 #pragma unroll
@@ -337,11 +337,11 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
   };
 
   const L4Consts kc;
-  f32x16_t y[MT][2];
+  f32x16_t y[MT][NB];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int v = 0; v < 16; ++v) y[mt][b][v] = 0.f;
 
@@ -358,11 +358,11 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
     };
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      f32x16_t acc[MT][2];
+      f32x16_t acc[MT][NB];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int v = 0; v < 16; ++v) acc[mt][b][v] = 0.f;
       u32x4_t av[2][MT];
@@ -375,19 +375,19 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) av[(q + 1) & 1][mt] = frag(st + 1, mt);
         }
-        bf16x8_t w[2];
+        bf16x8_t w[NB];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) w[b] = kc.unpack(k.w[b][st & 1][st >> 1]);
+        for (int b = 0; b < NB; ++b) w[b] = kc.unpack(k.w[b][st & 1][st >> 1]);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
+          for (int b = 0; b < NB; ++b)
             acc[mt][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, av[q & 1][mt]), w[b],
                                                                  acc[mt][b], 0, 0, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, MT, 0);   // LDS reads
 #pragma unroll
-        for (int u = 0; u < 2 * MT; ++u) {
-          __builtin_amdgcn_sched_group_barrier(0x002, 16 / (2 * MT), 0);   // VALU
+        for (int u = 0; u < NB * MT; ++u) {
+          __builtin_amdgcn_sched_group_barrier(0x002, 8 / MT, 0);   // VALU
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);               // MFMA
         }
       }
@@ -399,7 +399,7 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
           const f32x4_t sx = *reinterpret_cast<const f32x4_t*>(
               cur + Tl::kX + (g * Tl::kTokens + 32 * (MT * tg + mt) + 8 * q + 4 * (lane >> 5)) * 4);
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int v = 0; v < 4; ++v)
               y[mt][b][4 * q + v] =
@@ -427,12 +427,12 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
 #undef L4_STEP
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy may land after the workgroup ends
 
-  if (KG > 1) {
+  if constexpr (KG > 1) {
     // The groups' sums through LDS: every wave leaves its fragments, then each
     // group adds and finishes its share of them (4 tokens of a row, gate and
     // up together), so the epilogue runs on all waves.
     constexpr int F = MT * 8, SHARE = MT * 4 / KG;
-    static_assert(KG == 1 || (MT * 4) % KG == 0, "the fragments split evenly over the groups");
+    static_assert(KG == 1 || (NB == 2 && (MT * 4) % KG == 0), "the fragments split evenly over the groups");
     static_assert(KG == 1 || (KG / 2) * Tl::kGroup * F * 1024 <= KG * Tl::kBytes, "half of the groups fit in each array");
     __syncthreads();   // every copy into the slots and every read of them is done
     auto at = [&](int k, int f) {
@@ -473,18 +473,18 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
   if (a.splits > 1) {
     // fragments as they lie: [slice][tile][wave][mt][b][q][lane] float4
     f32x4_t* out = reinterpret_cast<f32x4_t*>(a.part) +
-                   (((int64_t)sl * per + i) * Tl::kGroup + gw) * (MT * 2 * 4 * 64) + lane;
+                   (((int64_t)sl * per + i) * Tl::kGroup + gw) * (MT * NB * 4 * 64) + lane;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          out[((mt * 2 + b) * 4 + q) * 64] =
+          out[((mt * NB + b) * 4 + q) * 64] =
               f32x4_t{y[mt][b][4 * q], y[mt][b][4 * q + 1], y[mt][b][4 * q + 2], y[mt][b][4 * q + 3]};
     return;
   }
-  const int64_t rbase = (rb * RG + rg) * (GATED ? 32 : 64) + (lane & 31);
+  const int64_t rbase = (rb * RG + rg) * (GATED ? 16 * NB : 32 * NB) + (lane & (GATED && NB == 1 ? 15 : 31));
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const int64_t t = t0 + 32 * (MT * tg + mt) + 4 * (lane >> 5);
@@ -494,53 +494,72 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
 #pragma unroll
       for (int v = 0; v < 8; ++v) {
         v0[v] = y[mt][0][4 * q + v];
-        v1[v] = y[mt][1][4 * q + v];
+        v1[v] = y[mt][NB - 1][4 * q + v];
       }
-      a.ep.template block<8, GATED>(t + 8 * q, a.tokens, rbase, a.m, v0, v1);
-      if (!GATED) a.ep.template block<8, false>(t + 8 * q, a.tokens, rbase + 32, a.m, v1, v1);
+      if constexpr (GATED && NB == 1) {
+        // gate sits in the lower 16 lanes of each 32, up in the upper: they
+        // trade, and finish four tokens each
+        float g4[4], u4[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float got = __shfl_xor(half ? v0[v] : v0[4 + v], 16);
+          g4[v] = half ? got : v0[v];
+          u4[v] = half ? v0[4 + v] : got;
+        }
+        a.ep.template block<4, true>(t + 8 * (q + half), a.tokens, rbase, a.m, g4, u4);
+      } else {
+        a.ep.template block<8, GATED>(t + 8 * q, a.tokens, rbase, a.m, v0, v1);
+        if (!GATED && NB == 2) a.ep.template block<8, false>(t + 8 * q, a.tokens, rbase + 32, a.m, v1, v1);
+      }
     }
   }
 }
 
-template <int GS, int MT, int TG, int RG, int KG, bool GATED>
+template <int GS, int MT, int NB, int TG, int RG, int KG, bool GATED>
 __global__ __launch_bounds__(64 * TG * RG * KG, 2) void l4_gemm_kernel(L4GemmArgs a) {
-  using Tl = L4Tile<GS, MT, TG, RG, KG>;
+  using Tl = L4Tile<GS, MT, NB, TG, RG, KG>;
   // two arrays, not one indexed at run time: a read of one is then known not
   // to alias the copies in flight into the other
   __shared__ __attribute__((aligned(16))) uint8_t s0[KG * Tl::kBytes];
   __shared__ __attribute__((aligned(16))) uint8_t s1[KG * Tl::kBytes];
-  l4_gemm_tile<GS, MT, TG, RG, KG, GATED>(a, s0, s1);
+  l4_gemm_tile<GS, MT, NB, TG, RG, KG, GATED>(a, s0, s1);
 }
 
 // Sums the K slices in slice order and finishes.  Thread: one float4 fragment
 // (4 tokens of one row; gate and up together for a pair).
-template <int MT, int TG, int RG, bool GATED>
+template <int MT, int NB, int TG, int RG, bool GATED>
 __global__ __launch_bounds__(256) void l4_reduce_kernel(L4GemmArgs a) {
-  constexpr int FR = TG * RG * MT * 2 * 4 * 64;   // fragments of one tile
+  constexpr int FR = TG * RG * MT * NB * 4 * 64;   // fragments of one tile
+  constexpr bool kPair = GATED && NB == 2;
   const int64_t per = a.tblocks * a.rblocks;
   int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  constexpr int PER = GATED ? FR / 2 : FR;
-  if (f >= per * PER) return;
+  constexpr int PER = kPair ? FR / 2 : FR;
+  if (f >= per * PER) return;   // whole waves: PER is a multiple of 64
   const int64_t i = f / PER;
   int k = (int)(f % PER);
   const int lane = k & 63, q = (k >> 6) & 3;
   k >>= 8;
   int b = 0;
-  if (!GATED) {
-    b = k & 1;
-    k >>= 1;
+  if (!kPair) {
+    b = k % NB;
+    k /= NB;
   }
   const int mt = k % MT, wave = k / MT, rg = wave % RG, tg = wave / RG;
-  const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.part) + i * FR + ((wave * MT + mt) * 2 + b) * 256 + q * 64 + lane;
+  const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.part) + i * FR + ((wave * MT + mt) * NB + b) * 256 + q * 64 + lane;
   f32x4_t v0 = p[0], v1 = {0.f, 0.f, 0.f, 0.f};
-  if (GATED) v1 = p[256];
+  if (kPair) v1 = p[256];
   for (int s = 1; s < a.splits; ++s) {
     v0 += p[(int64_t)s * per * FR];
-    if (GATED) v1 += p[(int64_t)s * per * FR + 256];
+    if (kPair) v1 += p[(int64_t)s * per * FR + 256];
+  }
+  if (GATED && NB == 1) {   // up is 16 lanes on
+#pragma unroll
+    for (int v = 0; v < 4; ++v) v1[v] = __shfl_xor(v0[v], 16);
+    if (lane & 16) return;
   }
   const int64_t tb = i % a.tblocks, rb = i / a.tblocks;
   const int64_t t = tb * (32 * MT * TG) + 32 * (MT * tg + mt) + 8 * q + 4 * (lane >> 5);
-  const int64_t r = (rb * RG + rg) * (GATED ? 32 : 64) + 32 * b + (lane & 31);
+  const int64_t r = (rb * RG + rg) * (GATED ? 16 * NB : 32 * NB) + 32 * b + (lane & (GATED && NB == 1 ? 15 : 31));
   const float g4[4] = {v0[0], v0[1], v0[2], v0[3]}, u4[4] = {v1[0], v1[1], v1[2], v1[3]};
   a.ep.template block<4, GATED>(t, a.tokens, r, a.m, g4, u4);
 }
@@ -622,15 +641,16 @@ gptq_status launch_l4_decode(const L4DecodeArgs& d, int gs, bool gated, bool gat
   }
 }
 
-template <int GS, int MT, int TG, int RG, int KG, bool GATED>
+template <int GS, int MT, int NB, int TG, int RG, int KG, bool GATED>
 gptq_status launch_l4_tile(const L4GemmArgs& g, hipStream_t stream) {
   const int64_t tiles = g.tblocks * g.rblocks;
-  hipLaunchKernelGGL((l4_gemm_kernel<GS, MT, TG, RG, KG, GATED>), dim3((unsigned)(tiles * g.splits)),
+  hipLaunchKernelGGL((l4_gemm_kernel<GS, MT, NB, TG, RG, KG, GATED>), dim3((unsigned)(tiles * g.splits)),
                      dim3(64 * TG * RG * KG), 0, stream, g);
   GPTQ_LAUNCH_CHECK();
   if (g.splits > 1) {
-    const int64_t frags = tiles * TG * RG * MT * 8 * 64 / (GATED ? 2 : 1);
-    hipLaunchKernelGGL((l4_reduce_kernel<MT, TG, RG, GATED>), dim3((unsigned)ceil_div(frags, 256)), dim3(256), 0, stream, g);
+    const int64_t frags = tiles * TG * RG * MT * NB * 4 * 64 / (GATED && NB == 2 ? 2 : 1);
+    hipLaunchKernelGGL((l4_reduce_kernel<MT, NB, TG, RG, GATED>), dim3((unsigned)ceil_div(frags, 256)), dim3(256), 0,
+                       stream, g);
     GPTQ_LAUNCH_CHECK();
   }
   return GPTQ_OK;
@@ -638,9 +658,9 @@ gptq_status launch_l4_tile(const L4GemmArgs& g, hipStream_t stream) {
 
 template <int GS, bool GATED>
 gptq_status launch_l4_shape(const L4GemmArgs& g, const L4Shape& s, hipStream_t stream) {
-  if (s.tokens == 32) return launch_l4_tile<GS, 1, 1, 2, 4, GATED>(g, stream);
-  if (s.tokens == 64) return launch_l4_tile<GS, 2, 1, 2, 4, GATED>(g, stream);
-  return launch_l4_tile<GS, 2, 2, 2, 1, GATED>(g, stream);
+  if (s.tokens == 32) return launch_l4_tile<GS, 1, 2, 1, 2, 4, GATED>(g, stream);
+  if (s.tokens == 64) return launch_l4_tile<GS, 2, 2, 1, 2, 4, GATED>(g, stream);
+  return launch_l4_tile<GS, 4, 1, 1, 4, 1, GATED>(g, stream);
 }
 
 gptq_status launch_l4_gemm(const L4GemmArgs& g, const L4Shape& s, int gs, bool gated, hipStream_t stream) {
