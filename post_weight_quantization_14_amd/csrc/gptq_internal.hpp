@@ -257,7 +257,7 @@ struct MoeLayout {
 MoeLayout plan_moe(const gptq_moe_config& c);
 struct MoeWork {
   int64_t block = 0;
-  size_t wts_off = 0, xp_off = 0, mid_off = 0, out_off = 0, total = 0;
+  size_t wts_off = 0, xp_off = 0, mid_off = 0, out_off = 0, logits_off = 0, total = 0;
 };
 MoeWork plan_moe_work(const gptq_moe_config& c, int64_t tokens);
 struct MoeCall {

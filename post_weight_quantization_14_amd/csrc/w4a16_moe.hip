@@ -39,6 +39,7 @@ struct MoeRouterArgs {
   const char* packed;     // expert e's column order at e·stride + order_off
   int64_t stride, order_off, n128;
   uint16_t* Xp;           // [pairs][n128]
+  double* logits;         // [tokens][experts] of moe_logits_kernel, or null: computed here
 };
 
 // a before b: larger, NaN above every number, ties to the lower index
@@ -122,6 +123,21 @@ __device__ __forceinline__ double moe_logit(const uint16_t* x, const void* R, in
   return s0;
 }
 
+// Logits of 16 experts (grid x) for a token (grid y), a wave each: where there
+// are many, on all CUs instead of one per token (64 tokens, 64 experts of
+// 2048: the router's 15 us become 5 + 6).
+__global__ __launch_bounds__(1024) void moe_logits_kernel(MoeRouterArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int64_t t = blockIdx.y;
+  const int h = (int)a.hidden, tid = threadIdx.x;
+  const int e = blockIdx.x * 16 + (tid >> 6);
+  l4_row_to_lds(a.X + t * a.ldx, h, a.xvec, lds, tid, 1024);
+  __syncthreads();
+  if (e >= a.experts) return;
+  const double s = moe_logit(reinterpret_cast<const uint16_t*>(lds), a.R, a.r_dt, a.vec, e, h, 0, 1);
+  if ((tid & 63) == 0) a.logits[t * a.experts + e] = s;
+}
+
 // One workgroup per token.  The logits are summed in 64 bits: which experts
 // are chosen hangs on the last bits of the k-th and the next, and a choice
 // that falls the other way is no rounding error in the result.  `parts` waves
@@ -155,11 +171,13 @@ __global__ __launch_bounds__(1024) void moe_router_kernel(MoeRouterArgs a) {
   };
   const int i0 = 8 * lane + 512 * part, istep = 2048 * a.parts;
   u32x4_t w[4], nx[4];
-  if (fast) fetch(e0, i0, w);   // in flight while the token is copied
+  if (fast && !a.logits) fetch(e0, i0, w);   // in flight while the token is copied
   l4_row_to_lds(a.X + t * a.ldx, h, a.xvec, reinterpret_cast<uint8_t*>(x), tid, 1024);
   for (int e = tid; e < E; e += 1024) rank[e] = 0;
   __syncthreads();
-  for (int e = e0; e < E; e += wpe) {
+  if (a.logits)
+    for (int e = tid; e < E; e += 1024) logit[e] = a.logits[t * E + e];
+  for (int e = a.logits ? E : e0; e < E; e += wpe) {
     double s0 = 0.0, s1 = 0.0;
     if (fast) {
       for (int i = i0; i - 8 * lane < h; i += istep) {
@@ -656,6 +674,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
   l4_store(Y, y_dt, t * ldy + r, v);
 }
 
+constexpr int64_t kMoeLogitsElsewhere = 1 << 20;   // logit products from which they get a launch of their own
 constexpr int64_t kSmallRouter = 65536;       // logit products that every workgroup repeats
 constexpr size_t kMoeMaxLds = 120 * 1024;   // beyond: fragments from memory
 
@@ -736,7 +755,8 @@ MoeWork plan_moe_work(const gptq_moe_config& c, int64_t tokens) {
   w.xp_off = w.wts_off + align256(pairs * sizeof(float));
   w.mid_off = w.xp_off + align256(pairs * h128 * sizeof(uint16_t));
   w.out_off = w.mid_off + align256(pairs * kMoeMaxPlanes * f128 * sizeof(uint16_t));
-  w.total = w.out_off + align256(pairs * (size_t)c.hidden * sizeof(float));
+  w.logits_off = w.out_off + align256(pairs * (size_t)c.hidden * sizeof(float));
+  w.total = w.logits_off + align256((size_t)w.block * (size_t)c.experts * sizeof(double));
   return w;
 }
 
@@ -762,6 +782,7 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
   float* wts = reinterpret_cast<float*>(wb + w.wts_off);
   uint16_t* mid = reinterpret_cast<uint16_t*>(wb + w.mid_off);
   float* out = reinterpret_cast<float*>(wb + w.out_off);
+  double* logits = reinterpret_cast<double*>(wb + w.logits_off);
   const size_t ysz = c.y_dtype == GPTQ_FP32 ? 4 : 2, rsz = c.res_dtype == GPTQ_FP32 ? 4 : 2;
   const char* packed = static_cast<const char*>(c.packed);
   const int h = (int)cfg.hidden;
@@ -815,6 +836,8 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
     r.order_off = (int64_t)L.gu.order_off;
     r.n128 = L.gu.n128;
     r.Xp = Xp;
+    r.logits = (int64_t)tk * cfg.experts * h > kMoeLogitsElsewhere && cfg.experts > 16 ? logits : nullptr;
+    if (r.logits) r.parts = 1;
     const void* res = c.res ? (const void*)(static_cast<const char*>(c.res) + (size_t)(t0 * c.ldr) * rsz) : nullptr;
     void* Y = static_cast<char*>(c.Y) + (size_t)(t0 * c.ldy) * ysz;
     // the workgroups of the GPU dealt over the experts that can be active
@@ -874,6 +897,12 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
       }
 #undef MOE_SMALL_DOWN
       continue;
+    }
+    if (r.logits) {
+      const size_t llds = (size_t)round_up(h, 8) * 2;
+      hipLaunchKernelGGL(moe_logits_kernel, dim3((unsigned)ceil_div(cfg.experts, 16), (unsigned)tk), dim3(1024), llds,
+                         stream, r);
+      GPTQ_LAUNCH_CHECK();
     }
     const size_t rlds = (size_t)round_up((int64_t)r.parts * cfg.experts, 2) * sizeof(double) +
                         (size_t)round_up(cfg.experts, 4) * sizeof(int) + (size_t)round_up(h, 8) * 2;

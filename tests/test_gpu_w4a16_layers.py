@@ -250,6 +250,8 @@ MOE = [
     (16, 4, 4, 256, 128, 4, 64, True, "silu", True, "bf16", "bf16", "bf16"),     # the most pairs of two launches
     (1, 16, 8, 4096, 256, 4, 64, True, "silu", True, "", "bf16", "bf16"),
     (1, 20, 8, 4096, 256, 4, 64, True, "silu", True, "", "bf16", "bf16"),
+    (50, 40, 3, 1024, 64, 4, 64, True, "silu", True, "", "fp32", "fp32"),        # logits in a launch of their own
+    (66, 33, 2, 999, 64, 4, 128, True, "silu", False, "", "bf16", "bf16"),
     (20, 3, 2, 4104, 1500, 4, 64, True, "silu", True, "bf16", "bf16", "bf16"),   # a pass that LDS does not hold
 ]
 
