@@ -250,22 +250,24 @@ struct L4LdsA {
   }
 };
 
-// Host: the split of `units` units over `wgs` workgroups.  ks waves share a
-// unit; the choice with the fullest rounds wins, the smaller ks on a tie (no
-// sums through LDS, fewer barriers).
+// Host: the split of `units` units (of rt row tiles) over `wgs` workgroups, ks
+// = 1 << kslog waves sharing a unit.  A round costs a wave its chunks (about
+// 1 us for each of 16 waves' KB at the HBM's pace) and, where waves share,
+// the sums through LDS and their two barriers (about the same).  Fullest
+// rounds alone chose 7 rounds of 2 chunks over 1 of 16 for 64 units on 5
+// workgroups: 61 us instead of 35.
 struct L4Split {
   int kslog, rounds;
 };
-inline L4Split l4_split(int64_t units, int64_t wgs, int64_t kc) {
+inline L4Split l4_split(int64_t units, int64_t wgs, int64_t kc, int rt) {
   L4Split best{0, 1};
-  double eff = 0.0;
+  int64_t least = -1;
   for (int lg = 0; lg <= 4; ++lg) {
     if (lg > 0 && (int64_t(1) << lg) > kc) break;
-    const int64_t per = wgs * (kL4Waves >> lg), rounds = ceil_div(units, per);
-    const int64_t cps = (kc + (1 << lg) - 1) >> lg;
-    const double e = (double)units * (double)kc / ((double)(rounds * per * cps) * (1 << lg));
-    if (e > eff * 1.05) {
-      eff = e;
+    const int64_t rounds = ceil_div(units, wgs * (kL4Waves >> lg)), cps = (kc + (1 << lg) - 1) >> lg;
+    const int64_t cost = rounds * (cps * rt * 5 + (lg ? 5 : 1));
+    if (least < 0 || cost < least) {
+      least = cost;
       best = L4Split{lg, (int)rounds};
     }
   }

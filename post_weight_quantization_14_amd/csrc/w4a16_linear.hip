@@ -781,7 +781,7 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
       d.vec = vec;
       d.ep = ep;
       const int64_t wgs = std::min<int64_t>(st.units, std::max<int64_t>(1, kL4Cus / ttiles));
-      const L4Split sp = l4_split(st.units, wgs, L.kc);
+      const L4Split sp = l4_split(st.units, wgs, L.kc, gated ? 2 : 1);
       st.kslog = sp.kslog;
       st.rounds = sp.rounds;
       d.st = st;

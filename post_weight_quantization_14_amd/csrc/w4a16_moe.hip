@@ -409,7 +409,7 @@ __global__ __launch_bounds__(kL4Threads) void moe_down_kernel(MoeExpertArgs a) {
 // four, with no pass of ids, X' or pair results through memory between them.
 constexpr int kSmallTokens = 16;
 constexpr int kSmallPairs = 64;
-constexpr int kSmallLogits = 512;
+constexpr int kSmallLogits = 64;
 
 struct MoeSmallArgs {
   MoeExpertArgs x;        // gate/up: A unused; down: the combine's part below
@@ -674,22 +674,33 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
   l4_store(Y, y_dt, t * ldy + r, v);
 }
 
-constexpr int64_t kMoeLogitsElsewhere = 1 << 20;   // logit products from which they get a launch of their own
-constexpr int64_t kSmallRouter = 65536;       // logit products that every workgroup repeats
-constexpr size_t kMoeMaxLds = 120 * 1024;   // beyond: fragments from memory
+constexpr int64_t kMoeLogitsElsewhere = 1 << 16;   // logit products from which they get a launch of their own
+// Logit products that every workgroup repeats: up to here it costs less than
+// the launches it saves (64 experts of 2048, 1 token: 34.5 us by four launches,
+// 27.2 by two; 16 of 2048, 4 tokens: 32.5 and 34.1).
+constexpr int64_t kSmallRouter = 65536, kSmallRouter2 = 131072;   // the latter for one or two tokens
+constexpr size_t kMoeMaxLds = 150 * 1024;
 
 // fills the launch-dependent fields; returns the dynamic LDS bytes, 0 < lds
 // with *in_lds when the rows of a pass fit
 size_t moe_plan(MoeExpertArgs& a, int tokens, int planes, int rt, int64_t wgs, bool* in_lds) {
-  a.pass = std::min(kMoePass, tokens);
-  a.quads = (int)ceil_div(a.pass, 4);
-  const L4Split sp = l4_split(a.st.units, wgs, a.st.kc);
+  const L4Split sp = l4_split(a.st.units, wgs, a.st.kc, rt);
   a.st.kslog = sp.kslog;
   a.st.rounds = sp.rounds;
-  const size_t red = sp.kslog ? (size_t)kL4Waves * rt * a.quads * 64 * sizeof(float) : 0;
-  const size_t rows = (size_t)a.pass * planes * (size_t)(a.k128 + kL4Pad) * 2;
-  *in_lds = rows + red <= kMoeMaxLds;
-  return *in_lds ? rows + red : red;
+  // as many tokens a pass as LDS holds, down to six; fewer would stream the
+  // codes too often, and fragments are read from memory instead (8 experts of
+  // 4096 x 2048, 64 tokens: 114 us from memory, 80 us in passes of 14)
+  for (a.pass = std::min(kMoePass, tokens);; --a.pass) {
+    a.quads = (int)ceil_div(a.pass, 4);
+    const size_t red = sp.kslog ? (size_t)kL4Waves * rt * a.quads * 64 * sizeof(float) : 0;
+    const size_t rows = (size_t)a.pass * planes * (size_t)(a.k128 + kL4Pad) * 2;
+    *in_lds = rows + red <= kMoeMaxLds;
+    if (*in_lds) return rows + red;
+    if (a.pass <= 6) break;
+  }
+  a.pass = std::min(kMoePass, tokens);
+  a.quads = (int)ceil_div(a.pass, 4);
+  return sp.kslog ? (size_t)kL4Waves * rt * a.quads * 64 * sizeof(float) : 0;
 }
 
 // Whether a call of `tokens` tokens takes the two-launch form.
@@ -697,7 +708,7 @@ bool moe_is_small(const gptq_moe_config& c, int64_t tokens, int planes, const Mo
   const size_t x = (size_t)tokens * (size_t)(L.gu.n128 + kL4Pad) * 2 + (size_t)tokens * (size_t)round_up(c.hidden, 8) * 2;
   const size_t mid = (size_t)(tokens * c.top_k * planes) * (size_t)(L.f128 + kL4Pad) * 2;
   return tokens <= kSmallTokens && tokens * c.top_k <= kSmallPairs && tokens * c.experts <= kSmallLogits &&
-         tokens * c.experts * c.hidden <= kSmallRouter && x <= 64 * 1024 && mid <= 100 * 1024;
+         tokens * c.experts * c.hidden <= (tokens <= 2 ? kSmallRouter2 : kSmallRouter) && x <= 64 * 1024 && mid <= 100 * 1024;
 }
 
 template <class A, class K>
