@@ -130,9 +130,12 @@ struct L4DecodeArgs {
   L4Epilogue ep;
 };
 
-// Few tokens: 16 (grid y) whose X' fits in LDS.  Unit = one row tile (linear) or one
-// gate/up pair of tiles (glu).  X' is gathered here (GATHER) or copied from X'
-// in memory.
+// Few tokens: 16 of them (grid y), whose X' fits in LDS.  Unit = one row tile
+// (linear) or one gate/up pair of tiles (glu).  X' is gathered here (GATHER) or
+// copied from X' in memory.  Bound by the code stream from HBM, at small sizes
+// by the chain launch - row - order - codes - sums and the call itself:
+// 4096 x 4096, 1 token 5.9 us (9.5 with Python's call), 11008 x 4096 pair
+// 16.7 us = 3.0 TB/s, 8192 x 29568 34.5 us = 3.9 TB/s.
 template <int GS, bool GATED, bool GATHER>
 __global__ __launch_bounds__(kL4Threads) void l4_decode_kernel(L4DecodeArgs a) {
   constexpr int RT = GATED ? 2 : 1;
@@ -237,17 +240,30 @@ struct L4GemmArgs {
   L4Epilogue ep;
 };
 
-// Tile: 32·MT·TG tokens x 32·NB·RG rows; TG·RG waves of 32·MT tokens x 32·NB rows on
-// v_mfma_f32_32x32x16_bf16, and KG such groups of waves that take every KG-th
-// chunk of the slice (few tokens: the chain of chunks is latency, and a
+// Tile: 32·MT·TG tokens x 32·NB·RG rows; TG·RG waves of 32·MT tokens x 32·NB
+// rows on v_mfma_f32_32x32x16_bf16, and KG such groups of waves that take every
+// KG-th chunk of the slice (few tokens: the chain of chunks is latency, and a
 // workgroup's groups run KG of them side by side).
+//
+// X' comes through LDS (direct copies, two slots), the codes straight into
+// registers in operand order: 4 bits a weight would be 16 as operands in LDS.
+// Bound by the issue of matrix and vector instructions, which a SIMD does one
+// after the other here (its cycles are 32 per product plus 4 per vector
+// instruction in every variant tried, within 5 %), and by the clock that the
+// power allows (1.9-2.05 GHz): the vector work per product decides the shape.
+// A wave of 128 tokens x 32 rows unpacks each operand once for four products
+// (64 x 64: two) and runs 2048 x 22016 x 4096 in 378 us = 0.98 PFLOP/s against
+// 396; the library's bf16 product of that shape takes 424 us.  Tried and not
+// kept: two chunks in flight behind a second barrier (+2 %), the fold between
+// the next products (+7 %: it reads the A fragments twice), A fragments two
+// steps ahead (0 %).
 template <int GS, int MT, int NB, int TG, int RG, int KG>
 struct L4Tile {
   static constexpr int kTokens = 32 * MT * TG, kRows = 32 * NB * RG, kGroup = TG * RG, kThreads = 64 * kGroup * KG;
   static constexpr int kNG = 4 / GS;
-  static constexpr int kX = kTokens * 256;                                         // X' of one chunk
-  static constexpr int kBytes = kX + ((kNG * kTokens * 4 + 255) & ~255);           // and its group sums
-  static constexpr int kXCopies = kX / 1024 / kGroup;                              // 1 KB copies per wave
+  static constexpr int kX = kTokens * 256;                                 // X' of one chunk
+  static constexpr int kBytes = kX + ((kNG * kTokens * 4 + 255) & ~255);   // and its group sums
+  static constexpr int kXCopies = kX / 1024 / kGroup;                      // 1 KB copies per wave
   static_assert(kX % (1024 * kGroup) == 0, "copies split evenly over the waves");
   static_assert(kTokens % 32 == 0, "sums are copied 32 or 64 floats at a time");
 };
@@ -311,9 +327,10 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
     }
   };
 
-  // operand b of a wave's 64 rows: lane l feeds row l % 32 of 32, which is row
-  // l % 16 of packed tile 2b + (l / 16) % 2; for a gate/up pair, whose tiles
-  // alternate, tile b + 2·((l / 16) % 2): b = 0 all gate, b = 1 all up.
+  // operand b of a wave's 32·NB rows: lane l feeds row l % 32 of 32, which is
+  // row l % 16 of packed tile 2b + (l / 16) % 2; for two operands of gate/up
+  // pairs, whose tiles alternate, tile b + 2·((l / 16) % 2): b = 0 all gate,
+  // b = 1 all up (one operand holds a gate tile and its up tile side by side).
   // Positions 32j + 16h + 8(l / 32).. of a chunk are word j of the packed lane
   // 16·(2h + l / 32) + l % 16.
   const int half = (lane >> 4) & 1;
@@ -354,7 +371,7 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
 
   const int trow = lane & 31;   // + 32·(MT·tg + mt): (t mod 16) is lane mod 16
   // One chunk.  Per 16-position step: the next step's A fragments are read
-  // from LDS, this step's two operands are unpacked and MT·2 products issued;
+  // from LDS, this step's NB operands are unpacked and MT·NB products issued;
   // the scheduling barriers spread the VALU work between the matrix
   // instructions (left alone the compiler unpacks a whole group first, and
   // reads each fragment right before its use).
@@ -394,8 +411,8 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
         __builtin_amdgcn_sched_group_barrier(0x100, MT, 0);   // LDS reads
 #pragma unroll
         for (int u = 0; u < NB * MT; ++u) {
-          __builtin_amdgcn_sched_group_barrier(0x002, 8 / MT, 0);   // VALU
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);               // MFMA
+          __builtin_amdgcn_sched_group_barrier(0x002, 8 / MT, 0);       // VALU
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);            // MFMA
         }
       }
       // D: lane l, v: token 8·(v / 4) + 4·(l / 32) + v % 4, row l % 32

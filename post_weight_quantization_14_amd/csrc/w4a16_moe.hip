@@ -11,8 +11,15 @@
 // gather between them.
 //
 // Launches for up to 64 tokens: router (a workgroup per token; it also gathers
-// the token into each chosen expert's column order), gate/up and down (some
-// workgroups per active expert, each a share of its row tiles), combine.
+// the token into each chosen expert's column order; its logits come from a
+// launch of their own where there are many), gate/up and down (some workgroups
+// per active expert, each a share of its row tiles), combine.  A token or a few
+// take two: see below.
+//
+// Bound by the chosen experts' codes and parameters from HBM: 64 tokens, 64
+// experts of 2048 x 1024, top 6: gate/up 39 us = 4.2 TB/s, down 25 us, router
+// 11 us, 83 us in all; 1 token, 8 experts of 4096 x 11008, top 2: 33 us and
+// 20 us, 55 us in all.
 #include <algorithm>
 
 #include "w4a16_device.hpp"
@@ -712,17 +719,8 @@ bool moe_is_small(const gptq_moe_config& c, int64_t tokens, int planes, const Mo
 }
 
 template <class A, class K>
-gptq_status moe_launch_any(K kernel, dim3 grid, size_t lds, const A& a, hipStream_t stream) {
+gptq_status moe_launch(K kernel, dim3 grid, size_t lds, const A& a, hipStream_t stream) {
   if (lds > 32768)
-    GPTQ_HIP_CHECK(hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
-  hipLaunchKernelGGL(kernel, grid, dim3(kL4Threads), lds, stream, a);
-  GPTQ_LAUNCH_CHECK();
-  return GPTQ_OK;
-}
-
-template <class K>
-gptq_status moe_launch(K kernel, dim3 grid, size_t lds, const MoeExpertArgs& a, hipStream_t stream) {
-  if (lds > 65536)
     GPTQ_HIP_CHECK(hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
   hipLaunchKernelGGL(kernel, grid, dim3(kL4Threads), lds, stream, a);
   GPTQ_LAUNCH_CHECK();
@@ -879,9 +877,9 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
       const size_t raw = (size_t)tk * (size_t)round_up(h, 8) * 2, red = (size_t)kL4Waves * 2 * g.quads * 64 * sizeof(float);
       lds = rows + std::max(raw, red);
       switch (steps(L.gu)) {
-        case 1: GPTQ_TRY(moe_launch_any(moe_small_gate_up_kernel<1>, ggrid, lds, sa, stream)); break;
-        case 2: GPTQ_TRY(moe_launch_any(moe_small_gate_up_kernel<2>, ggrid, lds, sa, stream)); break;
-        default: GPTQ_TRY(moe_launch_any(moe_small_gate_up_kernel<4>, ggrid, lds, sa, stream)); break;
+        case 1: GPTQ_TRY(moe_launch(moe_small_gate_up_kernel<1>, ggrid, lds, sa, stream)); break;
+        case 2: GPTQ_TRY(moe_launch(moe_small_gate_up_kernel<2>, ggrid, lds, sa, stream)); break;
+        default: GPTQ_TRY(moe_launch(moe_small_gate_up_kernel<4>, ggrid, lds, sa, stream)); break;
       }
       MoeSmallDownArgs sd;
       sd.x = d;
@@ -899,8 +897,8 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
             (size_t)kL4Waves * sd.x.quads * 64 * sizeof(float);
       const dim3 sgrid((unsigned)wgs);
 #define MOE_SMALL_DOWN(GS)                                                                                       \
-  GPTQ_TRY(d.planes == 3 ? moe_launch_any(moe_small_down_kernel<GS, 3>, sgrid, lds, sd, stream)                  \
-                         : moe_launch_any(moe_small_down_kernel<GS, 2>, sgrid, lds, sd, stream))
+  GPTQ_TRY(d.planes == 3 ? moe_launch(moe_small_down_kernel<GS, 3>, sgrid, lds, sd, stream)                  \
+                         : moe_launch(moe_small_down_kernel<GS, 2>, sgrid, lds, sd, stream))
       switch (steps(L.down)) {
         case 1: MOE_SMALL_DOWN(1); break;
         case 2: MOE_SMALL_DOWN(2); break;
@@ -909,19 +907,13 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
 #undef MOE_SMALL_DOWN
       continue;
     }
-    if (r.logits) {
-      const size_t llds = (size_t)round_up(h, 8) * 2;
-      hipLaunchKernelGGL(moe_logits_kernel, dim3((unsigned)ceil_div(cfg.experts, 16), (unsigned)tk), dim3(1024), llds,
-                         stream, r);
-      GPTQ_LAUNCH_CHECK();
-    }
-    const size_t rlds = (size_t)round_up((int64_t)r.parts * cfg.experts, 2) * sizeof(double) +
-                        (size_t)round_up(cfg.experts, 4) * sizeof(int) + (size_t)round_up(h, 8) * 2;
-    if (rlds > 65536)
-      GPTQ_HIP_CHECK(hipFuncSetAttribute((const void*)moe_router_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)rlds));
-    hipLaunchKernelGGL(moe_router_kernel, dim3((unsigned)tk), dim3(1024), rlds, stream, r);
-    GPTQ_LAUNCH_CHECK();
-
+    const size_t xlds = (size_t)round_up(h, 8) * 2;   // a token's row
+    if (r.logits)
+      GPTQ_TRY(moe_launch(moe_logits_kernel, dim3((unsigned)ceil_div(cfg.experts, 16), (unsigned)tk), xlds, r, stream));
+    GPTQ_TRY(moe_launch(moe_router_kernel, dim3((unsigned)tk),
+                        (size_t)round_up((int64_t)r.parts * cfg.experts, 2) * sizeof(double) +
+                            (size_t)round_up(cfg.experts, 4) * sizeof(int) + xlds,
+                        r, stream));
     switch (steps(L.gu)) {
       case 1: GPTQ_TRY(launch_gate_up<1>(ggrid, lds, in_lds, g, stream)); break;
       case 2: GPTQ_TRY(launch_gate_up<2>(ggrid, lds, in_lds, g, stream)); break;

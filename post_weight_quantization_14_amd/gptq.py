@@ -454,7 +454,18 @@ def _uint8(name: str, t: torch.Tensor) -> int:
     return t.nbytes
 
 
-def _with_workspace(call, nbytes, X: torch.Tensor, workspace: Optional[torch.Tensor], where: str) -> None:
+def _empty(shape, dtype: torch.dtype, X: torch.Tensor, stream) -> torch.Tensor:
+    """A new tensor whose memory the stream of the call may write at once: torch
+    hands out memory that is free in the order of the stream it is asked on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=X.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=X.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=X.device)
+
+
+def _with_workspace(call, nbytes, X: torch.Tensor, workspace: Optional[torch.Tensor], stream, where: str) -> None:
     """call(pointer, bytes) -> status on the caller's workspace (it then belongs
     to this call until its work is done), or on a new one of nbytes() bytes if
     there is none or the library finds it too small."""
@@ -462,7 +473,7 @@ def _with_workspace(call, nbytes, X: torch.Tensor, workspace: Optional[torch.Ten
         st = call(workspace.data_ptr(), _uint8("workspace", workspace))
         if st != _lib.GPTQ_ERR_WORKSPACE:
             return _check(st, where)
-    ws = torch.empty(nbytes(), dtype=torch.uint8, device=X.device)
+    ws = _empty(nbytes(), torch.uint8, X, stream)
     _check(call(ws.data_ptr(), ws.nbytes), where)
 
 
@@ -525,7 +536,7 @@ def gptq_w4a16_linear(X: torch.Tensor, packed: torch.Tensor, m: int, n: int, gro
     tokens = X.shape[0]
     _on(X, packed=packed, bias=bias, residual=residual, Y=Y, workspace=workspace)
     if Y is None:
-        Y = torch.empty(tokens, m, dtype=out_dtype, device=X.device)
+        Y = _empty((tokens, m), out_dtype, X, stream)
     e = _lib.GptqEpilogue(activation=_activation_code(activation))
     if bias is not None:
         e.bias, e.bias_dtype = _vector("bias", bias, m), _dtype_code(bias)
@@ -538,7 +549,7 @@ def gptq_w4a16_linear(X: torch.Tensor, packed: torch.Tensor, m: int, n: int, gro
     s = _stream_on(X, stream)
     with _device(X):
         _with_workspace(lambda ws, nbytes: fn(*args, ws, nbytes, s),
-                        lambda: gptq_w4a16_linear_workspace_bytes(tokens, m, n, group_size), X, workspace,
+                        lambda: gptq_w4a16_linear_workspace_bytes(tokens, m, n, group_size), X, workspace, stream,
                         "gptq_w4a16_linear")
     return Y
 
@@ -587,7 +598,7 @@ def gptq_w4a16_glu(X: torch.Tensor, packed: torch.Tensor, m: int, n: int, group_
     tokens = X.shape[0]
     _on(X, packed=packed, gate_bias=gate_bias, up_bias=up_bias, Y=Y, workspace=workspace)
     if Y is None:
-        Y = torch.empty(tokens, m, dtype=out_dtype, device=X.device)
+        Y = _empty((tokens, m), out_dtype, X, stream)
     some = gate_bias if gate_bias is not None else up_bias
     if gate_bias is not None and up_bias is not None and gate_bias.dtype != up_bias.dtype:
         raise TypeError("gate_bias and up_bias must have one dtype")
@@ -598,7 +609,7 @@ def gptq_w4a16_glu(X: torch.Tensor, packed: torch.Tensor, m: int, n: int, group_
     s = _stream_on(X, stream)
     with _device(X):
         _with_workspace(lambda ws, nbytes: fn(*args, ws, nbytes, s),
-                        lambda: gptq_w4a16_glu_workspace_bytes(tokens, m, n, group_size), X, workspace,
+                        lambda: gptq_w4a16_glu_workspace_bytes(tokens, m, n, group_size), X, workspace, stream,
                         "gptq_w4a16_glu")
     return Y
 
@@ -703,17 +714,16 @@ def gptq_w4a16_moe(X: torch.Tensor, router: torch.Tensor, packed: torch.Tensor, 
     int32 [tokens, top_k], topk_weights fp32 [tokens, top_k])."""
     ldx = _bf16_rows(X, cfg.hidden)
     tokens = X.shape[0]
-    dev = X.device
     _on(X, router=router, packed=packed, residual=residual, Y=Y, topk_ids=topk_ids, topk_weights=topk_weights,
         workspace=workspace)
     if tuple(router.shape) != (cfg.experts, cfg.hidden) or not router.is_contiguous():
         raise ValueError(f"router must be a contiguous [{cfg.experts}, {cfg.hidden}]")
     if Y is None:
-        Y = torch.empty(tokens, cfg.hidden, dtype=out_dtype, device=dev)
+        Y = _empty((tokens, cfg.hidden), out_dtype, X, stream)
     if topk_ids is None:
-        topk_ids = torch.empty(tokens, cfg.top_k, dtype=torch.int32, device=dev)
+        topk_ids = _empty((tokens, cfg.top_k), torch.int32, X, stream)
     if topk_weights is None:
-        topk_weights = torch.empty(tokens, cfg.top_k, dtype=torch.float32, device=dev)
+        topk_weights = _empty((tokens, cfg.top_k), torch.float32, X, stream)
     _int32(topk_ids=topk_ids)
     if topk_weights.dtype != torch.float32 or not topk_weights.is_contiguous():
         raise ValueError("topk_weights must be contiguous float32")
@@ -729,7 +739,7 @@ def gptq_w4a16_moe(X: torch.Tensor, router: torch.Tensor, packed: torch.Tensor, 
     s = _stream_on(X, stream)
     with _device(X):
         _with_workspace(lambda ws, nbytes: fn(*args, ws, nbytes, s),
-                        lambda: int(lib().gptq_w4a16_moe_workspace_bytes(ctypes.byref(c), tokens)), X, workspace,
+                        lambda: int(lib().gptq_w4a16_moe_workspace_bytes(ctypes.byref(c), tokens)), X, workspace, stream,
                         "gptq_w4a16_moe")
     return Y, topk_ids, topk_weights
 

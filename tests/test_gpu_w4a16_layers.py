@@ -485,6 +485,32 @@ def test_two_streams_at_once(pq, tokens):
         assert torch.equal(r.y, w)
 
 
+def test_calls_on_another_stream_allocate_for_it(pq):
+    """With stream= given and neither output nor workspace, both come from
+    memory that is that stream's: results hold while the current stream reuses
+    what it freed."""
+    Run = _three(pq, 24)
+    r = Run()
+    r.x.copy_(H.activations(24, 256, seed=5).cuda())
+    want = r().clone()
+    m, n = 256, 512
+    rng = np.random.default_rng(3)
+    w = H.weight(m, n, 4, 64, rng, H.group_index(n, 64, rng, True))
+    packed = pq.gptq_w4a16_pack(*H.gpu(w), n, 4, 64)
+    X = H.activations(40, n, seed=6).cuda()
+    ref = pq.gptq_w4a16_linear(X, packed, m, n, 64)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for handle in (s, s.cuda_stream):
+        outs = []
+        for _ in range(8):
+            outs.append(pq.gptq_w4a16_linear(X, packed, m, n, 64, stream=handle))
+            torch.empty(1 << 20, dtype=torch.uint8, device="cuda").fill_(255)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, ref) for o in outs)
+    assert torch.equal(r(), want)
+
+
 def test_empty_batches_and_small_workspaces(pq):
     m, n = 32, 64
     rng = np.random.default_rng(1)
