@@ -62,12 +62,30 @@ struct L4Epilogue {
   const void *bias, *bias2, *res;
   void* Y;
   int64_t ldr, ldy;
-  // N tokens (runs of 4, 8 apart, from t) of one row: every residual load is
-  // in flight before the first is used.  Under the type's branch and a range
-  // check each, they would be one memory latency apart.
+  // N tokens (runs of 4, 8 apart, from t) of one row.  The residual loads of
+  // them all are in flight together, a caller's further blocks may be loaded
+  // before the first is finished: under the type's branch and a range check
+  // each, they would be one memory latency apart.
+  template <int N>
+  __device__ __forceinline__ void residual(int64_t t, int64_t tokens, int64_t r, int64_t m, float (&rv)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) rv[i] = 0.f;
+    if (!res || r >= m || t >= tokens) return;
+    if (res_dt == GPTQ_FP32) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)   // past the last token: the last one's, not used
+        rv[i] = static_cast<const float*>(res)[std::min<int64_t>(t + 8 * (i / 4) + (i & 3), tokens - 1) * ldr + r];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        rv[i] = __uint_as_float(
+            (uint32_t) static_cast<const uint16_t*>(res)[std::min<int64_t>(t + 8 * (i / 4) + (i & 3), tokens - 1) * ldr + r]
+            << 16);
+    }
+  }
   template <int N, bool GATED>
   __device__ __forceinline__ void block(int64_t t, int64_t tokens, int64_t r, int64_t m, const float (&v)[N],
-                                        const float (&u)[N]) const {
+                                        const float (&u)[N], const float (&rv)[N]) const {
     if (r >= m || t >= tokens) return;
     const float b0 = bias ? l4_load(bias, bias_dt, r) : 0.f;
     float z[N];
@@ -75,30 +93,12 @@ struct L4Epilogue {
       const float b1 = bias2 ? l4_load(bias2, bias_dt, r) : 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) z[i] = l4_activate(v[i] + b0, act) * (u[i] + b1);
+    } else if (act == GPTQ_ACT_NONE) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = v[i] + b0 + rv[i];
     } else {
-      float rv[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) rv[i] = 0.f;
-      if (res) {
-        int64_t at[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) at[i] = std::min<int64_t>(t + 8 * (i / 4) + (i & 3), tokens - 1) * ldr + r;
-        if (res_dt == GPTQ_FP32) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) rv[i] = static_cast<const float*>(res)[at[i]];
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            rv[i] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(res)[at[i]] << 16);
-        }
-      }
-      if (act == GPTQ_ACT_NONE) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = v[i] + b0 + rv[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = l4_activate(v[i] + b0, act) + rv[i];
-      }
+      for (int i = 0; i < N; ++i) z[i] = l4_activate(v[i] + b0, act) + rv[i];
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -488,8 +488,13 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
       const int64_t t = t0 + 32 * (MT * tg + mt) + 8 * q + 4 * (lane >> 5);
       const int64_t r = (rb * RG + rg) * (GATED ? 32 : 64) + (lane & 31);
       const float g4[4] = {z[0][0], z[0][1], z[0][2], z[0][3]}, u4[4] = {z[1][0], z[1][1], z[1][2], z[1][3]};
-      a.ep.template block<4, GATED>(t, a.tokens, r, a.m, g4, u4);
-      if (!GATED) a.ep.template block<4, false>(t, a.tokens, r + 32, a.m, u4, u4);
+      float r0[4], r1[4];
+      if (!GATED) {
+        a.ep.residual(t, a.tokens, r, a.m, r0);
+        a.ep.residual(t, a.tokens, r + 32, a.m, r1);
+      }
+      a.ep.template block<4, GATED>(t, a.tokens, r, a.m, g4, u4, r0);
+      if (!GATED) a.ep.template block<4, false>(t, a.tokens, r + 32, a.m, u4, u4, r1);
     }
     return;
   }
@@ -508,33 +513,36 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
               f32x4_t{y[mt][b][4 * q], y[mt][b][4 * q + 1], y[mt][b][4 * q + 2], y[mt][b][4 * q + 3]};
     return;
   }
-  const int64_t rbase = (rb * RG + rg) * (GATED ? 16 * NB : 32 * NB) + (lane & (GATED && NB == 1 ? 15 : 31));
+  const int64_t rbase = (rb * RG + rg) * (GATED ? 16 : 32) + (lane & (GATED ? 15 : 31));
+  static_assert(KG > 1 || NB == 1, "the tiles of one group of waves have one operand");
+  float rv[MT][16];
+  if (!GATED) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) a.ep.residual(t0 + 32 * (MT * tg + mt) + 4 * (lane >> 5), a.tokens, rbase, a.m, rv[mt]);
+  }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const int64_t t = t0 + 32 * (MT * tg + mt) + 4 * (lane >> 5);
+    if (!GATED) {
+      float v[16];
 #pragma unroll
-    for (int q = 0; q < 4; q += 2) {   // 8 tokens at a time: tokens t + 8q + {0..3, 8..11}
-      float v0[8], v1[8];
+      for (int i = 0; i < 16; ++i) v[i] = y[mt][0][i];
+      a.ep.template block<16, false>(t, a.tokens, rbase, a.m, v, v, rv[mt]);
+      continue;
+    }
+    // gate sits in the lower 16 lanes of each 32, up in the upper: of each 8
+    // tokens (t + 8q + {0..3, 8..11}) they trade, and finish four each
 #pragma unroll
-      for (int v = 0; v < 8; ++v) {
-        v0[v] = y[mt][0][4 * q + v];
-        v1[v] = y[mt][NB - 1][4 * q + v];
+    for (int q = 0; q < 4; q += 2) {
+      float g4[4], u4[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float lo = y[mt][0][4 * q + v], hi = y[mt][0][4 * q + 4 + v];
+        const float got = __shfl_xor(half ? lo : hi, 16);
+        g4[v] = half ? got : lo;
+        u4[v] = half ? hi : got;
       }
-      if constexpr (GATED && NB == 1) {
-        // gate sits in the lower 16 lanes of each 32, up in the upper: they
-        // trade, and finish four tokens each
-        float g4[4], u4[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float got = __shfl_xor(half ? v0[v] : v0[4 + v], 16);
-          g4[v] = half ? got : v0[v];
-          u4[v] = half ? v0[4 + v] : got;
-        }
-        a.ep.template block<4, true>(t + 8 * (q + half), a.tokens, rbase, a.m, g4, u4);
-      } else {
-        a.ep.template block<8, GATED>(t + 8 * q, a.tokens, rbase, a.m, v0, v1);
-        if (!GATED && NB == 2) a.ep.template block<8, false>(t + 8 * q, a.tokens, rbase + 32, a.m, v1, v1);
-      }
+      a.ep.template block<4, true>(t + 8 * (q + half), a.tokens, rbase, a.m, g4, u4, u4);
     }
   }
 }
@@ -585,7 +593,9 @@ __global__ __launch_bounds__(256) void l4_reduce_kernel(L4GemmArgs a) {
   const int64_t t = tb * (32 * MT * TG) + 32 * (MT * tg + mt) + 8 * q + 4 * (lane >> 5);
   const int64_t r = (rb * RG + rg) * (GATED ? 16 * NB : 32 * NB) + 32 * b + (lane & (GATED && NB == 1 ? 15 : 31));
   const float g4[4] = {v0[0], v0[1], v0[2], v0[3]}, u4[4] = {v1[0], v1[1], v1[2], v1[3]};
-  a.ep.template block<4, GATED>(t, a.tokens, r, a.m, g4, u4);
+  float rv[4];
+  if (!GATED) a.ep.residual(t, a.tokens, r, a.m, rv);
+  a.ep.template block<4, GATED>(t, a.tokens, r, a.m, g4, u4, rv);
 }
 
 }  // namespace
@@ -617,19 +627,20 @@ gptq_status run_w4a16_glu_pack(const L4PairSource& src, const int32_t* g_idx, co
 }
 
 namespace {
-// the tile for a number of tokens, and the K slices that fill the GPU
+// a tile, and the K slices that fill the GPU
 struct L4Shape {
   int tokens = 128;                 // 32, 64 or 128, x 128 packed rows
   int64_t tblocks = 0, rblocks = 0;
   int64_t whole = 0;                // tiles that are not split
   int splits = 1, chunks = 0;
+  double us = 0.0;                  // estimate of its kernels
 };
 // Full rounds of workgroups take whole tiles; what is left over, or a call of
 // less than a round, is split along K to fill one (11008 x 4096, 256 tokens:
 // 54 us with 172 whole tiles, 43 us with each in two slices).
-L4Shape l4_shape(int64_t tokens, int64_t packed_rows, int64_t kc) {
+L4Shape l4_tile(int tile_tokens, int64_t tokens, int64_t packed_rows, int64_t kc) {
   L4Shape s;
-  s.tokens = tokens > 64 ? 128 : tokens > 32 ? 64 : 32;
+  s.tokens = tile_tokens;
   s.tblocks = ceil_div(tokens, s.tokens);
   s.rblocks = ceil_div(packed_rows, 128);
   const int64_t tiles = s.tblocks * s.rblocks;
@@ -645,13 +656,32 @@ L4Shape l4_shape(int64_t tokens, int64_t packed_rows, int64_t kc) {
     s.splits = (int)ceil_div(kc, s.chunks);
   }
   s.whole = s.splits > 1 ? tiles - left : tiles;
+  // Microseconds, fitted to runs of 4096..11008 wide weights: a step (a chunk;
+  // four, of the tiles with four groups) and a workgroup's start and end.  Two
+  // 128-token workgroups share a CU and take as long as one after the other.
+  const double step = s.tokens == 128 ? 1.15 : s.tokens == 64 ? 2.6 : 1.9, over = s.tokens == 128 ? 7.0 : 5.0;
+  auto rounds_us = [&](int64_t wgs, int64_t chunks) {
+    const double steps = s.tokens == 128 ? (double)chunks : (double)ceil_div(chunks, 4);
+    return (double)ceil_div(wgs, 256) * steps * step + (double)ceil_div(wgs, round) * over;
+  };
+  s.us = (s.whole ? rounds_us(s.whole, kc) : 0.0) + (s.splits > 1 ? rounds_us(left * s.splits, s.chunks) + 4.0 : 0.0);
   return s;
 }
+L4Shape l4_shape(int64_t tokens, int64_t packed_rows, int64_t kc) {
+  L4Shape best = l4_tile(32, tokens, packed_rows, kc);
+  for (int t : {64, 128}) {
+    const L4Shape s = l4_tile(t, tokens, packed_rows, kc);
+    if (s.us < best.us) best = s;
+  }
+  return best;
+}
 constexpr size_t kL4GatherLds = 65536;    // rows up to 32768 columns are gathered through LDS
-// the decode kernel's tiles of 16 tokens, for more than one of them only while
-// tokens x weight is two rounds of workgroups (1024 x 1024, 64 tokens: 13.3 us
-// by the tiled product and its launches, 10 us here)
-constexpr int64_t kL4DecodeWgs = 512;
+// the decode kernel's tiles of 16 tokens against the tiled product: its rounds
+// of workgroups, each a share of the chunks and about 2.5 us of its own, and
+// one launch less
+double l4_decode_us(int64_t tiles, int64_t units, int64_t kc, int rt) {
+  return (double)ceil_div(tiles * units, 256) * ((double)(kc * rt) / 16.0 + 2.5);
+}
 constexpr int64_t kL4GatherMax = 65536;   // up to this many elements of X' it gathers them itself
 constexpr size_t kL4MaxLds = 158 * 1024;
 constexpr int64_t kL4Cus = 256;
@@ -755,7 +785,8 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
     bool decode = false, gather = false;
     size_t dlds = 0;
     const int64_t ttiles = ceil_div(tk, 16);
-    if (ttiles == 1 || ttiles * st.units <= kL4DecodeWgs) {
+    const L4Shape sh = l4_shape(tk, L.mt * kL4Rows, L.kc);
+    if (ttiles == 1 || l4_decode_us(ttiles, st.units, L.kc, gated ? 2 : 1) < sh.us + 3.0) {
       const int64_t tt = std::min<int64_t>(tk, 16);   // tokens of a tile
       d.quads = (int)ceil_div(tt, 4);
       const size_t rows = (size_t)tt * (size_t)(L.n128 + kL4Pad) * 2;
@@ -807,7 +838,6 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
       GPTQ_TRY(launch_l4_decode(d, gs, gated, gather, dim3(grid, (unsigned)ttiles), dlds, stream));
       continue;
     }
-    const L4Shape sh = l4_shape(tk, L.mt * kL4Rows, L.kc);
     L4GemmArgs g;
     g.Xp = Xp;
     g.sums = xs;

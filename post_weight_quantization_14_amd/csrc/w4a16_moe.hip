@@ -360,11 +360,13 @@ __device__ __forceinline__ void moe_expert_units(const MoeExpertArgs& a, MoeList
   const int xrow = (int)a.k128 + kL4Pad;
   uint16_t* xsh = reinterpret_cast<uint16_t*>(lds);
   float* red = reinterpret_cast<float*>(lds + (LDS ? (size_t)a.pass * NP * xrow * 2 : 0));
-  for (int p0 = 0; p0 < list.count; p0 += a.pass) {
+  // grid z deals the passes of an expert of many tokens to workgroups
+  bool again = false;
+  for (int p0 = blockIdx.z * a.pass; p0 < list.count; p0 += gridDim.z * a.pass) {
     const int np = std::min(a.pass, list.count - p0);
     auto fill = [&] {
       if (!LDS) return;
-      if (p0) __syncthreads();   // the pass before has been read
+      if (again) __syncthreads();   // the pass before has been read
       const int pieces = (int)(a.k128 / 8);
       for (int i = tid; i < np * NP * pieces; i += kL4Threads) {
         const int q = i / pieces, k = 8 * (i % pieces);   // row q = token q / NP, plane q % NP
@@ -392,6 +394,7 @@ __device__ __forceinline__ void moe_expert_units(const MoeExpertArgs& a, MoeList
       const L4GlobalA af{a.A + (int64_t)list.pair[p0 + q] * NP * a.k128 + 8 * (lane >> 4), a.k128};
       l4_units<GS, RT, NP, B, NP == 3>(st, first, step, af, fill, end);
     }
+    again = true;
   }
 }
 
@@ -851,12 +854,15 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
     void* Y = static_cast<char*>(c.Y) + (size_t)(t0 * c.ldy) * ysz;
     // the workgroups of the GPU dealt over the experts that can be active
     const int64_t slots = std::min<int64_t>(cfg.experts, (int64_t)tk * cfg.top_k);
-    const int64_t share = std::max<int64_t>(1, 256 / slots);
+    // where an expert has more tokens than a pass on average, side by side
+    const int64_t passes = ceil_div((int64_t)tk * cfg.top_k, (int64_t)cfg.experts * kMoePass);
+    const int64_t share = std::max<int64_t>(1, 256 / (slots * passes));
     const int64_t gw = std::min<int64_t>(share, g.st.units), dw = std::min<int64_t>(share, d.st.units);
     g.tokens = d.tokens = tk;
     bool in_lds = false;
     size_t lds = moe_plan(g, tk, 1, 2, gw, &in_lds);
-    const dim3 ggrid((unsigned)std::min<int64_t>(gw, ceil_div(g.st.units, kL4Waves >> g.st.kslog)), (unsigned)slots);
+    const dim3 ggrid((unsigned)std::min<int64_t>(gw, ceil_div(g.st.units, kL4Waves >> g.st.kslog)), (unsigned)slots,
+                     (unsigned)passes);
     if (moe_is_small(cfg, tk, g.planes, L)) {
       MoeSmallArgs sa;
       sa.x = g;
@@ -920,7 +926,8 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
       default: GPTQ_TRY(launch_gate_up<4>(ggrid, lds, in_lds, g, stream)); break;
     }
     lds = moe_plan(d, tk, d.planes, 1, dw, &in_lds);
-    const dim3 dgrid((unsigned)std::min<int64_t>(dw, ceil_div(d.st.units, kL4Waves >> d.st.kslog)), (unsigned)slots);
+    const dim3 dgrid((unsigned)std::min<int64_t>(dw, ceil_div(d.st.units, kL4Waves >> d.st.kslog)), (unsigned)slots,
+                     (unsigned)passes);
     switch (steps(L.down)) {
       case 1: GPTQ_TRY(launch_down<1>(dgrid, lds, in_lds, d, stream)); break;
       case 2: GPTQ_TRY(launch_down<2>(dgrid, lds, in_lds, d, stream)); break;
