@@ -109,18 +109,32 @@ __device__ __forceinline__ double moe_logit(const uint16_t* x, const void* R, in
       }
     }
   } else {
-    for (int b = 64 * part; b < h; b += 256 * parts) {
-      float w[4];
+    // rows that are not 16-byte aligned: element by element, 16 in flight (the
+    // type's branch outside: inside, each load is a block with its own wait)
+    constexpr int U = 16;
+    for (int b = 64 * part; b < h; b += 64 * U * parts) {
+      float w[U];
+      if (r_dt == GPTQ_FP32) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = b + 64 * parts * u + lane;
-        w[u] = l4_load(R, r_dt, e * h + (i < h ? i : 0));
-        if (i >= h) w[u] = 0.f;
+        for (int u = 0; u < U; ++u) {
+          const int i = b + 64 * parts * u + lane;
+          w[u] = static_cast<const float*>(R)[e * h + (i < h ? i : 0)];
+        }
+      } else {
+        uint16_t q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = b + 64 * parts * u + lane;
+          q[u] = static_cast<const uint16_t*>(R)[e * h + (i < h ? i : 0)];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = __uint_as_float((uint32_t)q[u] << 16);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int i = b + 64 * parts * u + lane;
-        s0 = fma((double)__uint_as_float((uint32_t)x[i < h ? i : 0] << 16), (double)w[u], s0);
+        const float xi = __uint_as_float((uint32_t)x[i < h ? i : 0] << 16);
+        s0 = fma(i < h ? (double)xi : 0.0, i < h ? (double)w[u] : 0.0, s0);
       }
     }
   }
