@@ -177,8 +177,19 @@ __global__ __launch_bounds__(kL4Threads) void l4_decode_kernel(L4DecodeArgs a) {
 }
 
 // ---------------------------------------------------------------- many tokens
+// v = h + m + l, exactly: 8 of its 24 bits each
+struct L4Planes {
+  uint32_t h, m, l;   // bf16 values in the upper halves
+};
+__device__ __forceinline__ L4Planes l4_planes(float v) {
+  const uint32_t h = __float_as_uint(v) & 0xffff0000u;
+  const float r = v - __uint_as_float(h);
+  const uint32_t m = __float_as_uint(r) & 0xffff0000u;
+  return {h, m, __float_as_uint(r - __uint_as_float(m))};
+}
+
 // X' = X[:, order] and its group sums, groups-major (sums[c·NG + g][t], for the
-// tile kernel's contiguous copies).  A row of X is read once, 16 bytes a
+// tile kernel's contiguous copies, cut into three bf16 planes: an operand).  A row of X is read once, 16 bytes a
 // thread, into LDS and gathered from there: 2-byte loads at scattered columns
 // cost the memory pipe a cycle or more a lane (2048 x 4096: 13 us, through
 // LDS 8.5), LDS serves 64 of them in a few cycles.  Thread: 8 positions; GS·4
@@ -187,7 +198,7 @@ __global__ __launch_bounds__(kL4Threads) void l4_decode_kernel(L4DecodeArgs a) {
 template <int GS, bool LDS>
 __global__ __launch_bounds__(512) void l4_gather_kernel(const uint16_t* __restrict__ X, int64_t ldx,
                                                         const int32_t* __restrict__ order, int64_t n, int64_t n128,
-                                                        uint16_t* __restrict__ Xp, float* __restrict__ sums,
+                                                        uint16_t* __restrict__ Xp, uint2* __restrict__ sums,
                                                         int64_t tokens, int64_t tpad, int vec) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x;
@@ -222,14 +233,17 @@ __global__ __launch_bounds__(512) void l4_gather_kernel(const uint16_t* __restri
       u32x4_t{v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
 #pragma unroll
   for (int d = 1; d < 4 * GS; d <<= 1) s += __shfl_xor(s, d);
-  if ((tid & (4 * GS - 1)) == 0) sums[(p0 / (32 * GS)) * tpad + t] = s;
+  if ((tid & (4 * GS - 1)) == 0) {
+    const L4Planes p = l4_planes(s);
+    sums[(p0 / (32 * GS)) * tpad + t] = make_uint2((p.h >> 16) | p.m, p.l >> 16);
+  }
 }
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 
 struct L4GemmArgs {
   const uint16_t* Xp;     // [tokens][n128]
-  const float* sums;      // [kc·NG][tpad]
+  const uint2* sums;      // [kc·NG][tpad]: three bf16 planes
   const float2* params;
   const u32x4_t* codes;
   float* part;            // split tiles: [splits][tiles - whole][fragments]
@@ -247,25 +261,26 @@ struct L4GemmArgs {
 //
 // X' comes through LDS (direct copies, two slots), the codes straight into
 // registers in operand order: 4 bits a weight would be 16 as operands in LDS.
-// Bound by the issue of matrix and vector instructions, which a SIMD does one
-// after the other here (its cycles are 32 per product plus 4 per vector
-// instruction in every variant tried, within 5 %), and by the clock that the
-// power allows (1.9-2.05 GHz): the vector work per product decides the shape.
-// A wave of 128 tokens x 32 rows unpacks each operand once for four products
-// (64 x 64: two) and runs 2048 x 22016 x 4096 in 378 us = 0.98 PFLOP/s against
-// 396; the library's bf16 product of that shape takes 424 us.  Tried and not
-// kept: two chunks in flight behind a second barrier (+2 %), the fold between
-// the next products (+7 %: it reads the A fragments twice), A fragments two
-// steps ahead (0 %).
+// Bound by power: 2048 x 22016 x 4096 takes 375 us = 0.99 PFLOP/s with the
+// matrix cores busy 58 % of the cycles and the clock down to 1.8 GHz (products
+// alone, from registers, run at 1.92); the library's bf16 product of that shape
+// takes 424 us.  A wave of 128 tokens x 32 rows unpacks an operand once for four
+// products, one of 64 x 64 halves the LDS reads instead: 412 and 423 us for the
+// whole call.  The zero points' term is one more product per group, not a fold
+// with the sums: 16 vector instructions and 4 LDS reads fewer for each 32 x 32
+// (10 % fewer cycles, 2 % of the time).  Tried and not kept: two chunks in
+// flight behind a second barrier (+2 %), the fold between the next products
+// (+7 %: it reads the A fragments twice), A fragments two steps ahead (0 %),
+// waves of 128 x 64, one per SIMD (+35 %).
 template <int GS, int MT, int NB, int TG, int RG, int KG>
 struct L4Tile {
   static constexpr int kTokens = 32 * MT * TG, kRows = 32 * NB * RG, kGroup = TG * RG, kThreads = 64 * kGroup * KG;
   static constexpr int kNG = 4 / GS;
   static constexpr int kX = kTokens * 256;                                 // X' of one chunk
-  static constexpr int kBytes = kX + ((kNG * kTokens * 4 + 255) & ~255);   // and its group sums
+  static constexpr int kBytes = kX + kNG * kTokens * 8;   // and its group sums
   static constexpr int kXCopies = kX / 1024 / kGroup;                      // 1 KB copies per wave
   static_assert(kX % (1024 * kGroup) == 0, "copies split evenly over the waves");
-  static_assert(kTokens % 32 == 0, "sums are copied 32 or 64 floats at a time");
+  static_assert(kTokens <= 128, "the sums of a group are one copy of up to 64 lanes, two tokens each");
 };
 
 template <int GS, int MT, int NB, int TG, int RG, int KG, bool GATED>
@@ -302,28 +317,23 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
     const int q = (gw * U + u) * 64 + lane, t = q >> 4, pc = (q & 15) ^ (t & 15);
     xoff[u] = (int32_t)(t * a.n128 * 2 + pc * 16);
   }
-  // copies of the sums, 4 bytes a lane, 64 (or 32) tokens each, spread over
-  // the group's waves
-  constexpr int SW = Tl::kTokens >= 64 ? 64 : 32;          // tokens per copy
-  constexpr int SC = NG * Tl::kTokens / SW;
+  // copies of the sums, two tokens a lane, a group's each, spread over the waves
   const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<float*>(a.sums + t0), 0, (int32_t)std::min<int64_t>((a.kc * NG * a.tpad - t0) * 4, 0x7fffffff),
+      const_cast<uint2*>(a.sums + t0), 0, (int32_t)std::min<int64_t>((a.kc * NG * a.tpad - t0) * 8, 0x7fffffff),
       0x00020000);
-  auto issue = [&](int s, uint8_t* slots) {
+  auto issue = [&](int s, uint8_t* slots, int u0, int u1) {   // copies u0 .. u1 - 1; the sums with the first
     uint8_t* slot = slots + kg * Tl::kBytes;
     const int cc = c0 + std::min(s * KG + kg, nch - 1);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = u0; u < u1; ++u)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)(slot + (gw * U + u) * 1024), 16, xoff[u], cc * 256, 0, 0);
+    if (u0) return;
 #pragma unroll
-    for (int k = 0; k < (SC + Tl::kGroup - 1) / Tl::kGroup; ++k) {
-      const int c = k * Tl::kGroup + gw;
-      if (SC % Tl::kGroup == 0 || c < SC) {
-        const int g = c / (Tl::kTokens / SW), part = c % (Tl::kTokens / SW);
-        if (SW == 64 || lane < 32)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(slot + Tl::kX + c * SW * 4), 4, (part * SW + lane) * 4,
-                                                  (int32_t)((cc * NG + g) * a.tpad * 4), 0, 0);
-      }
+    for (int k = 0; k < (NG + Tl::kGroup - 1) / Tl::kGroup; ++k) {
+      const int g = k * Tl::kGroup + gw;
+      if ((NG % Tl::kGroup == 0 || g < NG) && (Tl::kTokens == 128 || lane < Tl::kTokens / 2))
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(slot + Tl::kX + g * Tl::kTokens * 8), 16, lane * 16,
+                                                (int32_t)((cc * NG + g) * a.tpad * 8), 0, 0);
     }
   };
 
@@ -375,7 +385,7 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
   // the scheduling barriers spread the VALU work between the matrix
   // instructions (left alone the compiler unpacks a whole group first, and
   // reads each fragment right before its use).
-  auto compute = [&](const uint8_t* cur, const Codes& k) {
+  auto compute = [&](const uint8_t* cur, const Codes& k, auto&& ahead) {
     auto frag = [&](int st, int mt) {
       const int t = 32 * (MT * tg + mt) + trow;
       return *reinterpret_cast<const u32x4_t*>(cur + t * 256 + (((2 * st + (lane >> 5)) ^ (t & 15)) * 16));
@@ -389,12 +399,28 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int v = 0; v < 16; ++v) acc[mt][b][v] = 0.f;
+      // -(16 + z)·Σx on the matrix cores too, both in exact bf16 planes: lanes
+      // 0..31 hold the sum's three against z's first two, the others against
+      // its third
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const L4Planes z = l4_planes(-l4_zero(k.p[b][g].y));
+        const uint32_t z0 = lane < 32 ? z.h : z.l, z1 = lane < 32 ? z.m : 0u;
+        const bf16x8_t zp = __builtin_bit_cast(bf16x8_t, u32x4_t{z0 | (z0 >> 16), z0 >> 16, z1 | (z1 >> 16), z1 >> 16});
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint2 sx = *reinterpret_cast<const uint2*>(cur + Tl::kX + (g * Tl::kTokens + 32 * (MT * tg + mt) + trow) * 8);
+          acc[mt][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, u32x4_t{sx.x, sx.y, sx.x, sx.y}),
+                                                               zp, acc[mt][b], 0, 0, 0);
+        }
+      }
       u32x4_t av[2][MT];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) av[0][mt] = frag(g * 2 * GS, mt);
 #pragma unroll
       for (int q = 0; q < 2 * GS; ++q) {
         const int st = g * 2 * GS + q;
+        ahead(st);
         if (q + 1 < 2 * GS) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) av[(q + 1) & 1][mt] = frag(st + 1, mt);
@@ -419,30 +445,33 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4_t sx = *reinterpret_cast<const f32x4_t*>(
-              cur + Tl::kX + (g * Tl::kTokens + 32 * (MT * tg + mt) + 8 * q + 4 * (lane >> 5)) * 4);
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              y[mt][b][4 * q + v] =
-                  fmaf(k.p[b][g].x, fmaf(-l4_zero(k.p[b][g].y), sx[v], acc[mt][b][4 * q + v]), y[mt][b][4 * q + v]);
-        }
+          for (int v = 0; v < 16; ++v) y[mt][b][v] = fmaf(k.p[b][g].x, acc[mt][b][v], y[mt][b][v]);
     }
   };
 
   Codes k0, k1;
-  issue(0, s0);
+  issue(0, s0, 0, U);
   fetch(0, k0);
-  // one step: every copy of this step has landed (all waves', after the
-  // barrier) and every wave is done with the other slot, which the next refills
+  // One step: every copy of this step has landed (all waves', after the
+  // barrier) and every wave is done with the other slot, which the next refills,
+  // two copies at a time between this step's products (all at once right after
+  // the barrier they block the wave: 4 % of the 2048-token pair).  The wait is
+  // the builtin: of one in inline asm the compiler does not know that it covers
+  // the codes, and puts another before their first use.
 #define L4_STEP(s, cur, kcur, nxt, knxt)                                          \
   {                                                                               \
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");      \
-    issue((s) + 1, nxt);                                                          \
-    fetch((s) + 1, knxt);                                                         \
-    if ((s) * KG + kg < nch) compute(cur + kg * Tl::kBytes, kcur);                \
+    asm volatile("" ::: "memory");                                                \
+    __builtin_amdgcn_s_waitcnt(0x0070);   /* vmcnt(0) lgkmcnt(0) */               \
+    __builtin_amdgcn_s_barrier();                                                 \
+    asm volatile("" ::: "memory");                                                \
+    if ((s) * KG + kg < nch)                                                      \
+      compute(cur + kg * Tl::kBytes, kcur, [&](int st) {                          \
+        if (2 * st >= U) return;                                                \
+        issue((s) + 1, nxt, 2 * st, 2 * st + 2);                            \
+        if (st == 0) fetch((s) + 1, knxt);                                        \
+      });                                                                         \
   }
   for (int s = 0; s < steps; s += 2) {
     L4_STEP(s, s0, k0, s1, k1)
@@ -742,7 +771,7 @@ L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n, int64_t packed_rows) {
   p.block = std::min<int64_t>(std::max<int64_t>(tokens, 1), kL4BlockTokens);
   p.tpad = round_up(p.block, 256);
   p.xs_off = align256((size_t)(p.block * n128) * sizeof(uint16_t));
-  p.part_off = p.xs_off + align256((size_t)(p.tpad * (n128 / 32)) * sizeof(float));
+  p.part_off = p.xs_off + align256((size_t)(p.tpad * (n128 / 32)) * sizeof(uint2));
   p.total = p.part_off;
   // the last, shorter block of a long call may take more slices than the others
   for (int64_t tk : {p.block, tokens % p.block}) {
@@ -760,7 +789,7 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
   const char* base = static_cast<const char*>(c.packed);
   char* w = static_cast<char*>(ws);
   uint16_t* Xp = reinterpret_cast<uint16_t*>(w);
-  float* xs = reinterpret_cast<float*>(w + p.xs_off);
+  uint2* xs = reinterpret_cast<uint2*>(w + p.xs_off);
   const int32_t* order = reinterpret_cast<const int32_t*>(base + L.order_off);
   L4Stream st;
   st.params = reinterpret_cast<const float2*>(base + L.param_off);
