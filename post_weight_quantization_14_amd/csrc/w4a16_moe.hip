@@ -78,9 +78,9 @@ __device__ __forceinline__ double moe_logit(const uint16_t* x, const void* R, in
         const int k = b + 512 * parts * u + 8 * lane;
         const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(x + (k < h ? k : 0));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {   // bf16·bf16: exact in fp32
-          s0 += (double)(__uint_as_float(xv[q] << 16) * __uint_as_float(w[u][q] << 16));
-          s1 += (double)(__uint_as_float(xv[q] & 0xffff0000u) * __uint_as_float(w[u][q] & 0xffff0000u));
+        for (int q = 0; q < 4; ++q) {
+          s0 = fma((double)__uint_as_float(xv[q] << 16), (double)__uint_as_float(w[u][q] << 16), s0);
+          s1 = fma((double)__uint_as_float(xv[q] & 0xffff0000u), (double)__uint_as_float(w[u][q] & 0xffff0000u), s1);
         }
       }
     }
@@ -209,9 +209,9 @@ __global__ __launch_bounds__(1024) void moe_router_kernel(MoeRouterArgs a) {
           const int k = i + 512 * a.parts * u;
           const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(x + (k < h ? k : 0));
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {   // bf16·bf16: exact in fp32
-            s0 += (double)(__uint_as_float(xv[q] << 16) * __uint_as_float(w[u][q] << 16));
-            s1 += (double)(__uint_as_float(xv[q] & 0xffff0000u) * __uint_as_float(w[u][q] & 0xffff0000u));
+          for (int q = 0; q < 4; ++q) {
+            s0 = fma((double)__uint_as_float(xv[q] << 16), (double)__uint_as_float(w[u][q] << 16), s0);
+            s1 = fma((double)__uint_as_float(xv[q] & 0xffff0000u), (double)__uint_as_float(w[u][q] & 0xffff0000u), s1);
           }
         }
 #pragma unroll

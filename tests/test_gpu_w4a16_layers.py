@@ -295,6 +295,25 @@ def test_moe_ties_go_to_the_lower_expert(pq, tokens):
     assert torch.all(wts == 0.25)
 
 
+@pytest.mark.parametrize("tokens,E", [(3, 8), (5, 24), (40, 24)])
+def test_moe_router_rows_of_the_types_lowest_value(pq, tokens, E):
+    # products of 1e38 and more, of both signs: their sums are finite in 64 bits
+    k, hidden, inter = 3, 128, 64
+    rng = np.random.default_rng(11)
+    experts = _experts(E, hidden, inter, 4, 32, rng, True)
+    cfg = pq.MoeConfig(hidden, inter, E, k, 4, 32, "silu", False)
+    packed = _pack(pq, cfg, experts)
+    X = H.activations(tokens, hidden, seed=12)
+    R = H.vector((E, hidden), "bf16", 13)
+    R[2] = torch.finfo(torch.bfloat16).min
+    R[5] = torch.finfo(torch.bfloat16).min
+    Y, ids, wts = pq.gptq_w4a16_moe(X.cuda(), R.cuda(), packed, cfg, out_dtype=torch.float32)
+    ref, bound, rids, rw = H.moe_ref(H.f64(X), H.f64(R), experts, hidden, inter, 4, k, "silu", False)
+    assert np.array_equal(ids.cpu().numpy(), rids)
+    assert np.max(np.abs(wts.cpu().numpy() - rw)) <= 1e-6
+    H.check(Y, ref, bound, "lowest rows")
+
+
 @pytest.mark.parametrize("tokens", [6, 20])
 def test_moe_token_of_nan_spoils_its_own_row(pq, tokens):
     E, k, hidden, inter = 8, 2, 128, 96
