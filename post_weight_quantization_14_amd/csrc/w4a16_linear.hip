@@ -248,8 +248,10 @@ struct L4GemmArgs {
   const u32x4_t* codes;
   float* part;            // split tiles: [splits][tiles - whole][fragments]
   int64_t n128, kc, Gp, mt, m, tokens, tpad;
-  int64_t tblocks, rblocks;
-  int64_t whole;          // tiles 0 .. whole - 1 take the whole K range, the others `splits` slices
+  // 32 bits, like all that is divided: 64-bit divisions before the first load
+  // took 1 us of a small call
+  uint32_t tblocks;
+  uint32_t whole, parted; // tiles 0 .. whole - 1 take the whole K range, the other `parted` `splits` slices
   int pmul, splits, chunks;   // K slices, chunks per slice
   L4Epilogue ep;
 };
@@ -292,18 +294,18 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
   const int kg = wave / Tl::kGroup, gw = wave % Tl::kGroup, rg = gw % RG, tg = gw / RG;
   // whole tiles first, then the slices of the others, slice by slice; tiles
   // run along the token blocks of a row block
-  int64_t i = blockIdx.x;
-  const int64_t parted = a.tblocks * a.rblocks - a.whole;   // tiles that are split
+  uint32_t i = blockIdx.x;
+  const int64_t parted = a.parted;
   const bool split = i >= a.whole && a.splits > 1;
   int sl = 0;
   if (split) {
-    const int64_t j = i - a.whole;
-    sl = (int)(j / parted);
-    i = a.whole + j % parted;
+    const uint32_t j = i - a.whole;
+    sl = (int)(j / a.parted);
+    i = a.whole + j % a.parted;
   }
   const int64_t tb = i % a.tblocks, rb = i / a.tblocks;
   const int64_t t0 = tb * Tl::kTokens;
-  const int c0 = sl * a.chunks, nch = split ? (int)std::min<int64_t>(a.chunks, a.kc - c0) : (int)a.kc;
+  const int c0 = sl * a.chunks, nch = split ? std::min(a.chunks, (int)a.kc - c0) : (int)a.kc;
   const int steps = (nch + KG - 1) / KG;   // this wave's chunk of step s: s·KG + kg
 
   // X' rows past the last token lie outside the descriptor and read as zero
@@ -508,6 +510,7 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
         for (int k = 1; k < KG; ++k) z[b] += *at(k, mt * 8 + b * 4 + q);
       }
       if (split) {
+        if (t0 + 32 * (MT * tg + mt) + 8 * q >= a.tokens) continue;   // not read
         f32x4_t* out = reinterpret_cast<f32x4_t*>(a.part) +
                        ((((int64_t)sl * parted + i - a.whole) * Tl::kGroup + gw) * F + mt * 8 + q) * 64 + lane;
         out[0] = z[0];
@@ -538,8 +541,9 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          out[((mt * NB + b) * 4 + q) * 64] =
-              f32x4_t{y[mt][b][4 * q], y[mt][b][4 * q + 1], y[mt][b][4 * q + 2], y[mt][b][4 * q + 3]};
+          if (t0 + 32 * (MT * tg + mt) + 8 * q < a.tokens)   // the others are not read
+            out[((mt * NB + b) * 4 + q) * 64] =
+                f32x4_t{y[mt][b][4 * q], y[mt][b][4 * q + 1], y[mt][b][4 * q + 2], y[mt][b][4 * q + 3]};
     return;
   }
   const int64_t rbase = (rb * RG + rg) * (GATED ? 16 : 32) + (lane & (GATED ? 15 : 31));
@@ -592,11 +596,11 @@ template <int MT, int NB, int TG, int RG, bool GATED>
 __global__ __launch_bounds__(256) void l4_reduce_kernel(L4GemmArgs a) {
   constexpr int FR = TG * RG * MT * NB * 4 * 64;   // fragments of one tile
   constexpr bool kPair = GATED && NB == 2;
-  const int64_t per = a.tblocks * a.rblocks - a.whole;
-  int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  constexpr int PER = kPair ? FR / 2 : FR;
-  if (f >= per * PER) return;   // whole waves: PER is a multiple of 64
-  const int64_t i = f / PER;
+  const int64_t per = a.parted;
+  const uint32_t f = blockIdx.x * 256 + threadIdx.x;
+  constexpr uint32_t PER = kPair ? FR / 2 : FR;
+  if (f >= a.parted * PER) return;   // whole waves: PER is a multiple of 64
+  const uint32_t i = f / PER;
   int k = (int)(f % PER);
   const int lane = k & 63, q = (k >> 6) & 3;
   k >>= 8;
@@ -606,7 +610,11 @@ __global__ __launch_bounds__(256) void l4_reduce_kernel(L4GemmArgs a) {
     k /= NB;
   }
   const int mt = k % MT, wave = k / MT, rg = wave % RG, tg = wave / RG;
-  const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.part) + i * FR + ((wave * MT + mt) * NB + b) * 256 + q * 64 + lane;
+  const uint32_t tile = a.whole + i;
+  const int64_t tb = tile % a.tblocks, rb = tile / a.tblocks;
+  const int64_t t = tb * (32 * MT * TG) + 32 * (MT * tg + mt) + 8 * q + 4 * (lane >> 5);
+  if (t - 4 * (lane >> 5) >= a.tokens) return;   // whole waves
+  const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.part) + (int64_t)i * FR + ((wave * MT + mt) * NB + b) * 256 + q * 64 + lane;
   f32x4_t v0 = p[0], v1 = {0.f, 0.f, 0.f, 0.f};
   if (kPair) v1 = p[256];
   for (int s = 1; s < a.splits; ++s) {
@@ -618,8 +626,6 @@ __global__ __launch_bounds__(256) void l4_reduce_kernel(L4GemmArgs a) {
     for (int v = 0; v < 4; ++v) v1[v] = __shfl_xor(v0[v], 16);
     if (lane & 16) return;
   }
-  const int64_t tile = a.whole + i, tb = tile % a.tblocks, rb = tile / a.tblocks;
-  const int64_t t = tb * (32 * MT * TG) + 32 * (MT * tg + mt) + 8 * q + 4 * (lane >> 5);
   const int64_t r = (rb * RG + rg) * (GATED ? 16 * NB : 32 * NB) + 32 * b + (lane & (GATED && NB == 1 ? 15 : 31));
   const float g4[4] = {v0[0], v0[1], v0[2], v0[3]}, u4[4] = {v1[0], v1[1], v1[2], v1[3]};
   float rv[4];
@@ -736,12 +742,11 @@ gptq_status launch_l4_decode(const L4DecodeArgs& d, int gs, bool gated, bool gat
 
 template <int GS, int MT, int NB, int TG, int RG, int KG, bool GATED>
 gptq_status launch_l4_tile(const L4GemmArgs& g, hipStream_t stream) {
-  const int64_t parted = g.tblocks * g.rblocks - g.whole;
-  hipLaunchKernelGGL((l4_gemm_kernel<GS, MT, NB, TG, RG, KG, GATED>), dim3((unsigned)(g.whole + parted * g.splits)),
+  hipLaunchKernelGGL((l4_gemm_kernel<GS, MT, NB, TG, RG, KG, GATED>), dim3(g.whole + g.parted * g.splits),
                      dim3(64 * TG * RG * KG), 0, stream, g);
   GPTQ_LAUNCH_CHECK();
   if (g.splits > 1) {
-    const int64_t frags = parted * TG * RG * MT * NB * 4 * 64 / (GATED && NB == 2 ? 2 : 1);
+    const int64_t frags = (int64_t)g.parted * TG * RG * MT * NB * 4 * 64 / (GATED && NB == 2 ? 2 : 1);
     hipLaunchKernelGGL((l4_reduce_kernel<MT, NB, TG, RG, GATED>), dim3((unsigned)ceil_div(frags, 256)), dim3(256), 0,
                        stream, g);
     GPTQ_LAUNCH_CHECK();
@@ -880,10 +885,10 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
     g.m = c.m;
     g.tokens = tk;
     g.tpad = p.tpad;
-    g.tblocks = sh.tblocks;
-    g.rblocks = sh.rblocks;
+    g.tblocks = (uint32_t)sh.tblocks;
     g.pmul = st.pmul;
-    g.whole = sh.whole;
+    g.whole = (uint32_t)sh.whole;
+    g.parted = (uint32_t)(sh.tblocks * sh.rblocks - sh.whole);
     g.splits = sh.splits;
     g.chunks = sh.chunks;
     g.ep = ep;
