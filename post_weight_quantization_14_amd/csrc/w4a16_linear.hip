@@ -134,8 +134,8 @@ struct L4DecodeArgs {
 // (linear) or one gate/up pair of tiles (glu).  X' is gathered here (GATHER) or
 // copied from X' in memory.  Bound by the code stream from HBM, at small sizes
 // by the chain launch - row - order - codes - sums and the call itself:
-// 4096 x 4096, 1 token 5.9 us (9.5 with Python's call), 11008 x 4096 pair
-// 16.7 us = 3.0 TB/s, 8192 x 29568 34.5 us = 3.9 TB/s.
+// 4096 x 4096, 1 token 5.9 us (9.4 with Python's call), 11008 x 4096 pair
+// 16.1 us = 3.2 TB/s, 8192 x 29568 34.5 us = 4.0 TB/s.
 template <int GS, bool GATED, bool GATHER>
 __global__ __launch_bounds__(kL4Threads) void l4_decode_kernel(L4DecodeArgs a) {
   constexpr int RT = GATED ? 2 : 1;

@@ -18,7 +18,7 @@
 //
 // Bound by the chosen experts' codes and parameters from HBM: 64 tokens, 64
 // experts of 2048 x 1024, top 6: gate/up 39 us = 4.2 TB/s, down 25 us, router
-// 11 us, 83 us in all; 1 token, 8 experts of 4096 x 11008, top 2: 33 us and
+// 10 us, 81 us in all; 1 token, 8 experts of 4096 x 11008, top 2: 33 us and
 // 20 us, 55 us in all.
 #include <algorithm>
 
