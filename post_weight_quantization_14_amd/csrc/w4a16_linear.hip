@@ -711,11 +711,12 @@ L4Shape l4_shape(int64_t tokens, int64_t packed_rows, int64_t kc) {
   return best;
 }
 constexpr size_t kL4GatherLds = 65536;    // rows up to 32768 columns are gathered through LDS
-// the decode kernel's tiles of 16 tokens against the tiled product: its rounds
-// of workgroups, each a share of the chunks and about 2.5 us of its own, and
-// one launch less
+// the decode kernel's tiles of 16 tokens against the tiled product: its start,
+// and rounds of workgroups that take a share of the chunks and about 1 us of
+// their own; and one launch less (4096 x 4096, 64 tokens: 14.5 us in four tiles
+// of 16, 18.1 in one of 64; 80 tokens: 20.0 and 17.1 in tiles of 32)
 double l4_decode_us(int64_t tiles, int64_t units, int64_t kc, int rt) {
-  return (double)ceil_div(tiles * units, 256) * ((double)(kc * rt) / 16.0 + 2.5);
+  return 2.5 + (double)ceil_div(tiles * units, 256) * ((double)(kc * rt) / 16.0 + 1.0);
 }
 constexpr int64_t kL4GatherMax = 65536;   // up to this many elements of X' it gathers them itself
 constexpr size_t kL4MaxLds = 158 * 1024;
