@@ -711,16 +711,19 @@ size_t moe_plan(MoeExpertArgs& a, int tokens, int planes, int rt, int64_t wgs, b
   const L4Split sp = l4_split(a.st.units, wgs, a.st.kc, rt);
   a.st.kslog = sp.kslog;
   a.st.rounds = sp.rounds;
-  // as many tokens a pass as LDS holds, down to six; fewer would stream the
-  // codes too often, and fragments are read from memory instead (8 experts of
-  // 4096 x 2048, 64 tokens: 114 us from memory, 80 us in passes of 14)
+  // as many tokens a pass as LDS holds, down to six or two thirds of an expert's
+  // mean: with fewer the codes stream too often, and fragments are read from
+  // memory instead (8 experts of 4096 x 2048, 64 tokens: 114 us from memory, 80
+  // in passes of 14; of 4096 x 11008, top 2, in passes of 3: 4 tokens 138 us
+  // against 181 from memory, 16 tokens 199 and 211, 32 tokens 280 and 245)
+  const int least = (int)std::min<int64_t>(6, ceil_div(2 * (int64_t)tokens * a.top_k, 3 * (int64_t)a.experts));
   for (a.pass = std::min(kMoePass, tokens);; --a.pass) {
     a.quads = (int)ceil_div(a.pass, 4);
     const size_t red = sp.kslog ? (size_t)kL4Waves * rt * a.quads * 64 * sizeof(float) : 0;
     const size_t rows = (size_t)a.pass * planes * (size_t)(a.k128 + kL4Pad) * 2;
     *in_lds = rows + red <= kMoeMaxLds;
     if (*in_lds) return rows + red;
-    if (a.pass <= 6) break;
+    if (a.pass <= least) break;
   }
   a.pass = std::min(kMoePass, tokens);
   a.quads = (int)ceil_div(a.pass, 4);

@@ -314,6 +314,25 @@ def test_moe_router_rows_of_the_types_lowest_value(pq, tokens, E):
     H.check(Y, ref, bound, "lowest rows")
 
 
+@pytest.mark.parametrize("tokens", [4, 6, 12])
+def test_moe_wide_inner_layer_in_small_passes(pq, tokens):
+    # three tokens' hidden activation fills LDS: passes of three, or (12 tokens) reads from memory;
+    # nearly all tokens choose one expert
+    E, k, hidden, inter = 2, 1, 64, 8192
+    rng = np.random.default_rng(21)
+    experts = _experts(E, hidden, inter, 4, 64, rng, True)
+    cfg = pq.MoeConfig(hidden, inter, E, k, 4, 64, "silu", True)
+    packed = _pack(pq, cfg, experts)
+    X = H.activations(tokens, hidden, seed=22).abs()
+    X[-1] = -X[-1]
+    R = torch.zeros(E, hidden, dtype=torch.bfloat16)
+    R[1] = 1.0
+    Y, ids, _ = pq.gptq_w4a16_moe(X.cuda(), R.cuda(), packed, cfg, out_dtype=torch.float32)
+    assert ids.flatten().tolist() == [1] * (tokens - 1) + [0]
+    ref, bound, _, _ = H.moe_ref(H.f64(X), H.f64(R), experts, hidden, inter, 4, k, "silu", True)
+    H.check(Y, ref, bound, "wide inner layer")
+
+
 @pytest.mark.parametrize("tokens", [6, 20])
 def test_moe_token_of_nan_spoils_its_own_row(pq, tokens):
     E, k, hidden, inter = 8, 2, 128, 96
