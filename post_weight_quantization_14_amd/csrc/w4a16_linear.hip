@@ -281,7 +281,7 @@ struct L4Tile {
   static constexpr int kX = kTokens * 256;                                 // X' of one chunk
   static constexpr int kBytes = kX + kNG * kTokens * 8;   // and its group sums
   static constexpr int kXCopies = kX / 1024 / kGroup;                      // 1 KB copies per wave
-  static_assert(kX % (1024 * kGroup) == 0, "copies split evenly over the waves");
+  static_assert(kX % (2048 * kGroup) == 0, "copies split evenly over the waves, two at a time");
   static_assert(kTokens <= 128, "the sums of a group are one copy of up to 64 lanes, two tokens each");
 };
 
