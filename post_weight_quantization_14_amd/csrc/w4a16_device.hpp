@@ -75,6 +75,7 @@ struct L4Stream {
   int64_t kc, Gp, units;
   int pmul;                // distance of groups in params: 16, or 0 for one group per row
   int kslog, rounds;
+  int kfirst, kcount;      // the chunks of this call: all kc, or a slice of them
 };
 
 // Runs a wave's share.  GS = 32-position steps per group (1, 2, 4); one group
@@ -100,8 +101,8 @@ __device__ __forceinline__ void l4_units(const L4Stream& st, int64_t first, int6
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int ks = 1 << st.kslog, sl = wave & (ks - 1);
-  const int cps = (int)((st.kc + ks - 1) >> st.kslog);
-  const int c0 = sl * cps, c1 = (int)std::min<int64_t>(st.kc, c0 + cps);
+  const int cps = (st.kcount + ks - 1) >> st.kslog;
+  const int c0 = st.kfirst + sl * cps, c1 = std::min(st.kfirst + st.kcount, c0 + cps);
   const int64_t u0 = first + (wave >> st.kslog);
   const L4Consts kc;
   struct Batch {
@@ -244,9 +245,9 @@ constexpr int kL4Pad = 8;
 struct L4LdsA {
   static constexpr bool kPrefetch = false;
   const uint16_t* row;
-  int plane;
+  int plane, first = 0;   // the chunk that the rows begin with
   __device__ __forceinline__ uint4 load(int c, int j, int p) const {
-    return *reinterpret_cast<const uint4*>(row + p * plane + c * kL4Chunk + 32 * j);
+    return *reinterpret_cast<const uint4*>(row + p * plane + (c - first) * kL4Chunk + 32 * j);
   }
 };
 

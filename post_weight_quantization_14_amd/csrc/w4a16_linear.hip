@@ -867,6 +867,8 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
       const L4Split sp = l4_split(st.units, wgs, L.kc, gated ? 2 : 1);
       st.kslog = sp.kslog;
       st.rounds = sp.rounds;
+      st.kfirst = 0;
+      st.kcount = (int)L.kc;
       d.st = st;
       // workgroups that the split leaves without units are not launched
       const unsigned grid = (unsigned)std::min<int64_t>(wgs, ceil_div(st.units, kL4Waves >> sp.kslog));

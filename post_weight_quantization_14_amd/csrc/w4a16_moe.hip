@@ -333,10 +333,10 @@ struct MoeExpertArgs {
   const uint16_t* A;          // [pairs][planes][k128], processing order
   int64_t k128;               // positions of the product's input
   const int32_t* ids;
-  int tokens, top_k, experts, pass, quads, act, planes;
+  int tokens, top_k, experts, pass, quads, act, planes, slices;
   int64_t rows;               // gate/up: f128 (positions); down: hidden
   uint16_t* mid;              // gate/up's result [pairs][planes][rows]: bf16 parts, largest first
-  float* out;                 // down's result [pairs][rows]
+  float* out;                 // down's result [slices][pairs][rows]
 };
 
 // act(gate)·up of one pair and row.  It leaves as 2 or 3 bf16 parts (16 or 24
@@ -371,21 +371,29 @@ __device__ __forceinline__ void moe_expert_units(const MoeExpertArgs& a, MoeList
   const int lane = threadIdx.x & 63, tid = threadIdx.x;
   const int upw = kL4Waves >> st.kslog;
   const int64_t first = (int64_t)blockIdx.x * upw, step = (int64_t)gridDim.x * upw;
-  const int xrow = (int)a.k128 + kL4Pad;
+  // grid z: passes of an expert of many tokens, and slices of K whose rows fit
+  const int slice = GATE_UP ? 0 : (int)(blockIdx.z % a.slices), z0 = GATE_UP ? blockIdx.z : blockIdx.z / a.slices;
+  const int zn = GATE_UP ? gridDim.z : gridDim.z / a.slices;
+  if (!GATE_UP) {
+    st.kcount = (int)((st.kc + a.slices - 1) / a.slices);
+    st.kfirst = slice * st.kcount;
+    st.kcount = std::min(st.kcount, (int)st.kc - st.kfirst);
+  }
+  const int per = GATE_UP ? (int)st.kc : (int)((st.kc + a.slices - 1) / a.slices);   // chunks of a row in LDS
+  const int xrow = per * kL4Chunk + kL4Pad;
   uint16_t* xsh = reinterpret_cast<uint16_t*>(lds);
   float* red = reinterpret_cast<float*>(lds + (LDS ? (size_t)a.pass * NP * xrow * 2 : 0));
-  // grid z deals the passes of an expert of many tokens to workgroups
   bool again = false;
-  for (int p0 = blockIdx.z * a.pass; p0 < list.count; p0 += gridDim.z * a.pass) {
+  for (int p0 = z0 * a.pass; p0 < list.count; p0 += zn * a.pass) {
     const int np = std::min(a.pass, list.count - p0);
     auto fill = [&] {
       if (!LDS) return;
       if (again) __syncthreads();   // the pass before has been read
-      const int pieces = (int)(a.k128 / 8);
+      const int pieces = st.kcount * (kL4Chunk / 8);
       for (int i = tid; i < np * NP * pieces; i += kL4Threads) {
         const int q = i / pieces, k = 8 * (i % pieces);   // row q = token q / NP, plane q % NP
         *reinterpret_cast<uint4*>(xsh + q * xrow + k) =
-            *reinterpret_cast<const uint4*>(a.A + ((int64_t)list.pair[p0 + q / NP] * NP + q % NP) * a.k128 + k);
+            *reinterpret_cast<const uint4*>(a.A + ((int64_t)list.pair[p0 + q / NP] * NP + q % NP) * a.k128 + st.kfirst * kL4Chunk + k);
       }
       __syncthreads();
     };
@@ -396,13 +404,13 @@ __device__ __forceinline__ void moe_expert_units(const MoeExpertArgs& a, MoeList
         if (GATE_UP) {
           moe_hidden(a, pair, r, z);
         } else {
-          a.out[pair * a.rows + r] = z[0];
+          a.out[((int64_t)slice * a.tokens * a.top_k + pair) * a.rows + r] = z[0];
         }
       });
     };
     const int q = std::min(lane & 15, np - 1);   // rows past the last: computed, not stored
     if (LDS) {
-      const L4LdsA af{xsh + q * NP * xrow + 8 * (lane >> 4), xrow};
+      const L4LdsA af{xsh + q * NP * xrow + 8 * (lane >> 4), xrow, GATE_UP ? 0 : st.kfirst};
       l4_units<GS, RT, NP, B, NP == 3>(st, first, step, af, fill, end);
     } else {
       const L4GlobalA af{a.A + (int64_t)list.pair[p0 + q] * NP * a.k128 + 8 * (lane >> 4), a.k128};
@@ -688,12 +696,18 @@ __global__ __launch_bounds__(kL4Threads) void moe_small_down_kernel(MoeSmallDown
 }
 
 __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restrict__ pairs, const float* __restrict__ wts,
-                                                          int top_k, int64_t hidden, const void* res, int res_dt,
+                                                          int top_k, int slices, int64_t hidden, const void* res, int res_dt,
                                                           int64_t ldr, void* Y, int y_dt, int64_t ldy) {
   const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
   if (r >= hidden) return;
   float v = 0.f;
-  for (int j = 0; j < top_k; ++j) v = fmaf(wts[t * top_k + j], pairs[(t * top_k + j) * hidden + r], v);
+  const int64_t slice = (int64_t)gridDim.y * top_k * hidden;
+  for (int j = 0; j < top_k; ++j) {
+    const float* p = pairs + (t * top_k + j) * hidden + r;
+    float d = p[0];
+    for (int s = 1; s < slices; ++s) d += p[s * slice];
+    v = fmaf(wts[t * top_k + j], d, v);
+  }
   if (res) v += l4_load(res, res_dt, t * ldr + r);
   l4_store(Y, y_dt, t * ldy + r, v);
 }
@@ -705,22 +719,45 @@ constexpr int64_t kMoeLogitsElsewhere = 1 << 16;   // logit products from which 
 constexpr int64_t kSmallRouter = 65536, kSmallRouter2 = 131072;   // the latter for one or two tokens
 constexpr size_t kMoeMaxLds = 150 * 1024;
 
+// The fewest tokens that are worth a pass: twice an expert's mean, six at most
+// (8 experts of 4096 x 11008, top 2, passes of 3 against slices of K with full
+// ones: 4 tokens 137 us and 181 from memory, 8 tokens 169 and 159, 16 tokens 194
+// and 175).
+int moe_least(int64_t tokens, int64_t top_k, int64_t experts) {
+  return (int)std::min<int64_t>(6, ceil_div(2 * tokens * top_k, experts));
+}
+// Slices of the down product's K: one where moe_least tokens' hidden activation
+// fits in LDS, else as many as make a full pass fit; the combine kernel adds
+// their results in slice order.  Up to 256 MB of those, beyond that one slice,
+// read from memory (the same experts, 32 tokens: 245 us from memory, 180 in
+// slices; 64 tokens 448 and 303).
+int moe_slices(const gptq_moe_config& c, int64_t tokens, int planes) {
+  const int64_t kc = ceil_div(c.inter, kL4Chunk), pass = std::min<int64_t>(kMoePass, tokens);
+  auto bytes = [&](int64_t rows, int64_t chunks) {   // and the waves' sums
+    return (size_t)rows * planes * (size_t)(chunks * kL4Chunk + kL4Pad) * 2 + (size_t)kL4Waves * ceil_div(rows, 4) * 256;
+  };
+  if (bytes(std::min<int64_t>(pass, moe_least(tokens, c.top_k, c.experts)), kc) <= kMoeMaxLds) return 1;
+  int64_t s = 2;
+  while (bytes(pass, ceil_div(kc, s)) > kMoeMaxLds) ++s;
+  s = ceil_div(kc, ceil_div(kc, s));   // none is empty
+  return (size_t)(s * tokens * c.top_k) * (size_t)c.hidden * sizeof(float) <= (size_t)256 << 20 ? (int)s : 1;
+}
+
 // fills the launch-dependent fields; returns the dynamic LDS bytes, 0 < lds
 // with *in_lds when the rows of a pass fit
 size_t moe_plan(MoeExpertArgs& a, int tokens, int planes, int rt, int64_t wgs, bool* in_lds) {
-  const L4Split sp = l4_split(a.st.units, wgs, a.st.kc, rt);
+  const int64_t per = ceil_div(a.st.kc, (int64_t)a.slices);   // chunks
+  const L4Split sp = l4_split(a.st.units, wgs, per, rt);
   a.st.kslog = sp.kslog;
   a.st.rounds = sp.rounds;
-  // as many tokens a pass as LDS holds, down to six or two thirds of an expert's
-  // mean: with fewer the codes stream too often, and fragments are read from
-  // memory instead (8 experts of 4096 x 2048, 64 tokens: 114 us from memory, 80
-  // in passes of 14; of 4096 x 11008, top 2, in passes of 3: 4 tokens 138 us
-  // against 181 from memory, 16 tokens 199 and 211, 32 tokens 280 and 245)
-  const int least = (int)std::min<int64_t>(6, ceil_div(2 * (int64_t)tokens * a.top_k, 3 * (int64_t)a.experts));
+  // as many tokens a pass as LDS holds, down to moe_least; fewer would stream the
+  // codes too often, and fragments are read from memory instead (8 experts of
+  // 4096 x 2048, 64 tokens: 114 us from memory, 80 in passes of 14)
+  const int least = moe_least(tokens, a.top_k, a.experts);
   for (a.pass = std::min(kMoePass, tokens);; --a.pass) {
     a.quads = (int)ceil_div(a.pass, 4);
     const size_t red = sp.kslog ? (size_t)kL4Waves * rt * a.quads * 64 * sizeof(float) : 0;
-    const size_t rows = (size_t)a.pass * planes * (size_t)(a.k128 + kL4Pad) * 2;
+    const size_t rows = (size_t)a.pass * planes * (size_t)(per * kL4Chunk + kL4Pad) * 2;
     *in_lds = rows + red <= kMoeMaxLds;
     if (*in_lds) return rows + red;
     if (a.pass <= least) break;
@@ -784,7 +821,10 @@ MoeWork plan_moe_work(const gptq_moe_config& c, int64_t tokens) {
   w.xp_off = w.wts_off + align256(pairs * sizeof(float));
   w.mid_off = w.xp_off + align256(pairs * h128 * sizeof(uint16_t));
   w.out_off = w.mid_off + align256(pairs * kMoeMaxPlanes * f128 * sizeof(uint16_t));
-  w.logits_off = w.out_off + align256(pairs * (size_t)c.hidden * sizeof(float));
+  int slices = 1;   // of either result type, of a full block and of the last
+  for (int64_t tk : {w.block, tokens % w.block})
+    if (tk > 0) slices = std::max({slices, moe_slices(c, tk, 2), moe_slices(c, tk, 3)});
+  w.logits_off = w.out_off + align256(pairs * (size_t)slices * (size_t)c.hidden * sizeof(float));
   w.total = w.logits_off + align256((size_t)w.block * (size_t)c.experts * sizeof(double));
   return w;
 }
@@ -823,7 +863,8 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
     a.stride = (int64_t)L.stride;
     a.param_off = (int64_t)l.param_off;
     a.code_off = (int64_t)l.code_off;
-    a.st = L4Stream{nullptr, nullptr, l.kc, l.Gp, units, l.g >= l.n128 ? 0 : kL4Rows, 0, 1};
+    a.st = L4Stream{nullptr, nullptr, l.kc, l.Gp, units, l.g >= l.n128 ? 0 : kL4Rows, 0, 1, 0, (int)l.kc};
+    a.slices = 1;
     a.k128 = l.n128;
     a.ids = ids;
     a.top_k = cfg.top_k;
@@ -874,8 +915,9 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
     // where an expert has more tokens than a pass on average, side by side
     const int64_t passes = ceil_div((int64_t)tk * cfg.top_k, (int64_t)cfg.experts * kMoePass);
     const int64_t share = std::max<int64_t>(1, 256 / (slots * passes));
-    const int64_t gw = std::min<int64_t>(share, g.st.units), dw = std::min<int64_t>(share, d.st.units);
+    const int64_t gw = std::min<int64_t>(share, g.st.units);
     g.tokens = d.tokens = tk;
+    d.slices = moe_slices(cfg, tk, d.planes);
     bool in_lds = false;
     size_t lds = moe_plan(g, tk, 1, 2, gw, &in_lds);
     const dim3 ggrid((unsigned)std::min<int64_t>(gw, ceil_div(g.st.units, kL4Waves >> g.st.kslog)), (unsigned)slots,
@@ -942,16 +984,17 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
       case 2: GPTQ_TRY(launch_gate_up<2>(ggrid, lds, in_lds, g, stream)); break;
       default: GPTQ_TRY(launch_gate_up<4>(ggrid, lds, in_lds, g, stream)); break;
     }
+    const int64_t dw = std::min<int64_t>(std::max<int64_t>(1, share / d.slices), d.st.units);
     lds = moe_plan(d, tk, d.planes, 1, dw, &in_lds);
     const dim3 dgrid((unsigned)std::min<int64_t>(dw, ceil_div(d.st.units, kL4Waves >> d.st.kslog)), (unsigned)slots,
-                     (unsigned)passes);
+                     (unsigned)(passes * d.slices));
     switch (steps(L.down)) {
       case 1: GPTQ_TRY(launch_down<1>(dgrid, lds, in_lds, d, stream)); break;
       case 2: GPTQ_TRY(launch_down<2>(dgrid, lds, in_lds, d, stream)); break;
       default: GPTQ_TRY(launch_down<4>(dgrid, lds, in_lds, d, stream)); break;
     }
     hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)ceil_div(cfg.hidden, 256), (unsigned)tk), dim3(256), 0, stream,
-                       (const float*)out, (const float*)wts, (int)cfg.top_k, cfg.hidden, res, c.res_dtype, c.ldr, Y,
+                       (const float*)out, (const float*)wts, (int)cfg.top_k, d.slices, cfg.hidden, res, c.res_dtype, c.ldr, Y,
                        c.y_dtype, c.ldy);
     GPTQ_LAUNCH_CHECK();
   }

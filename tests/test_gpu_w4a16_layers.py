@@ -314,9 +314,9 @@ def test_moe_router_rows_of_the_types_lowest_value(pq, tokens, E):
     H.check(Y, ref, bound, "lowest rows")
 
 
-@pytest.mark.parametrize("tokens", [4, 6, 12])
-def test_moe_wide_inner_layer_in_small_passes(pq, tokens):
-    # three tokens' hidden activation fills LDS: passes of three, or (12 tokens) reads from memory;
+@pytest.mark.parametrize("tokens,out", [(4, "fp32"), (6, "fp32"), (12, "fp32"), (12, "bf16"), (70, "bf16")])
+def test_moe_wide_inner_layer(pq, tokens, out):
+    # three tokens' hidden activation fills LDS: the down product's K is sliced;
     # nearly all tokens choose one expert
     E, k, hidden, inter = 2, 1, 64, 8192
     rng = np.random.default_rng(21)
@@ -327,10 +327,10 @@ def test_moe_wide_inner_layer_in_small_passes(pq, tokens):
     X[-1] = -X[-1]
     R = torch.zeros(E, hidden, dtype=torch.bfloat16)
     R[1] = 1.0
-    Y, ids, _ = pq.gptq_w4a16_moe(X.cuda(), R.cuda(), packed, cfg, out_dtype=torch.float32)
+    Y, ids, _ = pq.gptq_w4a16_moe(X.cuda(), R.cuda(), packed, cfg, out_dtype=H.TDT[out])
     assert ids.flatten().tolist() == [1] * (tokens - 1) + [0]
-    ref, bound, _, _ = H.moe_ref(H.f64(X), H.f64(R), experts, hidden, inter, 4, k, "silu", True)
-    H.check(Y, ref, bound, "wide inner layer")
+    ref, bound, _, _ = H.moe_ref(H.f64(X), H.f64(R), experts, hidden, inter, 4, k, "silu", True, out=out)
+    H.check(Y, ref, bound, "wide inner layer", out=out)
 
 
 @pytest.mark.parametrize("tokens", [6, 20])
