@@ -332,7 +332,8 @@ gptq_status gptq_w4a16_matmul_noalloc(const void* X, int64_t tokens, int64_t ldx
  * synchronisation, nothing allocated; calls may be captured into a graph.
  * `packed` is read only and may be shared by any number of concurrent calls;
  * `workspace` (256-byte aligned, contents not kept) belongs to one call at a
- * time.  tokens == 0 is a no-op.  Y may be the residual itself (the same
+ * time; *_workspace_bytes(tokens, ...) bytes serve every call of up to that
+ * many tokens.  tokens == 0 is a no-op.  Y may be the residual itself (the same
  * pointer, type and row stride); otherwise no output may overlap an input.
  *
  * gptq_w4a16_linear: Y[t][r] = act(Σ_c X[t][c]·Ŵ[r][c] + bias[r]) +

@@ -467,7 +467,7 @@ size_t gptq_w4a16_linear_workspace_bytes(int64_t tokens, int64_t m, int64_t n, i
   if (tokens < 0 || tokens > kL4MaxTokens || m < 0 || m > kL4MaxRows || n <= 0 || n > kL4MaxCols ||
       !w4_group_ok(group_size))
     return 0;
-  return plan_w4a16_linear(tokens, n, plan_w4a16(m, n, group_size).mt * 16).total;
+  return w4a16_linear_workspace(tokens, n, plan_w4a16(m, n, group_size).mt * 16);
 }
 
 gptq_status gptq_w4a16_linear(const void* X, int64_t tokens, int64_t ldx, const void* packed, size_t packed_bytes,
@@ -526,7 +526,7 @@ size_t gptq_w4a16_glu_workspace_bytes(int64_t tokens, int64_t m, int64_t n, int3
   if (tokens < 0 || tokens > kL4MaxTokens || m < 0 || m > kL4MaxRows || n <= 0 || n > kL4MaxCols ||
       !w4_group_ok(group_size))
     return 0;
-  return plan_w4a16_linear(tokens, n, plan_w4a16_pair(m, n, group_size).mt * 16).total;
+  return w4a16_linear_workspace(tokens, n, plan_w4a16_pair(m, n, group_size).mt * 16);
 }
 
 gptq_status gptq_w4a16_glu(const void* X, int64_t tokens, int64_t ldx, const void* packed, size_t packed_bytes,
@@ -599,7 +599,7 @@ size_t gptq_w4a16_moe_workspace_bytes(const gptq_moe_config* cfg, int64_t tokens
     clear_error();
     return 0;
   }
-  return plan_moe_work(*cfg, tokens).total;
+  return moe_workspace(*cfg, tokens);
 }
 
 gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const void* router, int32_t router_dtype,

@@ -235,6 +235,9 @@ struct L4LinearPlan {
 };
 // packed_rows: 16 x the packed tiles (gate and up together)
 L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n, int64_t packed_rows);
+// bytes that any call of up to `tokens` tokens can do with (a call of exactly
+// so many needs plan_w4a16_linear's total, which may be less)
+size_t w4a16_linear_workspace(int64_t tokens, int64_t n, int64_t packed_rows);
 struct L4Call {
   const uint16_t* X;
   int64_t tokens, ldx, m;
@@ -260,6 +263,7 @@ struct MoeWork {
   size_t wts_off = 0, xp_off = 0, mid_off = 0, out_off = 0, logits_off = 0, total = 0;
 };
 MoeWork plan_moe_work(const gptq_moe_config& c, int64_t tokens);
+size_t moe_workspace(const gptq_moe_config& c, int64_t tokens);   // for any count up to `tokens`
 struct MoeCall {
   const uint16_t* X;
   int64_t tokens, ldx;

@@ -771,6 +771,15 @@ gptq_status launch_l4_gemm(const L4GemmArgs& g, const L4Shape& s, int gs, bool g
 }
 }  // namespace
 
+namespace {
+// the K slices' partial sums of a launch sequence of tk tokens
+size_t l4_part_bytes(int64_t tk, int64_t packed_rows, int64_t kc) {
+  const L4Shape s = l4_shape(tk, packed_rows, kc);
+  if (s.splits == 1) return 0;
+  return align256((size_t)(s.splits * (s.tblocks * s.rblocks - s.whole)) * (size_t)(s.tokens * 128) * sizeof(float));
+}
+}  // namespace
+
 L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n, int64_t packed_rows) {
   L4LinearPlan p;
   const int64_t kc = ceil_div(n, kL4Chunk), n128 = kc * kL4Chunk;
@@ -780,14 +789,22 @@ L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n, int64_t packed_rows) {
   p.part_off = p.xs_off + align256((size_t)(p.tpad * (n128 / 32)) * sizeof(uint2));
   p.total = p.part_off;
   // the last, shorter block of a long call may take more slices than the others
-  for (int64_t tk : {p.block, tokens % p.block}) {
-    if (tk == 0) continue;
-    const L4Shape s = l4_shape(tk, packed_rows, kc);
-    if (s.splits > 1)
-      p.total = std::max(p.total, p.part_off + align256((size_t)(s.splits * (s.tblocks * s.rblocks - s.whole)) *
-                                                        (size_t)(s.tokens * 128) * sizeof(float)));
-  }
+  for (int64_t tk : {p.block, tokens % p.block})
+    if (tk > 0) p.total = std::max(p.total, p.part_off + l4_part_bytes(tk, packed_rows, kc));
   return p;
+}
+
+// Fewer tokens may be cut into more slices (2048 tokens of 4096 x 4096 fill the
+// GPU with whole tiles, 1024 take two slices), so the largest of the partial
+// sums of any count up to `tokens` is taken: the tiles change every 32 tokens,
+// 128 counts at most (5 us on the host, which is why a call checks its own
+// plan's size instead).
+size_t w4a16_linear_workspace(int64_t tokens, int64_t n, int64_t packed_rows) {
+  const L4LinearPlan p = plan_w4a16_linear(tokens, n, packed_rows);
+  size_t part = 0;
+  for (int64_t t = 32; t < p.block + 32; t += 32)
+    part = std::max(part, l4_part_bytes(std::min(t, p.block), packed_rows, ceil_div(n, kL4Chunk)));
+  return p.part_off + part;
 }
 
 gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, void* ws, const L4LinearPlan& p,

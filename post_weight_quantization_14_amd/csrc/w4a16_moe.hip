@@ -829,6 +829,15 @@ MoeWork plan_moe_work(const gptq_moe_config& c, int64_t tokens) {
   return w;
 }
 
+// The slices of K change with the tokens (none where a few fit in LDS, none
+// again where their results pass 256 MB), so the largest of all counts up to
+// `tokens`: 1 .. 64, and 64 with every rest.
+size_t moe_workspace(const gptq_moe_config& c, int64_t tokens) {
+  size_t most = plan_moe_work(c, tokens).total;
+  for (int64_t t = 1; t < std::min<int64_t>(tokens, 2 * kMoeTokens); ++t) most = std::max(most, plan_moe_work(c, t).total);
+  return most;
+}
+
 gptq_status run_moe_pack(const gptq_moe_config& c, int expert, const L4PairSource& gate_up, const int32_t* g_idx,
                          const uint32_t* down_qweight, const float* down_scales, const int32_t* down_zeros,
                          const int32_t* down_g_idx, void* packed, hipStream_t stream) {

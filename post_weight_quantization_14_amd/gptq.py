@@ -468,7 +468,7 @@ def _empty(shape, dtype: torch.dtype, X: torch.Tensor, stream) -> torch.Tensor:
 def _with_workspace(call, nbytes, X: torch.Tensor, workspace: Optional[torch.Tensor], stream, where: str) -> None:
     """call(pointer, bytes) -> status on the caller's workspace (it then belongs
     to this call until its work is done), or on a new one of nbytes() bytes if
-    there is none or the library finds it too small."""
+    there is none or the library finds it too small or misaligned."""
     if workspace is not None:
         st = call(workspace.data_ptr(), _uint8("workspace", workspace))
         if st != _lib.GPTQ_ERR_WORKSPACE:
@@ -531,7 +531,9 @@ def gptq_w4a16_linear(X: torch.Tensor, packed: torch.Tensor, m: int, n: int, gro
     """Y [tokens, m] = act(X·Ŵᵀ + bias) + residual for X [tokens, n] bf16 and
     gptq_w4a16_pack's packed weight.  bias [m] and residual [tokens, m] are
     bf16 or fp32; activation is none, relu, silu, gelu or gelu_tanh.  Y (bf16
-    or fp32; out_dtype if it is allocated here) may be the residual itself."""
+    or fp32; out_dtype if it is allocated here) may be the residual itself.
+    A workspace made for some number of tokens serves every smaller batch;
+    without one, or with one that is too small, the call allocates its own."""
     ldx = _bf16_rows(X, n)
     tokens = X.shape[0]
     _on(X, packed=packed, bias=bias, residual=residual, Y=Y, workspace=workspace)

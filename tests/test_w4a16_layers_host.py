@@ -147,6 +147,25 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(L):
         pq.MoeConfig(64, 32, 4, 2, activation="swish").c()
 
 
+@pytest.mark.parametrize("m,n,g", [(4096, 4096, 128), (11008, 4096, 128), (4096, 11008, 64), (1031, 1000, 64),
+                                   (128, 20000, -1), (17, 33, 32)])
+def test_workspace_of_the_largest_batch_serves_smaller_ones(L, lb, m, n, g):
+    """Sizes never fall as the tokens grow: fewer tokens may be cut into more
+    K slices than many, whose partial sums the larger size has to hold."""
+    counts = sorted({*range(0, 300), *range(300, 4200, 31), 4096, 4097, 5000, 8191, 8192, 8193, 12288, 100000})
+    for size in (lambda t: L.gptq_w4a16_linear_workspace_bytes(t, m, n, g),
+                 lambda t: L.gptq_w4a16_glu_workspace_bytes(t, m, n, g)):
+        sizes = [size(t) for t in counts]
+        assert sizes[0] > 0 and sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("cfg", [(4096, 11008, 8, 2), (32768, 32768, 64, 8), (2048, 1024, 64, 6), (64, 8192, 2, 1)])
+def test_moe_workspace_of_the_largest_batch_serves_smaller_ones(L, lb, cfg):
+    c = lb.GptqMoeConfig(*cfg, 4, 64, 2, 1)
+    sizes = [L.gptq_w4a16_moe_workspace_bytes(ctypes.byref(c), t) for t in (*range(0, 200), 1000, 4096, 4100)]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
+
+
 # ---------------------------------------------------------------- oracle pins
 def test_oracle_activations_closed_forms():
     x = np.array([-3.0, -0.5, 0.0, 0.5, 3.0])
