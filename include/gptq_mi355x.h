@@ -326,8 +326,11 @@ gptq_status gptq_w4a16_matmul_noalloc(const void* X, int64_t tokens, int64_t ldx
  * gptq_w4a16_matmul.  Shared rules: X is bf16 with unit column stride; Y is
  * GPTQ_BF16 or GPTQ_FP32; biases, residuals and router weights are either
  * type.  A code enters its bf16 product exactly (as 16 + q), every sum and
- * the epilogue are fp32, and the result is rounded once, to Y's type.  X must
- * be finite (an Inf or NaN makes its own token's outputs NaN).  The summation
+ * the epilogue are fp32, and the result is rounded once, to Y's type.  X may
+ * hold any finite value (no group's sum overflows for zero points -16 .. 15, or
+ * while Σ|x|·(16 + |z|) over a group stays below 2^12·FLT_MAX; what fp32 itself
+ * cannot hold is Inf or NaN); an Inf or NaN in X makes its own token's outputs
+ * NaN.  The summation
  * order is fixed: the same call gives the same bits.  Stream-ordered, no
  * synchronisation, nothing allocated; calls may be captured into a graph.
  * `packed` is read only and may be shared by any number of concurrent calls;

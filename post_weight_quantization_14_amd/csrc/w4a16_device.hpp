@@ -15,19 +15,27 @@ constexpr int kL4Rows = 16;     // weight rows per packed tile (MFMA N)
 constexpr int kL4Chunk = 128;   // positions per packed chunk (4 MFMA k-steps of 32)
 
 // ---------------------------------------------------------------- operands
-// A 4-bit code q becomes the bf16 16 + q with one shift and one AND-OR: bf16
-// numbers in [16, 32) are spaced 1/8, so q sits in mantissa bits 3..6 of
-// 0x4180.  Then
+// A 4-bit code q becomes the bf16 (16 + q)·2^-12 with one shift and one AND-OR:
+// bf16 numbers in [16, 32)·2^-12 are spaced 2^-15, so q sits in mantissa bits
+// 3..6 of 0x3B80.  Then
 //   Σ_k x_k·(q_k - z) = Σ_k x_k·(16 + q_k) - (16 + z)·Σ_k x_k,
 // with exact bf16 x bf16 products on the left.  16 is the smallest offset
 // whose binade holds every 4-bit code: the two sums are then at most ~5x the
 // difference for codes around the middle, and fp32 sums lose 2-3 bits to
 // the subtraction (an offset of 128 loses 5).
+//
+// Both sums are held times 2^-12, and a result is multiplied by 2^12 when it is
+// whole: 128 positions·31 < 2^12, so no sum of a group overflows for any finite
+// x, where x·(16 + q) alone would from 1.1e37 on, with a result of Inf - Inf.
+// The factor is exact: other results keep their bits (x below 2^-114 lose some
+// of theirs to fp32's smallest numbers).
+constexpr float kL4Down = 0x1p-12f, kL4Up = 0x1p12f;
+
 struct L4Consts {
   uint32_t m, c, one;
   // hidden from constant folding: VOP3 takes no literals, so as visible
   // constants each AND-OR would compile to two instructions
-  __device__ __forceinline__ L4Consts() : m(0x00780078u), c(0x41804180u), one(0x3F803F80u) {
+  __device__ __forceinline__ L4Consts() : m(0x00780078u), c(0x3B803B80u), one(0x39803980u) {
     asm volatile("" : "+v"(m), "+v"(c), "+v"(one));
   }
   __device__ __forceinline__ bf16x8_t unpack(uint32_t w) const {
@@ -38,8 +46,8 @@ struct L4Consts {
     r[3] = ((w >> 9) & m) | c;
     return __builtin_bit_cast(bf16x8_t, r);
   }
-  // q - zc for an integer 0 <= zc <= 15 (off = 16 + zc): exact in bf16, so the
-  // upper halves of the fp32 differences are the operand itself
+  // (q - zc)·2^-12 for an integer 0 <= zc <= 15 (off = (16 + zc)·2^-12): exact in
+  // bf16, so the upper halves of the fp32 differences are the operand itself
   __device__ __forceinline__ bf16x8_t unpack_centred(uint32_t w, float off) const {
     const u32x4_t r = __builtin_bit_cast(u32x4_t, unpack(w));
     u32x4_t o;
@@ -50,6 +58,7 @@ struct L4Consts {
     }
     return __builtin_bit_cast(bf16x8_t, o);
   }
+  // each 2^-12
   __device__ __forceinline__ bf16x8_t ones() const {
     return __builtin_bit_cast(bf16x8_t, u32x4_t{one, one, one, one});
   }
@@ -58,6 +67,7 @@ struct L4Consts {
 // packed group parameters hold (s, 128 + z)
 __device__ __forceinline__ float l4_zero(float y) { return y - 112.f; }
 __device__ __forceinline__ float l4_centre(float y) { return fminf(fmaxf(y - 128.f, 0.f), 15.f); }
+__device__ __forceinline__ float l4_centre_off(float y) { return fmaf(l4_centre(y), kL4Down, 16.f * kL4Down); }
 
 // ---------------------------------------------------------------- few tokens
 // The kernels of up to 16 tokens are bound by the code stream from HBM.  A
@@ -85,7 +95,7 @@ struct L4Stream {
 //   fill()            puts A where `af` reads it; called by every wave once,
 //                     after the first batch of codes has been requested
 //   af.load(c, j, p)  8 positions 128c + 32j + 8·(lane/16) of token lane % 16
-//   end(unit, y)      the wave's sums of its K share of a unit, every round
+//   end(unit, y)      2^-12 of the wave's sums of its K share of a unit, every round
 // The group sum Σx comes from the matrix cores too (A times a tile of ones):
 // in D's layout it already sits where the fold needs it, and the matrix cores
 // are idle in a product that is bound by its codes.
@@ -157,7 +167,7 @@ __device__ __forceinline__ void l4_units(const L4Stream& st, int64_t first, int6
           for (int p = 0; p < NP; ++p) sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], kc.ones(), sx, 0, 0, 0);
 #pragma unroll
           for (int t = 0; t < RT; ++t) {
-            const bf16x8_t w = CENTRED ? kc.unpack_centred(b.cw[i][t][j], 16.f + l4_centre(b.p[i][t][g].y))
+            const bf16x8_t w = CENTRED ? kc.unpack_centred(b.cw[i][t][j], l4_centre_off(b.p[i][t][g].y))
                                        : kc.unpack(b.cw[i][t][j]);
 #pragma unroll
             for (int p = 0; p < NP; ++p) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], w, acc[t], 0, 0, 0);
@@ -189,9 +199,10 @@ __device__ __forceinline__ void l4_units(const L4Stream& st, int64_t first, int6
   }
 }
 
-// Sums of the ks waves of each unit, in wave order, through LDS.  red: [16
-// waves][RT][quads][64] floats, quads = 4-token groups that hold tokens.  Calls
-// out(unit, token, row, value[RT]) once per result; every wave calls it.
+// 2^12 times the sums of the ks waves of each unit, added in wave order through
+// LDS.  red: [16 waves][RT][quads][64] floats, quads = 4-token groups that hold
+// tokens.  Calls out(unit, token, row, value[RT]) once per result; every wave
+// calls it.
 template <int RT, class OF>
 __device__ __forceinline__ void l4_finish(float* red, int quads, int tokens, int kslog, int64_t unit,
                                           const f32x4_t (&y)[RT], const OF& out) {
@@ -202,7 +213,7 @@ __device__ __forceinline__ void l4_finish(float* red, int quads, int tokens, int
       if (4 * (lane >> 4) + v >= tokens) break;
       float z[RT];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) z[t] = y[t][v];
+      for (int t = 0; t < RT; ++t) z[t] = y[t][v] * kL4Up;
       out(unit, 4 * (lane >> 4) + v, lane & 15, z);
     }
     return;
@@ -224,6 +235,7 @@ __device__ __forceinline__ void l4_finish(float* red, int quads, int tokens, int
       const float* p = red + (((ul << kslog) * RT + t) * quads + (tok >> 2)) * 64 + row * 4 + (tok & 3);
       z[t] = p[0];
       for (int s = 1; s < ks; ++s) z[t] += p[s * RT * quads * 64];
+      z[t] *= kL4Up;
     }
     out(base + ul, tok, row, z);
   }

@@ -188,7 +188,7 @@ __device__ __forceinline__ L4Planes l4_planes(float v) {
   return {h, m, __float_as_uint(r - __uint_as_float(m))};
 }
 
-// X' = X[:, order] and its group sums, groups-major (sums[c·NG + g][t], for the
+// X' = X[:, order] and 2^-12 of its group sums, groups-major (sums[c·NG + g][t], for the
 // tile kernel's contiguous copies, cut into three bf16 planes: an operand).  A row of X is read once, 16 bytes a
 // thread, into LDS and gathered from there: 2-byte loads at scattered columns
 // cost the memory pipe a cycle or more a lane (2048 x 4096: 13 us, through
@@ -228,7 +228,7 @@ __global__ __launch_bounds__(512) void l4_gather_kernel(const uint16_t* __restri
   }
   float s = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s += __uint_as_float(v[e] << 16);
+  for (int e = 0; e < 8; ++e) s = fmaf(__uint_as_float(v[e] << 16), kL4Down, s);
   *reinterpret_cast<u32x4_t*>(Xp + t * n128 + p0) =
       u32x4_t{v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
 #pragma unroll
@@ -481,6 +481,12 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
   }
 #undef L4_STEP
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy may land after the workgroup ends
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) y[mt][b][v] *= kL4Up;
 
   if constexpr (KG > 1) {
     // The groups' sums through LDS: every wave leaves its fragments, then each

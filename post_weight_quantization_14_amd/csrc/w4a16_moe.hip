@@ -660,7 +660,7 @@ __global__ __launch_bounds__(kL4Threads) void moe_small_down_kernel(MoeSmallDown
           const float s = cur.p[j][q].x, y0 = cur.p[j][q].y;
 #pragma unroll
           for (int st = q * GS; st < q * GS + GS; ++st) {
-            const bf16x8_t w = NP == 3 ? k.unpack_centred(cur.cw[j][st], 16.f + l4_centre(y0)) : k.unpack(cur.cw[j][st]);
+            const bf16x8_t w = NP == 3 ? k.unpack_centred(cur.cw[j][st], l4_centre_off(y0)) : k.unpack(cur.cw[j][st]);
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
               const bf16x8_t av = __builtin_bit_cast(
