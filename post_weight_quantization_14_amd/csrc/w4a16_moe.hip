@@ -347,7 +347,8 @@ __device__ __forceinline__ void moe_hidden(const MoeExpertArgs& a, int64_t pair,
   float v = l4_activate(z[0], a.act) * z[RT - 1];
   uint16_t* o = a.mid + pair * a.planes * a.rows + r;
   for (int p = 0; p < a.planes; ++p) {
-    const uint16_t part = l4_bf16(v);
+    uint16_t part = l4_bf16(v);
+    if ((part & 0x7fff) == 0x7f80) part = (uint16_t)(__float_as_uint(v) >> 16);   // finite v that rounds to Inf: cut
     const float f = __uint_as_float((uint32_t)part << 16);
     o[p * a.rows] = part;
     v = isfinite(f) ? v - f : 0.f;

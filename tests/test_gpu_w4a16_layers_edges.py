@@ -93,3 +93,29 @@ def test_moe_of_the_largest_activations(pq, tokens, out):
     assert np.array_equal(ids.cpu().numpy(), rids)
     assert 1e35 < np.abs(ref).max() < 0.5 * BIG
     H.check(Y, ref, bound, "largest activations, moe", out)
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_moe_hidden_value_above_the_largest_bf16(pq, tokens, out):
+    """A hidden activation between the largest bf16 and the largest fp32 value
+    stays finite in its bf16 parts.  One column, codes one above the zero
+    points: gate 2^64, up v·2^-64, down v·2^-10, every step exact (three parts
+    hold 24 bits; two hold the 16 of the second value)."""
+    values = np.array([0x7F7FFFFF if out == "fp32" else 0x7F7FFF00, 0xFF7FF100], dtype=np.uint32).view(np.float32)
+    E, k = 2, 1
+    one = lambda s: (H.pack_words(np.array([[5]])), np.array([[s]], dtype=np.float32),  # noqa: E731
+                     np.array([[4]], dtype=np.int32), np.zeros(1, dtype=np.int32))
+    cfg = pq.MoeConfig(1, 1, E, k, 4, 32, "none", True)
+    packed = torch.empty(pq.gptq_w4a16_moe_packed_bytes(cfg), dtype=torch.uint8, device="cuda")
+    for e in range(E):
+        pq.gptq_w4a16_moe_pack(cfg, e, *H.gpu(one(2.0 ** 64)[:3]), *H.gpu(one(values[e] * np.float32(2.0 ** -64))),
+                               *H.gpu(one(2.0 ** -10)), packed)
+    X = torch.ones(tokens, 1, dtype=torch.bfloat16, device="cuda")
+    for e in range(E):
+        R = torch.zeros(E, 1, dtype=torch.bfloat16, device="cuda")
+        R[e] = 1.0
+        Y, ids, _ = pq.gptq_w4a16_moe(X, R, packed, cfg, out_dtype=H.TDT[out])
+        assert torch.all(ids == e)
+        want = torch.full((tokens, 1), float(values[e]) * 2.0 ** -10, dtype=torch.float32).to(H.TDT[out])
+        assert torch.equal(Y.cpu(), want)
