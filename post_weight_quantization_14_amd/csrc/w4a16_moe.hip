@@ -57,6 +57,14 @@ __device__ __forceinline__ bool moe_before(double a, int ia, double b, int ib) {
   return ia < ib;
 }
 
+// Eight elements of x from k; zeros past its end, like the router's: an Inf of
+// x times a zero of the router would be NaN.
+__device__ __forceinline__ u32x4_t moe_x(const uint16_t* x, int k, int h) {
+  u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + (k < h ? k : 0));
+  if (k >= h) v = u32x4_t{0u, 0u, 0u, 0u};
+  return v;
+}
+
 // One logit in 64 bits by one wave: `part` of `parts` interleaved 512-element
 // pieces, four pieces in flight.
 __device__ __forceinline__ double moe_logit(const uint16_t* x, const void* R, int r_dt, int vec, int64_t e, int h,
@@ -76,7 +84,7 @@ __device__ __forceinline__ double moe_logit(const uint16_t* x, const void* R, in
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int k = b + 512 * parts * u + 8 * lane;
-        const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(x + (k < h ? k : 0));
+        const u32x4_t xv = moe_x(x, k, h);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           s0 = fma((double)__uint_as_float(xv[q] << 16), (double)__uint_as_float(w[u][q] << 16), s0);
@@ -100,7 +108,7 @@ __device__ __forceinline__ double moe_logit(const uint16_t* x, const void* R, in
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int k = b + 512 * parts * u + 8 * lane;
-        const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(x + (k < h ? k : 0));
+        const u32x4_t xv = moe_x(x, k, h);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           s0 = fma((double)__uint_as_float(xv[q] << 16), (double)w[u][q >> 1][2 * (q & 1)], s0);
@@ -207,7 +215,7 @@ __global__ __launch_bounds__(1024) void moe_router_kernel(MoeRouterArgs a) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int k = i + 512 * a.parts * u;
-          const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(x + (k < h ? k : 0));
+          const u32x4_t xv = moe_x(x, k, h);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             s0 = fma((double)__uint_as_float(xv[q] << 16), (double)__uint_as_float(w[u][q] << 16), s0);

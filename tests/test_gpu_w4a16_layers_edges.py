@@ -119,3 +119,33 @@ def test_moe_hidden_value_above_the_largest_bf16(pq, tokens, out):
         assert torch.all(ids == e)
         want = torch.full((tokens, 1), float(values[e]) * 2.0 ** -10, dtype=torch.float32).to(H.TDT[out])
         assert torch.equal(Y.cpu(), want)
+
+
+# two launches; a router workgroup per token that reads bf16 rows, fp32 rows or
+# unaligned ones; logits in a launch of their own
+@pytest.mark.parametrize("tokens,E,hidden,rdt", [(1, 8, 96, "bf16"), (3, 8, 96, "fp32"), (70, 9, 136, "bf16"),
+                                                 (70, 9, 136, "fp32"), (70, 9, 131, "bf16"), (70, 40, 1000, "bf16"),
+                                                 (70, 40, 1000, "fp32")])
+def test_moe_routes_a_token_with_an_infinity_by_its_logits(pq, tokens, E, hidden, rdt):
+    """x·router with one Inf in x, in any column: the logits are Inf of the
+    router's signs, so the experts are chosen by those (ties: the lower one)."""
+    k, inter = 3, 32
+    rng = np.random.default_rng(7)
+    cfg = pq.MoeConfig(hidden, inter, E, k, 4, 32, "silu", True)
+    packed = torch.empty(pq.gptq_w4a16_moe_packed_bytes(cfg), dtype=torch.uint8, device="cuda")
+    gi, gm = H.group_index(hidden, 32, rng, False), H.group_index(inter, 32, rng, False)
+    gate, down = H.weight(inter, hidden, 4, 32, rng, gi), H.weight(hidden, inter, 4, 32, rng, gm)
+    for e in range(E):
+        pq.gptq_w4a16_moe_pack(cfg, e, *H.gpu(gate[:3]), *H.gpu(gate), *H.gpu(down), packed)
+    X = H.activations(tokens, hidden, seed=8)
+    R = H.vector((E, hidden), rdt, 9)
+    want = np.argsort(-(H.f64(X) @ H.f64(R).T), axis=1, kind="stable")[:, :k]
+    for col in (0, 1, 7, 8, hidden // 2, hidden - 1):
+        B = X.clone()
+        B[tokens // 2, col] = float("inf")
+        Y, ids, _ = pq.gptq_w4a16_moe(B.cuda(), R.cuda(), packed, cfg)
+        rows = want.copy()
+        rows[tokens // 2] = np.argsort(-np.sign(H.f64(R)[:, col]), kind="stable")[:k]
+        assert np.array_equal(ids.cpu().numpy(), rows), col
+        keep = torch.arange(tokens) != tokens // 2
+        assert torch.isfinite(Y.cpu()[keep]).all() and torch.isnan(Y.cpu()[tokens // 2]).all()
