@@ -337,7 +337,9 @@ gptq_status gptq_w4a16_matmul_noalloc(const void* X, int64_t tokens, int64_t ldx
  * `workspace` (256-byte aligned, contents not kept) belongs to one call at a
  * time; *_workspace_bytes(tokens, ...) bytes serve every call of up to that
  * many tokens.  tokens == 0 is a no-op.  Y may be the residual itself (the same
- * pointer, type and row stride); otherwise no output may overlap an input.
+ * pointer, type and row stride); otherwise no output may overlap an input (a Y
+ * that shares a byte with a row of X or of the residual is refused; column
+ * slices of one buffer do not).
  *
  * gptq_w4a16_linear: Y[t][r] = act(Σ_c X[t][c]·Ŵ[r][c] + bias[r]) +
  * residual[t][r], with gptq_w4a16_pack's packed weight; bias [m] and residual

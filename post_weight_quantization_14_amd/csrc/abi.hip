@@ -463,6 +463,43 @@ static gptq_status check_l4_tensor(const char* name, const void* p, int32_t dtyp
   return GPTQ_OK;
 }
 
+struct RowSpan {
+  const void* p;
+  int64_t rows, pitch, width;   // of a row, in bytes; width <= pitch
+};
+
+// Whether a row of `a` shares a byte with a row of `b`.  Column slices of one
+// buffer lie between each other's rows and do not.
+static bool rows_overlap(const RowSpan& a, const RowSpan& b) {
+  const int64_t d = (int64_t)((intptr_t)b.p - (intptr_t)a.p);
+  if (d >= (a.rows - 1) * a.pitch + a.width || -d >= (b.rows - 1) * b.pitch + b.width) return false;
+  auto meet = [&](int64_t i, int64_t j) {   // a's row i and b's row j
+    const int64_t at = d + j * b.pitch - i * a.pitch;
+    return i >= 0 && i < a.rows && at < a.width && at + b.width > 0;
+  };
+  auto row_at = [&](int64_t x) { return x / a.pitch - (x % a.pitch < 0); };   // rounded down
+  if (a.pitch == b.pitch) {   // b's row j can meet a's rows j + q and j + q + 1, for every j alike
+    const int64_t q = row_at(d), j0 = std::max<int64_t>(0, -q), j1 = std::max<int64_t>(0, -q - 1);
+    return (j0 < b.rows && meet(j0 + q, j0)) || (j1 < b.rows && meet(j1 + q + 1, j1));
+  }
+  for (int64_t j = 0; j < b.rows; ++j) {
+    const int64_t i = std::max<int64_t>(0, row_at(d + j * b.pitch));
+    if (meet(i, j) || meet(i + 1, j)) return true;
+  }
+  return false;
+}
+
+// Y overlaps X, or the residual without being it
+static gptq_status check_l4_overlap(const void* X, int64_t ldx, int64_t n, const void* res, int32_t res_dtype, int64_t ldr,
+                                    const void* Y, int32_t y_dtype, int64_t ldy, int64_t m, int64_t tokens) {
+  const int64_t ysz = (int64_t)dtype_bytes(y_dtype), rsz = (int64_t)dtype_bytes(res_dtype);
+  const RowSpan y{Y, tokens, ldy * ysz, m * ysz};
+  if (rows_overlap(RowSpan{X, tokens, ldx * 2, n * 2}, y)) return fail(GPTQ_ERR_INVALID_ARG, "Y overlaps X");
+  if (res && res != Y && rows_overlap(RowSpan{res, tokens, ldr * rsz, m * rsz}, y))
+    return fail(GPTQ_ERR_INVALID_ARG, "Y overlaps the residual");
+  return GPTQ_OK;
+}
+
 size_t gptq_w4a16_linear_workspace_bytes(int64_t tokens, int64_t m, int64_t n, int32_t group_size) {
   if (tokens < 0 || tokens > kL4MaxTokens || m < 0 || m > kL4MaxRows || n <= 0 || n > kL4MaxCols ||
       !w4_group_ok(group_size))
@@ -486,6 +523,7 @@ gptq_status gptq_w4a16_linear(const void* X, int64_t tokens, int64_t ldx, const 
   const W4Layout L = plan_w4a16(m, n, group_size);
   const L4LinearPlan p = plan_w4a16_linear(tokens, n, L.mt * 16);
   GPTQ_TRY(check_l4_buffers(packed_bytes, L.total, workspace, ws_bytes, p.total));
+  GPTQ_TRY(check_l4_overlap(X, ldx, n, e.residual, e.residual_dtype, e.ldr, Y, y_dtype, ldy, m, tokens));
   const L4Call c{static_cast<const uint16_t*>(X), tokens, ldx, m, packed, e.activation, e.bias_dtype,
                  e.residual_dtype, y_dtype, e.bias, nullptr, e.residual, e.ldr, Y, ldy};
   return run_w4a16_linear(c, L, false, workspace, p, static_cast<hipStream_t>(stream));
@@ -542,6 +580,7 @@ gptq_status gptq_w4a16_glu(const void* X, int64_t tokens, int64_t ldx, const voi
   const W4Layout L = plan_w4a16_pair(m, n, group_size);
   const L4LinearPlan p = plan_w4a16_linear(tokens, n, L.mt * 16);
   GPTQ_TRY(check_l4_buffers(packed_bytes, L.total, workspace, ws_bytes, p.total));
+  GPTQ_TRY(check_l4_overlap(X, ldx, n, nullptr, 0, 0, Y, y_dtype, ldy, m, tokens));
   const L4Call c{static_cast<const uint16_t*>(X), tokens, ldx, m, packed, activation, bias_dtype, 0, y_dtype,
                  gate_bias, up_bias, nullptr, 0, Y, ldy};
   return run_w4a16_linear(c, L, true, workspace, p, static_cast<hipStream_t>(stream));
@@ -627,6 +666,7 @@ gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const voi
     return fail(GPTQ_ERR_INVALID_ARG, "topk_ids or topk_weights is misaligned");
   const MoeWork w = plan_moe_work(*cfg, tokens);
   GPTQ_TRY(check_l4_buffers(packed_bytes, plan_moe(*cfg).stride * (size_t)cfg->experts, workspace, ws_bytes, w.total));
+  GPTQ_TRY(check_l4_overlap(X, ldx, cfg->hidden, residual, residual_dtype, ldr, Y, y_dtype, ldy, cfg->hidden, tokens));
   const MoeCall c{static_cast<const uint16_t*>(X), tokens, ldx, router, router_dtype, packed, residual,
                   residual_dtype, ldr, Y, y_dtype, ldy, topk_ids, topk_weights};
   return run_moe(c, *cfg, workspace, w, static_cast<hipStream_t>(stream));

@@ -149,3 +149,29 @@ def test_moe_routes_a_token_with_an_infinity_by_its_logits(pq, tokens, E, hidden
         assert np.array_equal(ids.cpu().numpy(), rows), col
         keep = torch.arange(tokens) != tokens // 2
         assert torch.isfinite(Y.cpu()[keep]).all() and torch.isnan(Y.cpu()[tokens // 2]).all()
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 40])
+def test_output_between_the_rows_of_its_input(pq, tokens):
+    """X, the residual and Y are column slices of one buffer: none overlaps
+    another.  Shifted onto X by one column, the call is refused."""
+    m, n = 40, 200
+    rng = np.random.default_rng(tokens)
+    w = H.weight(m, n, 4, 64, rng, H.group_index(n, 64, rng, True))
+    packed = pq.gptq_w4a16_pack(*H.gpu(w), n, 4, 64)
+    X, R = H.activations(tokens, n, seed=1), H.vector((tokens, m), "bf16", 2)
+    for order in (("r", "x", "y"), ("y", "r", "x"), ("x", "y", "r")):
+        at, col = {}, 0
+        for name in order:
+            at[name] = col
+            col += n if name == "x" else m
+        buf = torch.zeros(tokens, col, dtype=torch.bfloat16, device="cuda")
+        x, r, y = (buf[:, at[v]:at[v] + (n if v == "x" else m)] for v in "xry")
+        x.copy_(X)
+        r.copy_(R)
+        pq.gptq_w4a16_linear(x, packed, m, n, 64, residual=r, Y=y)
+        ref, bound = H.linear_ref(H.f64(X), w, n, 4, residual=H.f64(R), out="bf16")
+        H.check(y, ref, bound, f"slices {order}", "bf16")
+        over = buf[:, at["x"]:at["x"] + m]
+        with pytest.raises(pq.GptqError, match="overlaps X"):
+            pq.gptq_w4a16_linear(x, packed, m, n, 64, Y=over)

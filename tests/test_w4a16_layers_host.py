@@ -147,6 +147,60 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(L):
         pq.MoeConfig(64, 32, 4, 2, activation="swish").c()
 
 
+def _meet(a, ra, pa, wa, b, rb, pb, wb):
+    """Whether rows of two strided byte matrices share a byte, the plain way."""
+    rows = lambda p, r, pitch, w: {q for i in range(r) for q in range(p + i * pitch, p + i * pitch + w)}  # noqa: E731
+    return bool(rows(a, ra, pa, wa) & rows(b, rb, pb, wb))
+
+
+def test_output_over_an_input_is_refused(L, lb):
+    """Every layout of X, Y and the residual in one buffer: refused where rows
+    share a byte (the last check before the launch, so the ones that pass are
+    made to fail after it: no device here runs them)."""
+    n, m, T = 40, 24, 5
+    packed = L.gptq_w4a16_packed_bytes(m, n, 32)
+    need = L.gptq_w4a16_linear_workspace_bytes(T, m, n, 32)
+    rng = np.random.default_rng(0)
+    seen = set()
+    for _ in range(400):
+        ldx, ldy, ydt = n + int(rng.choice([0, 3, 30, 60])), m + int(rng.choice([0, 1, 46, 76])), int(rng.integers(2))
+        size = 4 if ydt else 2
+        at = FAKE + size * int(rng.integers(-300, 300))
+        want = _meet(FAKE, T, 2 * ldx, 2 * n, at, T, size * ldy, size * m)
+        if not want:
+            continue      # would launch: tested on the GPU
+        seen.add((ldx * 2 == ldy * size, at < FAKE))
+        st = L.gptq_w4a16_linear(FAKE, T, ldx, FAKE * 8, packed, m, n, 32, None, at, ydt, ldy, FAKE * 16, need, None)
+        assert st == lb.GPTQ_ERR_INVALID_ARG and b"overlaps X" in L.gptq_last_error()
+    assert len(seen) == 4
+    E = lb.GptqEpilogue
+    for off, ldr in ((2, m), (-2 * m, m), (2 * m, m + 1), (0, m)):
+        e = E(residual=FAKE + off, residual_dtype=0 if off else 1, ldr=ldr)
+        st = L.gptq_w4a16_linear(FAKE * 4, T, n, FAKE * 8, packed, m, n, 32, ctypes.byref(e), FAKE, 0, m, FAKE * 16, need,
+                                 None)
+        assert st == lb.GPTQ_ERR_INVALID_ARG
+    c = lb.GptqMoeConfig(n, m, 4, 2, 4, 32, 2, 1)
+    pb, ws = L.gptq_w4a16_moe_packed_bytes(ctypes.byref(c)), L.gptq_w4a16_moe_workspace_bytes(ctypes.byref(c), T)
+    st = L.gptq_w4a16_moe(FAKE, T, n, FAKE * 2, 0, ctypes.byref(c), FAKE * 8, pb, FAKE, 0, n, FAKE, 0, n, None, None,
+                          FAKE * 16, ws, None)     # X, residual and Y are one
+    assert st == lb.GPTQ_ERR_INVALID_ARG and b"overlaps X" in L.gptq_last_error()
+    gb, gw = L.gptq_w4a16_glu_packed_bytes(m, n, 32), L.gptq_w4a16_glu_workspace_bytes(T, m, n, 32)
+    st = L.gptq_w4a16_glu(FAKE, T, n, FAKE * 8, gb, m, n, 32, 2, None, None, 0, FAKE + 2, 0, n, FAKE * 16, gw, None)
+    assert st == lb.GPTQ_ERR_INVALID_ARG and b"overlaps X" in L.gptq_last_error()
+
+
+def test_smaller_calls_pass_with_the_workspace_of_a_larger(L, lb):
+    """What refuses these calls is the check after the workspace's: Y on X."""
+    m = n = 4096
+    pb = L.gptq_w4a16_packed_bytes(m, n, 128)
+    for most in (2048, 4096, 8192):
+        need = L.gptq_w4a16_linear_workspace_bytes(most, m, n, 128)
+        for tokens in (most, 5000, 1024, 1000, 600, 64, 1):
+            if tokens <= most:
+                st = L.gptq_w4a16_linear(FAKE, tokens, n, FAKE, pb, m, n, 128, None, FAKE, 0, m, FAKE, need, None)
+                assert st == lb.GPTQ_ERR_INVALID_ARG, (most, tokens)
+
+
 @pytest.mark.parametrize("m,n,g", [(4096, 4096, 128), (11008, 4096, 128), (4096, 11008, 64), (1031, 1000, 64),
                                    (128, 20000, -1), (17, 33, 32)])
 def test_workspace_of_the_largest_batch_serves_smaller_ones(L, lb, m, n, g):
