@@ -460,7 +460,9 @@ def _empty(shape, dtype: torch.dtype, X: torch.Tensor, stream) -> torch.Tensor:
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=X.device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=X.device)
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        # ExternalStream(0) is not the default stream but a new one of torch's
+        stream = torch.cuda.ExternalStream(handle, device=X.device) if handle else torch.cuda.default_stream(X.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=X.device)
 

@@ -175,3 +175,30 @@ def test_output_between_the_rows_of_its_input(pq, tokens):
         over = buf[:, at["x"]:at["x"] + m]
         with pytest.raises(pq.GptqError, match="overlaps X"):
             pq.gptq_w4a16_linear(x, packed, m, n, 64, Y=over)
+
+
+def test_memory_of_a_call_belongs_to_the_stream_it_is_given(pq):
+    """Output and workspace come from the memory of the stream of the call, of
+    the default stream too where it is given as its handle, 0."""
+    m, n = 40, 200
+    rng = np.random.default_rng(4)
+    w = H.weight(m, n, 4, 64, rng, H.group_index(n, 64, rng, True))
+    packed = pq.gptq_w4a16_pack(*H.gpu(w), n, 4, 64)
+    X = H.activations(9, n, seed=5).cuda()
+    want = pq.gptq_w4a16_linear(X, packed, m, n, 64)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda.empty_cache()
+
+    def owner(t):
+        return [s["stream"] for s in torch.cuda.memory_snapshot()
+                if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
+
+    for stream, handle in ((0, 0), (torch.cuda.default_stream(), 0), (side, side.cuda_stream),
+                           (side.cuda_stream, side.cuda_stream)):
+        before = {s["address"] for s in torch.cuda.memory_snapshot()}
+        Y = pq.gptq_w4a16_linear(X, packed, m, n, 64, stream=stream)
+        torch.cuda.synchronize()
+        assert owner(Y) == [handle]
+        assert {s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] not in before} <= {handle}
+        assert torch.equal(Y, want)
