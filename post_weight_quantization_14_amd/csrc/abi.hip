@@ -2,6 +2,7 @@
 // workspace layout, then the stage launchers (hessian.hip, prepare.hip,
 // quantize.hip).  Every check here runs before any HIP call, so a rejected
 // call touches no GPU state.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -639,6 +640,31 @@ size_t gptq_w4a16_moe_workspace_bytes(const gptq_moe_config* cfg, int64_t tokens
     return 0;
   }
   return moe_workspace(*cfg, tokens);
+}
+
+// Host only, not in the public header: the kernels that a call would run, for
+// the tests, which say which of them each case is meant to reach.
+int gptq_internal_w4a16_linear_path(int64_t tokens, int64_t m, int64_t n, int32_t group_size, int32_t gated,
+                                    int32_t out[5]) {
+  if (tokens <= 0 || m <= 0 || n <= 0 || tokens > kL4MaxTokens || m > kL4MaxRows || n > kL4MaxCols ||
+      !w4_group_ok(group_size))
+    return 0;
+  const W4Layout L = gated ? plan_w4a16_pair(m, n, group_size) : plan_w4a16(m, n, group_size);
+  const L4Path p = w4a16_linear_path(tokens, L, gated != 0);
+  const int32_t v[5] = {p.tile, p.gather, p.whole, p.parted, p.splits};
+  std::copy(v, v + 5, out);
+  return 1;
+}
+
+int gptq_internal_w4a16_moe_path(const gptq_moe_config* cfg, int64_t tokens, int32_t y_dtype, int32_t out[7]) {
+  if (check_moe(cfg) != GPTQ_OK || tokens <= 0 || tokens > kL4MaxTokens || !float_dtype(y_dtype)) {
+    clear_error();
+    return 0;
+  }
+  const MoePath p = moe_path(*cfg, tokens, y_dtype);
+  const int32_t v[7] = {p.small, p.logits, p.gate_up_lds, p.gate_up_pass, p.down_lds, p.down_pass, p.slices};
+  std::copy(v, v + 7, out);
+  return 1;
 }
 
 gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const void* router, int32_t router_dtype,

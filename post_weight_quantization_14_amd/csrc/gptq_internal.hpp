@@ -238,6 +238,12 @@ L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n, int64_t packed_rows);
 // bytes that any call of up to `tokens` tokens can do with (a call of exactly
 // so many needs plan_w4a16_linear's total, which may be less)
 size_t w4a16_linear_workspace(int64_t tokens, int64_t n, int64_t packed_rows);
+// what the first launch sequence of such a call runs: 16 (decode kernel; `gather`:
+// X' gathered by it) or the tile kernel's tokens, its tiles and their K slices
+struct L4Path {
+  int tile, gather, whole, parted, splits;
+};
+L4Path w4a16_linear_path(int64_t tokens, const W4Layout& L, bool gated);
 struct L4Call {
   const uint16_t* X;
   int64_t tokens, ldx, m;
@@ -264,6 +270,13 @@ struct MoeWork {
 };
 MoeWork plan_moe_work(const gptq_moe_config& c, int64_t tokens);
 size_t moe_workspace(const gptq_moe_config& c, int64_t tokens);   // for any count up to `tokens`
+// what the first launch sequence of such a call runs: the two launches; logits in
+// a launch of their own; rows of gate/up and of down in LDS or read from memory,
+// tokens of a pass; down's K slices
+struct MoePath {
+  int small, logits, gate_up_lds, gate_up_pass, down_lds, down_pass, slices;
+};
+MoePath moe_path(const gptq_moe_config& c, int64_t tokens, int y_dtype);
 struct MoeCall {
   const uint16_t* X;
   int64_t tokens, ldx;

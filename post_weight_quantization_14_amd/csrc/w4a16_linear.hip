@@ -778,6 +778,34 @@ gptq_status launch_l4_gemm(const L4GemmArgs& g, const L4Shape& s, int gs, bool g
 }  // namespace
 
 namespace {
+// What a launch sequence of tk tokens runs.  Few tokens whose X' and sums fit in
+// LDS take the decode kernel, which gathers X' itself where that is a barrier or
+// two of work; the others the tiles of `shape`.
+struct L4Choice {
+  bool decode = false, gather = false;
+  int quads = 0, batch = 0;   // decode: 4-token groups of a tile, raw rows gathered at a time
+  size_t lds = 0;
+  L4Shape shape;
+};
+L4Choice l4_choose(int64_t tk, const W4Layout& L, bool gated) {
+  L4Choice c;
+  const int rt = gated ? 2 : 1;
+  const int64_t ttiles = ceil_div(tk, 16);
+  c.shape = l4_shape(tk, L.mt * kL4Rows, L.kc);
+  if (ttiles > 1 && l4_decode_us(ttiles, L.mt / rt, L.kc, rt) >= c.shape.us + 3.0) return c;
+  const int64_t tt = std::min<int64_t>(tk, 16);   // tokens of a tile
+  c.quads = (int)ceil_div(tt, 4);
+  const size_t rows = (size_t)tt * (size_t)(L.n128 + kL4Pad) * 2;
+  const size_t red = (size_t)kL4Waves * rt * c.quads * 64 * sizeof(float);
+  const size_t raw = (size_t)round_up(L.n * 2, 16);
+  c.decode = rows + red <= kL4MaxLds;
+  if (!c.decode) return c;
+  c.batch = (int)std::min<int64_t>(tt, (int64_t)((kL4MaxLds - rows) / raw));
+  c.gather = 2 * c.batch >= tt && tt * L.n128 <= kL4GatherMax;
+  c.lds = rows + std::max(red, c.gather ? raw * (size_t)c.batch : 0);
+  return c;
+}
+
 // the K slices' partial sums of a launch sequence of tk tokens
 size_t l4_part_bytes(int64_t tk, int64_t packed_rows, int64_t kc) {
   const L4Shape s = l4_shape(tk, packed_rows, kc);
@@ -798,6 +826,12 @@ L4LinearPlan plan_w4a16_linear(int64_t tokens, int64_t n, int64_t packed_rows) {
   for (int64_t tk : {p.block, tokens % p.block})
     if (tk > 0) p.total = std::max(p.total, p.part_off + l4_part_bytes(tk, packed_rows, kc));
   return p;
+}
+
+L4Path w4a16_linear_path(int64_t tokens, const W4Layout& L, bool gated) {
+  const L4Choice c = l4_choose(std::min(tokens, kL4BlockTokens), L, gated);
+  if (c.decode) return {16, c.gather, 0, 0, 1};
+  return {c.shape.tokens, 0, (int)c.shape.whole, (int)(c.shape.tblocks * c.shape.rblocks - c.shape.whole), c.shape.splits};
 }
 
 // Fewer tokens may be cut into more slices (2048 tokens of 4096 x 4096 fill the
@@ -837,27 +871,9 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
     const L4Epilogue ep{c.act, c.bias_dtype, c.res_dtype, c.y_dtype, c.bias, c.bias2,
                         c.res ? static_cast<const char*>(c.res) + (size_t)(t0 * c.ldr) * rsz : nullptr,
                         static_cast<char*>(c.Y) + (size_t)(t0 * c.ldy) * ysz, c.ldr, c.ldy};
-    // Few tokens whose X' and sums fit in LDS take the decode kernel, which
-    // gathers X' itself where that is a barrier or two of work.
-    L4DecodeArgs d;
-    bool decode = false, gather = false;
-    size_t dlds = 0;
-    const int64_t ttiles = ceil_div(tk, 16);
-    const L4Shape sh = l4_shape(tk, L.mt * kL4Rows, L.kc);
-    if (ttiles == 1 || l4_decode_us(ttiles, st.units, L.kc, gated ? 2 : 1) < sh.us + 3.0) {
-      const int64_t tt = std::min<int64_t>(tk, 16);   // tokens of a tile
-      d.quads = (int)ceil_div(tt, 4);
-      const size_t rows = (size_t)tt * (size_t)(L.n128 + kL4Pad) * 2;
-      const size_t red = (size_t)kL4Waves * (gated ? 2 : 1) * d.quads * 64 * sizeof(float);
-      const size_t raw = (size_t)round_up(L.n * 2, 16);
-      decode = rows + red <= kL4MaxLds;
-      if (decode) {
-        d.batch = (int)std::min<int64_t>(tt, (int64_t)((kL4MaxLds - rows) / raw));
-        gather = 2 * d.batch >= tt && tt * L.n128 <= kL4GatherMax;
-        dlds = rows + std::max(red, gather ? raw * (size_t)d.batch : 0);
-      }
-    }
-    if (!gather) {
+    const L4Choice ch = l4_choose(tk, L, gated);
+    const L4Shape& sh = ch.shape;
+    if (!ch.gather) {
       const size_t glds = (size_t)L.n * 2 <= kL4GatherLds ? (size_t)round_up(L.n * 2, 16) : 0;
       const dim3 ggrid((unsigned)tk, (unsigned)ceil_div(L.n128, 4096));
 #define L4_GATHER(GS)                                                                                             \
@@ -875,7 +891,11 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
 #undef L4_GATHER
       GPTQ_LAUNCH_CHECK();
     }
-    if (decode) {
+    if (ch.decode) {
+      const int64_t ttiles = ceil_div(tk, 16);
+      L4DecodeArgs d;
+      d.quads = ch.quads;
+      d.batch = ch.batch;
       d.X = X;
       d.order = order;
       d.ldx = c.ldx;
@@ -895,7 +915,7 @@ gptq_status run_w4a16_linear(const L4Call& c, const W4Layout& L, bool gated, voi
       d.st = st;
       // workgroups that the split leaves without units are not launched
       const unsigned grid = (unsigned)std::min<int64_t>(wgs, ceil_div(st.units, kL4Waves >> sp.kslog));
-      GPTQ_TRY(launch_l4_decode(d, gs, gated, gather, dim3(grid, (unsigned)ttiles), dlds, stream));
+      GPTQ_TRY(launch_l4_decode(d, gs, gated, ch.gather, dim3(grid, (unsigned)ttiles), ch.lds, stream));
       continue;
     }
     L4GemmArgs g;

@@ -784,6 +784,49 @@ bool moe_is_small(const gptq_moe_config& c, int64_t tokens, int planes, const Mo
          tokens * c.experts * c.hidden <= (tokens <= 2 ? kSmallRouter2 : kSmallRouter) && x <= 64 * 1024 && mid <= 100 * 1024;
 }
 
+// The form of a call of `tk` tokens: the two launches, or the split over the GPU
+// and the passes of gate/up and down (launch-dependent fields of g and d).
+struct MoeForm {
+  bool small, logits, gu_in_lds, down_in_lds;   // logits: in a launch of their own
+  int64_t slots, passes;
+  size_t gu_lds, down_lds;
+  dim3 gu_grid, down_grid;
+};
+MoeForm moe_form(const gptq_moe_config& c, int tk, const MoeLayout& L, MoeExpertArgs& g, MoeExpertArgs& d) {
+  MoeForm f{};
+  f.small = moe_is_small(c, tk, d.planes, L);
+  f.logits = !f.small && (int64_t)tk * c.experts * c.hidden > kMoeLogitsElsewhere && c.experts > 16;
+  // the workgroups of the GPU dealt over the experts that can be active; where an
+  // expert has more tokens than a pass on average, passes side by side
+  f.slots = std::min<int64_t>(c.experts, (int64_t)tk * c.top_k);
+  f.passes = ceil_div((int64_t)tk * c.top_k, (int64_t)c.experts * kMoePass);
+  const int64_t share = std::max<int64_t>(1, 256 / (f.slots * f.passes));
+  g.tokens = d.tokens = tk;
+  d.slices = moe_slices(c, tk, d.planes);
+  const int64_t gw = std::min<int64_t>(share, g.st.units);
+  f.gu_lds = moe_plan(g, tk, 1, 2, gw, &f.gu_in_lds);
+  f.gu_grid = dim3((unsigned)std::min<int64_t>(gw, ceil_div(g.st.units, kL4Waves >> g.st.kslog)), (unsigned)f.slots,
+                   (unsigned)f.passes);
+  const int64_t dw = std::min<int64_t>(std::max<int64_t>(1, share / d.slices), d.st.units);
+  f.down_lds = moe_plan(d, tk, d.planes, 1, dw, &f.down_in_lds);
+  f.down_grid = dim3((unsigned)std::min<int64_t>(dw, ceil_div(d.st.units, kL4Waves >> d.st.kslog)), (unsigned)f.slots,
+                     (unsigned)(f.passes * d.slices));
+  return f;
+}
+
+int moe_planes(int y_dtype) { return y_dtype == GPTQ_FP32 ? 3 : 2; }
+
+// Sizes of a product; one group per row folds as groups of 128 (pmul = 0 repeats
+// its parameters)
+void moe_sizes(MoeExpertArgs& a, const gptq_moe_config& c, const W4Layout& l, int64_t units, int planes) {
+  a.st = L4Stream{nullptr, nullptr, l.kc, l.Gp, units, l.g >= l.n128 ? 0 : kL4Rows, 0, 1, 0, (int)l.kc};
+  a.slices = 1;
+  a.k128 = l.n128;
+  a.top_k = c.top_k;
+  a.experts = c.experts;
+  a.planes = planes;
+}
+
 template <class A, class K>
 gptq_status moe_launch(K kernel, dim3 grid, size_t lds, const A& a, hipStream_t stream) {
   if (lds > 32768)
@@ -838,6 +881,15 @@ MoeWork plan_moe_work(const gptq_moe_config& c, int64_t tokens) {
   return w;
 }
 
+MoePath moe_path(const gptq_moe_config& c, int64_t tokens, int y_dtype) {
+  const MoeLayout L = plan_moe(c);
+  MoeExpertArgs g{}, d{};
+  moe_sizes(g, c, L.gu, L.gu.mt / 2, moe_planes(y_dtype));
+  moe_sizes(d, c, L.down, L.down.mt, moe_planes(y_dtype));
+  const MoeForm f = moe_form(c, (int)std::min<int64_t>(tokens, kMoeTokens), L, g, d);
+  return {f.small, f.logits, f.gu_in_lds, g.pass, f.down_in_lds, d.pass, d.slices};
+}
+
 // The slices of K change with the tokens (none where a few fit in LDS, none
 // again where their results pass 256 MB), so the largest of all counts up to
 // `tokens`: 1 .. 64, and 64 with every rest.
@@ -875,20 +927,14 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
   const int h = (int)cfg.hidden;
 
   uint16_t* Xp = reinterpret_cast<uint16_t*>(wb + w.xp_off);
-  // one group per row folds as groups of 128 (pmul = 0 repeats its parameters)
   auto weight = [&](MoeExpertArgs& a, const W4Layout& l, const char* base, int64_t units) {
     a.packed = base;
     a.stride = (int64_t)L.stride;
     a.param_off = (int64_t)l.param_off;
     a.code_off = (int64_t)l.code_off;
-    a.st = L4Stream{nullptr, nullptr, l.kc, l.Gp, units, l.g >= l.n128 ? 0 : kL4Rows, 0, 1, 0, (int)l.kc};
-    a.slices = 1;
-    a.k128 = l.n128;
+    moe_sizes(a, cfg, l, units, moe_planes(c.y_dtype));
     a.ids = ids;
-    a.top_k = cfg.top_k;
-    a.experts = cfg.experts;
     a.act = cfg.activation;
-    a.planes = c.y_dtype == GPTQ_FP32 ? 3 : 2;
     a.mid = mid;
     a.out = out;
   };
@@ -924,23 +970,12 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
     r.order_off = (int64_t)L.gu.order_off;
     r.n128 = L.gu.n128;
     r.Xp = Xp;
-    r.logits = (int64_t)tk * cfg.experts * h > kMoeLogitsElsewhere && cfg.experts > 16 ? logits : nullptr;
+    const MoeForm f = moe_form(cfg, tk, L, g, d);
+    r.logits = f.logits ? logits : nullptr;
     if (r.logits) r.parts = 1;
     const void* res = c.res ? (const void*)(static_cast<const char*>(c.res) + (size_t)(t0 * c.ldr) * rsz) : nullptr;
     void* Y = static_cast<char*>(c.Y) + (size_t)(t0 * c.ldy) * ysz;
-    // the workgroups of the GPU dealt over the experts that can be active
-    const int64_t slots = std::min<int64_t>(cfg.experts, (int64_t)tk * cfg.top_k);
-    // where an expert has more tokens than a pass on average, side by side
-    const int64_t passes = ceil_div((int64_t)tk * cfg.top_k, (int64_t)cfg.experts * kMoePass);
-    const int64_t share = std::max<int64_t>(1, 256 / (slots * passes));
-    const int64_t gw = std::min<int64_t>(share, g.st.units);
-    g.tokens = d.tokens = tk;
-    d.slices = moe_slices(cfg, tk, d.planes);
-    bool in_lds = false;
-    size_t lds = moe_plan(g, tk, 1, 2, gw, &in_lds);
-    const dim3 ggrid((unsigned)std::min<int64_t>(gw, ceil_div(g.st.units, kL4Waves >> g.st.kslog)), (unsigned)slots,
-                     (unsigned)passes);
-    if (moe_is_small(cfg, tk, g.planes, L)) {
+    if (f.small) {
       MoeSmallArgs sa;
       sa.x = g;
       sa.X = r.X;
@@ -958,11 +993,11 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
       sa.wts_out = r.wts_out;
       const size_t rows = (size_t)g.pass * (size_t)(g.k128 + kL4Pad) * 2;
       const size_t raw = (size_t)tk * (size_t)round_up(h, 8) * 2, red = (size_t)kL4Waves * 2 * g.quads * 64 * sizeof(float);
-      lds = rows + std::max(raw, red);
+      size_t lds = rows + std::max(raw, red);
       switch (steps(L.gu)) {
-        case 1: GPTQ_TRY(moe_launch(moe_small_gate_up_kernel<1>, ggrid, lds, sa, stream)); break;
-        case 2: GPTQ_TRY(moe_launch(moe_small_gate_up_kernel<2>, ggrid, lds, sa, stream)); break;
-        default: GPTQ_TRY(moe_launch(moe_small_gate_up_kernel<4>, ggrid, lds, sa, stream)); break;
+        case 1: GPTQ_TRY(moe_launch(moe_small_gate_up_kernel<1>, f.gu_grid, lds, sa, stream)); break;
+        case 2: GPTQ_TRY(moe_launch(moe_small_gate_up_kernel<2>, f.gu_grid, lds, sa, stream)); break;
+        default: GPTQ_TRY(moe_launch(moe_small_gate_up_kernel<4>, f.gu_grid, lds, sa, stream)); break;
       }
       MoeSmallDownArgs sd;
       sd.x = d;
@@ -998,18 +1033,14 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
                             (size_t)round_up(cfg.experts, 4) * sizeof(int) + xlds,
                         r, stream));
     switch (steps(L.gu)) {
-      case 1: GPTQ_TRY(launch_gate_up<1>(ggrid, lds, in_lds, g, stream)); break;
-      case 2: GPTQ_TRY(launch_gate_up<2>(ggrid, lds, in_lds, g, stream)); break;
-      default: GPTQ_TRY(launch_gate_up<4>(ggrid, lds, in_lds, g, stream)); break;
+      case 1: GPTQ_TRY(launch_gate_up<1>(f.gu_grid, f.gu_lds, f.gu_in_lds, g, stream)); break;
+      case 2: GPTQ_TRY(launch_gate_up<2>(f.gu_grid, f.gu_lds, f.gu_in_lds, g, stream)); break;
+      default: GPTQ_TRY(launch_gate_up<4>(f.gu_grid, f.gu_lds, f.gu_in_lds, g, stream)); break;
     }
-    const int64_t dw = std::min<int64_t>(std::max<int64_t>(1, share / d.slices), d.st.units);
-    lds = moe_plan(d, tk, d.planes, 1, dw, &in_lds);
-    const dim3 dgrid((unsigned)std::min<int64_t>(dw, ceil_div(d.st.units, kL4Waves >> d.st.kslog)), (unsigned)slots,
-                     (unsigned)(passes * d.slices));
     switch (steps(L.down)) {
-      case 1: GPTQ_TRY(launch_down<1>(dgrid, lds, in_lds, d, stream)); break;
-      case 2: GPTQ_TRY(launch_down<2>(dgrid, lds, in_lds, d, stream)); break;
-      default: GPTQ_TRY(launch_down<4>(dgrid, lds, in_lds, d, stream)); break;
+      case 1: GPTQ_TRY(launch_down<1>(f.down_grid, f.down_lds, f.down_in_lds, d, stream)); break;
+      case 2: GPTQ_TRY(launch_down<2>(f.down_grid, f.down_lds, f.down_in_lds, d, stream)); break;
+      default: GPTQ_TRY(launch_down<4>(f.down_grid, f.down_lds, f.down_in_lds, d, stream)); break;
     }
     hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)ceil_div(cfg.hidden, 256), (unsigned)tk), dim3(256), 0, stream,
                        (const float*)out, (const float*)wts, (int)cfg.top_k, d.slices, cfg.hidden, res, c.res_dtype, c.ldr, Y,
