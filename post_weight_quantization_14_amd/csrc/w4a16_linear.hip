@@ -481,12 +481,6 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
   }
 #undef L4_STEP
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy may land after the workgroup ends
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) y[mt][b][v] *= kL4Up;
 
   if constexpr (KG > 1) {
     // The groups' sums through LDS: every wave leaves its fragments, then each
@@ -514,6 +508,7 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
         z[b] = *at(0, mt * 8 + b * 4 + q);
 #pragma unroll
         for (int k = 1; k < KG; ++k) z[b] += *at(k, mt * 8 + b * 4 + q);
+        z[b] *= kL4Up;
       }
       if (split) {
         if (t0 + 32 * (MT * tg + mt) + 8 * q >= a.tokens) continue;   // not read
@@ -537,6 +532,12 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
     return;
   }
 
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) y[mt][b][v] *= kL4Up;
   if (split) {
     // fragments as they lie: [slice][tile][wave][mt][b][q][lane] float4
     f32x4_t* out = reinterpret_cast<f32x4_t*>(a.part) +
