@@ -309,6 +309,25 @@ def awq_quantize(W: torch.Tensor, x_tiles, cfg: RtnConfig, protect: float = 2.0)
 
 
 # ---------------------------------------------------------------- W4A16 product
+def _torch_stream(stream, device) -> torch.cuda.Stream:
+    """torch's object of a stream that is given as one or as its handle."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    # ExternalStream(0) is not the default stream but a new one of torch's
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
+def _new_packed(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
+    """Memory for a packed weight.  It outlives the call, so it is the current
+    stream's; a pack on another stream waits until the current one is done with
+    what was there before."""
+    packed = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device)
+    if stream is not None and like.is_cuda:
+        _torch_stream(stream, like.device).wait_stream(torch.cuda.current_stream(like.device))
+    return packed
+
+
 def gptq_w4a16_packed_bytes(m: int, n: int, group_size: int) -> int:
     return int(lib().gptq_w4a16_packed_bytes(m, n, group_size))
 
@@ -320,7 +339,7 @@ def gptq_w4a16_pack(qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Te
     m = qweight.shape[0]
     nbytes = gptq_w4a16_packed_bytes(m, n, group_size)
     if packed is None:
-        packed = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=qweight.device)
+        packed = _new_packed(nbytes, qweight, stream)
     st = lib().gptq_w4a16_pack(_ptr(qweight), _ptr(scales), _ptr(zeros), _ptr(g_idx), m, n, bits,
                                group_size, _ptr(packed), packed.numel() * packed.element_size(),
                                _stream(stream))
@@ -459,11 +478,7 @@ def _empty(shape, dtype: torch.dtype, X: torch.Tensor, stream) -> torch.Tensor:
     hands out memory that is free in the order of the stream it is asked on."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=X.device)
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        # ExternalStream(0) is not the default stream but a new one of torch's
-        stream = torch.cuda.ExternalStream(handle, device=X.device) if handle else torch.cuda.default_stream(X.device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_torch_stream(stream, X.device)):
         return torch.empty(shape, dtype=dtype, device=X.device)
 
 
@@ -578,8 +593,7 @@ def gptq_w4a16_glu_pack(gate_qweight: torch.Tensor, gate_scales: torch.Tensor, g
     _on(gate_qweight, gate_scales=gate_scales, gate_zeros=gate_zeros, up_qweight=up_qweight, up_scales=up_scales,
         up_zeros=up_zeros, g_idx=g_idx, packed=packed)
     if packed is None:
-        packed = torch.empty(max(gptq_w4a16_glu_packed_bytes(m, n, group_size), 1), dtype=torch.uint8,
-                             device=gate_qweight.device)
+        packed = _new_packed(gptq_w4a16_glu_packed_bytes(m, n, group_size), gate_qweight, stream)
     with _device(gate_qweight):
         st = lib().gptq_w4a16_glu_pack(_ptr(gate_qweight), _ptr(gate_scales), _ptr(gate_zeros), _ptr(up_qweight),
                                        _ptr(up_scales), _ptr(up_zeros), _ptr(g_idx), m, n, bits, group_size,

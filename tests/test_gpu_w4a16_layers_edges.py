@@ -202,3 +202,31 @@ def test_memory_of_a_call_belongs_to_the_stream_it_is_given(pq):
         assert owner(Y) == [handle]
         assert {s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] not in before} <= {handle}
         assert torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("pair", [False, True])
+def test_pack_on_another_stream_waits_for_the_memory_it_is_given(pq, pair):
+    """The packed weight's memory was freed on the current stream while work on
+    it was still to come there."""
+    m, n, g = 512, 1024, 64
+    rng = np.random.default_rng(6)
+    gidx = H.group_index(n, g, rng, True)
+    w = H.gpu(H.weight(m, n, 4, g, rng, gidx))
+    call = lambda s: (pq.gptq_w4a16_glu_pack(*w[:3], *w, n, 4, g, stream=s) if pair else       # noqa: E731
+                      pq.gptq_w4a16_pack(*w, n, 4, g, stream=s))
+    want = call(None)
+    head, body = want[:256].clone(), want[256:].clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    for handle in (side, side.cuda_stream):
+        was = torch.empty_like(want)
+        torch.cuda._sleep(50_000_000)
+        was.fill_(255)
+        at = was.data_ptr()
+        del was
+        got = call(handle)
+        assert got.data_ptr() == at
+        torch.cuda.synchronize()
+        assert torch.equal(got[256:], body) and torch.equal(got[:4], head[:4])
+        del got
