@@ -230,3 +230,59 @@ def test_pack_on_another_stream_waits_for_the_memory_it_is_given(pq, pair):
         torch.cuda.synchronize()
         assert torch.equal(got[256:], body) and torch.equal(got[:4], head[:4])
         del got
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_linear_of_the_most_columns(pq, tokens):
+    """2^20 columns, the most a call takes: groups of 32 and whole rows."""
+    m, n = 17, 1 << 20
+    rng = np.random.default_rng(1)
+    for g in (32, -1):
+        w = H.weight(m, n, 4, g, rng, H.group_index(n, g, rng, True))
+        packed = pq.gptq_w4a16_pack(*H.gpu(w), n, 4, g)
+        X = H.activations(tokens, n, seed=2)
+        Y = pq.gptq_w4a16_linear(X.cuda(), packed, m, n, g, out_dtype=torch.float32)
+        ref, bound = H.linear_ref(H.f64(X), w, n, 4)
+        H.check(Y, ref, bound, f"2^20 columns, {tokens} tokens, groups of {g}")
+    with pytest.raises(pq.GptqError, match="too large"):
+        pq.gptq_w4a16_linear(torch.empty(1, n + 1, dtype=torch.bfloat16, device="cuda"), packed, m, n + 1, 32)
+
+
+@pytest.mark.parametrize("m,n", [(40, 300), (40, 5003)])
+def test_linear_rows_beyond_32_bit_offsets(pq, m, n):
+    """Rows 2^27 elements apart: the last of 20 tokens is 2.4e9 in."""
+    tokens, ld = 20, 1 << 27
+    rng = np.random.default_rng(3)
+    w = H.weight(m, n, 4, 64, rng, H.group_index(n, 64, rng, True))
+    packed = pq.gptq_w4a16_pack(*H.gpu(w), n, 4, 64)
+    X, R = H.activations(tokens, n, seed=4), H.vector((tokens, m), "bf16", 5)
+    buf = torch.empty((tokens - 1) * ld + n + m, dtype=torch.bfloat16, device="cuda")
+    x, y = buf.as_strided((tokens, n), (ld, 1)), buf.as_strided((tokens, m), (ld, 1), n)
+    x.copy_(X)
+    y.copy_(R)
+    pq.gptq_w4a16_linear(x, packed, m, n, 64, residual=y, Y=y)
+    ref, bound = H.linear_ref(H.f64(X), w, n, 4, residual=H.f64(R), out="bf16")
+    H.check(y, ref, bound, f"rows 2^27 apart, {n} columns", "bf16")
+
+
+@pytest.mark.parametrize("hidden,inter,E,k,tokens", [(32768, 40, 3, 2, 1), (32768, 40, 3, 2, 9), (32768, 40, 20, 3, 9),
+                                                     (40, 32768, 3, 2, 1), (40, 32768, 3, 2, 9), (40, 32768, 2, 1, 30)])
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+def test_moe_of_the_most_columns(pq, hidden, inter, E, k, tokens, out):
+    g = 128
+    rng = np.random.default_rng(tokens)
+    cfg = pq.MoeConfig(hidden, inter, E, k, 4, g, "silu", True)
+    packed = torch.empty(pq.gptq_w4a16_moe_packed_bytes(cfg), dtype=torch.uint8, device="cuda")
+    experts = []
+    for e in range(E):
+        gi, gm = H.group_index(hidden, g, rng, True), H.group_index(inter, g, rng, True)
+        experts.append((H.weight(inter, hidden, 4, g, rng, gi), H.weight(inter, hidden, 4, g, rng, gi),
+                        H.weight(hidden, inter, 4, g, rng, gm)))
+        gate, up, down = experts[-1]
+        pq.gptq_w4a16_moe_pack(cfg, e, *H.gpu(gate[:3]), *H.gpu(up), *H.gpu(down), packed)
+    X = H.activations(tokens, hidden, seed=5, scale=0.125)
+    R = (H.vector((E, hidden), "fp32", 6) / hidden ** 0.5).to(torch.bfloat16)
+    Y, ids, _ = pq.gptq_w4a16_moe(X.cuda(), R.cuda(), packed, cfg, out_dtype=H.TDT[out])
+    ref, bound, rids, _ = H.moe_ref(H.f64(X), H.f64(R), experts, hidden, inter, 4, k, "silu", True, out=out)
+    assert np.array_equal(ids.cpu().numpy(), rids)
+    H.check(Y, ref, bound, f"experts of {hidden} x {inter}, {tokens} tokens", out)
