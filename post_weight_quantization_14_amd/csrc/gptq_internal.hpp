@@ -201,15 +201,12 @@ W4GemmPlan plan_w4a16_noalloc(int64_t tokens, int64_t m, int64_t n);
 gptq_status run_w4a16_matmul_noalloc(const uint16_t* X, int64_t tokens, int64_t ldx, const void* packed,
                                      const W4Layout& L, float* Y, int64_t ldy, hipStream_t stream);
 
-// Pieces of the pack and the gather that the layers below share: order[p] =
-// the column processed at position p (-1: padding) from g_idx, *flag != 0 if
-// g_idx does not split the columns; the host check of that flag (synchronises);
-// X' = X[:, order] with its 32- and 128-position sums.
+// Pieces of the pack that the layers below share: order[p] = the column
+// processed at position p (-1: padding) from g_idx, *flag != 0 if g_idx does not
+// split the columns; the host check of that flag (synchronises).
 gptq_status launch_w4_order(const int32_t* g_idx, const W4Layout& L, int32_t* order, int* flag,
                             hipStream_t stream);
 gptq_status check_w4_order(const int* flag, const char* where, hipStream_t stream);
-gptq_status launch_w4_gather(const uint16_t* X, int64_t ldx, const int32_t* order, int64_t n128, uint16_t* Xp,
-                             float* xs, float* xs4, int64_t tokens, hipStream_t stream);
 
 // ---------------------------------------------------------------- layers on packed weights
 // Two m x n weights of one input (gate and up), rows taken in row_order

@@ -776,8 +776,8 @@ gptq_status run_w4a16_pack(const uint32_t* qweight, const float* scales, const i
   return check_w4_order(flag, "gptq_w4a16_pack", stream);
 }
 
-gptq_status launch_w4_gather(const uint16_t* X, int64_t ldx, const int32_t* order, int64_t n128, uint16_t* Xp,
-                             float* xs, float* xs4, int64_t tokens, hipStream_t stream) {
+static gptq_status launch_w4_gather(const uint16_t* X, int64_t ldx, const int32_t* order, int64_t n128, uint16_t* Xp,
+                                    float* xs, float* xs4, int64_t tokens, hipStream_t stream) {
   const int64_t wpt = ceil_div(n128, 1024);
   const int64_t grid = 8 * ceil_div(tokens, 8) * wpt;
   hipLaunchKernelGGL(w4_gather_kernel, dim3((unsigned)grid), dim3(256), 0, stream, X, ldx, order, n128, Xp, xs,

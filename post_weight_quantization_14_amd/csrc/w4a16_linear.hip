@@ -134,8 +134,8 @@ struct L4DecodeArgs {
 // (linear) or one gate/up pair of tiles (glu).  X' is gathered here (GATHER) or
 // copied from X' in memory.  Bound by the code stream from HBM, at small sizes
 // by the chain launch - row - order - codes - sums and the call itself:
-// 4096 x 4096, 1 token 5.9 us (9.4 with Python's call), 11008 x 4096 pair
-// 16.1 us = 3.2 TB/s, 8192 x 29568 34.5 us = 4.0 TB/s.
+// 4096 x 4096, 1 token 6.9 us (9.4 with Python's call), 11008 x 4096 pair
+// 16.4 us = 3.1 TB/s, 8192 x 29568 33.7 us = 4.1 TB/s.
 template <int GS, bool GATED, bool GATHER>
 __global__ __launch_bounds__(kL4Threads) void l4_decode_kernel(L4DecodeArgs a) {
   constexpr int RT = GATED ? 2 : 1;
@@ -263,17 +263,18 @@ struct L4GemmArgs {
 //
 // X' comes through LDS (direct copies, two slots), the codes straight into
 // registers in operand order: 4 bits a weight would be 16 as operands in LDS.
-// Bound by power: 2048 x 22016 x 4096 takes 375 us = 0.99 PFLOP/s with the
-// matrix cores busy 58 % of the cycles and the clock down to 1.8 GHz (products
-// alone, from registers, run at 1.92); the library's bf16 product of that shape
-// takes 424 us.  A wave of 128 tokens x 32 rows unpacks an operand once for four
-// products, one of 64 x 64 halves the LDS reads instead: 412 and 423 us for the
-// whole call.  The zero points' term is one more product per group, not a fold
-// with the sums: 16 vector instructions and 4 LDS reads fewer for each 32 x 32
-// (10 % fewer cycles, 2 % of the time).  Tried and not kept: two chunks in
-// flight behind a second barrier (+2 %), the fold between the next products
-// (+7 %: it reads the A fragments twice), A fragments two steps ahead (0 %),
-// waves of 128 x 64, one per SIMD (+35 %).
+// Bound by issue: 2048 x 22016 x 4096 takes 358 us = 1.03 PFLOP/s in 675 000
+// cycles at 1.89 GHz, and the matrix instructions' 396 000 and the others'
+// 282 000 add up to that: the two waves of a SIMD leave the same barrier and
+// unpack and multiply in step, so neither hides the other's vector work.  (The
+// library's bf16 product of that shape takes 424 us.)  A wave of 128 tokens x
+// 32 rows unpacks an operand once for four products; one of 64 x 64, which
+// halves the LDS reads instead, took 3 % longer.  The zero points' term is one
+// more product per group, not a fold with the sums: 16 vector instructions and 4
+// LDS reads fewer for each 32 x 32 (2 % of the time).  Tried and not kept: two
+// chunks in flight behind a second barrier (+2 %), the fold between the next
+// products (+7 %: it reads the A fragments twice), A fragments two steps ahead
+// (0 %), waves of 128 x 64, one per SIMD (+35 %).
 template <int GS, int MT, int NB, int TG, int RG, int KG>
 struct L4Tile {
   static constexpr int kTokens = 32 * MT * TG, kRows = 32 * NB * RG, kGroup = TG * RG, kThreads = 64 * kGroup * KG;
