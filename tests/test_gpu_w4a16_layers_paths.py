@@ -254,3 +254,35 @@ def test_moe_down_reads_its_rows_from_memory(pq, g, hidden, inter, out):
         assert rel <= 5 * H.REL
     else:
         assert rel <= 5 * H.REL + 2.0 ** -8 + 2.0 ** -17 and off <= 0.05
+
+
+@pytest.mark.parametrize("gated,case", [(False, c) for c in LINEAR] + [(True, GLU[4]), (True, GLU[7])],
+                         ids=lambda v: _name(v) if isinstance(v, tuple) else "glu" if v else "linear")
+def test_graph_replays_on_every_path(pq, gated, case):
+    """Captured once, replayed with new inputs, eager calls on another workspace between."""
+    path, tokens, m, n = case
+    assert linear_path(pq.lib(), tokens, m, n, 64, gated) == path
+    rng = np.random.default_rng(m)
+    gidx = H.group_index(n, 64, rng, True)
+    w, v = (H.weight(m, n, 4, 64, rng, gidx) for _ in range(2))
+    if gated:
+        packed = pq.gptq_w4a16_glu_pack(*H.gpu(w[:3]), *H.gpu(v), n, 4, 64)
+        size, fn = pq.gptq_w4a16_glu_workspace_bytes, pq.gptq_w4a16_glu
+    else:
+        packed = pq.gptq_w4a16_pack(*H.gpu(w), n, 4, 64)
+        size, fn = pq.gptq_w4a16_linear_workspace_bytes, pq.gptq_w4a16_linear
+    ws = [torch.full((size(tokens, m, n, 64),), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    x, y = torch.zeros(tokens, n, dtype=torch.bfloat16, device="cuda"), torch.empty(tokens, m, device="cuda")
+    fn(x, packed, m, n, 64, Y=y, workspace=ws[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fn(x, packed, m, n, 64, Y=y, workspace=ws[0])
+    for k in range(4):
+        X = H.activations(tokens, n, seed=k).cuda()
+        x.copy_(X)
+        y.fill_(float("nan"))
+        graph.replay()
+        want = fn(X, packed, m, n, 64, out_dtype=torch.float32, workspace=ws[1])
+        torch.cuda.synchronize()
+        assert torch.isfinite(want).all() and torch.equal(y, want), f"replay {k}"
