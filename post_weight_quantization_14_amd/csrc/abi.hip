@@ -493,6 +493,12 @@ static bool rows_overlap(const RowSpan& a, const RowSpan& b) {
 // Y overlaps X, or the residual without being it
 static gptq_status check_l4_overlap(const void* X, int64_t ldx, int64_t n, const void* res, int32_t res_dtype, int64_t ldr,
                                     const void* Y, int32_t y_dtype, int64_t ldy, int64_t m, int64_t tokens) {
+  if (tokens == 1) {   // no second row: any stride will do
+    ldx = n;
+    ldr = ldy = m;
+  }
+  for (int64_t ld : {ldx, ldy, res ? ldr : 0})
+    if (ld > INT64_MAX / 8 / tokens) return fail(GPTQ_ERR_INVALID_ARG, "a row stride of %lld", (long long)ld);
   const int64_t ysz = (int64_t)dtype_bytes(y_dtype), rsz = (int64_t)dtype_bytes(res_dtype);
   const RowSpan y{Y, tokens, ldy * ysz, m * ysz};
   if (rows_overlap(RowSpan{X, tokens, ldx * 2, n * 2}, y)) return fail(GPTQ_ERR_INVALID_ARG, "Y overlaps X");

@@ -179,6 +179,14 @@ def test_output_over_an_input_is_refused(L, lb):
         st = L.gptq_w4a16_linear(FAKE * 4, T, n, FAKE * 8, packed, m, n, 32, ctypes.byref(e), FAKE, 0, m, FAKE * 16, need,
                                  None)
         assert st == lb.GPTQ_ERR_INVALID_ARG
+    for tokens in (1, T):      # strides whose bytes pass 64 bits: ignored for one row, refused for more
+        for big in (1 << 61, 1 << 62, (1 << 63) - 1):
+            e = E(residual=FAKE + 4, residual_dtype=1, ldr=big)
+            st = L.gptq_w4a16_linear(FAKE * 4, tokens, big, FAKE * 8, packed, m, n, 32, ctypes.byref(e), FAKE, 0, big,
+                                     FAKE * 16, need, None)
+            assert st == lb.GPTQ_ERR_INVALID_ARG
+            st = L.gptq_w4a16_linear(FAKE, tokens, big, FAKE * 8, packed, m, n, 32, None, FAKE, 0, m, FAKE * 16, need, None)
+            assert st == lb.GPTQ_ERR_INVALID_ARG
     c = lb.GptqMoeConfig(n, m, 4, 2, 4, 32, 2, 1)
     pb, ws = L.gptq_w4a16_moe_packed_bytes(ctypes.byref(c)), L.gptq_w4a16_moe_workspace_bytes(ctypes.byref(c), T)
     st = L.gptq_w4a16_moe(FAKE, T, n, FAKE * 2, 0, ctypes.byref(c), FAKE * 8, pb, FAKE, 0, n, FAKE, 0, n, None, None,
