@@ -27,8 +27,8 @@ constexpr int kL4Chunk = 128;   // positions per packed chunk (4 MFMA k-steps of
 // Both sums are held times 2^-12, and a result is multiplied by 2^12 when it is
 // whole: 128 positions·31 < 2^12, so no sum of a group overflows for any finite
 // x, where x·(16 + q) alone would from 1.1e37 on, with a result of Inf - Inf.
-// The factor is exact: other results keep their bits (x below 2^-114 lose some
-// of theirs to fp32's smallest numbers).
+// The factor is exact: other results keep their bits (of groups whose x are all
+// below 2^-102 some are lost to the smallest numbers of fp32 and of bf16 planes).
 constexpr float kL4Down = 0x1p-12f, kL4Up = 0x1p12f;
 
 struct L4Consts {

@@ -188,8 +188,12 @@ __device__ __forceinline__ L4Planes l4_planes(float v) {
   return {h, m, __float_as_uint(r - __uint_as_float(m))};
 }
 
-// X' = X[:, order] and 2^-12 of its group sums, groups-major (sums[c·NG + g][t], for the
-// tile kernel's contiguous copies, cut into three bf16 planes: an operand).  A row of X is read once, 16 bytes a
+constexpr float kL4SumDown = 0x1p-7f;
+
+// X' = X[:, order] and 2^-7 of its group sums (128 of them stay finite; the zero
+// points take the other 2^-5, bf16 planes end at 2^-133), groups-major
+// (sums[c·NG + g][t], for the tile kernel's contiguous copies, cut into three
+// bf16 planes: an operand).  A row of X is read once, 16 bytes a
 // thread, into LDS and gathered from there: 2-byte loads at scattered columns
 // cost the memory pipe a cycle or more a lane (2048 x 4096: 13 us, through
 // LDS 8.5), LDS serves 64 of them in a few cycles.  Thread: 8 positions; GS·4
@@ -228,7 +232,7 @@ __global__ __launch_bounds__(512) void l4_gather_kernel(const uint16_t* __restri
   }
   float s = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s = fmaf(__uint_as_float(v[e] << 16), kL4Down, s);
+  for (int e = 0; e < 8; ++e) s = fmaf(__uint_as_float(v[e] << 16), kL4SumDown, s);
   *reinterpret_cast<u32x4_t*>(Xp + t * n128 + p0) =
       u32x4_t{v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
 #pragma unroll
@@ -407,7 +411,7 @@ __device__ __forceinline__ void l4_gemm_tile(const L4GemmArgs& a, uint8_t* __res
       // its third
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const L4Planes z = l4_planes(-l4_zero(k.p[b][g].y));
+        const L4Planes z = l4_planes(l4_zero(k.p[b][g].y) * -(kL4Down / kL4SumDown));
         const uint32_t z0 = lane < 32 ? z.h : z.l, z1 = lane < 32 ? z.m : 0u;
         const bf16x8_t zp = __builtin_bit_cast(bf16x8_t, u32x4_t{z0 | (z0 >> 16), z0 >> 16, z1 | (z1 >> 16), z1 >> 16});
 #pragma unroll

@@ -286,3 +286,33 @@ def test_moe_of_the_most_columns(pq, hidden, inter, E, k, tokens, out):
     ref, bound, rids, _ = H.moe_ref(H.f64(X), H.f64(R), experts, hidden, inter, 4, k, "silu", True, out=out)
     assert np.array_equal(ids.cpu().numpy(), rids)
     H.check(Y, ref, bound, f"experts of {hidden} x {inter}, {tokens} tokens", out)
+
+
+@pytest.mark.parametrize("tokens,m,n", [(1, 130, 600), (40, 130, 600), (40, 130, 5003)])
+@pytest.mark.parametrize("power", [-100, 80])
+def test_linear_scales_exactly_with_its_activations(pq, tokens, m, n, power):
+    """Activations times a power of two give results times it, bit for bit: at
+    2^-100 the smallest step of a group's sum, held times 2^-12, is 2^-112."""
+    rng = np.random.default_rng(tokens)
+    w = H.weight(m, n, 4, 64, rng, H.group_index(n, 64, rng, True))
+    packed = pq.gptq_w4a16_pack(*H.gpu(w), n, 4, 64)
+    X = torch.from_numpy(rng.integers(-200, 201, size=(tokens, n)).astype(np.float32)).to(torch.bfloat16).cuda()
+    Y = pq.gptq_w4a16_linear(X, packed, m, n, 64, out_dtype=torch.float32)
+    Z = pq.gptq_w4a16_linear(X * 2.0 ** power, packed, m, n, 64, out_dtype=torch.float32)
+    assert torch.equal(Z, Y * 2.0 ** power)
+
+
+@pytest.mark.parametrize("tokens,m,n", [(1, 130, 600), (40, 130, 600), (40, 130, 5003)])
+def test_linear_of_the_smallest_activations(pq, tokens, m, n):
+    """Integers up to 200 times 2^-124: products held times 2^-12 end at fp32's
+    smallest step, 2^-149, that is 2^-13 of the activations' own step, each off by
+    half of one: n of them are sqrt(n)·2^-14 steps, where the results are about
+    sqrt(n)·115·6 steps: 9e-8 of them, and held to ten times that.  Sums of x in
+    bf16 parts, which end at 2^-133, must still hold the step itself."""
+    rng = np.random.default_rng(tokens)
+    w = H.weight(m, n, 4, 64, rng, H.group_index(n, 64, rng, True))
+    packed = pq.gptq_w4a16_pack(*H.gpu(w), n, 4, 64)
+    X = torch.from_numpy(rng.integers(-200, 201, size=(tokens, n)).astype(np.float32)).to(torch.bfloat16).cuda()
+    Y = pq.gptq_w4a16_linear(X, packed, m, n, 64, out_dtype=torch.float32).double()
+    Z = pq.gptq_w4a16_linear(X * 2.0 ** -124, packed, m, n, 64, out_dtype=torch.float32).double()
+    assert float((Z * 2.0 ** 124 - Y).norm() / Y.norm()) <= 9e-7
