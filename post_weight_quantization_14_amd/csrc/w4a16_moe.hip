@@ -57,12 +57,15 @@ __device__ __forceinline__ bool moe_before(double a, int ia, double b, int ib) {
   return ia < ib;
 }
 
-// Eight elements of x from k; zeros past its end, like the router's: an Inf of
-// x times a zero of the router would be NaN.
-__device__ __forceinline__ u32x4_t moe_x(const uint16_t* x, int k, int h) {
-  u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + (k < h ? k : 0));
-  if (k >= h) v = u32x4_t{0u, 0u, 0u, 0u};
-  return v;
+// A token's row in LDS ends with eight zeros, which lanes past its end read: an
+// Inf of x, from anywhere else in the row, times their zero of the router would
+// be NaN.  (Selecting zeros after the read: router 9.2 -> 11.3 us.)
+constexpr int kMoeTail = 8;
+__device__ __forceinline__ void moe_tail(uint16_t* x, int h, int i) {   // i = 0 .. 7
+  x[((h + 7) & ~7) + i] = 0;
+}
+__device__ __forceinline__ u32x4_t moe_x(const uint16_t* x, int k, int h) {   // h % 8 == 0
+  return *reinterpret_cast<const u32x4_t*>(x + (k < h ? k : h));
 }
 
 // One logit in 64 bits by one wave: `part` of `parts` interleaved 512-element
@@ -161,6 +164,7 @@ __global__ __launch_bounds__(1024) void moe_logits_kernel(MoeRouterArgs a) {
   const int h = (int)a.hidden, tid = threadIdx.x;
   const int e = blockIdx.x * 16 + (tid >> 6);
   l4_row_to_lds(a.X + t * a.ldx, h, a.xvec, lds, tid, 1024);
+  if (tid < kMoeTail) moe_tail(reinterpret_cast<uint16_t*>(lds), h, tid);
   __syncthreads();
   if (e >= a.experts) return;
   const double s = moe_logit(reinterpret_cast<const uint16_t*>(lds), a.R, a.r_dt, a.vec, e, h, 0, 1);
@@ -202,6 +206,7 @@ __global__ __launch_bounds__(1024) void moe_router_kernel(MoeRouterArgs a) {
   u32x4_t w[4], nx[4];
   if (fast && !a.logits) fetch(e0, i0, w);   // in flight while the token is copied
   l4_row_to_lds(a.X + t * a.ldx, h, a.xvec, reinterpret_cast<uint8_t*>(x), tid, 1024);
+  if (tid < kMoeTail) moe_tail(x, h, tid);
   for (int e = tid; e < E; e += 1024) rank[e] = 0;
   __syncthreads();
   if (a.logits)
@@ -471,7 +476,7 @@ __global__ __launch_bounds__(kL4Threads) void moe_small_gate_up_kernel(MoeSmallA
   __shared__ int rank[kSmallLogits];
   __shared__ int32_t ids[kSmallPairs];
   const MoeExpertArgs& g = a.x;
-  const int T = g.tokens, E = g.experts, K = g.top_k, h = a.hidden, hrow = (h + 7) & ~7;
+  const int T = g.tokens, E = g.experts, K = g.top_k, h = a.hidden, hrow = ((h + 7) & ~7) + kMoeTail;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int xrow = (int)g.k128 + kL4Pad;
@@ -480,6 +485,7 @@ __global__ __launch_bounds__(kL4Threads) void moe_small_gate_up_kernel(MoeSmallA
   float* red = reinterpret_cast<float*>(raw);                          // after the gather
   for (int t = 0; t < T; ++t)
     l4_row_to_lds(a.X + t * a.ldx, h, a.xvec, reinterpret_cast<uint8_t*>(raw + t * hrow), tid, kL4Threads);
+  if (tid < T * kMoeTail) moe_tail(raw + (tid / kMoeTail) * hrow, h, tid % kMoeTail);
   const int pairs = T * E;
   for (int i = tid; i < pairs; i += kL4Threads) rank[i] = 0;
   __syncthreads();
@@ -992,7 +998,7 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
       sa.ids_out = r.ids_out;
       sa.wts_out = r.wts_out;
       const size_t rows = (size_t)g.pass * (size_t)(g.k128 + kL4Pad) * 2;
-      const size_t raw = (size_t)tk * (size_t)round_up(h, 8) * 2, red = (size_t)kL4Waves * 2 * g.quads * 64 * sizeof(float);
+      const size_t raw = (size_t)tk * (size_t)(round_up(h, 8) + kMoeTail) * 2, red = (size_t)kL4Waves * 2 * g.quads * 64 * sizeof(float);
       size_t lds = rows + std::max(raw, red);
       switch (steps(L.gu)) {
         case 1: GPTQ_TRY(moe_launch(moe_small_gate_up_kernel<1>, f.gu_grid, lds, sa, stream)); break;
@@ -1025,7 +1031,7 @@ gptq_status run_moe(const MoeCall& c, const gptq_moe_config& cfg, void* ws, cons
 #undef MOE_SMALL_DOWN
       continue;
     }
-    const size_t xlds = (size_t)round_up(h, 8) * 2;   // a token's row
+    const size_t xlds = (size_t)(round_up(h, 8) + kMoeTail) * 2;   // a token's row
     if (r.logits)
       GPTQ_TRY(moe_launch(moe_logits_kernel, dim3((unsigned)ceil_div(cfg.experts, 16), (unsigned)tk), xlds, r, stream));
     GPTQ_TRY(moe_launch(moe_router_kernel, dim3((unsigned)tk),
