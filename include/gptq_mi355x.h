@@ -443,6 +443,103 @@ gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const voi
                            float* topk_weights, void* workspace, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * A key/value cache held in 4 bits, and attention
+ *
+ * What a decoder layer needs beside its products.  Tensors of tokens are
+ * [tokens][heads][head_dim] with unit stride in head_dim and any strides (in
+ * elements) between tokens and between heads, so slices of one projection's
+ * output and [heads][tokens][head_dim] tensors serve as they are.  Query heads
+ * h·(heads / kv_heads) .. read key head h.  Shared rules: stream-ordered, no
+ * synchronisation, nothing allocated; calls may be captured into a graph;
+ * results do not depend on anything but the arguments (the same call gives the
+ * same bits); no output may overlap an input; tokens == 0 or batch == 0 is a
+ * no-op.  Limits (GPTQ_ERR_UNSUPPORTED): head_dim 64 or 128, heads <= 4096,
+ * tokens <= 2^27, batch <= 2^20.
+ *
+ * The cache is `num_pages` pages of gptq_kv_page_bytes(cfg) bytes (16-byte
+ * aligned; owned by the caller; what is in them is private to these calls).  A
+ * page holds page_size positions (a power of two, 16 to 65536) of all key
+ * heads.  A call takes `batch` sequences:
+ *   cu_seqlens [batch + 1] device int32, ascending: rows cu_seqlens[b] ..
+ *              cu_seqlens[b + 1] of the token tensors are sequence b's n tokens
+ *              of this call; NULL: one each (tokens == batch).  Rows before the
+ *              first and behind the last sequence are left as they are.
+ *   kv_lens    [batch] device int32: positions of each sequence in the cache,
+ *              those of this call included.  Its n tokens are the last n.
+ *   page_table [batch][table_stride] device int32, table_width entries a row:
+ *              position p is in page page_table[b][p / page_size].  Entries past
+ *              a sequence's last position are not used.
+ *   status     device int32 or NULL: set to GPTQ_ERR_INVALID_ARG, in stream
+ *              order, if a sequence's rows, length or a page of it is out of
+ *              range (left as it is otherwise: the caller clears it).  Such a
+ *              sequence's tokens (a page out of range: those of the page) are not
+ *              written; what would be read from it is NaN.
+ *
+ * gptq_kv_append quantizes K and V (bf16 or fp32) into the cache.  Each token's
+ * and head's channels go by groups of group_size (32, 64, 128, or -1 for all),
+ * on the grid with lo = min x, hi = max x, a = max|x| of the group:
+ *   s = the smallest bf16 with 15·s >= hi - lo, 4096·s >= a, s >= 2^-100;
+ *   z = -rint(lo/s); q = clamp(rint(x/s) + z, 0, 15); the value kept is (q - z)·s,
+ * decided exactly (rint to even), within s/2 of x.  A group that holds NaN, Inf or
+ * a magnitude above 2^64 reads back as NaN.  Sequences must not share a page
+ * that the call writes.  More tokens than kv_lens[b] is out of range.
+ *
+ * gptq_kv_read gives the last n positions of each sequence as bf16 (rounded to
+ * nearest even) or fp32 (exact): with cu_seqlens the running sum of kv_lens, the
+ * whole cache.
+ *
+ * gptq_kv_attention: for token i of sequence b's n, position t its last
+ * kv_lens[b] - n + i,
+ *   Y = Σ_{p <= t} softmax_p(scale·Q·K̂[p])·V̂[p]
+ * for bf16 Q and Y: a token a sequence in decoding, several where drafts are
+ * checked, hundreds for a chunk of a prompt.  The tokens are appended first.
+ * The codes enter the products exactly, weights as two bf16 parts; all sums are
+ * fp32.  A token that sees no position (kv_lens[b] < n) gives zeros.  max_queries:
+ * the most tokens that a sequence has in this call, as far as the caller knows;
+ * it only chooses between kernels (0: one).  `workspace` (256-byte aligned,
+ * contents not kept) of gptq_kv_attention_workspace_bytes(cfg, heads, batch,
+ * tokens, max_queries) bytes belongs to one call at a time.
+ *
+ * gptq_prompt_attention: causal attention within each of `batch` sequences of
+ * bf16 Q, K, V, before any cache:
+ *   Y_i = Σ_{j <= i} softmax_j(scale·Q_i·K_j)·V_j.
+ * Weights are rounded to bf16 for the second product; all sums are fp32.  What
+ * a token does not see (later tokens, other sequences) may be anything, NaN too.
+ * cu_seqlens beyond 0 .. tokens is cut to it.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t kv_heads;
+  int32_t head_dim;       /* 64 or 128                                     */
+  int32_t group_size;     /* channels of a scale: 32, 64, 128, -1 (all)    */
+  int32_t page_size;      /* positions of a page                           */
+} gptq_kv_config;
+
+size_t gptq_kv_page_bytes(const gptq_kv_config* cfg);
+gptq_status gptq_kv_append(const gptq_kv_config* cfg, const void* K, const void* V, int32_t dtype, int64_t tokens,
+                           int64_t ldk, int64_t k_head_stride, int64_t ldv, int64_t v_head_stride,
+                           const int32_t* cu_seqlens, const int32_t* kv_lens, const int32_t* page_table,
+                           int64_t batch, int64_t table_width, int64_t table_stride, void* pages,
+                           int64_t num_pages, int32_t* status, void* stream);
+gptq_status gptq_kv_read(const gptq_kv_config* cfg, void* K, void* V, int32_t dtype, int64_t tokens, int64_t ldk,
+                         int64_t k_head_stride, int64_t ldv, int64_t v_head_stride, const int32_t* cu_seqlens,
+                         const int32_t* kv_lens, const int32_t* page_table, int64_t batch, int64_t table_width,
+                         int64_t table_stride, const void* pages, int64_t num_pages, int32_t* status,
+                         void* stream);
+size_t gptq_kv_attention_workspace_bytes(const gptq_kv_config* cfg, int32_t heads, int64_t batch, int64_t tokens,
+                                         int64_t max_queries);
+gptq_status gptq_kv_attention(const gptq_kv_config* cfg, const void* Q, int64_t tokens, int32_t heads, int64_t ldq,
+                              int64_t q_head_stride, const int32_t* cu_seqlens, int64_t max_queries,
+                              const int32_t* kv_lens, const int32_t* page_table, int64_t batch,
+                              int64_t table_width, int64_t table_stride, const void* pages, int64_t num_pages,
+                              float scale, void* Y, int64_t ldy, int64_t y_head_stride, int32_t* status,
+                              void* workspace, size_t ws_bytes, void* stream);
+gptq_status gptq_prompt_attention(const void* Q, const void* K, const void* V, int64_t tokens, int32_t heads,
+                                  int32_t kv_heads, int32_t head_dim, int64_t ldq, int64_t q_head_stride,
+                                  int64_t ldk, int64_t k_head_stride, int64_t ldv, int64_t v_head_stride,
+                                  const int32_t* cu_seqlens, int64_t batch, float scale, void* Y, int64_t ldy,
+                                  int64_t y_head_stride, void* stream);
+
+/* ------------------------------------------------------------------------
  * Export of a quantized layer to the tensor layout of GPTQ checkpoints.
  * Page "模型量化实战：从 INT8 PTQ 到 GPTQ…" §3.3 saves the quantized model as
  * a GPTQ checkpoint (about 4.1 GB for 7B) but does not define its tensors;

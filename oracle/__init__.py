@@ -48,6 +48,12 @@ from .quantized_layers import (  # noqa: F401,E402
     moe,
     route,
 )
+from .attention import (  # noqa: F401,E402
+    attention,
+    kv_group,
+    kv_kept,
+    smallest_bf16,
+)
 from .awq import (  # noqa: F401,E402
     awq_quantize,
     channel_abs_sum,

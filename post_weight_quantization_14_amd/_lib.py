@@ -51,6 +51,11 @@ class GptqMoeConfig(ctypes.Structure):
                 ("activation", ctypes.c_int32), ("renormalize", ctypes.c_int32)]
 
 
+class GptqKvConfig(ctypes.Structure):
+    _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("group_size", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -94,6 +99,16 @@ SIGNATURES = {
     "gptq_w4a16_moe_workspace_bytes": (_SZ, [ctypes.POINTER(GptqMoeConfig), _I64]),
     "gptq_w4a16_moe": (_ST, [_P, _I64, _I64, _P, _I32, ctypes.POINTER(GptqMoeConfig), _P, _SZ, _P, _I32, _I64, _P,
                              _I32, _I64, _P, _P, _P, _SZ, _P]),
+    "gptq_kv_page_bytes": (_SZ, [ctypes.POINTER(GptqKvConfig)]),
+    "gptq_kv_append": (_ST, [ctypes.POINTER(GptqKvConfig), _P, _P, _I32, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _I64,
+                             _I64, _I64, _P, _I64, _P, _P]),
+    "gptq_kv_read": (_ST, [ctypes.POINTER(GptqKvConfig), _P, _P, _I32, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _I64,
+                           _I64, _I64, _P, _I64, _P, _P]),
+    "gptq_kv_attention_workspace_bytes": (_SZ, [ctypes.POINTER(GptqKvConfig), _I32, _I64, _I64, _I64]),
+    "gptq_kv_attention": (_ST, [ctypes.POINTER(GptqKvConfig), _P, _I64, _I32, _I64, _I64, _P, _I64, _P, _P, _I64, _I64,
+                                _I64, _P, _I64, ctypes.c_float, _P, _I64, _I64, _P, _P, _SZ, _P]),
+    "gptq_prompt_attention": (_ST, [_P, _P, _P, _I64, _I32, _I32, _I32, _I64, _I64, _I64, _I64, _I64, _I64, _P, _I64,
+                                    ctypes.c_float, _P, _I64, _I64, _P]),
     "gptq_checkpoint_qweight_rows": (_I64, [_I64, _I32]),
     "gptq_checkpoint_qzeros_words": (_I64, [_I64, _I32]),
     "gptq_export_checkpoint": (_ST, [_P, _P, _P, _I64, _I64, _I32, _I32, _I32, _P, _P, _P, _P]),

@@ -1,0 +1,513 @@
+// Attention of the last tokens of each sequence over its 4-bit cache.
+//
+// With k̂ = (c - z)·s per group of channels and the same for values,
+//   logit[t] = scale·Σ_g s_g(t)·(Σ_{d in g} q_d·(128 + c_d(t)) - (128 + z_g(t))·Σ_{d in g} q_d),
+//   y_d = Σ_t p'(t)·(128 + c_d(t)) - Σ_t p'(t)·(128 + z(t)),  p' = softmax(t)·s(t):
+// 128 + c is a bf16 made from four bits by one AND-OR, so keys enter the matrix
+// cores exactly; scales and zero points are taken off in fp32.
+#include "attention.hpp"
+
+namespace gptq {
+namespace {
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kStep = 32;        // positions of a wave's step: two records
+constexpr float kNone = -3e38f;  // a running maximum that has seen nothing
+
+__device__ __forceinline__ float swap16(float x, float* y) {   // lane ^ 16
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  *y = __uint_as_float(r[1]);
+  return __uint_as_float(r[0]);
+}
+__device__ __forceinline__ float swap32(float x, float* y) {   // lane ^ 32
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  *y = __uint_as_float(r[1]);
+  return __uint_as_float(r[0]);
+}
+// over the four lanes that hold one query
+__device__ __forceinline__ float quad_max(float x) {
+  float y;
+  x = swap16(x, &y);
+  x = fmaxf(x, y);
+  x = swap32(x, &y);
+  return fmaxf(x, y);
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  float y;
+  x = swap16(x, &y);
+  x += y;
+  x = swap32(x, &y);
+  return x + y;
+}
+
+// The constants of the AND-OR, hidden from folding (VOP3 takes no literals).
+struct Consts {
+  uint32_t m, c;
+  __device__ __forceinline__ Consts() : m(0x000f000fu), c(0x43004300u) { asm volatile("" : "+v"(m), "+v"(c)); }
+  __device__ __forceinline__ uint32_t pair(uint32_t w) const { return (w & m) | c; }   // (128 + nibble 0, 128 + nibble 4)
+};
+
+struct Work {
+  KvLayout L;
+  KvSeqs q;
+  HeadRows Q, Y;
+  float scale;           // times log2(e)
+  int share;             // query heads of a key head
+  const uint8_t* pages;
+  float* partial;        // [2·wgs] of [rows][D] sums, [rows] maxima, [rows] sums of weights
+  int4* meta;            // [wgs]: (sequence, head · row tiles + tile, first slot, last workgroup) of a unit split over
+                         // workgroups that begins in this one; sequence -1: none
+};
+
+// A unit is one row tile (R query rows: tokens x the heads that share a key
+// head) of one key head of one sequence; its steps are 32 positions each.
+template <int R>
+struct Units {
+  const Work& w;
+  int64_t capacity;
+  __device__ __forceinline__ explicit Units(const Work& w_) : w(w_), capacity(std::min<int64_t>(w_.q.width * w_.L.recs * kKvRec, INT32_MAX)) {}
+  __device__ __forceinline__ KvSeq seq(int64_t b) const { return kv_seq(w.q, b, capacity); }
+  static __device__ __forceinline__ int64_t tiles(const KvSeq& s, int share) { return ((int64_t)s.n * share + R - 1) / R; }
+  static __device__ __forceinline__ int64_t steps(const KvSeq& s) { return std::max<int64_t>(1, ((int64_t)s.len + kStep - 1) / kStep); }
+  __device__ __forceinline__ int64_t count(int64_t b) const {
+    const KvSeq s = seq(b);
+    return tiles(s, w.share) * steps(s) * w.L.heads;
+  }
+};
+
+template <int D, int G>
+struct Step {
+  static constexpr int KS = D / 32, NG = D / G;
+  uint32_t k[2][KS], v[2][KS];
+  u32x4_t kp[2][NG], vp[2][NG];
+  bool bad;   // a page that is none
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const u32x4_t x = *reinterpret_cast<const u32x4_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = x[i];
+  } else {
+    const u32x2_t x = *reinterpret_cast<const u32x2_t*>(p);
+    w[0] = x[0];
+    w[1] = x[1];
+  }
+}
+
+// values of tile 2·b + h (channels 32·b + 2i + h) at four positions, as two operand words
+template <int D>
+__device__ __forceinline__ void value_pairs(const uint32_t (&w)[D / 32], int b, int h, const Consts& kc, uint32_t* o) {
+  if constexpr (D == 128) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t x = __builtin_amdgcn_perm(w[2 * e + 1], w[2 * e], 0x0c000c00u | (uint32_t)(4 + b) << 16 | (uint32_t)b);
+      o[e] = kc.pair(h ? x >> 4 : x);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) o[e] = kc.pair(w[e] >> (8 * b + 4 * h));
+  }
+}
+
+template <int D, int G, int NT>
+__global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel(Work w, int64_t min_piece) {
+  constexpr int R = 16 * NT, KS = D / 32, NG = D / G, MT = D / 16, PG = G / 32;   // PG: 32-channel steps of a group
+  constexpr int kPitch = D + 4;
+  __shared__ float so[kWaves][16][kPitch];
+  __shared__ float sm[kWaves][16], sl[kWaves][16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n16 = lane & 15, kg = lane >> 4;
+  const Units<R> units(w);
+  const Consts kc;
+
+  const int64_t total = uniform(ragged_total(w.q.batch, [&](int64_t b) { return units.count(b); }));
+  const int64_t piece = std::max((total + gridDim.x - 1) / (int64_t)gridDim.x, min_piece);
+  const int64_t begin = piece * blockIdx.x, end = std::min(total, begin + piece);
+  if (tid == 0) w.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (w.q.status)
+    for (int64_t b = (int64_t)blockIdx.x * kThreads + tid; b < w.q.batch; b += (int64_t)gridDim.x * kThreads)
+      if (units.seq(b).bad) kv_bad(w.q.status);
+
+  for (int64_t pos = begin; pos < end;) {
+    int64_t b = 0, at = 0;
+    if (!ragged_find(pos, w.q.batch, [&](int64_t i) { return units.count(i); }, &b, &at)) break;
+    const KvSeq s = uniform(units.seq(b));
+    const int64_t steps = Units<R>::steps(s);
+    const int64_t unit = at / steps;                       // head · tiles + tile
+    const int s0 = (int)(at - unit * steps);
+    const int s1 = (int)std::min<int64_t>(steps, s0 + (end - pos));
+    const int64_t tiles = Units<R>::tiles(s, w.share);
+    const int head = (int)(unit / tiles);
+    const int64_t row0 = (unit - head * tiles) * R;
+    const int64_t rows = std::min<int64_t>(R, (int64_t)s.n * w.share - row0);
+
+    // ---- queries: lane n16 of every quarter holds query row 16·nt + n16
+    bf16x8_t qf[NT][KS];
+    float qs[NT][NG];
+    int lim[NT];     // positions that the row sees
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int64_t r = row0 + nt * 16 + n16;
+      const bool there = r - row0 < rows;
+      const int tq = there ? (int)(r / w.share) : 0;
+      const int hq = head * w.share + (there ? (int)(r - (int64_t)tq * w.share) : 0);
+      lim[nt] = there ? s.len - s.n + tq + 1 : 0;
+      const uint16_t* qp = static_cast<const uint16_t*>(w.Q.p) + (s.row + tq) * w.Q.ld + hq * w.Q.hs + kg * 8;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        u32x4_t x = {0, 0, 0, 0};
+        if (there) {
+          if (w.Q.vec) {
+            x = *reinterpret_cast<const u32x4_t*>(qp + ks * 32);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = qp[ks * 32 + 2 * i] | (uint32_t)qp[ks * 32 + 2 * i + 1] << 16;
+          }
+        }
+        qf[nt][ks] = __builtin_bit_cast(bf16x8_t, x);
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t += __uint_as_float(x[i] << 16) + __uint_as_float(x[i] & 0xffff0000u);
+        t = quad_sum(t);
+        if (ks % PG == 0)
+          qs[nt][ks / PG] = t;
+        else
+          qs[nt][ks / PG] += t;
+      }
+    }
+    int least = INT32_MAX;   // positions that every row there sees
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) least = std::min(least, nt * 16 + n16 < rows ? lim[nt] : INT32_MAX);
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) least = std::min(least, __shfl_xor(least, d));
+    least = __builtin_amdgcn_readfirstlane(least);
+
+    f32x4_t o[NT][MT];
+    float m[NT], l[NT], zs[NT][NG];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt] = kNone;
+      l[nt] = 0.f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) zs[nt][g] = 0.f;
+#pragma unroll
+      for (int j = 0; j < MT; ++j) o[nt][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // ---- the wave's steps s0 + wave, + 4, ..
+    const int last = (s.len - 1) / kKvRec;   // record; pages past it may be none
+    const int32_t* table = w.q.table + b * w.q.stride;
+    int tbase = -1;
+    int32_t tab = 0;
+    auto load = [&](int st, Step<D, G>& x) {
+      x.bad = s.bad;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int rec = std::min(2 * st + u, last);
+        const int pi = s.bad ? 0 : rec >> w.L.rec_shift;
+        if (tbase < 0 || pi >= tbase + 64) {
+          tbase = pi;
+          tab = s.bad ? 0 : table[std::min(pi + lane, last >> w.L.rec_shift)];
+        }
+        int64_t id = __builtin_amdgcn_readlane(tab, pi - tbase);
+        if (id < 0 || id >= w.q.pages) {
+          id = 0;
+          x.bad = true;
+        }
+        const uint8_t* p = w.pages + ((id * w.L.heads + head) * w.L.recs + (s.bad ? 0 : rec & (w.L.recs - 1))) * (int64_t)kv_rec_bytes(D, G);
+        load_words(p + lane * (D / 8), x.k[u]);
+        load_words(p + kv_code_bytes(D) + lane * (D / 8), x.v[u]);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          x.kp[u][g] = *reinterpret_cast<const u32x4_t*>(p + 2 * kv_code_bytes(D) + g * 64 + kg * 16);
+          x.vp[u][g] = *reinterpret_cast<const u32x4_t*>(p + 2 * kv_code_bytes(D) + kv_param_bytes(D, G) + g * 64 + kg * 16);
+        }
+      }
+    };
+    auto compute = [&](int st, Step<D, G>& x) {
+      if (x.bad) {
+        if (lane == 0) kv_bad(w.q.status);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x.kp[u][g][r] = 0x7fc00000u;
+      }
+      // logits of positions 32·st + 16·u + 4·kg + r
+      float sx[NT][2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        bf16x8_t a[KS];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          u32x4_t t;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] = kc.pair(x.k[u][ks] >> (4 * i));
+          a[ks] = __builtin_bit_cast(bf16x8_t, t);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          float ps[4], pz[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t pw = x.kp[u][g][r];
+            ps[r] = __uint_as_float(pw & 0xffff0000u) * w.scale;
+            pz[r] = (float)((int)(int16_t)(uint16_t)pw + 128);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = g * PG; ks < (g + 1) * PG; ++ks)
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[ks], qf[nt][ks], acc, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float y = fmaf(-pz[r], qs[nt][g], acc[r]);
+              sx[nt][u][r] = g == 0 ? y * ps[r] : fmaf(y, ps[r], sx[nt][u][r]);
+            }
+          }
+        }
+      }
+      const bool edge = (st + 1) * kStep > least;
+      if (edge) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (st * kStep + u * 16 + kg * 4 + r >= lim[nt]) sx[nt][u][r] = -INFINITY;
+      }
+      // running maximum; sums are scaled again only when it grows by more than 2^8
+      bool grown = false;
+      float top[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float t = sx[nt][0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) t = fmaxf(t, sx[nt][i >> 2][i & 3]);
+        top[nt] = quad_max(t);
+        grown |= top[nt] > m[nt] + 8.f;
+      }
+      if (__ballot(grown)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float up = fmaxf(m[nt], top[nt]), f = exp2f(m[nt] - up);
+          m[nt] = up;
+          l[nt] *= f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) zs[nt][g] *= f;
+#pragma unroll
+          for (int j = 0; j < MT; ++j) o[nt][j] *= f;
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float& p = sx[nt][i >> 2][i & 3];
+          p = __builtin_amdgcn_exp2f(p - m[nt]);
+          l[nt] += p;
+        }
+      // values
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        bf16x8_t ph[NT], pl[NT];
+        float ps[2][4], pz[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t pw = x.vp[u][g][r];
+            ps[u][r] = __uint_as_float(pw & 0xffff0000u);
+            pz[u][r] = (float)((int)(int16_t)(uint16_t)pw + 128);
+          }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int u = i >> 2, r = i & 3;
+            float p = sx[nt][u][r] * ps[u][r];
+            if (edge && st * kStep + u * 16 + kg * 4 + r >= lim[nt]) p = 0.f;   // the scale there may be anything
+            const __bf16 h = (__bf16)p, lo = (__bf16)(p - (float)h);
+            ph[nt][i] = h;
+            pl[nt][i] = lo;
+            zs[nt][g] = fmaf((float)h + (float)lo, pz[u][r], zs[nt][g]);
+          }
+        }
+#pragma unroll
+        for (int j = g * PG * 2; j < (g + 1) * PG * 2; ++j) {
+          u32x4_t t;
+          uint32_t a0[2], a1[2];
+          value_pairs<D>(x.v[0], j >> 1, j & 1, kc, a0);
+          value_pairs<D>(x.v[1], j >> 1, j & 1, kc, a1);
+          t[0] = a0[0], t[1] = a0[1], t[2] = a1[0], t[3] = a1[1];
+          const bf16x8_t a = __builtin_bit_cast(bf16x8_t, t);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            o[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ph[nt], o[nt][j], 0, 0, 0);
+            o[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pl[nt], o[nt][j], 0, 0, 0);
+          }
+        }
+      }
+    };
+    if (s.len > 0) {
+      Step<D, G> cur, nxt;
+      int st = s0 + wave;
+      if (st < s1) load(st, cur);
+      for (; st < s1; st += kWaves) {
+        if (st + kWaves < s1) load(st + kWaves, nxt);
+        compute(st, cur);
+        cur = nxt;
+      }
+    }
+
+    // ---- the four waves' sums together, a tile of 16 rows at a time
+    const bool whole = s0 == 0 && s1 == steps;
+    const int slot = pos == begin ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1;
+    float* part = w.partial + (int64_t)slot * R * (D + 2);
+    if (!whole && s0 == 0 && tid == 0)
+      w.meta[blockIdx.x] = make_int4((int)b, (int)unit, slot, (int)((pos + steps - 1) / piece));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      l[nt] = quad_sum(l[nt]);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) zs[nt][g] = quad_sum(zs[nt][g]);
+      if (kg == 0) sm[wave][n16] = m[nt];
+      __syncthreads();
+      float up = kNone;
+#pragma unroll
+      for (int v = 0; v < kWaves; ++v) up = fmaxf(up, sm[v][n16]);
+      const float f = exp2f(m[nt] - up);
+      if (kg == 0) sl[wave][n16] = l[nt] * f;
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          so[wave][n16][(j >> 1) * 32 + 2 * (kg * 4 + r) + (j & 1)] = (o[nt][j][r] - zs[nt][j / (2 * PG)]) * f;
+      __syncthreads();
+      for (int i = tid; i < 16 * (D / 4); i += kThreads) {
+        const int n = i / (D / 4), d = i % (D / 4) * 4;
+        const int64_t r = row0 + nt * 16 + n;
+        if (r - row0 >= rows) continue;
+        float ll = 0.f;
+        f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+          ll += sl[v][n];
+          y += *reinterpret_cast<const f32x4_t*>(&so[v][n][d]);
+        }
+        if (whole) {
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;   // a row that sees nothing
+          const int64_t tq = r / w.share;
+          uint16_t* yp = const_cast<uint16_t*>(static_cast<const uint16_t*>(w.Y.p)) + (s.row + tq) * w.Y.ld +
+                         (head * w.share + (r - tq * w.share)) * w.Y.hs + d;
+          uint16_t h[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) h[c] = __builtin_bit_cast(uint16_t, (__bf16)(y[c] * inv));
+          if (w.Y.vec) {
+            *reinterpret_cast<u32x2_t*>(yp) = u32x2_t{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) yp[c] = h[c];
+          }
+        } else {
+          *reinterpret_cast<f32x4_t*>(part + (nt * 16 + n) * D + d) = y;
+          if (d == 0) {
+            float top = kNone;
+#pragma unroll
+            for (int v = 0; v < kWaves; ++v) top = fmaxf(top, sm[v][n]);
+            part[R * D + nt * 16 + n] = top;
+            part[R * D + R + nt * 16 + n] = ll;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    pos += s1 - s0;
+  }
+}
+
+// Joins the parts of a unit that was split: one wave per row.
+template <int D, int R>
+__global__ __launch_bounds__(256) void kv_join_kernel(Work w) {
+  const int4 u = w.meta[blockIdx.x];
+  if (u.x < 0) return;
+  const int lane = threadIdx.x & 63;
+  const Units<R> units(w);
+  const KvSeq s = uniform(units.seq(u.x));
+  const int64_t tiles = Units<R>::tiles(s, w.share);
+  const int head = (int)(u.y / tiles);
+  const int64_t row0 = (u.y - head * tiles) * R;
+  const int rows = (int)std::min<int64_t>(R, (int64_t)s.n * w.share - row0);
+  const int parts = u.w - (int)blockIdx.x + 1;
+  auto part = [&](int i) { return w.partial + (int64_t)(i == 0 ? u.z : 2 * ((int)blockIdx.x + i)) * R * (D + 2); };
+  for (int row = (int)blockIdx.y * 4 + uniform((int)threadIdx.x >> 6); row < rows; row += 4 * (int)gridDim.y) {
+    float up = kNone;
+    for (int i = lane; i < parts; i += 64) up = fmaxf(up, part(i)[R * D + row]);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) up = fmaxf(up, __shfl_xor(up, d));
+    constexpr int C = D / 64;
+    float ll = 0.f, y[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) y[c] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const float* p = part(i);
+      const float f = exp2f(p[R * D + row] - up);
+      ll = fmaf(p[R * D + R + row], f, ll);
+#pragma unroll
+      for (int c = 0; c < C; ++c) y[c] = fmaf(p[row * D + lane * C + c], f, y[c]);
+    }
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const int64_t r = row0 + row, tq = r / w.share;
+    uint16_t* yp = const_cast<uint16_t*>(static_cast<const uint16_t*>(w.Y.p)) + (s.row + tq) * w.Y.ld +
+                   (head * w.share + (r - tq * w.share)) * w.Y.hs + lane * C;
+#pragma unroll
+    for (int c = 0; c < C; ++c) yp[c] = __builtin_bit_cast(uint16_t, (__bf16)(y[c] * inv));
+  }
+}
+
+template <int D, int G, int NT>
+gptq_status launch(const Work& w, const KvAttentionPlan& p, hipStream_t stream) {
+  kv_attention_kernel<D, G, NT><<<p.wgs, kThreads, 0, stream>>>(w, 4);
+  GPTQ_LAUNCH_CHECK();
+  kv_join_kernel<D, 16 * NT><<<dim3(p.wgs, (p.rows + 3) / 4), 256, 0, stream>>>(w);
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+}  // namespace
+
+KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, int64_t tokens, int64_t max_queries) {
+  KvAttentionPlan p;
+  const int64_t rows = std::min(std::max<int64_t>(max_queries, 1), std::max<int64_t>(tokens, 1)) * (heads / L.heads);
+  p.tiles = rows > 16 ? 4 : 1;
+  p.wgs = 512;
+  p.rows = (int)std::min<int64_t>(rows, 16 * p.tiles);
+  p.partial = (size_t)2 * p.wgs * 16 * p.tiles * (L.dim + 2) * 4;
+  p.meta = (size_t)p.wgs * sizeof(int4);
+  p.total = align256(p.partial) + p.meta;
+  (void)batch;
+  return p;
+}
+
+gptq_status run_kv_attention(const KvLayout& L, int heads, const HeadRows& Q, const HeadRows& Y, float scale,
+                             const KvSeqs& q, const void* pages, void* ws, const KvAttentionPlan& p, hipStream_t stream) {
+  const Work w{L, q, Q, Y, scale * 1.44269504088896340736f, heads / L.heads, static_cast<const uint8_t*>(pages),
+               static_cast<float*>(ws), reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + align256(p.partial))};
+  auto tiled = [&](auto d, auto g) {
+    return p.tiles == 1 ? launch<d.value, g.value, 1>(w, p, stream) : launch<d.value, g.value, 4>(w, p, stream);
+  };
+  using std::integral_constant;
+  if (L.dim == 128 && L.group == 128) return tiled(integral_constant<int, 128>{}, integral_constant<int, 128>{});
+  if (L.dim == 128 && L.group == 64) return tiled(integral_constant<int, 128>{}, integral_constant<int, 64>{});
+  if (L.dim == 128) return tiled(integral_constant<int, 128>{}, integral_constant<int, 32>{});
+  if (L.group == 64) return tiled(integral_constant<int, 64>{}, integral_constant<int, 64>{});
+  return tiled(integral_constant<int, 64>{}, integral_constant<int, 32>{});
+}
+
+}  // namespace gptq

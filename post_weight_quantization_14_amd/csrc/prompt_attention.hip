@@ -1,0 +1,267 @@
+// Causal attention over whole prompts of different lengths, packed one after the
+// other: Y_i = Σ_{j <= i} softmax_j(scale·Q_i·K_j)·V_j within each sequence,
+// `heads / kv_heads` query heads to a key head.
+#include "attention.hpp"
+
+namespace gptq {
+namespace {
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kBM = 32 * kWaves;   // queries of a workgroup, 32 a wave
+constexpr int kBN = 64;            // keys of a tile
+constexpr float kNone = -3e38f;
+
+typedef __attribute__((__vector_size__(4 * sizeof(short)))) short v4i16_t;
+typedef __attribute__((address_space(3))) v4i16_t lds_v4i16_t;
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+__device__ __forceinline__ float half_max(float x) {   // with lane ^ 32
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Tiles in LDS are rows of D bf16 in pieces of 16 bytes; piece c of row t lies at
+// c ^ swz(t), so that 16 rows' reads of one piece (keys) and 8 rows' reads of
+// four pieces (values, transposed) each meet every bank equally often.
+template <int D>
+__device__ __forceinline__ int swz(int t) {
+  return D == 128 ? ((t & 3) << 2 | (t >> 2 & 3)) : ((t >> 1 & 1) << 2 | (t >> 2 & 3));
+}
+template <int D>
+__device__ __forceinline__ int lds_at(int t, int c) {   // in bytes
+  return t * (D * 2) + (c ^ swz<D>(t)) * 16;
+}
+
+struct Prompt {
+  HeadRows Q, K, V, Y;
+  const int32_t* cu;
+  int64_t batch, tokens, tiles;
+  int heads, share;
+  float scale;      // times log2(e), positive: a masked logit times it stays -Inf
+  uint32_t keep, flip;   // Q's bits and signs: a scale of 0 clears it, a negative one flips it
+};
+
+template <int D, bool VEC>
+__global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a) {
+  constexpr int KS = D / 16, DT = D / 32, CH = D / 8, TB = kBN * D * 2;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TB];   // [buffer][K, V]
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int n32 = lane & 31, half = lane >> 5;
+
+  const int64_t head = blockIdx.x % a.heads;
+  int64_t b = 0, at = 0;
+  auto seq = [&](int64_t i, int64_t* row) {
+    const int64_t r0 = std::min(std::max<int64_t>(a.cu[i], 0), a.tokens);
+    const int64_t r1 = std::min(std::max<int64_t>(a.cu[i + 1], r0), a.tokens);
+    *row = r0;
+    return r1 - r0;
+  };
+  if (!ragged_find(a.tiles - 1 - blockIdx.x / a.heads, a.batch, [&](int64_t i) {
+        int64_t r;
+        return (seq(i, &r) + kBM - 1) / kBM;
+      }, &b, &at))
+    return;
+  int64_t row0;
+  const int len = uniform((int)seq(b, &row0));
+  row0 = uniform(row0);
+  const int q0 = (int)at * kBM, w0 = q0 + wave * 32;   // the workgroup's and the wave's first query
+  const int iq = w0 + n32;                             // the lane's query
+  const int keys = std::min(len, q0 + kBM);            // that any of its queries sees
+  const int tiles = (keys + kBN - 1) / kBN;
+
+  const uint16_t* Kp = static_cast<const uint16_t*>(a.K.p) + row0 * a.K.ld + head / a.share * a.K.hs;
+  const uint16_t* Vp = static_cast<const uint16_t*>(a.V.p) + row0 * a.V.ld + head / a.share * a.V.hs;
+
+  bf16x8_t qf[KS];
+  {
+    const uint16_t* qp = static_cast<const uint16_t*>(a.Q.p) + (row0 + std::min(iq, len - 1)) * a.Q.ld + head * a.Q.hs + half * 8;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      u32x4_t x;
+      if (VEC) {
+        x = *reinterpret_cast<const u32x4_t*>(qp + ks * 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = qp[ks * 16 + 2 * i] | (uint32_t)qp[ks * 16 + 2 * i + 1] << 16;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = (x[i] & a.keep) ^ a.flip;
+      qf[ks] = __builtin_bit_cast(bf16x8_t, x);
+    }
+  }
+
+  // rows of a tile into LDS; rows past the last key repeat it (masked)
+  auto fetch = [&](int tile, int buf) {
+    constexpr int kPieces = kBN * CH / kThreads;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const uint16_t* X = v ? Vp : Kp;
+      const int64_t ld = v ? a.V.ld : a.K.ld;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int at = (i * kWaves + wave) * 64;   // of 64 pieces
+        const int t = (at + lane) / CH, c = ((at + lane) % CH) ^ swz<D>(t);
+        const uint16_t* src = X + (int64_t)std::min(tile * kBN + t, keys - 1) * ld + c * 8;
+        if (VEC) {
+          __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                           (lds_void_t*)(&lds[buf][v][at * 16]), 16, 0, 0);
+        } else {
+          u32x4_t x;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = src[2 * j] | (uint32_t)src[2 * j + 1] << 16;
+          *reinterpret_cast<u32x4_t*>(&lds[buf][v][(at + lane) * 16]) = x;
+        }
+      }
+    }
+  };
+
+  f32x16_t o[DT];
+  float m, l;
+  // A masked value meets a weight of 0, and 0·Inf is NaN.  Such values can only
+  // be in the last tiles; a result that is not finite is computed once more,
+  // carefully: what is not finite is left out of the product there, and counted
+  // for the queries that see it.
+  for (int careful = 0; careful < 2; ++careful) {
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
+    m = kNone;
+    l = 0.f;
+    fetch(0, 0);
+    for (int tile = 0; tile < tiles; ++tile) {
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      if (tile + 1 < tiles) fetch(tile + 1, (tile + 1) & 1);
+      const int k0 = tile * kBN;
+      if (k0 > w0 + 31) continue;   // the wave's queries see none of it (no barrier is skipped)
+      const uint8_t* kt = lds[tile & 1][0];
+      const uint8_t* vt = lds[tile & 1][1];
+      f32x16_t s[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(kt + lds_at<D>(u * 32 + n32, ks * 2 + half));
+          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[ks], s[u], 0, 0, 0);
+        }
+      }
+      const bool edge = k0 + kBN > w0 + 1;   // some query does not see some key
+      if (edge) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (k0 + u * 32 + 8 * (r >> 2) + 4 * half + (r & 3) > iq) s[u][r] = -INFINITY;
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int r = 1; r < 32; ++r) top = fmaxf(top, s[r >> 4][r & 15]);
+      top = half_max(top) * a.scale;
+      if (__ballot(top > m + 8.f)) {   // sums are scaled again only when the maximum grows by more than 2^8
+        const float up = fmaxf(m, top), f = exp2f(m - up);
+        m = up;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] *= f;
+      }
+      bf16x8_t p[4];
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        const float e = __builtin_amdgcn_exp2f(fmaf(s[r >> 4][r & 15], a.scale, -m));
+        l += e;
+        p[r >> 3][r & 7] = (__bf16)e;
+      }
+      const int g = lane >> 4, sl = lane & 15;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        f32x16_t more, less;   // counts, careful only
+        if (careful && edge) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) more[r] = less[r] = 0.f;
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const int t = kk * 16 + (g >> 1) * 4 + (sl >> 2), c = d * 32 + (g & 1) * 16 + (sl & 3) * 4;
+          const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t*)(vt + lds_at<D>(t, c >> 3) + (c & 7) * 2));
+          const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t*)(vt + lds_at<D>(t + 8, c >> 3) + (c & 7) * 2));
+          const auto both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          bf16x8_t v = __builtin_bit_cast(bf16x8_t, both);
+          if (careful && edge) {
+            bf16x8_t up, down, seen;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float x = (float)v[e];
+              const bool odd = !(fabsf(x) < INFINITY);
+              up[e] = (__bf16)(odd && !(x < 0.f) ? 1.f : 0.f);
+              down[e] = (__bf16)(odd && !(x > 0.f) ? 1.f : 0.f);
+              v[e] = odd ? (__bf16)0.f : v[e];
+              const int key = k0 + kk * 16 + (e >> 2) * 8 + half * 4 + (e & 3);
+              seen[e] = (__bf16)(key <= iq ? 1.f : 0.f);
+            }
+            more = __builtin_amdgcn_mfma_f32_32x32x16_bf16(up, seen, more, 0, 0, 0);
+            less = __builtin_amdgcn_mfma_f32_32x32x16_bf16(down, seen, less, 0, 0, 0);
+          }
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[kk], o[d], 0, 0, 0);
+        }
+        if (careful && edge) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[d][r] += (more[r] > 0.f ? INFINITY : 0.f) + (less[r] > 0.f ? -INFINITY : 0.f);
+        }
+      }
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sum += o[d][r] * 0.f;   // NaN if any is not finite
+    if (!__syncthreads_or(iq < len && sum != sum)) break;
+  }
+
+  l = half_sum(l);
+  if (iq < len) {
+    const float inv = 1.f / l;
+    uint16_t* yp = const_cast<uint16_t*>(static_cast<const uint16_t*>(a.Y.p)) + (row0 + iq) * a.Y.ld + head * a.Y.hs + 4 * half;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        uint16_t h[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) h[c] = __builtin_bit_cast(uint16_t, (__bf16)(o[d][r * 4 + c] * inv));
+        if (VEC) {
+          *reinterpret_cast<u32x2_t*>(yp + d * 32 + r * 8) = u32x2_t{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) yp[d * 32 + r * 8 + c] = h[c];
+        }
+      }
+  }
+}
+
+}  // namespace
+
+gptq_status run_prompt_attention(const PromptCall& c, hipStream_t stream) {
+  const int64_t tiles = (c.tokens + (kBM - 1) * std::min(c.batch, c.tokens)) / kBM;   // n tokens take at most (n + kBM - 1) / kBM
+  Prompt a{c.Q, c.K, c.V, c.Y, c.cu, c.batch, c.tokens, tiles, c.heads, c.heads / c.kv_heads,
+           c.scale == 0.f ? 1.f : fabsf(c.scale) * 1.44269504088896340736f, c.scale == 0.f ? 0u : ~0u,
+           c.scale < 0.f ? 0x80008000u : 0u};
+  const unsigned grid = (unsigned)(tiles * c.heads);
+  const bool vec = c.Q.vec && c.K.vec && c.V.vec && c.Y.vec;
+  if (c.dim == 128)
+    vec ? prompt_attention_kernel<128, true><<<grid, kThreads, 0, stream>>>(a)
+        : prompt_attention_kernel<128, false><<<grid, kThreads, 0, stream>>>(a);
+  else
+    vec ? prompt_attention_kernel<64, true><<<grid, kThreads, 0, stream>>>(a)
+        : prompt_attention_kernel<64, false><<<grid, kThreads, 0, stream>>>(a);
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+}  // namespace gptq

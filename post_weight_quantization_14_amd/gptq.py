@@ -762,6 +762,169 @@ def gptq_w4a16_moe(X: torch.Tensor, router: torch.Tensor, packed: torch.Tensor, 
     return Y, topk_ids, topk_weights
 
 
+# ---------------------------------------------------------------- attention and its 4-bit cache
+@dataclass(frozen=True)
+class KvConfig:
+    """A key/value cache held in 4 bits: heads and channels of its keys, the
+    channels that share a scale (-1: all of a head), positions of a page."""
+    kv_heads: int
+    head_dim: int = 128
+    group_size: int = 128
+    page_size: int = 64
+
+    def __post_init__(self):
+        c = _lib.GptqKvConfig(self.kv_heads, self.head_dim, self.group_size, self.page_size)
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ref", ctypes.byref(c))
+
+    def c(self) -> "_lib.GptqKvConfig":
+        return self._c
+
+
+def _heads(name: str, t: torch.Tensor, tokens: int, heads: int, dim: int) -> tuple:
+    """(token stride, head stride) of a [tokens, heads, dim] tensor."""
+    if t.dim() != 3 or tuple(t.shape) != (tokens, heads, dim) or (t.stride(2) != 1 and tokens > 0):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}] with unit stride in its last dimension")
+    return t.stride(0), t.stride(1)
+
+
+def _sequences(X: torch.Tensor, pages: torch.Tensor, page_bytes: int, page_table: torch.Tensor, kv_lens: torch.Tensor,
+               cu_seqlens: Optional[torch.Tensor], status: Optional[torch.Tensor], **more) -> tuple:
+    """The sequences of a call as the C entry points take them: cu_seqlens,
+    kv_lens, page_table, batch, its width and row stride, pages, their number."""
+    _on(X, pages=pages, page_table=page_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens, status=status, **more)
+    if page_bytes <= 0:
+        raise ValueError("the cache's config is not supported (gptq_kv_page_bytes is 0)")
+    batch = kv_lens.shape[0]
+    if kv_lens.dtype != torch.int32 or kv_lens.dim() != 1 or not kv_lens.is_contiguous():
+        raise ValueError("kv_lens must be a contiguous int32 [batch]")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != batch or (
+            page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be int32 [{batch}, pages of a sequence] with contiguous rows")
+    if cu_seqlens is not None and (cu_seqlens.dtype != torch.int32 or tuple(cu_seqlens.shape) != (batch + 1,)
+                                   or not cu_seqlens.is_contiguous()):
+        raise ValueError(f"cu_seqlens must be a contiguous int32 [{batch + 1}]")
+    if status is not None and (status.dtype != torch.int32 or status.numel() != 1):
+        raise ValueError("status must be one int32")
+    return (_ptr(cu_seqlens), kv_lens.data_ptr(), page_table.data_ptr(), batch, page_table.shape[1],
+            page_table.stride(0) if batch > 1 else page_table.shape[1], pages.data_ptr(),
+            _uint8("pages", pages) // page_bytes)
+
+
+def gptq_kv_page_bytes(cfg: KvConfig) -> int:
+    return int(lib().gptq_kv_page_bytes(cfg._ref))
+
+
+def gptq_kv_append(cfg: KvConfig, K: torch.Tensor, V: torch.Tensor, pages: torch.Tensor, page_table: torch.Tensor,
+                   kv_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantize K and V [tokens, kv_heads, head_dim] (bf16 or fp32) into the
+    pages (uint8, gptq_kv_page_bytes(cfg) bytes each).  kv_lens [batch]: each
+    sequence's positions with these tokens, which are its last.  cu_seqlens
+    [batch + 1]: its rows of K and V (None: one each)."""
+    tokens = K.shape[0]
+    kld, khs = _heads("K", K, tokens, cfg.kv_heads, cfg.head_dim)
+    vld, vhs = _heads("V", V, tokens, cfg.kv_heads, cfg.head_dim)
+    if K.dtype != V.dtype:
+        raise TypeError("K and V must have one dtype")
+    seqs = _sequences(K, pages, gptq_kv_page_bytes(cfg), page_table, kv_lens, cu_seqlens, status, V=V)
+    with _device(K):
+        st = lib().gptq_kv_append(cfg._ref, K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kld, khs, vld, vhs, *seqs,
+                                  _ptr(status), _stream_on(K, stream))
+    _check(st, "gptq_kv_append")
+
+
+def gptq_kv_read(cfg: KvConfig, pages: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, tokens: int,
+                 cu_seqlens: Optional[torch.Tensor] = None, K: Optional[torch.Tensor] = None,
+                 V: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                 status: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """(K, V) [tokens, kv_heads, head_dim], bf16 or fp32: the last
+    cu_seqlens[b + 1] - cu_seqlens[b] positions of each sequence (None: the last
+    one), as the cache keeps them."""
+    if K is None:
+        K = _empty((tokens, cfg.kv_heads, cfg.head_dim), out_dtype, pages, stream)
+    if V is None:
+        V = _empty((tokens, cfg.kv_heads, cfg.head_dim), K.dtype, pages, stream)
+    kld, khs = _heads("K", K, tokens, cfg.kv_heads, cfg.head_dim)
+    vld, vhs = _heads("V", V, tokens, cfg.kv_heads, cfg.head_dim)
+    if K.dtype != V.dtype:
+        raise TypeError("K and V must have one dtype")
+    seqs = _sequences(K, pages, gptq_kv_page_bytes(cfg), page_table, kv_lens, cu_seqlens, status, V=V)
+    with _device(K):
+        st = lib().gptq_kv_read(cfg._ref, K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kld, khs, vld, vhs, *seqs,
+                                _ptr(status), _stream_on(K, stream))
+    _check(st, "gptq_kv_read")
+    return K, V
+
+
+def gptq_kv_attention_workspace_bytes(cfg: KvConfig, heads: int, batch: int, tokens: int, max_queries: int = 1) -> int:
+    return int(lib().gptq_kv_attention_workspace_bytes(cfg._ref, heads, batch, tokens, max_queries))
+
+
+def gptq_kv_attention(cfg: KvConfig, Q: torch.Tensor, pages: torch.Tensor, page_table: torch.Tensor,
+                      kv_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                      max_queries: Optional[int] = None, scale: Optional[float] = None,
+                      Y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y [tokens, heads, head_dim] bf16: attention of each sequence's last
+    tokens over its cache (those tokens' keys and values appended before).
+    cu_seqlens as in gptq_kv_append; max_queries: the most tokens of a sequence
+    in this call as far as it is known (None: every token may be of one).  scale:
+    1/sqrt(head_dim) if None.  Without a workspace, or with one that is too
+    small, the call allocates its own."""
+    tokens, heads = Q.shape[0], Q.shape[1]
+    qld, qhs = _heads("Q", Q, tokens, heads, cfg.head_dim)
+    if Q.dtype != torch.bfloat16:
+        raise TypeError(f"Q must be bfloat16, not {Q.dtype}")
+    seqs = _sequences(Q, pages, gptq_kv_page_bytes(cfg), page_table, kv_lens, cu_seqlens, status, Y=Y,
+                      workspace=workspace)
+    if Y is None:
+        Y = _empty((tokens, heads, cfg.head_dim), torch.bfloat16, Q, stream)
+    yld, yhs = _heads("Y", Y, tokens, heads, cfg.head_dim)
+    if Y.dtype != torch.bfloat16:
+        raise TypeError(f"Y must be bfloat16, not {Y.dtype}")
+    if max_queries is None:
+        max_queries = 1 if cu_seqlens is None else tokens
+    cu, lens, table, batch, width, stride, pp, npages = seqs
+    fn = lib().gptq_kv_attention
+    args = (cfg._ref, Q.data_ptr(), tokens, heads, qld, qhs, cu, max_queries, lens, table, batch, width, stride, pp, npages,
+            cfg.head_dim ** -0.5 if scale is None else scale, Y.data_ptr(), yld, yhs, _ptr(status))
+    s = _stream_on(Q, stream)
+    with _device(Q):
+        _with_workspace(lambda ws, nbytes: fn(*args, ws, nbytes, s),
+                        lambda: gptq_kv_attention_workspace_bytes(cfg, heads, batch, tokens, max_queries), Q, workspace,
+                        stream, "gptq_kv_attention")
+    return Y
+
+
+def gptq_prompt_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_seqlens: torch.Tensor,
+                          scale: Optional[float] = None, Y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y [tokens, heads, head_dim] bf16: causal attention within each sequence
+    (rows cu_seqlens[b] .. cu_seqlens[b + 1]) of Q [tokens, heads, head_dim] and
+    K, V [tokens, kv_heads, head_dim], all bf16; heads / kv_heads query heads
+    read one key head.  scale: 1/sqrt(head_dim) if None."""
+    tokens, heads, dim = Q.shape
+    kv_heads = K.shape[1] if K.dim() == 3 else 0
+    qld, qhs = _heads("Q", Q, tokens, heads, dim)
+    kld, khs = _heads("K", K, tokens, kv_heads, dim)
+    vld, vhs = _heads("V", V, tokens, kv_heads, dim)
+    _on(Q, K=K, V=V, cu_seqlens=cu_seqlens, Y=Y)
+    if Y is None:
+        Y = _empty((tokens, heads, dim), torch.bfloat16, Q, stream)
+    yld, yhs = _heads("Y", Y, tokens, heads, dim)
+    if not Q.dtype == K.dtype == V.dtype == Y.dtype == torch.bfloat16:
+        raise TypeError("Q, K, V and Y must be bfloat16")
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 [sequences + 1]")
+    with _device(Q):
+        st = lib().gptq_prompt_attention(Q.data_ptr(), K.data_ptr(), V.data_ptr(), tokens, heads, kv_heads, dim, qld, qhs,
+                                         kld, khs, vld, vhs, cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1,
+                                         dim ** -0.5 if scale is None else scale, Y.data_ptr(), yld, yhs,
+                                         _stream_on(Q, stream))
+    _check(st, "gptq_prompt_attention")
+    return Y
+
+
 # ---------------------------------------------------------------- whole layer
 def alloc_outputs(m: int, n: int, cfg: QuantConfig, device) -> dict:
     words = gptq_qweight_words(n, cfg.bits)
