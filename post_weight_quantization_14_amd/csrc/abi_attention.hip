@@ -228,7 +228,7 @@ gptq_status gptq_prompt_attention(const void* Q, const void* K, const void* V, i
   GPTQ_TRY(check_rows("V", V, GPTQ_BF16, tokens, kv_heads, head_dim, ldv, v_head_stride, &c.V));
   GPTQ_TRY(check_rows("Y", Y, GPTQ_BF16, tokens, heads, head_dim, ldy, y_head_stride, &c.Y));
   if (bad_ptr(cu_seqlens, 4)) return fail(GPTQ_ERR_INVALID_ARG, "cu_seqlens is NULL or misaligned");
-  if ((tokens / 128 + std::min(batch, tokens) + 1) * heads > INT32_MAX)
+  if ((tokens / 128 + std::min(batch, tokens) + 1 + 8) * heads > INT32_MAX)
     return fail(GPTQ_ERR_UNSUPPORTED, "%lld tokens of %lld sequences of %d heads in one call", (long long)tokens,
                 (long long)batch, heads);
   if (overlap(c.Q, heads, c.Y, heads, tokens, head_dim, 2, 2) || overlap(c.K, kv_heads, c.Y, heads, tokens, head_dim, 2, 2) ||

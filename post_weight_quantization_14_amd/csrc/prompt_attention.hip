@@ -40,7 +40,7 @@ struct Prompt {
   HeadRows Q, K, V, Y;
   const int32_t* cu;
   int64_t batch, tokens, tiles;
-  int heads, share;
+  int kv_heads, share;
   float scale;      // times log2(e), positive: a masked logit times it stays -Inf
   uint32_t keep, flip;   // Q's bits and signs: a scale of 0 clears it, a negative one flips it
 };
@@ -52,7 +52,11 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int n32 = lane & 31, half = lane >> 5;
 
-  const int64_t head = blockIdx.x % a.heads;
+  // Workgroup i runs on XCD i % 8.  The heads that share a key head stay together
+  // on one, which then reads those keys from its own L2; tiles with the most keys
+  // go first.
+  const int64_t slot = blockIdx.x >> 3, group = slot / a.share * 8 + (blockIdx.x & 7);
+  const int64_t kvh = group % a.kv_heads, head = kvh * a.share + slot % a.share;
   int64_t b = 0, at = 0;
   auto seq = [&](int64_t i, int64_t* row) {
     const int64_t r0 = std::min(std::max<int64_t>(a.cu[i], 0), a.tokens);
@@ -60,7 +64,8 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
     *row = r0;
     return r1 - r0;
   };
-  if (!ragged_find(a.tiles - 1 - blockIdx.x / a.heads, a.batch, [&](int64_t i) {
+  if (group >= a.tiles * a.kv_heads) return;
+  if (!ragged_find(a.tiles - 1 - group / a.kv_heads, a.batch, [&](int64_t i) {
         int64_t r;
         return (seq(i, &r) + kBM - 1) / kBM;
       }, &b, &at))
@@ -73,8 +78,8 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
   const int keys = std::min(len, q0 + kBM);            // that any of its queries sees
   const int tiles = (keys + kBN - 1) / kBN;
 
-  const uint16_t* Kp = static_cast<const uint16_t*>(a.K.p) + row0 * a.K.ld + head / a.share * a.K.hs;
-  const uint16_t* Vp = static_cast<const uint16_t*>(a.V.p) + row0 * a.V.ld + head / a.share * a.V.hs;
+  const uint16_t* Kp = static_cast<const uint16_t*>(a.K.p) + row0 * a.K.ld + kvh * a.K.hs;
+  const uint16_t* Vp = static_cast<const uint16_t*>(a.V.p) + row0 * a.V.ld + kvh * a.V.hs;
 
   bf16x8_t qf[KS];
   {
@@ -94,26 +99,35 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
     }
   }
 
-  // rows of a tile into LDS; rows past the last key repeat it (masked)
+  // A tile's rows into LDS, straight from memory (descriptor bounds: rows past the
+  // last key read as zeros).  Piece i·256 + tid of a tile is row i·(256 / CH) +
+  // tid / CH, whose pieces lie as those of row tid / CH do: one address a lane.
+  const int t0 = tid / CH, c0 = (tid % CH ^ swz<D>(t0)) * 8;
+  const int kvoff = (int)(t0 * a.K.ld + c0) * 2, vvoff = (int)(t0 * a.V.ld + c0) * 2;
   auto fetch = [&](int tile, int buf) {
-    constexpr int kPieces = kBN * CH / kThreads;
+    constexpr int kRows = kThreads / CH;
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      const uint16_t* X = v ? Vp : Kp;
       const int64_t ld = v ? a.V.ld : a.K.ld;
+      const uint16_t* X = (v ? Vp : Kp) + (int64_t)tile * kBN * ld;
+      if (VEC) {
+        const int64_t left = ((int64_t)(keys - 1 - tile * kBN) * ld + D) * 2;
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint16_t*>(X), 0, (int)std::min<int64_t>(left, 0x7fffffff), 0x00020000);
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int at = (i * kWaves + wave) * 64;   // of 64 pieces
-        const int t = (at + lane) / CH, c = ((at + lane) % CH) ^ swz<D>(t);
-        const uint16_t* src = X + (int64_t)std::min(tile * kBN + t, keys - 1) * ld + c * 8;
-        if (VEC) {
-          __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                           (lds_void_t*)(&lds[buf][v][at * 16]), 16, 0, 0);
-        } else {
+        for (int i = 0; i < kBN / kRows; ++i)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(&lds[buf][v][(i * kThreads + wave * 64) * 16]), 16,
+                                                   v ? vvoff : kvoff, (int)(i * kRows * ld * 2), 0, 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBN / kRows; ++i) {
+          const int t = i * kRows + t0;
+          const bool there = tile * kBN + t < keys;
           u32x4_t x;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = src[2 * j] | (uint32_t)src[2 * j + 1] << 16;
-          *reinterpret_cast<u32x4_t*>(&lds[buf][v][(at + lane) * 16]) = x;
+          for (int j = 0; j < 4; ++j)
+            x[j] = there ? X[t * ld + c0 + 2 * j] | (uint32_t)X[t * ld + c0 + 2 * j + 1] << 16 : 0;
+          *reinterpret_cast<u32x4_t*>(&lds[buf][v][(i * kThreads + tid) * 16]) = x;
         }
       }
     }
@@ -125,7 +139,8 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
   // be in the last tiles; a result that is not finite is computed once more,
   // carefully: what is not finite is left out of the product there, and counted
   // for the queries that see it.
-  for (int careful = 0; careful < 2; ++careful) {
+  auto pass = [&](auto mode) {
+    constexpr bool careful = decltype(mode)::value;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -148,7 +163,7 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
         for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(kt + lds_at<D>(u * 32 + n32, ks * 2 + half));
+          const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(kt + lds_at<D>(n32, ks * 2 + half) + u * 32 * D * 2);
           s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[ks], s[u], 0, 0, 0);
         }
       }
@@ -181,19 +196,22 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
       const int g = lane >> 4, sl = lane & 15;
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        f32x16_t more, less;   // counts, careful only
-        if (careful && edge) {
+        f32x16_t more, less;   // counts
+        if constexpr (careful) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) more[r] = less[r] = 0.f;
         }
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          const int t = kk * 16 + (g >> 1) * 4 + (sl >> 2), c = d * 32 + (g & 1) * 16 + (sl & 3) * 4;
-          const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t*)(vt + lds_at<D>(t, c >> 3) + (c & 7) * 2));
-          const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t*)(vt + lds_at<D>(t + 8, c >> 3) + (c & 7) * 2));
+          // row kk·16 more: the same swizzle
+          const int t = (g >> 1) * 4 + (sl >> 2), c = d * 32 + (g & 1) * 16 + (sl & 3) * 4;
+          const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_v4i16_t*)(vt + lds_at<D>(t, c >> 3) + (c & 7) * 2 + kk * 16 * D * 2));
+          const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_v4i16_t*)(vt + lds_at<D>(t + 8, c >> 3) + (c & 7) * 2 + kk * 16 * D * 2));
           const auto both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
           bf16x8_t v = __builtin_bit_cast(bf16x8_t, both);
-          if (careful && edge) {
+          if constexpr (careful) if (edge) {
             bf16x8_t up, down, seen;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -210,7 +228,7 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
           }
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[kk], o[d], 0, 0, 0);
         }
-        if (careful && edge) {
+        if constexpr (careful) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) o[d][r] += (more[r] > 0.f ? INFINITY : 0.f) + (less[r] > 0.f ? -INFINITY : 0.f);
         }
@@ -221,8 +239,9 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int r = 0; r < 16; ++r) sum += o[d][r] * 0.f;   // NaN if any is not finite
-    if (!__syncthreads_or(iq < len && sum != sum)) break;
-  }
+    return __syncthreads_or(iq < len && sum != sum);
+  };
+  if (pass(std::false_type{})) pass(std::true_type{});
 
   l = half_sum(l);
   if (iq < len) {
@@ -249,11 +268,12 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
 
 gptq_status run_prompt_attention(const PromptCall& c, hipStream_t stream) {
   const int64_t tiles = (c.tokens + (kBM - 1) * std::min(c.batch, c.tokens)) / kBM;   // n tokens take at most (n + kBM - 1) / kBM
-  Prompt a{c.Q, c.K, c.V, c.Y, c.cu, c.batch, c.tokens, tiles, c.heads, c.heads / c.kv_heads,
+  Prompt a{c.Q, c.K, c.V, c.Y, c.cu, c.batch, c.tokens, tiles, c.kv_heads, c.heads / c.kv_heads,
            c.scale == 0.f ? 1.f : fabsf(c.scale) * 1.44269504088896340736f, c.scale == 0.f ? 0u : ~0u,
            c.scale < 0.f ? 0x80008000u : 0u};
-  const unsigned grid = (unsigned)(tiles * c.heads);
-  const bool vec = c.Q.vec && c.K.vec && c.V.vec && c.Y.vec;
+  const unsigned grid = (unsigned)(ceil_div(tiles * c.kv_heads, 8) * 8 * (c.heads / c.kv_heads));
+  const int64_t most = int64_t(1) << 23;   // a tile's rows are 32-bit offsets apart
+  const bool vec = c.Q.vec && c.K.vec && c.V.vec && c.Y.vec && c.K.ld < most && c.V.ld < most;
   if (c.dim == 128)
     vec ? prompt_attention_kernel<128, true><<<grid, kThreads, 0, stream>>>(a)
         : prompt_attention_kernel<128, false><<<grid, kThreads, 0, stream>>>(a);
