@@ -36,6 +36,28 @@ __device__ __forceinline__ int lds_at(int t, int c) {   // in bytes
   return t * (D * 2) + (c ^ swz<D>(t)) * 16;
 }
 
+// The values' operand of 32 channels at all 64 keys of a tile: for each 16 keys,
+// four rows of a column at `lo` and four at `hi`, transposed; 16 keys are STEP
+// bytes apart.  The reads and their wait are one block: of the builtin the
+// compiler does not see that it reads another buffer than the copies in flight
+// write, and makes it wait for them.
+template <int STEP>
+__device__ __forceinline__ void read_values(uint32_t lo, uint32_t hi, bf16x8_t (&v)[4]) {
+  u32x2_t r[8];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %9\n\t"
+      "ds_read_b64_tr_b16 %2, %8 offset:%10\n\tds_read_b64_tr_b16 %3, %9 offset:%10\n\t"
+      "ds_read_b64_tr_b16 %4, %8 offset:%11\n\tds_read_b64_tr_b16 %5, %9 offset:%11\n\t"
+      "ds_read_b64_tr_b16 %6, %8 offset:%12\n\tds_read_b64_tr_b16 %7, %9 offset:%12\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]), "=&v"(r[7])
+      : "v"(lo), "v"(hi), "n"(STEP), "n"(2 * STEP), "n"(3 * STEP)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = __builtin_bit_cast(bf16x8_t, u32x4_t{r[2 * i][0], r[2 * i][1], r[2 * i + 1][0], r[2 * i + 1][1]});
+}
+
 struct Prompt {
   HeadRows Q, K, V, Y;
   const int32_t* cu;
@@ -48,7 +70,9 @@ struct Prompt {
 template <int D, bool VEC>
 __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a) {
   constexpr int KS = D / 16, DT = D / 32, CH = D / 8, TB = kBN * D * 2;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TB];   // [buffer][K, V]
+  // Keys and values of a tile and of the next.  Two objects: the compiler makes a
+  // read wait for every copy in flight that may go to the object it reads.
+  __shared__ __attribute__((aligned(16))) uint8_t lds0[2 * TB], lds1[2 * TB];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int n32 = lane & 31, half = lane >> 5;
 
@@ -104,7 +128,7 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
   // tid / CH, whose pieces lie as those of row tid / CH do: one address a lane.
   const int t0 = tid / CH, c0 = (tid % CH ^ swz<D>(t0)) * 8;
   const int kvoff = (int)(t0 * a.K.ld + c0) * 2, vvoff = (int)(t0 * a.V.ld + c0) * 2;
-  auto fetch = [&](int tile, int buf) {
+  auto fetch = [&](int tile, uint8_t* buf) {
     constexpr int kRows = kThreads / CH;
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
@@ -116,7 +140,7 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
             const_cast<uint16_t*>(X), 0, (int)std::min<int64_t>(left, 0x7fffffff), 0x00020000);
 #pragma unroll
         for (int i = 0; i < kBN / kRows; ++i)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(&lds[buf][v][(i * kThreads + wave * 64) * 16]), 16,
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(buf + v * TB + (i * kThreads + wave * 64) * 16), 16,
                                                    v ? vvoff : kvoff, (int)(i * kRows * ld * 2), 0, 0);
       } else {
 #pragma unroll
@@ -127,7 +151,7 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             x[j] = there ? X[t * ld + c0 + 2 * j] | (uint32_t)X[t * ld + c0 + 2 * j + 1] << 16 : 0;
-          *reinterpret_cast<u32x4_t*>(&lds[buf][v][(i * kThreads + tid) * 16]) = x;
+          *reinterpret_cast<u32x4_t*>(buf + v * TB + (i * kThreads + tid) * 16) = x;
         }
       }
     }
@@ -147,15 +171,17 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
       for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
     m = kNone;
     l = 0.f;
-    fetch(0, 0);
-    for (int tile = 0; tile < tiles; ++tile) {
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
-      if (tile + 1 < tiles) fetch(tile + 1, (tile + 1) & 1);
+    fetch(0, lds0);
+    auto step = [&](int tile, uint8_t* cur, uint8_t* nxt) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0): this wave's copies have landed
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (tile + 1 < tiles) fetch(tile + 1, nxt);
       const int k0 = tile * kBN;
-      if (k0 > w0 + 31) continue;   // the wave's queries see none of it (no barrier is skipped)
-      const uint8_t* kt = lds[tile & 1][0];
-      const uint8_t* vt = lds[tile & 1][1];
+      if (k0 > w0 + 31) return;   // the wave's queries see none of it (no barrier is skipped)
+      const uint8_t* kt = cur;
+      const uint32_t vbase = (uint32_t)(uintptr_t)(lds_void_t*)(cur + TB);
       f32x16_t s[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -201,16 +227,12 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
 #pragma unroll
           for (int r = 0; r < 16; ++r) more[r] = less[r] = 0.f;
         }
+        const int t = (g >> 1) * 4 + (sl >> 2), c = d * 32 + (g & 1) * 16 + (sl & 3) * 4;
+        bf16x8_t vf[4];
+        read_values<16 * D * 2>(vbase + lds_at<D>(t, c >> 3) + (c & 7) * 2, vbase + lds_at<D>(t + 8, c >> 3) + (c & 7) * 2, vf);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          // row kk·16 more: the same swizzle
-          const int t = (g >> 1) * 4 + (sl >> 2), c = d * 32 + (g & 1) * 16 + (sl & 3) * 4;
-          const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_v4i16_t*)(vt + lds_at<D>(t, c >> 3) + (c & 7) * 2 + kk * 16 * D * 2));
-          const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_v4i16_t*)(vt + lds_at<D>(t + 8, c >> 3) + (c & 7) * 2 + kk * 16 * D * 2));
-          const auto both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-          bf16x8_t v = __builtin_bit_cast(bf16x8_t, both);
+          bf16x8_t v = vf[kk];
           if constexpr (careful) if (edge) {
             bf16x8_t up, down, seen;
 #pragma unroll
@@ -233,6 +255,10 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
           for (int r = 0; r < 16; ++r) o[d][r] += (more[r] > 0.f ? INFINITY : 0.f) + (less[r] > 0.f ? -INFINITY : 0.f);
         }
       }
+    };
+    for (int tile = 0; tile < tiles; tile += 2) {
+      step(tile, lds0, lds1);
+      if (tile + 1 < tiles) step(tile + 1, lds1, lds0);
     }
     float sum = 0.f;
 #pragma unroll
