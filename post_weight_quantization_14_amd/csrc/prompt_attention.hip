@@ -36,28 +36,6 @@ __device__ __forceinline__ int lds_at(int t, int c) {   // in bytes
   return t * (D * 2) + (c ^ swz<D>(t)) * 16;
 }
 
-// The values' operand of 32 channels at all 64 keys of a tile: for each 16 keys,
-// four rows of a column at `lo` and four at `hi`, transposed; 16 keys are STEP
-// bytes apart.  The reads and their wait are one block: of the builtin the
-// compiler does not see that it reads another buffer than the copies in flight
-// write, and makes it wait for them.
-template <int STEP>
-__device__ __forceinline__ void read_values(uint32_t lo, uint32_t hi, bf16x8_t (&v)[4]) {
-  u32x2_t r[8];
-  asm volatile(
-      "ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %9\n\t"
-      "ds_read_b64_tr_b16 %2, %8 offset:%10\n\tds_read_b64_tr_b16 %3, %9 offset:%10\n\t"
-      "ds_read_b64_tr_b16 %4, %8 offset:%11\n\tds_read_b64_tr_b16 %5, %9 offset:%11\n\t"
-      "ds_read_b64_tr_b16 %6, %8 offset:%12\n\tds_read_b64_tr_b16 %7, %9 offset:%12\n\t"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]), "=&v"(r[7])
-      : "v"(lo), "v"(hi), "n"(STEP), "n"(2 * STEP), "n"(3 * STEP)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v[i] = __builtin_bit_cast(bf16x8_t, u32x4_t{r[2 * i][0], r[2 * i][1], r[2 * i + 1][0], r[2 * i + 1][1]});
-}
-
 struct Prompt {
   HeadRows Q, K, V, Y;
   const int32_t* cu;
@@ -157,6 +135,20 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
     }
   };
 
+  // Where the lane's operands lie in a buffer: keys (row n32, pieces 2·ks + half)
+  // and values (transposed reads: four rows of a column at vlo, four at vhi).
+  // Whole offsets: behind a longer chain of sums the compiler loses sight of which
+  // buffer a read is of.
+  int kat[KS], vlo[DT], vhi[DT];
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) kat[ks] = lds_at<D>(n32, ks * 2 + half);
+#pragma unroll
+  for (int d = 0; d < DT; ++d) {
+    const int t = half * 4 + (lane >> 2 & 3), c = d * 32 + (lane >> 4 & 1) * 16 + (lane & 3) * 4;
+    vlo[d] = lds_at<D>(t, c >> 3) + (c & 7) * 2;
+    vhi[d] = lds_at<D>(t + 8, c >> 3) + (c & 7) * 2;
+  }
+
   f32x16_t o[DT];
   float m, l;
   // A masked value meets a weight of 0, and 0·Inf is NaN.  Such values can only
@@ -180,8 +172,6 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
       if (tile + 1 < tiles) fetch(tile + 1, nxt);
       const int k0 = tile * kBN;
       if (k0 > w0 + 31) return;   // the wave's queries see none of it (no barrier is skipped)
-      const uint8_t* kt = cur;
-      const uint32_t vbase = (uint32_t)(uintptr_t)(lds_void_t*)(cur + TB);
       f32x16_t s[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -189,7 +179,7 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
         for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(kt + lds_at<D>(n32, ks * 2 + half) + u * 32 * D * 2);
+          const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(cur + (kat[ks] + u * 32 * D * 2));
           s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[ks], s[u], 0, 0, 0);
         }
       }
@@ -219,7 +209,6 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
         l += e;
         p[r >> 3][r & 7] = (__bf16)e;
       }
-      const int g = lane >> 4, sl = lane & 15;
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         f32x16_t more, less;   // counts
@@ -227,12 +216,12 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a)
 #pragma unroll
           for (int r = 0; r < 16; ++r) more[r] = less[r] = 0.f;
         }
-        const int t = (g >> 1) * 4 + (sl >> 2), c = d * 32 + (g & 1) * 16 + (sl & 3) * 4;
-        bf16x8_t vf[4];
-        read_values<16 * D * 2>(vbase + lds_at<D>(t, c >> 3) + (c & 7) * 2, vbase + lds_at<D>(t + 8, c >> 3) + (c & 7) * 2, vf);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          bf16x8_t v = vf[kk];
+        for (int kk = 0; kk < 4; ++kk) {   // 16 rows further: the same swizzle
+          const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t*)(cur + (vlo[d] + (TB + kk * 16 * D * 2))));
+          const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t*)(cur + (vhi[d] + (TB + kk * 16 * D * 2))));
+          const auto both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          bf16x8_t v = __builtin_bit_cast(bf16x8_t, both);
           if constexpr (careful) if (edge) {
             bf16x8_t up, down, seen;
 #pragma unroll
