@@ -83,8 +83,9 @@ __device__ __forceinline__ KvSeq kv_seq(const KvSeqs& q, int64_t b, int64_t capa
   }
   const int64_t len = q.lens[b];
   s.bad = r0 < 0 || r1 < r0 || r1 > q.tokens || len < 0 || len > capacity;
-  s.row = std::min(std::max<int64_t>(r0, 0), q.tokens);
-  s.n = (int)(std::min(std::max(r1, s.row), q.tokens) - s.row);
+  s.row = r0 < 0 ? 0 : r0 > q.tokens ? q.tokens : r0;
+  const int64_t past = r1 > q.tokens ? q.tokens : r1;
+  s.n = past > s.row ? (int)(past - s.row) : 0;
   s.len = s.bad ? s.n : (int)len;
   return s;
 }

@@ -10,6 +10,9 @@
 namespace gptq {
 namespace {
 
+#define INLINE __attribute__((always_inline))
+typedef __attribute__((address_space(4))) int32_t constant_int;
+
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kStep = 32;        // positions of a wave's step: two records
 constexpr float kNone = -3e38f;  // a running maximum that has seen nothing
@@ -47,6 +50,11 @@ struct Consts {
   __device__ __forceinline__ uint32_t pair(uint32_t w) const { return (w & m) | c; }   // (128 + nibble 0, 128 + nibble 4)
 };
 
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {   // nearest even, one instruction
+  typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2_t;
+  return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b});
+}
+
 struct Work {
   KvLayout L;
   KvSeqs q;
@@ -60,18 +68,51 @@ struct Work {
 };
 
 // A unit is one row tile (R query rows: tokens x the heads that share a key
-// head) of one key head of one sequence; its steps are 32 positions each.
+// head) of one key head of one sequence; its steps are 32 positions each.  All
+// units' steps lie one after the other, by sequence, head and tile.  Lane i keeps
+// what it read of sequence i: batches of up to 64 are read once.
 template <int R>
 struct Units {
   const Work& w;
-  int64_t capacity;
-  __device__ __forceinline__ explicit Units(const Work& w_) : w(w_), capacity(std::min<int64_t>(w_.q.width * w_.L.recs * kKvRec, INT32_MAX)) {}
-  __device__ __forceinline__ KvSeq seq(int64_t b) const { return kv_seq(w.q, b, capacity); }
+  int64_t capacity, total;
+  KvSeq mine;
+  int64_t upto, own;   // steps of sequences 0 .. lane, and of this lane's
+  bool few;
+  __device__ __forceinline__ explicit Units(const Work& w_) : w(w_) {
+    capacity = min64(w.q.width * w.L.recs * kKvRec, INT32_MAX);
+    few = w.q.batch <= 64;
+    const int lane = threadIdx.x & 63;
+    if (few) {
+      mine = KvSeq{0, 0, 0, false};
+      own = 0;
+      if (lane < w.q.batch) {
+        mine = kv_seq(w.q, lane, capacity);
+        own = steps_of(mine);
+      }
+      upto = wave_scan(own);
+      total = uniform(__shfl(upto, 63));
+    } else {
+      total = uniform(ragged_total(w.q.batch, [&](int64_t b) { return steps_of(kv_seq(w.q, b, capacity)); }));
+    }
+  }
+  static __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
   static __device__ __forceinline__ int64_t tiles(const KvSeq& s, int share) { return ((int64_t)s.n * share + R - 1) / R; }
-  static __device__ __forceinline__ int64_t steps(const KvSeq& s) { return std::max<int64_t>(1, ((int64_t)s.len + kStep - 1) / kStep); }
-  __device__ __forceinline__ int64_t count(int64_t b) const {
-    const KvSeq s = seq(b);
-    return tiles(s, w.share) * steps(s) * w.L.heads;
+  static __device__ __forceinline__ int steps(const KvSeq& s) { return s.len > kStep ? (int)(((int64_t)s.len + kStep - 1) / kStep) : 1; }
+  __device__ __forceinline__ int64_t steps_of(const KvSeq& s) const { return tiles(s, w.share) * steps(s) * w.L.heads; }
+  // the sequence that step `pos` belongs to, and which of its steps it is
+  __device__ __forceinline__ KvSeq find(int64_t pos, int64_t* b, int64_t* at) const {
+    if (few) {
+      const int l = __ffsll((unsigned long long)__ballot(upto > pos)) - 1;
+      *b = l;
+      *at = pos - lane_of(upto - own, l);
+      return KvSeq{lane_of(mine.row, l), __builtin_amdgcn_readlane(mine.n, l), __builtin_amdgcn_readlane(mine.len, l),
+                   __builtin_amdgcn_readlane((int)mine.bad, l) != 0};
+    }
+    ragged_find(pos, w.q.batch, [&](int64_t i) { return steps_of(kv_seq(w.q, i, capacity)); }, b, at);
+    return uniform(kv_seq(w.q, *b, capacity));
+  }
+  static __device__ __forceinline__ int64_t lane_of(int64_t v, int l) {
+    return (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)v, l) | (int64_t)__builtin_amdgcn_readlane((int)(v >> 32), l) << 32;
   }
 };
 
@@ -122,26 +163,25 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
   const Units<R> units(w);
   const Consts kc;
 
-  const int64_t total = uniform(ragged_total(w.q.batch, [&](int64_t b) { return units.count(b); }));
-  const int64_t piece = std::max((total + gridDim.x - 1) / (int64_t)gridDim.x, min_piece);
-  const int64_t begin = piece * blockIdx.x, end = std::min(total, begin + piece);
+  const int64_t total = units.total, even = (total + gridDim.x - 1) / (int64_t)gridDim.x;
+  const int64_t piece = even > min_piece ? even : min_piece;
+  const int64_t begin = piece * blockIdx.x, end = begin + piece < total ? begin + piece : total;
   if (tid == 0) w.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (w.q.status)
     for (int64_t b = (int64_t)blockIdx.x * kThreads + tid; b < w.q.batch; b += (int64_t)gridDim.x * kThreads)
-      if (units.seq(b).bad) kv_bad(w.q.status);
+      if (kv_seq(w.q, b, units.capacity).bad) kv_bad(w.q.status);
 
   for (int64_t pos = begin; pos < end;) {
     int64_t b = 0, at = 0;
-    if (!ragged_find(pos, w.q.batch, [&](int64_t i) { return units.count(i); }, &b, &at)) break;
-    const KvSeq s = uniform(units.seq(b));
-    const int64_t steps = Units<R>::steps(s);
+    const KvSeq s = units.find(pos, &b, &at);
+    const int steps = Units<R>::steps(s);
     const int64_t unit = at / steps;                       // head · tiles + tile
     const int s0 = (int)(at - unit * steps);
-    const int s1 = (int)std::min<int64_t>(steps, s0 + (end - pos));
+    const int s1 = steps - s0 < end - pos ? steps : s0 + (int)(end - pos);
     const int64_t tiles = Units<R>::tiles(s, w.share);
     const int head = (int)(unit / tiles);
     const int64_t row0 = (unit - head * tiles) * R;
-    const int64_t rows = std::min<int64_t>(R, (int64_t)s.n * w.share - row0);
+    const int rows = (int)Units<R>::min64(R, (int64_t)s.n * w.share - row0);
 
     // ---- queries: lane n16 of every quarter holds query row 16·nt + n16
     bf16x8_t qf[NT][KS];
@@ -198,35 +238,39 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
 
     // ---- the wave's steps s0 + wave, + 4, ..
     const int last = (s.len - 1) / kKvRec;   // record; pages past it may be none
-    const int32_t* table = w.q.table + b * w.q.stride;
-    int tbase = -1;
-    int32_t tab = 0;
-    auto load = [&](int st, Step<D, G>& x) {
-      x.bad = s.bad;
+    // page numbers go through the scalar unit a step ahead of the records in them
+    const constant_int* table = (const constant_int*)(w.q.table + b * w.q.stride);
+    struct Pages {
+      int id[2];
+    };
+    auto page_of = [&](int st) INLINE {
+      Pages p;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) p.id[u] = s.bad ? -1 : table[min(2 * st + u, last) >> w.L.rec_shift];
+      return p;
+    };
+    const uint32_t head_at = (uint32_t)head << w.L.rec_shift;
+    auto load = [&](int st, const Pages& pg, Step<D, G>& x) INLINE {
+      x.bad = false;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int rec = std::min(2 * st + u, last);
-        const int pi = s.bad ? 0 : rec >> w.L.rec_shift;
-        if (tbase < 0 || pi >= tbase + 64) {
-          tbase = pi;
-          tab = s.bad ? 0 : table[std::min(pi + lane, last >> w.L.rec_shift)];
-        }
-        int64_t id = __builtin_amdgcn_readlane(tab, pi - tbase);
+        int64_t id = pg.id[u];
         if (id < 0 || id >= w.q.pages) {
           id = 0;
           x.bad = true;
         }
-        const uint8_t* p = w.pages + ((id * w.L.heads + head) * w.L.recs + (s.bad ? 0 : rec & (w.L.recs - 1))) * (int64_t)kv_rec_bytes(D, G);
+        const uint32_t rec = head_at + (min(2 * st + u, last) & (w.L.recs - 1));
+        const uint8_t* p = w.pages + id * w.L.page_bytes + (int64_t)rec * kv_rec_bytes(D, G);
         load_words(p + lane * (D / 8), x.k[u]);
-        load_words(p + kv_code_bytes(D) + lane * (D / 8), x.v[u]);
+        load_words(p + (kv_code_bytes(D) + lane * (D / 8)), x.v[u]);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          x.kp[u][g] = *reinterpret_cast<const u32x4_t*>(p + 2 * kv_code_bytes(D) + g * 64 + kg * 16);
-          x.vp[u][g] = *reinterpret_cast<const u32x4_t*>(p + 2 * kv_code_bytes(D) + kv_param_bytes(D, G) + g * 64 + kg * 16);
+          x.kp[u][g] = *reinterpret_cast<const u32x4_t*>(p + (2 * kv_code_bytes(D) + g * 64 + kg * 16));
+          x.vp[u][g] = *reinterpret_cast<const u32x4_t*>(p + (2 * kv_code_bytes(D) + kv_param_bytes(D, G) + g * 64 + kg * 16));
         }
       }
     };
-    auto compute = [&](int st, Step<D, G>& x) {
+    auto compute = [&](int st, Step<D, G>& x) INLINE {
       if (x.bad) {
         if (lane == 0) kv_bad(w.q.status);
 #pragma unroll
@@ -327,16 +371,27 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
           }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          float pw[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int u = i >> 2, r = i & 3;
-            float p = sx[nt][u][r] * ps[u][r];
-            if (edge && st * kStep + u * 16 + kg * 4 + r >= lim[nt]) p = 0.f;   // the scale there may be anything
-            const __bf16 h = (__bf16)p, lo = (__bf16)(p - (float)h);
-            ph[nt][i] = h;
-            pl[nt][i] = lo;
-            zs[nt][g] = fmaf((float)h + (float)lo, pz[u][r], zs[nt][g]);
+          for (int i = 0; i < 8; ++i) pw[i] = sx[nt][i >> 2][i & 3] * ps[i >> 2][i & 3];
+          if (edge) {   // the scale there may be anything
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (st * kStep + (i >> 2) * 16 + kg * 4 + (i & 3) >= lim[nt]) pw[i] = 0.f;
           }
+          u32x4_t hw, lw;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t h = pack_bf16(pw[2 * i], pw[2 * i + 1]);
+            const float h0 = __uint_as_float(h << 16), h1 = __uint_as_float(h & 0xffff0000u);
+            const uint32_t lo = pack_bf16(pw[2 * i] - h0, pw[2 * i + 1] - h1);
+            hw[i] = h;
+            lw[i] = lo;
+            zs[nt][g] = fmaf(h0 + __uint_as_float(lo << 16), pz[i >> 1][2 * i & 3], zs[nt][g]);
+            zs[nt][g] = fmaf(h1 + __uint_as_float(lo & 0xffff0000u), pz[i >> 1][(2 * i & 3) + 1], zs[nt][g]);
+          }
+          ph[nt] = __builtin_bit_cast(bf16x8_t, hw);
+          pl[nt] = __builtin_bit_cast(bf16x8_t, lw);
         }
 #pragma unroll
         for (int j = g * PG * 2; j < (g + 1) * PG * 2; ++j) {
@@ -357,11 +412,15 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
     if (s.len > 0) {
       Step<D, G> cur, nxt;
       int st = s0 + wave;
-      if (st < s1) load(st, cur);
-      for (; st < s1; st += kWaves) {
-        if (st + kWaves < s1) load(st + kWaves, nxt);
-        compute(st, cur);
-        cur = nxt;
+      if (st < s1) {
+        load(st, page_of(st), cur);
+        Pages ahead = page_of(min(st + kWaves, s1 - 1));
+        for (; st < s1; st += kWaves) {
+          load(min(st + kWaves, s1 - 1), ahead, nxt);
+          ahead = page_of(min(st + 2 * kWaves, s1 - 1));
+          compute(st, cur);
+          cur = nxt;
+        }
       }
     }
 
@@ -437,12 +496,11 @@ __global__ __launch_bounds__(256) void kv_join_kernel(Work w) {
   const int4 u = w.meta[blockIdx.x];
   if (u.x < 0) return;
   const int lane = threadIdx.x & 63;
-  const Units<R> units(w);
-  const KvSeq s = uniform(units.seq(u.x));
+  const KvSeq s = uniform(kv_seq(w.q, u.x, Units<R>::min64(w.q.width * w.L.recs * kKvRec, INT32_MAX)));
   const int64_t tiles = Units<R>::tiles(s, w.share);
   const int head = (int)(u.y / tiles);
   const int64_t row0 = (u.y - head * tiles) * R;
-  const int rows = (int)std::min<int64_t>(R, (int64_t)s.n * w.share - row0);
+  const int rows = (int)Units<R>::min64(R, (int64_t)s.n * w.share - row0);
   const int parts = u.w - (int)blockIdx.x + 1;
   auto part = [&](int i) { return w.partial + (int64_t)(i == 0 ? u.z : 2 * ((int)blockIdx.x + i)) * R * (D + 2); };
   for (int row = (int)blockIdx.y * 4 + uniform((int)threadIdx.x >> 6); row < rows; row += 4 * (int)gridDim.y) {
