@@ -160,7 +160,7 @@ gptq_status run_kv_read(const KvLayout& L, const HeadRows& K, const HeadRows& V,
                         const void* pages, hipStream_t stream);
 
 struct KvAttentionPlan {
-  int tiles;          // 16-row tiles of queries that a workgroup holds: 1 or 4
+  int tiles;          // 16-row tiles of queries that a workgroup holds: 1 or 2
   int wgs;            // workgroups that the positions are split over
   int rows;           // rows of a unit that should hold queries
   size_t partial, meta, total;   // workspace bytes

@@ -55,16 +55,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {   // nearest e
   return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b});
 }
 
+struct Split {
+  int64_t token;      // of the unit's first row
+  int head;           // key head
+  uint32_t hq0;       // query head of the first row within the group
+  int rows, slot;     // of the first part; part i > 0 is slot 2·(workgroup + i)
+  int parts;          // 0: no such unit
+  int pad;
+};
+
 struct Work {
   KvLayout L;
   KvSeqs q;
   HeadRows Q, Y;
-  float scale;           // times log2(e)
+  float scale;           // times log2(e), positive: a masked logit times it stays -Inf
+  uint32_t keep, flip;   // Q's bits and signs: a scale of 0 clears it, a negative one flips it
   int share;             // query heads of a key head
+  uint32_t share_inv;    // above 2^32 / share: x / share = umulhi(x, share_inv) for x below 2^13 (not for share 1)
   const uint8_t* pages;
   float* partial;        // [2·wgs] of [rows][D] sums, [rows] maxima, [rows] sums of weights
-  int4* meta;            // [wgs]: (sequence, head · row tiles + tile, first slot, last workgroup) of a unit split over
-                         // workgroups that begins in this one; sequence -1: none
+  Split* meta;           // [wgs]: of a unit split over workgroups that begins in this one
 };
 
 // A unit is one row tile (R query rows: tokens x the heads that share a key
@@ -116,6 +126,12 @@ struct Units {
   }
 };
 
+// a / b of uniform numbers, by 32 bits where they do
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
 template <int D, int G>
 struct Step {
   static constexpr int KS = D / 32, NG = D / G;
@@ -153,7 +169,7 @@ __device__ __forceinline__ void value_pairs(const uint32_t (&w)[D / 32], int b, 
 }
 
 template <int D, int G, int NT>
-__global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel(Work w, int64_t min_piece) {
+__global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64_t min_piece) {
   constexpr int R = 16 * NT, KS = D / 32, NG = D / G, MT = D / 16, PG = G / 32;   // PG: 32-channel steps of a group
   constexpr int kPitch = D + 4;
   __shared__ float so[kWaves][16][kPitch];
@@ -166,7 +182,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
   const int64_t total = units.total, even = (total + gridDim.x - 1) / (int64_t)gridDim.x;
   const int64_t piece = even > min_piece ? even : min_piece;
   const int64_t begin = piece * blockIdx.x, end = begin + piece < total ? begin + piece : total;
-  if (tid == 0) w.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (tid == 0) w.meta[blockIdx.x].parts = 0;
   if (w.q.status)
     for (int64_t b = (int64_t)blockIdx.x * kThreads + tid; b < w.q.batch; b += (int64_t)gridDim.x * kThreads)
       if (kv_seq(w.q, b, units.capacity).bad) kv_bad(w.q.status);
@@ -175,66 +191,40 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
     int64_t b = 0, at = 0;
     const KvSeq s = units.find(pos, &b, &at);
     const int steps = Units<R>::steps(s);
-    const int64_t unit = at / steps;                       // head · tiles + tile
+    const int64_t unit = divide(at, steps);                       // head · tiles + tile
     const int s0 = (int)(at - unit * steps);
     const int s1 = steps - s0 < end - pos ? steps : s0 + (int)(end - pos);
     const int64_t tiles = Units<R>::tiles(s, w.share);
-    const int head = (int)(unit / tiles);
-    const int64_t row0 = (unit - head * tiles) * R;
+    const int head = (int)divide(unit, tiles);
+    const int64_t row0 = (unit - head * tiles) * R, tq0 = divide(row0, w.share);
+    const uint32_t hq0 = (uint32_t)(row0 - tq0 * w.share);   // row0 is head hq0 of the group, token tq0
     const int rows = (int)Units<R>::min64(R, (int64_t)s.n * w.share - row0);
 
     // ---- queries: lane n16 of every quarter holds query row 16·nt + n16
-    bf16x8_t qf[NT][KS];
-    float qs[NT][NG];
+    u32x4_t qx[NT][KS];
     int lim[NT];     // positions that the row sees
+    const uint16_t* qp[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int64_t r = row0 + nt * 16 + n16;
-      const bool there = r - row0 < rows;
-      const int tq = there ? (int)(r / w.share) : 0;
-      const int hq = head * w.share + (there ? (int)(r - (int64_t)tq * w.share) : 0);
-      lim[nt] = there ? s.len - s.n + tq + 1 : 0;
-      const uint16_t* qp = static_cast<const uint16_t*>(w.Q.p) + (s.row + tq) * w.Q.ld + hq * w.Q.hs + kg * 8;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        u32x4_t x = {0, 0, 0, 0};
-        if (there) {
-          if (w.Q.vec) {
-            x = *reinterpret_cast<const u32x4_t*>(qp + ks * 32);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = qp[ks * 32 + 2 * i] | (uint32_t)qp[ks * 32 + 2 * i + 1] << 16;
-          }
-        }
-        qf[nt][ks] = __builtin_bit_cast(bf16x8_t, x);
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t += __uint_as_float(x[i] << 16) + __uint_as_float(x[i] & 0xffff0000u);
-        t = quad_sum(t);
-        if (ks % PG == 0)
-          qs[nt][ks / PG] = t;
-        else
-          qs[nt][ks / PG] += t;
-      }
+      const int i = nt * 16 + n16 < rows ? nt * 16 + n16 : 0;   // rows past the last: computed, not stored
+      const uint32_t h = hq0 + i, t = w.share == 1 ? h : __umulhi(h, w.share_inv);
+      lim[nt] = s.len - s.n + (int)tq0 + (int)t + 1;
+      qp[nt] = static_cast<const uint16_t*>(w.Q.p) + (s.row + tq0 + t) * w.Q.ld + (head * w.share + (h - t * w.share)) * w.Q.hs + kg * 8;
     }
-    int least = INT32_MAX;   // positions that every row there sees
+    if (w.Q.vec) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) least = std::min(least, nt * 16 + n16 < rows ? lim[nt] : INT32_MAX);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int d = 1; d < 16; d <<= 1) least = std::min(least, __shfl_xor(least, d));
-    least = __builtin_amdgcn_readfirstlane(least);
-
-    f32x4_t o[NT][MT];
-    float m[NT], l[NT], zs[NT][NG];
+        for (int ks = 0; ks < KS; ++ks) qx[nt][ks] = *reinterpret_cast<const u32x4_t*>(qp[nt] + ks * 32);
+    } else {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt] = kNone;
-      l[nt] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int g = 0; g < NG; ++g) zs[nt][g] = 0.f;
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int j = 0; j < MT; ++j) o[nt][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+          for (int i = 0; i < 4; ++i) qx[nt][ks][i] = qp[nt][ks * 32 + 2 * i] | (uint32_t)qp[nt][ks * 32 + 2 * i + 1] << 16;
     }
+    const int least = s.len - s.n + (int)tq0 + 1;   // positions that every row sees
 
     // ---- the wave's steps s0 + wave, + 4, ..
     const int last = (s.len - 1) / kKvRec;   // record; pages past it may be none
@@ -254,11 +244,9 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
       x.bad = false;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        int64_t id = pg.id[u];
-        if (id < 0 || id >= w.q.pages) {
-          id = 0;
-          x.bad = true;
-        }
+        const bool none = (uint32_t)pg.id[u] >= (uint32_t)w.q.pages;
+        const int64_t id = none ? 0 : pg.id[u];
+        x.bad |= none;
         const uint32_t rec = head_at + (min(2 * st + u, last) & (w.L.recs - 1));
         const uint8_t* p = w.pages + id * w.L.page_bytes + (int64_t)rec * kv_rec_bytes(D, G);
         load_words(p + lane * (D / 8), x.k[u]);
@@ -270,6 +258,42 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
         }
       }
     };
+    Step<D, G> cur, nxt;
+    int st = s0 + wave;
+    const bool some = st < s1 && s.len > 0;
+    Pages ahead;
+    if (some) {
+      load(st, page_of(st), cur);
+      ahead = page_of(min(st + kWaves, s1 - 1));
+    }
+
+    bf16x8_t qf[NT][KS];
+    float qs[NT][NG];   // sums of the query's channels, by group
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qx[nt][ks][i] = (qx[nt][ks][i] & w.keep) ^ w.flip;
+        qf[nt][ks] = __builtin_bit_cast(bf16x8_t, qx[nt][ks]);
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t += __uint_as_float(qx[nt][ks][i] << 16) + __uint_as_float(qx[nt][ks][i] & 0xffff0000u);
+        t = quad_sum(t);
+        qs[nt][ks / PG] = ks % PG == 0 ? t : qs[nt][ks / PG] + t;
+      }
+    f32x4_t o[NT][MT];
+    float m[NT], l[NT], zs[NT][NG];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt] = kNone;
+      l[nt] = 0.f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) zs[nt][g] = 0.f;
+#pragma unroll
+      for (int j = 0; j < MT; ++j) o[nt][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
     auto compute = [&](int st, Step<D, G>& x) INLINE {
       if (x.bad) {
         if (lane == 0) kv_bad(w.q.status);
@@ -298,7 +322,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const uint32_t pw = x.kp[u][g][r];
-            ps[r] = __uint_as_float(pw & 0xffff0000u) * w.scale;
+            ps[r] = __uint_as_float(pw & 0xffff0000u);
             pz[r] = (float)((int)(int16_t)(uint16_t)pw + 128);
           }
 #pragma unroll
@@ -333,7 +357,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
         float t = sx[nt][0][0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) t = fmaxf(t, sx[nt][i >> 2][i & 3]);
-        top[nt] = quad_max(t);
+        top[nt] = quad_max(t) * w.scale;
         grown |= top[nt] > m[nt] + 8.f;
       }
       if (__ballot(grown)) {
@@ -353,7 +377,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float& p = sx[nt][i >> 2][i & 3];
-          p = __builtin_amdgcn_exp2f(p - m[nt]);
+          p = __builtin_amdgcn_exp2f(fmaf(p, w.scale, -m[nt]));
           l[nt] += p;
         }
       // values
@@ -409,18 +433,16 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
         }
       }
     };
-    if (s.len > 0) {
-      Step<D, G> cur, nxt;
-      int st = s0 + wave;
-      if (st < s1) {
-        load(st, page_of(st), cur);
-        Pages ahead = page_of(min(st + kWaves, s1 - 1));
-        for (; st < s1; st += kWaves) {
-          load(min(st + kWaves, s1 - 1), ahead, nxt);
-          ahead = page_of(min(st + 2 * kWaves, s1 - 1));
-          compute(st, cur);
-          cur = nxt;
-        }
+    if (some) {
+      for (;;) {
+        load(min(st + kWaves, s1 - 1), ahead, nxt);
+        ahead = page_of(min(st + 2 * kWaves, s1 - 1));
+        compute(st, cur);
+        if ((st += kWaves) >= s1) break;
+        load(min(st + kWaves, s1 - 1), ahead, cur);
+        ahead = page_of(min(st + 2 * kWaves, s1 - 1));
+        compute(st, nxt);
+        if ((st += kWaves) >= s1) break;
       }
     }
 
@@ -429,7 +451,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
     const int slot = pos == begin ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1;
     float* part = w.partial + (int64_t)slot * R * (D + 2);
     if (!whole && s0 == 0 && tid == 0)
-      w.meta[blockIdx.x] = make_int4((int)b, (int)unit, slot, (int)((pos + steps - 1) / piece));
+      w.meta[blockIdx.x] = Split{s.row + tq0, head, hq0, rows, slot, (int)((pos + steps - 1) / piece) - (int)blockIdx.x + 1, 0};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       l[nt] = quad_sum(l[nt]);
@@ -450,8 +472,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
       __syncthreads();
       for (int i = tid; i < 16 * (D / 4); i += kThreads) {
         const int n = i / (D / 4), d = i % (D / 4) * 4;
-        const int64_t r = row0 + nt * 16 + n;
-        if (r - row0 >= rows) continue;
+        if (nt * 16 + n >= rows) continue;
         float ll = 0.f;
         f32x4_t y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -461,9 +482,9 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
         }
         if (whole) {
           const float inv = ll == 0.f ? 0.f : 1.f / ll;   // a row that sees nothing
-          const int64_t tq = r / w.share;
-          uint16_t* yp = const_cast<uint16_t*>(static_cast<const uint16_t*>(w.Y.p)) + (s.row + tq) * w.Y.ld +
-                         (head * w.share + (r - tq * w.share)) * w.Y.hs + d;
+          const uint32_t i = hq0 + nt * 16 + n, t = w.share == 1 ? i : __umulhi(i, w.share_inv);
+          uint16_t* yp = const_cast<uint16_t*>(static_cast<const uint16_t*>(w.Y.p)) + (s.row + tq0 + t) * w.Y.ld +
+                         (head * w.share + (i - t * w.share)) * w.Y.hs + d;
           uint16_t h[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) h[c] = __builtin_bit_cast(uint16_t, (__bf16)(y[c] * inv));
@@ -490,42 +511,78 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void kv_attention_kernel
   }
 }
 
-// Joins the parts of a unit that was split: one wave per row.
+// Joins the parts of units that were split.  A workgroup looks at four entries of
+// `meta`, four waves at each: they share the parts of a row, whose loads are all
+// in flight at once (a chain of loads, not their bytes, is what this costs).
 template <int D, int R>
-__global__ __launch_bounds__(256) void kv_join_kernel(Work w) {
-  const int4 u = w.meta[blockIdx.x];
-  if (u.x < 0) return;
-  const int lane = threadIdx.x & 63;
-  const KvSeq s = uniform(kv_seq(w.q, u.x, Units<R>::min64(w.q.width * w.L.recs * kKvRec, INT32_MAX)));
-  const int64_t tiles = Units<R>::tiles(s, w.share);
-  const int head = (int)(u.y / tiles);
-  const int64_t row0 = (u.y - head * tiles) * R;
-  const int rows = (int)Units<R>::min64(R, (int64_t)s.n * w.share - row0);
-  const int parts = u.w - (int)blockIdx.x + 1;
-  auto part = [&](int i) { return w.partial + (int64_t)(i == 0 ? u.z : 2 * ((int)blockIdx.x + i)) * R * (D + 2); };
-  for (int row = (int)blockIdx.y * 4 + uniform((int)threadIdx.x >> 6); row < rows; row += 4 * (int)gridDim.y) {
-    float up = kNone;
-    for (int i = lane; i < parts; i += 64) up = fmaxf(up, part(i)[R * D + row]);
+__global__ __launch_bounds__(1024) void kv_join_kernel(Work w) {
+  constexpr int C = D / 64;
+  constexpr int64_t kSize = R * (D + 2);
+  __shared__ float sy[4][4][D], sw[4][4][2];
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), e = wave >> 2, q = wave & 3;
+  const int first = (int)blockIdx.x * 4 + e;
+  const Split u = w.meta[first];
+  const int parts = uniform(u.parts), rows = parts ? uniform(u.rows) : 0;
+  const float* p0 = w.partial + uniform(u.slot) * kSize;
+  const float* p1 = w.partial + 2 * (int64_t)first * kSize;
+  for (int row = (int)blockIdx.y; __syncthreads_or(row < rows); row += (int)gridDim.y) {
+    if (row < rows) {   // the wave's parts: q, q + 4, ..
+      float up = kNone, ll = 0.f, y[C];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) up = fmaxf(up, __shfl_xor(up, d));
-    constexpr int C = D / 64;
-    float ll = 0.f, y[C];
+      for (int c = 0; c < C; ++c) y[c] = 0.f;
+      for (int i0 = q; i0 < parts; i0 += 32) {
+        float m[8], l[8], v[8][C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) y[c] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const float* p = part(i);
-      const float f = exp2f(p[R * D + row] - up);
-      ll = fmaf(p[R * D + R + row], f, ll);
+        for (int j = 0; j < 8; ++j) {
+          const int i = min(i0 + 4 * j, parts - 1);
+          const float* p = i == 0 ? p0 : p1 + 2 * i * kSize;
+          m[j] = p[R * D + row];
+          l[j] = p[R * D + R + row];
 #pragma unroll
-      for (int c = 0; c < C; ++c) y[c] = fmaf(p[row * D + lane * C + c], f, y[c]);
+          for (int c = 0; c < C; ++c) v[j][c] = p[row * D + lane * C + c];
+        }
+        float top = up;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, m[j]);
+        const float f = exp2f(up - top);
+        up = top;
+        ll *= f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) y[c] *= f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool there = i0 + 4 * j < parts;
+          const float g = there ? exp2f(m[j] - up) : 0.f;
+          ll += there ? l[j] * g : 0.f;
+#pragma unroll
+          for (int c = 0; c < C; ++c) y[c] += there ? v[j][c] * g : 0.f;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) sy[e][q][lane * C + c] = y[c];
+      if (lane == 0) sw[e][q][0] = up, sw[e][q][1] = ll;
     }
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    const int64_t r = row0 + row, tq = r / w.share;
-    uint16_t* yp = const_cast<uint16_t*>(static_cast<const uint16_t*>(w.Y.p)) + (s.row + tq) * w.Y.ld +
-                   (head * w.share + (r - tq * w.share)) * w.Y.hs + lane * C;
+    __syncthreads();
+    if (row < rows && q == 0) {
+      float up = kNone, ll = 0.f, y[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) yp[c] = __builtin_bit_cast(uint16_t, (__bf16)(y[c] * inv));
+      for (int i = 0; i < 4; ++i) up = fmaxf(up, sw[e][i][0]);
+#pragma unroll
+      for (int c = 0; c < C; ++c) y[c] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = exp2f(sw[e][i][0] - up);
+        ll = fmaf(sw[e][i][1], f, ll);
+#pragma unroll
+        for (int c = 0; c < C; ++c) y[c] = fmaf(sy[e][i][lane * C + c], f, y[c]);
+      }
+      const float inv = ll == 0.f ? 0.f : 1.f / ll;   // a row that sees nothing
+      const uint32_t i = uniform((int)u.hq0) + row, t = w.share == 1 ? i : __umulhi(i, w.share_inv);
+      uint16_t* yp = const_cast<uint16_t*>(static_cast<const uint16_t*>(w.Y.p)) + (u.token + t) * w.Y.ld +
+                     (u.head * w.share + (i - t * w.share)) * w.Y.hs + lane * C;
+#pragma unroll
+      for (int c = 0; c < C; ++c) yp[c] = __builtin_bit_cast(uint16_t, (__bf16)(y[c] * inv));
+    }
   }
 }
 
@@ -533,7 +590,7 @@ template <int D, int G, int NT>
 gptq_status launch(const Work& w, const KvAttentionPlan& p, hipStream_t stream) {
   kv_attention_kernel<D, G, NT><<<p.wgs, kThreads, 0, stream>>>(w, 4);
   GPTQ_LAUNCH_CHECK();
-  kv_join_kernel<D, 16 * NT><<<dim3(p.wgs, (p.rows + 3) / 4), 256, 0, stream>>>(w);
+  kv_join_kernel<D, 16 * NT><<<dim3(p.wgs / 4, p.rows), 1024, 0, stream>>>(w);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
@@ -543,11 +600,11 @@ gptq_status launch(const Work& w, const KvAttentionPlan& p, hipStream_t stream) 
 KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, int64_t tokens, int64_t max_queries) {
   KvAttentionPlan p;
   const int64_t rows = std::min(std::max<int64_t>(max_queries, 1), std::max<int64_t>(tokens, 1)) * (heads / L.heads);
-  p.tiles = rows > 16 ? 4 : 1;
+  p.tiles = rows > 16 ? 2 : 1;
   p.wgs = 512;
   p.rows = (int)std::min<int64_t>(rows, 16 * p.tiles);
   p.partial = (size_t)2 * p.wgs * 16 * p.tiles * (L.dim + 2) * 4;
-  p.meta = (size_t)p.wgs * sizeof(int4);
+  p.meta = (size_t)p.wgs * sizeof(Split);
   p.total = align256(p.partial) + p.meta;
   (void)batch;
   return p;
@@ -555,10 +612,12 @@ KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, i
 
 gptq_status run_kv_attention(const KvLayout& L, int heads, const HeadRows& Q, const HeadRows& Y, float scale,
                              const KvSeqs& q, const void* pages, void* ws, const KvAttentionPlan& p, hipStream_t stream) {
-  const Work w{L, q, Q, Y, scale * 1.44269504088896340736f, heads / L.heads, static_cast<const uint8_t*>(pages),
-               static_cast<float*>(ws), reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + align256(p.partial))};
+  const Work w{L, q, Q, Y, scale == 0.f ? 1.f : fabsf(scale) * 1.44269504088896340736f, scale == 0.f ? 0u : ~0u,
+               scale < 0.f ? 0x80008000u : 0u, heads / L.heads, (uint32_t)((1ull << 32) / (heads / L.heads) + 1),
+               static_cast<const uint8_t*>(pages),
+               static_cast<float*>(ws), reinterpret_cast<Split*>(static_cast<uint8_t*>(ws) + align256(p.partial))};
   auto tiled = [&](auto d, auto g) {
-    return p.tiles == 1 ? launch<d.value, g.value, 1>(w, p, stream) : launch<d.value, g.value, 4>(w, p, stream);
+    return p.tiles == 1 ? launch<d.value, g.value, 1>(w, p, stream) : launch<d.value, g.value, 2>(w, p, stream);
   };
   using std::integral_constant;
   if (L.dim == 128 && L.group == 128) return tiled(integral_constant<int, 128>{}, integral_constant<int, 128>{});
