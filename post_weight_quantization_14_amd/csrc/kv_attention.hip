@@ -43,6 +43,12 @@ __device__ __forceinline__ float quad_sum(float x) {
   return x + y;
 }
 
+// lane n of the row of 16
+template <int N>
+__device__ __forceinline__ float row_lane(float x) {
+  return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0x150 + N, 0xf, 0xf, true));
+}
+
 // The constants of the AND-OR, hidden from folding (VOP3 takes no literals).
 struct Consts {
   uint32_t m, c;
@@ -53,6 +59,13 @@ struct Consts {
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {   // nearest even, one instruction
   typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2_t;
   return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b});
+}
+
+template <class F>
+__device__ __forceinline__ void by_index(const F& f) {   // f(0) .. f(7), each a constant
+  f(std::integral_constant<int, 0>{}), f(std::integral_constant<int, 1>{}), f(std::integral_constant<int, 2>{});
+  f(std::integral_constant<int, 3>{}), f(std::integral_constant<int, 4>{}), f(std::integral_constant<int, 5>{});
+  f(std::integral_constant<int, 6>{}), f(std::integral_constant<int, 7>{});
 }
 
 struct Split {
@@ -136,8 +149,8 @@ template <int D, int G>
 struct Step {
   static constexpr int KS = D / 32, NG = D / G;
   uint32_t k[2][KS], v[2][KS];
-  u32x4_t kp[2][NG], vp[2][NG];
-  bool bad;   // a page that is none
+  uint32_t pw[NG];   // params: lane 16·kg + 4·j + r has those of position 4·kg + r, j: keys of the two records, values
+  bool bad;          // a page that is none
 };
 
 template <int N>
@@ -240,8 +253,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
       return p;
     };
     const uint32_t head_at = (uint32_t)head << w.L.rec_shift;
+    const int param_at = 2 * kv_code_bytes(D) + (n16 >> 3) * kv_param_bytes(D, G) + (kg * 4 + (n16 & 3)) * 4;
     auto load = [&](int st, const Pages& pg, Step<D, G>& x) INLINE {
       x.bad = false;
+      const uint8_t* base[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const bool none = (uint32_t)pg.id[u] >= (uint32_t)w.q.pages;
@@ -251,12 +266,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
         const uint8_t* p = w.pages + id * w.L.page_bytes + (int64_t)rec * kv_rec_bytes(D, G);
         load_words(p + lane * (D / 8), x.k[u]);
         load_words(p + (kv_code_bytes(D) + lane * (D / 8)), x.v[u]);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          x.kp[u][g] = *reinterpret_cast<const u32x4_t*>(p + (2 * kv_code_bytes(D) + g * 64 + kg * 16));
-          x.vp[u][g] = *reinterpret_cast<const u32x4_t*>(p + (2 * kv_code_bytes(D) + kv_param_bytes(D, G) + g * 64 + kg * 16));
-        }
+        base[u] = p;
       }
+      const uint8_t* p = (lane & 4 ? base[1] : base[0]) + param_at;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) x.pw[g] = *reinterpret_cast<const uint32_t*>(p + g * 64);
     };
     Step<D, G> cur, nxt;
     int st = s0 + wave;
@@ -295,15 +309,13 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
     }
 
     auto compute = [&](int st, Step<D, G>& x) INLINE {
-      if (x.bad) {
-        if (lane == 0) kv_bad(w.q.status);
+      float sf[NG], zf[NG];   // scales and 128 + zero points, of the positions of `pw`
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x.kp[u][g][r] = 0x7fc00000u;
+      for (int g = 0; g < NG; ++g) {
+        sf[g] = __uint_as_float(x.bad ? 0x7fc00000u : x.pw[g] & 0xffff0000u);
+        zf[g] = (float)((int)(int16_t)(uint16_t)x.pw[g] + 128);
       }
+      if (x.bad && lane == 0) kv_bad(w.q.status);
       // logits of positions 32·st + 16·u + 4·kg + r
       float sx[NT][2][4];
 #pragma unroll
@@ -318,24 +330,21 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
         }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          float ps[4], pz[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const uint32_t pw = x.kp[u][g][r];
-            ps[r] = __uint_as_float(pw & 0xffff0000u);
-            pz[r] = (float)((int)(int16_t)(uint16_t)pw + 128);
-          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = g * PG; ks < (g + 1) * PG; ++ks)
               acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[ks], qf[nt][ks], acc, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float y = fmaf(-pz[r], qs[nt][g], acc[r]);
-              sx[nt][u][r] = g == 0 ? y * ps[r] : fmaf(y, ps[r], sx[nt][u][r]);
-            }
+            auto one = [&](auto r) INLINE {
+              constexpr int R0 = decltype(r)::value;
+              const float z = u ? row_lane<4 + R0>(zf[g]) : row_lane<R0>(zf[g]);
+              const float f = u ? row_lane<4 + R0>(sf[g]) : row_lane<R0>(sf[g]);
+              const float y = acc[R0] - z * qs[nt][g];
+              sx[nt][u][R0] = g == 0 ? y * f : sx[nt][u][R0] + y * f;
+            };
+            one(std::integral_constant<int, 0>{}), one(std::integral_constant<int, 1>{});
+            one(std::integral_constant<int, 2>{}), one(std::integral_constant<int, 3>{});
           }
         }
       }
@@ -384,20 +393,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         bf16x8_t ph[NT], pl[NT];
-        float ps[2][4], pz[2][4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const uint32_t pw = x.vp[u][g][r];
-            ps[u][r] = __uint_as_float(pw & 0xffff0000u);
-            pz[u][r] = (float)((int)(int16_t)(uint16_t)pw + 128);
-          }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float pw[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) pw[i] = sx[nt][i >> 2][i & 3] * ps[i >> 2][i & 3];
+          by_index([&](auto i) INLINE { pw[i.value] = row_lane<8 + i.value>(sf[g]) * sx[nt][i.value >> 2][i.value & 3]; });
           if (edge) {   // the scale there may be anything
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -411,9 +410,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
             const uint32_t lo = pack_bf16(pw[2 * i] - h0, pw[2 * i + 1] - h1);
             hw[i] = h;
             lw[i] = lo;
-            zs[nt][g] = fmaf(h0 + __uint_as_float(lo << 16), pz[i >> 1][2 * i & 3], zs[nt][g]);
-            zs[nt][g] = fmaf(h1 + __uint_as_float(lo & 0xffff0000u), pz[i >> 1][(2 * i & 3) + 1], zs[nt][g]);
+            pw[2 * i] = h0 + __uint_as_float(lo << 16);
+            pw[2 * i + 1] = h1 + __uint_as_float(lo & 0xffff0000u);
           }
+          by_index([&](auto i) INLINE { zs[nt][g] += row_lane<8 + i.value>(zf[g]) * pw[i.value]; });
           ph[nt] = __builtin_bit_cast(bf16x8_t, hw);
           pl[nt] = __builtin_bit_cast(bf16x8_t, lw);
         }
