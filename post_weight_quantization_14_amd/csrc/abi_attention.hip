@@ -175,7 +175,7 @@ size_t gptq_kv_attention_workspace_bytes(const gptq_kv_config* cfg, int32_t head
     clear_error();
     return 0;
   }
-  return plan_kv_attention(plan_kv(*cfg), heads, batch, tokens, max_queries).total;
+  return plan_kv_attention(plan_kv(*cfg), heads, batch, tokens, max_queries, 0).total;
 }
 
 gptq_status gptq_kv_attention(const gptq_kv_config* cfg, const void* Q, int64_t tokens, int32_t heads, int64_t ldq,
@@ -202,7 +202,7 @@ gptq_status gptq_kv_attention(const gptq_kv_config* cfg, const void* Q, int64_t 
   if (overlap(q, heads, y, heads, tokens, L.dim, 2, 2)) return fail(GPTQ_ERR_INVALID_ARG, "Y overlaps Q");
   if (meet(span_of(y, tokens, heads, L.dim, 2), Span{pages, L.page_bytes * num_pages}))
     return fail(GPTQ_ERR_INVALID_ARG, "Y overlaps the pages");
-  const KvAttentionPlan p = plan_kv_attention(L, heads, batch, tokens, max_queries);
+  const KvAttentionPlan p = plan_kv_attention(L, heads, batch, tokens, max_queries, table_width * cfg->page_size);
   if (workspace == nullptr || ws_bytes < p.total || bad_ptr(workspace, 256))
     return fail(GPTQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu (256-byte aligned)", ws_bytes, p.total);
   return run_kv_attention(L, heads, q, y, scale, s, pages, workspace, p, static_cast<hipStream_t>(stream));

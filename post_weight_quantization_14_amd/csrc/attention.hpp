@@ -161,11 +161,14 @@ gptq_status run_kv_read(const KvLayout& L, const HeadRows& K, const HeadRows& V,
 
 struct KvAttentionPlan {
   int tiles;          // 16-row tiles of queries that a workgroup holds: 1 or 2
-  int wgs;            // workgroups that the positions are split over
+  bool whole;         // a workgroup for each unit (row tile and key head of a sequence), not an equal piece of all
+  int wgs;            // workgroups
   int rows;           // rows of a unit that should hold queries
-  size_t partial, meta, total;   // workspace bytes
+  size_t partial, total;   // workspace bytes
 };
-KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, int64_t tokens, int64_t max_queries);
+// capacity: positions of a sequence that the page table can hold (no part in the workspace's size)
+KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, int64_t tokens, int64_t max_queries,
+                                  int64_t capacity);
 gptq_status run_kv_attention(const KvLayout& L, int heads, const HeadRows& Q, const HeadRows& Y, float scale,
                              const KvSeqs& q, const void* pages, void* ws, const KvAttentionPlan& p, hipStream_t stream);
 

@@ -13,9 +13,9 @@ namespace {
 #define INLINE __attribute__((always_inline))
 typedef __attribute__((address_space(4))) int32_t constant_int;
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kStep = 32;        // positions of a wave's step: two records
 constexpr float kNone = -3e38f;  // a running maximum that has seen nothing
+constexpr int kMaxWgs = 512;     // of a split call
 
 __device__ __forceinline__ float swap16(float x, float* y) {   // lane ^ 16
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -92,9 +92,11 @@ struct Work {
 
 // A unit is one row tile (R query rows: tokens x the heads that share a key
 // head) of one key head of one sequence; its steps are 32 positions each.  All
-// units' steps lie one after the other, by sequence, head and tile.  Lane i keeps
-// what it read of sequence i: batches of up to 64 are read once.
-template <int R>
+// units' steps lie one after the other, by sequence, head and tile (WHOLE: all
+// units, of one step each here).  Lane i keeps what it read of sequence i: batches of
+// up to 64 are read once.
+constexpr int kLeast = 4;   // steps that a workgroup takes at least: one for each wave
+template <int R, bool WHOLE>
 struct Units {
   const Work& w;
   int64_t capacity, total;
@@ -121,7 +123,7 @@ struct Units {
   static __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
   static __device__ __forceinline__ int64_t tiles(const KvSeq& s, int share) { return ((int64_t)s.n * share + R - 1) / R; }
   static __device__ __forceinline__ int steps(const KvSeq& s) { return s.len > kStep ? (int)(((int64_t)s.len + kStep - 1) / kStep) : 1; }
-  __device__ __forceinline__ int64_t steps_of(const KvSeq& s) const { return tiles(s, w.share) * steps(s) * w.L.heads; }
+  __device__ __forceinline__ int64_t steps_of(const KvSeq& s) const { return tiles(s, w.share) * (WHOLE ? 1 : steps(s)) * w.L.heads; }
   // the sequence that step `pos` belongs to, and which of its steps it is
   __device__ __forceinline__ KvSeq find(int64_t pos, int64_t* b, int64_t* at) const {
     if (few) {
@@ -181,21 +183,24 @@ __device__ __forceinline__ void value_pairs(const uint32_t (&w)[D / 32], int b, 
   }
 }
 
-template <int D, int G, int NT>
-__global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64_t min_piece) {
-  constexpr int R = 16 * NT, KS = D / 32, NG = D / G, MT = D / 16, PG = G / 32;   // PG: 32-channel steps of a group
+// W waves share a unit's steps.  WHOLE: a workgroup takes one unit; otherwise each
+// takes an equal piece of all units' steps, and units cut by a piece's end are
+// joined by kv_join_kernel.
+template <int D, int G, int NT, int W, bool WHOLE>
+__global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
+  constexpr int kThreads = 64 * W, R = 16 * NT, KS = D / 32, NG = D / G, MT = D / 16, PG = G / 32;   // PG: 32-channel steps of a group
   constexpr int kPitch = D + 4;
-  __shared__ float so[kWaves][16][kPitch];
-  __shared__ float sm[kWaves][16], sl[kWaves][16];
+  __shared__ float so[W][16][kPitch];
+  __shared__ float sm[W][16], sl[W][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n16 = lane & 15, kg = lane >> 4;
-  const Units<R> units(w);
+  const Units<R, WHOLE> units(w);
   const Consts kc;
 
-  const int64_t total = units.total, even = (total + gridDim.x - 1) / (int64_t)gridDim.x;
-  const int64_t piece = even > min_piece ? even : min_piece;
-  const int64_t begin = piece * blockIdx.x, end = begin + piece < total ? begin + piece : total;
-  if (tid == 0) w.meta[blockIdx.x].parts = 0;
+  // in steps, or in units where each is taken whole
+  const int64_t even = divide(units.total + gridDim.x - 1, gridDim.x), piece = WHOLE || even > kLeast ? even : kLeast;
+  const int64_t begin = piece * blockIdx.x, end = begin + piece < units.total ? begin + piece : units.total;
+  if (!WHOLE && tid == 0) w.meta[blockIdx.x].parts = 0;
   if (w.q.status)
     for (int64_t b = (int64_t)blockIdx.x * kThreads + tid; b < w.q.batch; b += (int64_t)gridDim.x * kThreads)
       if (kv_seq(w.q, b, units.capacity).bad) kv_bad(w.q.status);
@@ -203,15 +208,15 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
   for (int64_t pos = begin; pos < end;) {
     int64_t b = 0, at = 0;
     const KvSeq s = units.find(pos, &b, &at);
-    const int steps = Units<R>::steps(s);
-    const int64_t unit = divide(at, steps);                       // head · tiles + tile
-    const int s0 = (int)(at - unit * steps);
-    const int s1 = steps - s0 < end - pos ? steps : s0 + (int)(end - pos);
-    const int64_t tiles = Units<R>::tiles(s, w.share);
+    const int steps = units.steps(s);
+    const int64_t unit = WHOLE ? at : divide(at, steps);          // head · tiles + tile
+    const int s0 = WHOLE ? 0 : (int)(at - unit * steps);
+    const int s1 = WHOLE || steps - s0 < end - pos ? steps : s0 + (int)(end - pos);
+    const int64_t tiles = units.tiles(s, w.share);
     const int head = (int)divide(unit, tiles);
     const int64_t row0 = (unit - head * tiles) * R, tq0 = divide(row0, w.share);
     const uint32_t hq0 = (uint32_t)(row0 - tq0 * w.share);   // row0 is head hq0 of the group, token tq0
-    const int rows = (int)Units<R>::min64(R, (int64_t)s.n * w.share - row0);
+    const int rows = (int)units.min64(R, (int64_t)s.n * w.share - row0);
 
     // ---- queries: lane n16 of every quarter holds query row 16·nt + n16
     u32x4_t qx[NT][KS];
@@ -278,7 +283,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
     Pages ahead;
     if (some) {
       load(st, page_of(st), cur);
-      ahead = page_of(min(st + kWaves, s1 - 1));
+      ahead = page_of(min(st + W, s1 - 1));
     }
 
     bf16x8_t qf[NT][KS];
@@ -435,19 +440,19 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
     };
     if (some) {
       for (;;) {
-        load(min(st + kWaves, s1 - 1), ahead, nxt);
-        ahead = page_of(min(st + 2 * kWaves, s1 - 1));
+        load(min(st + W, s1 - 1), ahead, nxt);
+        ahead = page_of(min(st + 2 * W, s1 - 1));
         compute(st, cur);
-        if ((st += kWaves) >= s1) break;
-        load(min(st + kWaves, s1 - 1), ahead, cur);
-        ahead = page_of(min(st + 2 * kWaves, s1 - 1));
+        if ((st += W) >= s1) break;
+        load(min(st + W, s1 - 1), ahead, cur);
+        ahead = page_of(min(st + 2 * W, s1 - 1));
         compute(st, nxt);
-        if ((st += kWaves) >= s1) break;
+        if ((st += W) >= s1) break;
       }
     }
 
     // ---- the four waves' sums together, a tile of 16 rows at a time
-    const bool whole = s0 == 0 && s1 == steps;
+    const bool whole = WHOLE || (s0 == 0 && s1 == steps);
     const int slot = pos == begin ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1;
     float* part = w.partial + (int64_t)slot * R * (D + 2);
     if (!whole && s0 == 0 && tid == 0)
@@ -461,7 +466,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
       __syncthreads();
       float up = kNone;
 #pragma unroll
-      for (int v = 0; v < kWaves; ++v) up = fmaxf(up, sm[v][n16]);
+      for (int v = 0; v < W; ++v) up = fmaxf(up, sm[v][n16]);
       const float f = exp2f(m[nt] - up);
       if (kg == 0) sl[wave][n16] = l[nt] * f;
 #pragma unroll
@@ -476,7 +481,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
         float ll = 0.f;
         f32x4_t y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int v = 0; v < kWaves; ++v) {
+        for (int v = 0; v < W; ++v) {
           ll += sl[v][n];
           y += *reinterpret_cast<const f32x4_t*>(&so[v][n][d]);
         }
@@ -499,7 +504,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
           if (d == 0) {
             float top = kNone;
 #pragma unroll
-            for (int v = 0; v < kWaves; ++v) top = fmaxf(top, sm[v][n]);
+            for (int v = 0; v < W; ++v) top = fmaxf(top, sm[v][n]);
             part[R * D + nt * 16 + n] = top;
             part[R * D + R + nt * 16 + n] = ll;
           }
@@ -507,106 +512,137 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(Work w, int64
       }
       __syncthreads();
     }
-    pos += s1 - s0;
+    pos += WHOLE ? 1 : s1 - s0;
   }
 }
 
-// Joins the parts of units that were split.  A workgroup looks at four entries of
-// `meta`, four waves at each: they share the parts of a row, whose loads are all
-// in flight at once (a chain of loads, not their bytes, is what this costs).
+// Joins the parts of units that were split: a wave takes a row of a unit at a time.
+// The units are few and anywhere among `meta`, so each workgroup lists them first.
+// What this costs is a chain of loads, not their bytes: a row's parts are all in
+// flight at once, 64 at the most.
+constexpr int kJoinWgs = 512;
 template <int D, int R>
-__global__ __launch_bounds__(1024) void kv_join_kernel(Work w) {
-  constexpr int C = D / 64;
+__global__ __launch_bounds__(256) void kv_join_kernel(Work w, int wgs, int most_rows) {
   constexpr int64_t kSize = R * (D + 2);
-  __shared__ float sy[4][4][D], sw[4][4][2];
-  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), e = wave >> 2, q = wave & 3;
-  const int first = (int)blockIdx.x * 4 + e;
-  const Split u = w.meta[first];
-  const int parts = uniform(u.parts), rows = parts ? uniform(u.rows) : 0;
-  const float* p0 = w.partial + uniform(u.slot) * kSize;
-  const float* p1 = w.partial + 2 * (int64_t)first * kSize;
-  for (int row = (int)blockIdx.y; __syncthreads_or(row < rows); row += (int)gridDim.y) {
-    if (row < rows) {   // the wave's parts: q, q + 4, ..
-      float up = kNone, ll = 0.f, y[C];
+  constexpr int L4 = D / 4, P = 64 / L4;   // lanes of a row, four channels each; parts side by side
+  __shared__ int16_t list[kMaxWgs];
+  __shared__ int count[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  constexpr int E = kMaxWgs / 256;
+  int found = 0, parts_of[E];
 #pragma unroll
-      for (int c = 0; c < C; ++c) y[c] = 0.f;
-      for (int i0 = q; i0 < parts; i0 += 32) {
-        float m[8], l[8], v[8][C];
+  for (int e = 0; e < E; ++e) {
+    const int i = tid * E + e;
+    parts_of[e] = i < wgs ? w.meta[i].parts : 0;
+  }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = min(i0 + 4 * j, parts - 1);
+  for (int e = 0; e < E; ++e) found += parts_of[e] > 0;
+  const int before = (int)wave_scan(found);
+  if (lane == 63) count[wave] = before;
+  __syncthreads();
+  int at = before - found, all = 0;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (v < wave) at += count[v];
+    all += count[v];
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (parts_of[e] > 0) list[at++] = (int16_t)(tid * E + e);
+  __syncthreads();
+  const int c4 = lane % L4 * 4, side = lane / L4;
+  for (int pair = (int)blockIdx.x * 4 + wave; pair < uniform(all) * most_rows; pair += (int)gridDim.x * 4) {
+    const int first = uniform((int)list[pair / most_rows]);
+    const Split u = w.meta[first];
+    const int parts = uniform(u.parts);
+    const float* p0 = w.partial + uniform(u.slot) * kSize;
+    const float* p1 = w.partial + 2 * (int64_t)first * kSize;
+    for (int row = pair % most_rows; row < uniform(u.rows); row += most_rows) {
+      float up = kNone, ll = 0.f;
+      f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+      auto some = [&](auto n, int base) INLINE {   // parts base + P·j + side, j < N
+        constexpr int N = decltype(n)::value;
+        float m[N], l[N];
+        f32x4_t v[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int i = min(base + P * j + side, parts - 1);
           const float* p = i == 0 ? p0 : p1 + 2 * i * kSize;
           m[j] = p[R * D + row];
           l[j] = p[R * D + R + row];
-#pragma unroll
-          for (int c = 0; c < C; ++c) v[j][c] = p[row * D + lane * C + c];
+          v[j] = *reinterpret_cast<const f32x4_t*>(p + row * D + c4);
         }
         float top = up;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, m[j]);
+        for (int j = 0; j < N; ++j) top = fmaxf(top, m[j]);
+#pragma unroll
+        for (int d = L4; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
         const float f = exp2f(up - top);
         up = top;
         ll *= f;
+        y *= f;
 #pragma unroll
-        for (int c = 0; c < C; ++c) y[c] *= f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const bool there = i0 + 4 * j < parts;
-          const float g = there ? exp2f(m[j] - up) : 0.f;
-          ll += there ? l[j] * g : 0.f;
-#pragma unroll
-          for (int c = 0; c < C; ++c) y[c] += there ? v[j][c] * g : 0.f;
+        for (int j = 0; j < N; ++j) {
+          const float g = exp2f(m[j] - up);
+          if (base + P * j + side < parts) {
+            ll = fmaf(l[j], g, ll);
+            y += v[j] * g;
+          }
         }
+      };
+      if (parts <= 4 * P)
+        some(std::integral_constant<int, 4>{}, 0);
+      else
+        for (int base = 0; base < parts; base += 16 * P) some(std::integral_constant<int, 16>{}, base);
+#pragma unroll
+      for (int d = L4; d < 64; d <<= 1) {
+        ll += __shfl_xor(ll, d);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] += __shfl_xor(y[c], d);
       }
-#pragma unroll
-      for (int c = 0; c < C; ++c) sy[e][q][lane * C + c] = y[c];
-      if (lane == 0) sw[e][q][0] = up, sw[e][q][1] = ll;
-    }
-    __syncthreads();
-    if (row < rows && q == 0) {
-      float up = kNone, ll = 0.f, y[C];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) up = fmaxf(up, sw[e][i][0]);
-#pragma unroll
-      for (int c = 0; c < C; ++c) y[c] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float f = exp2f(sw[e][i][0] - up);
-        ll = fmaf(sw[e][i][1], f, ll);
-#pragma unroll
-        for (int c = 0; c < C; ++c) y[c] = fmaf(sy[e][i][lane * C + c], f, y[c]);
-      }
+      if (side) continue;
       const float inv = ll == 0.f ? 0.f : 1.f / ll;   // a row that sees nothing
       const uint32_t i = uniform((int)u.hq0) + row, t = w.share == 1 ? i : __umulhi(i, w.share_inv);
       uint16_t* yp = const_cast<uint16_t*>(static_cast<const uint16_t*>(w.Y.p)) + (u.token + t) * w.Y.ld +
-                     (u.head * w.share + (i - t * w.share)) * w.Y.hs + lane * C;
+                     (u.head * w.share + (i - t * w.share)) * w.Y.hs + c4;
 #pragma unroll
-      for (int c = 0; c < C; ++c) yp[c] = __builtin_bit_cast(uint16_t, (__bf16)(y[c] * inv));
+      for (int c = 0; c < 4; ++c) yp[c] = __builtin_bit_cast(uint16_t, (__bf16)(y[c] * inv));
     }
   }
 }
 
 template <int D, int G, int NT>
 gptq_status launch(const Work& w, const KvAttentionPlan& p, hipStream_t stream) {
-  kv_attention_kernel<D, G, NT><<<p.wgs, kThreads, 0, stream>>>(w, 4);
+  if (p.whole) {
+    kv_attention_kernel<D, G, NT, 8, true><<<p.wgs, 512, 0, stream>>>(w);
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+  }
+  kv_attention_kernel<D, G, NT, 4, false><<<p.wgs, 256, 0, stream>>>(w);
   GPTQ_LAUNCH_CHECK();
-  kv_join_kernel<D, 16 * NT><<<dim3(p.wgs / 4, p.rows), 1024, 0, stream>>>(w);
+  kv_join_kernel<D, 16 * NT><<<kJoinWgs, 256, 0, stream>>>(w, p.wgs, p.rows);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
 
 }  // namespace
 
-KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, int64_t tokens, int64_t max_queries) {
+// Positions of the longest sequence that the page table can hold up to which a
+// unit is one workgroup's.
+constexpr int64_t kWhole = 2048;
+
+KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, int64_t tokens, int64_t max_queries,
+                                  int64_t capacity) {
   KvAttentionPlan p;
-  const int64_t rows = std::min(std::max<int64_t>(max_queries, 1), std::max<int64_t>(tokens, 1)) * (heads / L.heads);
+  const int64_t share = heads / L.heads;
+  const int64_t rows = std::min(std::max<int64_t>(max_queries, 1), std::max<int64_t>(tokens, 1)) * share;
   p.tiles = rows > 16 ? 2 : 1;
-  p.wgs = 512;
   p.rows = (int)std::min<int64_t>(rows, 16 * p.tiles);
-  p.partial = (size_t)2 * p.wgs * 16 * p.tiles * (L.dim + 2) * 4;
-  p.meta = (size_t)p.wgs * sizeof(Split);
-  p.total = align256(p.partial) + p.meta;
-  (void)batch;
+  p.whole = capacity <= kWhole;
+  const int64_t units = L.heads * (tokens * share / (16 * p.tiles) + std::min(batch, tokens));   // at the most
+  p.wgs = (int)(p.whole ? std::min<int64_t>(units, INT32_MAX) : kMaxWgs);
+  p.partial = (size_t)2 * kMaxWgs * 16 * p.tiles * (L.dim + 2) * 4;
+  p.total = align256(p.partial) + (size_t)kMaxWgs * sizeof(Split);
   return p;
 }
 
