@@ -104,14 +104,26 @@ __device__ __forceinline__ KvSeq uniform(const KvSeq& s) {
   return KvSeq{uniform(s.row), uniform(s.n), uniform(s.len), uniform((int)s.bad) != 0};
 }
 
-__device__ __forceinline__ int64_t wave_scan(int64_t v) {   // sum over lanes 0 .. this one
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
+// sum over lanes 0 .. this one
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+  auto add = [&](auto ctrl, auto rows) {   // lanes of `rows` add what DPP `ctrl` brings them
+    constexpr int C = decltype(ctrl)::value, M = decltype(rows)::value;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, C, M, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(v >> 32), C, M, 0xf, false);
+    v += (int64_t)((uint64_t)hi << 32 | lo);
+  };
+  using std::integral_constant;
+  add(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});   // 1, 2, 4, 8 lanes before, in rows of 16
+  add(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+  add(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+  add(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+  add(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});   // the row before's last lane, to rows 1 and 3
+  add(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});   // lane 31, to rows 2 and 3
   return v;
+}
+// a value of lane l, the same l in all
+__device__ __forceinline__ int64_t lane_value(int64_t v, int l) {
+  return (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)v, l) | (int64_t)__builtin_amdgcn_readlane((int)(v >> 32), l) << 32;
 }
 
 // The sum of count(b) over the batch.  Called by whole waves.
@@ -119,9 +131,7 @@ template <class F>
 __device__ __forceinline__ int64_t ragged_total(int64_t batch, const F& count) {
   int64_t v = 0;
   for (int64_t b = threadIdx.x & 63; b < batch; b += 64) v += count(b);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+  return lane_value(wave_scan(v), 63);
 }
 
 // The sequence b in whose count(b) pieces the `index`-th piece of all lies, and
@@ -138,10 +148,10 @@ __device__ __forceinline__ bool ragged_find(int64_t index, int64_t batch, const 
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
       *b = base + l;
-      *at = index - uniform(__shfl(upto - c, l));
+      *at = index - lane_value(upto - c, l);
       return true;
     }
-    index -= uniform(__shfl(upto, 63));
+    index -= lane_value(upto, 63);
   }
   return false;
 }

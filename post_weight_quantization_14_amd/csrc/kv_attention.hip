@@ -115,9 +115,9 @@ struct Units {
         own = steps_of(mine);
       }
       upto = wave_scan(own);
-      total = uniform(__shfl(upto, 63));
+      total = lane_value(upto, 63);
     } else {
-      total = uniform(ragged_total(w.q.batch, [&](int64_t b) { return steps_of(kv_seq(w.q, b, capacity)); }));
+      total = ragged_total(w.q.batch, [&](int64_t b) { return steps_of(kv_seq(w.q, b, capacity)); });
     }
   }
   static __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -129,15 +129,12 @@ struct Units {
     if (few) {
       const int l = __ffsll((unsigned long long)__ballot(upto > pos)) - 1;
       *b = l;
-      *at = pos - lane_of(upto - own, l);
-      return KvSeq{lane_of(mine.row, l), __builtin_amdgcn_readlane(mine.n, l), __builtin_amdgcn_readlane(mine.len, l),
+      *at = pos - lane_value(upto - own, l);
+      return KvSeq{lane_value(mine.row, l), __builtin_amdgcn_readlane(mine.n, l), __builtin_amdgcn_readlane(mine.len, l),
                    __builtin_amdgcn_readlane((int)mine.bad, l) != 0};
     }
     ragged_find(pos, w.q.batch, [&](int64_t i) { return steps_of(kv_seq(w.q, i, capacity)); }, b, at);
     return uniform(kv_seq(w.q, *b, capacity));
-  }
-  static __device__ __forceinline__ int64_t lane_of(int64_t v, int l) {
-    return (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)v, l) | (int64_t)__builtin_amdgcn_readlane((int)(v >> 32), l) << 32;
   }
 };
 
@@ -198,7 +195,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
   const Consts kc;
 
   // in steps, or in units where each is taken whole
-  const int64_t even = divide(units.total + gridDim.x - 1, gridDim.x), piece = WHOLE || even > kLeast ? even : kLeast;
+  const int64_t even = divide(units.total + gridDim.x - 1, gridDim.x), piece = WHOLE ? 1 : even > kLeast ? even : kLeast;
   const int64_t begin = piece * blockIdx.x, end = begin + piece < units.total ? begin + piece : units.total;
   if (!WHOLE && tid == 0) w.meta[blockIdx.x].parts = 0;
   if (w.q.status)
