@@ -763,6 +763,8 @@ def gptq_w4a16_moe(X: torch.Tensor, router: torch.Tensor, packed: torch.Tensor, 
 
 
 # ---------------------------------------------------------------- attention and its 4-bit cache
+# These calls are made for every layer of every token: a call's checks read each
+# attribute once.
 @dataclass(frozen=True)
 class KvConfig:
     """A key/value cache held in 4 bits: heads and channels of its keys, the
@@ -776,43 +778,73 @@ class KvConfig:
         c = _lib.GptqKvConfig(self.kv_heads, self.head_dim, self.group_size, self.page_size)
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_ref", ctypes.byref(c))
+        object.__setattr__(self, "_page_bytes", None)
 
     def c(self) -> "_lib.GptqKvConfig":
         return self._c
 
 
+def gptq_kv_page_bytes(cfg: KvConfig) -> int:
+    if cfg._page_bytes is None:
+        object.__setattr__(cfg, "_page_bytes", int(lib().gptq_kv_page_bytes(cfg._ref)))
+    return cfg._page_bytes
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _heads(name: str, t: torch.Tensor, tokens: int, heads: int, dim: int) -> tuple:
     """(token stride, head stride) of a [tokens, heads, dim] tensor."""
-    if t.dim() != 3 or tuple(t.shape) != (tokens, heads, dim) or (t.stride(2) != 1 and tokens > 0):
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}] with unit stride in its last dimension")
-    return t.stride(0), t.stride(1)
+    if t.shape != (tokens, heads, dim):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}]")
+    ld, hs, one = t.stride()
+    if one != 1 and tokens > 0:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return ld, hs
 
 
-def _sequences(X: torch.Tensor, pages: torch.Tensor, page_bytes: int, page_table: torch.Tensor, kv_lens: torch.Tensor,
-               cu_seqlens: Optional[torch.Tensor], status: Optional[torch.Tensor], **more) -> tuple:
+def _sequences(cfg: KvConfig, X: torch.Tensor, other: Optional[torch.Tensor], pages: torch.Tensor,
+               page_table: torch.Tensor, kv_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor],
+               status: Optional[torch.Tensor]) -> tuple:
     """The sequences of a call as the C entry points take them: cu_seqlens,
-    kv_lens, page_table, batch, its width and row stride, pages, their number."""
-    _on(X, pages=pages, page_table=page_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens, status=status, **more)
+    kv_lens, page_table, batch, its width and row stride, pages, their number;
+    and status."""
+    dev = X.get_device()
+    if not (0 <= dev == pages.get_device() == page_table.get_device() == kv_lens.get_device()
+            and (cu_seqlens is None or cu_seqlens.get_device() == dev) and (other is None or other.get_device() == dev)
+            and (status is None or status.get_device() == dev)):
+        _on(X, pages=pages, page_table=page_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens, output=other, status=status)
+    page_bytes = cfg._page_bytes or gptq_kv_page_bytes(cfg)
     if page_bytes <= 0:
         raise ValueError("the cache's config is not supported (gptq_kv_page_bytes is 0)")
     batch = kv_lens.shape[0]
-    if kv_lens.dtype != torch.int32 or kv_lens.dim() != 1 or not kv_lens.is_contiguous():
+    if kv_lens.dtype is not torch.int32 or kv_lens.dim() != 1 or not kv_lens.is_contiguous():
         raise ValueError("kv_lens must be a contiguous int32 [batch]")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != batch or (
-            page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    shape, ld = page_table.shape, page_table.stride()
+    if page_table.dtype is not torch.int32 or len(shape) != 2 or shape[0] != batch or (shape[1] > 1 and ld[1] != 1):
         raise ValueError(f"page_table must be int32 [{batch}, pages of a sequence] with contiguous rows")
-    if cu_seqlens is not None and (cu_seqlens.dtype != torch.int32 or tuple(cu_seqlens.shape) != (batch + 1,)
-                                   or not cu_seqlens.is_contiguous()):
-        raise ValueError(f"cu_seqlens must be a contiguous int32 [{batch + 1}]")
-    if status is not None and (status.dtype != torch.int32 or status.numel() != 1):
-        raise ValueError("status must be one int32")
-    return (_ptr(cu_seqlens), kv_lens.data_ptr(), page_table.data_ptr(), batch, page_table.shape[1],
-            page_table.stride(0) if batch > 1 else page_table.shape[1], pages.data_ptr(),
-            _uint8("pages", pages) // page_bytes)
+    cu = None
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype is not torch.int32 or cu_seqlens.shape != (batch + 1,) or not cu_seqlens.is_contiguous():
+            raise ValueError(f"cu_seqlens must be a contiguous int32 [{batch + 1}]")
+        cu = cu_seqlens.data_ptr()
+    st = None
+    if status is not None:
+        if status.dtype is not torch.int32 or status.numel() != 1:
+            raise ValueError("status must be one int32")
+        st = status.data_ptr()
+    if not pages.is_contiguous():
+        raise ValueError("pages must be contiguous")
+    return (cu, kv_lens.data_ptr(), page_table.data_ptr(), batch, shape[1], ld[0] if batch > 1 else shape[1],
+            pages.data_ptr(), pages.nbytes // page_bytes), st
 
 
-def gptq_kv_page_bytes(cfg: KvConfig) -> int:
-    return int(lib().gptq_kv_page_bytes(cfg._ref))
+def _run_on(X: torch.Tensor, fn, args: tuple) -> int:
+    """fn(*args) with X's GPU as the current device."""
+    if X.get_device() == _current_device():
+        return fn(*args)
+    with _Device(X):
+        return fn(*args)
 
 
 def gptq_kv_append(cfg: KvConfig, K: torch.Tensor, V: torch.Tensor, pages: torch.Tensor, page_table: torch.Tensor,
@@ -825,13 +857,13 @@ def gptq_kv_append(cfg: KvConfig, K: torch.Tensor, V: torch.Tensor, pages: torch
     tokens = K.shape[0]
     kld, khs = _heads("K", K, tokens, cfg.kv_heads, cfg.head_dim)
     vld, vhs = _heads("V", V, tokens, cfg.kv_heads, cfg.head_dim)
-    if K.dtype != V.dtype:
+    if K.dtype is not V.dtype:
         raise TypeError("K and V must have one dtype")
-    seqs = _sequences(K, pages, gptq_kv_page_bytes(cfg), page_table, kv_lens, cu_seqlens, status, V=V)
-    with _device(K):
-        st = lib().gptq_kv_append(cfg._ref, K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kld, khs, vld, vhs, *seqs,
-                                  _ptr(status), _stream_on(K, stream))
-    _check(st, "gptq_kv_append")
+    seqs, status = _sequences(cfg, K, V, pages, page_table, kv_lens, cu_seqlens, status)
+    st = _run_on(K, lib().gptq_kv_append, (cfg._ref, K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kld, khs, vld, vhs,
+                                           *seqs, status, _stream_on(K, stream)))
+    if st:
+        _check(st, "gptq_kv_append")
 
 
 def gptq_kv_read(cfg: KvConfig, pages: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, tokens: int,
@@ -841,19 +873,20 @@ def gptq_kv_read(cfg: KvConfig, pages: torch.Tensor, page_table: torch.Tensor, k
     """(K, V) [tokens, kv_heads, head_dim], bf16 or fp32: the last
     cu_seqlens[b + 1] - cu_seqlens[b] positions of each sequence (None: the last
     one), as the cache keeps them."""
+    shape = (tokens, cfg.kv_heads, cfg.head_dim)
     if K is None:
-        K = _empty((tokens, cfg.kv_heads, cfg.head_dim), out_dtype, pages, stream)
+        K = _empty(shape, out_dtype, pages, stream)
     if V is None:
-        V = _empty((tokens, cfg.kv_heads, cfg.head_dim), K.dtype, pages, stream)
-    kld, khs = _heads("K", K, tokens, cfg.kv_heads, cfg.head_dim)
-    vld, vhs = _heads("V", V, tokens, cfg.kv_heads, cfg.head_dim)
-    if K.dtype != V.dtype:
+        V = _empty(shape, K.dtype, pages, stream)
+    kld, khs = _heads("K", K, *shape)
+    vld, vhs = _heads("V", V, *shape)
+    if K.dtype is not V.dtype:
         raise TypeError("K and V must have one dtype")
-    seqs = _sequences(K, pages, gptq_kv_page_bytes(cfg), page_table, kv_lens, cu_seqlens, status, V=V)
-    with _device(K):
-        st = lib().gptq_kv_read(cfg._ref, K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kld, khs, vld, vhs, *seqs,
-                                _ptr(status), _stream_on(K, stream))
-    _check(st, "gptq_kv_read")
+    seqs, status = _sequences(cfg, K, V, pages, page_table, kv_lens, cu_seqlens, status)
+    st = _run_on(K, lib().gptq_kv_read, (cfg._ref, K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kld, khs, vld, vhs,
+                                         *seqs, status, _stream_on(K, stream)))
+    if st:
+        _check(st, "gptq_kv_read")
     return K, V
 
 
@@ -872,28 +905,38 @@ def gptq_kv_attention(cfg: KvConfig, Q: torch.Tensor, pages: torch.Tensor, page_
     in this call as far as it is known (None: every token may be of one).  scale:
     1/sqrt(head_dim) if None.  Without a workspace, or with one that is too
     small, the call allocates its own."""
-    tokens, heads = Q.shape[0], Q.shape[1]
-    qld, qhs = _heads("Q", Q, tokens, heads, cfg.head_dim)
-    if Q.dtype != torch.bfloat16:
+    dim = cfg.head_dim
+    if Q.dim() != 3:
+        raise ValueError(f"Q must be [tokens, heads, {dim}]")
+    tokens, heads, _ = shape = tuple(Q.shape)
+    qld, qhs = _heads("Q", Q, tokens, heads, dim)
+    if Q.dtype is not torch.bfloat16:
         raise TypeError(f"Q must be bfloat16, not {Q.dtype}")
-    seqs = _sequences(Q, pages, gptq_kv_page_bytes(cfg), page_table, kv_lens, cu_seqlens, status, Y=Y,
-                      workspace=workspace)
+    seqs, status = _sequences(cfg, Q, Y, pages, page_table, kv_lens, cu_seqlens, status)
     if Y is None:
-        Y = _empty((tokens, heads, cfg.head_dim), torch.bfloat16, Q, stream)
-    yld, yhs = _heads("Y", Y, tokens, heads, cfg.head_dim)
-    if Y.dtype != torch.bfloat16:
-        raise TypeError(f"Y must be bfloat16, not {Y.dtype}")
+        Y = _empty(shape, torch.bfloat16, Q, stream)
+        yld, yhs = heads * dim, dim
+    else:
+        yld, yhs = _heads("Y", Y, tokens, heads, dim)
+        if Y.dtype is not torch.bfloat16:
+            raise TypeError(f"Y must be bfloat16, not {Y.dtype}")
     if max_queries is None:
         max_queries = 1 if cu_seqlens is None else tokens
-    cu, lens, table, batch, width, stride, pp, npages = seqs
     fn = lib().gptq_kv_attention
-    args = (cfg._ref, Q.data_ptr(), tokens, heads, qld, qhs, cu, max_queries, lens, table, batch, width, stride, pp, npages,
-            cfg.head_dim ** -0.5 if scale is None else scale, Y.data_ptr(), yld, yhs, _ptr(status))
+    args = (cfg._ref, Q.data_ptr(), tokens, heads, qld, qhs, seqs[0], max_queries, *seqs[1:],
+            dim ** -0.5 if scale is None else scale, Y.data_ptr(), yld, yhs, status)
     s = _stream_on(Q, stream)
-    with _device(Q):
-        _with_workspace(lambda ws, nbytes: fn(*args, ws, nbytes, s),
-                        lambda: gptq_kv_attention_workspace_bytes(cfg, heads, batch, tokens, max_queries), Q, workspace,
-                        stream, "gptq_kv_attention")
+    st = _lib.GPTQ_ERR_WORKSPACE
+    if workspace is not None:
+        if workspace.get_device() != Q.get_device():
+            raise ValueError(f"workspace is on {workspace.device}, Q on {Q.device}")
+        st = _run_on(Q, fn, (*args, workspace.data_ptr(), _uint8("workspace", workspace), s))
+    if st == _lib.GPTQ_ERR_WORKSPACE:
+        nbytes = max(gptq_kv_attention_workspace_bytes(cfg, heads, seqs[3], tokens, max_queries), 1)
+        ws = _empty(nbytes, torch.uint8, Q, stream)
+        st = _run_on(Q, fn, (*args, ws.data_ptr(), nbytes, s))
+    if st:
+        _check(st, "gptq_kv_attention")
     return Y
 
 
@@ -903,25 +946,31 @@ def gptq_prompt_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_
     (rows cu_seqlens[b] .. cu_seqlens[b + 1]) of Q [tokens, heads, head_dim] and
     K, V [tokens, kv_heads, head_dim], all bf16; heads / kv_heads query heads
     read one key head.  scale: 1/sqrt(head_dim) if None."""
-    tokens, heads, dim = Q.shape
-    kv_heads = K.shape[1] if K.dim() == 3 else 0
+    if Q.dim() != 3 or K.dim() != 3:
+        raise ValueError("Q and K must be [tokens, heads, head_dim]")
+    tokens, heads, dim = shape = tuple(Q.shape)
+    kv_heads = K.shape[1]
     qld, qhs = _heads("Q", Q, tokens, heads, dim)
     kld, khs = _heads("K", K, tokens, kv_heads, dim)
     vld, vhs = _heads("V", V, tokens, kv_heads, dim)
-    _on(Q, K=K, V=V, cu_seqlens=cu_seqlens, Y=Y)
+    dev = Q.get_device()
+    if not (0 <= dev == K.get_device() == V.get_device() == cu_seqlens.get_device() and (Y is None or Y.get_device() == dev)):
+        _on(Q, K=K, V=V, cu_seqlens=cu_seqlens, Y=Y)
     if Y is None:
-        Y = _empty((tokens, heads, dim), torch.bfloat16, Q, stream)
-    yld, yhs = _heads("Y", Y, tokens, heads, dim)
-    if not Q.dtype == K.dtype == V.dtype == Y.dtype == torch.bfloat16:
+        Y = _empty(shape, torch.bfloat16, Q, stream)
+        yld, yhs = heads * dim, dim
+    else:
+        yld, yhs = _heads("Y", Y, tokens, heads, dim)
+    if not Q.dtype is K.dtype is V.dtype is Y.dtype is torch.bfloat16:
         raise TypeError("Q, K, V and Y must be bfloat16")
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
+    if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be a contiguous int32 [sequences + 1]")
-    with _device(Q):
-        st = lib().gptq_prompt_attention(Q.data_ptr(), K.data_ptr(), V.data_ptr(), tokens, heads, kv_heads, dim, qld, qhs,
-                                         kld, khs, vld, vhs, cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1,
-                                         dim ** -0.5 if scale is None else scale, Y.data_ptr(), yld, yhs,
-                                         _stream_on(Q, stream))
-    _check(st, "gptq_prompt_attention")
+    st = _run_on(Q, lib().gptq_prompt_attention,
+                 (Q.data_ptr(), K.data_ptr(), V.data_ptr(), tokens, heads, kv_heads, dim, qld, qhs, kld, khs, vld, vhs,
+                  cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, dim ** -0.5 if scale is None else scale, Y.data_ptr(),
+                  yld, yhs, _stream_on(Q, stream)))
+    if st:
+        _check(st, "gptq_prompt_attention")
     return Y
 
 
