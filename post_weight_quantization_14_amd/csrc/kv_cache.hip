@@ -20,16 +20,12 @@ constexpr int kThreads = 256;
 // ---------------------------------------------------------------- grid
 struct Grid {
   float s, inv;
-  int z;
 };
 
-// Both decisions that decide a code are made exactly.  s: the guess (a little
+// Both decisions that decide a code are made exactly.  s here: the guess (a little
 // low, then cut to bf16 from above) is the wanted bf16 or the one below it, and
 // 64-bit arithmetic tells which: 15·s and 4096·s are exact, hi - lo is rounded
-// once in 53 bits.  x/s: q = x·inv is off by at most 2 units of 2^-23, so the
-// integer next to it is the nearest of x/s or, near a tie, its neighbour; the
-// remainder x - r·s (exact by one fused step: r·s has 21 bits and x lies
-// within a factor of two of it, or r is 0) tells.
+// once in 53 bits.
 __device__ __forceinline__ Grid make_grid(float lo, float hi, uint32_t top) {
   Grid g;
   const float a = __uint_as_float(top);
@@ -38,24 +34,43 @@ __device__ __forceinline__ Grid make_grid(float lo, float hi, uint32_t top) {
   const double range = (double)hi - (double)lo;
   const double sd = (double)__uint_as_float(bits);
   if (sd * 15. < range || sd * 4096. < (double)a) bits += 0x10000u;
+  if (!(top <= 0x5f800000u)) bits = 0x7fc00000u;   // 2^64; NaN and Inf have larger bits
   g.s = __uint_as_float(bits);
-  g.inv = 1.f / g.s;
-  g.z = 0;
-  if (!(top <= 0x5f800000u)) {   // 2^64; NaN and Inf have larger bits
-    g.s = __uint_as_float(0x7fc00000u);
-    g.inv = 0.f;
-  }
+  g.inv = __builtin_amdgcn_rcpf(g.s);
   return g;
 }
 
-// rint(x/s), ties to even
-__device__ __forceinline__ int steps(float x, const Grid& g) {
+// rint(x/s), ties to even, plus 0x4b400000 (NaN: anything).  |x/s| <= 4096, and
+// x·inv is off by at most 2 units of 2^-23.
+//   bf16 x: one correction by the remainder.  At a tie x/s is representable, so the
+// remainder is exact and the corrected quotient is the tie itself; off a tie x/s is
+// at least 2^-9 (of 1 or of itself) away from it, as x and s have eight bits, and the
+// error is below 2^-11.  Adding 1.5·2^23 rounds to an integer, in the low bits.
+__device__ __forceinline__ uint32_t steps(float x, const Grid& g, uint16_t) {
+  const float q = x * g.inv;
+  return __float_as_uint(fmaf(fmaf(-q, g.s, x), g.inv, q) + 12582912.f);
+}
+//   fp32 x: the integer next to x·inv is the nearest of x/s or, near a tie, its
+// neighbour; the remainder x - r·s (exact by one fused step: r·s has 21 bits and
+// x lies within a factor of two of it, or r is 0) tells.
+__device__ __forceinline__ uint32_t steps(float x, const Grid& g, float) {
   float r = rintf(x * g.inv);
   const float t = fmaf(-r, g.s, x), half = 0.5f * g.s;
   const bool odd = (int)r & 1;
   if (t > half || (t == half && odd)) r += 1.f;
   if (t < -half || (t == -half && odd)) r -= 1.f;
-  return (int)r;
+  return __float_as_uint(r + 12582912.f);
+}
+
+// with the lanes that share a group (4, 8 or 16 neighbours), by DPP: quads, then
+// halves of rows and rows mirrored, whose lanes agree within quads by then
+template <int N, class F>
+__device__ __forceinline__ uint32_t among(uint32_t x, const F& f) {
+  x = f(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xb1, 0xf, 0xf, true));
+  x = f(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4e, 0xf, 0xf, true));
+  if constexpr (N > 4) x = f(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x141, 0xf, 0xf, true));
+  if constexpr (N > 8) x = f(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x140, 0xf, 0xf, true));
+  return x;
 }
 
 template <int D, int G>
@@ -202,19 +217,16 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvLayout L, HeadRow
       hi = fmaxf(hi, x[i]);
       top = std::max(top, __float_as_uint(x[i]) & 0x7fffffffu);
     }
-#pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) {
-      lo = fminf(lo, __shfl_xor(lo, d));
-      hi = fmaxf(hi, __shfl_xor(hi, d));
-      top = std::max(top, (uint32_t)__shfl_xor((int)top, d));
-    }
-    Grid g = make_grid(lo, hi, top);
-    g.z = -steps(lo, g);
+    auto f32 = [](uint32_t u) { return __uint_as_float(u); };
+    lo = f32(among<kLanes>(__float_as_uint(lo), [&](uint32_t a, uint32_t b) { return __float_as_uint(fminf(f32(a), f32(b))); }));
+    hi = f32(among<kLanes>(__float_as_uint(hi), [&](uint32_t a, uint32_t b) { return __float_as_uint(fmaxf(f32(a), f32(b))); }));
+    top = among<kLanes>(top, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+    const Grid g = make_grid(lo, hi, top);
     const bool nan = g.s != g.s;
-    if (nan) g.z = 0;
+    const int z = nan ? 0 : 0x4b400000 - (int)steps(lo, g, T{}), shift = z - 0x4b400000;
     int c[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = nan ? 0 : std::min(std::max(steps(x[i], g) + g.z, 0), 15);
+    for (int i = 0; i < 8; ++i) c[i] = std::min(std::max((int)steps(x[i], g, T{}) + shift, 0), 15);   // NaN: any code
     if (v == 0) {
       uint32_t w = 0;
 #pragma unroll
@@ -226,7 +238,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvLayout L, HeadRow
         reinterpret_cast<uint8_t*>(rec)[R::value_byte(t, j, b)] = (uint8_t)(c[2 * b] | c[2 * b + 1] << 4);
     }
     if (j % kLanes == 0)
-      rec[R::param_word(v, t, j / kLanes)] = __float_as_uint(g.s) | (uint32_t)(uint16_t)(int16_t)g.z;
+      rec[R::param_word(v, t, j / kLanes)] = __float_as_uint(g.s) | (uint32_t)(uint16_t)(int16_t)z;
   }
   __syncthreads();
   uint8_t* out = pages + (k.page * L.heads + head) * L.recs * (int64_t)(R::kWords * 4) +
