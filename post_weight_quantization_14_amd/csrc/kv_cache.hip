@@ -98,32 +98,31 @@ struct Rec {
   }
 };
 
+// eight neighbouring channels, as they lie in memory and as numbers
 template <class T>
-__device__ __forceinline__ void load8(const T* p, bool vec, float (&x)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, bool vec, float (&x)[8]) {
-  if (vec) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
+struct Eight {
+  u32x4_t w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, bool vec) {
+    if (vec) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = p[i];
-  }
-}
-template <>
-__device__ __forceinline__ void load8<uint16_t>(const uint16_t* p, bool vec, float (&x)[8]) {
-  if (vec) {
-    const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p);
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const u32x4_t*>(p)[i];
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(a[i] << 16);
-      x[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(T) == 4)
+          w[i / 4][i % 4] = __float_as_uint(p[i]);
+        else
+          w[0][i / 2] = (i & 1 ? w[0][i / 2] : 0u) | (uint32_t)p[i] << (16 * (i & 1));
+      }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float((uint32_t)p[i] << 16);
   }
-}
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4)
+      return __uint_as_float(w[i / 4][i % 4]);
+    else
+      return __uint_as_float(i & 1 ? w[0][i / 2] & 0xffff0000u : w[0][i / 2] << 16);
+  }
+};
 
 // A sequence whose tokens all have a position: one with fewer positions than
 // tokens is out of range here.
@@ -192,23 +191,27 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvLayout L, HeadRow
   if (head == 0 && q.status) report(q, L);
   Block k;
   if (!find_block(q, L, &k)) return;
+  constexpr int kItems = 2 * kKvRec * R::kChunks / kThreads, kLanes = G / 8;
+  Eight<T> raw[kItems];
+#pragma unroll
+  for (int n = 0; n < kItems; ++n) {   // all in flight at once
+    const int it = n * kThreads + tid, v = it / (kKvRec * R::kChunks), t = it / R::kChunks % kKvRec, j = it % R::kChunks;
+    // positions that are not the call's: its nearest token once more, not written
+    const int p = min(max(k.blk * kKvRec + t, k.p0), k.p1 - 1);
+    const HeadRows& X = v ? V : K;
+    const int64_t row = k.s.row + (p - (k.s.len - k.s.n));
+    raw[n].load(static_cast<const T*>(X.p) + row * X.ld + head * X.hs + j * 8, X.vec);
+  }
   if (k.page < 0) {
     if (tid == 0) kv_bad(q.status);
     return;
   }
-  constexpr int kItems = 2 * kKvRec * R::kChunks, kLanes = G / 8;
 #pragma unroll
-  for (int it = tid; it < kItems; it += kThreads) {
-    const int v = it / (kKvRec * R::kChunks), t = it / R::kChunks % kKvRec, j = it % R::kChunks;
-    const int p = k.blk * kKvRec + t;
+  for (int n = 0; n < kItems; ++n) {
+    const int it = n * kThreads + tid, v = it / (kKvRec * R::kChunks), t = it / R::kChunks % kKvRec, j = it % R::kChunks;
     float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (p >= k.p0 && p < k.p1) {
-      const HeadRows& X = v ? V : K;
-      const int64_t row = k.s.row + (p - (k.s.len - k.s.n));
-      load8(static_cast<const T*>(X.p) + row * X.ld + head * X.hs + j * 8, X.vec, x);
-    }
+    for (int i = 0; i < 8; ++i) x[i] = raw[n].at(i);
     float lo = x[0], hi = x[0];
     uint32_t top = 0;
 #pragma unroll
