@@ -186,81 +186,95 @@ template <int D, int G, class T>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvLayout L, HeadRows K, HeadRows V, KvSeqs q,
                                                              uint8_t* __restrict__ pages) {
   using R = Rec<D, G>;
-  __shared__ __attribute__((aligned(16))) uint32_t rec[R::kWords];
-  const int tid = threadIdx.x, head = blockIdx.y;
-  if (head == 0 && q.status) report(q, L);
+  __shared__ __attribute__((aligned(16))) uint32_t recs[2][R::kWords];   // of this head and, while it leaves, of the next
+  const int tid = threadIdx.x;
+  if (blockIdx.y == 0 && q.status) report(q, L);
   Block k;
   if (!find_block(q, L, &k)) return;
   constexpr int kItems = 2 * kKvRec * R::kChunks / kThreads, kLanes = G / 8;
-  Eight<T> raw[kItems];
+  const T* src[kItems];
 #pragma unroll
-  for (int n = 0; n < kItems; ++n) {   // all in flight at once
+  for (int n = 0; n < kItems; ++n) {
     const int it = n * kThreads + tid, v = it / (kKvRec * R::kChunks), t = it / R::kChunks % kKvRec, j = it % R::kChunks;
     // positions that are not the call's: its nearest token once more, not written
     const int p = min(max(k.blk * kKvRec + t, k.p0), k.p1 - 1);
     const HeadRows& X = v ? V : K;
-    const int64_t row = k.s.row + (p - (k.s.len - k.s.n));
-    raw[n].load(static_cast<const T*>(X.p) + row * X.ld + head * X.hs + j * 8, X.vec);
+    src[n] = static_cast<const T*>(X.p) + (k.s.row + (p - (k.s.len - k.s.n))) * X.ld + j * 8;
   }
+  Eight<T> raw[kItems], ahead[kItems];
+  auto load = [&](int head, Eight<T> (&x)[kItems]) {   // all in flight at once, a head ahead
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+      const HeadRows& X = n * kThreads + tid < kKvRec * R::kChunks ? K : V;
+      x[n].load(src[n] + head * X.hs, X.vec);
+    }
+  };
+  load(blockIdx.y, ahead);
   if (k.page < 0) {
     if (tid == 0) kv_bad(q.status);
     return;
   }
+  for (int head = blockIdx.y, turn = 0; head < L.heads; head += gridDim.y, ++turn) {
+    uint32_t* rec = recs[turn & 1];
 #pragma unroll
-  for (int n = 0; n < kItems; ++n) {
-    const int it = n * kThreads + tid, v = it / (kKvRec * R::kChunks), t = it / R::kChunks % kKvRec, j = it % R::kChunks;
-    float x[8];
+    for (int n = 0; n < kItems; ++n) raw[n] = ahead[n];
+    if (head + (int)gridDim.y < L.heads) load(head + gridDim.y, ahead);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = raw[n].at(i);
-    float lo = x[0], hi = x[0];
-    uint32_t top = 0;
+    for (int n = 0; n < kItems; ++n) {
+      const int it = n * kThreads + tid, v = it / (kKvRec * R::kChunks), t = it / R::kChunks % kKvRec, j = it % R::kChunks;
+      float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo = fminf(lo, x[i]);
-      hi = fmaxf(hi, x[i]);
-      top = std::max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+      for (int i = 0; i < 8; ++i) x[i] = raw[n].at(i);
+      float lo = x[0], hi = x[0];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+        top = std::max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+      }
+      auto f32 = [](uint32_t u) { return __uint_as_float(u); };
+      lo = f32(among<kLanes>(__float_as_uint(lo), [&](uint32_t a, uint32_t b) { return __float_as_uint(fminf(f32(a), f32(b))); }));
+      hi = f32(among<kLanes>(__float_as_uint(hi), [&](uint32_t a, uint32_t b) { return __float_as_uint(fmaxf(f32(a), f32(b))); }));
+      top = among<kLanes>(top, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+      const Grid g = make_grid(lo, hi, top);
+      const bool nan = g.s != g.s;
+      const int z = nan ? 0 : 0x4b400000 - (int)steps(lo, g, T{}), shift = z - 0x4b400000;
+      int c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = std::min(std::max((int)steps(x[i], g, T{}) + shift, 0), 15);   // NaN: any code
+      if (v == 0) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w |= (uint32_t)c[i] << (4 * (4 * (i & 1) + (i >> 1)));
+        rec[R::key_word(t, j)] = w;
+      } else {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          reinterpret_cast<uint8_t*>(rec)[R::value_byte(t, j, b)] = (uint8_t)(c[2 * b] | c[2 * b + 1] << 4);
+      }
+      if (j % kLanes == 0)
+        rec[R::param_word(v, t, j / kLanes)] = __float_as_uint(g.s) | (uint32_t)(uint16_t)(int16_t)z;
     }
-    auto f32 = [](uint32_t u) { return __uint_as_float(u); };
-    lo = f32(among<kLanes>(__float_as_uint(lo), [&](uint32_t a, uint32_t b) { return __float_as_uint(fminf(f32(a), f32(b))); }));
-    hi = f32(among<kLanes>(__float_as_uint(hi), [&](uint32_t a, uint32_t b) { return __float_as_uint(fmaxf(f32(a), f32(b))); }));
-    top = among<kLanes>(top, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
-    const Grid g = make_grid(lo, hi, top);
-    const bool nan = g.s != g.s;
-    const int z = nan ? 0 : 0x4b400000 - (int)steps(lo, g, T{}), shift = z - 0x4b400000;
-    int c[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = std::min(std::max((int)steps(x[i], g, T{}) + shift, 0), 15);   // NaN: any code
-    if (v == 0) {
-      uint32_t w = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w |= (uint32_t)c[i] << (4 * (4 * (i & 1) + (i >> 1)));
-      rec[R::key_word(t, j)] = w;
-    } else {
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        reinterpret_cast<uint8_t*>(rec)[R::value_byte(t, j, b)] = (uint8_t)(c[2 * b] | c[2 * b + 1] << 4);
+    __syncthreads();
+    uint8_t* out = pages + (k.page * L.heads + head) * L.recs * (int64_t)(R::kWords * 4) +
+                   (int64_t)(k.blk & (L.recs - 1)) * (R::kWords * 4);
+    if (k.p1 - k.p0 == kKvRec) {
+      for (int w = tid; w < R::kWords / 4; w += kThreads)
+        reinterpret_cast<u32x4_t*>(out)[w] = reinterpret_cast<const u32x4_t*>(rec)[w];
+      continue;
     }
-    if (j % kLanes == 0)
-      rec[R::param_word(v, t, j / kLanes)] = __float_as_uint(g.s) | (uint32_t)(uint16_t)(int16_t)z;
-  }
-  __syncthreads();
-  uint8_t* out = pages + (k.page * L.heads + head) * L.recs * (int64_t)(R::kWords * 4) +
-                 (int64_t)(k.blk & (L.recs - 1)) * (R::kWords * 4);
-  if (k.p1 - k.p0 == kKvRec) {
-    for (int w = tid; w < R::kWords / 4; w += kThreads)
-      reinterpret_cast<u32x4_t*>(out)[w] = reinterpret_cast<const u32x4_t*>(rec)[w];
-    return;
-  }
-  const int t0 = k.p0 - k.blk * kKvRec, t1 = k.p1 - k.blk * kKvRec;
-  for (int w = tid; w < R::kWords; w += kThreads) {
-    const int t = R::position(w);
-    const bool first = t >= t0 && t < t1;
-    if (D == 64 && w >= R::kCodeWords && w < 2 * R::kCodeWords) {   // two positions, 16 bits each
-      const bool second = t + 1 >= t0 && t + 1 < t1;
-      if (first) reinterpret_cast<uint16_t*>(out)[2 * w] = (uint16_t)rec[w];
-      if (second) reinterpret_cast<uint16_t*>(out)[2 * w + 1] = (uint16_t)(rec[w] >> 16);
-    } else if (first) {
-      reinterpret_cast<uint32_t*>(out)[w] = rec[w];
+    const int t0 = k.p0 - k.blk * kKvRec, t1 = k.p1 - k.blk * kKvRec;
+    for (int w = tid; w < R::kWords; w += kThreads) {
+      const int t = R::position(w);
+      const bool first = t >= t0 && t < t1;
+      if (D == 64 && w >= R::kCodeWords && w < 2 * R::kCodeWords) {   // two positions, 16 bits each
+        const bool second = t + 1 >= t0 && t + 1 < t1;
+        if (first) reinterpret_cast<uint16_t*>(out)[2 * w] = (uint16_t)rec[w];
+        if (second) reinterpret_cast<uint16_t*>(out)[2 * w + 1] = (uint16_t)(rec[w] >> 16);
+      } else if (first) {
+        reinterpret_cast<uint32_t*>(out)[w] = rec[w];
+      }
     }
   }
 }
@@ -270,65 +284,75 @@ template <int D, int G, class T>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvLayout L, HeadRows K, HeadRows V, KvSeqs q,
                                                            const uint8_t* __restrict__ pages) {
   using R = Rec<D, G>;
-  __shared__ __attribute__((aligned(16))) uint32_t rec[R::kWords];
-  const int tid = threadIdx.x, head = blockIdx.y;
-  if (head == 0 && q.status) report(q, L);
+  __shared__ __attribute__((aligned(16))) uint32_t recs[2][R::kWords];
+  const int tid = threadIdx.x;
+  if (blockIdx.y == 0 && q.status) report(q, L);
   Block k;
   if (!find_block(q, L, &k)) return;
-  if (k.page < 0) {
-    if (tid == 0) kv_bad(q.status);
-  } else {
-    const uint8_t* in = pages + (k.page * L.heads + head) * L.recs * (int64_t)(R::kWords * 4) +
-                        (int64_t)(k.blk & (L.recs - 1)) * (R::kWords * 4);
-    for (int w = tid; w < R::kWords / 4; w += kThreads)
-      reinterpret_cast<u32x4_t*>(rec)[w] = reinterpret_cast<const u32x4_t*>(in)[w];
-  }
-  __syncthreads();
-  constexpr int kItems = 2 * kKvRec * R::kChunks;
+  if (k.page < 0 && tid == 0) kv_bad(q.status);
+  constexpr bool kTwice = R::kWords / 4 > kThreads;   // whether a record is more than a piece of 16 bytes a thread
+  static_assert(R::kWords / 4 <= 2 * kThreads, "");
+  u32x4_t ahead = {}, more = {};
+  auto load = [&](int head) {   // a head ahead
+    const u32x4_t* in = reinterpret_cast<const u32x4_t*>(
+        pages + ((k.page < 0 ? 0 : k.page) * L.heads + head) * L.recs * (int64_t)(R::kWords * 4) +
+        (int64_t)(k.blk & (L.recs - 1)) * (R::kWords * 4));
+    if (tid < R::kWords / 4) ahead = in[tid];
+    if (kTwice && tid + kThreads < R::kWords / 4) more = in[tid + kThreads];
+  };
+  load(blockIdx.y);
+  for (int head = blockIdx.y, turn = 0; head < L.heads; head += gridDim.y, ++turn) {
+    uint32_t* rec = recs[turn & 1];
+    if (tid < R::kWords / 4) reinterpret_cast<u32x4_t*>(rec)[tid] = ahead;
+    if (kTwice && tid + kThreads < R::kWords / 4) reinterpret_cast<u32x4_t*>(rec)[tid + kThreads] = more;
+    if (head + (int)gridDim.y < L.heads) load(head + gridDim.y);
+    __syncthreads();
+    constexpr int kItems = 2 * kKvRec * R::kChunks;
 #pragma unroll
-  for (int it = tid; it < kItems; it += kThreads) {
-    const int v = it / (kKvRec * R::kChunks), t = it / R::kChunks % kKvRec, j = it % R::kChunks;
-    const int p = k.blk * kKvRec + t;
-    if (p < k.p0 || p >= k.p1) continue;
-    const uint32_t pw = k.page < 0 ? 0x7fc00000u : rec[R::param_word(v, t, j * 8 / G)];
-    const float s = __uint_as_float(pw & 0xffff0000u);
-    const int z = (int16_t)(uint16_t)pw;
-    float x[8];
-    if (v == 0) {
-      const uint32_t w = rec[R::key_word(t, j)];
+    for (int it = tid; it < kItems; it += kThreads) {
+      const int v = it / (kKvRec * R::kChunks), t = it / R::kChunks % kKvRec, j = it % R::kChunks;
+      const int p = k.blk * kKvRec + t;
+      if (p < k.p0 || p >= k.p1) continue;
+      const uint32_t pw = k.page < 0 ? 0x7fc00000u : rec[R::param_word(v, t, j * 8 / G)];
+      const float s = __uint_as_float(pw & 0xffff0000u);
+      const int z = (int16_t)(uint16_t)pw;
+      float x[8];
+      if (v == 0) {
+        const uint32_t w = rec[R::key_word(t, j)];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = (float)((int)(w >> (4 * (4 * (i & 1) + (i >> 1))) & 15) - z) * s;
-    } else {
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int w = reinterpret_cast<const uint8_t*>(rec)[R::value_byte(t, j, b)];
-        x[2 * b] = (float)((w & 15) - z) * s;
-        x[2 * b + 1] = (float)((w >> 4) - z) * s;
-      }
-    }
-    const HeadRows& X = v ? V : K;
-    const int64_t row = k.s.row + (p - (k.s.len - k.s.n));
-    T* out = const_cast<T*>(static_cast<const T*>(X.p)) + row * X.ld + head * X.hs + j * 8;
-    if constexpr (sizeof(T) == 4) {
-      if (X.vec) {
-        reinterpret_cast<float4*>(out)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4*>(out)[1] = make_float4(x[4], x[5], x[6], x[7]);
+        for (int i = 0; i < 8; ++i) x[i] = (float)((int)(w >> (4 * (4 * (i & 1) + (i >> 1))) & 15) - z) * s;
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = x[i];
+        for (int b = 0; b < 4; ++b) {
+          const int w = reinterpret_cast<const uint8_t*>(rec)[R::value_byte(t, j, b)];
+          x[2 * b] = (float)((w & 15) - z) * s;
+          x[2 * b + 1] = (float)((w >> 4) - z) * s;
+        }
       }
-    } else {
-      uint16_t h[8];
+      const HeadRows& X = v ? V : K;
+      const int64_t row = k.s.row + (p - (k.s.len - k.s.n));
+      T* out = const_cast<T*>(static_cast<const T*>(X.p)) + row * X.ld + head * X.hs + j * 8;
+      if constexpr (sizeof(T) == 4) {
+        if (X.vec) {
+          reinterpret_cast<float4*>(out)[0] = make_float4(x[0], x[1], x[2], x[3]);
+          reinterpret_cast<float4*>(out)[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = __builtin_bit_cast(uint16_t, (__bf16)x[i]);
-      if (X.vec) {
-        u32x4_t o;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
-        *reinterpret_cast<u32x4_t*>(out) = o;
+          for (int i = 0; i < 8; ++i) out[i] = x[i];
+        }
       } else {
+        uint16_t h[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = h[i];
+        for (int i = 0; i < 8; ++i) h[i] = __builtin_bit_cast(uint16_t, (__bf16)x[i]);
+        if (X.vec) {
+          u32x4_t o;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+          *reinterpret_cast<u32x4_t*>(out) = o;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) out[i] = h[i];
+        }
       }
     }
   }
@@ -336,6 +360,13 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvLayout L, HeadRows 
 
 // Blocks of 16 positions that the tokens can touch: n tokens touch at most (n + 30) / 16.
 int64_t most_blocks(const KvSeqs& q) { return q.cu ? (q.tokens + 30 * std::min(q.batch, q.tokens)) / 16 : q.batch; }
+
+// The heads are shared by as many workgroups as fill the card (8 a CU); each takes
+// every so manieth head of its 16 positions, whose place it finds once.
+dim3 grid_of(const KvLayout& L, const KvSeqs& q) {
+  const int64_t blocks = most_blocks(q);
+  return dim3((unsigned)blocks, (unsigned)std::min<int64_t>(L.heads, ceil_div(2048, blocks)));
+}
 
 template <class F>
 gptq_status by_shape(const KvLayout& L, int dtype, const F& f) {
@@ -353,7 +384,7 @@ gptq_status by_shape(const KvLayout& L, int dtype, const F& f) {
 gptq_status run_kv_append(const KvLayout& L, const HeadRows& K, const HeadRows& V, int dtype, const KvSeqs& q,
                           void* pages, hipStream_t stream) {
   return by_shape(L, dtype, [&](auto d, auto g, auto t) {
-    kv_append_kernel<d.value, g.value, decltype(t)><<<dim3((unsigned)most_blocks(q), L.heads), kThreads, 0, stream>>>(
+    kv_append_kernel<d.value, g.value, decltype(t)><<<grid_of(L, q), kThreads, 0, stream>>>(
         L, K, V, q, static_cast<uint8_t*>(pages));
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
@@ -363,7 +394,7 @@ gptq_status run_kv_append(const KvLayout& L, const HeadRows& K, const HeadRows& 
 gptq_status run_kv_read(const KvLayout& L, const HeadRows& K, const HeadRows& V, int dtype, const KvSeqs& q,
                         const void* pages, hipStream_t stream) {
   return by_shape(L, dtype, [&](auto d, auto g, auto t) {
-    kv_read_kernel<d.value, g.value, decltype(t)><<<dim3((unsigned)most_blocks(q), L.heads), kThreads, 0, stream>>>(
+    kv_read_kernel<d.value, g.value, decltype(t)><<<grid_of(L, q), kThreads, 0, stream>>>(
         L, K, V, q, static_cast<const uint8_t*>(pages));
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;

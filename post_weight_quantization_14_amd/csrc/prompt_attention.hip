@@ -46,7 +46,7 @@ struct Prompt {
 };
 
 template <int D, bool VEC>
-__global__ __launch_bounds__(kThreads, 2) void prompt_attention_kernel(Prompt a) {
+__global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_kernel(Prompt a) {
   constexpr int KS = D / 16, DT = D / 32, CH = D / 8, TB = kBN * D * 2;
   // Keys and values of a tile and of the next.  Two objects: the compiler makes a
   // read wait for every copy in flight that may go to the object it reads.
