@@ -126,6 +126,11 @@ __device__ __forceinline__ int64_t lane_value(int64_t v, int l) {
   return (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)v, l) | (int64_t)__builtin_amdgcn_readlane((int)(v >> 32), l) << 32;
 }
 
+__device__ __forceinline__ KvSeq lane_value(const KvSeq& s, int l) {
+  return KvSeq{lane_value(s.row, l), __builtin_amdgcn_readlane(s.n, l), __builtin_amdgcn_readlane(s.len, l),
+               __builtin_amdgcn_readlane((int)s.bad, l) != 0};
+}
+
 // The sum of count(b) over the batch.  Called by whole waves.
 template <class F>
 __device__ __forceinline__ int64_t ragged_total(int64_t batch, const F& count) {
@@ -136,9 +141,9 @@ __device__ __forceinline__ int64_t ragged_total(int64_t batch, const F& count) {
 
 // The sequence b in whose count(b) pieces the `index`-th piece of all lies, and
 // which of them it is; false past the last.  Called by whole waves, which look at
-// 64 sequences at a time.
+// 64 sequences at a time: what count() kept of its last call in lane `l` is of b.
 template <class F>
-__device__ __forceinline__ bool ragged_find(int64_t index, int64_t batch, const F& count, int64_t* b, int64_t* at) {
+__device__ __forceinline__ bool ragged_find(int64_t index, int64_t batch, const F& count, int64_t* b, int64_t* at, int* l) {
   const int lane = threadIdx.x & 63;
   index = uniform(index);
   for (int64_t base = 0; base < batch; base += 64) {
@@ -146,9 +151,9 @@ __device__ __forceinline__ bool ragged_find(int64_t index, int64_t batch, const 
     const int64_t upto = wave_scan(c);
     const uint64_t past = __ballot(upto > index);   // wave-uniform
     if (past) {
-      const int l = __ffsll((unsigned long long)past) - 1;
-      *b = base + l;
-      *at = index - lane_value(upto - c, l);
+      *l = __ffsll((unsigned long long)past) - 1;
+      *b = base + *l;
+      *at = index - lane_value(upto - c, *l);
       return true;
     }
     index -= lane_value(upto, 63);

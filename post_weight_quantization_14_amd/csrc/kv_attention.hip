@@ -126,15 +126,20 @@ struct Units {
   __device__ __forceinline__ int64_t steps_of(const KvSeq& s) const { return tiles(s, w.share) * (WHOLE ? 1 : steps(s)) * w.L.heads; }
   // the sequence that step `pos` belongs to, and which of its steps it is
   __device__ __forceinline__ KvSeq find(int64_t pos, int64_t* b, int64_t* at) const {
+    KvSeq s = mine;
+    int l;
     if (few) {
-      const int l = __ffsll((unsigned long long)__ballot(upto > pos)) - 1;
+      l = __ffsll((unsigned long long)__ballot(upto > pos)) - 1;
       *b = l;
       *at = pos - lane_value(upto - own, l);
-      return KvSeq{lane_value(mine.row, l), __builtin_amdgcn_readlane(mine.n, l), __builtin_amdgcn_readlane(mine.len, l),
-                   __builtin_amdgcn_readlane((int)mine.bad, l) != 0};
+    } else {
+      auto count = [&](int64_t i) {
+        s = kv_seq(w.q, i, capacity);
+        return steps_of(s);
+      };
+      ragged_find(pos, w.q.batch, count, b, at, &l);
     }
-    ragged_find(pos, w.q.batch, [&](int64_t i) { return steps_of(kv_seq(w.q, i, capacity)); }, b, at);
-    return uniform(kv_seq(w.q, *b, capacity));
+    return lane_value(s, l);
   }
 };
 

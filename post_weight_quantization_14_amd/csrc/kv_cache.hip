@@ -154,10 +154,17 @@ __device__ __forceinline__ bool find_block(const KvSeqs& q, const KvLayout& L, B
   if (q.cu == nullptr) {   // one token each: block = sequence
     k->b = blockIdx.x;
     if (k->b >= q.batch) return false;
-  } else if (!ragged_find(blockIdx.x, q.batch, [&](int64_t b) { return blocks_of(written_seq(q, L, b)); }, &k->b, &at)) {
-    return false;
+    k->s = uniform(written_seq(q, L, k->b));
+  } else {
+    KvSeq mine;
+    int l;
+    auto count = [&](int64_t b) {
+      mine = written_seq(q, L, b);
+      return blocks_of(mine);
+    };
+    if (!ragged_find(blockIdx.x, q.batch, count, &k->b, &at, &l)) return false;
+    k->s = lane_value(mine, l);
   }
-  k->s = uniform(written_seq(q, L, k->b));
   const int first = k->s.len - k->s.n;
   k->blk = first / kKvRec + (int)at;
   k->p0 = std::max(first, k->blk * kKvRec);

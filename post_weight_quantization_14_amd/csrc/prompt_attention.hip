@@ -59,22 +59,19 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
   // go first.
   const int64_t slot = blockIdx.x >> 3, group = slot / a.share * 8 + (blockIdx.x & 7);
   const int64_t kvh = group % a.kv_heads, head = kvh * a.share + slot % a.share;
-  int64_t b = 0, at = 0;
-  auto seq = [&](int64_t i, int64_t* row) {
-    const int64_t r0 = std::min(std::max<int64_t>(a.cu[i], 0), a.tokens);
-    const int64_t r1 = std::min(std::max<int64_t>(a.cu[i + 1], r0), a.tokens);
-    *row = r0;
-    return r1 - r0;
-  };
   if (group >= a.tiles * a.kv_heads) return;
-  if (!ragged_find(a.tiles - 1 - group / a.kv_heads, a.batch, [&](int64_t i) {
-        int64_t r;
-        return (seq(i, &r) + kBM - 1) / kBM;
-      }, &b, &at))
-    return;
-  int64_t row0;
-  const int len = uniform((int)seq(b, &row0));
-  row0 = uniform(row0);
+  int64_t b = 0, at = 0, row0 = 0;
+  int from, len = 0;
+  auto count = [&](int64_t i) {   // tiles of sequence i
+    const int64_t r0 = a.cu[i], r1 = a.cu[i + 1];
+    row0 = r0 < 0 ? 0 : r0 > a.tokens ? a.tokens : r0;
+    const int64_t past = r1 > a.tokens ? a.tokens : r1;
+    len = past > row0 ? (int)(past - row0) : 0;
+    return (int64_t)((len + kBM - 1) / kBM);
+  };
+  if (!ragged_find(a.tiles - 1 - group / a.kv_heads, a.batch, count, &b, &at, &from)) return;
+  row0 = lane_value(row0, from);
+  len = __builtin_amdgcn_readlane(len, from);
   const int q0 = (int)at * kBM, w0 = q0 + wave * 32;   // the workgroup's and the wave's first query
   const int iq = w0 + n32;                             // the lane's query
   const int keys = std::min(len, q0 + kBM);            // that any of its queries sees
