@@ -6,6 +6,8 @@
 namespace gptq {
 namespace {
 
+#define INLINE __attribute__((always_inline))
+
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kBM = 32 * kWaves;   // queries of a workgroup, 32 a wave
 constexpr int kBN = 64;            // keys of a tile
@@ -171,15 +173,23 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
       if (k0 > w0 + 31) return;   // the wave's queries see none of it (no barrier is skipped)
       f32x16_t s[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {   // two sums by turns: a product need not wait for the one before
           const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(cur + (kat[ks] + u * 32 * D * 2));
           s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[ks], s[u], 0, 0, 0);
         }
+      __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);   // operands are read eight products ahead
+#pragma unroll
+      for (int i = 0; i < 2 * KS - 8; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
+      __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
       const bool edge = k0 + kBN > w0 + 1;   // some query does not see some key
       if (edge) {
 #pragma unroll
@@ -206,37 +216,44 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
         l += e;
         p[r >> 3][r & 7] = (__bf16)e;
       }
+      auto columns = [&](int d, int kk) INLINE {   // 16 rows further: the same swizzle
+        const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t*)(cur + (vlo[d] + (TB + kk * 16 * D * 2))));
+        const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t*)(cur + (vhi[d] + (TB + kk * 16 * D * 2))));
+        const auto both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        return __builtin_bit_cast(bf16x8_t, both);
+      };
+      if constexpr (!careful) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        f32x16_t more, less;   // counts
-        if constexpr (careful) {
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(columns(d, kk), p[kk], o[d], 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          f32x16_t more, less;   // counts
 #pragma unroll
           for (int r = 0; r < 16; ++r) more[r] = less[r] = 0.f;
-        }
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {   // 16 rows further: the same swizzle
-          const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t*)(cur + (vlo[d] + (TB + kk * 16 * D * 2))));
-          const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t*)(cur + (vhi[d] + (TB + kk * 16 * D * 2))));
-          const auto both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-          bf16x8_t v = __builtin_bit_cast(bf16x8_t, both);
-          if constexpr (careful) if (edge) {
-            bf16x8_t up, down, seen;
+          for (int kk = 0; kk < 4; ++kk) {
+            bf16x8_t v = columns(d, kk);
+            if (edge) {
+              bf16x8_t up, down, seen;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float x = (float)v[e];
-              const bool odd = !(fabsf(x) < INFINITY);
-              up[e] = (__bf16)(odd && !(x < 0.f) ? 1.f : 0.f);
-              down[e] = (__bf16)(odd && !(x > 0.f) ? 1.f : 0.f);
-              v[e] = odd ? (__bf16)0.f : v[e];
-              const int key = k0 + kk * 16 + (e >> 2) * 8 + half * 4 + (e & 3);
-              seen[e] = (__bf16)(key <= iq ? 1.f : 0.f);
+              for (int e = 0; e < 8; ++e) {
+                const float x = (float)v[e];
+                const bool odd = !(fabsf(x) < INFINITY);
+                up[e] = (__bf16)(odd && !(x < 0.f) ? 1.f : 0.f);
+                down[e] = (__bf16)(odd && !(x > 0.f) ? 1.f : 0.f);
+                v[e] = odd ? (__bf16)0.f : v[e];
+                const int key = k0 + kk * 16 + (e >> 2) * 8 + half * 4 + (e & 3);
+                seen[e] = (__bf16)(key <= iq ? 1.f : 0.f);
+              }
+              more = __builtin_amdgcn_mfma_f32_32x32x16_bf16(up, seen, more, 0, 0, 0);
+              less = __builtin_amdgcn_mfma_f32_32x32x16_bf16(down, seen, less, 0, 0, 0);
             }
-            more = __builtin_amdgcn_mfma_f32_32x32x16_bf16(up, seen, more, 0, 0, 0);
-            less = __builtin_amdgcn_mfma_f32_32x32x16_bf16(down, seen, less, 0, 0, 0);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[kk], o[d], 0, 0, 0);
           }
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[kk], o[d], 0, 0, 0);
-        }
-        if constexpr (careful) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) o[d][r] += (more[r] > 0.f ? INFINITY : 0.f) + (less[r] > 0.f ? -INFINITY : 0.f);
         }
