@@ -175,9 +175,9 @@ gptq_status run_kv_read(const KvLayout& L, const HeadRows& K, const HeadRows& V,
                         const void* pages, hipStream_t stream);
 
 struct KvAttentionPlan {
-  int tiles;          // 16-row tiles of queries that a workgroup holds: 1 or 2
+  int tile;           // rows of queries that a workgroup holds at once: 8, 16 or 32
   bool whole;         // a workgroup for each unit (row tile and key head of a sequence), not an equal piece of all
-  int wgs;            // workgroups
+  int wgs, waves;     // workgroups, and waves of each
   int rows;           // rows of a unit that should hold queries
   size_t partial, total;   // workspace bytes
 };

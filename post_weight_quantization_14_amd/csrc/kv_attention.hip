@@ -43,12 +43,6 @@ __device__ __forceinline__ float quad_sum(float x) {
   return x + y;
 }
 
-// lane n of the row of 16
-template <int N>
-__device__ __forceinline__ float row_lane(float x) {
-  return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0x150 + N, 0xf, 0xf, true));
-}
-
 // The constants of the AND-OR, hidden from folding (VOP3 takes no literals).
 struct Consts {
   uint32_t m, c;
@@ -61,11 +55,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {   // nearest e
   return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b});
 }
 
-template <class F>
-__device__ __forceinline__ void by_index(const F& f) {   // f(0) .. f(7), each a constant
-  f(std::integral_constant<int, 0>{}), f(std::integral_constant<int, 1>{}), f(std::integral_constant<int, 2>{});
-  f(std::integral_constant<int, 3>{}), f(std::integral_constant<int, 4>{}), f(std::integral_constant<int, 5>{});
-  f(std::integral_constant<int, 6>{}), f(std::integral_constant<int, 7>{});
+template <int N, class F>
+__device__ __forceinline__ void by_index(const F& f) {   // f(0) .. f(N - 1), each a constant
+  if constexpr (N > 0) {
+    by_index<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
 }
 
 struct Split {
@@ -149,11 +144,21 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   return a / b;
 }
 
-template <int D, int G>
+// lane n of the row of 16 for SP 1, of the lane's own four for SP 2
+template <int SP, int N>
+__device__ __forceinline__ float lane_of(float x) {
+  constexpr int kCtrl = SP == 1 ? 0x150 + N : (N & 3) * 0x55;
+  return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), kCtrl, 0xf, 0xf, true));
+}
+
+// Params of the step's positions.  SP 1: lane 16·kg + 4·j + r has those of position
+// 4·kg + r, j = 0, 1: keys of the two records, 2, 3: values.  SP 2: lane
+// 16·kg + 8·u + 4·i + r has those of position 4·kg + r of record u, word 0 keys, word 1 values.
+template <int D, int G, int SP>
 struct Step {
   static constexpr int KS = D / 32, NG = D / G;
   uint32_t k[2][KS], v[2][KS];
-  uint32_t pw[NG];   // params: lane 16·kg + 4·j + r has those of position 4·kg + r, j: keys of the two records, values
+  uint32_t pw[SP][NG];
   bool bad;          // a page that is none
 };
 
@@ -188,14 +193,15 @@ __device__ __forceinline__ void value_pairs(const uint32_t (&w)[D / 32], int b, 
 // W waves share a unit's steps.  WHOLE: a workgroup takes one unit; otherwise each
 // takes an equal piece of all units' steps, and units cut by a piece's end are
 // joined by kv_join_kernel.
-template <int D, int G, int NT, int W, bool WHOLE>
+template <int D, int G, int NT, int SP, int W, bool WHOLE>
 __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
-  constexpr int kThreads = 64 * W, R = 16 * NT, KS = D / 32, NG = D / G, MT = D / 16, PG = G / 32;   // PG: 32-channel steps of a group
+  constexpr int kThreads = 64 * W, R = 16 * NT / SP, NC = 16 / SP, E = 8 / SP, KS = D / 32, NG = D / G, MT = D / 16, PG = G / 32;   // PG: 32-channel steps of a group
   constexpr int kPitch = D + 4;
   __shared__ float so[W][16][kPitch];
   __shared__ float sm[W][16], sl[W][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n16 = lane & 15, kg = lane >> 4;
+  const int nq = n16 % NC, half = n16 / NC;   // query row of the column, record of its logits
   const Units<R, WHOLE> units(w);
   const Consts kc;
 
@@ -220,13 +226,13 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
     const uint32_t hq0 = (uint32_t)(row0 - tq0 * w.share);   // row0 is head hq0 of the group, token tq0
     const int rows = (int)units.min64(R, (int64_t)s.n * w.share - row0);
 
-    // ---- queries: lane n16 of every quarter holds query row 16·nt + n16
+    // ---- queries: column n16 holds query row 16·nt + nq
     u32x4_t qx[NT][KS];
     int lim[NT];     // positions that the row sees
     const uint16_t* qp[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int i = nt * 16 + n16 < rows ? nt * 16 + n16 : 0;   // rows past the last: computed, not stored
+      const int i = nt * 16 + nq < rows ? nt * 16 + nq : 0;   // rows past the last: computed, not stored
       const uint32_t h = hq0 + i, t = w.share == 1 ? h : __umulhi(h, w.share_inv);
       lim[nt] = s.len - s.n + (int)tq0 + (int)t + 1;
       qp[nt] = static_cast<const uint16_t*>(w.Q.p) + (s.row + tq0 + t) * w.Q.ld + (head * w.share + (h - t * w.share)) * w.Q.hs + kg * 8;
@@ -247,27 +253,29 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
     const int least = s.len - s.n + (int)tq0 + 1;   // positions that every row sees
 
     // ---- the wave's steps s0 + wave, + 4, ..
-    const int last = (s.len - 1) / kKvRec;   // record; pages past it may be none
+    const int last = uniform((s.len - 1) / kKvRec);   // record; pages past it may be none
     // page numbers go through the scalar unit a step ahead of the records in them
-    const constant_int* table = (const constant_int*)(w.q.table + b * w.q.stride);
+    const constant_int* table = (const constant_int*)uniform((int64_t)(s.bad ? w.q.lens + b : w.q.table + b * w.q.stride));
+    const int page_shift = uniform(s.bad ? 31 : w.L.rec_shift);   // any number that can be read
     struct Pages {
       int id[2];
     };
     auto page_of = [&](int st) INLINE {
       Pages p;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) p.id[u] = s.bad ? -1 : table[min(2 * st + u, last) >> w.L.rec_shift];
+      for (int u = 0; u < 2; ++u) p.id[u] = table[min(2 * st + u, last) >> page_shift];
       return p;
     };
     const uint32_t head_at = (uint32_t)head << w.L.rec_shift;
-    const int param_at = 2 * kv_code_bytes(D) + (n16 >> 3) * kv_param_bytes(D, G) + (kg * 4 + (n16 & 3)) * 4;
-    auto load = [&](int st, const Pages& pg, Step<D, G>& x) INLINE {
+    const int param_at = 2 * kv_code_bytes(D) + (SP == 1 ? (n16 >> 3) * kv_param_bytes(D, G) : 0) + (kg * 4 + (n16 & 3)) * 4;
+    auto load = [&](int st, const Pages& pg, Step<D, G, SP>& x) INLINE {
       x.bad = false;
       const uint8_t* base[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const bool none = (uint32_t)pg.id[u] >= (uint32_t)w.q.pages;
-        const int64_t id = none ? 0 : pg.id[u];
+        const int page = uniform(pg.id[u]);
+        const bool none = s.bad || (uint32_t)page >= (uint32_t)w.q.pages;
+        const int64_t id = none ? 0 : page;
         x.bad |= none;
         const uint32_t rec = head_at + (min(2 * st + u, last) & (w.L.recs - 1));
         const uint8_t* p = w.pages + id * w.L.page_bytes + (int64_t)rec * kv_rec_bytes(D, G);
@@ -275,34 +283,18 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
         load_words(p + (kv_code_bytes(D) + lane * (D / 8)), x.v[u]);
         base[u] = p;
       }
-      const uint8_t* p = (lane & 4 ? base[1] : base[0]) + param_at;
+      const uint8_t* p = ((SP == 1 ? lane & 4 : half) ? base[1] : base[0]) + param_at;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) x.pw[g] = *reinterpret_cast<const uint32_t*>(p + g * 64);
+      for (int i = 0; i < SP; ++i)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) x.pw[i][g] = *reinterpret_cast<const uint32_t*>(p + i * kv_param_bytes(D, G) + g * 64);
     };
-    Step<D, G> cur, nxt;
+    Step<D, G, SP> cur, nxt;
     int st = s0 + wave;
     const bool some = st < s1 && s.len > 0;
     Pages ahead;
-    if (some) {
-      load(st, page_of(st), cur);
-      ahead = page_of(min(st + W, s1 - 1));
-    }
-
     bf16x8_t qf[NT][KS];
     float qs[NT][NG];   // sums of the query's channels, by group
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) qx[nt][ks][i] = (qx[nt][ks][i] & w.keep) ^ w.flip;
-        qf[nt][ks] = __builtin_bit_cast(bf16x8_t, qx[nt][ks]);
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t += __uint_as_float(qx[nt][ks][i] << 16) + __uint_as_float(qx[nt][ks][i] & 0xffff0000u);
-        t = quad_sum(t);
-        qs[nt][ks / PG] = ks % PG == 0 ? t : qs[nt][ks / PG] + t;
-      }
     f32x4_t o[NT][MT];
     float m[NT], l[NT], zs[NT][NG];
 #pragma unroll
@@ -315,16 +307,20 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
       for (int j = 0; j < MT; ++j) o[nt][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
 
-    auto compute = [&](int st, Step<D, G>& x) INLINE {
-      float sf[NG], zf[NG];   // scales and 128 + zero points, of the positions of `pw`
+    auto compute = [&](int st, Step<D, G, SP>& x) INLINE {
+      float sf[SP][NG], zf[SP][NG];   // scales and 128 + zero points, of the positions of `pw`
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        sf[g] = __uint_as_float(x.bad ? 0x7fc00000u : x.pw[g] & 0xffff0000u);
-        zf[g] = (float)((int)(int16_t)(uint16_t)x.pw[g] + 128);
-      }
+      for (int i = 0; i < SP; ++i)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          sf[i][g] = __uint_as_float(x.bad ? 0x7fc00000u : x.pw[i][g] & 0xffff0000u);
+          zf[i][g] = (float)((int)(int16_t)(uint16_t)x.pw[i][g] + 128);
+        }
       if (x.bad && lane == 0) kv_bad(w.q.status);
-      // logits of positions 32·st + 16·u + 4·kg + r
-      float sx[NT][2][4];
+      // logits of positions at(i), i = 4·record + r (SP 1), r (SP 2)
+      float sx[NT][E];
+      auto at = [&](int i) { return st * kStep + (SP == 1 ? (i >> 2) * 16 : half * 16) + kg * 4 + (i & 3); };
+      f32x4_t acc[NT][NG][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         bf16x8_t a[KS];
@@ -336,43 +332,54 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
           a[ks] = __builtin_bit_cast(bf16x8_t, t);
         }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+            acc[nt][g][u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = g * PG; ks < (g + 1) * PG; ++ks)
-              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[ks], qf[nt][ks], acc, 0, 0, 0);
-            auto one = [&](auto r) INLINE {
-              constexpr int R0 = decltype(r)::value;
-              const float z = u ? row_lane<4 + R0>(zf[g]) : row_lane<R0>(zf[g]);
-              const float f = u ? row_lane<4 + R0>(sf[g]) : row_lane<R0>(sf[g]);
-              const float y = acc[R0] - z * qs[nt][g];
-              sx[nt][u][R0] = g == 0 ? y * f : sx[nt][u][R0] + y * f;
-            };
-            one(std::integral_constant<int, 0>{}), one(std::integral_constant<int, 1>{});
-            one(std::integral_constant<int, 2>{}), one(std::integral_constant<int, 3>{});
+              acc[nt][g][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[ks], qf[nt][ks], acc[nt][g][u], 0, 0, 0);
           }
+        if constexpr (SP == 1) {
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              by_index<4>([&](auto r) INLINE {
+                const float z = u ? lane_of<1, 4 + r.value>(zf[0][g]) : lane_of<1, r.value>(zf[0][g]);
+                const float f = u ? lane_of<1, 4 + r.value>(sf[0][g]) : lane_of<1, r.value>(sf[0][g]);
+                const float y = acc[nt][g][u][r.value] - z * qs[nt][g];
+                float& o = sx[nt][u * 4 + r.value];
+                o = g == 0 ? y * f : o + y * f;
+              });
         }
+      }
+      if constexpr (SP == 2) {   // each half of the columns takes a record's
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          by_index<4>([&](auto r) INLINE {
+            const float c = half ? acc[0][g][1][r.value] : acc[0][g][0][r.value];
+            const float y = c - lane_of<2, r.value>(zf[0][g]) * qs[0][g], f = lane_of<2, r.value>(sf[0][g]);
+            float& o = sx[0][r.value];
+            o = g == 0 ? y * f : o + y * f;
+          });
       }
       const bool edge = (st + 1) * kStep > least;
       if (edge) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (st * kStep + u * 16 + kg * 4 + r >= lim[nt]) sx[nt][u][r] = -INFINITY;
+          for (int i = 0; i < E; ++i)
+            if (at(i) >= lim[nt]) sx[nt][i] = -INFINITY;
       }
-      // running maximum; sums are scaled again only when it grows by more than 2^8
+      // running maximum of a column; its sums are scaled again only when that grows by more than 2^8
       bool grown = false;
       float top[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float t = sx[nt][0][0];
+        float t = sx[nt][0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) t = fmaxf(t, sx[nt][i >> 2][i & 3]);
+        for (int i = 1; i < E; ++i) t = fmaxf(t, sx[nt][i]);
         top[nt] = quad_max(t) * w.scale;
         grown |= top[nt] > m[nt] + 8.f;
       }
@@ -391,8 +398,8 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float& p = sx[nt][i >> 2][i & 3];
+        for (int i = 0; i < E; ++i) {
+          float& p = sx[nt][i];
           p = __builtin_amdgcn_exp2f(fmaf(p, w.scale, -m[nt]));
           l[nt] += p;
         }
@@ -402,16 +409,16 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
         bf16x8_t ph[NT], pl[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float pw[8];
-          by_index([&](auto i) INLINE { pw[i.value] = row_lane<8 + i.value>(sf[g]) * sx[nt][i.value >> 2][i.value & 3]; });
+          float pw[E];
+          by_index<E>([&](auto i) INLINE { pw[i.value] = lane_of<SP, 8 + i.value>(sf[SP - 1][g]) * sx[nt][i.value]; });
           if (edge) {   // the scale there may be anything
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (st * kStep + (i >> 2) * 16 + kg * 4 + (i & 3) >= lim[nt]) pw[i] = 0.f;
+            for (int i = 0; i < E; ++i)
+              if (at(i) >= lim[nt]) pw[i] = 0.f;
           }
-          u32x4_t hw, lw;
+          uint32_t hw[E / 2], lw[E / 2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < E / 2; ++i) {
             const uint32_t h = pack_bf16(pw[2 * i], pw[2 * i + 1]);
             const float h0 = __uint_as_float(h << 16), h1 = __uint_as_float(h & 0xffff0000u);
             const uint32_t lo = pack_bf16(pw[2 * i] - h0, pw[2 * i + 1] - h1);
@@ -420,9 +427,21 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
             pw[2 * i] = h0 + __uint_as_float(lo << 16);
             pw[2 * i + 1] = h1 + __uint_as_float(lo & 0xffff0000u);
           }
-          by_index([&](auto i) INLINE { zs[nt][g] += row_lane<8 + i.value>(zf[g]) * pw[i.value]; });
-          ph[nt] = __builtin_bit_cast(bf16x8_t, hw);
-          pl[nt] = __builtin_bit_cast(bf16x8_t, lw);
+          by_index<E>([&](auto i) INLINE { zs[nt][g] += lane_of<SP, 8 + i.value>(zf[SP - 1][g]) * pw[i.value]; });
+          u32x4_t hx, lx;
+          if constexpr (SP == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) hx[i] = hw[i], lx[i] = lw[i];
+          } else {   // a column's weights stand at its record's positions, zeros at the other's
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool mine = half == i >> 1;
+              hx[i] = mine ? hw[i & 1] : 0;
+              lx[i] = mine ? lw[i & 1] : 0;
+            }
+          }
+          ph[nt] = __builtin_bit_cast(bf16x8_t, hx);
+          pl[nt] = __builtin_bit_cast(bf16x8_t, lx);
         }
 #pragma unroll
         for (int j = g * PG * 2; j < (g + 1) * PG * 2; ++j) {
@@ -441,6 +460,21 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
       }
     };
     if (some) {
+      load(st, page_of(st), cur);
+      ahead = page_of(min(st + W, s1 - 1));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qx[nt][ks][i] = (qx[nt][ks][i] & w.keep) ^ w.flip;
+          qf[nt][ks] = __builtin_bit_cast(bf16x8_t, qx[nt][ks]);
+          float t = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t += __uint_as_float(qx[nt][ks][i] << 16) + __uint_as_float(qx[nt][ks][i] & 0xffff0000u);
+          t = quad_sum(t);
+          qs[nt][ks / PG] = ks % PG == 0 ? t : qs[nt][ks / PG] + t;
+        }
       for (;;) {
         load(min(st + W, s1 - 1), ahead, nxt);
         ahead = page_of(min(st + 2 * W, s1 - 1));
@@ -453,7 +487,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
       }
     }
 
-    // ---- the four waves' sums together, a tile of 16 rows at a time
+    // ---- the waves' sums together, and for SP 2 the halves of the columns: 16 columns at a time
     const bool whole = WHOLE || (s0 == 0 && s1 == steps);
     const int slot = pos == begin ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1;
     float* part = w.partial + (int64_t)slot * R * (D + 2);
@@ -468,7 +502,9 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
       __syncthreads();
       float up = kNone;
 #pragma unroll
-      for (int v = 0; v < W; ++v) up = fmaxf(up, sm[v][n16]);
+      for (int v = 0; v < W; ++v)
+#pragma unroll
+        for (int c = 0; c < SP; ++c) up = fmaxf(up, sm[v][c * NC + nq]);
       const float f = exp2f(m[nt] - up);
       if (kg == 0) sl[wave][n16] = l[nt] * f;
 #pragma unroll
@@ -477,16 +513,18 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
         for (int r = 0; r < 4; ++r)
           so[wave][n16][(j >> 1) * 32 + 2 * (kg * 4 + r) + (j & 1)] = (o[nt][j][r] - zs[nt][j / (2 * PG)]) * f;
       __syncthreads();
-      for (int i = tid; i < 16 * (D / 4); i += kThreads) {
+      for (int i = tid; i < NC * (D / 4); i += kThreads) {
         const int n = i / (D / 4), d = i % (D / 4) * 4;
         if (nt * 16 + n >= rows) continue;
         float ll = 0.f;
         f32x4_t y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int v = 0; v < W; ++v) {
-          ll += sl[v][n];
-          y += *reinterpret_cast<const f32x4_t*>(&so[v][n][d]);
-        }
+        for (int v = 0; v < W; ++v)
+#pragma unroll
+          for (int c = 0; c < SP; ++c) {
+            ll += sl[v][c * NC + n];
+            y += *reinterpret_cast<const f32x4_t*>(&so[v][c * NC + n][d]);
+          }
         if (whole) {
           const float inv = ll == 0.f ? 0.f : 1.f / ll;   // a row that sees nothing
           const uint32_t i = hq0 + nt * 16 + n, t = w.share == 1 ? i : __umulhi(i, w.share_inv);
@@ -506,7 +544,9 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
           if (d == 0) {
             float top = kNone;
 #pragma unroll
-            for (int v = 0; v < W; ++v) top = fmaxf(top, sm[v][n]);
+            for (int v = 0; v < W; ++v)
+#pragma unroll
+              for (int c = 0; c < SP; ++c) top = fmaxf(top, sm[v][c * NC + n]);
             part[R * D + nt * 16 + n] = top;
             part[R * D + R + nt * 16 + n] = ll;
           }
@@ -613,37 +653,59 @@ __global__ __launch_bounds__(256) void kv_join_kernel(Work w, int wgs, int most_
   }
 }
 
-template <int D, int G, int NT>
+template <int D, int G, int NT, int SP>
 gptq_status launch(const Work& w, const KvAttentionPlan& p, hipStream_t stream) {
   if (p.whole) {
-    kv_attention_kernel<D, G, NT, 8, true><<<p.wgs, 512, 0, stream>>>(w);
+    if (p.waves == 8)
+      kv_attention_kernel<D, G, NT, SP, 8, true><<<p.wgs, 512, 0, stream>>>(w);
+    else if (p.waves == 4)
+      kv_attention_kernel<D, G, NT, SP, 4, true><<<p.wgs, 256, 0, stream>>>(w);
+    else if (p.waves == 2)
+      kv_attention_kernel<D, G, NT, SP, 2, true><<<p.wgs, 128, 0, stream>>>(w);
+    else
+      kv_attention_kernel<D, G, NT, SP, 1, true><<<p.wgs, 64, 0, stream>>>(w);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
   }
-  kv_attention_kernel<D, G, NT, 4, false><<<p.wgs, 256, 0, stream>>>(w);
+  kv_attention_kernel<D, G, NT, SP, 4, false><<<p.wgs, 256, 0, stream>>>(w);
   GPTQ_LAUNCH_CHECK();
-  kv_join_kernel<D, 16 * NT><<<kJoinWgs, 256, 0, stream>>>(w, p.wgs, p.rows);
+  kv_join_kernel<D, 16 * NT / SP><<<kJoinWgs, 256, 0, stream>>>(w, p.wgs, p.rows);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
 
 }  // namespace
 
-// Positions of the longest sequence that the page table can hold up to which a
-// unit is one workgroup's.
-constexpr int64_t kWhole = 2048;
+// A unit is a workgroup's of its own, in one launch, where the page table holds no
+// longer sequence than kWhole; otherwise a long one would be waited for, and
+// workgroups get equal pieces of all units' steps.  Heads of 128, 8 key heads, us
+// (whole / pieces): 1 x 512 tokens 7.4 / 9.2, 32 x 768 9.7 / 13.6, 64 x 1000 17.8 /
+// 20.8, 128 x 250 of 32 heads 30 / 53, but 1 x 1024 9.6 / 9.3, 1 x 2048 14.4 / 10.0.
+// Its waves are as many as leave a CU eight at the most: 64 x 100 of 32 heads, 2048
+// units, 10.4 with one wave each, 13.9 with two, 16.4 with four; 64 x 512, 512 units,
+// 17.2, 14.6 and 10.3.
+constexpr int64_t kWhole = 1024, kMostUnits = 1 << 22;   // a grid's limit is 2^32 threads
+// Smaller tiles of rows while there is a CU for each unit: 4 sequences x 5 tokens x
+// 4 heads a key head over 2048 positions 22.8 us with tiles of 32, 14.7 with 8; 16
+// sequences (384 units of 8 rows) 23.5 and 28.4.
+constexpr int64_t kUnits = 256;
 
 KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, int64_t tokens, int64_t max_queries,
                                   int64_t capacity) {
   KvAttentionPlan p;
   const int64_t share = heads / L.heads;
   const int64_t rows = std::min(std::max<int64_t>(max_queries, 1), std::max<int64_t>(tokens, 1)) * share;
-  p.tiles = rows > 16 ? 2 : 1;
-  p.rows = (int)std::min<int64_t>(rows, 16 * p.tiles);
-  p.whole = capacity <= kWhole;
-  const int64_t units = L.heads * (tokens * share / (16 * p.tiles) + std::min(batch, tokens));   // at the most
-  p.wgs = (int)(p.whole ? std::min<int64_t>(units, INT32_MAX) : kMaxWgs);
-  p.partial = (size_t)2 * kMaxWgs * 16 * p.tiles * (L.dim + 2) * 4;
+  const int tile = rows > 16 ? 32 : rows > 8 ? 16 : 8;
+  p.tile = tile;
+  auto units = [&](int tile) { return L.heads * (tokens * share / tile + std::min(batch, tokens)); };   // at the most
+  p.whole = capacity <= kWhole && units(tile) <= kMostUnits;
+  if (p.whole)
+    while (p.tile > 8 && units(p.tile / 2) <= kUnits) p.tile /= 2;
+  p.rows = (int)std::min<int64_t>(rows, p.tile);
+  p.wgs = p.whole ? (int)units(p.tile) : kMaxWgs;
+  p.waves = 8;
+  while (p.waves > 1 && (int64_t)p.wgs * p.waves > 2048) p.waves /= 2;
+  p.partial = (size_t)2 * kMaxWgs * tile * (L.dim + 2) * 4;   // whatever the capacity
   p.total = align256(p.partial) + (size_t)kMaxWgs * sizeof(Split);
   return p;
 }
@@ -655,7 +717,9 @@ gptq_status run_kv_attention(const KvLayout& L, int heads, const HeadRows& Q, co
                static_cast<const uint8_t*>(pages),
                static_cast<float*>(ws), reinterpret_cast<Split*>(static_cast<uint8_t*>(ws) + align256(p.partial))};
   auto tiled = [&](auto d, auto g) {
-    return p.tiles == 1 ? launch<d.value, g.value, 1>(w, p, stream) : launch<d.value, g.value, 2>(w, p, stream);
+    return p.tile == 8    ? launch<d.value, g.value, 1, 2>(w, p, stream)
+           : p.tile == 16 ? launch<d.value, g.value, 1, 1>(w, p, stream)
+                          : launch<d.value, g.value, 2, 1>(w, p, stream);
   };
   using std::integral_constant;
   if (L.dim == 128 && L.group == 128) return tiled(integral_constant<int, 128>{}, integral_constant<int, 128>{});
