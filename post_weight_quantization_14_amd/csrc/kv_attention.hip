@@ -295,12 +295,18 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
     Pages ahead;
     bf16x8_t qf[NT][KS];
     float qs[NT][NG];   // sums of the query's channels, by group
+    constexpr bool kMat = NT == 2 && NG == 1;   // sums of zero points by the matrix cores too
+    f32x4_t zo[NT];
+    uint32_t za[4] = {0, 0, 0, 0};
+    // bytes that lane takes of its own word (4 .. 7) and its neighbour's (0 .. 3): even lanes both high halves, odd both low
+    const uint32_t zsel = lane & 1 ? 0x05040100u : 0x03020706u;
     f32x4_t o[NT][MT];
     float m[NT], l[NT], zs[NT][NG];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt] = kNone;
       l[nt] = 0.f;
+      zo[nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int g = 0; g < NG; ++g) zs[nt][g] = 0.f;
 #pragma unroll
@@ -391,6 +397,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
           l[nt] *= f;
 #pragma unroll
           for (int g = 0; g < NG; ++g) zs[nt][g] *= f;
+          if (kMat) zo[nt] *= f;
 #pragma unroll
           for (int j = 0; j < MT; ++j) o[nt][j] *= f;
         }
@@ -406,6 +413,18 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
       // values
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
+        if constexpr (kMat) {
+          // 128 + z = hi + lo with 8 bits each; quad 2 of a row of lanes has record 0's, quad 3 record 1's
+          const uint32_t zi = (uint32_t)((int)(int16_t)(uint16_t)x.pw[0][g] + 128);
+          const float lo = (float)(zi & 255u), hi = zf[0][g] - lo;
+          const uint32_t own = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+          const uint32_t other = __builtin_amdgcn_mov_dpp(own, 0xb1, 0xf, 0xf, true);
+          const uint32_t both = __builtin_amdgcn_perm(own, other, zsel);
+          za[0] = __builtin_amdgcn_update_dpp(za[0], both, 0x44, 0xf, 0x4, false);
+          za[1] = __builtin_amdgcn_update_dpp(za[1], both, 0xee, 0xf, 0x4, false);
+          za[2] = __builtin_amdgcn_update_dpp(za[2], both, 0x44, 0xf, 0x8, false);
+          za[3] = __builtin_amdgcn_update_dpp(za[3], both, 0xee, 0xf, 0x8, false);
+        }
         bf16x8_t ph[NT], pl[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -420,6 +439,12 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
 #pragma unroll
           for (int i = 0; i < E / 2; ++i) {
             const uint32_t h = pack_bf16(pw[2 * i], pw[2 * i + 1]);
+            if constexpr (NT == 2) {
+              hw[i] = h;
+              pw[2 * i] = __uint_as_float(h << 16);
+              pw[2 * i + 1] = __uint_as_float(h & 0xffff0000u);
+              continue;
+            }
             const float h0 = __uint_as_float(h << 16), h1 = __uint_as_float(h & 0xffff0000u);
             const uint32_t lo = pack_bf16(pw[2 * i] - h0, pw[2 * i + 1] - h1);
             hw[i] = h;
@@ -427,11 +452,11 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
             pw[2 * i] = h0 + __uint_as_float(lo << 16);
             pw[2 * i + 1] = h1 + __uint_as_float(lo & 0xffff0000u);
           }
-          by_index<E>([&](auto i) INLINE { zs[nt][g] += lane_of<SP, 8 + i.value>(zf[SP - 1][g]) * pw[i.value]; });
+          if constexpr (!kMat) by_index<E>([&](auto i) INLINE { zs[nt][g] += lane_of<SP, 8 + i.value>(zf[SP - 1][g]) * pw[i.value]; });
           u32x4_t hx, lx;
           if constexpr (SP == 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) hx[i] = hw[i], lx[i] = lw[i];
+            for (int i = 0; i < 4; ++i) hx[i] = hw[i], lx[i] = NT == 1 ? lw[i] : 0;
           } else {   // a column's weights stand at its record's positions, zeros at the other's
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -442,6 +467,9 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
           }
           ph[nt] = __builtin_bit_cast(bf16x8_t, hx);
           pl[nt] = __builtin_bit_cast(bf16x8_t, lx);
+          if constexpr (kMat)
+            zo[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8_t, u32x4_t{za[0], za[1], za[2], za[3]}), ph[nt], zo[nt], 0, 0, 0);
         }
 #pragma unroll
         for (int j = g * PG * 2; j < (g + 1) * PG * 2; ++j) {
@@ -454,7 +482,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             o[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ph[nt], o[nt][j], 0, 0, 0);
-            o[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pl[nt], o[nt][j], 0, 0, 0);
+            if constexpr (NT == 1) o[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pl[nt], o[nt][j], 0, 0, 0);
           }
         }
       }
@@ -496,6 +524,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       l[nt] = quad_sum(l[nt]);
+      if (kMat) zs[nt][0] = kg >= 2 ? zo[nt][0] + zo[nt][1] : 0.f;   // rows 8, 9 and 12, 13
 #pragma unroll
       for (int g = 0; g < NG; ++g) zs[nt][g] = quad_sum(zs[nt][g]);
       if (kg == 0) sm[wave][n16] = m[nt];

@@ -12,13 +12,16 @@ p_j (they sum to 1) over values v_j:
   weights: an error e of every logit changes y by at most (e^(2e) - 1)·Σ p|v|;
       exp2 and its argument add 8u + u·|logit|·4 relative to each weight.
   values, cache: weights times s as two bf16 parts, 2^-16 of p·s; two chains over t
-      positions, (2·t + 16)·u·Σ p·s·(271 + |z|).
+      positions, (2·t + 16)·u·Σ p·s·(271 + |z|).  Where a sequence brings more than 16
+      query rows for a key head, weights times s are rounded once instead: both chains
+      take the rounded weight w, so that y = Σ w·(c - z) with w = p·s·(1 + d), |d| <= B,
+      and that costs B·Σ p·s·|c - z| = B·Σ p|v|.
   values, bf16: a weight is rounded once, B of it: B·Σ p|v|; (2·t + 16)·u·Σ p|v|.
   result: rounded once, B·|y|.
 
 These are worst cases.  In the root mean square a rounding to bf16 is at most
 B/sqrt(3) of the value, and independent from one weight to the next:
-      |Y - y|_F <= B/sqrt(3)·(|y|_F + |sqrt(Σ p² v²)|_F) (the second term: bf16 weights only),
+      |Y - y|_F <= B/sqrt(3)·(|y|_F + |sqrt(Σ p² v²)|_F) (the second term: weights rounded once only),
 and MARGIN = 1.1 covers the fp32 parts, which are below 2^-14 of that for the sizes here.
 """
 from __future__ import annotations
@@ -108,6 +111,7 @@ def reference(q, k, v, scale, total, news, grid=None):
     share = heads // k.shape[1]
     ys, es, ss = [], [], []
     qa = ka = 0
+    once = grid is None or max(news) * share > 16
     for t, n in zip(total, news):
         y, e, s2 = (np.zeros((n, heads, dim)) for _ in range(3))
         for h in range(heads):
@@ -122,8 +126,7 @@ def reference(q, k, v, scale, total, news, grid=None):
             pv = p @ np.abs(vh)
             if grid is None:
                 ex = (2 * dim + 8) * U * abs(scale) * (np.abs(qh) @ np.abs(kh).T)
-                ev = (2 * t + 16) * U * pv + B * pv
-                s2[:, h] = (p ** 2) @ (vh ** 2)
+                ev = (2 * t + 16) * U * pv
             else:
                 (ks, kz), (vs, vz), group = grid
                 ks, kz, vs, vz = (a[ka:ka + t, h // share] for a in (ks, kz, vs, vz))
@@ -132,6 +135,9 @@ def reference(q, k, v, scale, total, news, grid=None):
                                        + dim / 32 * (np.abs(qh) @ np.abs(kh).T))
                 ps = np.repeat(p @ (vs * (271 + np.abs(vz))), group, axis=1)
                 ev = (2 * t + 16) * U * ps + 2.0 ** -16 * np.repeat(p @ (vs * (16 + np.abs(vz))), group, axis=1)
+            if once:
+                ev = ev + B * pv
+                s2[:, h] = (p ** 2) @ (vh ** 2)
             ex = np.max(np.where(seen, ex, 0), axis=1, keepdims=True, initial=0)
             xa = np.max(np.where(seen, np.abs(x), 0), axis=1, keepdims=True, initial=0)
             rel = np.expm1(2 * ex) + 16 * U + 8 * U * xa
