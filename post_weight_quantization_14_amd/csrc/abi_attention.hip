@@ -112,6 +112,14 @@ gptq_status check_page_bytes(const KvLayout& L, int64_t pages) {
   return GPTQ_OK;
 }
 
+gptq_status check_beside_pages(const HeadRows& k, const HeadRows& v, const KvLayout& L, int64_t tokens, int size,
+                               const void* pages, int64_t count) {
+  const Span cache{pages, L.page_bytes * count};
+  if (meet(span_of(k, tokens, L.heads, L.dim, size), cache) || meet(span_of(v, tokens, L.heads, L.dim, size), cache))
+    return fail(GPTQ_ERR_INVALID_ARG, "K or V overlaps the pages");
+  return GPTQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -141,6 +149,7 @@ gptq_status gptq_kv_append(const gptq_kv_config* cfg, const void* K, const void*
   GPTQ_TRY(check_rows("K", K, dtype, tokens, L.heads, L.dim, ldk, k_head_stride, &k));
   GPTQ_TRY(check_rows("V", V, dtype, tokens, L.heads, L.dim, ldv, v_head_stride, &v));
   GPTQ_TRY(check_seqs(cu_seqlens, kv_lens, page_table, batch, tokens, table_width, table_stride, num_pages, status, pages, &q));
+  GPTQ_TRY(check_beside_pages(k, v, L, tokens, dtype == GPTQ_FP32 ? 4 : 2, pages, num_pages));
   return run_kv_append(L, k, v, dtype, q, pages, static_cast<hipStream_t>(stream));
 }
 
@@ -162,9 +171,7 @@ gptq_status gptq_kv_read(const gptq_kv_config* cfg, void* K, void* V, int32_t dt
   GPTQ_TRY(check_seqs(cu_seqlens, kv_lens, page_table, batch, tokens, table_width, table_stride, num_pages, status, pages, &q));
   const int size = dtype == GPTQ_FP32 ? 4 : 2;
   if (overlap(k, L.heads, v, L.heads, tokens, L.dim, size, size)) return fail(GPTQ_ERR_INVALID_ARG, "K overlaps V");
-  const Span cache{pages, L.page_bytes * num_pages};
-  if (meet(span_of(k, tokens, L.heads, L.dim, size), cache) || meet(span_of(v, tokens, L.heads, L.dim, size), cache))
-    return fail(GPTQ_ERR_INVALID_ARG, "K or V overlaps the pages");
+  GPTQ_TRY(check_beside_pages(k, v, L, tokens, size, pages, num_pages));
   return run_kv_read(L, k, v, dtype, q, pages, static_cast<hipStream_t>(stream));
 }
 
@@ -228,7 +235,8 @@ gptq_status gptq_prompt_attention(const void* Q, const void* K, const void* V, i
   GPTQ_TRY(check_rows("V", V, GPTQ_BF16, tokens, kv_heads, head_dim, ldv, v_head_stride, &c.V));
   GPTQ_TRY(check_rows("Y", Y, GPTQ_BF16, tokens, heads, head_dim, ldy, y_head_stride, &c.Y));
   if (bad_ptr(cu_seqlens, 4)) return fail(GPTQ_ERR_INVALID_ARG, "cu_seqlens is NULL or misaligned");
-  if ((tokens / 128 + std::min(batch, tokens) + 1 + 8) * heads > INT32_MAX)
+  // workgroups of 256 threads, of which a grid holds fewer than 2^32
+  if ((tokens / 128 + std::min(batch, tokens) + 1 + 8) * heads >= int64_t(1) << 24)
     return fail(GPTQ_ERR_UNSUPPORTED, "%lld tokens of %lld sequences of %d heads in one call", (long long)tokens,
                 (long long)batch, heads);
   if (overlap(c.Q, heads, c.Y, heads, tokens, head_dim, 2, 2) || overlap(c.K, kv_heads, c.Y, heads, tokens, head_dim, 2, 2) ||

@@ -32,6 +32,7 @@ typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
 //   Byte b of a value unit holds channels 32·b + 2i (low nibble) and 32·b + 2i + 1.
 //   A param word is bf16(s) << 16 | (uint16)z.
 constexpr int kKvRec = 16;
+constexpr int64_t kKvMost = int64_t(1) << 30;   // positions of a sequence: sums of two stay in 31 bits
 
 struct KvLayout {
   int heads, dim, group, recs;   // recs: records of one head in a page (a power of two)

@@ -69,7 +69,6 @@ struct Split {
   uint32_t hq0;       // query head of the first row within the group
   int rows, slot;     // of the first part; part i > 0 is slot 2·(workgroup + i)
   int parts;          // 0: no such unit
-  int pad;
 };
 
 struct Work {
@@ -99,7 +98,7 @@ struct Units {
   int64_t upto, own;   // steps of sequences 0 .. lane, and of this lane's
   bool few;
   __device__ __forceinline__ explicit Units(const Work& w_) : w(w_) {
-    capacity = min64(w.q.width * w.L.recs * kKvRec, INT32_MAX);
+    capacity = min64(w.q.width * w.L.recs * kKvRec, kKvMost);
     few = w.q.batch <= 64;
     const int lane = threadIdx.x & 63;
     if (few) {
@@ -520,7 +519,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
     const int slot = pos == begin ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1;
     float* part = w.partial + (int64_t)slot * R * (D + 2);
     if (!whole && s0 == 0 && tid == 0)
-      w.meta[blockIdx.x] = Split{s.row + tq0, head, hq0, rows, slot, (int)((pos + steps - 1) / piece) - (int)blockIdx.x + 1, 0};
+      w.meta[blockIdx.x] = Split{s.row + tq0, head, hq0, rows, slot, (int)((pos + steps - 1) / piece) - (int)blockIdx.x + 1};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       l[nt] = quad_sum(l[nt]);

@@ -127,7 +127,7 @@ struct Eight {
 // A sequence whose tokens all have a position: one with fewer positions than
 // tokens is out of range here.
 __device__ __forceinline__ KvSeq written_seq(const KvSeqs& q, const KvLayout& L, int64_t b) {
-  KvSeq s = kv_seq(q, b, std::min<int64_t>(q.width * L.recs * kKvRec, INT32_MAX));
+  KvSeq s = kv_seq(q, b, std::min<int64_t>(q.width * L.recs * kKvRec, kKvMost));
   if (s.n > s.len) {
     s.bad = true;
     s.len = s.n;

@@ -77,9 +77,9 @@ def test_cache_argument_errors(L, lb, name):
     assert call(width=0) == bad and call(stride=4) == bad and call(count=0) == bad and call(count=-4) == bad
     assert call(width=1 << 31, stride=1 << 31) == no and call(count=1 << 31) == no
     assert call(pages=None) == bad and call(pages=FAR + 8) == bad
+    assert call(K=FAR + 64) == bad and call(V=FAR + 20 * 18432 - 2) == bad
     if name == "gptq_kv_read":
         assert call(V=FAKE) == bad and call(V=FAKE + 1024 * 7 + 512) == bad
-        assert call(K=FAR + 64) == bad and call(V=FAR + 20 * 18432 - 2) == bad
 
 
 def test_attention_argument_errors(L, lb):
@@ -131,6 +131,8 @@ def test_prompt_argument_errors(L, lb):
     assert call(tokens=-1) == bad and call(batch=-2) == bad and call(heads=0) == bad and call(kvh=0) == bad
     assert call(heads=6) == bad and call(heads=4100, kvh=4100) == no and call(dim=96) == no and call(dim=0) == no
     assert call(tokens=1 << 28) == no and call(tokens=1 << 27, heads=4096, ldq=4096 * 64, ldy=4096 * 64, Y=1 << 60) == no
+    # more workgroups than a grid holds
+    assert call(tokens=1 << 24, batch=1 << 20, heads=64, ldq=4096, ldy=4096, Y=1 << 60) == no
     for s in (math.inf, math.nan):
         assert call(scale=s) == bad
     for name in ("Q", "K", "V", "Y", "cu"):
