@@ -5,6 +5,19 @@
 //   y_d = Σ_t p'(t)·(128 + c_d(t)) - Σ_t p'(t)·(128 + z(t)),  p' = softmax(t)·s(t):
 // 128 + c is a bf16 made from four bits by one AND-OR, so keys enter the matrix
 // cores exactly; scales and zero points are taken off in fp32.
+//
+// What bounds it.  A step of 32 positions reads 4.6 KB (heads of 128, one scale
+// each) and takes about 230 vector instructions for up to 8 rows, most of them to
+// spread codes, then some 100 more for every further 16.  Decoding many sequences
+// is near memory: 64 of up to 8192 tokens with 8 key heads (288 MB) take 78 us, 3.7
+// TB/s; the same loads without the arithmetic 68 us; the vector unit is busy 68% of
+// the time, the matrix cores 22%.  Long steps in flight do not help (two ahead instead
+// of one: 83 us, three: 87), nor do three waves a SIMD (79 us).
+//   One sequence of 32768 tokens (38 MB) takes 19.5 us: 14 in pieces (a wave has four
+// steps; before them three loads wait for each other: lengths, page numbers, codes)
+// and 5 to join 64 of them.  One of 512 takes 7.6 us, 5.1 without arithmetic.
+//   A chunk of 512 tokens over 8192 takes 112 us, 0.6 PFLOP/s: here the vector
+// unit spreads the codes again for every 32 rows.
 #include "attention.hpp"
 
 namespace gptq {
@@ -15,7 +28,7 @@ typedef __attribute__((address_space(4))) int32_t constant_int;
 
 constexpr int kStep = 32;        // positions of a wave's step: two records
 constexpr float kNone = -3e38f;  // a running maximum that has seen nothing
-constexpr int kMaxWgs = 512;     // of a split call
+constexpr int kMaxWgs = 512;     // of a split call: two a CU (768: 1 x 32768 28 us instead of 20, for the parts to join)
 
 __device__ __forceinline__ float swap16(float x, float* y) {   // lane ^ 16
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -192,6 +205,13 @@ __device__ __forceinline__ void value_pairs(const uint32_t (&w)[D / 32], int b, 
 // W waves share a unit's steps.  WHOLE: a workgroup takes one unit; otherwise each
 // takes an equal piece of all units' steps, and units cut by a piece's end are
 // joined by kv_join_kernel.
+//   Rows are columns of the products.  With SP 2 (up to 8 rows) both halves of the 16
+// columns hold the same rows; the left half keeps the logits of the step's first
+// record, the right half those of the second, each with sums of its own, so that no
+// lane works for rows that are not there: 64 sequences 86 -> 79 us.  NT 2 holds 32
+// rows: codes are spread once for both tiles, weights are rounded to bf16 once
+// (2^-8 of each, as the result is; with two parts 140 us instead of 112 for the chunk
+// above), and with one scale a head a product sums the zero points as well.
 template <int D, int G, int NT, int SP, int W, bool WHOLE>
 __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
   constexpr int kThreads = 64 * W, R = 16 * NT / SP, NC = 16 / SP, E = 8 / SP, KS = D / 32, NG = D / G, MT = D / 16, PG = G / 32;   // PG: 32-channel steps of a group
@@ -589,7 +609,9 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
 // Joins the parts of units that were split: a wave takes a row of a unit at a time.
 // The units are few and anywhere among `meta`, so each workgroup lists them first.
 // What this costs is a chain of loads, not their bytes: a row's parts are all in
-// flight at once, 64 at the most.
+// flight at once, 64 at the most.  5 us after 1 x 32768 tokens, 4 after a chunk;
+// four waves a row, or lists in LDS that spare the second look at `meta`, won nothing
+// there and cost 64 ragged sequences 3 us.
 constexpr int kJoinWgs = 512;
 template <int D, int R>
 __global__ __launch_bounds__(256) void kv_join_kernel(Work w, int wgs, int most_rows) {
