@@ -803,6 +803,13 @@ def _heads(name: str, t: torch.Tensor, tokens: int, heads: int, dim: int) -> tup
     return ld, hs
 
 
+def _new_heads(tokens: int, heads: int, dim: int, dtype: torch.dtype, X: torch.Tensor, stream) -> torch.Tensor:
+    """_empty's [tokens, heads, dim], by the cheapest of torch's ways where the stream is the current one."""
+    if stream is None:
+        return torch.empty_strided((tokens, heads, dim), (heads * dim, dim, 1), dtype=dtype, device=X.device)
+    return _empty((tokens, heads, dim), dtype, X, stream)
+
+
 def _sequences(cfg: KvConfig, X: torch.Tensor, other: Optional[torch.Tensor], pages: torch.Tensor,
                page_table: torch.Tensor, kv_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor],
                status: Optional[torch.Tensor]) -> tuple:
@@ -873,15 +880,19 @@ def gptq_kv_read(cfg: KvConfig, pages: torch.Tensor, page_table: torch.Tensor, k
     """(K, V) [tokens, kv_heads, head_dim], bf16 or fp32: the last
     cu_seqlens[b + 1] - cu_seqlens[b] positions of each sequence (None: the last
     one), as the cache keeps them."""
-    shape = (tokens, cfg.kv_heads, cfg.head_dim)
+    heads, dim = cfg.kv_heads, cfg.head_dim
+    kld = vld = heads * dim
+    khs = vhs = dim
     if K is None:
-        K = _empty(shape, out_dtype, pages, stream)
+        K = _new_heads(tokens, heads, dim, out_dtype if V is None else V.dtype, pages, stream)
+    else:
+        kld, khs = _heads("K", K, tokens, heads, dim)
     if V is None:
-        V = _empty(shape, K.dtype, pages, stream)
-    kld, khs = _heads("K", K, *shape)
-    vld, vhs = _heads("V", V, *shape)
-    if K.dtype is not V.dtype:
-        raise TypeError("K and V must have one dtype")
+        V = _new_heads(tokens, heads, dim, K.dtype, pages, stream)
+    else:
+        vld, vhs = _heads("V", V, tokens, heads, dim)
+        if K.dtype is not V.dtype:
+            raise TypeError("K and V must have one dtype")
     seqs, status = _sequences(cfg, K, V, pages, page_table, kv_lens, cu_seqlens, status)
     st = _run_on(K, lib().gptq_kv_read, (cfg._ref, K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kld, khs, vld, vhs,
                                          *seqs, status, _stream_on(K, stream)))
@@ -908,13 +919,13 @@ def gptq_kv_attention(cfg: KvConfig, Q: torch.Tensor, pages: torch.Tensor, page_
     dim = cfg.head_dim
     if Q.dim() != 3:
         raise ValueError(f"Q must be [tokens, heads, {dim}]")
-    tokens, heads, _ = shape = tuple(Q.shape)
+    tokens, heads, _ = Q.shape
     qld, qhs = _heads("Q", Q, tokens, heads, dim)
     if Q.dtype is not torch.bfloat16:
         raise TypeError(f"Q must be bfloat16, not {Q.dtype}")
     seqs, status = _sequences(cfg, Q, Y, pages, page_table, kv_lens, cu_seqlens, status)
     if Y is None:
-        Y = _empty(shape, torch.bfloat16, Q, stream)
+        Y = _new_heads(tokens, heads, dim, torch.bfloat16, Q, stream)
         yld, yhs = heads * dim, dim
     else:
         yld, yhs = _heads("Y", Y, tokens, heads, dim)
@@ -948,7 +959,7 @@ def gptq_prompt_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_
     read one key head.  scale: 1/sqrt(head_dim) if None."""
     if Q.dim() != 3 or K.dim() != 3:
         raise ValueError("Q and K must be [tokens, heads, head_dim]")
-    tokens, heads, dim = shape = tuple(Q.shape)
+    tokens, heads, dim = Q.shape
     kv_heads = K.shape[1]
     qld, qhs = _heads("Q", Q, tokens, heads, dim)
     kld, khs = _heads("K", K, tokens, kv_heads, dim)
@@ -957,7 +968,7 @@ def gptq_prompt_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_
     if not (0 <= dev == K.get_device() == V.get_device() == cu_seqlens.get_device() and (Y is None or Y.get_device() == dev)):
         _on(Q, K=K, V=V, cu_seqlens=cu_seqlens, Y=Y)
     if Y is None:
-        Y = _empty(shape, torch.bfloat16, Q, stream)
+        Y = _new_heads(tokens, heads, dim, torch.bfloat16, Q, stream)
         yld, yhs = heads * dim, dim
     else:
         yld, yhs = _heads("Y", Y, tokens, heads, dim)
