@@ -9,7 +9,10 @@ namespace {
 #define INLINE __attribute__((always_inline))
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kBM = 32 * kWaves;   // queries of a workgroup, 32 a wave
+// Queries of a workgroup: 32 a wave, or 32 for the KH waves that take a part of a
+// tile's keys each.
+template <int KH>
+constexpr int kBM = 32 * kWaves / KH;
 constexpr int kBN = 64;            // keys of a tile
 constexpr float kNone = -3e38f;
 
@@ -42,6 +45,7 @@ struct Prompt {
   HeadRows Q, K, V, Y;
   const int32_t* cu;
   int64_t batch, tokens, tiles;
+  int64_t fold;     // tiles of each head that go from the last to the first; those after them the other way
   int kv_heads, share;
   float scale;      // times log2(e), positive: a masked logit times it stays -Inf
   uint32_t keep, flip;   // Q's bits and signs: a scale of 0 clears it, a negative one flips it
@@ -59,22 +63,26 @@ struct Prompt {
 // reads from it it falls by 10%; waves in two groups that take turns at products and
 // weights, raised priorities or another order of tiles gave the same within a few percent.
 //   One prompt is bound by its longest workgroup: 2048 tokens of 32 heads 47 us, of
-// one head 38: 32 tiles of 1.05 us in a row and about 6 us around them.
+// one head 38 where a wave takes all keys: 32 tiles of 1.05 us in a row and about 6 us
+// around them.
 //   Heads of 64 run three waves a SIMD, where the rarely taken second pass spills:
 // 23 prompts of up to 333 tokens 15.2 us, two waves 16.8; 8192 tokens of 32 heads 307
 // and 320; 2048, where one workgroup is waited for, 35 and 34.
-template <int D, bool VEC>
+template <int D, bool VEC, int KH>
 __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_kernel(Prompt a) {
-  constexpr int KS = D / 16, DT = D / 32, CH = D / 8, TB = kBN * D * 2;
+  constexpr int KS = D / 16, DT = D / 32, CH = D / 8, TB = kBN * D * 2, BM = kBM<KH>, U = 2 / KH;   // U: 32 keys each
   // Keys and values of a tile and of the next.  Two objects: the compiler makes a
   // read wait for every copy in flight that may go to the object it reads.
   __shared__ __attribute__((aligned(16))) uint8_t lds0[2 * TB], lds1[2 * TB];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int n32 = lane & 31, half = lane >> 5;
+  const int part = KH == 2 ? wave & 1 : 0;   // of a tile's keys
 
   // Workgroup i runs on XCD i % 8.  The heads that share a key head stay together
   // on one, which then reads those keys from its own L2; tiles with the most keys
-  // go first, so that the last workgroups to start are the shortest.
+  // go first, so that the last workgroups to start are the shortest.  Where all run at
+  // once, two a CU, the second half goes the other way: the longest share a CU with the
+  // shortest (2048 tokens of 32 heads 51.8 us instead of 53.5, 2 x 900 30 instead of 34).
   const int64_t slot = blockIdx.x >> 3, group = slot / a.share * 8 + (blockIdx.x & 7);
   const int64_t kvh = group % a.kv_heads, head = kvh * a.share + slot % a.share;
   if (group >= a.tiles * a.kv_heads) return;
@@ -85,14 +93,15 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
     row0 = r0 < 0 ? 0 : r0 > a.tokens ? a.tokens : r0;
     const int64_t past = r1 > a.tokens ? a.tokens : r1;
     len = past > row0 ? (int)(past - row0) : 0;
-    return (int64_t)((len + kBM - 1) / kBM);
+    return (int64_t)((len + BM - 1) / BM);
   };
-  if (!ragged_find(a.tiles - 1 - group / a.kv_heads, a.batch, count, &b, &at, &from)) return;
+  const int64_t rank = group / a.kv_heads;
+  if (!ragged_find(rank < a.fold ? a.tiles - 1 - rank : rank - a.fold, a.batch, count, &b, &at, &from)) return;
   row0 = lane_value(row0, from);
   len = __builtin_amdgcn_readlane(len, from);
-  const int q0 = (int)at * kBM, w0 = q0 + wave * 32;   // the workgroup's and the wave's first query
+  const int q0 = (int)at * BM, w0 = q0 + wave / KH * 32;   // the workgroup's and the wave's first query
   const int iq = w0 + n32;                             // the lane's query
-  const int keys = std::min(len, q0 + kBM);            // that any of its queries sees
+  const int keys = std::min(len, q0 + BM);            // that any of its queries sees
   const int tiles = (keys + kBN - 1) / kBN;
 
   const uint16_t* Kp = static_cast<const uint16_t*>(a.K.p) + row0 * a.K.ld + kvh * a.K.hs;
@@ -156,10 +165,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
   // buffer a read is of.
   int kat[KS], vlo[DT], vhi[DT];
 #pragma unroll
-  for (int ks = 0; ks < KS; ++ks) kat[ks] = lds_at<D>(n32, ks * 2 + half);
+  for (int ks = 0; ks < KS; ++ks) kat[ks] = lds_at<D>(n32, ks * 2 + half) + part * 32 * D * 2;   // 32 rows further: the same swizzle
 #pragma unroll
   for (int d = 0; d < DT; ++d) {
-    const int t = half * 4 + (lane >> 2 & 3), c = d * 32 + (lane >> 4 & 1) * 16 + (lane & 3) * 4;
+    const int t = part * 32 + half * 4 + (lane >> 2 & 3), c = d * 32 + (lane >> 4 & 1) * 16 + (lane & 3) * 4;
     vlo[d] = lds_at<D>(t, c >> 3) + (c & 7) * 2;
     vhi[d] = lds_at<D>(t + 8, c >> 3) + (c & 7) * 2;
   }
@@ -185,38 +194,39 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       if (tile + 1 < tiles) fetch(tile + 1, nxt);
-      const int k0 = tile * kBN;
+      const int k0 = tile * kBN + part * 32;   // the wave's first key
       if (k0 > w0 + 31) return;   // the wave's queries see none of it (no barrier is skipped)
-      f32x16_t s[2];
+      f32x16_t s[U];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {   // two sums by turns: a product need not wait for the one before
+        for (int u = 0; u < U; ++u) {   // two sums by turns: a product need not wait for the one before
           const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(cur + (kat[ks] + u * 32 * D * 2));
           s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[ks], s[u], 0, 0, 0);
         }
-      __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);   // operands are read eight products ahead
+      constexpr int kAhead = U * KS < 8 ? U * KS : 8;
+      __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);   // operands are read eight products ahead
 #pragma unroll
-      for (int i = 0; i < 2 * KS - 8; ++i) {
+      for (int i = 0; i < U * KS - kAhead; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
-      __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
-      const bool edge = k0 + kBN > w0 + 1;   // some query does not see some key
+      __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+      const bool edge = k0 + 32 * U > w0 + 1;   // some query does not see some key
       if (edge) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int r = 0; r < 16; ++r)
             if (k0 + u * 32 + 8 * (r >> 2) + 4 * half + (r & 3) > iq) s[u][r] = -INFINITY;
       }
       float top = s[0][0];
 #pragma unroll
-      for (int r = 1; r < 32; ++r) top = fmaxf(top, s[r >> 4][r & 15]);
+      for (int r = 1; r < 16 * U; ++r) top = fmaxf(top, s[r >> 4][r & 15]);
       top = half_max(top) * a.scale;
       if (__ballot(top > m + 8.f)) {   // sums are scaled again only when the maximum grows by more than 2^8
         const float up = fmaxf(m, top), f = exp2f(m - up);
@@ -225,9 +235,9 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] *= f;
       }
-      bf16x8_t p[4];
+      bf16x8_t p[2 * U];
 #pragma unroll
-      for (int r = 0; r < 32; ++r) {
+      for (int r = 0; r < 16 * U; ++r) {
         const float e = __builtin_amdgcn_exp2f(fmaf(s[r >> 4][r & 15], a.scale, -m));
         l += e;
         p[r >> 3][r & 7] = (__bf16)e;
@@ -240,7 +250,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
       };
       if constexpr (!careful) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
+        for (int kk = 0; kk < 2 * U; ++kk)
 #pragma unroll
           for (int d = 0; d < DT; ++d)
             o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(columns(d, kk), p[kk], o[d], 0, 0, 0);
@@ -251,7 +261,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
 #pragma unroll
           for (int r = 0; r < 16; ++r) more[r] = less[r] = 0.f;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
+          for (int kk = 0; kk < 2 * U; ++kk) {
             bf16x8_t v = columns(d, kk);
             if (edge) {
               bf16x8_t up, down, seen;
@@ -289,6 +299,35 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
   if (pass(std::false_type{})) pass(std::true_type{});
 
   l = half_sum(l);
+  if constexpr (KH == 2) {   // the odd wave's sums to the even one, by way of LDS
+    // [DT][4][64 lanes] pieces of 16 bytes for each two waves, then maxima and sums
+    static_assert(DT * 4 * 64 * 16 <= 2 * TB && kWaves == 4, "");
+    uint8_t* mine = wave < 2 ? lds0 : lds1;
+    __shared__ float om[2][64], ol[2][64];
+    __syncthreads();
+    if (part) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<f32x4_t*>(mine + ((d * 4 + r) * 64 + lane) * 16) =
+              f32x4_t{o[d][4 * r], o[d][4 * r + 1], o[d][4 * r + 2], o[d][4 * r + 3]};
+      om[wave >> 1][lane] = m;
+      ol[wave >> 1][lane] = l;
+    }
+    __syncthreads();
+    if (part) return;
+    const float m1 = om[wave >> 1][lane], up = fmaxf(m, m1), f0 = exp2f(m - up), f1 = exp2f(m1 - up);
+    l = l * f0 + ol[wave >> 1][lane] * f1;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const f32x4_t other = *reinterpret_cast<const f32x4_t*>(mine + ((d * 4 + r) * 64 + lane) * 16);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[d][4 * r + c] = o[d][4 * r + c] * f0 + other[c] * f1;
+      }
+  }
   if (iq < len) {
     const float inv = 1.f / l;
     uint16_t* yp = const_cast<uint16_t*>(static_cast<const uint16_t*>(a.Y.p)) + (row0 + iq) * a.Y.ld + head * a.Y.hs + 4 * half;
@@ -309,24 +348,37 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
   }
 }
 
-}  // namespace
-
-gptq_status run_prompt_attention(const PromptCall& c, hipStream_t stream) {
-  const int64_t tiles = (c.tokens + (kBM - 1) * std::min(c.batch, c.tokens)) / kBM;   // n tokens take at most (n + kBM - 1) / kBM
-  Prompt a{c.Q, c.K, c.V, c.Y, c.cu, c.batch, c.tokens, tiles, c.kv_heads, c.heads / c.kv_heads,
+template <int KH>
+gptq_status launch(const PromptCall& c, hipStream_t stream) {
+  constexpr int BM = kBM<KH>;
+  const int64_t tiles = (c.tokens + (BM - 1) * std::min(c.batch, c.tokens)) / BM;   // n tokens take at most (n + BM - 1) / BM
+  Prompt a{c.Q, c.K, c.V, c.Y, c.cu, c.batch, c.tokens, tiles, tiles * c.heads <= 512 ? 256 / c.heads : tiles, c.kv_heads, c.heads / c.kv_heads,
            c.scale == 0.f ? 1.f : fabsf(c.scale) * 1.44269504088896340736f, c.scale == 0.f ? 0u : ~0u,
            c.scale < 0.f ? 0x80008000u : 0u};
   const unsigned grid = (unsigned)(ceil_div(tiles * c.kv_heads, 8) * 8 * (c.heads / c.kv_heads));
   const int64_t most = int64_t(1) << 23;   // a tile's rows are 32-bit offsets apart
   const bool vec = c.Q.vec && c.K.vec && c.V.vec && c.Y.vec && c.K.ld < most && c.V.ld < most;
   if (c.dim == 128)
-    vec ? prompt_attention_kernel<128, true><<<grid, kThreads, 0, stream>>>(a)
-        : prompt_attention_kernel<128, false><<<grid, kThreads, 0, stream>>>(a);
+    vec ? prompt_attention_kernel<128, true, KH><<<grid, kThreads, 0, stream>>>(a)
+        : prompt_attention_kernel<128, false, KH><<<grid, kThreads, 0, stream>>>(a);
   else
-    vec ? prompt_attention_kernel<64, true><<<grid, kThreads, 0, stream>>>(a)
-        : prompt_attention_kernel<64, false><<<grid, kThreads, 0, stream>>>(a);
+    vec ? prompt_attention_kernel<64, true, KH><<<grid, kThreads, 0, stream>>>(a)
+        : prompt_attention_kernel<64, false, KH><<<grid, kThreads, 0, stream>>>(a);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
+}
+
+}  // namespace
+
+// Two waves share 32 queries, each with half of every tile's keys, where workgroups
+// of 128 queries leave CUs idle: their chain of tiles is what is waited for.  us
+// (shared / not): 8 heads of 128, 2048 tokens (128 workgroups of 128) 30 / 40, 4096
+// (256) 58 / 75, 8192 (512) 162 / 165; 32 heads, 500 tokens 12.1 / 15.5, 2048 (512) 57 /
+// 54; 8 heads of 64, 8192 (512) 91 / 112, but 23 prompts of 200, 14 heads (812) 17.4 /
+// 13.2.  Prompts of one tile have nothing to share: 64 tokens 7.3 / 6.7.
+gptq_status run_prompt_attention(const PromptCall& c, hipStream_t stream) {
+  const int64_t wgs = (c.tokens + 127 * std::min(c.batch, c.tokens)) / 128 * c.heads;
+  return wgs <= (c.dim == 64 ? 512 : 256) && c.tokens > kBN * c.batch ? launch<2>(c, stream) : launch<1>(c, stream);
 }
 
 }  // namespace gptq

@@ -224,6 +224,31 @@ def test_either_side_of_the_one_launch_limit(pq, width, heads, kv_heads, dim, gr
     against_cache(y, q, k, v, cfg, total, new, f"width {width}")
 
 
+# up to 256 workgroups of 128 queries (heads of 64: 512) two waves share 32 queries, beyond that each has its own:
+# three sequences of 512 tokens are 6 of them a head
+@pytest.mark.parametrize("heads,dim", [(1, 128), (42, 128), (43, 128), (1, 64), (85, 64), (86, 64)])
+@pytest.mark.parametrize("total", [[512], [300, 212], [65, 383, 64]])
+def test_either_form_of_prompts(pq, heads, dim, total):
+    """Results, and a NaN value and an infinite key that only the last tokens see."""
+    T = sum(total)
+    q, k, v = (torch.randn(T, h, dim, generator=torch.Generator().manual_seed(h + dim)).to(torch.bfloat16)
+               for h in (heads, 1, 1))
+    some = sorted({0, heads // 2, heads - 1})
+    ref = reference(f64(q[:, some]), f64(k), f64(v), dim ** -0.5, total, total)
+    cu = starts(total).cuda()
+    y = pq.gptq_prompt_attention(q.cuda(), k.cuda(), v.cuda(), cu)
+    check(y[:, some], *ref, f"{heads} heads of {dim}, {total}")
+    last = total[0] - 1
+    v[last] = float("nan")
+    k[T - 1, 0, 0] = float("inf")
+    z = pq.gptq_prompt_attention(q.cuda(), k.cuda(), v.cuda(), cu)
+    rest = [i for i in range(T) if i not in (last, T - 1)]
+    check(z[rest][:, some], *(r[rest] for r in ref), "but the last")
+    assert torch.isnan(z[last]).all()
+    again = pq.gptq_prompt_attention(q.cuda(), k.cuda(), v.cuda(), cu)
+    assert torch.equal(z.view(torch.int16), again.view(torch.int16))
+
+
 @pytest.mark.parametrize("most", [1, 2])
 def test_the_most_heads(pq, most):
     """4096 query heads of one key head."""
