@@ -13,9 +13,9 @@
 // TB/s; the same loads without the arithmetic 68 us; the vector unit is busy 68% of
 // the time, the matrix cores 22%.  Long steps in flight do not help (two ahead instead
 // of one: 83 us, three: 87), nor do three waves a SIMD (79 us).
-//   One sequence of 32768 tokens (38 MB) takes 19.5 us: 14 in pieces (a wave has four
+//   One sequence of 32768 tokens (38 MB) takes 18 us: 13 in pieces (a wave has four
 // steps; before them three loads wait for each other: lengths, page numbers, codes)
-// and 5 to join 64 of them.  One of 512 takes 7.6 us, 5.1 without arithmetic.
+// and 5 to join 32 of them.  One of 512 takes 7.6 us, 5.1 without arithmetic.
 //   A chunk of 512 tokens over 8192 takes 112 us, 0.6 PFLOP/s: here the vector
 // unit spreads the codes again for every 32 rows.
 #include "attention.hpp"
@@ -102,7 +102,6 @@ struct Work {
 // units' steps lie one after the other, by sequence, head and tile (WHOLE: all
 // units, of one step each here).  Lane i keeps what it read of sequence i: batches of
 // up to 64 are read once.
-constexpr int kLeast = 4;   // steps that a workgroup takes at least: one for each wave
 template <int R, bool WHOLE>
 struct Units {
   const Work& w;
@@ -225,7 +224,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
   const Consts kc;
 
   // in steps, or in units where each is taken whole
-  const int64_t even = divide(units.total + gridDim.x - 1, gridDim.x), piece = WHOLE ? 1 : even > kLeast ? even : kLeast;
+  const int64_t even = divide(units.total + gridDim.x - 1, gridDim.x), piece = WHOLE ? 1 : even > W ? even : W;   // a step for each wave
   const int64_t begin = piece * blockIdx.x, end = begin + piece < units.total ? begin + piece : units.total;
   if (!WHOLE && tid == 0) w.meta[blockIdx.x].parts = 0;
   if (w.q.status)
@@ -717,7 +716,10 @@ gptq_status launch(const Work& w, const KvAttentionPlan& p, hipStream_t stream) 
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
   }
-  kv_attention_kernel<D, G, NT, SP, 4, false><<<p.wgs, 256, 0, stream>>>(w);
+  if (p.waves == 8)
+    kv_attention_kernel<D, G, NT, SP, 8, false><<<p.wgs, 512, 0, stream>>>(w);
+  else
+    kv_attention_kernel<D, G, NT, SP, 4, false><<<p.wgs, 256, 0, stream>>>(w);
   GPTQ_LAUNCH_CHECK();
   kv_join_kernel<D, 16 * NT / SP><<<kJoinWgs, 256, 0, stream>>>(w, p.wgs, p.rows);
   GPTQ_LAUNCH_CHECK();
@@ -739,6 +741,12 @@ constexpr int64_t kWhole = 1024, kMostUnits = 1 << 22;   // a grid's limit is 2^
 // 4 heads a key head over 2048 positions 22.8 us with tiles of 32, 14.7 with 8; 16
 // sequences (384 units of 8 rows) 23.5 and 28.4.
 constexpr int64_t kUnits = 256;
+// Pieces go to 256 workgroups of 8 waves where few units are cut into many parts, so
+// that half of these are joined, and there are steps for all waves; to 512 of 4
+// otherwise.  us (8 waves / 4), one sequence: 1 key head, 32768 positions 16.9 / 22.9,
+// 8 heads 18.2 / 19.7, 8192 of 8 heads 11.8 / 13.8, but 4096 11.3 / 10.3; 16 sequences of
+// 4096, 128 units, 20.6 either way, 64 54.8 / 51.6; a chunk of 512 tokens (512 units) 117 / 112.
+constexpr int64_t kWideUnits = 64, kWidePositions = 256 * 8 * kStep;
 
 KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, int64_t tokens, int64_t max_queries,
                                   int64_t capacity) {
@@ -752,9 +760,15 @@ KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, i
   if (p.whole)
     while (p.tile > 8 && units(p.tile / 2) <= kUnits) p.tile /= 2;
   p.rows = (int)std::min<int64_t>(rows, p.tile);
-  p.wgs = p.whole ? (int)units(p.tile) : kMaxWgs;
-  p.waves = 8;
-  while (p.waves > 1 && (int64_t)p.wgs * p.waves > 2048) p.waves /= 2;
+  if (p.whole) {
+    p.wgs = (int)units(p.tile);
+    p.waves = 8;
+    while (p.waves > 1 && (int64_t)p.wgs * p.waves > 2048) p.waves /= 2;
+  } else {
+    const bool wide = units(tile) <= kWideUnits && units(tile) * capacity >= kWidePositions;
+    p.wgs = wide ? kMaxWgs / 2 : kMaxWgs;
+    p.waves = wide ? 8 : 4;
+  }
   p.partial = (size_t)2 * kMaxWgs * tile * (L.dim + 2) * 4;   // whatever the capacity
   p.total = align256(p.partial) + (size_t)kMaxWgs * sizeof(Split);
   return p;

@@ -249,6 +249,25 @@ def test_either_form_of_prompts(pq, heads, dim, total):
     assert torch.equal(z.view(torch.int16), again.view(torch.int16))
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim,group,news", [(8, 2, 128, 64, 1), (24, 2, 64, 32, 1), (8, 2, 128, 128, 9),
+                                                         (12, 3, 64, 64, 3)])
+@pytest.mark.parametrize("total", [[6000, 40, 1], [700], [33, 2000]])
+def test_few_units_of_long_tables(pq, heads, kv_heads, dim, group, news, total):
+    """Tables for 65536 positions of the units together and more: pieces are taken by eight waves."""
+    new = [min(news, n) for n in total]
+    cfg = pq.KvConfig(kv_heads, dim, group, 64)
+    k, v = keys_values(sum(total), kv_heads, dim, seed=len(total))
+    pages = Pages(pq, cfg, total).fill(k, v)
+    table = torch.full((len(total), 600), -1, dtype=torch.int32, device="cuda")
+    table[:, :pages.table.shape[1]] = pages.table
+    q = torch.randn(sum(new), heads, dim, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    run = lambda: pq.gptq_kv_attention(cfg, q.cuda(), pages.bytes, table, pages.lens,  # noqa: E731
+                                       cu_seqlens=starts(new).cuda(), max_queries=news)
+    y = run()
+    against_cache(y, q, k, v, cfg, total, new, f"{heads} heads, {total}")
+    assert torch.equal(y, run())
+
+
 @pytest.mark.parametrize("most", [1, 2])
 def test_the_most_heads(pq, most):
     """4096 query heads of one key head."""
