@@ -454,7 +454,7 @@ gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const voi
  * results do not depend on anything but the arguments (the same call gives the
  * same bits); no output may overlap an input; tokens == 0 or batch == 0 is a
  * no-op.  Limits (GPTQ_ERR_UNSUPPORTED): head_dim 64 or 128, heads <= 4096,
- * tokens <= 2^27, batch <= 2^20.  A sequence has up to 2^30 positions.
+ * tokens <= 2^27, batch <= 2^16.  A sequence has up to 2^30 positions.
  *
  * The cache is `num_pages` pages of gptq_kv_page_bytes(cfg) bytes (16-byte
  * aligned; owned by the caller; what is in them is private to these calls).  A
@@ -493,13 +493,14 @@ gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const voi
  *   Y = Σ_{p <= t} softmax_p(scale·Q·K̂[p])·V̂[p]
  * for bf16 Q and Y: a token a sequence in decoding, several where drafts are
  * checked, hundreds for a chunk of a prompt.  The tokens are appended first.
- * The codes enter the products exactly; all sums are fp32.  Weights enter as two
- * bf16 parts, but rounded to bf16 where max_queries·heads / kv_heads is above 16.
- * A token that sees no position (kv_lens[b] < n) gives zeros.  max_queries:
- * the most tokens that a sequence has in this call, as far as the caller knows;
- * it chooses between kernels and nothing else (0: one).  `workspace` (256-byte aligned,
- * contents not kept) of gptq_kv_attention_workspace_bytes(cfg, heads, batch,
- * tokens, max_queries) bytes belongs to one call at a time.
+ * The codes enter the products exactly; all sums are fp32 (and stay finite for |Q|
+ * up to 2^108).  Weights enter as two bf16 parts, but rounded to bf16 where
+ * max_queries·heads / kv_heads is above 16.  A token that sees no position
+ * (kv_lens[b] < n) gives zeros.  max_queries: the most tokens that a sequence has
+ * in this call, as far as the caller knows; it chooses between kernels and nothing
+ * else (0: one).  `workspace` (256-byte aligned, contents not kept) of
+ * gptq_kv_attention_workspace_bytes(cfg, heads, batch, tokens, max_queries) bytes
+ * belongs to one call at a time.
  *
  * gptq_prompt_attention: causal attention within each of `batch` sequences of
  * bf16 Q, K, V, before any cache:

@@ -9,7 +9,7 @@ using namespace gptq;
 namespace {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 27;   // rows of a call
-constexpr int64_t kMaxBatch = int64_t(1) << 20;
+constexpr int64_t kMaxBatch = int64_t(1) << 16;   // workgroups look for their sequence 64 at a time
 constexpr int kMaxHeads = 4096;
 
 template <class... A>

@@ -122,6 +122,8 @@ struct Units {
       }
       upto = wave_scan(own);
       total = lane_value(upto, 63);
+    } else if (WHOLE) {
+      total = INT64_MAX;   // find() tells
     } else {
       total = ragged_total(w.q.batch, [&](int64_t b) { return steps_of(kv_seq(w.q, b, capacity)); });
     }
@@ -130,8 +132,8 @@ struct Units {
   static __device__ __forceinline__ int64_t tiles(const KvSeq& s, int share) { return ((int64_t)s.n * share + R - 1) / R; }
   static __device__ __forceinline__ int steps(const KvSeq& s) { return s.len > kStep ? (int)(((int64_t)s.len + kStep - 1) / kStep) : 1; }
   __device__ __forceinline__ int64_t steps_of(const KvSeq& s) const { return tiles(s, w.share) * (WHOLE ? 1 : steps(s)) * w.L.heads; }
-  // the sequence that step `pos` belongs to, and which of its steps it is
-  __device__ __forceinline__ KvSeq find(int64_t pos, int64_t* b, int64_t* at) const {
+  // the sequence that step `pos` belongs to, and which of its steps it is; false past the last
+  __device__ __forceinline__ bool find(int64_t pos, KvSeq* found, int64_t* b, int64_t* at) const {
     KvSeq s = mine;
     int l;
     if (few) {
@@ -143,9 +145,10 @@ struct Units {
         s = kv_seq(w.q, i, capacity);
         return steps_of(s);
       };
-      ragged_find(pos, w.q.batch, count, b, at, &l);
+      if (!ragged_find(pos, w.q.batch, count, b, at, &l)) return false;
     }
-    return lane_value(s, l);
+    *found = lane_value(s, l);
+    return true;
   }
 };
 
@@ -233,7 +236,8 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
 
   for (int64_t pos = begin; pos < end;) {
     int64_t b = 0, at = 0;
-    const KvSeq s = units.find(pos, &b, &at);
+    KvSeq s;
+    if (!units.find(pos, &s, &b, &at)) break;
     const int steps = units.steps(s);
     const int64_t unit = WHOLE ? at : divide(at, steps);          // head · tiles + tile
     const int s0 = WHOLE ? 0 : (int)(at - unit * steps);

@@ -824,9 +824,9 @@ def _sequences(cfg: KvConfig, X: torch.Tensor, other: Optional[torch.Tensor], pa
     page_bytes = cfg._page_bytes or gptq_kv_page_bytes(cfg)
     if page_bytes <= 0:
         raise ValueError("the cache's config is not supported (gptq_kv_page_bytes is 0)")
-    batch = kv_lens.shape[0]
     if kv_lens.dtype is not torch.int32 or kv_lens.dim() != 1 or not kv_lens.is_contiguous():
         raise ValueError("kv_lens must be a contiguous int32 [batch]")
+    batch = kv_lens.shape[0]
     shape, ld = page_table.shape, page_table.stride()
     if page_table.dtype is not torch.int32 or len(shape) != 2 or shape[0] != batch or (shape[1] > 1 and ld[1] != 1):
         raise ValueError(f"page_table must be int32 [{batch}, pages of a sequence] with contiguous rows")

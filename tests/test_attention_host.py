@@ -66,7 +66,7 @@ def test_cache_argument_errors(L, lb, name):
     for kw, st in BAD_CONFIGS:
         assert call(cfg=config(lb, **kw)) == {"bad": bad, "no": no}[st], kw
     assert call(dtype=2) == no and call(dtype=-1) == no
-    assert call(tokens=(1 << 27) + 1) == no and call(batch=(1 << 20) + 1) == no
+    assert call(tokens=(1 << 27) + 1) == no and call(batch=(1 << 16) + 1) == no
     assert call(K=None) == bad and call(V=None) == bad and call(K=FAKE + 1) == bad and call(V=FAKE + 2, dtype=1) == bad
     assert call(ldk=127) == bad and call(khs=127) == bad and call(ldv=-512) == bad and call(vhs=-128) == bad
     assert call(ldk=500) == bad                                  # rows of four heads 128 apart overlap
@@ -132,7 +132,8 @@ def test_prompt_argument_errors(L, lb):
     assert call(heads=6) == bad and call(heads=4100, kvh=4100) == no and call(dim=96) == no and call(dim=0) == no
     assert call(tokens=1 << 28) == no and call(tokens=1 << 27, heads=4096, ldq=4096 * 64, ldy=4096 * 64, Y=1 << 60) == no
     # more workgroups than a grid holds
-    assert call(tokens=1 << 24, batch=1 << 20, heads=64, ldq=4096, ldy=4096, Y=1 << 60) == no
+    assert call(tokens=1 << 24, batch=1 << 16, heads=128, ldq=8192, ldy=8192, Y=1 << 60) == no
+    assert call(batch=(1 << 16) + 1) == no
     for s in (math.inf, math.nan):
         assert call(scale=s) == bad
     for name in ("Q", "K", "V", "Y", "cu"):

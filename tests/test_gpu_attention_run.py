@@ -286,6 +286,25 @@ def test_the_most_heads(pq, most):
     check(y[:, some], *reference(f64(q[:, some]), f64(k), f64(v), 0.125, total, total), "prompt of 4096 heads")
 
 
+@pytest.mark.parametrize("total,news", [([300, 20], 1), ([300, 20], 9), ([1500], 2)])
+def test_queries_of_any_size(pq, total, news):
+    """Queries 2^100 times as large with a scale 2^-100 times as large: the same bits."""
+    cfg = pq.KvConfig(2, 128, 64, 16)
+    k, v = keys_values(sum(total), 2, 128, seed=41)
+    pages = Pages(pq, cfg, total).fill(k, v)
+    new = [news] * len(total)
+    q = torch.randn(sum(new), 8, 128, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    args = (pages.bytes, pages.table, pages.lens, starts(new).cuda(), news)
+    y = pq.gptq_kv_attention(cfg, q, *args, scale=0.125)
+    for e in (100, -60):
+        assert torch.equal(y, pq.gptq_kv_attention(cfg, q * 2.0 ** e, *args, scale=0.125 * 2.0 ** -e))
+    cu, kd, vd = starts(total).cuda(), k.cuda(), v.cuda()
+    q = torch.randn(sum(total), 8, 128, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).cuda()
+    y = pq.gptq_prompt_attention(q, kd, vd, cu, scale=0.125)
+    for e in (100, -60):
+        assert torch.equal(y, pq.gptq_prompt_attention(q * 2.0 ** e, kd, vd, cu, scale=0.125 * 2.0 ** -e))
+
+
 def test_shared_pages_and_a_sequence_twice(pq):
     """Two sequences over the pages of one prefix, and one sequence listed twice."""
     cfg = pq.KvConfig(2, 128, -1, 16)
