@@ -11,7 +11,7 @@
 // spread codes, then some 100 more for every further 16.  Decoding many sequences
 // is near memory: 64 of up to 8192 tokens with 8 key heads (288 MB) take 78 us, 3.7
 // TB/s; the same loads without the arithmetic 68 us; the vector unit is busy 68% of
-// the time, the matrix cores 22%.  Long steps in flight do not help (two ahead instead
+// the time, the matrix cores 22%.  More steps in flight do not help (two ahead instead
 // of one: 83 us, three: 87), nor do three waves a SIMD (79 us).
 //   One sequence of 32768 tokens (38 MB) takes 18 us: 13 in pieces (a wave has four
 // steps; before them three loads wait for each other: lengths, page numbers, codes)
