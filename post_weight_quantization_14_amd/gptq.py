@@ -824,12 +824,19 @@ def _sequences(cfg: KvConfig, X: torch.Tensor, other: Optional[torch.Tensor], pa
     page_bytes = cfg._page_bytes or gptq_kv_page_bytes(cfg)
     if page_bytes <= 0:
         raise ValueError("the cache's config is not supported (gptq_kv_page_bytes is 0)")
-    if kv_lens.dtype is not torch.int32 or kv_lens.dim() != 1 or not kv_lens.is_contiguous():
-        raise ValueError("kv_lens must be a contiguous int32 [batch]")
-    batch = kv_lens.shape[0]
-    shape, ld = page_table.shape, page_table.stride()
-    if page_table.dtype is not torch.int32 or len(shape) != 2 or shape[0] != batch or (shape[1] > 1 and ld[1] != 1):
-        raise ValueError(f"page_table must be int32 [{batch}, pages of a sequence] with contiguous rows")
+    shape = page_table.shape
+    if page_table.dtype is not torch.int32 or len(shape) != 2:
+        raise ValueError("page_table must be int32 [batch, pages of a sequence]")
+    batch, width = shape
+    if kv_lens.dtype is not torch.int32 or kv_lens.shape != (batch,) or not kv_lens.is_contiguous():
+        raise ValueError(f"kv_lens must be a contiguous int32 [{batch}], as page_table has rows")
+    ld = width
+    if not page_table.is_contiguous():
+        ld, one = page_table.stride()
+        if batch == 1:
+            ld = width
+        if width > 1 and one != 1:
+            raise ValueError("page_table must have contiguous rows")
     cu = None
     if cu_seqlens is not None:
         if cu_seqlens.dtype is not torch.int32 or cu_seqlens.shape != (batch + 1,) or not cu_seqlens.is_contiguous():
@@ -842,16 +849,18 @@ def _sequences(cfg: KvConfig, X: torch.Tensor, other: Optional[torch.Tensor], pa
         st = status.data_ptr()
     if not pages.is_contiguous():
         raise ValueError("pages must be contiguous")
-    return (cu, kv_lens.data_ptr(), page_table.data_ptr(), batch, shape[1], ld[0] if batch > 1 else shape[1],
-            pages.data_ptr(), pages.nbytes // page_bytes), st
+    return (cu, kv_lens.data_ptr(), page_table.data_ptr(), batch, width, ld, pages.data_ptr(),
+            pages.nbytes // page_bytes), st
 
 
-def _run_on(X: torch.Tensor, fn, args: tuple) -> int:
-    """fn(*args) with X's GPU as the current device."""
-    if X.get_device() == _current_device():
-        return fn(*args)
+def _run_on(X: torch.Tensor, stream, fn, *args) -> int:
+    """fn(*args, stream) with X's GPU as the current device."""
+    dev = X.get_device()
+    s = _raw_stream(dev) if stream is None and _raw_stream is not None else _stream_on(X, stream)
+    if dev == _current_device():
+        return fn(*args, s)
     with _Device(X):
-        return fn(*args)
+        return fn(*args, s)
 
 
 def gptq_kv_append(cfg: KvConfig, K: torch.Tensor, V: torch.Tensor, pages: torch.Tensor, page_table: torch.Tensor,
@@ -867,8 +876,8 @@ def gptq_kv_append(cfg: KvConfig, K: torch.Tensor, V: torch.Tensor, pages: torch
     if K.dtype is not V.dtype:
         raise TypeError("K and V must have one dtype")
     seqs, status = _sequences(cfg, K, V, pages, page_table, kv_lens, cu_seqlens, status)
-    st = _run_on(K, lib().gptq_kv_append, (cfg._ref, K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kld, khs, vld, vhs,
-                                           *seqs, status, _stream_on(K, stream)))
+    st = _run_on(K, stream, lib().gptq_kv_append, cfg._ref, K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kld, khs,
+                 vld, vhs, *seqs, status)
     if st:
         _check(st, "gptq_kv_append")
 
@@ -883,19 +892,20 @@ def gptq_kv_read(cfg: KvConfig, pages: torch.Tensor, page_table: torch.Tensor, k
     heads, dim = cfg.kv_heads, cfg.head_dim
     kld = vld = heads * dim
     khs = vhs = dim
-    if K is None:
+    own = K is None
+    if own:
         K = _new_heads(tokens, heads, dim, out_dtype if V is None else V.dtype, pages, stream)
     else:
         kld, khs = _heads("K", K, tokens, heads, dim)
     if V is None:
-        V = _new_heads(tokens, heads, dim, K.dtype, pages, stream)
+        V = torch.empty_like(K) if own and stream is None else _new_heads(tokens, heads, dim, K.dtype, pages, stream)
     else:
         vld, vhs = _heads("V", V, tokens, heads, dim)
         if K.dtype is not V.dtype:
             raise TypeError("K and V must have one dtype")
     seqs, status = _sequences(cfg, K, V, pages, page_table, kv_lens, cu_seqlens, status)
-    st = _run_on(K, lib().gptq_kv_read, (cfg._ref, K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kld, khs, vld, vhs,
-                                         *seqs, status, _stream_on(K, stream)))
+    st = _run_on(K, stream, lib().gptq_kv_read, cfg._ref, K.data_ptr(), V.data_ptr(), _dtype_code(K), tokens, kld, khs,
+                 vld, vhs, *seqs, status)
     if st:
         _check(st, "gptq_kv_read")
     return K, V
@@ -936,16 +946,15 @@ def gptq_kv_attention(cfg: KvConfig, Q: torch.Tensor, pages: torch.Tensor, page_
     fn = lib().gptq_kv_attention
     args = (cfg._ref, Q.data_ptr(), tokens, heads, qld, qhs, seqs[0], max_queries, *seqs[1:],
             dim ** -0.5 if scale is None else scale, Y.data_ptr(), yld, yhs, status)
-    s = _stream_on(Q, stream)
     st = _lib.GPTQ_ERR_WORKSPACE
     if workspace is not None:
-        if workspace.get_device() != Q.get_device():
-            raise ValueError(f"workspace is on {workspace.device}, Q on {Q.device}")
-        st = _run_on(Q, fn, (*args, workspace.data_ptr(), _uint8("workspace", workspace), s))
+        if workspace.get_device() != Q.get_device() or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {Q.device}")
+        st = _run_on(Q, stream, fn, *args, workspace.data_ptr(), workspace.nbytes)
     if st == _lib.GPTQ_ERR_WORKSPACE:
         nbytes = max(gptq_kv_attention_workspace_bytes(cfg, heads, seqs[3], tokens, max_queries), 1)
         ws = _empty(nbytes, torch.uint8, Q, stream)
-        st = _run_on(Q, fn, (*args, ws.data_ptr(), nbytes, s))
+        st = _run_on(Q, stream, fn, *args, ws.data_ptr(), nbytes)
     if st:
         _check(st, "gptq_kv_attention")
     return Y
@@ -974,12 +983,12 @@ def gptq_prompt_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_
         yld, yhs = _heads("Y", Y, tokens, heads, dim)
     if not Q.dtype is K.dtype is V.dtype is Y.dtype is torch.bfloat16:
         raise TypeError("Q, K, V and Y must be bfloat16")
-    if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
+    sequences = cu_seqlens.numel() - 1
+    if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or sequences < 0 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be a contiguous int32 [sequences + 1]")
-    st = _run_on(Q, lib().gptq_prompt_attention,
-                 (Q.data_ptr(), K.data_ptr(), V.data_ptr(), tokens, heads, kv_heads, dim, qld, qhs, kld, khs, vld, vhs,
-                  cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, dim ** -0.5 if scale is None else scale, Y.data_ptr(),
-                  yld, yhs, _stream_on(Q, stream)))
+    st = _run_on(Q, stream, lib().gptq_prompt_attention, Q.data_ptr(), K.data_ptr(), V.data_ptr(), tokens, heads, kv_heads,
+                 dim, qld, qhs, kld, khs, vld, vhs, cu_seqlens.data_ptr(), sequences, dim ** -0.5 if scale is None else scale,
+                 Y.data_ptr(), yld, yhs)
     if st:
         _check(st, "gptq_prompt_attention")
     return Y
