@@ -374,3 +374,40 @@ def test_an_oracle_of_the_whole_path(pq):
     ref = oracle.attention(f64(q), kk, vk, 0.125, [20])
     # the result is rounded once: half a step, 2^-8, and the fp32 chains are far below another 2^-12 of the largest
     assert np.all(np.abs(f64(y) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -12 * np.abs(ref).max())
+
+
+def test_refusals_in_words(pq):
+    """What the calls say of tensors that do not fit, before anything is launched."""
+    cfg = pq.KvConfig(2, 64, 32, 16)
+    k, v = (t.cuda() for t in keys_values(20, 2, 64, seed=50))
+    pages = Pages(pq, cfg, [20]).fill(k, v)
+    q = torch.randn(1, 4, 64).to(torch.bfloat16).cuda()
+    fits = dict(pages=pages.bytes, page_table=pages.table, kv_lens=pages.lens)
+    bad = [("page_table", pages.table.long(), "page_table"), ("page_table", pages.table[0], "page_table"),
+           ("page_table", pages.table.repeat(1, 2)[:, ::2], "contiguous rows"), ("page_table", pages.table.cpu(), "page_table is on"),
+           ("kv_lens", ints([20, 20]), "kv_lens"), ("kv_lens", pages.lens.long(), "kv_lens"), ("kv_lens", pages.lens[0], "kv_lens"),
+           ("pages", pages.bytes[:, ::2], "pages must be contiguous"), ("pages", pages.bytes.cpu(), "pages is on")]
+    before = pages.bytes.clone()
+    for name, t, match in bad:
+        kw = {**fits, name: t}
+        for call in (lambda: pq.gptq_kv_attention(cfg, q, **kw), lambda: pq.gptq_kv_append(cfg, k[:1], v[:1], **kw),
+                     lambda: pq.gptq_kv_read(cfg, tokens=1, **kw)):
+            with pytest.raises(ValueError, match=match if name != "pages" or "on" not in match else "on"):
+                call()
+    for cu in (ints([0, 1, 2]), ints([0, 1]).long(), ints([0, 1]).cpu()):
+        with pytest.raises(ValueError):
+            pq.gptq_kv_attention(cfg, q, **fits, cu_seqlens=cu)
+    for kw, error in ((dict(status=ints([0, 0])), ValueError), (dict(workspace=torch.zeros(1 << 20, dtype=torch.uint8)), ValueError),
+                      (dict(Y=torch.empty(1, 4, 64, device="cuda")), TypeError), (dict(Y=q), pq.GptqError),
+                      (dict(scale=float("nan")), pq.GptqError), (dict(max_queries=-1), pq.GptqError)):
+        with pytest.raises(error):
+            pq.gptq_kv_attention(cfg, q, **fits, **kw)
+    odd = torch.zeros(pages.bytes.numel() + 1, dtype=torch.uint8, device="cuda")[1:].view_as(pages.bytes)
+    with pytest.raises(pq.GptqError, match="16-byte"):
+        pq.gptq_kv_attention(cfg, q, **{**fits, "pages": odd})
+    with pytest.raises(pq.GptqError, match="table 0 wide"):
+        pq.gptq_kv_attention(cfg, q, **{**fits, "page_table": pages.table[:, :0]})
+    with pytest.raises(pq.GptqError, match="one token a sequence"):
+        pq.gptq_kv_append(cfg, k[:3], v[:3], **fits)
+    torch.cuda.synchronize()
+    assert torch.equal(before, pages.bytes)
