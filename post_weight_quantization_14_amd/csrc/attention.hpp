@@ -162,6 +162,24 @@ __device__ __forceinline__ bool ragged_find(int64_t index, int64_t batch, const 
   return false;
 }
 
+// ---------------------------------------------------------------- softmax
+// The running maximum of x·scale over raw logits x is kept as m + rest: m the rounded
+// product, of which weights 2^(x·scale - m) by one fused step keep every bit while half
+// a step of m is below 1.  From 2^23 on that half step would be their exponent (past 2^31
+// the largest weight itself would be Inf or 0), so rest takes it: the product's exact
+// remainder.  Below, rest is 0 and costs nothing.
+constexpr float kFar = 0x1p23f;
+
+// Raises the maximum to top·scale where that is more; the factor for what was summed before.
+__device__ __forceinline__ float raise_to(float top, float scale, float* m, float* rest) {
+  const float m0 = *m, rest0 = *rest;
+  if (fmaf(top, scale, -m0) - rest0 > 0.f) {
+    *m = top * scale;
+    *rest = fabsf(*m) > kFar ? fmaf(top, scale, -*m) : 0.f;
+  }
+  return exp2f((m0 - *m) + (rest0 - *rest));
+}
+
 // A tensor [tokens][heads][D] with unit stride in D, strides in elements.
 struct HeadRows {
   const void* p;

@@ -174,7 +174,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
   }
 
   f32x16_t o[DT];
-  float m, l;
+  float m, rest, l;   // weights are relative to 2^(m + rest)
   // A masked value meets a weight of 0, and 0·Inf is NaN.  Such values can only
   // be in the last tiles; a result that is not finite is computed once more,
   // carefully: what is not finite is left out of the product there, and counted
@@ -186,7 +186,9 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
 #pragma unroll
       for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
     m = kNone;
+    rest = 0.f;
     l = 0.f;
+    uint64_t far = 0;   // lanes with a rest
     fetch(0, lds0);
     auto step = [&](int tile, uint8_t* cur, uint8_t* nxt) {
       asm volatile("" ::: "memory");
@@ -227,18 +229,25 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
       float top = s[0][0];
 #pragma unroll
       for (int r = 1; r < 16 * U; ++r) top = fmaxf(top, s[r >> 4][r & 15]);
-      top = half_max(top) * a.scale;
-      if (__ballot(top > m + 8.f)) {   // sums are scaled again only when the maximum grows by more than 2^8
-        const float up = fmaxf(m, top), f = exp2f(m - up);
-        m = up;
+      top = half_max(top);
+      if (__ballot(fmaf(top, a.scale, -m) - rest > 8.f)) {   // sums are scaled again only when the maximum grows by more than 2^8
+        const float f = raise_to(top, a.scale, &m, &rest);
+        far = __ballot(rest != 0.f);
         l *= f;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] *= f;
       }
+      float by = a.scale, base = m;
+      if (far) {
+#pragma unroll
+        for (int r = 0; r < 16 * U; ++r) s[r >> 4][r & 15] = fmaf(s[r >> 4][r & 15], a.scale, -m) - rest;
+        by = 1.f;
+        base = 0.f;
+      }
       bf16x8_t p[2 * U];
 #pragma unroll
       for (int r = 0; r < 16 * U; ++r) {
-        const float e = __builtin_amdgcn_exp2f(fmaf(s[r >> 4][r & 15], a.scale, -m));
+        const float e = __builtin_amdgcn_exp2f(fmaf(s[r >> 4][r & 15], by, -base));
         l += e;
         p[r >> 3][r & 7] = (__bf16)e;
       }
@@ -303,7 +312,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
     // [DT][4][64 lanes] pieces of 16 bytes for each two waves, then maxima and sums
     static_assert(DT * 4 * 64 * 16 <= 2 * TB && kWaves == 4, "");
     uint8_t* mine = wave < 2 ? lds0 : lds1;
-    __shared__ float om[2][64], ol[2][64];
+    __shared__ float om[2][64], orest[2][64], ol[2][64];
     __syncthreads();
     if (part) {
 #pragma unroll
@@ -313,11 +322,13 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
           *reinterpret_cast<f32x4_t*>(mine + ((d * 4 + r) * 64 + lane) * 16) =
               f32x4_t{o[d][4 * r], o[d][4 * r + 1], o[d][4 * r + 2], o[d][4 * r + 3]};
       om[wave >> 1][lane] = m;
+      orest[wave >> 1][lane] = rest;
       ol[wave >> 1][lane] = l;
     }
     __syncthreads();
     if (part) return;
-    const float m1 = om[wave >> 1][lane], up = fmaxf(m, m1), f0 = exp2f(m - up), f1 = exp2f(m1 - up);
+    const float m1 = om[wave >> 1][lane], rest1 = orest[wave >> 1][lane], more = (m1 - m) + (rest1 - rest);
+    const float f0 = more > 0.f ? exp2f(-more) : 1.f, f1 = more > 0.f ? 1.f : exp2f(more);   // NaN: an infinite logit was seen
     l = l * f0 + ol[wave >> 1][lane] * f1;
 #pragma unroll
     for (int d = 0; d < DT; ++d)

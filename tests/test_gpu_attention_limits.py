@@ -1,0 +1,81 @@
+"""Attention at the ends of what it takes: logits of any size, pages and rows out of
+range beside good ones, long chunks, prompts and batches."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from attention_helpers import check, f64, reference, starts
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import post_weight_quantization_14_amd as pq
+    pq.lib()
+    return pq
+
+
+# ---------------------------------------------------------------- logits of any size
+EXPONENTS = (16, 23, 25, 28, 31, 33, 36, 40, 60, 90, 107)
+
+
+def far_inputs(tokens, news, heads, kv_heads, dim, seed):
+    """Queries whose logits are products with one channel of the keys, exact in fp32 and 2^16 to 2^107 times as
+    large; every third token's are ordinary, every third's nothing.  Keys have integers in that channel, so that
+    two of them are equal or hundreds apart: a weight is 1/n or below e^-40."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(news, heads, dim, generator=g)
+    k = torch.randn(tokens, kv_heads, dim, generator=g)
+    v = torch.randn(tokens, kv_heads, dim, generator=g)
+    k[..., 0] = torch.randint(-200, 201, (tokens, kv_heads), generator=g).float()
+    kind = (torch.arange(news)[:, None] + torch.arange(heads)) % 3
+    e = torch.tensor(EXPONENTS)[(torch.arange(news)[:, None] * 7 + torch.arange(heads)) % len(EXPONENTS)]
+    far = torch.zeros(news, heads, dim)
+    far[..., 0] = torch.where(torch.rand(news, heads, generator=g) < 0.5, 1.0, -1.0) * 2.0 ** e
+    q = torch.where((kind == 0)[..., None], far, torch.where((kind == 1)[..., None], q * 0.05, torch.zeros(())))
+    return q.to(torch.bfloat16), k.to(torch.bfloat16), v.to(torch.bfloat16), kind.numpy()
+
+
+def check_far(y, ref, weighed, once, what):
+    """Weights are equal numbers or nothing; weighed: Σ p·|v|.  One rounding of the result to bf16, 2^-8 of it; one of
+    each weight where they are bf16 (a maximum up to 2^23 is held to half a step of 1/2, so the largest weight is
+    2^d, |d| <= 1/2, and rounded like any other), 2^-16 where they have two parts; fp32 sums of some hundred terms and
+    of the cache's offsets (271 steps of a value at the most here), 2^-13 of the largest that is weighed."""
+    y = f64(y)
+    assert np.all(np.isfinite(y)), f"{what}: {int(np.sum(~np.isfinite(y)))} outputs not finite"
+    err = np.abs(y - ref)
+    bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 if once else 2.0 ** -16) * weighed + 2.0 ** -13 * np.max(weighed, axis=2, keepdims=True)
+    print(f"{what}: worst error {np.max(err / bound):.3f} of its bound", flush=True)
+    assert np.all(err <= bound), f"{what}: {int(np.sum(err > bound))} outputs beyond the bound"
+
+
+def by_words(q, k, v, scale, total, news):
+    """(the oracle's attention, the same of |v|) of rows packed as `news` over keys packed as `total`."""
+    out, qa, ka = [], 0, 0
+    for t, n in zip(total, news):
+        x = [f64(q[qa:qa + n]), f64(k[ka:ka + t]), f64(v[ka:ka + t])]
+        out.append([oracle.attention(*x[:2], w, scale, np.arange(t - n, t)) for w in (x[2], np.abs(x[2]))])
+        qa, ka = qa + n, ka + t
+    return tuple(np.concatenate(o) for o in zip(*out))
+
+
+# two waves to 32 queries where workgroups are few, one otherwise
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 2, 128), (3, 1, 64), (100, 1, 128), (200, 2, 64)])
+@pytest.mark.parametrize("scale", [None, -0.3])
+def test_prompt_logits_of_any_size(pq, heads, kv_heads, dim, scale):
+    total = [200, 133]
+    q, k, v, kind = far_inputs(333, 333, heads, kv_heads, dim, seed=heads)
+    y = pq.gptq_prompt_attention(q.cuda(), k.cuda(), v.cuda(), starts(total).cuda(), scale=scale)
+    s = dim ** -0.5 if scale is None else scale
+    share = heads // kv_heads
+    for h in sorted({0, 1, heads // 2, heads - 1}):
+        qh, kh, vh = q[:, h:h + 1], k[:, h // share:h // share + 1], v[:, h // share:h // share + 1]
+        ref, weighed = by_words(qh, kh, vh, s, total, total)
+        far, near = kind[:, h] != 1, kind[:, h] == 1
+        check_far(y[:, h:h + 1][far], ref[far], weighed[far], True, f"head {h} of {heads}, scale {scale}")
+        calm = torch.where(torch.from_numpy(near)[:, None, None], qh, torch.zeros_like(qh))
+        check(y[:, h:h + 1][near], *(r[near] for r in reference(f64(calm), f64(kh), f64(vh), s, total, total)), f"head {h}, ordinary")
