@@ -76,11 +76,25 @@ __device__ __forceinline__ void by_index(const F& f) {   // f(0) .. f(N - 1), ea
   }
 }
 
+// The rest of the largest of several maxima m + rest: `each` gives them to its argument,
+// `top` is the largest m (equal m's have a rest alike, or none).  They are looked at only
+// where some lane's top may have one.
+template <class F>
+__device__ __forceinline__ float rest_of(float top, const F& each) {
+  float rest = 0.f;
+  if (__builtin_expect(__ballot(fabsf(top) > kFar) != 0, 0)) {
+    rest = -INFINITY;
+    each([&](float m, float r) INLINE { rest = m == top ? fmaxf(rest, r) : rest; });
+  }
+  return rest;
+}
+
 struct Split {
   int64_t token;      // of the unit's first row
   int head;           // key head
   uint32_t hq0;       // query head of the first row within the group
   int rows, slot;     // of the first part; part i > 0 is slot 2·(workgroup + i)
+  int least;          // positions that its first row sees
   int parts;          // 0: no such unit
 };
 
@@ -93,7 +107,7 @@ struct Work {
   int share;             // query heads of a key head
   uint32_t share_inv;    // above 2^32 / share: x / share = umulhi(x, share_inv) for x below 2^13 (not for share 1)
   const uint8_t* pages;
-  float* partial;        // [2·wgs] of [rows][D] sums, [rows] maxima, [rows] sums of weights
+  float* partial;        // [2·wgs] of [rows][D] sums, [rows] maxima and their rests, [rows] sums of weights
   Split* meta;           // [wgs]: of a unit split over workgroups that begins in this one
 };
 
@@ -219,7 +233,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
   constexpr int kThreads = 64 * W, R = 16 * NT / SP, NC = 16 / SP, E = 8 / SP, KS = D / 32, NG = D / G, MT = D / 16, PG = G / 32;   // PG: 32-channel steps of a group
   constexpr int kPitch = D + 4;
   __shared__ float so[W][16][kPitch];
-  __shared__ float sm[W][16], sl[W][16];
+  __shared__ float sm[W][16], sr[W][16], sl[W][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n16 = lane & 15, kg = lane >> 4;
   const int nq = n16 % NC, half = n16 / NC;   // query row of the column, record of its logits
@@ -327,10 +341,12 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
     // bytes that lane takes of its own word (4 .. 7) and its neighbour's (0 .. 3): even lanes both high halves, odd both low
     const uint32_t zsel = lane & 1 ? 0x05040100u : 0x03020706u;
     f32x4_t o[NT][MT];
-    float m[NT], l[NT], zs[NT][NG];
+    float m[NT], rest[NT], l[NT], zs[NT][NG];   // weights are relative to 2^(m + rest)
+    uint64_t far = 0;   // lanes with a rest
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt] = kNone;
+      rest[nt] = 0.f;
       l[nt] = 0.f;
       zo[nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -413,14 +429,15 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
         float t = sx[nt][0];
 #pragma unroll
         for (int i = 1; i < E; ++i) t = fmaxf(t, sx[nt][i]);
-        top[nt] = quad_max(t) * w.scale;
-        grown |= top[nt] > m[nt] + 8.f;
+        top[nt] = quad_max(t);
+        grown |= fmaf(top[nt], w.scale, -m[nt]) - rest[nt] > 8.f;
       }
       if (__ballot(grown)) {
+        bool rests = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float up = fmaxf(m[nt], top[nt]), f = exp2f(m[nt] - up);
-          m[nt] = up;
+          const float f = raise_to(top[nt], w.scale, &m[nt], &rest[nt]);
+          rests |= rest[nt] != 0.f;
           l[nt] *= f;
 #pragma unroll
           for (int g = 0; g < NG; ++g) zs[nt][g] *= f;
@@ -428,13 +445,26 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
 #pragma unroll
           for (int j = 0; j < MT; ++j) o[nt][j] *= f;
         }
+        far = __ballot(rests);
+      }
+      float by = w.scale, base[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) base[nt] = m[nt];
+      if (__builtin_expect(far != 0, 0)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) sx[nt][i] = fmaf(sx[nt][i], w.scale, -m[nt]) - rest[nt];
+          base[nt] = 0.f;
+        }
+        by = 1.f;
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < E; ++i) {
           float& p = sx[nt][i];
-          p = __builtin_amdgcn_exp2f(fmaf(p, w.scale, -m[nt]));
+          p = __builtin_amdgcn_exp2f(fmaf(p, by, -base[nt]));
           l[nt] += p;
         }
       // values
@@ -547,23 +577,31 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
     // ---- the waves' sums together, and for SP 2 the halves of the columns: 16 columns at a time
     const bool whole = WHOLE || (s0 == 0 && s1 == steps);
     const int slot = pos == begin ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1;
-    float* part = w.partial + (int64_t)slot * R * (D + 2);
+    float* part = w.partial + (int64_t)slot * R * (D + 3);
     if (!whole && s0 == 0 && tid == 0)
-      w.meta[blockIdx.x] = Split{s.row + tq0, head, hq0, rows, slot, (int)((pos + steps - 1) / piece) - (int)blockIdx.x + 1};
+      w.meta[blockIdx.x] = Split{s.row + tq0, head, hq0, rows, slot, least, (int)((pos + steps - 1) / piece) - (int)blockIdx.x + 1};
+    auto top_of = [&](int row, float* rest) INLINE {   // of the waves' and halves' maxima of a row
+      float up = kNone;
+#pragma unroll
+      for (int v = 0; v < W; ++v)
+#pragma unroll
+        for (int c = 0; c < SP; ++c) up = fmaxf(up, sm[v][c * NC + row]);
+      *rest = rest_of(up, [&](auto take) INLINE {
+        for (int v = 0; v < W; ++v)
+          for (int c = 0; c < SP; ++c) take(sm[v][c * NC + row], sr[v][c * NC + row]);
+      });
+      return up;
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       l[nt] = quad_sum(l[nt]);
       if (kMat) zs[nt][0] = kg >= 2 ? zo[nt][0] + zo[nt][1] : 0.f;   // rows 8, 9 and 12, 13
 #pragma unroll
       for (int g = 0; g < NG; ++g) zs[nt][g] = quad_sum(zs[nt][g]);
-      if (kg == 0) sm[wave][n16] = m[nt];
+      if (kg == 0) sm[wave][n16] = m[nt], sr[wave][n16] = rest[nt];
       __syncthreads();
-      float up = kNone;
-#pragma unroll
-      for (int v = 0; v < W; ++v)
-#pragma unroll
-        for (int c = 0; c < SP; ++c) up = fmaxf(up, sm[v][c * NC + nq]);
-      const float f = exp2f(m[nt] - up);
+      float up_rest;
+      const float up = top_of(nq, &up_rest), f = exp2f((m[nt] - up) + (rest[nt] - up_rest));
       if (kg == 0) sl[wave][n16] = l[nt] * f;
 #pragma unroll
       for (int j = 0; j < MT; ++j)
@@ -584,8 +622,8 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
             y += *reinterpret_cast<const f32x4_t*>(&so[v][c * NC + n][d]);
           }
         if (whole) {
-          const float inv = ll == 0.f ? 0.f : 1.f / ll;   // a row that sees nothing
           const uint32_t i = hq0 + nt * 16 + n, t = w.share == 1 ? i : __umulhi(i, w.share_inv);
+          const float inv = least + (int)t > 0 ? 1.f / ll : 0.f;   // a row that sees nothing gives zeros
           uint16_t* yp = const_cast<uint16_t*>(static_cast<const uint16_t*>(w.Y.p)) + (s.row + tq0 + t) * w.Y.ld +
                          (head * w.share + (i - t * w.share)) * w.Y.hs + d;
           uint16_t h[4];
@@ -600,13 +638,10 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
         } else {
           *reinterpret_cast<f32x4_t*>(part + (nt * 16 + n) * D + d) = y;
           if (d == 0) {
-            float top = kNone;
-#pragma unroll
-            for (int v = 0; v < W; ++v)
-#pragma unroll
-              for (int c = 0; c < SP; ++c) top = fmaxf(top, sm[v][c * NC + n]);
-            part[R * D + nt * 16 + n] = top;
-            part[R * D + R + nt * 16 + n] = ll;
+            float top_rest;
+            part[R * D + nt * 16 + n] = top_of(n, &top_rest);
+            part[R * D + R + nt * 16 + n] = top_rest;
+            part[R * D + 2 * R + nt * 16 + n] = ll;
           }
         }
       }
@@ -625,7 +660,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
 constexpr int kJoinWgs = 512;
 template <int D, int R>
 __global__ __launch_bounds__(256) void kv_join_kernel(Work w, int wgs, int most_rows) {
-  constexpr int64_t kSize = R * (D + 2);
+  constexpr int64_t kSize = R * (D + 3);
   constexpr int L4 = D / 4, P = 64 / L4;   // lanes of a row, four channels each; parts side by side
   __shared__ int16_t list[kMaxWgs];
   __shared__ int count[4];
@@ -660,18 +695,22 @@ __global__ __launch_bounds__(256) void kv_join_kernel(Work w, int wgs, int most_
     const float* p0 = w.partial + uniform(u.slot) * kSize;
     const float* p1 = w.partial + 2 * (int64_t)first * kSize;
     for (int row = pair % most_rows; row < uniform(u.rows); row += most_rows) {
-      float up = kNone, ll = 0.f;
+      float up = kNone, up_rest = 0.f, ll = 0.f;
       f32x4_t y = {0.f, 0.f, 0.f, 0.f};
       auto some = [&](auto n, int base) INLINE {   // parts base + P·j + side, j < N
         constexpr int N = decltype(n)::value;
-        float m[N], l[N];
+        float m[N], l[N], rest[N];
         f32x4_t v[N];
+        auto part = [&](int j) INLINE {
+          const int i = min(base + P * j + side, parts - 1);
+          return i == 0 ? p0 : p1 + 2 * i * kSize;
+        };
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          const int i = min(base + P * j + side, parts - 1);
-          const float* p = i == 0 ? p0 : p1 + 2 * i * kSize;
+          const float* p = part(j);
           m[j] = p[R * D + row];
-          l[j] = p[R * D + R + row];
+          rest[j] = 0.f;
+          l[j] = p[R * D + 2 * R + row];
           v[j] = *reinterpret_cast<const f32x4_t*>(p + row * D + c4);
         }
         float top = up;
@@ -679,13 +718,22 @@ __global__ __launch_bounds__(256) void kv_join_kernel(Work w, int wgs, int most_
         for (int j = 0; j < N; ++j) top = fmaxf(top, m[j]);
 #pragma unroll
         for (int d = L4; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-        const float f = exp2f(up - top);
+        float top_rest = rest_of(top, [&](auto take) INLINE {
+          take(up, up_rest);
+#pragma unroll
+          for (int j = 0; j < N; ++j) take(m[j], rest[j] = part(j)[R * D + R + row]);
+        });
+        if (__builtin_expect(__ballot(top_rest != 0.f) != 0, 0))
+#pragma unroll
+          for (int d = L4; d < 64; d <<= 1) top_rest = fmaxf(top_rest, __shfl_xor(top_rest, d));
+        const float f = exp2f((up - top) + (up_rest - top_rest));
         up = top;
+        up_rest = top_rest;
         ll *= f;
         y *= f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          const float g = exp2f(m[j] - up);
+          const float g = exp2f((m[j] - up) + (rest[j] - up_rest));
           if (base + P * j + side < parts) {
             ll = fmaf(l[j], g, ll);
             y += v[j] * g;
@@ -703,8 +751,8 @@ __global__ __launch_bounds__(256) void kv_join_kernel(Work w, int wgs, int most_
         for (int c = 0; c < 4; ++c) y[c] += __shfl_xor(y[c], d);
       }
       if (side) continue;
-      const float inv = ll == 0.f ? 0.f : 1.f / ll;   // a row that sees nothing
       const uint32_t i = uniform((int)u.hq0) + row, t = w.share == 1 ? i : __umulhi(i, w.share_inv);
+      const float inv = u.least + (int)t > 0 ? 1.f / ll : 0.f;   // a row that sees nothing gives zeros
       uint16_t* yp = const_cast<uint16_t*>(static_cast<const uint16_t*>(w.Y.p)) + (u.token + t) * w.Y.ld +
                      (u.head * w.share + (i - t * w.share)) * w.Y.hs + c4;
 #pragma unroll
@@ -780,7 +828,7 @@ KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, i
     p.wgs = wide ? kMaxWgs / 2 : kMaxWgs;
     p.waves = wide ? 8 : 4;
   }
-  p.partial = (size_t)2 * kMaxWgs * tile * (L.dim + 2) * 4;   // whatever the capacity
+  p.partial = (size_t)2 * kMaxWgs * tile * (L.dim + 3) * 4;   // whatever the capacity
   p.total = align256(p.partial) + (size_t)kMaxWgs * sizeof(Split);
   return p;
 }

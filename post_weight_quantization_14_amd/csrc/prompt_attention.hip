@@ -238,7 +238,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
         for (int d = 0; d < DT; ++d) o[d] *= f;
       }
       float by = a.scale, base = m;
-      if (far) {
+      if (__builtin_expect(far != 0, 0)) {
 #pragma unroll
         for (int r = 0; r < 16 * U; ++r) s[r >> 4][r & 15] = fmaf(s[r >> 4][r & 15], a.scale, -m) - rest;
         by = 1.f;

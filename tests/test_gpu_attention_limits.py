@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle
-from attention_helpers import check, f64, reference, starts
+from attention_helpers import Pages, check, f64, kept, reference, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +79,40 @@ def test_prompt_logits_of_any_size(pq, heads, kv_heads, dim, scale):
         check_far(y[:, h:h + 1][far], ref[far], weighed[far], True, f"head {h} of {heads}, scale {scale}")
         calm = torch.where(torch.from_numpy(near)[:, None, None], qh, torch.zeros_like(qh))
         check(y[:, h:h + 1][near], *(r[near] for r in reference(f64(calm), f64(kh), f64(vh), s, total, total)), f"head {h}, ordinary")
+
+
+# (heads, kv heads, dim, group), tokens of each sequence: up to 8, 16 and more query rows of a key head
+@pytest.mark.parametrize("heads,kv_heads,dim,group", [(8, 2, 128, 128), (6, 2, 128, 64), (4, 1, 64, 32)])
+@pytest.mark.parametrize("news", [1, 3, 11])
+@pytest.mark.parametrize("total,width", [([60, 333, 17], None), ([60, 333, 17], 80), ([2500, 40], None), ([1300], 1000)])
+@pytest.mark.parametrize("scale", [None, -0.3])
+def test_cached_logits_of_any_size(pq, heads, kv_heads, dim, group, news, total, width, scale):
+    """In one launch, in pieces that are joined, and in wide pieces; rows that see nothing stay zeros beside them."""
+    page = 16 if width else 64
+    new = [news] * len(total) + [2]
+    total = total + [1]                         # whose first token sees nothing
+    cfg = pq.KvConfig(kv_heads, dim, group, page)
+    q, k, v, kind = far_inputs(sum(total), sum(new), heads, kv_heads, dim, seed=news)
+    pages = Pages(pq, cfg, total, seed=1).fill(k, v)
+    table = pages.table
+    if width:
+        table = torch.full((len(total), width), -1, dtype=torch.int32, device="cuda")
+        n = min(width, pages.table.shape[1])
+        table[:, :n] = pages.table[:, :n]
+    y = pq.gptq_kv_attention(cfg, q.cuda(), pages.bytes, table, pages.lens, cu_seqlens=starts(new).cuda(), max_queries=news,
+                             scale=scale)
+    assert (y[-2] == 0).all()
+    s = dim ** -0.5 if scale is None else scale
+    (kk, ks, kz), (vk, vs, vz) = kept(f64(k), group), kept(f64(v), group)
+    kd, vd = torch.from_numpy(kk), torch.from_numpy(vk)
+    share, what = heads // kv_heads, f"{news} of {total}, scale {scale}"
+    for h in sorted({0, 1, heads - 1}):
+        one = slice(h // share, h // share + 1)
+        ref, weighed = by_words(q[:, h:h + 1], kd[:, one], vd[:, one], s, total, new)
+        far, near = kind[:, h] != 1, kind[:, h] == 1
+        far[-2] = near[-2] = False
+        check_far(y[:, h:h + 1][far], ref[far], weighed[far], news * share > 16, f"head {h}, {what}")
+        calm = torch.where(torch.from_numpy(near)[:, None, None], q[:, h:h + 1], torch.zeros((), dtype=q.dtype))
+        grid = tuple((a[:, one], b[:, one]) for a, b in ((ks, kz), (vs, vz))) + (group,)
+        r = reference(f64(calm), kk[:, one], vk[:, one], s, total, new, grid)
+        check(y[:, h:h + 1][near], *(t[near] for t in r), f"head {h}, ordinary")
