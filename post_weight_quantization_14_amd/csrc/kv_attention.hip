@@ -187,7 +187,7 @@ struct Step {
   static constexpr int KS = D / 32, NG = D / G;
   uint32_t k[2][KS], v[2][KS];
   uint32_t pw[SP][NG];
-  bool bad;          // a page that is none
+  bool bad;          // a page that is none, of the lane's own record
 };
 
 template <int N>
@@ -305,21 +305,22 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
     const uint32_t head_at = (uint32_t)head << w.L.rec_shift;
     const int param_at = 2 * kv_code_bytes(D) + (SP == 1 ? (n16 >> 3) * kv_param_bytes(D, G) : 0) + (kg * 4 + (n16 & 3)) * 4;
     auto load = [&](int st, const Pages& pg, Step<D, G, SP>& x) INLINE {
-      x.bad = false;
       const uint8_t* base[2];
+      bool none[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int page = uniform(pg.id[u]);
-        const bool none = s.bad || (uint32_t)page >= (uint32_t)w.q.pages;
-        const int64_t id = none ? 0 : page;
-        x.bad |= none;
+        none[u] = s.bad || (uint32_t)page >= (uint32_t)w.q.pages;
+        const int64_t id = none[u] ? 0 : page;
         const uint32_t rec = head_at + (min(2 * st + u, last) & (w.L.recs - 1));
         const uint8_t* p = w.pages + id * w.L.page_bytes + (int64_t)rec * kv_rec_bytes(D, G);
         load_words(p + lane * (D / 8), x.k[u]);
         load_words(p + (kv_code_bytes(D) + lane * (D / 8)), x.v[u]);
         base[u] = p;
       }
-      const uint8_t* p = ((SP == 1 ? lane & 4 : half) ? base[1] : base[0]) + param_at;
+      const bool second = SP == 1 ? lane & 4 : half;
+      x.bad = second ? none[1] : none[0];
+      const uint8_t* p = (second ? base[1] : base[0]) + param_at;
 #pragma unroll
       for (int i = 0; i < SP; ++i)
 #pragma unroll
@@ -365,7 +366,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
           sf[i][g] = __uint_as_float(x.bad ? 0x7fc00000u : x.pw[i][g] & 0xffff0000u);
           zf[i][g] = (float)((int)(int16_t)(uint16_t)x.pw[i][g] + 128);
         }
-      if (x.bad && lane == 0) kv_bad(w.q.status);
+      if (x.bad) kv_bad(w.q.status);
       // logits of positions at(i), i = 4·record + r (SP 1), r (SP 2)
       float sx[NT][E];
       auto at = [&](int i) { return st * kStep + (SP == 1 ? (i >> 2) * 16 : half * 16) + kg * 4 + (i & 3); };

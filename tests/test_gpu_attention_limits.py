@@ -116,3 +116,32 @@ def test_cached_logits_of_any_size(pq, heads, kv_heads, dim, group, news, total,
         grid = tuple((a[:, one], b[:, one]) for a, b in ((ks, kz), (vs, vz))) + (group,)
         r = reference(f64(calm), kk[:, one], vk[:, one], s, total, new, grid)
         check(y[:, h:h + 1][near], *(t[near] for t in r), f"head {h}, ordinary")
+
+
+# ---------------------------------------------------------------- out of range beside in range
+@pytest.mark.parametrize("heads,kv_heads,dim,group", [(4, 4, 64, 64), (8, 2, 128, 64), (12, 1, 64, 32), (40, 2, 128, 128)])
+@pytest.mark.parametrize("width", [None, 100])
+def test_a_bad_page_reaches_only_those_who_read_it(pq, heads, kv_heads, dim, group, width):
+    """Pages of one record: a token that ends before the bad page reads nothing of it, in the same step too."""
+    cfg = pq.KvConfig(kv_heads, dim, group, 16)
+    n = 90
+    _, k, v, _ = far_inputs(n, 1, heads, kv_heads, dim, seed=3)
+    pages = Pages(pq, cfg, [n]).fill(k, v)
+    table = torch.full((1, width or pages.table.shape[1]), -1, dtype=torch.int32, device="cuda")
+    table[:, :6] = pages.table[:, :6]
+    q = torch.randn(n, heads, dim, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    run = lambda st: pq.gptq_kv_attention(cfg, q, pages.bytes, table, pages.lens, cu_seqlens=starts([n]).cuda(),  # noqa: E731
+                                          status=st)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    clean = run(st)
+    assert st.item() == 0 and torch.isfinite(clean).all()
+    for page in (0, 1, 2, 3, 5):
+        old = table[0, page].item()
+        for bad in (-1, pages.count):
+            table[0, page] = bad
+            st.zero_()
+            y = run(st)
+            assert st.item() == -1
+            assert torch.equal(y[:16 * page], clean[:16 * page]), f"page {page}: tokens that do not read it"
+            assert torch.isnan(y[16 * page:]).all(), f"page {page}: tokens that do"
+        table[0, page] = old
