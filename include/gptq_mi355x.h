@@ -494,11 +494,13 @@ gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const voi
  * for bf16 Q and Y: a token a sequence in decoding, several where drafts are
  * checked, hundreds for a chunk of a prompt.  The tokens are appended first.
  * The codes enter the products exactly; all sums are fp32 (and stay finite for |Q|
- * up to 2^108).  Weights enter as two bf16 parts, but rounded to bf16 where
- * max_queries·heads / kv_heads is above 16.  A token that sees no position
- * (kv_lens[b] < n) gives zeros.  max_queries: the most tokens that a sequence has
- * in this call, as far as the caller knows; it chooses between kernels and nothing
- * else (0: one).  `workspace` (256-byte aligned, contents not kept) of
+ * up to 2^108).  A token that sees no position (kv_lens[b] < n) gives zeros.
+ * max_queries: the most tokens that a sequence has in this call, as far as the
+ * caller knows (0: one).  It chooses between kernels, which give the right results
+ * for any number, and how weights enter: up to 16 as two bf16 parts (2^-16 of each
+ * is left), above 16 rounded to bf16 as in gptq_prompt_attention, which is faster;
+ * 16 may be said for longer chunks whose weights are to have two parts.
+ * `workspace` (256-byte aligned, contents not kept) of
  * gptq_kv_attention_workspace_bytes(cfg, heads, batch, tokens, max_queries) bytes
  * belongs to one call at a time.
  *

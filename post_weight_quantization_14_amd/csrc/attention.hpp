@@ -195,6 +195,7 @@ gptq_status run_kv_read(const KvLayout& L, const HeadRows& K, const HeadRows& V,
 
 struct KvAttentionPlan {
   int tile;           // rows of queries that a workgroup holds at once: 8, 16 or 32
+  int parts;          // bf16 parts of a weight: 2, or 1 (of tiles of 32)
   bool whole;         // a workgroup for each unit (row tile and key head of a sequence), not an equal piece of all
   int wgs, waves;     // workgroups, and waves of each
   int rows;           // rows of a unit that should hold queries

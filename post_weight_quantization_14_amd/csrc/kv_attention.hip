@@ -225,10 +225,10 @@ __device__ __forceinline__ void value_pairs(const uint32_t (&w)[D / 32], int b, 
 // columns hold the same rows; the left half keeps the logits of the step's first
 // record, the right half those of the second, each with sums of its own, so that no
 // lane works for rows that are not there: 64 sequences 86 -> 79 us.  NT 2 holds 32
-// rows: codes are spread once for both tiles, weights are rounded to bf16 once
-// (2^-8 of each, as the result is; with two parts 140 us instead of 112 for the chunk
-// above), and with one scale a head a product sums the zero points as well.
-template <int D, int G, int NT, int SP, int W, bool WHOLE>
+// rows: codes are spread once for both tiles, and with one scale a head a product sums
+// the zero points as well.  PARTS is in how many bf16 parts weights enter: 2 leave 2^-16
+// of each, 1 leaves 2^-8, as the result's own rounding does.
+template <int D, int G, int NT, int SP, int PARTS, int W, bool WHOLE>
 __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
   constexpr int kThreads = 64 * W, R = 16 * NT / SP, NC = 16 / SP, E = 8 / SP, KS = D / 32, NG = D / G, MT = D / 16, PG = G / 32;   // PG: 32-channel steps of a group
   constexpr int kPitch = D + 4;
@@ -497,7 +497,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
 #pragma unroll
           for (int i = 0; i < E / 2; ++i) {
             const uint32_t h = pack_bf16(pw[2 * i], pw[2 * i + 1]);
-            if constexpr (NT == 2) {
+            if constexpr (PARTS == 1) {
               hw[i] = h;
               pw[2 * i] = __uint_as_float(h << 16);
               pw[2 * i + 1] = __uint_as_float(h & 0xffff0000u);
@@ -514,7 +514,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
           u32x4_t hx, lx;
           if constexpr (SP == 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) hx[i] = hw[i], lx[i] = NT == 1 ? lw[i] : 0;
+            for (int i = 0; i < 4; ++i) hx[i] = hw[i], lx[i] = PARTS == 2 ? lw[i] : 0;
           } else {   // a column's weights stand at its record's positions, zeros at the other's
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -525,9 +525,11 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
           }
           ph[nt] = __builtin_bit_cast(bf16x8_t, hx);
           pl[nt] = __builtin_bit_cast(bf16x8_t, lx);
-          if constexpr (kMat)
-            zo[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8_t, u32x4_t{za[0], za[1], za[2], za[3]}), ph[nt], zo[nt], 0, 0, 0);
+          if constexpr (kMat) {
+            const bf16x8_t z = __builtin_bit_cast(bf16x8_t, u32x4_t{za[0], za[1], za[2], za[3]});
+            zo[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z, ph[nt], zo[nt], 0, 0, 0);
+            if constexpr (PARTS == 2) zo[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z, pl[nt], zo[nt], 0, 0, 0);
+          }
         }
 #pragma unroll
         for (int j = g * PG * 2; j < (g + 1) * PG * 2; ++j) {
@@ -540,7 +542,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             o[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ph[nt], o[nt][j], 0, 0, 0);
-            if constexpr (NT == 1) o[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pl[nt], o[nt][j], 0, 0, 0);
+            if constexpr (PARTS == 2) o[nt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pl[nt], o[nt][j], 0, 0, 0);
           }
         }
       }
@@ -762,24 +764,24 @@ __global__ __launch_bounds__(256) void kv_join_kernel(Work w, int wgs, int most_
   }
 }
 
-template <int D, int G, int NT, int SP>
+template <int D, int G, int NT, int SP, int PARTS>
 gptq_status launch(const Work& w, const KvAttentionPlan& p, hipStream_t stream) {
   if (p.whole) {
     if (p.waves == 8)
-      kv_attention_kernel<D, G, NT, SP, 8, true><<<p.wgs, 512, 0, stream>>>(w);
+      kv_attention_kernel<D, G, NT, SP, PARTS, 8, true><<<p.wgs, 512, 0, stream>>>(w);
     else if (p.waves == 4)
-      kv_attention_kernel<D, G, NT, SP, 4, true><<<p.wgs, 256, 0, stream>>>(w);
+      kv_attention_kernel<D, G, NT, SP, PARTS, 4, true><<<p.wgs, 256, 0, stream>>>(w);
     else if (p.waves == 2)
-      kv_attention_kernel<D, G, NT, SP, 2, true><<<p.wgs, 128, 0, stream>>>(w);
+      kv_attention_kernel<D, G, NT, SP, PARTS, 2, true><<<p.wgs, 128, 0, stream>>>(w);
     else
-      kv_attention_kernel<D, G, NT, SP, 1, true><<<p.wgs, 64, 0, stream>>>(w);
+      kv_attention_kernel<D, G, NT, SP, PARTS, 1, true><<<p.wgs, 64, 0, stream>>>(w);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
   }
   if (p.waves == 8)
-    kv_attention_kernel<D, G, NT, SP, 8, false><<<p.wgs, 512, 0, stream>>>(w);
+    kv_attention_kernel<D, G, NT, SP, PARTS, 8, false><<<p.wgs, 512, 0, stream>>>(w);
   else
-    kv_attention_kernel<D, G, NT, SP, 4, false><<<p.wgs, 256, 0, stream>>>(w);
+    kv_attention_kernel<D, G, NT, SP, PARTS, 4, false><<<p.wgs, 256, 0, stream>>>(w);
   GPTQ_LAUNCH_CHECK();
   kv_join_kernel<D, 16 * NT / SP><<<kJoinWgs, 256, 0, stream>>>(w, p.wgs, p.rows);
   GPTQ_LAUNCH_CHECK();
@@ -797,6 +799,13 @@ gptq_status launch(const Work& w, const KvAttentionPlan& p, hipStream_t stream) 
 // units, 10.4 with one wave each, 13.9 with two, 16.4 with four; 64 x 512, 512 units,
 // 17.2, 14.6 and 10.3.
 constexpr int64_t kWhole = 1024, kMostUnits = 1 << 22;   // a grid's limit is 2^32 threads
+// Weights are rounded once for chunks, where the matrix cores and the vector unit are the
+// bound (512 tokens over 8192, 32 heads on 8: 112 us, 132 in two parts; groups of 64 148 and
+// 187): from more tokens a sequence on than drafts have, whatever the heads.
+constexpr int64_t kDrafts = 16;
+// Two parts for 32 rows of more scales than one a head are short of registers: 16 sequences
+// of 4096, 6 drafts of 4 heads a key head, groups of 64 39.8 us by tiles of 16 rows and 42.9
+// of 32, groups of 32 51 and 115; with one scale a head 33.7 and 29.7.
 // Smaller tiles of rows while there is a CU for each unit: 4 sequences x 5 tokens x
 // 4 heads a key head over 2048 positions 22.8 us with tiles of 32, 14.7 with 8; 16
 // sequences (384 units of 8 rows) 23.5 and 28.4.
@@ -813,7 +822,8 @@ KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, i
   KvAttentionPlan p;
   const int64_t share = heads / L.heads;
   const int64_t rows = std::min(std::max<int64_t>(max_queries, 1), std::max<int64_t>(tokens, 1)) * share;
-  const int tile = rows > 16 ? 32 : rows > 8 ? 16 : 8;
+  p.parts = rows / share > kDrafts ? 1 : 2;
+  const int tile = rows <= 8 ? 8 : rows <= 16 || (p.parts == 2 && L.group != L.dim) ? 16 : 32;
   p.tile = tile;
   auto units = [&](int tile) { return L.heads * (tokens * share / tile + std::min(batch, tokens)); };   // at the most
   p.whole = capacity <= kWhole && units(tile) <= kMostUnits;
@@ -841,9 +851,11 @@ gptq_status run_kv_attention(const KvLayout& L, int heads, const HeadRows& Q, co
                static_cast<const uint8_t*>(pages),
                static_cast<float*>(ws), reinterpret_cast<Split*>(static_cast<uint8_t*>(ws) + align256(p.partial))};
   auto tiled = [&](auto d, auto g) {
-    return p.tile == 8    ? launch<d.value, g.value, 1, 2>(w, p, stream)
-           : p.tile == 16 ? launch<d.value, g.value, 1, 1>(w, p, stream)
-                          : launch<d.value, g.value, 2, 1>(w, p, stream);
+    if (p.tile == 8) return launch<d.value, g.value, 1, 2, 2>(w, p, stream);
+    if (p.tile == 16) return launch<d.value, g.value, 1, 1, 2>(w, p, stream);
+    if constexpr (d.value == g.value)
+      if (p.parts == 2) return launch<d.value, g.value, 2, 1, 2>(w, p, stream);
+    return launch<d.value, g.value, 2, 1, 1>(w, p, stream);
   };
   using std::integral_constant;
   if (L.dim == 128 && L.group == 128) return tiled(integral_constant<int, 128>{}, integral_constant<int, 128>{});
