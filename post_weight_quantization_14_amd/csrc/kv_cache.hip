@@ -24,8 +24,9 @@ struct Grid {
 
 // Both decisions that decide a code are made exactly.  s here: the guess (a little
 // low, then cut to bf16 from above) is the wanted bf16 or the one below it, and
-// 64-bit arithmetic tells which: 15·s and 4096·s are exact, hi - lo is rounded
-// once in 53 bits.
+// 64-bit arithmetic tells which: 15·s and 4096·s are exact and have 12 bits, so hi - lo,
+// rounded once to 53, compares with 15·s as it would unrounded unless it is rounded to it
+// (15 and a negative 2^-60): there the rounding error's sign tells.
 __device__ __forceinline__ Grid make_grid(float lo, float hi, uint32_t top) {
   Grid g;
   const float a = __uint_as_float(top);
@@ -33,7 +34,12 @@ __device__ __forceinline__ Grid make_grid(float lo, float hi, uint32_t top) {
   uint32_t bits = (__float_as_uint(want) + 0xffffu) & 0xffff0000u;
   const double range = (double)hi - (double)lo;
   const double sd = (double)__uint_as_float(bits);
-  if (sd * 15. < range || sd * 4096. < (double)a) bits += 0x10000u;
+  bool low = sd * 15. < range || sd * 4096. < (double)a;
+  if (sd * 15. == range) {   // exact: of two terms' sum the error is a sum of what each lost
+    const double back = range - hi;
+    low |= (hi - (range - back)) - (lo + back) > 0.;
+  }
+  if (low) bits += 0x10000u;
   if (!(top <= 0x5f800000u)) bits = 0x7fc00000u;   // 2^64; NaN and Inf have larger bits
   g.s = __uint_as_float(bits);
   g.inv = __builtin_amdgcn_rcpf(g.s);

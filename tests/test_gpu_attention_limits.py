@@ -171,3 +171,24 @@ def test_weights_keep_their_bits(pq, heads, kv_heads, dim, group, news, most, wi
     off = (y.cpu() != torch.from_numpy(ref).to(torch.bfloat16)).double().mean().item()
     print(f"{off:.5f} of the results are not the nearest", flush=True)
     assert off <= 1.5 / 128
+
+
+# ---------------------------------------------------------------- the cache's grid
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 128)])
+def test_a_range_just_above_fifteen_steps(pq, dtype, dim, group):
+    """max - min that 53 bits round to 15 steps: the step is the next one up, or not, by what was rounded away."""
+    rows = []
+    for e in (-40, 0, 33):
+        for m in (1.0, 1.5, 1.0078125, 1.9921875):         # 15·m has at most 12 bits, 8 of them where bf16 holds it
+            for tiny in (2.0 ** -60, -2.0 ** -60, 2.0 ** -54, -2.0 ** -52, 0.0):
+                for sign in (1.0, -1.0):
+                    x = torch.linspace(0.1, 0.9, group, dtype=torch.float64) * (15 * m)
+                    x[3], x[group - 2] = 15 * m, tiny
+                    rows.append(sign * x * 2.0 ** e)
+    x = torch.stack(rows).to(dtype)
+    x = x.repeat_interleave(dim // group, 0).reshape(-1, 1, dim)
+    cfg = pq.KvConfig(1, dim, group, 16)
+    K, V = Pages(pq, cfg, [x.shape[0]]).fill(x, x).read(out_dtype=torch.float32)
+    want = torch.from_numpy(oracle.kv_kept(f64(x), group)).float()
+    assert torch.equal(K.cpu(), want) and torch.equal(V.cpu(), want)
