@@ -780,6 +780,9 @@ class KvConfig:
         object.__setattr__(self, "_ref", ctypes.byref(c))
         object.__setattr__(self, "_page_bytes", None)
 
+    def __reduce__(self):   # copies and pickles are made from the fields: the C struct's address is of one process
+        return type(self), (self.kv_heads, self.head_dim, self.group_size, self.page_size)
+
     def c(self) -> "_lib.GptqKvConfig":
         return self._c
 
