@@ -926,9 +926,10 @@ def gptq_kv_attention(cfg: KvConfig, Q: torch.Tensor, pages: torch.Tensor, page_
     """Y [tokens, heads, head_dim] bf16: attention of each sequence's last
     tokens over its cache (those tokens' keys and values appended before).
     cu_seqlens as in gptq_kv_append; max_queries: the most tokens of a sequence
-    in this call as far as it is known (None: every token may be of one).  scale:
-    1/sqrt(head_dim) if None.  Without a workspace, or with one that is too
-    small, the call allocates its own."""
+    in this call as far as it is known (None: a sequence's equal share of them).
+    It chooses between kernels, and above 16 weights are rounded to bf16, which
+    otherwise have two bf16 parts.  scale: 1/sqrt(head_dim) if None.  Without a
+    workspace, or with one that is too small, the call allocates its own."""
     dim = cfg.head_dim
     if Q.dim() != 3:
         raise ValueError(f"Q must be [tokens, heads, {dim}]")
@@ -945,7 +946,7 @@ def gptq_kv_attention(cfg: KvConfig, Q: torch.Tensor, pages: torch.Tensor, page_
         if Y.dtype is not torch.bfloat16:
             raise TypeError(f"Y must be bfloat16, not {Y.dtype}")
     if max_queries is None:
-        max_queries = 1 if cu_seqlens is None else tokens
+        max_queries = -(-tokens // max(seqs[3], 1))
     fn = lib().gptq_kv_attention
     args = (cfg._ref, Q.data_ptr(), tokens, heads, qld, qhs, seqs[0], max_queries, *seqs[1:],
             dim ** -0.5 if scale is None else scale, Y.data_ptr(), yld, yhs, status)

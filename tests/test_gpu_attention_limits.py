@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle
-from attention_helpers import Pages, check, f64, kept, reference, starts
+from attention_helpers import Pages, check, f64, kept, keys_values, reference, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -192,3 +192,21 @@ def test_a_range_just_above_fifteen_steps(pq, dtype, dim, group):
     K, V = Pages(pq, cfg, [x.shape[0]]).fill(x, x).read(out_dtype=torch.float32)
     want = torch.from_numpy(oracle.kv_kept(f64(x), group)).float()
     assert torch.equal(K.cpu(), want) and torch.equal(V.cpu(), want)
+
+
+@pytest.mark.parametrize("batch,news", [(64, 1), (20, 3), (1, 40)])
+def test_max_queries_left_out_is_an_equal_share(pq, batch, news):
+    """A decode batch given by cu_seqlens takes the kernel of one token a sequence: the same bits."""
+    cfg = pq.KvConfig(2, 64, 64, 16)
+    k, v = keys_values(50 * batch, 2, 64, seed=5)
+    pages = Pages(pq, cfg, [50] * batch).fill(k, v)
+    table = torch.full((batch, 80), -1, dtype=torch.int32, device="cuda")   # in pieces: the tile is what max_queries says
+    table[:, :pages.table.shape[1]] = pages.table
+    q = torch.randn(batch * news, 8, 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    args = (pages.bytes, table, pages.lens, starts([news] * batch).cuda())
+    y = pq.gptq_kv_attention(cfg, q, *args)
+    assert torch.equal(y, pq.gptq_kv_attention(cfg, q, *args, max_queries=news))
+    other = pq.gptq_kv_attention(cfg, q, *args, max_queries=40 if news < 16 else 1)
+    assert not torch.equal(y, other)            # the kernels do differ in bits
+    if news == 1:
+        assert torch.equal(y, pq.gptq_kv_attention(cfg, q, *args[:3]))
