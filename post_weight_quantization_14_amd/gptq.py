@@ -850,8 +850,8 @@ def _sequences(cfg: KvConfig, X: torch.Tensor, other: Optional[torch.Tensor], pa
         if status.dtype is not torch.int32 or status.numel() != 1:
             raise ValueError("status must be one int32")
         st = status.data_ptr()
-    if not pages.is_contiguous():
-        raise ValueError("pages must be contiguous")
+    if pages.dtype is not torch.uint8 or not pages.is_contiguous():
+        raise ValueError("pages must be contiguous uint8")
     return (cu, kv_lens.data_ptr(), page_table.data_ptr(), batch, width, ld, pages.data_ptr(),
             pages.nbytes // page_bytes), st
 

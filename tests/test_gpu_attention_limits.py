@@ -210,3 +210,20 @@ def test_max_queries_left_out_is_an_equal_share(pq, batch, news):
     assert not torch.equal(y, other)            # the kernels do differ in bits
     if news == 1:
         assert torch.equal(y, pq.gptq_kv_attention(cfg, q, *args[:3]))
+
+
+def test_pages_are_bytes(pq):
+    """Pages of another dtype are refused by every call, and untouched."""
+    cfg = pq.KvConfig(2, 64, 64, 16)
+    k, v = (t.cuda() for t in keys_values(20, 2, 64, seed=1))
+    pages = Pages(pq, cfg, [20]).fill(k, v)
+    q = torch.randn(1, 4, 64).to(torch.bfloat16).cuda()
+    before = pages.bytes.clone()
+    for dtype in (torch.int8, torch.int32, torch.float32, torch.bfloat16):
+        bad = (pages.bytes.view(dtype), pages.table, pages.lens)
+        for call in (lambda: pq.gptq_kv_append(cfg, k[:1], v[:1], *bad), lambda: pq.gptq_kv_read(cfg, *bad, 1),
+                     lambda: pq.gptq_kv_attention(cfg, q, *bad)):
+            with pytest.raises(ValueError, match="uint8"):
+                call()
+    torch.cuda.synchronize()
+    assert torch.equal(before, pages.bytes)
