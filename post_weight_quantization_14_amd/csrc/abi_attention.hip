@@ -66,18 +66,37 @@ bool meet(const Span& a, const Span& b) {
   const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
   return d < a.bytes && -d < b.bytes;
 }
-// rows of two tensors of one size of element that share a byte, where both are slices of one buffer's rows
-bool overlap(const HeadRows& a, int64_t ha, const HeadRows& b, int64_t hb, int64_t tokens, int dim, int sa, int sb) {
-  if (!meet(span_of(a, tokens, ha, dim, sa), span_of(b, tokens, hb, dim, sb))) return false;
-  if (tokens > 1 && a.ld * sa == b.ld * sb && a.ld > 0) {   // beside each other in every row: like one token
-    const int64_t pitch = a.ld * sa, wa = ((ha - 1) * a.hs + dim) * sa, wb = ((hb - 1) * b.hs + dim) * sb;
-    if (wa <= pitch && wb <= pitch) {
-      int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % pitch;
-      if (d < 0) d += pitch;
-      return d < wa || d + wb > pitch;
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b != 0 && (a ^ b) < 0); }
+// Whether |d + o·S + i·s| < w for some o in o0 .. o1, i in i0 .. i1 (S >= s > 0, or 0 where its range is only 0).
+// Rows of a tensor do not overlap, so S is at least the inner rows' span and few o come into question.
+bool near_zero(int64_t d, int64_t S, int64_t o0, int64_t o1, int64_t s, int64_t i0, int64_t i1, int64_t w) {
+  if (S > 0) {
+    o0 = std::max(o0, floor_div(-w - i1 * s - d, S));
+    o1 = std::min(o1, floor_div(w - i0 * s - d, S) + 1);
+  }
+  for (int64_t o = o0; o <= o1; ++o) {
+    const int64_t r = d + o * S, i = s > 0 ? floor_div(-r, s) : 0;
+    for (int64_t j = i; j <= i + 1; ++j) {
+      const int64_t x = r + std::min(std::max(j, i0), i1) * s;
+      if (x < w && -x < w) return true;
     }
   }
-  return true;
+  return false;
+}
+// Rows of two tensors of the same tokens that share a byte.  Exact where strides of tokens and heads are the
+// same, as of slices of one buffer in any order of its dimensions, or where each token's heads lie within the same
+// pitch; otherwise spans that meet count.
+bool overlap(const HeadRows& a, int64_t ha, const HeadRows& b, int64_t hb, int64_t tokens, int dim, int size) {
+  if (!meet(span_of(a, tokens, ha, dim, size), span_of(b, tokens, hb, dim, size))) return false;
+  if (tokens > 1 && a.ld != b.ld) return true;
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)), w = (int64_t)dim * size;
+  const int64_t ld = a.ld * size, hs = (ha > 1 ? a.hs : b.hs) * size, t = tokens - 1;
+  if (ha == 1 || hb == 1 || a.hs == b.hs)
+    return ld >= hs ? near_zero(d, ld, -t, t, hs, 1 - ha, hb - 1, w) : near_zero(d, hs, 1 - ha, hb - 1, ld, -t, t, w);
+  const int64_t wa = (ha - 1) * a.hs * size + w, wb = (hb - 1) * b.hs * size + w;
+  if (tokens == 1 || wa > ld || wb > ld) return true;
+  const int64_t at = d - floor_div(d, ld) * ld;   // b's first byte within a's pitch
+  return at < wa || at + wb > ld;
 }
 
 gptq_status check_seqs(const int32_t* cu, const int32_t* lens, const int32_t* table, int64_t batch, int64_t tokens,
@@ -170,7 +189,7 @@ gptq_status gptq_kv_read(const gptq_kv_config* cfg, void* K, void* V, int32_t dt
   GPTQ_TRY(check_rows("V", V, dtype, tokens, L.heads, L.dim, ldv, v_head_stride, &v));
   GPTQ_TRY(check_seqs(cu_seqlens, kv_lens, page_table, batch, tokens, table_width, table_stride, num_pages, status, pages, &q));
   const int size = dtype == GPTQ_FP32 ? 4 : 2;
-  if (overlap(k, L.heads, v, L.heads, tokens, L.dim, size, size)) return fail(GPTQ_ERR_INVALID_ARG, "K overlaps V");
+  if (overlap(k, L.heads, v, L.heads, tokens, L.dim, size)) return fail(GPTQ_ERR_INVALID_ARG, "K overlaps V");
   GPTQ_TRY(check_beside_pages(k, v, L, tokens, size, pages, num_pages));
   return run_kv_read(L, k, v, dtype, q, pages, static_cast<hipStream_t>(stream));
 }
@@ -206,7 +225,7 @@ gptq_status gptq_kv_attention(const gptq_kv_config* cfg, const void* Q, int64_t 
   GPTQ_TRY(check_rows("Q", Q, GPTQ_BF16, tokens, heads, L.dim, ldq, q_head_stride, &q));
   GPTQ_TRY(check_rows("Y", Y, GPTQ_BF16, tokens, heads, L.dim, ldy, y_head_stride, &y));
   GPTQ_TRY(check_seqs(cu_seqlens, kv_lens, page_table, batch, tokens, table_width, table_stride, num_pages, status, pages, &s));
-  if (overlap(q, heads, y, heads, tokens, L.dim, 2, 2)) return fail(GPTQ_ERR_INVALID_ARG, "Y overlaps Q");
+  if (overlap(q, heads, y, heads, tokens, L.dim, 2)) return fail(GPTQ_ERR_INVALID_ARG, "Y overlaps Q");
   if (meet(span_of(y, tokens, heads, L.dim, 2), Span{pages, L.page_bytes * num_pages}))
     return fail(GPTQ_ERR_INVALID_ARG, "Y overlaps the pages");
   const KvAttentionPlan p = plan_kv_attention(L, heads, batch, tokens, max_queries, table_width * cfg->page_size);
@@ -239,8 +258,8 @@ gptq_status gptq_prompt_attention(const void* Q, const void* K, const void* V, i
   if ((tokens / 128 + std::min(batch, tokens) + 1 + 8) * heads >= int64_t(1) << 24)
     return fail(GPTQ_ERR_UNSUPPORTED, "%lld tokens of %lld sequences of %d heads in one call", (long long)tokens,
                 (long long)batch, heads);
-  if (overlap(c.Q, heads, c.Y, heads, tokens, head_dim, 2, 2) || overlap(c.K, kv_heads, c.Y, heads, tokens, head_dim, 2, 2) ||
-      overlap(c.V, kv_heads, c.Y, heads, tokens, head_dim, 2, 2))
+  if (overlap(c.Q, heads, c.Y, heads, tokens, head_dim, 2) || overlap(c.K, kv_heads, c.Y, heads, tokens, head_dim, 2) ||
+      overlap(c.V, kv_heads, c.Y, heads, tokens, head_dim, 2))
     return fail(GPTQ_ERR_INVALID_ARG, "Y overlaps Q, K or V");
   c.cu = cu_seqlens;
   c.batch = batch;
@@ -250,6 +269,18 @@ gptq_status gptq_prompt_attention(const void* Q, const void* K, const void* V, i
   c.dim = head_dim;
   c.scale = scale;
   return run_prompt_attention(c, static_cast<hipStream_t>(stream));
+}
+
+// What tests ask the checks of the calls above; host only.
+int gptq_internal_heads_overlap(const void* a, int64_t lda, int64_t hsa, int64_t ha, const void* b, int64_t ldb,
+                                int64_t hsb, int64_t hb, int64_t tokens, int32_t dim, int32_t dtype) {
+  HeadRows ra, rb;
+  if (check_rows("a", a, dtype, tokens, ha, dim, lda, hsa, &ra) != GPTQ_OK ||
+      check_rows("b", b, dtype, tokens, hb, dim, ldb, hsb, &rb) != GPTQ_OK) {
+    clear_error();
+    return -1;
+  }
+  return overlap(ra, ha, rb, hb, tokens, dim, dtype == GPTQ_FP32 ? 4 : 2);
 }
 
 }  // extern "C"

@@ -4,6 +4,7 @@ import ctypes
 import os
 import pickle
 
+import numpy as np
 import pytest
 import torch
 
@@ -26,3 +27,43 @@ def test_a_config_is_copied_and_pickled(pq):
         assert other.c() is not cfg.c() and bytes(other.c()) == bytes(cfg.c())
         assert pq.gptq_kv_page_bytes(other) == nbytes
         assert ctypes.cast(other._ref, ctypes.c_void_p).value == ctypes.addressof(other.c())
+
+
+def rows_of(at, ld, hs, heads, tokens, dim):
+    """Every element that a [tokens, heads, dim] tensor holds."""
+    return (at + ld * np.arange(tokens)[:, None, None] + hs * np.arange(heads)[:, None] + np.arange(dim)).ravel()
+
+
+def test_what_overlaps_is_found_and_nothing_else(pq):
+    """Against every element: slices of one buffer in any order of its dimensions, shifted by anything."""
+    fn = pq.lib().gptq_internal_heads_overlap
+    P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    fn.argtypes, fn.restype = [P, I64, I64, I64, P, I64, I64, I64, I64, I32, I32], ctypes.c_int
+    base, rng, found = 1 << 20, np.random.default_rng(0), [0, 0]
+    for _ in range(4000):
+        dim, tokens = int(rng.choice([64, 128])), int(rng.integers(1, 9))
+        ha, hb = int(rng.integers(1, 6)), int(rng.integers(1, 6))
+        if rng.random() < 0.5:
+            hb = ha
+        most, gap, each = max(ha, hb), int(rng.integers(0, 4)), int(rng.integers(1, 4))
+        hs = each * dim + int(rng.choice([0, 0, 8, 3]))
+        ld = most * hs + gap * dim
+        if rng.random() < 0.3:                      # heads before tokens
+            ld, hs = hs, max(tokens, 1) * hs + gap * dim
+        shift = int(rng.choice([0, 1, 8, dim // 2, dim - 1, dim, dim + 1])) + int(rng.integers(-3, 4)) * int(rng.choice([dim, hs, ld]))
+        a, b = 10 ** 5, 10 ** 5 + shift
+        want = bool(np.intersect1d(rows_of(a, ld, hs, ha, tokens, dim), rows_of(b, ld, hs, hb, tokens, dim)).size)
+        size, dtype = (2, 0) if rng.random() < 0.5 else (4, 1)
+        got = fn(base + a * size, ld, hs, ha, base + b * size, ld, hs, hb, tokens, dim, dtype)
+        assert got == int(want), (ld, hs, ha, hb, shift, tokens, dim)
+        found[want] += 1
+    assert min(found) > 800
+    # other strides of heads within the same pitch, and what is not told apart: other strides of tokens
+    assert fn(base, 1024, 128, 4, base + 2 * 512, 1024, 64, 8, 9, 64, 0) == 0
+    assert fn(base, 1024, 128, 4, base + 2 * 446, 1024, 64, 8, 9, 64, 0) == 1   # a has 448
+    assert fn(base, 1024, 128, 4, base + 2 * 512, 1088, 64, 8, 9, 64, 0) == 1
+    # the largest sizes
+    assert fn(base, 1 << 31, 64, 4096, base + (1 << 30), 1 << 31, 64, 4096, 1 << 27, 64, 0) == 0
+    assert fn(base, 1 << 31, 64, 4096, base + (1 << 19), 1 << 31, 64, 4096, 1 << 27, 64, 0) == 0
+    assert fn(base, 1 << 31, 64, 4096, base + (1 << 19) - 2, 1 << 31, 64, 4096, 1 << 27, 64, 0) == 1
+    assert fn(base, 64, 1 << 34, 4096, base + (1 << 33), 64, 1 << 34, 4096, 1 << 27, 64, 0) == 1

@@ -227,3 +227,26 @@ def test_pages_are_bytes(pq):
                 call()
     torch.cuda.synchronize()
     assert torch.equal(before, pages.bytes)
+
+
+def test_results_beside_each_other_in_one_buffer(pq):
+    """Keys and values read into one buffer, head beside head or heads before tokens; results between queries' heads."""
+    cfg = pq.KvConfig(3, 64, 32, 16)
+    k, v = keys_values(40, 3, 64, seed=1)
+    pages = Pages(pq, cfg, [40]).fill(k, v)
+    want = pages.read()
+    for shape, parts in (((40, 3, 2, 64), lambda t: (t[:, :, 0], t[:, :, 1])),
+                         ((3, 2, 40, 64), lambda t: (t[:, 0].transpose(0, 1), t[:, 1].transpose(0, 1)))):
+        K, V = parts(torch.zeros(shape, dtype=torch.bfloat16, device="cuda"))
+        pages.read(K=K, V=V)
+        assert torch.equal(K, want[0]) and torch.equal(V, want[1])
+    x = torch.randn(40, 3, 2, 64, device="cuda").to(torch.bfloat16)
+    q, y = x[:, :, 0], x[:, :, 1]
+    near, cu = q.contiguous(), starts([40]).cuda()
+    pq.gptq_prompt_attention(q, *want, cu, Y=y)
+    assert torch.equal(x[:, :, 0], near) and torch.equal(y, pq.gptq_prompt_attention(near, *want, cu))
+    pq.gptq_kv_attention(cfg, q, pages.bytes, pages.table, pages.lens, cu_seqlens=cu, Y=y)
+    assert torch.equal(x[:, :, 0], near)
+    assert torch.equal(y, pq.gptq_kv_attention(cfg, near, pages.bytes, pages.table, pages.lens, cu_seqlens=cu))
+    with pytest.raises(pq.GptqError, match="overlaps"):
+        pq.gptq_prompt_attention(q, *want, cu, Y=x.view(40, 6, 64)[:, 2:5])
