@@ -55,6 +55,13 @@ gptq_status check_rows(const char* name, const void* p, int32_t dtype, int64_t t
   return GPTQ_OK;
 }
 
+// times log2(e), as the kernels take it
+gptq_status check_scale(float scale) {
+  if (!std::isfinite(scale * 1.44269504088896340736f))
+    return fail(GPTQ_ERR_INVALID_ARG, "scale=%g: it or log2(e) times it is not finite", (double)scale);
+  return GPTQ_OK;
+}
+
 struct Span {
   const void* p;
   int64_t bytes;   // from the first to past the last
@@ -216,7 +223,7 @@ gptq_status gptq_kv_attention(const gptq_kv_config* cfg, const void* Q, int64_t 
   if (heads <= 0 || heads % cfg->kv_heads != 0 || max_queries < 0)
     return fail(GPTQ_ERR_INVALID_ARG, "heads=%d (kv_heads=%d) max_queries=%lld", heads, cfg->kv_heads, (long long)max_queries);
   if (heads > kMaxHeads) return fail(GPTQ_ERR_UNSUPPORTED, "heads=%d above %d", heads, kMaxHeads);
-  if (!std::isfinite(scale)) return fail(GPTQ_ERR_INVALID_ARG, "scale is not finite");
+  GPTQ_TRY(check_scale(scale));
   if (tokens == 0 || batch == 0) return GPTQ_OK;
   const KvLayout L = plan_kv(*cfg);
   GPTQ_TRY(check_page_bytes(L, num_pages));
@@ -246,7 +253,7 @@ gptq_status gptq_prompt_attention(const void* Q, const void* K, const void* V, i
   if (heads > kMaxHeads) return fail(GPTQ_ERR_UNSUPPORTED, "heads=%d above %d", heads, kMaxHeads);
   if (head_dim != 64 && head_dim != 128)
     return fail(GPTQ_ERR_UNSUPPORTED, "head_dim=%d (built: 64, 128)", head_dim);
-  if (!std::isfinite(scale)) return fail(GPTQ_ERR_INVALID_ARG, "scale is not finite");
+  GPTQ_TRY(check_scale(scale));
   if (tokens == 0 || batch == 0) return GPTQ_OK;
   PromptCall c;
   GPTQ_TRY(check_rows("Q", Q, GPTQ_BF16, tokens, heads, head_dim, ldq, q_head_stride, &c.Q));
