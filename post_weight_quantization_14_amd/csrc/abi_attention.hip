@@ -208,7 +208,7 @@ size_t gptq_kv_attention_workspace_bytes(const gptq_kv_config* cfg, int32_t head
     clear_error();
     return 0;
   }
-  return plan_kv_attention(plan_kv(*cfg), heads, batch, tokens, max_queries, 0).total;
+  return plan_kv_attention(plan_kv(*cfg), heads, batch, tokens, max_queries, false, 0).total;
 }
 
 gptq_status gptq_kv_attention(const gptq_kv_config* cfg, const void* Q, int64_t tokens, int32_t heads, int64_t ldq,
@@ -235,7 +235,8 @@ gptq_status gptq_kv_attention(const gptq_kv_config* cfg, const void* Q, int64_t 
   if (overlap(q, heads, y, heads, tokens, L.dim, 2)) return fail(GPTQ_ERR_INVALID_ARG, "Y overlaps Q");
   if (meet(span_of(y, tokens, heads, L.dim, 2), Span{pages, L.page_bytes * num_pages}))
     return fail(GPTQ_ERR_INVALID_ARG, "Y overlaps the pages");
-  const KvAttentionPlan p = plan_kv_attention(L, heads, batch, tokens, max_queries, table_width * cfg->page_size);
+  const KvAttentionPlan p = plan_kv_attention(L, heads, batch, tokens, max_queries, cu_seqlens == nullptr,
+                                              table_width * cfg->page_size);
   if (workspace == nullptr || ws_bytes < p.total || bad_ptr(workspace, 256))
     return fail(GPTQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu (256-byte aligned)", ws_bytes, p.total);
   return run_kv_attention(L, heads, q, y, scale, s, pages, workspace, p, static_cast<hipStream_t>(stream));
@@ -278,7 +279,20 @@ gptq_status gptq_prompt_attention(const void* Q, const void* K, const void* V, i
   return run_prompt_attention(c, static_cast<hipStream_t>(stream));
 }
 
-// What tests ask the checks of the calls above; host only.
+// What tests ask the checks and choices of the calls above; host only.
+int gptq_internal_kv_attention_plan(const gptq_kv_config* cfg, int32_t heads, int64_t batch, int64_t tokens,
+                                    int64_t max_queries, int32_t each, int64_t capacity, int32_t out[6]) {
+  if (check_kv_config(cfg) != GPTQ_OK || check_counts(tokens, batch) != GPTQ_OK || heads <= 0 || heads > kMaxHeads ||
+      heads % cfg->kv_heads != 0 || max_queries < 0 || tokens == 0 || batch == 0) {
+    clear_error();
+    return 0;
+  }
+  const KvAttentionPlan p = plan_kv_attention(plan_kv(*cfg), heads, batch, tokens, max_queries, each != 0, capacity);
+  const int32_t v[6] = {p.tile, p.parts, p.whole, p.wgs, p.waves, p.rows};
+  std::copy(v, v + 6, out);
+  return 1;
+}
+
 int gptq_internal_heads_overlap(const void* a, int64_t lda, int64_t hsa, int64_t ha, const void* b, int64_t ldb,
                                 int64_t hsb, int64_t hb, int64_t tokens, int32_t dim, int32_t dtype) {
   HeadRows ra, rb;

@@ -201,9 +201,10 @@ struct KvAttentionPlan {
   int rows;           // rows of a unit that should hold queries
   size_t partial, total;   // workspace bytes
 };
-// capacity: positions of a sequence that the page table can hold (no part in the workspace's size)
+// each: one token a sequence (no cu_seqlens); capacity: positions of a sequence that the page table can hold.
+// Neither makes the workspace larger than {false, 0}.
 KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, int64_t tokens, int64_t max_queries,
-                                  int64_t capacity);
+                                  bool each, int64_t capacity);
 gptq_status run_kv_attention(const KvLayout& L, int heads, const HeadRows& Q, const HeadRows& Y, float scale,
                              const KvSeqs& q, const void* pages, void* ws, const KvAttentionPlan& p, hipStream_t stream);
 

@@ -797,7 +797,8 @@ gptq_status launch(const Work& w, const KvAttentionPlan& p, hipStream_t stream) 
 // 20.8, 128 x 250 of 32 heads 30 / 53, but 1 x 1024 9.6 / 9.3, 1 x 2048 14.4 / 10.0.
 // Its waves are as many as leave a CU eight at the most: 64 x 100 of 32 heads, 2048
 // units, 10.4 with one wave each, 13.9 with two, 16.4 with four; 64 x 512, 512 units,
-// 17.2, 14.6 and 10.3.
+// 17.2, 14.9 and 11.1; and have a step of the table each, eight of them two: 1 x 250 of 32
+// heads 6.0 with four, 6.7 with eight, 1 x 100 5.2 and 5.6, 1 x 500 7.7 with eight.
 constexpr int64_t kWhole = 1024, kMostUnits = 1 << 22;   // a grid's limit is 2^32 threads
 // Weights are rounded once for chunks, where the matrix cores and the vector unit are the
 // bound (512 tokens over 8192, 32 heads on 8: 112 us, 132 in two parts; groups of 64 148 and
@@ -818,22 +819,27 @@ constexpr int64_t kUnits = 256;
 constexpr int64_t kWideUnits = 64, kWidePositions = 256 * 8 * kStep;
 
 KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, int64_t tokens, int64_t max_queries,
-                                  int64_t capacity) {
+                                  bool each, int64_t capacity) {
   KvAttentionPlan p;
-  const int64_t share = heads / L.heads;
-  const int64_t rows = std::min(std::max<int64_t>(max_queries, 1), std::max<int64_t>(tokens, 1)) * share;
+  const int64_t share = heads / L.heads, some = std::min(batch, tokens);   // sequences that may have tokens
+  const int64_t rows = (each ? 1 : std::min(std::max<int64_t>(max_queries, 1), std::max<int64_t>(tokens, 1))) * share;
   p.parts = rows / share > kDrafts ? 1 : 2;
   const int tile = rows <= 8 ? 8 : rows <= 16 || (p.parts == 2 && L.group != L.dim) ? 16 : 32;
   p.tile = tile;
-  auto units = [&](int tile) { return L.heads * (tokens * share / tile + std::min(batch, tokens)); };   // at the most
-  p.whole = capacity <= kWhole && units(tile) <= kMostUnits;
+  // Units at the most, for the grid: n rows take up to (n + tile - 1) / tile.  And as many as there should be, for the
+  // choices: every sequence with the rows that max_queries says (the bound gives 64 sequences of 8 rows 120 a key head).
+  auto most = [&](int tile) {
+    return L.heads * (each ? batch * ceil_div(share, tile) : (tokens * share + (tile - 1) * some) / tile);
+  };
+  auto units = [&](int tile) { return std::min(most(tile), L.heads * some * ceil_div(rows, tile)); };
+  p.whole = capacity <= kWhole && most(tile) <= kMostUnits;
   if (p.whole)
-    while (p.tile > 8 && units(p.tile / 2) <= kUnits) p.tile /= 2;
+    while (p.tile > 8 && units(p.tile / 2) <= kUnits && most(p.tile / 2) <= kMostUnits) p.tile /= 2;
   p.rows = (int)std::min<int64_t>(rows, p.tile);
   if (p.whole) {
-    p.wgs = (int)units(p.tile);
-    p.waves = 8;
-    while (p.waves > 1 && (int64_t)p.wgs * p.waves > 2048) p.waves /= 2;
+    p.wgs = (int)most(p.tile);
+    p.waves = capacity >= 2 * 8 * kStep ? 8 : 4;
+    while (p.waves > 1 && (units(p.tile) * p.waves > 2048 || p.waves * kStep > capacity)) p.waves /= 2;
   } else {
     const bool wide = units(tile) <= kWideUnits && units(tile) * capacity >= kWidePositions;
     p.wgs = wide ? kMaxWgs / 2 : kMaxWgs;

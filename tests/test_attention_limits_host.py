@@ -79,3 +79,58 @@ def test_scales_that_the_kernels_cannot_hold_are_refused(pq, scale):
                                at, 1 << 30, None) == _lib.GPTQ_ERR_INVALID_ARG
     assert L.gptq_prompt_attention(at, at * 2, at * 3, 9, 8, 4, 64, 512, 64, 256, 64, 256, 64, at, 2, scale, at * 4, 512, 64,
                                    None) == _lib.GPTQ_ERR_INVALID_ARG
+
+
+# ---------------------------------------------------------------- the form of a call
+def plan(pq, cfg, heads, batch, tokens, most, each, capacity):
+    fn = pq.lib().gptq_internal_kv_attention_plan
+    fn.argtypes = [ctypes.c_void_p, ctypes.c_int32] + [ctypes.c_int64] * 3 + [ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_int32)]
+    out = (ctypes.c_int32 * 6)()
+    assert fn(ctypes.byref(cfg.c()), heads, batch, tokens, most, each, capacity, out) == 1
+    return dict(zip(("tile", "parts", "whole", "wgs", "waves", "rows"), out))
+
+
+@pytest.mark.parametrize("share", [1, 4, 8])
+@pytest.mark.parametrize("each", [0, 1])
+def test_decode_batches_take_the_waves_that_their_units_fill(pq, share, each):
+    """64 sequences of 8 key heads are 512 units whatever the heads that share one: four waves each."""
+    p = plan(pq, pq.KvConfig(8), 8 * share, 64, 64, 1, each, 1024)
+    assert (p["tile"], p["parts"], p["whole"], p["waves"]) == (8, 2, 1, 4)
+    assert p["wgs"] == 512 if each else p["wgs"] >= 512
+    # short tables: a step for each wave, two for each of eight
+    for capacity, waves in ((16, 1), (64, 2), (128, 4), (256, 4), (511, 4), (512, 8), (1024, 8)):
+        assert plan(pq, pq.KvConfig(8), 8 * share, 4, 4, 1, each, capacity)["waves"] == waves
+    # few long sequences: eight waves from 65536 positions of the units together on
+    for length, waves, wgs in ((4096, 4, 512), (8192, 8, 256)):
+        p = plan(pq, pq.KvConfig(8), 8 * share, 1, 1, 1, each, length)
+        assert (p["whole"], p["waves"], p["wgs"]) == (0, waves, wgs)
+
+
+def test_every_unit_has_a_workgroup(pq):
+    """Calls in one launch: any split of the tokens over the sequences takes no more row tiles than the grid has."""
+    rng = np.random.default_rng(1)
+    for _ in range(3000):
+        kv_heads, share, batch = int(rng.choice([1, 2, 8])), int(rng.integers(1, 41)), int(rng.integers(1, 90))
+        counts = rng.integers(0, int(rng.choice([2, 4, 60])), batch)
+        each = bool(rng.random() < 0.3)
+        if each:
+            counts[:] = 1
+        tokens = int(counts.sum())
+        if tokens == 0:
+            continue
+        p = plan(pq, pq.KvConfig(kv_heads, 64, int(rng.choice([32, 64]))), kv_heads * share, batch, tokens,
+                 int(rng.choice([0, 1, 5, 16, 17, 100])), each, 512)
+        units = kv_heads * int(sum(-(-int(n) * share // p["tile"]) for n in counts))
+        assert p["whole"] and units <= p["wgs"] and (not each or units == p["wgs"])
+        assert p["tile"] in (8, 16, 32) and (p["parts"] == 2 or p["tile"] <= 32) and 1 <= p["rows"] <= p["tile"]
+
+
+def test_the_workspace_covers_every_form(pq):
+    """gptq_kv_attention_workspace_bytes knows neither cu_seqlens nor the table: what a call takes is no more."""
+    for group in (32, 64, 128):
+        cfg = pq.KvConfig(2, 128, group)
+        for heads in (2, 8, 80):
+            for most in (1, 5, 17, 400):
+                tiles = [plan(pq, cfg, heads, 64, 64, most, each, cap)["tile"] for each in (0, 1) for cap in (0, 512, 8192, 1 << 20)]
+                parts = pq.gptq_kv_attention_workspace_bytes(cfg, heads, 64, 64, most)
+                assert parts >= 2 * 512 * max(tiles) * (128 + 2) * 4
