@@ -143,23 +143,32 @@ __device__ __forceinline__ int64_t ragged_total(int64_t batch, const F& count) {
 // The sequence b in whose count(b) pieces the `index`-th piece of all lies, and
 // which of them it is; false past the last.  Called by whole waves, which look at
 // 64 sequences at a time: what count() kept of its last call in lane `l` is of b.
+// `base` sequences before have `before` pieces: a search for a later piece goes on from there.
 template <class F>
-__device__ __forceinline__ bool ragged_find(int64_t index, int64_t batch, const F& count, int64_t* b, int64_t* at, int* l) {
+__device__ __forceinline__ bool ragged_find(int64_t index, int64_t batch, const F& count, int64_t* b, int64_t* at, int* l,
+                                            int64_t* base, int64_t* before) {
   const int lane = threadIdx.x & 63;
-  index = uniform(index);
-  for (int64_t base = 0; base < batch; base += 64) {
-    const int64_t c = base + lane < batch ? count(base + lane) : 0;
+  index = uniform(index) - *before;
+  for (; *base < batch; *base += 64) {
+    const int64_t c = *base + lane < batch ? count(*base + lane) : 0;
     const int64_t upto = wave_scan(c);
     const uint64_t past = __ballot(upto > index);   // wave-uniform
     if (past) {
       *l = __ffsll((unsigned long long)past) - 1;
-      *b = base + *l;
+      *b = *base + *l;
       *at = index - lane_value(upto - c, *l);
       return true;
     }
-    index -= lane_value(upto, 63);
+    const int64_t all = lane_value(upto, 63);
+    index -= all;
+    *before += all;
   }
   return false;
+}
+template <class F>
+__device__ __forceinline__ bool ragged_find(int64_t index, int64_t batch, const F& count, int64_t* b, int64_t* at, int* l) {
+  int64_t base = 0, before = 0;
+  return ragged_find(index, batch, count, b, at, l, &base, &before);
 }
 
 // ---------------------------------------------------------------- softmax

@@ -111,17 +111,25 @@ struct Work {
   Split* meta;           // [wgs]: of a unit split over workgroups that begins in this one
 };
 
+// a / b of uniform numbers, by 32 bits where they do
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
 // A unit is one row tile (R query rows: tokens x the heads that share a key
 // head) of one key head of one sequence; its steps are 32 positions each.  All
 // units' steps lie one after the other, by sequence, head and tile (WHOLE: all
 // units, of one step each here).  Lane i keeps what it read of sequence i: batches of
-// up to 64 are read once.
+// up to 64 are read once.  Of larger ones a unit's index tells its sequence where each
+// has as many (one token each, taken whole); else a workgroup searches on from its last.
 template <int R, bool WHOLE>
 struct Units {
   const Work& w;
   int64_t capacity, total;
   KvSeq mine;
   int64_t upto, own;   // steps of sequences 0 .. lane, and of this lane's
+  int64_t base = 0, before = 0;   // of the search
   bool few;
   __device__ __forceinline__ explicit Units(const Work& w_) : w(w_) {
     capacity = min64(w.q.width * w.L.recs * kKvRec, kKvMost);
@@ -147,30 +155,31 @@ struct Units {
   static __device__ __forceinline__ int steps(const KvSeq& s) { return s.len > kStep ? (int)(((int64_t)s.len + kStep - 1) / kStep) : 1; }
   __device__ __forceinline__ int64_t steps_of(const KvSeq& s) const { return tiles(s, w.share) * (WHOLE ? 1 : steps(s)) * w.L.heads; }
   // the sequence that step `pos` belongs to, and which of its steps it is; false past the last
-  __device__ __forceinline__ bool find(int64_t pos, KvSeq* found, int64_t* b, int64_t* at) const {
+  __device__ __forceinline__ bool find(int64_t pos, KvSeq* found, int64_t* b, int64_t* at) {
     KvSeq s = mine;
     int l;
     if (few) {
       l = __ffsll((unsigned long long)__ballot(upto > pos)) - 1;
       *b = l;
       *at = pos - lane_value(upto - own, l);
+    } else if (WHOLE && w.q.cu == nullptr) {
+      const int64_t each = (int64_t)((w.share + R - 1) / R) * w.L.heads;
+      *b = divide(pos, each);
+      *at = pos - *b * each;
+      if (*b >= w.q.batch) return false;
+      *found = uniform(kv_seq(w.q, *b, capacity));
+      return true;
     } else {
       auto count = [&](int64_t i) {
         s = kv_seq(w.q, i, capacity);
         return steps_of(s);
       };
-      if (!ragged_find(pos, w.q.batch, count, b, at, &l)) return false;
+      if (!ragged_find(pos, w.q.batch, count, b, at, &l, &base, &before)) return false;
     }
     *found = lane_value(s, l);
     return true;
   }
 };
-
-// a / b of uniform numbers, by 32 bits where they do
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
-  return a / b;
-}
 
 // lane n of the row of 16 for SP 1, of the lane's own four for SP 2
 template <int SP, int N>
@@ -237,7 +246,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n16 = lane & 15, kg = lane >> 4;
   const int nq = n16 % NC, half = n16 / NC;   // query row of the column, record of its logits
-  const Units<R, WHOLE> units(w);
+  Units<R, WHOLE> units(w);
   const Consts kc;
 
   // in steps, or in units where each is taken whole

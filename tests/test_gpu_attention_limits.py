@@ -250,3 +250,27 @@ def test_results_beside_each_other_in_one_buffer(pq):
     assert torch.equal(y, pq.gptq_kv_attention(cfg, near, pages.bytes, pages.table, pages.lens, cu_seqlens=cu))
     with pytest.raises(pq.GptqError, match="overlaps"):
         pq.gptq_prompt_attention(q, *want, cu, Y=x.view(40, 6, 64)[:, 2:5])
+
+
+# ---------------------------------------------------------------- the largest batches
+@pytest.mark.parametrize("batch,kv_heads,share", [(65536, 1, 1), (65535, 2, 3), (5000, 2, 20)])
+@pytest.mark.parametrize("width", [2, 80])                 # in one launch, in pieces
+@pytest.mark.parametrize("given", [False, True])
+def test_batches_of_up_to_65536_sequences(pq, batch, kv_heads, share, width, given):
+    """Sequences that repeat: some against 64 bits, the others equal to those, whether cu_seqlens is given or not."""
+    cfg = pq.KvConfig(kv_heads, 64, 64, 16)
+    kinds, heads = 97, kv_heads * share
+    total = [1 + i % 23 for i in range(kinds)]
+    k, v = keys_values(sum(total), kv_heads, 64, seed=3)
+    pages = Pages(pq, cfg, total).fill(k, v)
+    q = torch.randn(kinds, heads, 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    kind = torch.arange(batch) % kinds
+    table = torch.full((batch, width), -1, dtype=torch.int32, device="cuda")
+    table[:, :2] = pages.table[kind][:, :2]
+    cu = torch.arange(batch + 1, dtype=torch.int32, device="cuda") if given else None
+    y = pq.gptq_kv_attention(cfg, q[kind].cuda(), pages.bytes, table, pages.lens[kind], cu_seqlens=cu, max_queries=1)
+    (kk, ks, kz), (vk, vs, vz) = kept(f64(k), 64), kept(f64(v), 64)
+    ref = reference(f64(q), kk, vk, 0.125, total, [1] * kinds, ((ks, kz), (vs, vz), 64))
+    check(y[:kinds], *ref, f"{batch} sequences")
+    assert torch.equal(y, y[:kinds][kind])
+    check(y[-kinds:], *(r[kind[-kinds:]] for r in ref), "the last")
