@@ -808,7 +808,11 @@ gptq_status launch(const Work& w, const KvAttentionPlan& p, hipStream_t stream) 
 // units, 10.4 with one wave each, 13.9 with two, 16.4 with four; 64 x 512, 512 units,
 // 17.2, 14.9 and 11.1; and have a step of the table each, eight of them two: 1 x 250 of 32
 // heads 6.0 with four, 6.7 with eight, 1 x 100 5.2 and 5.6, 1 x 500 7.7 with eight.
+//   With cu_seqlens each such workgroup searches the batch for its unit, so larger ones go in
+// pieces, which search once: sequences of 20 tokens, 32 heads on 8, us (whole / pieces):
+// 1600 73 / 132, 4096 330 / 327, 16384 4222 / 1299.
 constexpr int64_t kWhole = 1024, kMostUnits = 1 << 22;   // a grid's limit is 2^32 threads
+constexpr int64_t kSearched = 4096;
 // Weights are rounded once for chunks, where the matrix cores and the vector unit are the
 // bound (512 tokens over 8192, 32 heads on 8: 112 us, 132 in two parts; groups of 64 148 and
 // 187): from more tokens a sequence on than drafts have, whatever the heads.
@@ -841,7 +845,7 @@ KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, i
     return L.heads * (each ? batch * ceil_div(share, tile) : (tokens * share + (tile - 1) * some) / tile);
   };
   auto units = [&](int tile) { return std::min(most(tile), L.heads * some * ceil_div(rows, tile)); };
-  p.whole = capacity <= kWhole && most(tile) <= kMostUnits;
+  p.whole = capacity <= kWhole && most(tile) <= kMostUnits && (each || batch <= kSearched);
   if (p.whole)
     while (p.tile > 8 && units(p.tile / 2) <= kUnits && most(p.tile / 2) <= kMostUnits) p.tile /= 2;
   p.rows = (int)std::min<int64_t>(rows, p.tile);

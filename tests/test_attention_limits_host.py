@@ -100,6 +100,9 @@ def test_decode_batches_take_the_waves_that_their_units_fill(pq, share, each):
     # short tables: a step for each wave, two for each of eight
     for capacity, waves in ((16, 1), (64, 2), (128, 4), (256, 4), (511, 4), (512, 8), (1024, 8)):
         assert plan(pq, pq.KvConfig(8), 8 * share, 4, 4, 1, each, capacity)["waves"] == waves
+    # large batches whose units would have to be searched for go in pieces
+    assert plan(pq, pq.KvConfig(8), 8 * share, 4096, 4096, 1, each, 512)["whole"] == 1
+    assert plan(pq, pq.KvConfig(8), 8 * share, 4097, 4097, 1, each, 512)["whole"] == each
     # few long sequences: eight waves from 65536 positions of the units together on
     for length, waves, wgs in ((4096, 4, 512), (8192, 8, 256)):
         p = plan(pq, pq.KvConfig(8), 8 * share, 1, 1, 1, each, length)
