@@ -473,7 +473,8 @@ gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const voi
  *              order, if a sequence's rows, length or a page of it is out of
  *              range (left as it is otherwise: the caller clears it).  Such a
  *              sequence's tokens (a page out of range: those of the page) are not
- *              written; what would be read from it is NaN.
+ *              written; what would be read from it is NaN.  If cu_seqlens falls,
+ *              what becomes of sequences behind the fall is not defined.
  *
  * gptq_kv_append quantizes K and V (bf16 or fp32) into the cache.  Each token's
  * and head's channels go by groups of group_size (32, 64, 128, or -1 for all),
@@ -493,8 +494,8 @@ gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const voi
  *   Y = Σ_{p <= t} softmax_p(scale·Q·K̂[p])·V̂[p]
  * for bf16 Q and Y: a token a sequence in decoding, several where drafts are
  * checked, hundreds for a chunk of a prompt.  The tokens are appended first.
- * The codes enter the products exactly; all sums are fp32 (and stay finite for |Q|
- * up to 2^108).  A token that sees no position (kv_lens[b] < n) gives zeros.
+ * The codes enter the products exactly; all sums are fp32 (and stay finite while
+ * |Q| <= 2^108 and head_dim·|Q|·|K| <= 2^126, also times scale·log2(e)).  A token that sees no position (kv_lens[b] < n) gives zeros.
  * max_queries: the most tokens that a sequence has in this call, as far as the
  * caller knows (0: one).  It chooses between kernels, which give the right results
  * for any number, and how weights enter: up to 16 as two bf16 parts (2^-16 of each
@@ -507,7 +508,9 @@ gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const voi
  * gptq_prompt_attention: causal attention within each of `batch` sequences of
  * bf16 Q, K, V, before any cache:
  *   Y_i = Σ_{j <= i} softmax_j(scale·Q_i·K_j)·V_j.
- * Weights are rounded to bf16 for the second product; all sums are fp32.  What
+ * Weights are rounded to bf16 for the second product; all sums are fp32 (and stay
+ * finite while head_dim·|Q|·|K| <= 2^126, also times scale·log2(e), and tokens·|V|
+ * <= 2^119).  What
  * a token does not see (later tokens, other sequences) may be anything, NaN too.
  * cu_seqlens beyond 0 .. tokens is cut to it.
  * ---------------------------------------------------------------------- */

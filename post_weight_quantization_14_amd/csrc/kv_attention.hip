@@ -6,7 +6,7 @@
 // 128 + c is a bf16 made from four bits by one AND-OR, so keys enter the matrix
 // cores exactly; scales and zero points are taken off in fp32.
 //
-// What bounds it.  A step of 32 positions reads 4.6 KB (heads of 128, one scale
+// What bounds it.  A step of 32 positions reads 4.35 KB (heads of 128, one scale
 // each) and takes about 230 vector instructions for up to 8 rows, most of them to
 // spread codes, then some 100 more for every further 16.  Decoding many sequences
 // is near memory: 64 of up to 8192 tokens with 8 key heads (288 MB) take 78 us, 3.7

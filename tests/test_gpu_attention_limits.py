@@ -274,3 +274,116 @@ def test_batches_of_up_to_65536_sequences(pq, batch, kv_heads, share, width, giv
     check(y[:kinds], *ref, f"{batch} sequences")
     assert torch.equal(y, y[:kinds][kind])
     check(y[-kinds:], *(r[kind[-kinds:]] for r in ref), "the last")
+
+
+@pytest.mark.parametrize("a,b", [(90, 20), (55, 55), (108, 0), (100, -60), (-30, 55)])
+@pytest.mark.parametrize("news", [1, 9, 20])
+def test_queries_and_keys_of_any_size(pq, a, b, news):
+    """Queries 2^a and keys 2^b times as large with a scale 2^-(a + b) times as large: the same bits."""
+    cfg = pq.KvConfig(2, 128, 64, 16)
+    total, new = [300, 45], [news, news]
+    k, v = (t.cuda() for t in keys_values(345, 2, 128, seed=41))
+    q = torch.randn(345, 8, 128, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    ys = []
+    for e, f in ((0, 0), (a, b)):
+        pages = Pages(pq, cfg, total).fill(k * 2.0 ** f, v)
+        scale = 0.125 * 2.0 ** -(e + f)
+        ys.append((pq.gptq_kv_attention(cfg, q[:2 * news] * 2.0 ** e, pages.bytes, pages.table, pages.lens, starts(new).cuda(),
+                                        news, scale=scale),
+                   pq.gptq_prompt_attention(q * 2.0 ** e, k * 2.0 ** f, v, starts(total).cuda(), scale=scale)))
+    assert torch.isfinite(ys[0][0]).all() and torch.isfinite(ys[0][1]).all()
+    assert torch.equal(ys[0][0], ys[1][0]) and torch.equal(ys[0][1], ys[1][1])
+
+
+@pytest.mark.parametrize("rows", [[0, 40, 20, 90], [-3, 40, 60, 90], [0, 40, 60, 95], [0, 200, 60, 90], [0, 40, 61, 90]])
+def test_rows_out_of_range_touch_nothing_else(pq, rows):
+    """Pages of sequences out of range and spare ones keep every byte, sequences in range are done, rows of sequences out
+    of range read as NaN, rows of none are left as they are."""
+    cfg = pq.KvConfig(2, 64, 64, 16)
+    total = [40, 20, 30]
+    k, v = keys_values(90, 2, 64, seed=9)
+    news = [b - a for a, b in zip(rows, rows[1:])]
+    good = [b for b in range(3) if 0 <= rows[b] <= rows[b + 1] <= 90 and news[b] <= total[b]]
+    assert 0 < len(good) < 3
+    cu, st = torch.tensor(rows, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    pages, want = Pages(pq, cfg, total), Pages(pq, cfg, total)
+    pq.gptq_kv_append(cfg, k.cuda(), v.cuda(), pages.bytes, pages.table, pages.lens, cu_seqlens=cu, status=st)
+    assert st.item() == -1
+    for b in good:
+        own = slice(rows[b], rows[b + 1])
+        pq.gptq_kv_append(cfg, k[own].cuda(), v[own].cuda(), want.bytes, want.table[b:b + 1], want.lens[b:b + 1],
+                          cu_seqlens=starts([news[b]]).cuda())
+    assert torch.equal(pages.bytes, want.bytes)
+    count = torch.zeros(90, dtype=torch.int64)          # sequences that claim a row
+    for b in range(3):
+        count[max(rows[b], 0):max(rows[b + 1], 0)] += 1
+    K, V = (torch.full((90, 2, 64), 5.0, device="cuda") for _ in range(2))
+    st.zero_()
+    pq.gptq_kv_read(cfg, pages.bytes, pages.table, pages.lens, 90, cu_seqlens=cu, K=K, V=V, status=st)
+    assert st.item() == -1
+    for got, x in ((K.cpu(), k), (V.cpu(), v)):
+        ref = torch.from_numpy(kept(f64(x), 64)[0]).float()
+        assert (got[count == 0] == 5).all()
+        for b in range(3):
+            own = torch.zeros(90, dtype=torch.bool)
+            own[max(rows[b], 0):max(rows[b + 1], 0)] = True
+            own &= count == 1
+            assert torch.equal(got[own], ref[own]) if b in good else torch.isnan(got[own]).all()
+
+
+def test_falling_rows_of_prompts(pq):
+    """Ranges that fall are empty, ranges past the rows are cut, rows of none are left as they are."""
+    q, k, v = (torch.randn(50, 2, 64, generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).cuda() for i in range(3))
+    for rows, own in (([40, 10, 60, 20], (10, 50)), ([30, 20, 20, 45], (20, 45)), ([7, 3, -5, 12], (0, 12))):
+        Y = torch.full((50, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+        pq.gptq_prompt_attention(q, k, v, torch.tensor(rows, dtype=torch.int32, device="cuda"), Y=Y)
+        part = slice(*own)
+        want = pq.gptq_prompt_attention(q[part].contiguous(), k[part].contiguous(), v[part].contiguous(),
+                                        torch.tensor([0, own[1] - own[0]], dtype=torch.int32, device="cuda"))
+        assert torch.equal(Y[part], want)
+        Y[part] = 5.0
+        assert (Y == 5).all()
+
+
+# ---------------------------------------------------------------- lengths in earnest
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 128), (16, 4, 64)])
+@pytest.mark.parametrize("total", [[6000], [2311, 4000, 77]])
+def test_long_prompts(pq, heads, kv_heads, dim, total):
+    g = torch.Generator().manual_seed(heads)
+    q, k, v = (torch.randn(sum(total), h, dim, generator=g).to(torch.bfloat16) for h in (heads, kv_heads, kv_heads))
+    k = (k.float() + torch.randn(kv_heads, dim, generator=g)).to(torch.bfloat16)
+    y = pq.gptq_prompt_attention(q.cuda(), k.cuda(), v.cuda(), starts(total).cuda())
+    for h in (1, heads - 1):
+        one = slice(h * kv_heads // heads, h * kv_heads // heads + 1)
+        check(y[:, h:h + 1], *reference(f64(q[:, h:h + 1]), f64(k[:, one]), f64(v[:, one]), dim ** -0.5, total, total),
+              f"head {h} of {heads}, {total}")
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,group", [(8, 2, 128, 128), (8, 2, 128, 64), (8, 2, 128, 32), (14, 2, 64, 32)])
+@pytest.mark.parametrize("total,news", [([8192], [512]), ([5000, 3001], [300, 177]), ([9000, 7000, 40], [1, 1, 1]),
+                                        ([4097, 4000], [6, 5])])
+def test_long_caches(pq, heads, kv_heads, dim, group, total, news):
+    """Chunks, drafts and tokens over thousands of positions of several key heads."""
+    cfg = pq.KvConfig(kv_heads, dim, group, 64)
+    k, v = keys_values(sum(total), kv_heads, dim, seed=7)
+    pages = Pages(pq, cfg, total, 7).fill(k, v)
+    q = torch.randn(sum(news), heads, dim, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16)
+    y = pq.gptq_kv_attention(cfg, q.cuda(), pages.bytes, pages.table, pages.lens, cu_seqlens=starts(news).cuda(), max_queries=max(news))
+    share = heads // kv_heads
+    for h in (0, heads - 2):
+        one = slice(h // share, h // share + 1)
+        (kk, ks, kz), (vk, vs, vz) = kept(f64(k[:, one]), group), kept(f64(v[:, one]), group)
+        check(y[:, h:h + 1], *reference(f64(q[:, h:h + 1]), kk, vk, dim ** -0.5, total, news, ((ks, kz), (vs, vz), group)),
+              f"head {h} of {heads}, {news} over {total}")
+
+
+def test_a_long_sequence_of_eight_key_heads(pq):
+    cfg = pq.KvConfig(8, 128, 64, 64)
+    k, v = keys_values(32768, 8, 128, seed=2)
+    pages = Pages(pq, cfg, [32768], 3).fill(k, v)
+    q = torch.randn(1, 64, 128, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16)
+    y = pq.gptq_kv_attention(cfg, q.cuda(), pages.bytes, pages.table, pages.lens)
+    for h in (0, 31, 63):
+        one = slice(h // 8, h // 8 + 1)
+        (kk, ks, kz), (vk, vs, vz) = kept(f64(k[:, one]), 64), kept(f64(v[:, one]), 64)
+        check(y[:, h:h + 1], *reference(f64(q[:, h:h + 1]), kk, vk, 128 ** -0.5, [32768], [1], ((ks, kz), (vs, vz), 64)), f"head {h}")
