@@ -495,7 +495,8 @@ gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const voi
  * for bf16 Q and Y: a token a sequence in decoding, several where drafts are
  * checked, hundreds for a chunk of a prompt.  The tokens are appended first.
  * The codes enter the products exactly; all sums are fp32 (and stay finite while
- * |Q| <= 2^108 and head_dim·|Q|·|K| <= 2^126, also times scale·log2(e)).  A token that sees no position (kv_lens[b] < n) gives zeros.
+ * |Q| <= 2^108 and head_dim·|Q|·|K| <= 2^126, also times scale·log2(e)).  A token that sees no position (kv_lens[b] < n) gives
+ * zeros; scale 0 weighs all positions alike, whatever Q holds.
  * max_queries: the most tokens that a sequence has in this call, as far as the
  * caller knows (0: one).  It chooses between kernels, which give the right results
  * for any number, and how weights enter: up to 16 as two bf16 parts (2^-16 of each
