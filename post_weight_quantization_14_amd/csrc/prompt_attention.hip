@@ -174,7 +174,12 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
   }
 
   f32x16_t o[DT];
-  float m, rest, l;   // weights are relative to 2^(m + rest)
+  float m, l, by;   // weights are 2^(logit·by - m)
+  // A maximum with a rest lies here while the wave has one: its logits are then taken
+  // relative to it before their weights, and m is 0, by 1.  (In registers, heads of 64
+  // reloaded one a tile, behind the copies in flight: 98 -> 117 us for 8192 tokens of 8.)
+  __shared__ float far_m[kThreads], far_rest[kThreads];
+  uint64_t far;     // lanes with a rest
   // A masked value meets a weight of 0, and 0·Inf is NaN.  Such values can only
   // be in the last tiles; a result that is not finite is computed once more,
   // carefully: what is not finite is left out of the product there, and counted
@@ -186,9 +191,9 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
 #pragma unroll
       for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
     m = kNone;
-    rest = 0.f;
     l = 0.f;
-    uint64_t far = 0;   // lanes with a rest
+    by = a.scale;
+    far = 0;
     fetch(0, lds0);
     auto step = [&](int tile, uint8_t* cur, uint8_t* nxt) {
       asm volatile("" ::: "memory");
@@ -230,24 +235,28 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
 #pragma unroll
       for (int r = 1; r < 16 * U; ++r) top = fmaxf(top, s[r >> 4][r & 15]);
       top = half_max(top);
-      if (__ballot(fmaf(top, a.scale, -m) - rest > 8.f)) {   // sums are scaled again only when the maximum grows by more than 2^8
+      if (far | __ballot(fmaf(top, a.scale, -m) > 8.f)) {   // sums are scaled again only when the maximum grows by more than 2^8
+        float rest = 0.f;
+        if (__builtin_expect(far != 0, 0)) m = far_m[tid], rest = far_rest[tid];
         const float f = raise_to(top, a.scale, &m, &rest);
         far = __ballot(rest != 0.f);
+        by = a.scale;
+        if (__builtin_expect(far != 0, 0)) {
+          far_m[tid] = m;
+          far_rest[tid] = rest;
+#pragma unroll
+          for (int r = 0; r < 16 * U; ++r) s[r >> 4][r & 15] = fmaf(s[r >> 4][r & 15], a.scale, -m) - rest;
+          m = 0.f;
+          by = 1.f;
+        }
         l *= f;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] *= f;
       }
-      float by = a.scale, base = m;
-      if (__builtin_expect(far != 0, 0)) {
-#pragma unroll
-        for (int r = 0; r < 16 * U; ++r) s[r >> 4][r & 15] = fmaf(s[r >> 4][r & 15], a.scale, -m) - rest;
-        by = 1.f;
-        base = 0.f;
-      }
       bf16x8_t p[2 * U];
 #pragma unroll
       for (int r = 0; r < 16 * U; ++r) {
-        const float e = __builtin_amdgcn_exp2f(fmaf(s[r >> 4][r & 15], by, -base));
+        const float e = __builtin_amdgcn_exp2f(fmaf(s[r >> 4][r & 15], by, -m));
         l += e;
         p[r >> 3][r & 7] = (__bf16)e;
       }
@@ -313,6 +322,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
     static_assert(DT * 4 * 64 * 16 <= 2 * TB && kWaves == 4, "");
     uint8_t* mine = wave < 2 ? lds0 : lds1;
     __shared__ float om[2][64], orest[2][64], ol[2][64];
+    float rest = 0.f;
+    if (far) m = far_m[tid], rest = far_rest[tid];
     __syncthreads();
     if (part) {
 #pragma unroll
