@@ -28,7 +28,7 @@ typedef __attribute__((address_space(4))) int32_t constant_int;
 
 constexpr int kStep = 32;        // positions of a wave's step: two records
 constexpr float kNone = -3e38f;  // a running maximum that has seen nothing
-constexpr int kMaxWgs = 512;     // of a split call: two a CU (768: 1 x 32768 28 us instead of 20, for the parts to join)
+constexpr int kMaxWgs = 512;     // of a split call: two a CU (768: 1 x 32768 30 us instead of 20, 64 x 4096 57 instead of 53)
 
 __device__ __forceinline__ float swap16(float x, float* y) {   // lane ^ 16
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -243,6 +243,9 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
   constexpr int kPitch = D + 4;
   __shared__ float so[W][16][kPitch];
   __shared__ float sm[W][16], sr[W][16], sl[W][16];
+  // Maxima with a rest lie here while the wave has one: its logits are then taken relative
+  // to them before their weights, and m is 0, by 1 (registers are short).
+  __shared__ float far_m[W][NT * 16], far_rest[W][NT * 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n16 = lane & 15, kg = lane >> 4;
   const int nq = n16 % NC, half = n16 / NC;   // query row of the column, record of its logits
@@ -341,22 +344,17 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
     Pages ahead;
     bf16x8_t qf[NT][KS];
     float qs[NT][NG];   // sums of the query's channels, by group
-    // The next step's codes are asked for before this one is computed, or where registers
-    // are short once its keys are done with (16 x 4096 tokens, 6 drafts, groups of 64: 34.0 us
-    // instead of 35.7).
-    constexpr bool kLate = NT == 2 && NG > 1;
     constexpr bool kMat = NT == 2 && NG == 1;   // sums of zero points by the matrix cores too
     f32x4_t zo[NT];
     uint32_t za[4] = {0, 0, 0, 0};
     // bytes that lane takes of its own word (4 .. 7) and its neighbour's (0 .. 3): even lanes both high halves, odd both low
     const uint32_t zsel = lane & 1 ? 0x05040100u : 0x03020706u;
     f32x4_t o[NT][MT];
-    float m[NT], rest[NT], l[NT], zs[NT][NG];   // weights are relative to 2^(m + rest)
+    float m[NT], by = w.scale, l[NT], zs[NT][NG];   // weights are 2^(logit·by - m)
     uint64_t far = 0;   // lanes with a rest
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt] = kNone;
-      rest[nt] = 0.f;
       l[nt] = 0.f;
       zo[nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -366,7 +364,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
     }
 
     auto compute = [&](int st, Step<D, G, SP>& x, auto next) INLINE {
-      if constexpr (!kLate) next();
+      next();
       float sf[SP][NG], zf[SP][NG];   // scales and 128 + zero points, of the positions of `pw`
 #pragma unroll
       for (int i = 0; i < SP; ++i)
@@ -418,11 +416,6 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
             o = g == 0 ? y * f : o + y * f;
           });
       }
-      if constexpr (kLate) {
-        __builtin_amdgcn_sched_barrier(0);
-        next();
-        __builtin_amdgcn_sched_barrier(0);
-      }
       const bool edge = (st + 1) * kStep > least;
       if (edge) {
 #pragma unroll
@@ -440,12 +433,15 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
 #pragma unroll
         for (int i = 1; i < E; ++i) t = fmaxf(t, sx[nt][i]);
         top[nt] = quad_max(t);
-        grown |= fmaf(top[nt], w.scale, -m[nt]) - rest[nt] > 8.f;
+        grown |= fmaf(top[nt], w.scale, -m[nt]) > 8.f;
       }
-      if (__ballot(grown)) {
+      if (far | __ballot(grown)) {
+        float rest[NT];
         bool rests = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          rest[nt] = 0.f;
+          if (__builtin_expect(far != 0, 0)) m[nt] = far_m[wave][nt * 16 + n16], rest[nt] = far_rest[wave][nt * 16 + n16];
           const float f = raise_to(top[nt], w.scale, &m[nt], &rest[nt]);
           rests |= rest[nt] != 0.f;
           l[nt] *= f;
@@ -456,25 +452,25 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
           for (int j = 0; j < MT; ++j) o[nt][j] *= f;
         }
         far = __ballot(rests);
-      }
-      float by = w.scale, base[NT];
+        by = w.scale;
+        if (__builtin_expect(far != 0, 0)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) base[nt] = m[nt];
-      if (__builtin_expect(far != 0, 0)) {
+          for (int nt = 0; nt < NT; ++nt) {
+            far_m[wave][nt * 16 + n16] = m[nt];   // the same in the four lanes of a column
+            far_rest[wave][nt * 16 + n16] = rest[nt];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int i = 0; i < E; ++i) sx[nt][i] = fmaf(sx[nt][i], w.scale, -m[nt]) - rest[nt];
-          base[nt] = 0.f;
+            for (int i = 0; i < E; ++i) sx[nt][i] = fmaf(sx[nt][i], w.scale, -m[nt]) - rest[nt];
+            m[nt] = 0.f;
+          }
+          by = 1.f;
         }
-        by = 1.f;
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < E; ++i) {
           float& p = sx[nt][i];
-          p = __builtin_amdgcn_exp2f(fmaf(p, by, -base[nt]));
+          p = __builtin_amdgcn_exp2f(fmaf(p, by, -m[nt]));
           l[nt] += p;
         }
       // values
@@ -606,14 +602,16 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      float rest = 0.f;
+      if (far) m[nt] = far_m[wave][nt * 16 + n16], rest = far_rest[wave][nt * 16 + n16];
       l[nt] = quad_sum(l[nt]);
       if (kMat) zs[nt][0] = kg >= 2 ? zo[nt][0] + zo[nt][1] : 0.f;   // rows 8, 9 and 12, 13
 #pragma unroll
       for (int g = 0; g < NG; ++g) zs[nt][g] = quad_sum(zs[nt][g]);
-      if (kg == 0) sm[wave][n16] = m[nt], sr[wave][n16] = rest[nt];
+      if (kg == 0) sm[wave][n16] = m[nt], sr[wave][n16] = rest;
       __syncthreads();
       float up_rest;
-      const float up = top_of(nq, &up_rest), f = exp2f((m[nt] - up) + (rest[nt] - up_rest));
+      const float up = top_of(nq, &up_rest), f = exp2f((m[nt] - up) + (rest - up_rest));
       if (kg == 0) sl[wave][n16] = l[nt] * f;
 #pragma unroll
       for (int j = 0; j < MT; ++j)
@@ -802,34 +800,34 @@ gptq_status launch(const Work& w, const KvAttentionPlan& p, hipStream_t stream) 
 // A unit is a workgroup's of its own, in one launch, where the page table holds no
 // longer sequence than kWhole; otherwise a long one would be waited for, and
 // workgroups get equal pieces of all units' steps.  Heads of 128, 8 key heads, us
-// (whole / pieces): 1 x 512 tokens 7.4 / 9.2, 32 x 768 9.7 / 13.6, 64 x 1000 17.8 /
-// 20.8, 128 x 250 of 32 heads 30 / 53, but 1 x 1024 9.6 / 9.3, 1 x 2048 14.4 / 10.0.
+// (whole / pieces): 1 x 512 tokens 7.4 / 9.2, 32 x 768 of 32 key heads 22.5 / 27.4, 64 x 1000
+// 16.8 / 19.3, 128 x 250 of 32 heads 31 / 53, but 1 x 1024 10.1 / 9.3, 1 x 2048 15.0 / 10.8.
 // Its waves are as many as leave a CU eight at the most: 64 x 100 of 32 heads, 2048
-// units, 10.4 with one wave each, 13.9 with two, 16.4 with four; 64 x 512, 512 units,
-// 17.2, 14.9 and 11.1; and have a step of the table each, eight of them two: 1 x 250 of 32
-// heads 6.0 with four, 6.7 with eight, 1 x 100 5.2 and 5.6, 1 x 500 7.7 with eight.
+// units, 10.9 with one wave each, 14.8 with two, 17 with four; 64 x 512, 512 units,
+// 17.5, 15.1 and 10.7; and have a step of the table each, eight of them three: 1 x 100
+// 5.1 with four, 5.6 with eight, 1 x 250 5.9 and 6.7, 1 x 512 7.4 and 7.9, 1 x 900 10.4 and 10.3.
 //   With cu_seqlens each such workgroup searches the batch for its unit, so larger ones go in
 // pieces, which search once: sequences of 20 tokens, 32 heads on 8, us (whole / pieces):
 // 1600 73 / 132, 4096 330 / 327, 16384 4222 / 1299.
 constexpr int64_t kWhole = 1024, kMostUnits = 1 << 22;   // a grid's limit is 2^32 threads
 constexpr int64_t kSearched = 4096;
 // Weights are rounded once for chunks, where the matrix cores and the vector unit are the
-// bound (512 tokens over 8192, 32 heads on 8: 112 us, 132 in two parts; groups of 64 148 and
-// 187): from more tokens a sequence on than drafts have, whatever the heads.
+// bound (512 tokens over 8192, 32 heads on 8: 113 us, 131 in two parts; groups of 64 148 and
+// 187, of 32 238 and 320): from more tokens a sequence on than drafts have, whatever the heads.
 constexpr int64_t kDrafts = 16;
 // Two parts for 32 rows of more scales than one a head are short of registers: 16 sequences
-// of 4096, 6 drafts of 4 heads a key head, groups of 64 39.8 us by tiles of 16 rows and 42.9
-// of 32, groups of 32 51 and 115; with one scale a head 33.7 and 29.7.
-// Smaller tiles of rows while there is a CU for each unit: 4 sequences x 5 tokens x
-// 4 heads a key head over 2048 positions 22.8 us with tiles of 32, 14.7 with 8; 16
-// sequences (384 units of 8 rows) 23.5 and 28.4.
+// of 4096, 6 drafts of 4 heads a key head, groups of 64 39.5 us by tiles of 16 rows and 42.5
+// of 32, groups of 32 51 and 118; with one scale a head 33.4 and 29.6.
+// Smaller tiles of rows while there is a CU for each unit: 5 tokens x 4 heads a key
+// head over 900 positions, us with tiles of 32, 16 and 8: 4 sequences 15.1, -, 10.3 (96 units
+// of 8), 16 sequences 15.4, 11.7 (256 of 16) and 15.5 (384 of 8).
 constexpr int64_t kUnits = 256;
 // Pieces go to 256 workgroups of 8 waves where few units are cut into many parts, so
-// that half of these are joined, and there are steps for all waves; to 512 of 4
-// otherwise.  us (8 waves / 4), one sequence: 1 key head, 32768 positions 16.9 / 22.9,
-// 8 heads 18.2 / 19.7, 8192 of 8 heads 11.8 / 13.8, but 4096 11.3 / 10.3; 16 sequences of
-// 4096, 128 units, 20.6 either way, 64 54.8 / 51.6; a chunk of 512 tokens (512 units) 117 / 112.
-constexpr int64_t kWideUnits = 64, kWidePositions = 256 * 8 * kStep;
+// that half of these are joined; to 512 of 4 otherwise.  us (8 waves / 4), one sequence: 1
+// key head, 8192 positions 11.9 / 12.3, 32768 17.8 / 24.3; 8 heads, 8192 12.3 / 14.3, 32768
+// 16.4 / 18.5, but 4096 11.8 / 10.9; 4 sequences of 2048 (32 units) 11.3 / 12.5, 8 of 4096 (64)
+// 15.0 / 15.2, 64 of 4096 55 / 51; a chunk of 512 tokens (512 units) 118 / 113.
+constexpr int64_t kWideUnits = 64, kWideFew = 16, kWidePositions = 8192;
 
 KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, int64_t tokens, int64_t max_queries,
                                   bool each, int64_t capacity) {
@@ -851,10 +849,10 @@ KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, i
   p.rows = (int)std::min<int64_t>(rows, p.tile);
   if (p.whole) {
     p.wgs = (int)most(p.tile);
-    p.waves = capacity >= 2 * 8 * kStep ? 8 : 4;
+    p.waves = capacity >= 3 * 8 * kStep ? 8 : 4;
     while (p.waves > 1 && (units(p.tile) * p.waves > 2048 || p.waves * kStep > capacity)) p.waves /= 2;
   } else {
-    const bool wide = units(tile) <= kWideUnits && units(tile) * capacity >= kWidePositions;
+    const bool wide = units(tile) <= kWideUnits && (units(tile) >= kWideFew || capacity >= kWidePositions);
     p.wgs = wide ? kMaxWgs / 2 : kMaxWgs;
     p.waves = wide ? 8 : 4;
   }

@@ -97,15 +97,16 @@ def test_decode_batches_take_the_waves_that_their_units_fill(pq, share, each):
     p = plan(pq, pq.KvConfig(8), 8 * share, 64, 64, 1, each, 1024)
     assert (p["tile"], p["parts"], p["whole"], p["waves"]) == (8, 2, 1, 4)
     assert p["wgs"] == 512 if each else p["wgs"] >= 512
-    # short tables: a step for each wave, two for each of eight
-    for capacity, waves in ((16, 1), (64, 2), (128, 4), (256, 4), (511, 4), (512, 8), (1024, 8)):
+    # short tables: a step for each wave, three for each of eight
+    for capacity, waves in ((16, 1), (64, 2), (128, 4), (256, 4), (767, 4), (768, 8), (1024, 8)):
         assert plan(pq, pq.KvConfig(8), 8 * share, 4, 4, 1, each, capacity)["waves"] == waves
     # large batches whose units would have to be searched for go in pieces
     assert plan(pq, pq.KvConfig(8), 8 * share, 4096, 4096, 1, each, 512)["whole"] == 1
     assert plan(pq, pq.KvConfig(8), 8 * share, 4097, 4097, 1, each, 512)["whole"] == each
-    # few long sequences: eight waves from 65536 positions of the units together on
-    for length, waves, wgs in ((4096, 4, 512), (8192, 8, 256)):
-        p = plan(pq, pq.KvConfig(8), 8 * share, 1, 1, 1, each, length)
+    # in pieces: eight waves for few units of 8192 positions, and for 16 to 64 of any
+    for kv_heads, length, waves, wgs in ((8, 4096, 4, 512), (8, 8192, 8, 256), (1, 32768, 8, 256), (16, 2048, 8, 256),
+                                         (64, 4096, 8, 256), (65, 32768, 4, 512)):
+        p = plan(pq, pq.KvConfig(kv_heads), kv_heads * share, 1, 1, 1, each, length)
         assert (p["whole"], p["waves"], p["wgs"]) == (0, waves, wgs)
 
 
