@@ -9,15 +9,13 @@
 // What bounds it.  A step of 32 positions reads 4.35 KB (heads of 128, one scale
 // each) and takes about 230 vector instructions for up to 8 rows, most of them to
 // spread codes, then some 100 more for every further 16.  Decoding many sequences
-// is near memory: 64 of up to 8192 tokens with 8 key heads (288 MB) take 78 us, 3.7
-// TB/s; the same loads without the arithmetic 68 us; the vector unit is busy 68% of
-// the time, the matrix cores 22%.  More steps in flight do not help (two ahead instead
-// of one: 83 us, three: 87), nor do three waves a SIMD (79 us).
-//   One sequence of 32768 tokens (38 MB) takes 18 us: 13 in pieces (a wave has four
+// is near memory: 64 of up to 8192 tokens with 8 key heads (288 MB) take 80 us, 3.6
+// TB/s; the vector unit is busy 67% of the time, the matrix cores 22%.
+//   One sequence of 32768 tokens (38 MB) takes 18.5 us: 14 in pieces (a wave has four
 // steps; before them three loads wait for each other: lengths, page numbers, codes)
-// and 5 to join 32 of them.  One of 512 takes 7.6 us, 5.1 without arithmetic.
-//   A chunk of 512 tokens over 8192 takes 112 us, 0.6 PFLOP/s: here the vector
-// unit spreads the codes again for every 32 rows.
+// and 4 to 5 to join 32 of them.  One of 512 takes 7.6 us, most of it that chain.
+//   A chunk of 512 tokens over 8192 takes 113 us, 0.59 PFLOP/s: here the vector
+// unit spreads the codes again for every 32 rows, busy 77% of the time, the matrix cores 27%.
 #include "attention.hpp"
 
 namespace gptq {
@@ -233,7 +231,7 @@ __device__ __forceinline__ void value_pairs(const uint32_t (&w)[D / 32], int b, 
 //   Rows are columns of the products.  With SP 2 (up to 8 rows) both halves of the 16
 // columns hold the same rows; the left half keeps the logits of the step's first
 // record, the right half those of the second, each with sums of its own, so that no
-// lane works for rows that are not there: 64 sequences 86 -> 79 us.  NT 2 holds 32
+// lane works for rows that are not there: 64 x 4096 56.6 -> 53.1 us.  NT 2 holds 32
 // rows: codes are spread once for both tiles, and with one scale a head a product sums
 // the zero points as well.  PARTS is in how many bf16 parts weights enter: 2 leave 2^-16
 // of each, 1 leaves 2^-8, as the result's own rounding does.
@@ -664,9 +662,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(Work w) {
 // Joins the parts of units that were split: a wave takes a row of a unit at a time.
 // The units are few and anywhere among `meta`, so each workgroup lists them first.
 // What this costs is a chain of loads, not their bytes: a row's parts are all in
-// flight at once, 64 at the most.  5 us after 1 x 32768 tokens, 4 after a chunk;
-// four waves a row, or lists in LDS that spare the second look at `meta`, won nothing
-// there and cost 64 ragged sequences 3 us.
+// flight at once, 64 at the most.  4 to 5 us after 1 x 32768 tokens and after a chunk.
 constexpr int kJoinWgs = 512;
 template <int D, int R>
 __global__ __launch_bounds__(256) void kv_join_kernel(Work w, int wgs, int most_rows) {
@@ -800,33 +796,33 @@ gptq_status launch(const Work& w, const KvAttentionPlan& p, hipStream_t stream) 
 // A unit is a workgroup's of its own, in one launch, where the page table holds no
 // longer sequence than kWhole; otherwise a long one would be waited for, and
 // workgroups get equal pieces of all units' steps.  Heads of 128, 8 key heads, us
-// (whole / pieces): 1 x 512 tokens 7.4 / 9.2, 32 x 768 of 32 key heads 22.5 / 27.4, 64 x 1000
-// 16.8 / 19.3, 128 x 250 of 32 heads 31 / 53, but 1 x 1024 10.1 / 9.3, 1 x 2048 15.0 / 10.8.
+// (whole / pieces): 1 x 512 tokens 7.5 / 10.7, 32 x 768 of 32 key heads 22.2 / 26.7, 64 x 1000
+// 16.7 / 19.1, 128 x 250 of 32 heads 31 / 54, 1 x 1024 10.2 / 10.5, but 1 x 2048 15.0 / 10.9.
 // Its waves are as many as leave a CU eight at the most: 64 x 100 of 32 heads, 2048
-// units, 10.9 with one wave each, 14.8 with two, 17 with four; 64 x 512, 512 units,
-// 17.5, 15.1 and 10.7; and have a step of the table each, eight of them three: 1 x 100
-// 5.1 with four, 5.6 with eight, 1 x 250 5.9 and 6.7, 1 x 512 7.4 and 7.9, 1 x 900 10.4 and 10.3.
+// units, 11.1 with one wave each, 14.7 with two, 17.6 with four; 64 x 512, 512 units,
+// 17.7, 15.3 and 10.9; and have a step of the table each, eight of them three: 1 x 100
+// 5.3 with four, 5.8 with eight, 1 x 250 6.1 and 6.9, 1 x 512 7.5 and 8.0, 1 x 900 10.5 and 10.3.
 //   With cu_seqlens each such workgroup searches the batch for its unit, so larger ones go in
 // pieces, which search once: sequences of 20 tokens, 32 heads on 8, us (whole / pieces):
 // 1600 73 / 132, 4096 330 / 327, 16384 4222 / 1299.
 constexpr int64_t kWhole = 1024, kMostUnits = 1 << 22;   // a grid's limit is 2^32 threads
 constexpr int64_t kSearched = 4096;
 // Weights are rounded once for chunks, where the matrix cores and the vector unit are the
-// bound (512 tokens over 8192, 32 heads on 8: 113 us, 131 in two parts; groups of 64 148 and
-// 187, of 32 238 and 320): from more tokens a sequence on than drafts have, whatever the heads.
+// bound (512 tokens over 8192, 32 heads on 8: 112 us, 130 in two parts; groups of 64 147 and
+// 182, of 32 236 and 319): from more tokens a sequence on than drafts have, whatever the heads.
 constexpr int64_t kDrafts = 16;
 // Two parts for 32 rows of more scales than one a head are short of registers: 16 sequences
-// of 4096, 6 drafts of 4 heads a key head, groups of 64 39.5 us by tiles of 16 rows and 42.5
-// of 32, groups of 32 51 and 118; with one scale a head 33.4 and 29.6.
+// of 4096, 6 drafts of 4 heads a key head, groups of 64 39.5 us by tiles of 16 rows and 41.1
+// of 32, groups of 32 51 and 106; with one scale a head 33.5 and 29.7.
 // Smaller tiles of rows while there is a CU for each unit: 5 tokens x 4 heads a key
-// head over 900 positions, us with tiles of 32, 16 and 8: 4 sequences 15.1, -, 10.3 (96 units
-// of 8), 16 sequences 15.4, 11.7 (256 of 16) and 15.5 (384 of 8).
+// head over 900 positions, us with tiles of 32, 16 and 8: 4 sequences 15.4, -, 10.4 (96 units
+// of 8), 16 sequences 15.4, 11.9 (256 of 16) and 15.5 (384 of 8).
 constexpr int64_t kUnits = 256;
 // Pieces go to 256 workgroups of 8 waves where few units are cut into many parts, so
 // that half of these are joined; to 512 of 4 otherwise.  us (8 waves / 4), one sequence: 1
-// key head, 8192 positions 11.9 / 12.3, 32768 17.8 / 24.3; 8 heads, 8192 12.3 / 14.3, 32768
-// 16.4 / 18.5, but 4096 11.8 / 10.9; 4 sequences of 2048 (32 units) 11.3 / 12.5, 8 of 4096 (64)
-// 15.0 / 15.2, 64 of 4096 55 / 51; a chunk of 512 tokens (512 units) 118 / 113.
+// key head, 8192 positions 12.0 / 12.5, 32768 17.8 / 24.4; 8 heads, 8192 12.7 / 14.6, 32768
+// 16.7 / 18.6, but 4096 12.0 / 11.1; 4 sequences of 2048 (32 units) 11.2 / 12.5, 8 of 4096 (64)
+// 15.3 / 15.4, 64 of 4096 54 / 51; a chunk of 512 tokens (512 units) 117 / 112.
 constexpr int64_t kWideUnits = 64, kWideFew = 16, kWidePositions = 8192;
 
 KvAttentionPlan plan_kv_attention(const KvLayout& L, int heads, int64_t batch, int64_t tokens, int64_t max_queries,

@@ -193,10 +193,10 @@ __device__ __forceinline__ void report(const KvSeqs& q, const KvLayout& L) {
 // One workgroup per record (16 positions of one head): a thread quantizes eight
 // neighbouring channels (16 bytes of bf16) of a token, lanes of a group share
 // their extremes by swaps, the codes are put in order in LDS and leave in whole
-// rows.  Bound by memory for prompts (2 bytes in, 0.53 out per value): 8 of 2048
-// tokens, 8 heads of 128, groups of 64 (86 MB) 21 us, 4.1 TB/s; by launch and three
-// dependent loads (sequence, page, tokens) for a decode step: 16 sequences of 32 heads
-// 5.6 us.
+// rows.  Bound by memory for prompts (2 bytes in, 0.56 out per value): 8 of 2048
+// tokens, 8 heads of 128, groups of 64 (86 MB) 22.5 us, 3.8 TB/s, from fp32 (153 MB) 34.6,
+// 4.4 TB/s; by launch and three dependent loads (sequence, page, tokens) for a decode step:
+// 16 sequences of 32 heads 5.3 us.
 template <int D, int G, class T>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvLayout L, HeadRows K, HeadRows V, KvSeqs q,
                                                              uint8_t* __restrict__ pages) {
@@ -297,7 +297,8 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvLayout L, HeadRow
 // ---------------------------------------------------------------- read
 // The same records and threads the other way: whole rows to LDS, a thread makes
 // eight channels of a token, (c - z)·s exactly.  Bound by memory: 8 prompts
-// of 2048 tokens, 8 heads of 128, groups of 64 (86 MB) 15.5 us, 5.5 TB/s.
+// of 2048 tokens, 8 heads of 128, groups of 64 (86 MB) 16.7 us, 5.1 TB/s, part of it from
+// the last cache; to fp32 (153 MB) 43 us, 3.5 TB/s, four bytes of five written.
 template <int D, int G, class T>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvLayout L, HeadRows K, HeadRows V, KvSeqs q,
                                                            const uint8_t* __restrict__ pages) {
@@ -381,7 +382,7 @@ int64_t most_blocks(const KvSeqs& q) { return q.cu ? (q.tokens + 30 * std::min(q
 
 // The heads are shared by as many workgroups as fill the card (8 a CU); each takes
 // every so manieth head of its 16 positions, whose place it finds once (8 prompts of
-// 2048 written and read 40 us; 42.5 with twice as many, 52 with one for each head).
+// 2048 written and read 39.2 us; 41.7 with twice as many, 49.1 with one for each head).
 dim3 grid_of(const KvLayout& L, const KvSeqs& q) {
   const int64_t blocks = most_blocks(q);
   return dim3((unsigned)blocks, (unsigned)std::min<int64_t>(L.heads, ceil_div(2048, blocks)));

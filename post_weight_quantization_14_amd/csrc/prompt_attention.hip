@@ -55,19 +55,20 @@ struct Prompt {
 // 64 keys, and they are the second product's operand as they stand; a wave keeps
 // its 32 queries and their results in registers, and keys and values come through
 // LDS once for the four waves.  One pass with a running maximum; weights are
-// rounded to bf16 (2^-8 of each, as the result is), their sum is of the unrounded.
-//   Long prompts are bound by the matrix cores' power.  6 prompts of up to 8192
-// tokens, 64 heads on 8: 2.3 ms, 1.09 PFLOP/s, 70% of a large product of the
-// library (1.55); the clock falls to 1.9 GHz (1.81 in that product), and the cores
-// are busy 59% of the time.  Without the copies to LDS the time stays, without
-// reads from it it falls by 10%; waves in two groups that take turns at products and
-// weights, raised priorities or another order of tiles gave the same within a few percent.
-//   One prompt is bound by its longest workgroup: 2048 tokens of 32 heads 47 us, of
-// one head 38 where a wave takes all keys: 32 tiles of 1.05 us in a row and about 6 us
-// around them.
+// rounded to bf16 (2^-8 of each, as the result is), their sum is of the unrounded.  In two
+// parts 2048 tokens of 32 heads would take 68 us instead of 52, 6 x 4000 of 64 heads 2201
+// instead of 1557, for an error against 64 bits of 0.0016 instead of 0.0018 to 0.0021, of
+// which 0.0016 is the result's rounding.
+//   Long prompts are bound by issue.  6 of up to 8192 tokens, 64 heads on 8: 2.38 ms, 1.05
+// PFLOP/s, 68% of a large product of the library; the matrix cores are busy 59% of the cycles
+// (75% in that product), the vector unit 51%, and waves wait 42% of theirs for an
+// instruction to issue: the two of a SIMD put no more products beside weights.  Power takes
+// its part: the clock under these counters was 1.57 GHz, 1.71 in that product, 2.43 in decoding.
+//   One prompt is bound by its longest workgroup: 2048 tokens of 32 heads 49 us, of
+// one head 38 where a wave takes all keys, 32 tiles in a row, and 28 where it takes half.
 //   Heads of 64 run three waves a SIMD, where the rarely taken second pass spills:
-// 23 prompts of up to 333 tokens 15.2 us, two waves 16.8; 8192 tokens of 32 heads 307
-// and 320; 2048, where one workgroup is waited for, 35 and 34.
+// 23 prompts of 200 tokens 14.3 us, two waves 16.7; 8192 tokens of 32 heads 293 and 317;
+// 2048 31 and 34.
 template <int D, bool VEC, int KH>
 __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_kernel(Prompt a) {
   constexpr int KS = D / 16, DT = D / 32, CH = D / 8, TB = kBN * D * 2, BM = kBM<KH>, U = 2 / KH;   // U: 32 keys each
@@ -82,7 +83,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prompt_attention_ke
   // on one, which then reads those keys from its own L2; tiles with the most keys
   // go first, so that the last workgroups to start are the shortest.  Where all run at
   // once, two a CU, the second half goes the other way: the longest share a CU with the
-  // shortest (2048 tokens of 32 heads 51.8 us instead of 53.5, 2 x 900 30 instead of 34).
+  // shortest (2 x 900 tokens of 32 heads 32.1 us instead of 35.8, 2048 52.4 instead of 52.9).
   const int64_t slot = blockIdx.x >> 3, group = slot / a.share * 8 + (blockIdx.x & 7);
   const int64_t kvh = group % a.kv_heads, head = kvh * a.share + slot % a.share;
   if (group >= a.tiles * a.kv_heads) return;
@@ -395,9 +396,9 @@ gptq_status launch(const PromptCall& c, hipStream_t stream) {
 // Two waves share 32 queries, each with half of every tile's keys, where workgroups
 // of 128 queries leave CUs idle: their chain of tiles is what is waited for.  us
 // (shared / not): 8 heads of 128, 2048 tokens (128 workgroups of 128) 30 / 40, 4096
-// (256) 58 / 75, 8192 (512) 162 / 165; 32 heads, 500 tokens 12.1 / 15.5, 2048 (512) 57 /
-// 54; 8 heads of 64, 8192 (512) 91 / 112, but 23 prompts of 200, 14 heads (812) 17.4 /
-// 13.2.  Prompts of one tile have nothing to share: 64 tokens 7.3 / 6.7.
+// (256) 59 / 74, 8192 (512) 164 / 161; 32 heads, 500 tokens 12.5 / 15.5, 2048 (512) 54 /
+// 50; 8 heads of 64, 8192 (512) 89 / 107, but 16 (1024) 170 / 162 and 23 prompts of 200, 14
+// heads (812) 16.8 / 13.6.  Prompts of one tile have nothing to share: 64 tokens 7.5 / 6.8.
 gptq_status run_prompt_attention(const PromptCall& c, hipStream_t stream) {
   const int64_t wgs = (c.tokens + 127 * std::min(c.batch, c.tokens)) / 128 * c.heads;
   return wgs <= (c.dim == 64 ? 512 : 256) && c.tokens > kBN * c.batch ? launch<2>(c, stream) : launch<1>(c, stream);
