@@ -487,7 +487,7 @@ gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const voi
  *
  * gptq_kv_read gives the last n positions of each sequence as bf16 (rounded to
  * nearest even) or fp32 (exact): with cu_seqlens the running sum of kv_lens, the
- * whole cache.
+ * whole cache.  More than kv_lens[b] is out of range here too.
  *
  * gptq_kv_attention: for token i of sequence b's n, position t its last
  * kv_lens[b] - n + i,
@@ -495,8 +495,9 @@ gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const voi
  * for bf16 Q and Y: a token a sequence in decoding, several where drafts are
  * checked, hundreds for a chunk of a prompt.  The tokens are appended first.
  * The codes enter the products exactly; all sums are fp32 (and stay finite while
- * |Q| <= 2^108 and head_dim·|Q|·|K| <= 2^126, also times scale·log2(e)).  A token that sees no position (kv_lens[b] < n) gives
- * zeros; scale 0 weighs all positions alike, whatever Q holds.
+ * |Q| <= 2^108 and head_dim·|Q|·|K| <= 2^126, also times scale·log2(e)).  A token
+ * that sees no position (kv_lens[b] < n) gives zeros; a scale of 0 weighs all
+ * positions alike, whatever Q holds.
  * max_queries: the most tokens that a sequence has in this call, as far as the
  * caller knows (0: one).  It chooses between kernels, which give the right results
  * for any number, and how weights enter: up to 16 as two bf16 parts (2^-16 of each
@@ -511,9 +512,8 @@ gptq_status gptq_w4a16_moe(const void* X, int64_t tokens, int64_t ldx, const voi
  *   Y_i = Σ_{j <= i} softmax_j(scale·Q_i·K_j)·V_j.
  * Weights are rounded to bf16 for the second product; all sums are fp32 (and stay
  * finite while head_dim·|Q|·|K| <= 2^126, also times scale·log2(e), and tokens·|V|
- * <= 2^119).  What
- * a token does not see (later tokens, other sequences) may be anything, NaN too.
- * cu_seqlens beyond 0 .. tokens is cut to it.
+ * <= 2^119).  What a token does not see (later tokens, other sequences) may be
+ * anything, NaN too.  cu_seqlens beyond 0 .. tokens is cut to it.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int32_t kv_heads;
